@@ -10,12 +10,12 @@
 
 #include <atomic>
 #include <mutex>
-#include <unordered_map>
 
 #include "bgmv.cuh"
 #include "bgmv_fused.cuh"
 #include "floor.cuh"
 #include "common.cuh"
+#include "host.cuh"
 #include "keyed.cuh"
 #include "lora_delta.h"
 #include "route.cuh"
@@ -26,17 +26,6 @@ using namespace lora;
 namespace {
 
 constexpr int kAbiVersion = 2;
-
-inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-inline size_t align256(size_t b) { return (b + 255) & ~(size_t)255; }
-
-int env_int(const char* name, int dflt) {
-  const char* v = getenv(name);
-  if (!v || !*v) return dflt;
-  char* end = nullptr;
-  long x = strtol(v, &end, 10);
-  return (end && *end == 0) ? (int)x : dflt;
-}
 
 // Cluster size of the small-segment kernel: 16 CTAs per key when there are few
 // keys (decode: spread each adapter's bytes over many SMs), fewer when there
@@ -75,28 +64,6 @@ int b_stage_bytes() {
   }();
   return v;
 }
-bool use_pdl() {
-  static const bool on = env_int("LORA_PDL", 1) != 0;
-  return on;
-}
-// Limit of the kernels' bounded waits, read at each launch
-// (lora_set_wait_limit_ns).
-std::atomic<uint64_t> g_wait_limit_ns{kWaitLimitNs};
-
-// Per-(kernel, device) function attributes, set once: the dynamic shared
-// memory opt-in (to the largest size requested so far) and the non-portable
-// cluster size.
-struct KernelAttrCache {
-  std::mutex mu;
-  std::unordered_map<uint64_t, int> smem;  // (kernel, device) -> bytes granted
-  std::unordered_map<uint64_t, bool> cluster;
-  std::unordered_map<uint64_t, int> occupancy;  // (kernel, device, smem) -> CTAs per SM
-};
-KernelAttrCache& attr_cache() {
-  static KernelAttrCache c;
-  return c;
-}
-
 // Resident CTAs per SM of `kernel` with `threads` threads and `smem_bytes` of
 // dynamic shared memory, ignoring tensor memory; at least 1.
 template <class K>
@@ -133,37 +100,6 @@ int ctas_per_sm(K kernel, int threads, int smem_bytes) {
   c.occupancy[id] = n;
   return n;
 }
-
-template <class K>
-cudaError_t prepare_kernel(K kernel, int smem_bytes, bool big_cluster) {
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  const uint64_t id = (reinterpret_cast<uint64_t>(reinterpret_cast<const void*>(kernel)) << 6) ^
-                      (uint64_t)dev;
-  KernelAttrCache& c = attr_cache();
-  std::lock_guard<std::mutex> lock(c.mu);
-  if (smem_bytes > 48 * 1024) {
-    auto it = c.smem.find(id);
-    if (it == c.smem.end() || it->second < smem_bytes) {
-      e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes);
-      if (e != cudaSuccess) return e;
-      // all of the unified L1 as shared memory, so that several such CTAs fit
-      e = cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout,
-                               cudaSharedmemCarveoutMaxShared);
-      if (e != cudaSuccess) return e;
-      c.smem[id] = smem_bytes;
-    }
-  }
-  if (big_cluster && !c.cluster[id]) {
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-    if (e != cudaSuccess) return e;
-    c.cluster[id] = true;
-  }
-  return cudaSuccess;
-}
-
-int cuda_status(cudaError_t e) { return e == cudaSuccess ? LORA_OK : LORA_ERR_CUDA; }
 
 int make_slices(const int32_t* widths, int S, int offset_start, Slices& sl, int* rel) {
   if (!widths || S < 1 || S > kMaxSlices) return S > kMaxSlices ? LORA_ERR_UNSUPPORTED : LORA_ERR_ARG;
@@ -437,18 +373,6 @@ size_t ws_plane_bytes(int n, int hs) { return align256((size_t)(n > 0 ? n : 1) *
 // the tensor-core shrink can split k across more CTAs.
 size_t ws_bytes_for(int n, int n_keys, int hs, int planes = 1) {
   return ws_head_bytes(n, n_keys) + (size_t)planes * ws_plane_bytes(n, hs);
-}
-
-int sm_count() {
-  static int cache[64] = {0};
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 148;
-  if (!cache[dev]) {
-    int v = 0;
-    cudaDeviceGetAttribute(&v, cudaDevAttrMultiProcessorCount, dev);
-    cache[dev] = v > 0 ? v : 148;
-  }
-  return cache[dev];
 }
 
 Workspace carve(void* ws, int n, int n_keys) {
