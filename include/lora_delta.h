@@ -74,6 +74,12 @@ typedef struct CUstream_st *lora_stream_t; /* == cudaStream_t */
 #define LORA_DEV_ERR_ALIGN 16u  /* a table address is not 16-byte aligned: slice skipped */
 #define LORA_DEV_ERR_INTERNAL 32u /* a launch invariant of the library failed (a bug)   */
 #define LORA_DEV_ERR_SEGMENT 64u  /* segment starts not nondecreasing in [0, n]: clamped  */
+#define LORA_DEV_ERR_LENGTH 128u  /* a request's length is negative or past its limits: clamped */
+#define LORA_DEV_ERR_PAGE 256u    /* a cache page is missing or outside the cache: skipped  */
+
+/* element types of rows that are not bf16 only */
+#define LORA_BF16 0
+#define LORA_F16 1
 
 /* Human-readable name of a status code (static string). */
 const char *lora_status_string(int status);
@@ -413,6 +419,130 @@ int lora_delta_fused_noalloc(void *out, int64_t ld_out, const void *x, int n, in
                              const int32_t *widths, int S, int R, int max_loras,
                              int offset_start, int add_inputs, uint32_t *err_word,
                              lora_stream_t stream);
+
+/*
+ * Serving step around the delta.  A request's keys and values live in pages of
+ * `page_size` tokens (a multiple of 16, at most 1024); block_table[b][p] is
+ * the page that holds tokens p * page_size .. of request b.  None of the pages
+ * has these calls: a step's order is lora_batch_plan once, then in each layer
+ * the projections with lora_delta_fused (seq_slot of the plan),
+ * lora_kv4_append (slot_map of the plan) and lora_kv4_attention.
+ * Limits: at most 4096 requests; n_reqs * max_pages and max_pages * page_size
+ * below 2^31 (LORA_ERR_UNSUPPORTED beyond).
+ */
+
+/*
+ * lora_batch_plan -- the maps of one step from the requests' lengths, and the
+ * pages that its new tokens need.  Request b holds ctx_len[b] tokens and adds
+ * new_len[b]; its rows follow those of request b - 1.
+ *   ctx_len, new_len [n_reqs] int32 (in).
+ *   req_slot    [n_reqs] int32 (in) or NULL: the request's adapter slot.
+ *   block_table [n_reqs, ld_table] int32 (in/out): entries below
+ *               ceil(ctx / page_size) are read; the entries of new pages, up to
+ *               ceil((ctx + new) / page_size), are written.
+ *   free_pages, free_count (in), free_left (out): a stack of free pages and its
+ *               height; page k of all the step's new pages, in request order,
+ *               is free_pages[*free_count - 1 - k], and *free_left is the height
+ *               left.  free_left may be free_count.  With a free_left of its own
+ *               the call changes nothing that it reads, and can be repeated.
+ *               All three NULL: the tables hold every page already.
+ *   row_start   [n_reqs + 1] int32 (out): request b's rows are row_start[b] ..
+ *               row_start[b + 1] - 1.
+ *   seq_len     [n_reqs] int32 (out): ctx + new.
+ *   row_req, position, seq_slot [n_rows] int32, slot_map [n_rows] int64 (out):
+ *               the row's request, its token's position, its adapter slot and
+ *               its cache slot page * page_size + position % page_size.  Rows
+ *               past the last request get -1, 0, -1 and -1 (no delta, not
+ *               stored), so a batch may be padded to a fixed n_rows.
+ * Handled, with LORA_DEV_ERR_LENGTH: a negative length counts as 0, a length
+ * past max_pages * page_size is cut there, and rows past n_rows are cut off
+ * (row_start and seq_len count what is left).  With LORA_DEV_ERR_PAGE: a token
+ * whose page is missing (an entry < 0, the stack empty) gets slot -1, and the
+ * table an entry of -1.  Requires 16-byte aligned row arrays.
+ */
+int lora_batch_plan(const int32_t *ctx_len, const int32_t *new_len, const int32_t *req_slot,
+                    int n_reqs, int n_rows, int page_size, int32_t *block_table, int64_t ld_table,
+                    int max_pages, const int32_t *free_pages, const int32_t *free_count,
+                    int32_t *free_left, int32_t *row_start, int32_t *seq_len, int32_t *row_req,
+                    int32_t *position, int64_t *slot_map, int32_t *seq_slot, uint32_t *err_word,
+                    lora_stream_t stream);
+
+/*
+ * lora_pages_release -- the pages of finished requests back onto the free
+ * stack: for every b with done[b] != 0, the entries >= 0 among its first
+ * ceil(seq_len[b] / page_size), in (request, page) order, are stored from
+ * free_pages[*free_count] up, become -1 in the table, and are counted in
+ * *free_count.  Pages beyond free_cap stay in the table (LORA_DEV_ERR_PAGE); a
+ * length outside [0, max_pages * page_size] is clamped (LORA_DEV_ERR_LENGTH).
+ */
+int lora_pages_release(const int32_t *done, const int32_t *seq_len, int n_reqs, int page_size,
+                       int32_t *block_table, int64_t ld_table, int max_pages, int32_t *free_pages,
+                       int free_cap, int32_t *free_count, uint32_t *err_word,
+                       lora_stream_t stream);
+
+/*
+ * The 4-bit cache: [num_pages][kv_heads][page_size / 16] tiles of 16 tokens.
+ * head_dim is 64, 128 or 256, in groups of 64.  A (token, head, group) keeps
+ * m = f16(min), s = f16((max - min) * (1 / 15)) and codes
+ * c = clamp(rint((x - m) * (1 / s)), 0, 15) (0 where s is 0), each step rounded
+ * to float32, and stands for s * c + m.  Magnitudes up to 65504 are held; a
+ * group with an infinity, a NaN or more reads as NaN.  The bytes of a tile, W = min(D, 128):
+ *   key codes [D / W][16 tokens][4 c][W / 32 words]: nibble i of word w is dim
+ *     64 (w / 2) + 16 c + 8 (w % 2) + i of the plane; key pairs [16][D / 64] of f16 (s, m);
+ *   value codes [D / W][2 h][8 g][4 c][W / 32 words]: nibble j of the low (high) half of
+ *     word w is dim 64 (w / 2) + 8 g + 4 (w % 2) + j of token 8 h + 2 c (+ 1); value pairs.
+ * dtype (LORA_BF16 or LORA_F16) is the type of the rows beside it.
+ * lora_kv4_page_bytes gives the bytes of one page, all heads (0 for sizes
+ * that are not supported).  `pages` must be 16-byte aligned.
+ */
+size_t lora_kv4_page_bytes(int page_size, int kv_heads, int head_dim);
+
+/*
+ * lora_kv4_append -- quantise the rows k, v [n, kv_heads * head_dim] (row
+ * strides ld_k, ld_v in elements, multiples of 8) and store row i at slot
+ * slot_map[i].  A negative slot is not stored; a slot past the cache is not
+ * stored and sets LORA_DEV_ERR_PAGE.  Slots of one call must differ.
+ */
+int lora_kv4_append(void *pages, int64_t num_pages, int page_size, int kv_heads, int head_dim,
+                    int dtype, const void *k, int64_t ld_k, const void *v, int64_t ld_v,
+                    const int64_t *slot_map, int n, uint32_t *err_word, lora_stream_t stream);
+
+/*
+ * lora_kv4_read -- the values that stored rows stand for, rounded once to the
+ * row type: row i of k, v is slot slot_map[i]; a negative slot reads as zeros,
+ * one past the cache too, with LORA_DEV_ERR_PAGE.
+ */
+int lora_kv4_read(const void *pages, int64_t num_pages, int page_size, int kv_heads, int head_dim,
+                  int dtype, void *k, int64_t ld_k, void *v, int64_t ld_v, const int64_t *slot_map,
+                  int n, uint32_t *err_word, lora_stream_t stream);
+
+/*
+ * lora_kv4_attention -- causal attention of a step's rows over the cache.  Row
+ * i of request b (row_start[b] <= i < row_start[b + 1]) stands at position
+ * P = seq_len[b] - row_start[b + 1] + i and sees the tokens t <= P, with
+ * window > 0 only t > P - window:
+ *   out[i, h] = sum_t softmax_t(scale * q[i, h] . K[t, h / g]) V[t, h / g],
+ *   g = q_heads / kv_heads
+ * over the values that the cache stands for.  q, out [n, q_heads * head_dim]
+ * with row strides ld_q, ld_out (multiples of 8 elements).  lse [n, q_heads]
+ * float32 (out) or NULL: the log of the softmax's denominator.  max_q_len:
+ * the most rows of one request, known to the host; a request with more gets
+ * zeros and LORA_DEV_ERR_LENGTH.  Tokens in a page outside [0, num_pages) or
+ * past the table are not seen (LORA_DEV_ERR_PAGE / LORA_DEV_ERR_LENGTH).  A row
+ * that sees nothing, and rows outside every request, get zeros (lse -inf).
+ * What the cache holds at tokens that are not seen has no influence.
+ * workspace: lora_kv4_attention_workspace_size() bytes, 256-byte aligned.  Its
+ * first lora_kv4_attention_zeroed_bytes() bytes must be zero before its first
+ * use and are left zero; calls that may overlap need workspaces of their own.
+ */
+size_t lora_kv4_attention_workspace_size(void);
+size_t lora_kv4_attention_zeroed_bytes(void);
+int lora_kv4_attention(void *out, int64_t ld_out, const void *q, int64_t ld_q, int n, int q_heads,
+                       const void *pages, int64_t num_pages, int page_size, int kv_heads,
+                       int head_dim, int dtype, const int32_t *block_table, int64_t ld_table,
+                       int max_pages, const int32_t *row_start, const int32_t *seq_len, int n_reqs,
+                       int max_q_len, float scale, int window, float *lse, void *workspace,
+                       size_t ws_bytes, uint32_t *err_word, lora_stream_t stream);
 
 /*
  * lora_get_error -- copy the device error word to *host_out after all work

@@ -30,6 +30,8 @@ __all__ = [
     "lora_moe_w2_delta", "lora_moe_w2_delta_routed", "lora_get_error", "new_error_word",
     "lora_delta_fused_noalloc", "lora_noalloc_scratch_bytes", "lora_set_wait_limit_ns",
     "WAIT_LIMIT_DEFAULT_NS",
+    "BatchPlan", "Kv4Cache", "lora_batch_plan", "lora_pages_release", "lora_kv4_page_bytes",
+    "lora_kv4_append", "lora_kv4_read", "lora_kv4_attention", "lora_kv4_attention_workspace",
 ]
 
 # Default limit of the kernels' bounded waits (2 s of the GPU's global timer).
@@ -481,3 +483,8 @@ def lora_get_error(err: torch.Tensor, clear: bool = True, stream=None) -> int:
     _check("lora_get_error", lib().lora_get_error(_ptr(err), ctypes.byref(host), int(clear),
                                                   _stream(stream)))
     return int(host.value)
+
+
+from .serve import (BatchPlan, Kv4Cache, lora_batch_plan, lora_kv4_append,  # noqa: E402
+                    lora_kv4_attention, lora_kv4_attention_workspace, lora_kv4_page_bytes,
+                    lora_kv4_read, lora_pages_release)

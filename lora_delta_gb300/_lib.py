@@ -53,6 +53,16 @@ SIGNATURES = {
     "lora_noalloc_scratch_bytes": (_sz, []),
     "lora_delta_fused_noalloc": (_i, [_vp, _i64, _vp, _i, _i, _vp, _vp, _vp, _vp, _vp, _i, _i,
                                       _i, _i, _i, _vp, _vp]),
+    "lora_batch_plan": (_i, [_vp, _vp, _vp, _i, _i, _i, _vp, _i64, _i, _vp, _vp, _vp, _vp, _vp,
+                             _vp, _vp, _vp, _vp, _vp, _vp]),
+    "lora_pages_release": (_i, [_vp, _vp, _i, _i, _vp, _i64, _i, _vp, _i, _vp, _vp, _vp]),
+    "lora_kv4_page_bytes": (_sz, [_i, _i, _i]),
+    "lora_kv4_append": (_i, [_vp, _i64, _i, _i, _i, _i, _vp, _i64, _vp, _i64, _vp, _i, _vp, _vp]),
+    "lora_kv4_read": (_i, [_vp, _i64, _i, _i, _i, _i, _vp, _i64, _vp, _i64, _vp, _i, _vp, _vp]),
+    "lora_kv4_attention_workspace_size": (_sz, []),
+    "lora_kv4_attention_zeroed_bytes": (_sz, []),
+    "lora_kv4_attention": (_i, [_vp, _i64, _vp, _i64, _i, _i, _vp, _i64, _i, _i, _i, _i, _vp, _i64,
+                                _i, _vp, _vp, _i, _i, _f, _i, _vp, _vp, _sz, _vp, _vp]),
 }
 
 _LIB = None

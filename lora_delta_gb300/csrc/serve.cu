@@ -1,0 +1,230 @@
+// C ABI of the serving-step operators beside the delta: the batch plan, the
+// 4-bit key/value cache's store and read, and attention over it.  Host-side
+// validation and dispatch onto the caller's stream; nothing here allocates or
+// synchronizes, and every failure is a status code.
+#include <math.h>
+
+#include <type_traits>
+
+#include "common.cuh"
+#include "host.cuh"
+#include "kv4.cuh"
+#include "kv4_attn.cuh"
+#include "lora_delta.h"
+#include "plan.cuh"
+
+using namespace lora;
+
+namespace {
+
+inline bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+inline bool aligned8(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 7u) == 0; }
+
+int check_page_size(int page_size) {
+  if (page_size < 1) return LORA_ERR_ARG;
+  return page_size % kKvTile || page_size > 1024 ? LORA_ERR_UNSUPPORTED : LORA_OK;
+}
+
+// The cache's own arguments, common to store, read and attention.
+int check_cache(const void* pages, int64_t num_pages, int page_size, int heads, int head_dim,
+                int dtype) {
+  if (!pages || num_pages < 1 || heads < 1) return LORA_ERR_ARG;
+  if (dtype != LORA_BF16 && dtype != LORA_F16) return LORA_ERR_ARG;
+  if (const int rc = check_page_size(page_size)) return rc;
+  if (head_dim != 64 && head_dim != 128 && head_dim != 256) return LORA_ERR_UNSUPPORTED;
+  if (num_pages > INT32_MAX || heads > 1024) return LORA_ERR_UNSUPPORTED;
+  return aligned16(pages) ? LORA_OK : LORA_ERR_ALIGN;
+}
+
+int check_rows(const void* p, int64_t ld, int n, int width) {
+  if (!p) return LORA_ERR_ARG;
+  if (n > 1 && ld < width) return LORA_ERR_SHAPE;
+  return ld % 8 || !aligned16(p) ? LORA_ERR_ALIGN : LORA_OK;
+}
+
+// f(kernel for head_dim and type)
+template <class F>
+int by_type(int head_dim, int dtype, F f) {
+  const bool bf = dtype == LORA_BF16;
+  if (head_dim == 64) return bf ? f(std::integral_constant<int, 64>(), std::true_type())
+                                : f(std::integral_constant<int, 64>(), std::false_type());
+  if (head_dim == 128) return bf ? f(std::integral_constant<int, 128>(), std::true_type())
+                                 : f(std::integral_constant<int, 128>(), std::false_type());
+  return bf ? f(std::integral_constant<int, 256>(), std::true_type())
+            : f(std::integral_constant<int, 256>(), std::false_type());
+}
+
+int rows_call(bool store, const void* k, int64_t ld_k, const void* v, int64_t ld_v, void* pages,
+              int64_t num_pages, int page_size, int heads, int head_dim, int dtype,
+              const int64_t* slot_map, int n, uint32_t* err, cudaStream_t stream) {
+  if (n < 0) return LORA_ERR_ARG;
+  if (n == 0) return LORA_OK;
+  int rc = check_cache(pages, num_pages, page_size, heads, head_dim, dtype);
+  if (rc) return rc;
+  if (!slot_map) return LORA_ERR_ARG;
+  if ((rc = check_rows(k, ld_k, n, heads * head_dim))) return rc;
+  if ((rc = check_rows(v, ld_v, n, heads * head_dim))) return rc;
+  if (!aligned8(slot_map) || !aligned4(err)) return LORA_ERR_ALIGN;
+  Kv4Rows a = {};
+  a.k = k;
+  a.v = v;
+  a.ld_k = ld_k;
+  a.ld_v = ld_v;
+  a.pages = reinterpret_cast<uint8_t*>(pages);
+  a.num_slots = num_pages * page_size;
+  a.page_size = page_size;
+  a.heads = heads;
+  a.slot_map = slot_map;
+  a.n = n;
+  a.err = err;
+  const int64_t items = (int64_t)n * 2 * heads * (head_dim / 8);
+  const int64_t want = (items + 255) / 256, most = (int64_t)sm_count() * 32;
+  const unsigned grid = (unsigned)(want < most ? want : most);
+  return by_type(head_dim, dtype, [&](auto d, auto bf) {
+    constexpr int D = decltype(d)::value;
+    constexpr bool BF16 = decltype(bf)::value;
+    if (store)
+      kv4_append_kernel<D, BF16><<<grid, 256, 0, stream>>>(a);
+    else
+      kv4_read_kernel<D, BF16><<<grid, 256, 0, stream>>>(a);
+    return cuda_status(cudaGetLastError());
+  });
+}
+
+}  // namespace
+
+extern "C" {
+
+int lora_batch_plan(const int32_t* ctx_len, const int32_t* new_len, const int32_t* req_slot,
+                    int n_reqs, int n_rows, int page_size, int32_t* block_table, int64_t ld_table,
+                    int max_pages, const int32_t* free_pages, const int32_t* free_count,
+                    int32_t* free_left, int32_t* row_start, int32_t* seq_len, int32_t* row_req,
+                    int32_t* position, int64_t* slot_map, int32_t* seq_slot, uint32_t* err_word,
+                    lora_stream_t stream) {
+  if (n_reqs < 0 || n_rows < 0 || max_pages < 0 || !row_start) return LORA_ERR_ARG;
+  if (n_reqs > 0 && (!ctx_len || !new_len || !block_table || !seq_len)) return LORA_ERR_ARG;
+  if (n_rows > 0 && (!row_req || !position || !slot_map || !seq_slot)) return LORA_ERR_ARG;
+  if ((free_pages != nullptr) != (free_count != nullptr) ||
+      (free_pages != nullptr) != (free_left != nullptr))
+    return LORA_ERR_ARG;
+  if (const int rc = check_page_size(page_size)) return rc;
+  if (n_reqs > kPlanMaxReqs || (int64_t)n_reqs * max_pages > INT32_MAX ||
+      (int64_t)max_pages * page_size > INT32_MAX)
+    return LORA_ERR_UNSUPPORTED;
+  if (n_reqs > 1 && ld_table < max_pages) return LORA_ERR_SHAPE;
+  if (!aligned16(row_req) || !aligned16(position) || !aligned16(slot_map) || !aligned16(seq_slot))
+    return LORA_ERR_ALIGN;
+  PlanArgs a = {ctx_len,    new_len,   req_slot, n_reqs,   n_rows,   page_size, max_pages,
+                block_table, ld_table, free_pages, free_count, free_left, row_start, seq_len,
+                row_req,    position,  slot_map, seq_slot, err_word};
+  const int smem = (int)plan_smem_bytes(n_reqs);
+  if (prepare_kernel(batch_plan_kernel, smem, false) != cudaSuccess) return LORA_ERR_CUDA;
+  const int64_t per_cta = kPlanThreads * kPlanRowsPerThread;
+  int ctas = 1;
+  while (ctas < kPlanMaxCluster && ctas * per_cta < n_rows) ctas *= 2;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = (unsigned)ctas;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)ctas);
+  cfg.blockDim = dim3(kPlanThreads);
+  cfg.dynamicSmemBytes = (size_t)smem;
+  cfg.stream = (cudaStream_t)stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = ctas > 1 ? 1 : 0;
+  return cuda_status(cudaLaunchKernelEx(&cfg, batch_plan_kernel, (const PlanArgs)a, ctas));
+}
+
+int lora_pages_release(const int32_t* done, const int32_t* seq_len, int n_reqs, int page_size,
+                       int32_t* block_table, int64_t ld_table, int max_pages, int32_t* free_pages,
+                       int free_cap, int32_t* free_count, uint32_t* err_word,
+                       lora_stream_t stream) {
+  if (n_reqs < 0 || max_pages < 0 || free_cap < 0) return LORA_ERR_ARG;
+  if (n_reqs == 0 || max_pages == 0) return LORA_OK;
+  if (!done || !seq_len || !block_table || !free_pages || !free_count) return LORA_ERR_ARG;
+  if (const int rc = check_page_size(page_size)) return rc;
+  if (n_reqs > kPlanMaxReqs || (int64_t)n_reqs * max_pages > INT32_MAX) return LORA_ERR_UNSUPPORTED;
+  if (n_reqs > 1 && ld_table < max_pages) return LORA_ERR_SHAPE;
+  pages_release_kernel<<<1, kPlanThreads, 0, (cudaStream_t)stream>>>(
+      done, seq_len, n_reqs, page_size, block_table, ld_table, max_pages, free_pages, free_cap,
+      free_count, err_word);
+  return cuda_status(cudaGetLastError());
+}
+
+size_t lora_kv4_page_bytes(int page_size, int kv_heads, int head_dim) {
+  if (check_page_size(page_size) || kv_heads < 1) return 0;
+  if (head_dim != 64 && head_dim != 128 && head_dim != 256) return 0;
+  return (size_t)kv_heads * (page_size / kKvTile) * kv4_tile_bytes(head_dim);
+}
+
+int lora_kv4_append(void* pages, int64_t num_pages, int page_size, int kv_heads, int head_dim,
+                    int dtype, const void* k, int64_t ld_k, const void* v, int64_t ld_v,
+                    const int64_t* slot_map, int n, uint32_t* err_word, lora_stream_t stream) {
+  return rows_call(true, k, ld_k, v, ld_v, pages, num_pages, page_size, kv_heads, head_dim, dtype,
+                   slot_map, n, err_word, (cudaStream_t)stream);
+}
+
+int lora_kv4_read(const void* pages, int64_t num_pages, int page_size, int kv_heads, int head_dim,
+                  int dtype, void* k, int64_t ld_k, void* v, int64_t ld_v, const int64_t* slot_map,
+                  int n, uint32_t* err_word, lora_stream_t stream) {
+  return rows_call(false, k, ld_k, v, ld_v, const_cast<void*>(pages), num_pages, page_size,
+                   kv_heads, head_dim, dtype, slot_map, n, err_word, (cudaStream_t)stream);
+}
+
+size_t lora_kv4_attention_workspace_size(void) { return 256; }
+size_t lora_kv4_attention_zeroed_bytes(void) { return 256; }
+
+int lora_kv4_attention(void* out, int64_t ld_out, const void* q, int64_t ld_q, int n, int q_heads,
+                       const void* pages, int64_t num_pages, int page_size, int kv_heads,
+                       int head_dim, int dtype, const int32_t* block_table, int64_t ld_table,
+                       int max_pages, const int32_t* row_start, const int32_t* seq_len, int n_reqs,
+                       int max_q_len, float scale, int window, float* lse, void* workspace,
+                       size_t ws_bytes, uint32_t* err_word, lora_stream_t stream) {
+  if (n < 0 || n_reqs < 0 || max_pages < 0 || window < 0 || q_heads < 1 || max_q_len < 0)
+    return LORA_ERR_ARG;
+  if (n == 0) return LORA_OK;
+  int rc = check_cache(pages, num_pages, page_size, kv_heads, head_dim, dtype);
+  if (rc) return rc;
+  if (q_heads % kv_heads) return LORA_ERR_SHAPE;
+  if (!row_start || (n_reqs > 0 && (!seq_len || !block_table))) return LORA_ERR_ARG;
+  if (n_reqs > kAttnMaxReqs || (int64_t)max_pages * page_size > INT32_MAX || q_heads > 65535)
+    return LORA_ERR_UNSUPPORTED;
+  if ((rc = check_rows(out, ld_out, n, q_heads * head_dim))) return rc;
+  if ((rc = check_rows(q, ld_q, n, q_heads * head_dim))) return rc;
+  if (n_reqs > 1 && ld_table < max_pages) return LORA_ERR_SHAPE;
+  if (!workspace || ws_bytes < lora_kv4_attention_workspace_size()) return LORA_ERR_WORKSPACE;
+  AttnArgs a = {};
+  a.out = out;
+  a.q = q;
+  a.ld_out = ld_out;
+  a.ld_q = ld_q;
+  a.n = n;
+  a.q_heads = q_heads;
+  a.heads = kv_heads;
+  a.group = q_heads / kv_heads;
+  a.pages = reinterpret_cast<const uint8_t*>(pages);
+  a.num_pages = num_pages;
+  a.page_size = page_size;
+  a.table = block_table;
+  a.ld_table = ld_table;
+  a.max_pages = max_pages;
+  a.row_start = row_start;
+  a.seq_len = seq_len;
+  a.B = n_reqs;
+  a.max_q_len = max_q_len;
+  a.window = window;
+  a.scale_log2 = (float)((double)scale * 1.4426950408889634);
+  a.lse = lse;
+  a.err = err_word;
+  return by_type(head_dim, dtype, [&](auto d, auto bf) {
+    constexpr int D = decltype(d)::value;
+    constexpr bool BF16 = decltype(bf)::value;
+    kv4_attn_simple_kernel<D, BF16>
+        <<<dim3((unsigned)n, (unsigned)q_heads), 128, 0, (cudaStream_t)stream>>>(a);
+    return cuda_status(cudaGetLastError());
+  });
+}
+
+}  // extern "C"

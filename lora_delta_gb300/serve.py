@@ -1,0 +1,216 @@
+"""The serving step around the delta: the batch plan, the 4-bit key/value cache and attention
+over it.
+
+As in the rest of the binding, every function only marshals tensors into the C ABI of
+``include/lora_delta.h`` (where layouts, limits and errors are stated) on torch's current CUDA
+stream, and turns a nonzero status into ``LoraError``.
+"""
+from __future__ import annotations
+
+import torch
+
+from . import LoraError, _dev
+from ._lib import lib
+
+_DTYPES = {torch.bfloat16: 0, torch.float16: 1}
+
+
+def _call(name, *args):
+    rc = getattr(lib(), name)(*args)
+    if rc:
+        raise LoraError(name, rc)
+
+
+def _at(t):
+    return None if t is None else t.data_ptr()
+
+
+def _raw_stream(stream):
+    return (torch.cuda.current_stream() if stream is None else stream).cuda_stream
+
+
+def _i32(t, name, size=None):
+    _dev(t, name, torch.int32)
+    if size is not None and t.numel() < size:
+        raise ValueError(f"{name} must have {size} entries, got {t.numel()}")
+    return t.data_ptr()
+
+
+def _table(t, n_reqs):
+    if not t.is_cuda or t.dtype != torch.int32 or t.dim() != 2 or t.shape[0] < n_reqs or \
+            (t.shape[1] > 1 and t.stride(1) != 1 and n_reqs > 0):
+        raise ValueError("block_table must be an int32 CUDA tensor [n_reqs, max_pages] with adjacent entries")
+    return t.data_ptr(), t.stride(0), t.shape[1]
+
+
+def _rows(t, name, heads, head_dim, dtype):
+    """Pointer and row stride of a [n, heads, head_dim] tensor whose rows may lie apart."""
+    if not t.is_cuda or t.dtype != dtype:
+        raise ValueError(f"{name} must be a {dtype} CUDA tensor")
+    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != head_dim:
+        raise ValueError(f"{name} must be [n, {heads}, {head_dim}], got {tuple(t.shape)}")
+    if t.stride(2) != 1 or (heads > 1 and t.stride(1) != head_dim):
+        raise ValueError(f"{name}'s heads must lie next to one another")
+    return t.data_ptr(), t.stride(0) if t.shape[0] > 1 else heads * head_dim
+
+
+class BatchPlan:
+    """What ``lora_batch_plan`` writes for a batch of up to ``n_reqs`` requests padded to ``n_rows``
+    rows: ``row_start`` [n_reqs + 1], ``seq_len`` [n_reqs], ``row_req``, ``position``, ``seq_slot``
+    [n_rows] int32 and ``slot_map`` [n_rows] int64."""
+
+    def __init__(self, n_reqs: int, n_rows: int, page_size: int, device="cuda"):
+        def ints(n):
+            return torch.empty(n, dtype=torch.int32, device=device)
+
+        self.n_reqs, self.n_rows, self.page_size = int(n_reqs), int(n_rows), int(page_size)
+        self.row_start, self.seq_len = ints(n_reqs + 1), ints(n_reqs)
+        self.row_req, self.position, self.seq_slot = ints(n_rows), ints(n_rows), ints(n_rows)
+        self.slot_map = torch.empty(n_rows, dtype=torch.int64, device=device)
+        self._out = [t.data_ptr() for t in (self.row_start, self.seq_len, self.row_req,
+                                            self.position, self.slot_map, self.seq_slot)]
+
+
+def lora_batch_plan(plan: BatchPlan, ctx_len, new_len, block_table, req_slot=None, free_pages=None,
+                    free_count=None, free_left=None, err=None, stream=None) -> BatchPlan:
+    """The step's maps and new pages from the requests' lengths, into ``plan``'s tensors.
+
+    ``free_pages`` / ``free_count`` [1] are the stack of free pages; the height that is left goes to
+    ``free_left`` [1], or back into ``free_count`` where none is given."""
+    B = plan.n_reqs
+    if free_pages is not None and free_left is None:
+        free_left = free_count
+    _call("lora_batch_plan", _i32(ctx_len, "ctx_len", B), _i32(new_len, "new_len", B),
+          None if req_slot is None else _i32(req_slot, "req_slot", B), B, plan.n_rows,
+          plan.page_size, *_table(block_table, B),
+          *(None if t is None else _i32(t, name) for t, name in (
+              (free_pages, "free_pages"), (free_count, "free_count"), (free_left, "free_left"))),
+          *plan._out, _at(err), _raw_stream(stream))
+    return plan
+
+
+def lora_pages_release(done, seq_len, block_table, page_size: int, free_pages, free_count, err=None,
+                       stream=None):
+    """The pages of the requests with ``done[b] != 0`` back onto the stack of free pages."""
+    B = done.numel()
+    _call("lora_pages_release", _i32(done, "done"), _i32(seq_len, "seq_len", B), B, int(page_size),
+          *_table(block_table, B), _i32(free_pages, "free_pages"), free_pages.numel(),
+          _i32(free_count, "free_count"), _at(err), _raw_stream(stream))
+
+
+def lora_kv4_page_bytes(page_size: int, kv_heads: int, head_dim: int) -> int:
+    return int(lib().lora_kv4_page_bytes(int(page_size), int(kv_heads), int(head_dim)))
+
+
+class Kv4Cache:
+    """A key/value cache held in 4 bits.
+
+    ``pages`` is its memory, uint8 [num_pages, kv_heads, page_size / 16, tile bytes]; ``dtype``
+    (bfloat16 or float16) is the type of the keys, values and queries beside it."""
+
+    def __init__(self, pages: torch.Tensor, page_size: int, head_dim: int, dtype=torch.bfloat16):
+        _dev(pages, "pages", torch.uint8)
+        if dtype not in _DTYPES:
+            raise ValueError(f"the cache's rows are bfloat16 or float16, not {dtype}")
+        self.pages, self.page_size, self.head_dim, self.dtype = pages, int(page_size), int(head_dim), dtype
+        self.num_pages, self.kv_heads = int(pages.shape[0]), int(pages.shape[1])
+        want = lora_kv4_page_bytes(page_size, self.kv_heads, head_dim)
+        if not want:
+            raise ValueError(f"pages of {page_size} tokens and heads of {head_dim} are not supported")
+        if pages.numel() != self.num_pages * want:
+            raise ValueError(f"a page of this cache has {want} bytes")
+        self._args = (pages.data_ptr(), self.num_pages, self.page_size, self.kv_heads, self.head_dim,
+                      _DTYPES[dtype])
+
+    @classmethod
+    def empty(cls, num_pages: int, page_size: int, kv_heads: int, head_dim: int,
+              dtype=torch.bfloat16, device="cuda") -> "Kv4Cache":
+        """A cache of its own memory, its contents unspecified."""
+        nbytes = lora_kv4_page_bytes(page_size, kv_heads, head_dim)
+        if not nbytes:
+            raise ValueError(f"pages of {page_size} tokens, {kv_heads} heads of {head_dim} are not supported")
+        tiles = kv_heads * (page_size // 16)
+        return cls(torch.empty(num_pages, kv_heads, page_size // 16, nbytes // tiles,
+                               dtype=torch.uint8, device=device), page_size, head_dim, dtype)
+
+
+def _slots(slot_map, n):
+    _dev(slot_map, "slot_map", torch.int64)
+    if slot_map.numel() != n:
+        raise ValueError(f"slot_map must have {n} entries, got {slot_map.numel()}")
+    return slot_map.data_ptr()
+
+
+def lora_kv4_append(cache: Kv4Cache, k, v, slot_map, err=None, stream=None):
+    """Quantise the rows ``k``, ``v`` [n, kv_heads, head_dim] and store row i at ``slot_map[i]``
+    (a negative slot is not stored).  The rows may be slices of a fused projection's output."""
+    n = k.shape[0]
+    if v.shape[0] != n:
+        raise ValueError("k and v must have the same number of rows")
+    _call("lora_kv4_append", *cache._args, *_rows(k, "k", cache.kv_heads, cache.head_dim, cache.dtype),
+          *_rows(v, "v", cache.kv_heads, cache.head_dim, cache.dtype), _slots(slot_map, n), n,
+          _at(err), _raw_stream(stream))
+
+
+def lora_kv4_read(cache: Kv4Cache, k, v, slot_map, err=None, stream=None):
+    """The values that stored rows stand for, into ``k``, ``v`` [n, kv_heads, head_dim]."""
+    n = k.shape[0]
+    if v.shape[0] != n:
+        raise ValueError("k and v must have the same number of rows")
+    _call("lora_kv4_read", *cache._args, *_rows(k, "k", cache.kv_heads, cache.head_dim, cache.dtype),
+          *_rows(v, "v", cache.kv_heads, cache.head_dim, cache.dtype), _slots(slot_map, n), n,
+          _at(err), _raw_stream(stream))
+
+
+def lora_kv4_attention_workspace(device="cuda") -> torch.Tensor:
+    """A workspace for ``lora_kv4_attention``, ready for its first use."""
+    L = lib()
+    ws = torch.empty(int(L.lora_kv4_attention_workspace_size()), dtype=torch.uint8, device=device)
+    ws[:int(L.lora_kv4_attention_zeroed_bytes())].zero_()
+    return ws
+
+
+# One workspace per (device, stream) for callers that pass none: calls on one
+# stream run in order and may share it.
+_ATTN_WS: dict = {}
+
+
+def _attn_workspace(device, stream):
+    s = torch.cuda.current_stream(device) if stream is None else stream
+    key = (device.index, s.cuda_stream)
+    ws = _ATTN_WS.get(key)
+    if ws is None:
+        with torch.cuda.stream(s):
+            ws = lora_kv4_attention_workspace(device)
+            if torch.cuda.is_current_stream_capturing():
+                return ws, s.cuda_stream  # the graph's own, zeroed by each replay
+        _ATTN_WS[key] = ws
+    return ws, s.cuda_stream
+
+
+def lora_kv4_attention(out, q, cache: Kv4Cache, block_table, row_start, seq_len, max_q_len: int,
+                       scale: float | None = None, window: int = 0, lse=None, workspace=None,
+                       err=None, stream=None):
+    """Causal attention of the rows ``q`` [n, q_heads, head_dim] over the cache, into ``out``.
+
+    ``row_start`` [n_reqs + 1] and ``seq_len`` [n_reqs] as ``lora_batch_plan`` writes them; a request's
+    keys must be stored before.  ``max_q_len``: the most rows of one request.  ``scale`` defaults to
+    head_dim ** -0.5; ``window`` > 0 limits a row to the last ``window`` tokens up to its own.  ``lse``
+    [n, q_heads] float32 receives the log of the softmax's denominator."""
+    n, q_heads = q.shape[0], q.shape[1]
+    B = seq_len.numel()
+    if out.shape != q.shape:
+        raise ValueError("out and q must have the same shape")
+    if lse is not None:
+        _dev(lse, "lse", torch.float32)
+        if lse.numel() != n * q_heads:
+            raise ValueError("lse must be [n, q_heads]")
+    if workspace is None:
+        workspace, raw = _attn_workspace(q.device, stream)
+    else:
+        raw = _raw_stream(stream)
+    _call("lora_kv4_attention", *_rows(out, "out", q_heads, cache.head_dim, cache.dtype),
+          *_rows(q, "q", q_heads, cache.head_dim, cache.dtype), n, q_heads, *cache._args,
+          *_table(block_table, B), _i32(row_start, "row_start", B + 1), _i32(seq_len, "seq_len"), B,
+          max_q_len, cache.head_dim ** -0.5 if scale is None else scale, window, _at(lse),
+          workspace.data_ptr(), workspace.numel(), _at(err), raw)
