@@ -10,6 +10,7 @@
 #include "host.cuh"
 #include "kv4.cuh"
 #include "kv4_attn.cuh"
+#include "kv4_prefill.cuh"
 #include "lora_delta.h"
 #include "plan.cuh"
 
@@ -90,6 +91,37 @@ int rows_call(bool store, const void* k, int64_t ld_k, const void* v, int64_t ld
     return cuda_status(cudaGetLastError());
   });
 }
+
+// Configurations of the decode kernel: warps by the registers of their sums,
+// stages by the shared memory that is left (about 40 KB of copies in flight a
+// CTA cover the latency of HBM).
+template <int D, bool BF16, int NT>
+using DecCfg = Dec<D, BF16, NT, (D * NT <= 128 ? 16 : 8),
+                   (D == 64 ? 8 : D == 256 ? (NT == 1 ? 5 : 4) : NT == 1 ? 5 : 8)>;
+
+template <class C>
+int launch_decode(const AttnArgs& a, cudaStream_t stream) {
+  const int smem = (int)C::smem(a.B);
+  if (prepare_kernel(kv4_decode_kernel<C>, smem, false) != cudaSuccess) return LORA_ERR_CUDA;
+  int ctas = sm_count();
+  if (ctas > kAttnMaxCtas) ctas = kAttnMaxCtas;
+  static const int alone = env_int("LORA_ATTN_ALONE", 128);
+  kv4_decode_kernel<C><<<ctas, C::THREADS, smem, stream>>>(a, alone, 1);
+  return cuda_status(cudaGetLastError());
+}
+
+// Floats of the partial results of every configuration.
+template <class C>
+constexpr size_t dec_partials() {
+  return (size_t)kAttnMaxCtas * (2 + C::NW) * C::SLOT;
+}
+constexpr size_t max2(size_t x, size_t y) { return x > y ? x : y; }
+constexpr size_t kPartialFloats =
+    max2(max2(max2(dec_partials<DecCfg<64, true, 1>>(), dec_partials<DecCfg<64, true, 2>>()),
+              max2(dec_partials<DecCfg<64, true, 4>>(), dec_partials<DecCfg<128, true, 1>>())),
+         max2(max2(dec_partials<DecCfg<128, true, 2>>(), dec_partials<DecCfg<128, true, 4>>()),
+              max2(dec_partials<DecCfg<256, true, 1>>(), dec_partials<DecCfg<256, true, 2>>())));
+constexpr size_t kCounterBytes = (size_t)kAttnMaxCtas * 4;
 
 }  // namespace
 
@@ -173,8 +205,8 @@ int lora_kv4_read(const void* pages, int64_t num_pages, int page_size, int kv_he
                    kv_heads, head_dim, dtype, slot_map, n, err_word, (cudaStream_t)stream);
 }
 
-size_t lora_kv4_attention_workspace_size(void) { return 256; }
-size_t lora_kv4_attention_zeroed_bytes(void) { return 256; }
+size_t lora_kv4_attention_workspace_size(void) { return kCounterBytes + kPartialFloats * 4; }
+size_t lora_kv4_attention_zeroed_bytes(void) { return kCounterBytes; }
 
 int lora_kv4_attention(void* out, int64_t ld_out, const void* q, int64_t ld_q, int n, int q_heads,
                        const void* pages, int64_t num_pages, int page_size, int kv_heads,
@@ -195,6 +227,8 @@ int lora_kv4_attention(void* out, int64_t ld_out, const void* q, int64_t ld_q, i
   if ((rc = check_rows(q, ld_q, n, q_heads * head_dim))) return rc;
   if (n_reqs > 1 && ld_table < max_pages) return LORA_ERR_SHAPE;
   if (!workspace || ws_bytes < lora_kv4_attention_workspace_size()) return LORA_ERR_WORKSPACE;
+  if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return LORA_ERR_ALIGN;
+  if ((int64_t)n_reqs * max_pages * (page_size / kKvTile) > INT32_MAX) return LORA_ERR_UNSUPPORTED;
   AttnArgs a = {};
   a.out = out;
   a.q = q;
@@ -218,9 +252,17 @@ int lora_kv4_attention(void* out, int64_t ld_out, const void* q, int64_t ld_q, i
   a.scale_log2 = (float)((double)scale * 1.4426950408889634);
   a.lse = lse;
   a.err = err_word;
+  a.wait_ns = g_wait_limit_ns.load(std::memory_order_relaxed);
+  a.counters = reinterpret_cast<uint32_t*>(workspace);
+  a.partials = reinterpret_cast<float*>(reinterpret_cast<char*>(workspace) + kCounterBytes);
+  const int64_t rows = (int64_t)max_q_len * a.group;
   return by_type(head_dim, dtype, [&](auto d, auto bf) {
     constexpr int D = decltype(d)::value;
     constexpr bool BF16 = decltype(bf)::value;
+    if (rows <= 8) return launch_decode<DecCfg<D, BF16, 1>>(a, (cudaStream_t)stream);
+    if (rows <= 16) return launch_decode<DecCfg<D, BF16, 2>>(a, (cudaStream_t)stream);
+    if constexpr (D < 256)
+      if (rows <= 32) return launch_decode<DecCfg<D, BF16, 4>>(a, (cudaStream_t)stream);
     kv4_attn_simple_kernel<D, BF16>
         <<<dim3((unsigned)n, (unsigned)q_heads), 128, 0, (cudaStream_t)stream>>>(a);
     return cuda_status(cudaGetLastError());
