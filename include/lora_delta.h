@@ -427,8 +427,10 @@ int lora_delta_fused_noalloc(void *out, int64_t ld_out, const void *x, int n, in
  * has these calls: a step's order is lora_batch_plan once, then in each layer
  * the projections with lora_delta_fused (seq_slot of the plan),
  * lora_kv4_append (slot_map of the plan) and lora_kv4_attention.
- * Limits: at most 4096 requests; n_reqs * max_pages and max_pages * page_size
- * below 2^31 (LORA_ERR_UNSUPPORTED beyond).
+ * Limits: at most 4096 requests of at most 2^29 tokens (max_pages * page_size);
+ * n_reqs * max_pages below 2^31, and n_reqs * max_pages * (page_size / 16) *
+ * kv_heads and n * q_heads / kv_heads below 2^31 for the attention
+ * (LORA_ERR_UNSUPPORTED beyond).
  */
 
 /*

@@ -2,19 +2,24 @@
 // key/value head (single tokens, a few tokens): the cache is read once and
 // codes go from shared memory into matrix-instruction operands with one AND.
 //
-// Per 16-token tile and (request, head), with R = 8 NT query rows as columns:
+// Per 16-token tile and (request, head), with 8 NT query rows as columns:
 //   S^T = K Q^T    A = codes of 16 tokens x 16 dims, B = q of 16 dims x 8 rows
-//   O^T = V^T P^T  A = codes of 16 dims x 16 tokens, B = p of 16 tokens x 8 rows
+//   O^T = V^T P^T  A = codes of 16 dims x 16 tokens, B = weights of 16 tokens x 8 rows
 // A code c in bits 0-3 of a 16-bit half is the f16 subnormal c 2^-24 and in
 // bits 4-7 c 2^-20.  Keys: the operand's odd code pairs are the latter, so q is
 // laid out with 2^-4 on the dims they meet.  Values: the odd pairs are rows
 // 8-15 of the product, which take 2^-4 at the end.  Scales and least values:
 //   s_t,g sum_d q_d c_d + m_t,g sum_d q_d    per group g of 64 dims (float32)
-//   sum_t (p_t s_t,g) c_t + sum_t p_t m_t,g  the first sum's weights in f16
-// q is brought to f16 by a power of two of its row (exact: 8 or 11 significant
-// bits), p s to f16 by a power of two of the largest s so far, with p <= 2^8
-// of a running maximum that follows lazily: 11 bits where f16 is normal, down
-// to 2^-21 of the largest weight.  Sums, maxima and the m terms are float32.
+//   sum_t (p_t s_t,g) c_t + sum_t p_t m_t,g
+// where the last sum and the denominator sum_t p_t are one more product, with
+// the m of each group and ones as its rows.  q is brought to f16 by a power of
+// two of its row (exact: 8 or 11 significant bits).  p is 2^6 exp2(s - max)
+// with a running maximum that follows lazily (p <= 2^14), rounded to f16 once;
+// p s is rounded to f16 with s taken relative to the largest so far.  Both
+// keep 11 bits down to 2^-20 of the largest weight.  Sums are float32.
+//
+// A warp works on units of two tiles, so that waits, votes and page look-ups
+// are paid once for 32 tokens.
 #pragma once
 
 #include "kv4.cuh"
@@ -28,12 +33,14 @@ struct AttnArgs {
   const void* q;
   int64_t ld_out, ld_q;
   int n, q_heads, heads, group;  // group = q_heads / heads
+  uint32_t group_inv;            // ceil(2^16 / group): x / group is (x group_inv) >> 16 for x < 32
   const uint8_t* pages;
   int64_t num_pages;
   int page_size;
   const int32_t* table;
   int64_t ld_table;
-  int max_pages;
+  int cap;           // max_pages * page_size tokens, at most 2^29
+  uint32_t tpp_inv;  // ceil(2^31 / (page_size / 16)), for tile numbers
   const int32_t* row_start;
   const int32_t* seq_len;
   int B, max_q_len, window;
@@ -44,6 +51,14 @@ struct AttnArgs {
   uint32_t* counters;  // [kAttnMaxCtas], zero between calls
   float* partials;     // [kAttnMaxCtas][2] slots, then [kAttnMaxCtas * warps] slots
 };
+
+// Division of a row number below 32 by the group.
+__device__ __forceinline__ int div_group(const AttnArgs& a, int x) { return (int)(((uint32_t)x * a.group_inv) >> 16); }
+
+// The page of a tile of 16 tokens.
+__device__ __forceinline__ int page_of_tile(const AttnArgs& a, int tile) {
+  return (int)(((uint64_t)(uint32_t)tile * a.tpp_inv) >> 31);
+}
 
 constexpr int kAttnMaxCtas = 256;
 constexpr float kNoMax = -1e30f;  // running maximum before any token
@@ -75,35 +90,45 @@ __device__ __forceinline__ uint32_t half2_bits(float lo, float hi) {
 // 2^e for -126 <= e <= 127.
 __device__ __forceinline__ float pow2i(int e) { return __int_as_float((e + 127) << 23); }
 
-template <int D_, bool BF16_, int NT_, int NW_, int STAGES_>
+template <int D_, bool BF16_, int NT_, int NW_>
 struct Dec {
-  static constexpr int D = D_, NT = NT_, NW = NW_, STAGES = STAGES_;
+  static constexpr int D = D_, NT = NT_, NW = NW_;
   static constexpr bool BF16 = BF16_;
   static constexpr int G = D / 64, W = D < 128 ? D : 128, NP = D / W, WD = W / 32;
   static constexpr int MM = D / 16;  // matrix products of a tile's values
   static constexpr int TILE = kv4_tile_bytes(D), HALF = kv4_half_bytes(D);
+  static constexpr int UNIT = 2 * kKvTile;  // tokens of a unit
   static constexpr int ROWS = 8 * NT;
   static constexpr int QREGS = D / 8;  // q operands of one column tile
   // operands of q stay in registers where there is room beside the sums
   static constexpr bool QSMEM = QREGS * NT > 32;
-  static constexpr int SLOT = 32 * (MM * 4 + 4) * NT;  // floats of a partial result
-  static constexpr int RING = STAGES * TILE > SLOT * 4 ? STAGES * TILE : SLOT * 4;
+  static constexpr int F4 = 32 * MM * NT;           // float4s of O in a partial result
+  static constexpr int SLOT = 4 * (F4 + 32 * NT);   // floats of a partial result
   static constexpr int QBYTES = QSMEM ? QREGS * NT * 32 * 4 : 0;
+  static constexpr int QROW = QSMEM ? 0 : ROWS * D * 2;  // bytes of the next item's q
   static constexpr int THREADS = NW * 32;
-  static constexpr size_t smem(int B) {
-    return (size_t)NW * (RING + QBYTES) + (size_t)(B + 1) * 4 + 16;
+  // a warp's ring of units; it also holds a partial result.  Two or three
+  // units a warp are some 150 KB in flight on an SM, more than HBM's latency
+  // asks for; deeper rings only make the loads that a warp waits for (q, page
+  // numbers) queue behind them.
+  static constexpr int MIN_STAGES = (SLOT * 4 + 2 * TILE - 1) / (2 * TILE) < 2 ? 2 : (SLOT * 4 + 2 * TILE - 1) / (2 * TILE);
+  static constexpr int MAX_STAGES = MIN_STAGES > (D == 64 ? 4 : 3) ? MIN_STAGES : (D == 64 ? 4 : 3);
+  static constexpr size_t smem(int B, int stages) {
+    return (size_t)NW * (stages * 2 * TILE + QROW + QBYTES) + (size_t)(B + 1) * 4 + 16;
   }
 };
 
-// Running state of one (request, head): O^T sums, the p m sums, denominators
-// and maxima of the lane's columns (2 c and 2 c + 1 of each column tile).
+// Running state of one (request, head): O^T sums, the sums of p m (lanes of
+// row group g < G) and of p (g == G), and the maxima (log2) of the lane's
+// columns, 2 c and 2 c + 1 of each column tile.
 template <class C>
 struct DecState {
   float o[C::NT][C::MM][4];
-  float z[C::NT][C::G][2];
+  float z[C::NT][4];
   float l[C::NT][2], m[C::NT][2];
-  int fexp;  // the f16 weights are p s 2^fexp
+  int sexp;  // scales are taken as s 2^-sexp
 };
+constexpr int kMinSexp = -14, kMaxSexp = 15;
 
 template <class C>
 __device__ __forceinline__ void dec_reset(DecState<C>& st) {
@@ -114,28 +139,26 @@ __device__ __forceinline__ void dec_reset(DecState<C>& st) {
 #pragma unroll
       for (int j = 0; j < 4; ++j) st.o[n][i][j] = 0.0f;
 #pragma unroll
-    for (int g = 0; g < C::G; ++g) st.z[n][g][0] = st.z[n][g][1] = 0.0f;
+    for (int j = 0; j < 4; ++j) st.z[n][j] = 0.0f;
     st.l[n][0] = st.l[n][1] = 0.0f;
     st.m[n][0] = st.m[n][1] = kNoMax;
   }
-  st.fexp = 126;
+  st.sexp = kMinSexp;
 }
 
-// Sums over the lanes that share columns; o becomes the sum of p v in float32.
+// The sums of p m and p to every lane; o becomes the sum of p v in float32.
 template <class C>
 __device__ __forceinline__ void dec_finish(DecState<C>& st) {
-  const float f0 = pow2i(-st.fexp < -126 ? -126 : -st.fexp) * 16777216.0f, f1 = f0 * 0.0625f;
+  const int c = threadIdx.x & 3;
+  const float f0 = pow2i(18 + st.sexp), f1 = f0 * 0.0625f;  // 2^24 for the codes, 2^-6 for p
 #pragma unroll
   for (int n = 0; n < C::NT; ++n)
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
-#pragma unroll
-      for (int d = 4; d < 32; d <<= 1) st.l[n][e] += __shfl_xor_sync(0xffffffffu, st.l[n][e], d);
+      st.l[n][e] = __shfl_sync(0xffffffffu, st.z[n][e], C::G * 4 + c) * 0.015625f;
 #pragma unroll
       for (int g = 0; g < C::G; ++g) {
-        float z = st.z[n][g][e];
-#pragma unroll
-        for (int d = 4; d < 32; d <<= 1) z += __shfl_xor_sync(0xffffffffu, z, d);
+        const float z = __shfl_sync(0xffffffffu, st.z[n][e], g * 4 + c) * 0.015625f;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           st.o[n][4 * g + i][e] = fmaf(st.o[n][4 * g + i][e], f0, z);
@@ -145,7 +168,8 @@ __device__ __forceinline__ void dec_finish(DecState<C>& st) {
     }
 }
 
-// A finished state to / added from a slot (float4s of the 32 lanes).
+// A finished state to a slot: the float4s of O, then (m, l) of the columns, a
+// lane's next to one another's.
 template <class C>
 __device__ __forceinline__ void dec_save(const DecState<C>& st, float* slot, int lane) {
   float4* p = reinterpret_cast<float4*>(slot) + lane;
@@ -154,31 +178,16 @@ __device__ __forceinline__ void dec_save(const DecState<C>& st, float* slot, int
 #pragma unroll
     for (int i = 0; i < C::MM; ++i)
       p[(n * C::MM + i) * 32] = make_float4(st.o[n][i][0], st.o[n][i][1], st.o[n][i][2], st.o[n][i][3]);
-    p[(C::NT * C::MM + n) * 32] = make_float4(st.m[n][0], st.m[n][1], st.l[n][0], st.l[n][1]);
+    p[C::F4 + n * 32] = make_float4(st.m[n][0], st.m[n][1], st.l[n][0], st.l[n][1]);
   }
 }
-template <class C>
-__device__ __forceinline__ void dec_add(DecState<C>& st, const float* slot, int lane) {
-  const float4* p = reinterpret_cast<const float4*>(slot) + lane;
-#pragma unroll
-  for (int n = 0; n < C::NT; ++n) {
-    const float4 ml = p[(C::NT * C::MM + n) * 32];
-    const float m0 = fmaxf(st.m[n][0], ml.x), m1 = fmaxf(st.m[n][1], ml.y);
-    const float a0 = exp2_fast(st.m[n][0] - m0), a1 = exp2_fast(st.m[n][1] - m1);
-    const float b0 = exp2_fast(ml.x - m0), b1 = exp2_fast(ml.y - m1);
-    st.m[n][0] = m0;
-    st.m[n][1] = m1;
-    st.l[n][0] = st.l[n][0] * a0 + ml.z * b0;
-    st.l[n][1] = st.l[n][1] * a1 + ml.w * b1;
-#pragma unroll
-    for (int i = 0; i < C::MM; ++i) {
-      const float4 v = p[(n * C::MM + i) * 32];
-      st.o[n][i][0] = st.o[n][i][0] * a0 + v.x * b0;
-      st.o[n][i][1] = st.o[n][i][1] * a1 + v.y * b1;
-      st.o[n][i][2] = st.o[n][i][2] * a0 + v.z * b0;
-      st.o[n][i][3] = st.o[n][i][3] * a1 + v.w * b1;
-    }
-  }
+// (o, ml) += (o2, ml2), each sums relative to its own maxima.
+__device__ __forceinline__ void dec_join(float4& o, float4& ml, const float4& o2, const float4& ml2) {
+  const float m0 = fmaxf(ml.x, ml2.x), m1 = fmaxf(ml.y, ml2.y);
+  const float a0 = exp2_fast(ml.x - m0), a1 = exp2_fast(ml.y - m1);
+  const float b0 = exp2_fast(ml2.x - m0), b1 = exp2_fast(ml2.y - m1);
+  ml = make_float4(m0, m1, ml.z * a0 + ml2.z * b0, ml.w * a1 + ml2.w * b1);
+  o = make_float4(o.x * a0 + o2.x * b0, o.y * a1 + o2.y * b1, o.z * a0 + o2.z * b0, o.w * a1 + o2.w * b1);
 }
 
 // What a (request, head) is: its rows, and the tiles that they see.
@@ -186,36 +195,35 @@ struct DecReq {
   int row0, rows;     // first row of the batch; query rows (tokens * group)
   int pos0;           // position of the first row
   int seq;            // tokens that may be seen (clipped to the table)
-  int tile0, tiles;   // first tile and number of tiles, 0 for a request without rows here
+  int tile0, units;   // first tile and number of units, 0 for a request without rows here
 };
 
 __device__ __forceinline__ DecReq dec_request(const AttnArgs& a, int b, int max_rows, uint32_t& bad) {
   DecReq r;
   const int start = a.row_start[b], end = a.row_start[b + 1];
-  const int64_t cap = (int64_t)a.max_pages * a.page_size;
   const int seq = a.seq_len[b];
   r.row0 = start;
   r.rows = 0;
   r.pos0 = 0;
   r.seq = 0;
   r.tile0 = 0;
-  r.tiles = 0;
+  r.units = 0;
   if (end <= start) return r;
   if (start < 0 || end > a.n || end - start > a.max_q_len) {
     bad |= LORA_DEV_ERR_LENGTH;
     return r;
   }
-  const int64_t rows = (int64_t)(end - start) * a.group;
+  const int rows = (end - start) * a.group;
   if (rows > max_rows) return r;
-  r.rows = (int)rows;
-  if (seq < 0 || seq > cap) bad |= LORA_DEV_ERR_LENGTH;
+  r.rows = rows;
+  if (seq < 0 || seq > a.cap) bad |= LORA_DEV_ERR_LENGTH;
   r.pos0 = seq - (end - start);
-  r.seq = seq < 0 ? 0 : (seq > cap ? (int)cap : seq);
+  r.seq = seq < 0 ? 0 : (seq > a.cap ? a.cap : seq);
   const int first = a.window > 0 && r.pos0 + 1 - a.window > 0 ? r.pos0 + 1 - a.window : 0;
   r.tile0 = first / kKvTile;
   const int last = (r.seq + kKvTile - 1) / kKvTile;
-  // (a request that sees nothing keeps one tile, all of it masked)
-  r.tiles = last > r.tile0 ? last - r.tile0 : 1;
+  // (a request that sees nothing keeps one unit, all of it masked)
+  r.units = last > r.tile0 ? (last - r.tile0 + 1) / 2 : 1;
   return r;
 }
 
@@ -230,8 +238,8 @@ __device__ __forceinline__ void dec_write(const AttnArgs& a, const DecReq& r, in
     for (int e = 0; e < 2; ++e) {
       const int rr = n * 8 + 2 * c + e;
       if (rr >= r.rows) continue;
-      const int j = rr / a.group, head = h * a.group + rr - j * a.group;
-      const float l = st.l[n][e], inv = l != 0.0f ? 1.0f / l : 0.0f;
+      const int j = div_group(a, rr), head = h * a.group + rr - j * a.group;
+      const float l = st.l[n][e], inv = l != 0.0f ? __frcp_rn(l) : 0.0f;
       uint16_t* out = reinterpret_cast<uint16_t*>(a.out) + (int64_t)(r.row0 + j) * a.ld_out + head * C::D;
 #pragma unroll
       for (int q = 0; q < C::G; ++q) {
@@ -248,46 +256,336 @@ __device__ __forceinline__ void dec_write(const AttnArgs& a, const DecReq& r, in
     }
 }
 
-// Zeros to the rows of a range.
-template <bool BF16, int D>
-__device__ void zero_rows(const AttnArgs& a, int lo, int hi, int part, int parts) {
-  const int per = a.q_heads * (D / 8);
-  for (int64_t i = (int64_t)part * blockDim.x + threadIdx.x; i < (int64_t)(hi - lo) * per;
-       i += (int64_t)parts * blockDim.x) {
-    const int64_t row = lo + i / per;
-    const int k = (int)(i % per);
-    *reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(a.out) + row * a.ld_out + k * 8) =
-        make_uint4(0, 0, 0, 0);
-    if (a.lse && k % (D / 8) == 0) a.lse[row * a.q_heads + k / (D / 8)] = -INFINITY;
+// The float4 number x of a joined result to out: two columns' two adjacent dims.
+template <class C>
+__device__ __forceinline__ void dec_write_part(const AttnArgs& a, const DecReq& r, int h, int x,
+                                               const float4& o, const float4& ml) {
+  const int lane = x & 31, g = lane >> 2, c = lane & 3, i = (x >> 5) % C::MM, n = (x >> 5) / C::MM;
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {
+    const int rr = n * 8 + 2 * c + e;
+    if (rr >= r.rows) continue;
+    const int j = div_group(a, rr), head = h * a.group + rr - j * a.group;
+    const float l = e ? ml.w : ml.z, inv = l != 0.0f ? __frcp_rn(l) : 0.0f;
+    uint16_t* out = reinterpret_cast<uint16_t*>(a.out) + (int64_t)(r.row0 + j) * a.ld_out + head * C::D;
+    *reinterpret_cast<uint32_t*>(out + (i / 4) * 64 + 8 * g + 2 * (i % 4)) =
+        pack2<C::BF16>((e ? o.y : o.x) * inv, (e ? o.w : o.z) * inv);
+    if (a.lse && i == 0 && g == 0)
+      a.lse[(int64_t)(r.row0 + j) * a.q_heads + head] =
+          l != 0.0f ? ((e ? ml.y : ml.x) + log2f(l)) * 0.69314718055994531f : -INFINITY;
   }
 }
 
-// The tiles of all (request, head)s, laid end to end, are shared out evenly:
-// a CTA takes a contiguous range and its warps contiguous parts of that.  A
-// warp streams its tiles through a ring of bulk copies of its own.  Where a
-// (request, head) ends inside a warp's part it is written; what crosses parts
-// is joined over the CTA's warps, and over CTAs by the last of them to arrive,
-// in the order of the tiles (so results do not depend on the order of events).
+// Zeros to the rows [lo, hi), shared out over `parts` CTAs.
 template <class C>
-__global__ void __launch_bounds__(C::THREADS, 1) kv4_decode_kernel(const AttnArgs a, int min_tiles,
-                                                                   int only) {
+__device__ __noinline__ void zero_rows(uint16_t* out, int64_t ld_out, int q_heads, float* lse, int lo,
+                                       int hi, int part, int parts) {
+  const int width = q_heads * (C::D / 8);
+  for (int row = lo + part; row < hi; row += parts) {
+    for (int k = threadIdx.x; k < width; k += blockDim.x)
+      *reinterpret_cast<uint4*>(out + row * ld_out + k * 8) = make_uint4(0, 0, 0, 0);
+    if (lse)
+      for (int k = threadIdx.x; k < q_heads; k += blockDim.x) lse[(int64_t)row * q_heads + k] = -INFINITY;
+  }
+}
+
+// One unit: scores, weights and sums of the two tiles at `unit`.  With `edge`
+// (of the whole warp) some row does not see some token, or a tile was not read
+// (its bit of `got` is 0).
+template <class C>
+__device__ __forceinline__ void dec_unit(const AttnArgs& a, const DecReq& r, DecState<C>& st,
+                                         uint8_t* unit, int tok0, uint32_t got, bool edge, int pos1,
+                                         const uint32_t* q_s,
+                                         const uint32_t (&qf)[C::QSMEM ? 1 : C::NT][C::QSMEM ? 1 : C::QREGS],
+                                         const float (&qa)[C::NT][2], const float (&qb)[C::NT][C::G][2],
+                                         float (&thr)[C::NT][2], int lane) {
+  const int g = lane >> 2, c = lane & 3;
+  auto seen_by_any = [&](int t, int tok) {
+    return ((got >> t) & 1u) && tok < r.seq && tok <= pos1 && (a.window <= 0 || tok > r.pos0 - a.window);
+  };
+  auto seen_by = [&](int tok, int col) {
+    const int pos = r.pos0 + div_group(a, col);
+    return tok <= pos && (a.window <= 0 || tok > pos - a.window);
+  };
+  if (edge) {
+    // values' scales of tokens that no row sees may hold anything; one that is
+    // not finite is left out here and makes the rows that do see it NaN
+    uint32_t* sp = reinterpret_cast<uint32_t*>(unit + (lane >> 4) * C::TILE + C::HALF + 8 * C::D) + (lane & 15) * C::G;
+    const bool any = seen_by_any(lane >> 4, tok0 + lane);
+    bool odd = false;
+#pragma unroll
+    for (int q = 0; q < C::G; ++q)
+      odd |= (sp[q] & 0x7c00u) == 0x7c00u || (sp[q] & 0x7c000000u) == 0x7c000000u;
+    if (!any || odd) {
+#pragma unroll
+      for (int q = 0; q < C::G; ++q) sp[q] = 0;
+    }
+    for (uint32_t lost = __ballot_sync(0xffffffffu, any && odd); lost; lost &= lost - 1)
+#pragma unroll
+      for (int n = 0; n < C::NT; ++n)
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+          if (seen_by(tok0 + __ffs(lost) - 1, n * 8 + 2 * c + k)) st.z[n][k] = __int_as_float(0x7fffffff);
+    fence_proxy_async_smem();  // (the stage is next written by a bulk copy)
+    __syncwarp();
+  }
+  float s[2][C::NT][4];
+  bool up = false;
+#pragma unroll
+  for (int t = 0; t < 2; ++t) {
+    const uint8_t* tile = unit + t * C::TILE;
+    float sc[C::NT][C::G][4];
+#pragma unroll
+    for (int n = 0; n < C::NT; ++n)
+#pragma unroll
+      for (int q = 0; q < C::G; ++q)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) sc[n][q][i] = 0.0f;
+#pragma unroll
+    for (int p = 0; p < C::NP; ++p) {
+      uint32_t k0[C::WD], k1[C::WD];  // tokens g and g + 8
+      const uint8_t* kp = tile + p * 8 * C::W + g * (C::W / 2) + c * (C::W / 8);
+      if (C::WD == 4) {
+        *reinterpret_cast<uint4*>(k0) = *reinterpret_cast<const uint4*>(kp);
+        *reinterpret_cast<uint4*>(k1) = *reinterpret_cast<const uint4*>(kp + 4 * C::W);
+      } else {
+        *reinterpret_cast<uint2*>(k0) = *reinterpret_cast<const uint2*>(kp);
+        *reinterpret_cast<uint2*>(k1) = *reinterpret_cast<const uint2*>(kp + 4 * C::W);
+      }
+#pragma unroll
+      for (int w = 0; w < C::WD; ++w)
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          const uint32_t x0 = u ? k0[w] >> 8 : k0[w], x1 = u ? k1[w] >> 8 : k1[w];
+          const uint32_t a0 = x0 & 0x000f000fu, a2 = x0 & 0x00f000f0u;
+          const uint32_t a1 = x1 & 0x000f000fu, a3 = x1 & 0x00f000f0u;
+          const int at = (p * C::WD + w) * 4 + 2 * u;
+#pragma unroll
+          for (int n = 0; n < C::NT; ++n) {
+            const uint32_t b0 = C::QSMEM ? q_s[(n * C::QREGS + at) * 32] : qf[C::QSMEM ? 0 : n][C::QSMEM ? 0 : at];
+            const uint32_t b1 = C::QSMEM ? q_s[(n * C::QREGS + at + 1) * 32] : qf[C::QSMEM ? 0 : n][C::QSMEM ? 0 : at + 1];
+            mma_f16(sc[n][(p * C::WD + w) / 2], a0, a1, a2, a3, b0, b1);
+          }
+        }
+    }
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      float2 ks[C::G];  // scales and least values of token g + 8 u
+#pragma unroll
+      for (int q = 0; q < C::G; ++q)
+        ks[q] = __half22float2(*reinterpret_cast<const __half2*>(tile + 8 * C::D + ((g + 8 * u) * C::G + q) * 4));
+#pragma unroll
+      for (int n = 0; n < C::NT; ++n)
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          float v = ks[0].x * sc[n][0][2 * u + k];
+#pragma unroll
+          for (int q = 1; q < C::G; ++q) v = fmaf(ks[q].x, sc[n][q][2 * u + k], v);
+#pragma unroll
+          for (int q = 0; q < C::G; ++q) v = fmaf(ks[q].y, qb[n][q][k], v);
+          s[t][n][2 * u + k] = v;
+        }
+    }
+  }
+  if (edge) {
+#pragma unroll
+    for (int t = 0; t < 2; ++t)
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const int tok = tok0 + t * kKvTile + g + 8 * u;
+        const bool any = seen_by_any(t, tok);
+#pragma unroll
+        for (int n = 0; n < C::NT; ++n)
+#pragma unroll
+          for (int k = 0; k < 2; ++k)
+            if (!any || !seen_by(tok, n * 8 + 2 * c + k)) s[t][n][2 * u + k] = -INFINITY;
+      }
+  }
+#pragma unroll
+  for (int n = 0; n < C::NT; ++n)
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+      up |= fmaxf(fmaxf(s[0][n][k], s[0][n][2 + k]), fmaxf(s[1][n][k], s[1][n][2 + k])) > thr[n][k];
+
+  // scales and least values of tokens 2 c, 2 c + 1 and 2 c + 8, 2 c + 9, paired
+  __half2 vs[2][2][C::G], vm[2][2][C::G];
+#pragma unroll
+  for (int t = 0; t < 2; ++t)
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      uint32_t x[2][C::G];
+      const uint8_t* sp = unit + t * C::TILE + C::HALF + 8 * C::D + (2 * c + 8 * u) * C::G * 4;
+      if (C::G == 1) {
+        const uint2 v = *reinterpret_cast<const uint2*>(sp);
+        x[0][0] = v.x;
+        x[1][0] = v.y;
+      } else {
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+#pragma unroll
+          for (int q = 0; q < C::G; q += 2)
+            *reinterpret_cast<uint2*>(&x[e][q]) = *reinterpret_cast<const uint2*>(sp + (e * C::G + q) * 4);
+      }
+#pragma unroll
+      for (int q = 0; q < C::G; ++q) {
+        const uint32_t lo = __byte_perm(x[0][q], x[1][q], 0x5410), hi = __byte_perm(x[0][q], x[1][q], 0x7632);
+        vs[t][u][q] = *reinterpret_cast<const __half2*>(&lo);
+        vm[t][u][q] = *reinterpret_cast<const __half2*>(&hi);
+      }
+    }
+  __half2 top2 = vs[0][0][0];
+#pragma unroll
+  for (int t = 0; t < 2; ++t)
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+#pragma unroll
+      for (int q = 0; q < C::G; ++q) top2 = __hmax2(top2, vs[t][u][q]);
+  const float stop = __half2float(__hmax(__low2half(top2), __high2half(top2)));
+  up |= stop >= pow2i(st.sexp + 1);
+
+  // new maxima only where a score is 2^8 above the old one, or a scale 2^1
+  // above its unit
+  if (__any_sync(0xffffffffu, up)) {
+    float smax = 0.0f;  // (a scale that is not finite poisons its own rows only)
+#pragma unroll
+    for (int t = 0; t < 2; ++t)
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int q = 0; q < C::G; ++q) {
+          const float2 f = __half22float2(vs[t][u][q]);
+          smax = fmaxf(smax, fmaxf(f.x <= 65504.0f ? f.x : 0.0f, f.y <= 65504.0f ? f.y : 0.0f));
+        }
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) smax = fmaxf(smax, __shfl_xor_sync(0xffffffffu, smax, d));
+    int e = (int)((__float_as_uint(smax) >> 23) & 255u) - 127;
+    e = e > kMaxSexp ? kMaxSexp : e;
+    e = e < st.sexp ? st.sexp : e;
+    const float fold = pow2i(st.sexp - e);
+    st.sexp = e;
+#pragma unroll
+    for (int n = 0; n < C::NT; ++n)
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        float top = fmaxf(fmaxf(s[0][n][k], s[0][n][2 + k]), fmaxf(s[1][n][k], s[1][n][2 + k]));
+#pragma unroll
+        for (int d = 4; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+        const float m1 = fmaxf(st.m[n][k], top * qa[n][k]), keep = exp2_fast(st.m[n][k] - m1);
+        st.m[n][k] = m1;
+        thr[n][k] = __fdividef(m1 + 8.0f, qa[n][k]);
+        st.z[n][k] *= keep;
+        const float ko = keep * fold;
+#pragma unroll
+        for (int i = 0; i < C::MM; ++i) {
+          st.o[n][i][k] *= ko;
+          st.o[n][i][2 + k] *= ko;
+        }
+      }
+  }
+
+  const __half2 unit_s = __float2half2_rn(pow2i(-st.sexp));
+  const uint32_t ones = g == C::G ? 0x3c003c00u : 0u;
+#pragma unroll
+  for (int t = 0; t < 2; ++t) {
+    uint32_t pt[C::NT][2];  // weights of tokens 2 c, + 1 and + 8, + 9 of row g
+#pragma unroll
+    for (int n = 0; n < C::NT; ++n)
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        float p[2];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          p[k] = exp2_fast(fmaf(s[t][n][2 * u + k], qa[n][k], 6.0f - st.m[n][k]));
+          if (edge && s[t][n][2 * u + k] == -INFINITY) p[k] = 0.0f;
+        }
+        pt[n][u] = transpose8(half2_bits(p[0], p[1]));
+      }
+    uint32_t za[2];
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      za[u] = ones;
+#pragma unroll
+      for (int q = 0; q < C::G; ++q)
+        if (g == q) za[u] = *reinterpret_cast<const uint32_t*>(&vm[t][u][q]);
+    }
+    uint32_t pw[C::NT][C::G][2];
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+#pragma unroll
+      for (int q = 0; q < C::G; ++q) {
+        const __half2 f = __hmul2(vs[t][u][q], unit_s);
+#pragma unroll
+        for (int n = 0; n < C::NT; ++n) {
+          const __half2 w = __hmul2(*reinterpret_cast<const __half2*>(&pt[n][u]), f);
+          pw[n][q][u] = *reinterpret_cast<const uint32_t*>(&w);
+        }
+      }
+#pragma unroll
+    for (int n = 0; n < C::NT; ++n) mma_f16(st.z[n], za[0], 0u, za[1], 0u, pt[n][0], pt[n][1]);
+#pragma unroll
+    for (int p = 0; p < C::NP; ++p) {
+      uint32_t v0[C::WD], v1[C::WD];  // tokens 2 c, + 1 and 2 c + 8, + 9
+      const uint8_t* vp = unit + t * C::TILE + C::HALF + p * 8 * C::W + g * (C::W / 2) + c * (C::W / 8);
+      if (C::WD == 4) {
+        *reinterpret_cast<uint4*>(v0) = *reinterpret_cast<const uint4*>(vp);
+        *reinterpret_cast<uint4*>(v1) = *reinterpret_cast<const uint4*>(vp + 4 * C::W);
+      } else {
+        *reinterpret_cast<uint2*>(v0) = *reinterpret_cast<const uint2*>(vp);
+        *reinterpret_cast<uint2*>(v1) = *reinterpret_cast<const uint2*>(vp + 4 * C::W);
+      }
+#pragma unroll
+      for (int w = 0; w < C::WD; ++w)
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          const uint32_t x0 = u ? v0[w] >> 8 : v0[w], x1 = u ? v1[w] >> 8 : v1[w];
+          const uint32_t a0 = x0 & 0x000f000fu, a1 = x0 & 0x00f000f0u;
+          const uint32_t a2 = x1 & 0x000f000fu, a3 = x1 & 0x00f000f0u;
+          const int q = (p * C::WD + w) / 2;
+#pragma unroll
+          for (int n = 0; n < C::NT; ++n)
+            mma_f16(st.o[n][(p * C::WD + w) * 2 + u], a0, a1, a2, a3, pw[n][q][0], pw[n][q][1]);
+        }
+    }
+  }
+}
+
+// The work of all (request, head)s, laid end to end, is shared out evenly: a
+// CTA takes a contiguous range and its warps contiguous parts of that.  An item
+// counts its units and kItemCost more, for what its beginning and end take.  A
+// warp streams its units through a ring of bulk copies of its own; the next
+// item's q comes by asynchronous copies meanwhile.  Where a (request, head)
+// lies inside a warp's part it is written; what crosses parts is joined over
+// the CTA's warps, and over CTAs by the last of them to arrive, in the order of
+// the units (so results do not depend on the order of events).
+constexpr int kItemCost = 2;
+
+template <class C>
+__global__ void __launch_bounds__(C::THREADS, 1) kv4_decode_kernel(const AttnArgs a, int stages,
+                                                                   int min_units) {
   extern __shared__ __align__(128) uint8_t dec_smem[];
-  __shared__ uint64_t bars[C::NW][C::STAGES];
+  __shared__ uint64_t bars[C::NW][C::MAX_STAGES];
   __shared__ int scan_s[C::NW];
-  __shared__ int max_s, over_s, last_s;
-  __shared__ int seg_b[C::NW][2], seg_h[C::NW][2];  // partial results of the warps (-1: none)
-  __shared__ int64_t seg_lo[C::NW][2], seg_hi[C::NW][2];
+  __shared__ int max_s, over_s, last_s, chains_s;
+  // segments of items that cross the warps' parts: [0] the warp's first, [1]
+  // its last (b -1: none), and the items' first and last + 1 unit
+  __shared__ int seg_b[C::NW][2], seg_h[C::NW][2], seg_lo[C::NW][2], seg_hi[C::NW][2];
+  __shared__ int chain_s[2 * C::NW];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, c = lane & 3;
-  uint8_t* ring = dec_smem + warp * C::RING;
-  uint32_t* q_s = reinterpret_cast<uint32_t*>(dec_smem + C::NW * C::RING + warp * C::QBYTES) + lane;
-  int32_t* pre = reinterpret_cast<int32_t*>(dec_smem + C::NW * (C::RING + C::QBYTES));
+  const int ring_bytes = stages * 2 * C::TILE;
+  uint8_t* ring = dec_smem + warp * ring_bytes;
+  uint8_t* q_next = dec_smem + C::NW * ring_bytes + warp * C::QROW;
+  uint32_t* q_s = reinterpret_cast<uint32_t*>(dec_smem + C::NW * (ring_bytes + C::QROW) + warp * C::QBYTES) + lane;
+  int32_t* pre = reinterpret_cast<int32_t*>(dec_smem + C::NW * (ring_bytes + C::QROW + C::QBYTES));
   const int cta = blockIdx.x, n_ctas = gridDim.x;
 
-  if (lane < C::STAGES) mbar_init(&bars[warp][lane], 1);
+  if (lane < stages) mbar_init(&bars[warp][lane], 1);
+  if (lane < 2) seg_b[warp][lane] = -1;
   if (tid == 0) max_s = over_s = 0;
   fence_barrier_init();
+  // (what the kernel before wrote is read from here on)
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   __syncthreads();
-  // tiles of one head, summed over the requests
+  // work of one head, summed over the requests
   uint32_t bad = 0;
   {
     const int per = (a.B + C::THREADS - 1) / C::THREADS;
@@ -295,10 +593,10 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_decode_kernel(const AttnArg
     for (int i = 0; i < per; ++i) {
       const int b = tid * per + i;
       if (b >= a.B) break;
-      const DecReq r = dec_request(a, b, C::ROWS, bad);
-      pre[b] = r.tiles;
-      sum += r.tiles;
-      most = most > r.tiles ? most : r.tiles;
+      const int units = dec_request(a, b, C::ROWS, bad).units;
+      pre[b] = units ? units + kItemCost : 0;
+      sum += pre[b];
+      most = most > units ? most : units;
     }
     if (bad) over_s = 1;
     int inc = sum;
@@ -324,143 +622,178 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_decode_kernel(const AttnArg
   }
   __syncthreads();
   if (cta == 0 && bad) set_error(a.err, bad);
-  if (only) {  // rows that no request here covers
-    const int r0 = a.B > 0 ? a.row_start[0] : 0, r1 = a.B > 0 ? a.row_start[a.B] : 0;
-    if (r0 > 0) zero_rows<C::BF16, C::D>(a, 0, r0 < a.n ? r0 : a.n, cta, n_ctas);
-    if (r1 < a.n) zero_rows<C::BF16, C::D>(a, r1 < 0 ? 0 : r1, a.n, cta, n_ctas);
-    if (over_s)
-      for (int b = 0; b < a.B; ++b)
-        if (pre[b + 1] == pre[b]) {
-          const int lo = a.row_start[b], hi = a.row_start[b + 1];
-          zero_rows<C::BF16, C::D>(a, lo < 0 ? 0 : lo, hi < a.n ? hi : a.n, cta, n_ctas);
-        }
+  // rows that no request covers, and requests that are refused
+  uint16_t* const out = reinterpret_cast<uint16_t*>(a.out);
+  const int first_row = a.B > 0 ? a.row_start[0] : a.n, last_row = a.B > 0 ? a.row_start[a.B] : a.n;
+  if (first_row > 0 || last_row < a.n || over_s) {
+#pragma unroll 1
+    for (int b = over_s ? -1 : a.B - 1; b <= a.B; ++b) {
+      int lo, hi;
+      if (b < 0 || (b == a.B - 1 && !over_s)) {
+        lo = 0;
+        hi = first_row;
+      } else if (b == a.B) {
+        lo = last_row;
+        hi = a.n;
+      } else {
+        if (pre[b + 1] != pre[b]) continue;
+        lo = a.row_start[b];
+        hi = a.row_start[b + 1];
+      }
+      zero_rows<C>(out, a.ld_out, a.q_heads, a.lse, lo < 0 ? 0 : lo, hi < a.n ? hi : a.n, cta, n_ctas);
+    }
   }
 
-  // this CTA's range of tiles
-  const int64_t total = (int64_t)pre[a.B] * a.heads;
-  int64_t t0, t1, chunk;
-  if (a.B * a.heads <= n_ctas && max_s <= min_tiles) {  // a CTA a (request, head)
+  // this CTA's range
+  const int total = pre[a.B] * a.heads;
+  int t0, t1, chunk;
+  if (a.B * a.heads <= n_ctas && max_s <= min_units) {  // a CTA a (request, head)
     chunk = 0;
     t0 = t1 = total;
     const int b = cta / a.heads;
     if (b < a.B) {
-      const int tiles = pre[b + 1] - pre[b];
-      t0 = (int64_t)pre[b] * a.heads + (int64_t)(cta - b * a.heads) * tiles;
-      t1 = t0 + tiles;
+      const int cost = pre[b + 1] - pre[b];
+      t0 = pre[b] * a.heads + (cta - b * a.heads) * cost;
+      t1 = t0 + cost - (cost ? kItemCost : 0);
     }
   } else {
     chunk = (total + n_ctas - 1) / n_ctas;
     if (chunk < C::NW) chunk = C::NW;
-    t0 = cta * chunk < total ? cta * chunk : total;
-    t1 = t0 + chunk < total ? t0 + chunk : total;
+    t0 = (int64_t)cta * chunk < total ? cta * chunk : total;
+    t1 = total - t0 < chunk ? total : t0 + chunk;
   }
   if (t0 >= t1) return;
-  const int part = (int)((t1 - t0 + C::NW - 1) / C::NW);
-  const int64_t w0 = t0 + (int64_t)warp * part < t1 ? t0 + (int64_t)warp * part : t1;
-  const int64_t w1 = w0 + part < t1 ? w0 + part : t1;
+  const int part = (t1 - t0 + C::NW - 1) / C::NW;
+  const int w0 = t0 + warp * part < t1 ? t0 + warp * part : t1;
+  const int w1 = w0 + part < t1 ? w0 + part : t1;
 
-  float* my_first = a.partials + ((int64_t)2 * kAttnMaxCtas + (int64_t)cta * C::NW + warp) * C::SLOT;
-  float* my_last = reinterpret_cast<float*>(ring);
-  if (lane < 2) seg_b[warp][lane] = -1;
-  __syncwarp();
-
-  // the (request, head, tile) of a flat number; the request's first tile in pre
-  auto find = [&](int64_t f, int& b, int& h, int& tile) {
+  // a place in the work: request, head, unit (up to units + kItemCost)
+  struct Place {
+    int b, h, u;
+  };
+  auto find = [&](int f) {
     int lo = 0, hi = a.B;
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
-      if ((int64_t)pre[mid] * a.heads <= f) lo = mid; else hi = mid;
+      if (pre[mid] * a.heads <= f) lo = mid; else hi = mid;
     }
-    b = lo;
-    const int tiles = pre[b + 1] - pre[b];
-    const int64_t rest = f - (int64_t)pre[b] * a.heads;
-    h = (int)(rest / tiles);
-    tile = (int)(rest - (int64_t)h * tiles);
+    const int cost = pre[lo + 1] - pre[lo], rest = f - pre[lo] * a.heads, h = rest / cost;
+    return Place{lo, h, rest - h * cost};
+  };
+  auto next_item = [&](Place& p) {  // (there is one)
+    p.u = 0;
+    if (++p.h < a.heads) return;
+    p.h = 0;
+    do ++p.b; while (pre[p.b + 1] == pre[p.b]);
   };
 
   DecState<C> st;
-  if (w0 < w1) {
-    uint32_t unused = 0;
-    // the producer's place: request pb, head ph, tile pt of it; pages of the
-    // next 32 tiles are held one a lane
-    int pb, ph, pt, pblk = 0;
-    int64_t pf = w0;
-    find(w0, pb, ph, pt);
-    DecReq pr = dec_request(a, pb, C::ROWS, unused);
-    int page_reg = -1;
+  uint32_t unused = 0;
+  int f = w0;
+  Place at = {0, 0, 0};
+  DecReq r = {};
+  if (f < w1) {
+    at = find(f);
+    r = dec_request(a, at.b, C::ROWS, unused);
+    if (at.u >= r.units) {  // the part begins in the cost of an item's end
+      f += r.units + kItemCost - at.u;
+      if (f < w1) {
+        next_item(at);
+        r = dec_request(a, at.b, C::ROWS, unused);
+      }
+    }
+  }
+  if (f < w1) {
+    // q of an item to shared memory: rows of D values
+    auto fetch_q = [&](const DecReq& rq, int h) {
+#pragma unroll
+      for (int i = 0; i < C::QROW / 512; ++i) {  // (where q's operands stay in registers)
+        const int x = i * 32 + lane, rr = x / (C::D / 8), d8 = x % (C::D / 8), j = div_group(a, rr);
+        if (rr < rq.rows)
+          cp_async16(q_next + x * 16, reinterpret_cast<const uint16_t*>(a.q) + (int64_t)(rq.row0 + j) * a.ld_q +
+                                          (h * a.group + rr - j * a.group) * C::D + d8 * 8);
+      }
+    };
+    fetch_q(r, at.h);
+    // the producer's place; the addresses of its next 32 tiles, one a lane
+    Place pp = at;
+    DecReq pr = r;
+    int pf = f, pblk = 0;
+    const uint8_t* src = nullptr;
+    uint32_t there = 0;  // which of the 32 are read
     bool fresh = true;
-    uint32_t held = 0, phase = 0;  // stages with a tile; their barriers' parities
+    uint32_t phase = 0, have = 0;  // parities of the stages' barriers; the tiles of them that are read, two bits each
     const int tpp = a.page_size / kKvTile;
-    auto issue = [&](int stage) {  // the next tile of the part into a stage
+    auto issue = [&](int stage) {  // the next unit of the part into a stage
       if (pf >= w1) return;
-      if (fresh || pt - pblk == 32) {
-        pblk = pt;
+      if (fresh || pp.u - pblk == 16) {
+        pblk = pp.u;
         fresh = false;
-        const int t = pt + lane;
-        page_reg = -1;
-        if (t < pr.tiles && (pr.tile0 + t) * kKvTile < pr.seq) {
-          page_reg = a.table[(int64_t)pb * a.ld_table + (pr.tile0 + t) / tpp];
-          if (page_reg < 0 || page_reg >= a.num_pages) {
-            // (reported by the warp that would read it)
-            if (pf + lane < w1) set_error(a.err, LORA_DEV_ERR_PAGE);
-            page_reg = -1;
-          }
+        const int t = pr.tile0 + 2 * pp.u + lane;
+        src = nullptr;
+        if (2 * pp.u + lane < 2 * pr.units && t * kKvTile < pr.seq) {
+          const int nth = page_of_tile(a, t), page = a.table[(int64_t)pp.b * a.ld_table + nth];
+          if (page >= 0 && page < a.num_pages)
+            src = a.pages + (((int64_t)page * a.heads + pp.h) * tpp + (t - nth * tpp)) * C::TILE;
+          else if (pf + (lane >> 1) < w1)  // (reported by the warp that would read it)
+            set_error(a.err, LORA_DEV_ERR_PAGE);
         }
+        there = __ballot_sync(0xffffffffu, src != nullptr);
       }
-      const int page = __shfl_sync(0xffffffffu, page_reg, pt - pblk);
-      if (page >= 0) {
-        if (lane == 0) {
-          const int64_t tile = ((int64_t)page * a.heads + ph) * tpp + (pr.tile0 + pt) % tpp;
-          mbar_arrive_expect_tx(&bars[warp][stage], C::TILE);
-          bulk_g2s(ring + stage * C::TILE, a.pages + tile * C::TILE, C::TILE, &bars[warp][stage]);
-        }
-        held |= 1u << stage;
-      }
+      const int k = 2 * (pp.u - pblk);
+      const uint32_t got = (there >> k) & 3u;
+      if (got && lane == k) mbar_arrive_expect_tx(&bars[warp][stage], (got == 3u ? 2 : 1) * C::TILE);
+      __syncwarp();
+      if (lane >> 1 == k >> 1 && src)
+        bulk_g2s(ring + (stage * 2 + (lane & 1)) * C::TILE, src, C::TILE, &bars[warp][stage]);
+      have |= got << (2 * stage);
       ++pf;
-      if (++pt == pr.tiles) {
-        pt = 0;
+      if (++pp.u == pr.units) {
+        pf += kItemCost;
         fresh = true;
-        if (++ph == a.heads && pf < w1) {
-          ph = 0;
-          do ++pb; while (pre[pb + 1] == pre[pb]);
-          pr = dec_request(a, pb, C::ROWS, unused);
+        if (pf < w1) {
+          next_item(pp);
+          pr = dec_request(a, pp.b, C::ROWS, unused);
         }
       }
     };
-#pragma unroll 1
-    for (int s = 0; s < C::STAGES; ++s) issue(s);
-
-    int b, h, t;
-    find(w0, b, h, t);
-    int64_t f = w0;
     int stage = 0;
+#pragma unroll 1
+    for (; stage < stages; ++stage) issue(stage);
+    stage = 0;
+
     while (f < w1) {
-      const DecReq r = dec_request(a, b, C::ROWS, unused);
-      const int64_t item0 = f - t, item1 = item0 + r.tiles;
-      const int t_end = item1 < w1 ? r.tiles : (int)(w1 - item0);
+      const int item0 = f - at.u, item1 = item0 + r.units;
+      const int u_end = item1 < w1 ? r.units : w1 - item0;
       // q of the item: the lane's row g of each column tile, dims of its c
+      asm volatile("cp.async.wait_all;" ::: "memory");
+      __syncwarp();
       uint32_t qf[C::QSMEM ? 1 : C::NT][C::QSMEM ? 1 : C::QREGS];
-      float qa[C::NT][2], qb[C::NT][C::G][2];  // factors of the lane's columns
+      float qa[C::NT][2], qb[C::NT][C::G][2], thr[C::NT][2];  // of the lane's columns
 #pragma unroll
       for (int n = 0; n < C::NT; ++n) {
-        const int rr = n * 8 + g;
+        const int rr = n * 8 + g, j = div_group(a, rr);
         uint4 raw[C::G][2];
         float top = 0.0f, sum[C::G];
-        const int j = rr / a.group;
-        const uint16_t* qp = reinterpret_cast<const uint16_t*>(a.q) +
-                             (int64_t)(r.row0 + j) * a.ld_q + (h * a.group + rr - j * a.group) * C::D;
 #pragma unroll
         for (int q = 0; q < C::G; ++q) {
           sum[q] = 0.0f;
 #pragma unroll
-          for (int u = 0; u < 2; ++u) {
-            raw[q][u] = rr < r.rows ? ldg_nc_v4(qp + q * 64 + c * 16 + u * 8) : make_uint4(0, 0, 0, 0);
-            const uint32_t* w = reinterpret_cast<const uint32_t*>(&raw[q][u]);
+          for (int x = 0; x < 2; ++x) {
+            raw[q][x] = make_uint4(0, 0, 0, 0);
+            if (rr < r.rows) {
+              if (C::QSMEM)
+                raw[q][x] = ldg_nc_v4(reinterpret_cast<const uint16_t*>(a.q) + (int64_t)(r.row0 + j) * a.ld_q +
+                                      (at.h * a.group + rr - j * a.group) * C::D + q * 64 + c * 16 + x * 8);
+              else
+                raw[q][x] = *reinterpret_cast<const uint4*>(q_next + (rr * C::D + q * 64 + c * 16 + x * 8) * 2);
+            }
+            const uint32_t* w = reinterpret_cast<const uint32_t*>(&raw[q][x]);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-              const float2 x = unpack2<C::BF16>(w[i]);
-              top = fmaxf(top, fmaxf(fabsf(x.x), fabsf(x.y)));
-              sum[q] += x.x + x.y;
+              const float2 v = unpack2<C::BF16>(w[i]);
+              top = fmaxf(top, fmaxf(fabsf(v.x), fabsf(v.y)));
+              sum[q] += v.x + v.y;
             }
           }
         }
@@ -470,315 +803,162 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_decode_kernel(const AttnArg
 #pragma unroll
           for (int q = 0; q < C::G; ++q) sum[q] += __shfl_xor_sync(0xffffffffu, sum[q], d);
         }
-        // q 2^(14 - e) with 2^e <= top < 2^(e + 1) is at most 2^15
+        // q 2^(14 - e) with 2^e <= top < 2^(e + 1) is at most 2^15; the
+        // scale's sign goes with q, so that a larger product is a larger score
         int e = (int)((__float_as_uint(top) >> 23) & 255u) - 127;
         e = e < -100 ? -100 : e;
-        const float up = pow2i(14 - e);
+        const float mul = a.scale_log2 < 0.0f ? -pow2i(14 - e) : pow2i(14 - e);
 #pragma unroll
         for (int q = 0; q < C::G; ++q)
 #pragma unroll
-          for (int u = 0; u < 2; ++u) {
-            const uint32_t* w = reinterpret_cast<const uint32_t*>(&raw[q][u]);
+          for (int y = 0; y < 2; ++y) {
+            const uint32_t* w = reinterpret_cast<const uint32_t*>(&raw[q][y]);
             float x[8];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
               const float2 v = unpack2<C::BF16>(w[i]);
-              x[2 * i] = v.x * up;
-              x[2 * i + 1] = v.y * up;
+              x[2 * i] = v.x * mul;
+              x[2 * i + 1] = v.y * mul;
             }
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
               const float k = i % 2 ? 0.0625f : 1.0f;
               const uint32_t v = half2_bits(x[i] * k, x[4 + i] * k);
-              const int at = (q * 2 + u) * 4 + i;
+              const int to = (q * 2 + y) * 4 + i;
               if (C::QSMEM)
-                q_s[(n * C::QREGS + at) * 32] = v;
+                q_s[(n * C::QREGS + to) * 32] = v;
               else
-                qf[C::QSMEM ? 0 : n][C::QSMEM ? 0 : at] = v;
+                qf[C::QSMEM ? 0 : n][C::QSMEM ? 0 : to] = v;
             }
           }
-        const float fa = a.scale_log2 * pow2i(e) * 1024.0f;  // 2^24 / 2^14
+        const float fa = fabsf(a.scale_log2) * pow2i(e) * 1024.0f;  // 2^24 / 2^14
+        const float fb = mul * 5.9604644775390625e-8f;              // 2^-24, as the codes have
 #pragma unroll
         for (int k = 0; k < 2; ++k) {  // the column 2 c + k is lane group 2 c + k's row
           qa[n][k] = __shfl_sync(0xffffffffu, fa, (2 * c + k) * 4);
+          thr[n][k] = -INFINITY;
 #pragma unroll
           for (int q = 0; q < C::G; ++q)
-            qb[n][q][k] = a.scale_log2 * __shfl_sync(0xffffffffu, sum[q], (2 * c + k) * 4);
+            qb[n][q][k] = __shfl_sync(0xffffffffu, sum[q] * fb, (2 * c + k) * 4);
         }
       }
-      if (C::QSMEM) __syncwarp();
+      __syncwarp();
+      // the item after this one
+      Place nx = at;
+      DecReq rn = r;
+      const int f_next = item1 + kItemCost;
+      if (f_next < w1) {
+        next_item(nx);
+        rn = dec_request(a, nx.b, C::ROWS, unused);
+        fetch_q(rn, nx.h);
+      }
       dec_reset(st);
+      // every row sees the tokens [see0, see1)
+      const int pos1 = r.pos0 + div_group(a, r.rows - 1);
+      const int see1 = r.pos0 + 1 < r.seq ? r.pos0 + 1 : r.seq;
+      const int see0 = a.window > 0 && pos1 + 1 - a.window > 0 ? pos1 + 1 - a.window : 0;
 
 #pragma unroll 1
-      for (; t < t_end; ++t) {
-        if (held & (1u << stage)) {
+      for (int u = at.u; u < u_end; ++u) {
+        const uint32_t got = (have >> (2 * stage)) & 3u;
+        if (got) {
           if (!__all_sync(0xffffffffu,
                           mbar_wait_bounded(&bars[warp][stage], (phase >> stage) & 1u, a.wait_ns))) {
             // given up: the copies in flight still write to this CTA's memory,
             // so they are waited for; the rest of the part is not read
             if (lane == 0) {
               set_error(a.err, LORA_DEV_ERR_TIMEOUT);
-              for (int x = 0; x < C::STAGES; ++x)
-                if (held & (1u << x)) mbar_wait_bounded(&bars[warp][x], (phase >> x) & 1u, kWaitLimitNs);
+              for (int x = 0; x < stages; ++x)
+                if ((have >> (2 * x)) & 3u) mbar_wait_bounded(&bars[warp][x], (phase >> x) & 1u, kWaitLimitNs);
             }
             __syncwarp();
-            held = 0;
+            have = 0;
             pf = w1;
             continue;
           }
           phase ^= 1u << stage;
-          held &= ~(1u << stage);
-          const uint8_t* tile = ring + stage * C::TILE;
-          const int tok0 = (r.tile0 + t) * kKvTile;  // token of row 0
-          float sc[C::NT][C::G][4];
-#pragma unroll
-          for (int n = 0; n < C::NT; ++n)
-#pragma unroll
-            for (int q = 0; q < C::G; ++q)
-#pragma unroll
-              for (int i = 0; i < 4; ++i) sc[n][q][i] = 0.0f;
-#pragma unroll
-          for (int p = 0; p < C::NP; ++p) {
-            uint32_t k0[C::WD], k1[C::WD];  // tokens g and g + 8
-            const uint8_t* kp = tile + p * 8 * C::W + g * (C::W / 2) + c * (C::W / 8);
-            if (C::WD == 4) {
-              *reinterpret_cast<uint4*>(k0) = *reinterpret_cast<const uint4*>(kp);
-              *reinterpret_cast<uint4*>(k1) = *reinterpret_cast<const uint4*>(kp + 4 * C::W);
-            } else {
-              *reinterpret_cast<uint2*>(k0) = *reinterpret_cast<const uint2*>(kp);
-              *reinterpret_cast<uint2*>(k1) = *reinterpret_cast<const uint2*>(kp + 4 * C::W);
-            }
-#pragma unroll
-            for (int w = 0; w < C::WD; ++w)
-#pragma unroll
-              for (int u = 0; u < 2; ++u) {
-                const uint32_t x0 = u ? k0[w] >> 8 : k0[w], x1 = u ? k1[w] >> 8 : k1[w];
-                const uint32_t a0 = x0 & 0x000f000fu, a2 = x0 & 0x00f000f0u;
-                const uint32_t a1 = x1 & 0x000f000fu, a3 = x1 & 0x00f000f0u;
-#pragma unroll
-                for (int n = 0; n < C::NT; ++n) {
-                  const int at = (p * C::WD + w) * 4 + 2 * u;
-                  const uint32_t b0 = C::QSMEM ? q_s[(n * C::QREGS + at) * 32] : qf[C::QSMEM ? 0 : n][C::QSMEM ? 0 : at];
-                  const uint32_t b1 = C::QSMEM ? q_s[(n * C::QREGS + at + 1) * 32] : qf[C::QSMEM ? 0 : n][C::QSMEM ? 0 : at + 1];
-                  mma_f16(sc[n][(p * C::WD + w) / 2], a0, a1, a2, a3, b0, b1);
-                }
-              }
-          }
-          // scales and least values of tokens g and g + 8
-          float2 ks[2][C::G], vs[2][C::G];
-#pragma unroll
-          for (int u = 0; u < 2; ++u)
-#pragma unroll
-            for (int q = 0; q < C::G; ++q) {
-              const int at = 8 * C::D + ((g + 8 * u) * C::G + q) * 4;
-              ks[u][q] = __half22float2(*reinterpret_cast<const __half2*>(tile + at));
-              vs[u][q] = __half22float2(*reinterpret_cast<const __half2*>(tile + C::HALF + at));
-            }
-          // tokens past the last row's position, or before the first row's
-          // window, are not read at all; rows in between are masked one by one
-          const int pos1 = r.pos0 + (r.rows - 1) / a.group;
-          const bool edge = tok0 + kKvTile > r.pos0 + 1 || tok0 + kKvTile > r.seq ||
-                            (a.window > 0 && tok0 <= pos1 - a.window);
-          float s[C::NT][4];
-#pragma unroll
-          for (int n = 0; n < C::NT; ++n)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const int u = i >> 1, k = i & 1;
-              float v = 0.0f, z = 0.0f;
-#pragma unroll
-              for (int q = 0; q < C::G; ++q) {
-                v = fmaf(ks[u][q].x, sc[n][q][i], v);
-                z = fmaf(ks[u][q].y, qb[n][q][k], z);
-              }
-              s[n][i] = fmaf(v, qa[n][k], z);
-            }
-          if (edge) {
-#pragma unroll
-            for (int u = 0; u < 2; ++u) {
-              const int tok = tok0 + g + 8 * u;
-              // (a token that no row sees may hold anything)
-              const bool any = tok < r.seq && tok <= pos1 &&
-                               (a.window <= 0 || tok > r.pos0 - a.window);
-#pragma unroll
-              for (int q = 0; q < C::G; ++q)
-                if (!any) vs[u][q] = make_float2(0.0f, 0.0f);
-#pragma unroll
-              for (int n = 0; n < C::NT; ++n)
-#pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                  const int pos = r.pos0 + (n * 8 + 2 * c + k) / a.group;
-                  if (!any || tok > pos || (a.window > 0 && tok <= pos - a.window))
-                    s[n][2 * u + k] = -INFINITY;
-                }
-            }
-          }
-          // maxima: a new one only where a score is 2^8 above the old, or the
-          // weights would leave f16
-          bool up = false;
-          float smax = 0.0f;
-#pragma unroll
-          for (int n = 0; n < C::NT; ++n)
-#pragma unroll
-            for (int k = 0; k < 2; ++k)
-              up |= fmaxf(s[n][k], s[n][2 + k]) > st.m[n][k] + 8.0f;
-#pragma unroll
-          for (int q = 0; q < C::G; ++q)  // (a scale that is not finite poisons its own rows only)
-            smax = fmaxf(smax, fmaxf(vs[0][q].x <= 65504.0f ? vs[0][q].x : 0.0f,
-                                     vs[1][q].x <= 65504.0f ? vs[1][q].x : 0.0f));
-          const float fcur = pow2i(st.fexp);
-          up |= smax * fcur > 128.0f;
-          if (__any_sync(0xffffffffu, up)) {
-#pragma unroll
-            for (int d = 1; d < 32; d <<= 1) smax = fmaxf(smax, __shfl_xor_sync(0xffffffffu, smax, d));
-            // 2^e <= smax < 2^(e + 1); s 2^f < 2^7 with f = 6 - e
-            int fe = 6 - ((int)((__float_as_uint(smax) >> 23) & 255u) - 127);
-            fe = fe < st.fexp ? fe : st.fexp;
-            const float fold = pow2i(fe - st.fexp < -126 ? -126 : fe - st.fexp);
-            st.fexp = fe;
-#pragma unroll
-            for (int n = 0; n < C::NT; ++n)
-#pragma unroll
-              for (int k = 0; k < 2; ++k) {
-                float top = fmaxf(s[n][k], s[n][2 + k]);
-#pragma unroll
-                for (int d = 4; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-                const float m1 = fmaxf(st.m[n][k], top), keep = exp2_fast(st.m[n][k] - m1);
-                st.m[n][k] = m1;
-                st.l[n][k] *= keep;
-#pragma unroll
-                for (int q = 0; q < C::G; ++q) st.z[n][q][k] *= keep;
-                const float ko = keep * fold;
-#pragma unroll
-                for (int i = 0; i < C::MM; ++i) {
-                  st.o[n][i][k] *= ko;
-                  st.o[n][i][2 + k] *= ko;
-                }
-              }
-          }
-          const float f16f = pow2i(st.fexp);
-          uint32_t pw[C::NT][C::G][2];  // weights of the values' products
-#pragma unroll
-          for (int n = 0; n < C::NT; ++n) {
-            float pr4[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) pr4[i] = exp2_fast(s[n][i] - st.m[n][i & 1]);
-            st.l[n][0] += pr4[0] + pr4[2];
-            st.l[n][1] += pr4[1] + pr4[3];
-#pragma unroll
-            for (int q = 0; q < C::G; ++q) {
-              const float f0 = vs[0][q].x * f16f, f1 = vs[1][q].x * f16f;
-              float w[4] = {pr4[0] * f0, pr4[1] * f0, pr4[2] * f1, pr4[3] * f1};
-              float y[4] = {pr4[0] * vs[0][q].y, pr4[1] * vs[0][q].y, pr4[2] * vs[1][q].y,
-                            pr4[3] * vs[1][q].y};
-              if (edge) {  // (0 x inf, where one row sees the token and another does not)
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                  if (pr4[i] == 0.0f) w[i] = y[i] = 0.0f;
-              }
-              st.z[n][q][0] += y[0] + y[2];
-              st.z[n][q][1] += y[1] + y[3];
-              pw[n][q][0] = transpose8(half2_bits(w[0], w[1]));
-              pw[n][q][1] = transpose8(half2_bits(w[2], w[3]));
-            }
-          }
-#pragma unroll
-          for (int p = 0; p < C::NP; ++p) {
-            uint32_t v0[C::WD], v1[C::WD];  // tokens 2 c, + 1 and 2 c + 8, + 9
-            const uint8_t* vp = tile + C::HALF + p * 8 * C::W + g * (C::W / 2) + c * (C::W / 8);
-            if (C::WD == 4) {
-              *reinterpret_cast<uint4*>(v0) = *reinterpret_cast<const uint4*>(vp);
-              *reinterpret_cast<uint4*>(v1) = *reinterpret_cast<const uint4*>(vp + 4 * C::W);
-            } else {
-              *reinterpret_cast<uint2*>(v0) = *reinterpret_cast<const uint2*>(vp);
-              *reinterpret_cast<uint2*>(v1) = *reinterpret_cast<const uint2*>(vp + 4 * C::W);
-            }
-#pragma unroll
-            for (int w = 0; w < C::WD; ++w)
-#pragma unroll
-              for (int u = 0; u < 2; ++u) {
-                const uint32_t x0 = u ? v0[w] >> 8 : v0[w], x1 = u ? v1[w] >> 8 : v1[w];
-                const uint32_t a0 = x0 & 0x000f000fu, a1 = x0 & 0x00f000f0u;
-                const uint32_t a2 = x1 & 0x000f000fu, a3 = x1 & 0x00f000f0u;
-                const int q = (p * C::WD + w) / 2;
-#pragma unroll
-                for (int n = 0; n < C::NT; ++n)
-                  mma_f16(st.o[n][(p * C::WD + w) * 2 + u], a0, a1, a2, a3, pw[n][q][0], pw[n][q][1]);
-              }
-          }
+          have &= ~(3u << (2 * stage));
+          const int tok0 = (r.tile0 + 2 * u) * kKvTile;
+          uint8_t* unit = ring + stage * 2 * C::TILE;
+          const bool edge = got != 3u || tok0 < see0 || tok0 + C::UNIT > see1;
+          dec_unit<C>(a, r, st, unit, tok0, got, edge, pos1, q_s, qf, qa, qb, thr, lane);
           __syncwarp();
         }
         issue(stage);
-        stage = stage + 1 == C::STAGES ? 0 : stage + 1;
+        stage = stage + 1 == stages ? 0 : stage + 1;
       }
-      f = item0 + t_end;
       dec_finish(st);
       if (item0 >= w0 && item1 <= w1) {
-        dec_write(a, r, h, st, lane);
+        dec_write(a, r, at.h, st, lane);
       } else {
         // a part of an item: the warp's first goes to memory, where its ring
-        // is still in use; its last stays in registers until the end
-        const int which = f >= w1 ? 1 : 0;
+        // is still in use; its last to the ring, which has served
+        const bool last = f_next >= w1;
         if (lane == 0) {
-          seg_b[warp][which] = b;
-          seg_h[warp][which] = h;
-          seg_lo[warp][which] = item0;
-          seg_hi[warp][which] = item1;
+          seg_b[warp][last] = at.b;
+          seg_h[warp][last] = at.h;
+          seg_lo[warp][last] = item0;
+          seg_hi[warp][last] = item1;
         }
-        if (which == 0) dec_save(st, my_first, lane);
+        dec_save(st, last ? reinterpret_cast<float*>(ring)
+                          : a.partials + (2 * kAttnMaxCtas + cta * C::NW + warp) * (int64_t)C::SLOT, lane);
       }
-      t = 0;
-      if (f < w1 && ++h == a.heads) {
-        h = 0;
-        do ++b; while (pre[b + 1] == pre[b]);
-      }
+      f = f_next;
+      at = nx;
+      r = rn;
     }
-    __syncwarp();
-    if (seg_b[warp][1] >= 0) dec_save(st, my_last, lane);
   }
   __syncthreads();
 
-  // the CTA's parts of items: the warp that holds an item's first part here
-  // adds the parts of the warps after it
-  auto slot_of = [&](int w, int which) -> float* {
-    return which ? reinterpret_cast<float*>(dec_smem + w * C::RING)
-                 : a.partials + ((int64_t)2 * kAttnMaxCtas + (int64_t)cta * C::NW + w) * C::SLOT;
-  };
-#pragma unroll 1
-  for (int which = 0; which < 2; ++which) {
-    const int b = seg_b[warp][which];
-    if (b < 0) continue;
-    const int64_t lo = seg_lo[warp][which], hi = seg_hi[warp][which];
-    // the item's first part in this CTA is its own first tile, or the CTA's
-    const int64_t from = which == 0 || lo < w0 ? w0 : lo;
-    if (from > t0 && lo < from) continue;
-    const DecReq r = dec_request(a, b, C::ROWS, bad);
-    const int h = seg_h[warp][which];
-    // this warp's own part, then those that follow
-    dec_reset(st);
-    dec_add(st, slot_of(warp, which), lane);
-    for (int w = warp + 1; w < C::NW; ++w) {
-      const int64_t at = t0 + (int64_t)w * part;
-      if (at >= hi || at >= t1) break;
-      dec_add(st, slot_of(w, seg_b[w][0] >= 0 && seg_lo[w][0] == lo ? 0 : 1), lane);
+  // Joining in the CTA.  An item's segments are those of adjacent warps; its
+  // first one here stands for it: warp w's, where the item began in w's part
+  // or before the CTA's range.
+  if (warp == 0) {
+    const int w = lane >> 1, which = lane & 1;
+    const bool head = w < C::NW && seg_b[w][which] >= 0 && (seg_lo[w][which] >= t0 + w * part || w == 0);
+    const uint32_t heads = __ballot_sync(0xffffffffu, head);
+    if (head) chain_s[__popc(heads & ((1u << lane) - 1u))] = lane;
+    if (lane == 0) chains_s = __popc(heads);
+  }
+  __syncthreads();
+  for (int y = tid; y < chains_s * C::F4; y += C::THREADS) {
+    const int x = y % C::F4, w = chain_s[y / C::F4] >> 1, which = chain_s[y / C::F4] & 1;
+    const int lo = seg_lo[w][which], hi = seg_hi[w][which];
+    const int to = ((hi < t1 ? hi : t1) - t0 + part - 1) / part;
+    const int mlx = C::F4 + x / (32 * C::MM) * 32 + (x & 31);
+    float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f), ml = make_float4(kNoMax, kNoMax, 0.0f, 0.0f);
+#pragma unroll 4
+    for (int i = w; i < to; ++i) {
+      const bool first = i == w ? which == 0 : seg_b[i][0] >= 0 && seg_lo[i][0] == lo;
+      const float4* slot = reinterpret_cast<const float4*>(
+          first ? a.partials + (2 * kAttnMaxCtas + cta * C::NW + i) * (int64_t)C::SLOT
+                : reinterpret_cast<const float*>(dec_smem + i * ring_bytes));
+      dec_join(o, ml, slot[x], slot[mlx]);
     }
-    if (lo >= t0 && hi <= t1)
-      dec_write(a, r, h, st, lane);
-    else
-      dec_save(st, a.partials + ((int64_t)2 * cta + (lo > t0 ? 1 : 0)) * C::SLOT, lane);
+    if (lo >= t0 && hi <= t1) {
+      const DecReq rq = dec_request(a, seg_b[w][which], C::ROWS, unused);
+      dec_write_part<C>(a, rq, seg_h[w][which], x, o, ml);
+    } else {
+      float4* slot = reinterpret_cast<float4*>(a.partials + (2 * cta + (lo > t0 ? 1 : 0)) * (int64_t)C::SLOT);
+      slot[x] = o;
+      if (x / 32 % C::MM == 0) slot[mlx] = ml;
+    }
   }
   if (chunk == 0) return;
 
-  // items that cross CTAs: at most two here, the one that the CTA's first tile
-  // is part of and the one that its last is part of
+  // Joining over CTAs: at most two items, the one that the CTA's first unit is
+  // part of and the one that its last is part of.  Where the threads are more
+  // than a result's float4s, each group of threads adds some of the CTAs.
+  constexpr int PAR = C::THREADS > C::F4 ? C::THREADS / C::F4 : 1;
 #pragma unroll 1
   for (int side = 0; side < 2; ++side) {
-    int b, h, t;
-    find(side == 0 ? t0 : t1 - 1, b, h, t);
-    const int64_t lo = (side == 0 ? t0 : t1 - 1) - t, hi = lo + pre[b + 1] - pre[b];
-    if (lo >= t0 && hi <= t1) continue;
-    if (side == 1 && lo <= t0) continue;  // (the same item, seen on side 0)
-    const int c0 = (int)(lo / chunk), c1 = (int)((hi - 1) / chunk);
+    const int ref = side == 0 ? t0 : t1 - 1;
+    const Place p = find(ref);
+    const DecReq rq = dec_request(a, p.b, C::ROWS, unused);
+    const int lo = ref - p.u, hi = lo + rq.units;
+    // (not an item that lies in the CTA, or whose cost alone reaches into it)
+    if ((lo >= t0 && hi <= t1) || hi <= t0 || (side == 1 && lo <= t0)) continue;
+    const int c0 = lo / chunk, c1 = (hi - 1) / chunk;
     __threadfence();
     __syncthreads();
     if (tid == 0) {
@@ -789,12 +969,33 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_decode_kernel(const AttnArg
     __syncthreads();
     if (!last_s) continue;
     __threadfence();
-    if (warp == 0) {
-      const DecReq r = dec_request(a, b, C::ROWS, bad);
-      dec_reset(st);
-      for (int i = c0; i <= c1; ++i)
-        dec_add(st, a.partials + ((int64_t)2 * i + (lo > i * chunk ? 1 : 0)) * C::SLOT, lane);
-      dec_write(a, r, h, st, lane);
+    float4* share = reinterpret_cast<float4*>(dec_smem);  // [PAR][F4][2], PAR * F4 <= THREADS
+#pragma unroll 1
+    for (int x = tid % C::F4, k = tid / C::F4; x < C::F4 && k < PAR; x += C::THREADS) {
+      const int mlx = C::F4 + x / (32 * C::MM) * 32 + (x & 31);
+      float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f), ml = make_float4(kNoMax, kNoMax, 0.0f, 0.0f);
+#pragma unroll 4
+      for (int i = c0 + k; i <= c1; i += PAR) {
+        const float4* slot = reinterpret_cast<const float4*>(
+            a.partials + (2 * i + (lo > i * chunk ? 1 : 0)) * (int64_t)C::SLOT);
+        dec_join(o, ml, __ldcg(slot + x), __ldcg(slot + mlx));
+      }
+      if (PAR == 1) {
+        dec_write_part<C>(a, rq, p.h, x, o, ml);
+      } else {
+        share[(k * C::F4 + x) * 2] = o;
+        share[(k * C::F4 + x) * 2 + 1] = ml;
+      }
+    }
+    if (PAR > 1) {
+      __syncthreads();
+      if (tid < C::F4) {
+        float4 o = share[tid * 2], ml = share[tid * 2 + 1];
+#pragma unroll
+        for (int k = 1; k < PAR; ++k)
+          dec_join(o, ml, share[(k * C::F4 + tid) * 2], share[(k * C::F4 + tid) * 2 + 1]);
+        dec_write_part<C>(a, rq, p.h, tid, o, ml);
+      }
     }
   }
 }

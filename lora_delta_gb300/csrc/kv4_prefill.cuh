@@ -1,116 +1,775 @@
-// Attention over the 4-bit key/value cache for many query rows per request.
+// Attention over the 4-bit key/value cache for many query rows per request and
+// key/value head, on the tensor cores (tcgen05).
+//
+// An item is up to 256 query rows (a request's tokens x the heads that share a
+// key/value head; 128 rows at head_dim 256) and the tokens that they see, in
+// tiles of 128 (64).  Roles of a CTA, handing over through mbarriers:
+//   load warp       bulk copies of the tile's packed 16-token blocks
+//   4 expand warps  codes to f16 values s c + m in the operands' 128-byte
+//                   swizzled layout, keys [token][dim], values [dim][token]
+//   MMA warp        S = Q K^T (128 x 128 a row half, in tensor memory), then
+//                   O += P V with P read from tensor memory
+//   4 softmax warps a row half: a thread a row; scores to weights in place of
+//                   S, running maximum (followed lazily: O is scaled only when
+//                   a row's maximum grew by 2^8), denominator, the final O / l
+// The two row halves alternate, so the MMAs of one run while the other's
+// weights are computed; tiles are expanded once for both.
+// Keys and values are rounded to f16 (2^-12 relative) where tiles are expanded:
+// two packed instructions a pair of codes.  Scaling S instead would cost one
+// per score, group and query row.  Where that rounding could show (scores of
+// large keys and queries: an estimated error of a score above 2^-10), a tile's
+// keys come in two operands, the second holding what the first lost, and S is
+// the sum of two products; ordinary tiles do without.  Queries are brought to f16 by a power of
+// two of their row (exact), weights are 2^7 p with p <= 2^8.
 #pragma once
 
 #include "kv4_attn.cuh"
+#include "tc.cuh"
 
 namespace lora {
 
-// One CTA per (row, query head): tokens in chunks of 128, a thread's token's
-// score, then the chunk's values with a thread per dim.
-template <int D, bool BF16>
-__global__ void __launch_bounds__(128) kv4_attn_simple_kernel(const AttnArgs a) {
-  const int row = blockIdx.x, qh = blockIdx.y, head = qh / a.group, tid = threadIdx.x;
-  constexpr int G = D / kKvGroup;
-  __shared__ float q_s[D];
-  __shared__ float p_s[128];
-  __shared__ float red_s[8];
-  __shared__ int req_s;
-  uint16_t* out = reinterpret_cast<uint16_t*>(a.out) + (int64_t)row * a.ld_out + qh * D;
+template <int D_, bool BF16_>
+struct Pre {
+  static constexpr int D = D_;
+  static constexpr bool BF16 = BF16_;
+  static constexpr int G = D / 64, W = D < 128 ? D : 128, NP = D / W, WD = W / 32;
+  static constexpr int TILE = kv4_tile_bytes(D), HALF = kv4_half_bytes(D);
+  static constexpr int MT = D == 256 ? 1 : 2;       // row halves of 128
+  static constexpr int NKV = D == 256 ? 64 : 128;   // tokens of a tile
+  static constexpr int TPK = NKV / kKvTile;
+  static constexpr int ROWS = MT * 128;
+  // blocks lie 16 bytes apart modulo 128, so that lanes reading the same place
+  // of neighbouring blocks do not meet in a bank
+  static constexpr int RSTRIDE = TILE + 16;
+  static constexpr int RAW = TPK * RSTRIDE;
+  static constexpr int KV = NKV * D * 2;            // an expanded operand
+  static constexpr int KVB = D == 64 ? 6 : 3;       // expanded operands in flight
+  static constexpr int Q = ROWS * D * 2;
+  static constexpr int INFO = 8;                    // tiles described at once
+  static constexpr int SOFT_WARPS = 4 * MT;
+  static constexpr int EXP_WARP = SOFT_WARPS, MMA_WARP = EXP_WARP + 4, LOAD_WARP = MMA_WARP + 1;
+  static constexpr int THREADS = (LOAD_WARP + 1) * 32;
+  static constexpr size_t smem(int B) {
+    return 1024 + (size_t)Q + KVB * KV + 2 * RAW + (size_t)(B + 1) * 4;
+  }
+};
+
+// An item: rows [r0, r0 + rows) of the request's (token, head) rows.
+struct PreItem {
+  int b, h, r0, rows;
+  int row0, pos0, seq;  // first row of the batch, its position, visible tokens
+  int kv0, lo, hi, tiles;  // first token copied; tokens [lo, hi) are seen by some row
+};
+
+__device__ __forceinline__ int pre_rows(const AttnArgs& a, int b, int min_rows, uint32_t& bad) {
+  const int start = a.row_start[b], end = a.row_start[b + 1];
+  if (end <= start) return 0;
+  if (start < 0 || end > a.n || end - start > a.max_q_len) return 0;  // (reported by the decode kernel)
+  if ((end - start) * a.group <= min_rows) return 0;
+  if (a.seq_len[b] < 0 || a.seq_len[b] > a.cap) bad |= LORA_DEV_ERR_LENGTH;
+  return (int)(end - start);
+}
+
+// A CTA's items: one of each gridDim.x in turn, forwards and backwards
+// alternately, since a prompt's items come by falling work.
+__device__ __forceinline__ int pre_nth(int round) {
+  return round * gridDim.x + (round & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+}
+
+template <class C>
+__device__ __forceinline__ PreItem pre_item(const AttnArgs& a, const int32_t* pre, int item) {
+  PreItem it;
+  const int total = pre[a.B];
+  it.h = item % a.heads;
+  const int rt = total - 1 - item / a.heads;  // a prompt's last rows see most: first
+  int lo = 0, hi = a.B;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (pre[mid] <= rt) lo = mid; else hi = mid;
+  }
+  it.b = lo;
+  it.row0 = a.row_start[lo];
+  const int tokens = a.row_start[lo + 1] - it.row0;
+  const int rows = tokens * a.group;
+  const int seq = a.seq_len[lo];
+  it.r0 = (rt - pre[lo]) * C::ROWS;
+  it.rows = rows - it.r0 < C::ROWS ? rows - it.r0 : C::ROWS;
+  it.pos0 = seq - tokens;
+  it.seq = seq < 0 ? 0 : (seq > a.cap ? a.cap : seq);
+  const int pos_lo = it.pos0 + it.r0 / a.group, pos_hi = it.pos0 + (it.r0 + it.rows - 1) / a.group;
+  it.lo = a.window > 0 && pos_lo + 1 - a.window > 0 ? pos_lo + 1 - a.window : 0;
+  it.hi = pos_hi + 1 < it.seq ? pos_hi + 1 : it.seq;
+  it.kv0 = it.lo / kKvTile * kKvTile;
+  // (rows that see nothing keep one tile, all of it masked)
+  it.tiles = it.hi > it.kv0 ? (it.hi - it.kv0 + C::NKV - 1) / C::NKV : 1;
+  return it;
+}
+
+// Four packed pairs of codes (two words' places) to values: bits 0-3 and 4-7
+// of each half, exact integers first, then one rounding of s c + m.
+__device__ __forceinline__ uint32_t code_lo(uint32_t w) {
+  const uint32_t x = (w & 0x000f000fu) | 0x64006400u;  // 1024 + c
+  const __half2 h = __hsub2(*reinterpret_cast<const __half2*>(&x), __float2half2_rn(1024.0f));
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ uint32_t code_hi(uint32_t w) {
+  const uint32_t x = (w & 0x00f000f0u) | 0x64006400u;  // 1024 + 16 c
+  const __half2 h = __hfma2(*reinterpret_cast<const __half2*>(&x), __float2half2_rn(0.0625f),
+                            __float2half2_rn(-64.0f));
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ uint32_t code_value(uint32_t c, __half2 s, __half2 m) {
+  const __half2 h = __hfma2(*reinterpret_cast<const __half2*>(&c), s, m);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ bool half_finite(__half x) {
+  return (__half_as_ushort(x) & 0x7c00u) != 0x7c00u;
+}
+
+// Two float32 values worked on by one instruction.
+__device__ __forceinline__ uint64_t f32x2(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ void f32x2_split(uint64_t v, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma_f32x2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add_f32x2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
+template <class C>
+__global__ void __launch_bounds__(C::THREADS, 1) kv4_prefill_kernel(const AttnArgs a, int min_rows) {
+  extern __shared__ uint8_t pre_smem_raw[];
+  __shared__ uint64_t raw_full[2], raw_empty[2], kv_full[C::KVB], kv_empty[C::KVB];
+  __shared__ uint64_t q_full[2], s_full[2], p_full[2], pv_done[2], size_full[2], size_empty[2], drain_bar;
+  __shared__ float size_s[2][C::SOFT_WARPS][C::G];  // of two items: the largest |scale q_g|^2 of a warp's rows
+  __shared__ uint32_t taddr_s;
+  __shared__ uint32_t info_pages[C::INFO];             // blocks of a tile that were copied
+  __shared__ uint32_t info_two[C::INFO];               // keys in two operands
+  __shared__ uint32_t info_bad[C::INFO][C::NKV / 32];  // tokens whose values are not finite
+  __shared__ int scan_s[32];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  uint8_t* smem = pre_smem_raw + ((1024 - (smem_addr(pre_smem_raw) & 1023)) & 1023);
+  uint8_t* q_s = smem;
+  uint8_t* kv_s = smem + C::Q;
+  uint8_t* raw_s = kv_s + C::KVB * C::KV;
+  int32_t* pre = reinterpret_cast<int32_t*>(raw_s + 2 * C::RAW);
+
   if (tid == 0) {
-    int b = -1;
-    for (int i = 0; i < a.B; ++i)
-      if (a.row_start[i] <= row && row < a.row_start[i + 1]) b = i;
-    req_s = b;
-  }
-  __syncthreads();
-  const int b = req_s;
-  int64_t hi = 0, lo = 0;
-  if (b >= 0) {
-    const int64_t seq = a.seq_len[b], cap = (int64_t)a.max_pages * a.page_size;
-    hi = seq - (a.row_start[b + 1] - row) + 1;
-    if (seq < 0 || seq > cap) {
-      if (tid == 0) set_error(a.err, LORA_DEV_ERR_LENGTH);
-      hi = hi > cap ? cap : hi;
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&raw_full[i], 1);
+      mbar_init(&size_full[i], C::SOFT_WARPS);
+      mbar_init(&size_empty[i], 4);
+      mbar_init(&raw_empty[i], 4);
+      mbar_init(&q_full[i], 4);
+      mbar_init(&s_full[i], 1);
+      mbar_init(&p_full[i], 4);
+      mbar_init(&pv_done[i], 1);
     }
-    if (a.row_start[b + 1] - a.row_start[b] > a.max_q_len) {
-      if (tid == 0) set_error(a.err, LORA_DEV_ERR_LENGTH);
-      hi = 0;
+    for (int i = 0; i < C::KVB; ++i) {
+      mbar_init(&kv_full[i], 4);
+      mbar_init(&kv_empty[i], 1);
     }
-    lo = a.window > 0 && hi > a.window ? hi - a.window : 0;
+    mbar_init(&drain_bar, 1);
+    fence_barrier_init();
   }
-  for (int d = tid; d < D; d += 128) {
-    const uint16_t raw = reinterpret_cast<const uint16_t*>(a.q)[(int64_t)row * a.ld_q + qh * D + d];
-    q_s[d] = unpack2<BF16>(raw).x * a.scale_log2;
+  // row tiles of the requests, summed
+  uint32_t bad = 0;
+  {
+    const int per = (a.B + C::THREADS - 1) / C::THREADS;
+    int sum = 0;
+    for (int i = 0; i < per; ++i) {
+      const int b = tid * per + i;
+      if (b >= a.B) break;
+      const int rows = pre_rows(a, b, min_rows, bad) * a.group;
+      pre[b] = (rows + C::ROWS - 1) / C::ROWS;
+      sum += pre[b];
+    }
+    int inc = sum;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int u = __shfl_up_sync(0xffffffffu, inc, d);
+      if (lane >= d) inc += u;
+    }
+    if (lane == 31) scan_s[warp] = inc;
+    __syncthreads();
+    int base = inc - sum;
+    for (int w = 0; w < warp; ++w) base += scan_s[w];
+    for (int i = 0; i < per; ++i) {
+      const int b = tid * per + i;
+      if (b >= a.B) break;
+      const int t = pre[b];
+      pre[b] = base;
+      base += t;
+    }
+    if (tid == C::THREADS - 1) pre[a.B] = base;
   }
+  if (warp == C::MMA_WARP) tc::tmem_alloc(&taddr_s, 512);
+  tc::fence_before_sync();
   __syncthreads();
-  float m = -INFINITY, l = 0.0f, acc[(D + 127) / 128] = {};
-  uint8_t* pages = const_cast<uint8_t*>(a.pages);
-  const int64_t slots = a.num_pages * a.page_size;
-  auto slot_of = [&](int64_t t) -> int64_t {
-    const int page = a.table[(int64_t)b * a.ld_table + t / a.page_size];
-    const int64_t s = (int64_t)page * a.page_size + t % a.page_size;
-    return page >= 0 && s < slots ? s : -1;
-  };
-  for (int64_t t0 = lo; t0 < hi; t0 += 128) {
-    const int64_t t = t0 + tid;
-    float s = -INFINITY;
-    if (t < hi) {
-      const int64_t slot = slot_of(t);
-      if (slot < 0) {
-        set_error(a.err, LORA_DEV_ERR_PAGE);
-      } else {
-        int tok;
-        const uint8_t* tile = kv4_tile(pages, slot, head, a.page_size, a.heads, kv4_tile_bytes(D), tok);
-        const __half2* sm = reinterpret_cast<const __half2*>(tile + 8 * D) + tok * G;
-        s = 0.0f;
-        for (int d8 = 0; d8 < D / 8; ++d8) {
-          const uint32_t w = *reinterpret_cast<const uint32_t*>(tile + kv4_key_word<D>(tok, d8));
-          const float2 f = __half22float2(sm[d8 / 8]);
-          for (int i = 0; i < 8; ++i)
-            s = fmaf(q_s[d8 * 8 + i], fmaf(f.x, (float)((w >> (4 * i)) & 15u), f.y), s);
+  tc::fence_after_sync();
+  if (bad && blockIdx.x == 0) set_error(a.err, bad);
+  const uint32_t tmem = taddr_s;
+  const int items = pre[a.B] * a.heads;
+  constexpr uint32_t kO = 256;  // first tensor-memory column of the sums
+  bool ok = true;
+  bool issued = false;
+
+  if (warp == C::LOAD_WARP) {
+    // ------------------------------------------------------------------ load
+    uint32_t n = 0;  // tiles so far
+    for (int round = 0, i; (i = pre_nth(round)) < items && ok; ++round) {
+      const PreItem it = pre_item<C>(a, pre, i);
+      const int32_t* table = a.table + (int64_t)it.b * a.ld_table;
+      for (int j = 0; j < it.tiles && ok; ++j, ++n) {
+        const int st = n & 1;
+        const int tok = it.kv0 + j * C::NKV + lane * kKvTile;
+        int page = -1;
+        if (lane < C::TPK && tok < it.hi) {
+          page = table[page_of_tile(a, tok / kKvTile)];
+          if (page < 0 || page >= a.num_pages) {
+            set_error(a.err, LORA_DEV_ERR_PAGE);
+            page = -1;
+          }
+        }
+        if (n >= 2) ok = mbar_wait_bounded(&raw_empty[st], ((n >> 1) - 1) & 1, a.wait_ns);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        const uint32_t got = __ballot_sync(0xffffffffu, page >= 0);
+        if (lane == 0) {
+          info_pages[n % C::INFO] = got;
+          for (int w = 0; w < C::NKV / 32; ++w) info_bad[n % C::INFO][w] = 0;
+          if (got)
+            mbar_arrive_expect_tx(&raw_full[st], __popc(got) * C::TILE);
+          else
+            mbar_arrive(&raw_full[st]);
+        }
+        __syncwarp();
+        if (page >= 0) {
+          const int tpp = a.page_size / kKvTile, t = tok / kKvTile;
+          const int64_t tile = ((int64_t)page * a.heads + it.h) * tpp + (t - page_of_tile(a, t) * tpp);
+          bulk_g2s(raw_s + st * C::RAW + lane * C::RSTRIDE, a.pages + tile * C::TILE, C::TILE,
+                   &raw_full[st]);
         }
       }
     }
-    float top = s;
-    for (int d = 16; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-    if ((tid & 31) == 0) red_s[tid >> 5] = top;
-    __syncthreads();
-    top = fmaxf(fmaxf(red_s[0], red_s[1]), fmaxf(red_s[2], red_s[3]));
-    const float m1 = fmaxf(m, top), base = m1 == -INFINITY ? 0.0f : m1;
-    const float p = exp2f(s - base), keep = exp2f(m - base);
-    float sum = p;
-    for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-    p_s[tid] = p;
-    if ((tid & 31) == 0) red_s[4 + (tid >> 5)] = sum;
-    __syncthreads();
-    l = l * keep + red_s[4] + red_s[5] + red_s[6] + red_s[7];
-    for (int u = 0; u < (D + 127) / 128; ++u) {
-      acc[u] *= keep;
-      const int d = tid + u * 128;
-      if (d >= D) continue;
-      for (int j = 0; j < 128 && t0 + j < hi; ++j) {
-        if (p_s[j] == 0.0f) continue;
-        const int64_t slot = slot_of(t0 + j);
-        if (slot < 0) continue;
-        int tok;
-        const uint8_t* tile = kv4_tile(pages, slot, head, a.page_size, a.heads, kv4_tile_bytes(D), tok) +
-                              kv4_half_bytes(D);
-        const uint8_t* hp = tile + kv4_value_half<D>(tok, d / 8) + ((d / 4) % 2) * 4;
-        const float2 f = __half22float2(reinterpret_cast<const __half2*>(tile + 8 * D)[tok * G + d / 64]);
-        const uint32_t code = (*reinterpret_cast<const uint16_t*>(hp) >> (4 * (d % 4))) & 15u;
-        acc[u] = fmaf(p_s[j], fmaf(f.x, (float)code, f.y), acc[u]);
+    // (the copies still in flight write to this CTA's memory)
+    for (uint32_t k = n >= 2 ? n - 2 : 0; k < n; ++k)
+      if (!mbar_wait_bounded(&raw_full[k & 1], (k >> 1) & 1, kWaitLimitNs)) ok = false;
+  } else if (warp == C::MMA_WARP) {
+    // ------------------------------------------------------------------- MMA
+    if (lane == 0) {
+      const uint32_t id_qk = tc::idesc_f16_f32(128, C::NKV), id_pv = tc::idesc_f16_f32(128, C::D);
+      uint32_t k = 0, n = 0;                       // operands and tiles so far
+      uint32_t n_it[2] = {0, 0}, n_t[2] = {0, 0};  // items and tiles of each row half
+      auto wait_kv = [&](uint32_t x) {
+        ok = ok && mbar_wait_bounded(&kv_full[x % C::KVB], (x / C::KVB) & 1, a.wait_ns);
+        tc::fence_after_sync();
+      };
+      // S of a half from the keys in operand x, and x + 1 where they are two
+      auto qk = [&](int m, uint32_t x, bool two) {
+        const uint32_t qa = smem_addr(q_s) + m * 128 * C::D * 2;
+#pragma unroll 1
+        for (int y = 0; y < (two ? 2 : 1); ++y) {
+          const uint32_t ka = smem_addr(kv_s) + ((x + y) % C::KVB) * C::KV;
+#pragma unroll
+          for (int d = 0; d < C::D / 16; ++d)
+            tc::mma_bf16(tmem + m * 128, tc::sw128_desc(qa + (d / 4) * 16384 + (d % 4) * 32),
+                         tc::sw128_desc(ka + (d / 4) * C::NKV * 128 + (d % 4) * 32), id_qk, d > 0 || y > 0);
+        }
+        issued = true;
+        tc::mma_commit(&s_full[m]);
+      };
+      for (int round = 0, i; (i = pre_nth(round)) < items && ok; ++round) {
+        const PreItem it = pre_item<C>(a, pre, i);
+        const int mt = it.rows > 128 ? 2 : 1;
+        wait_kv(k);
+        bool two = ok && info_two[n % C::INFO];
+        if (two) wait_kv(k + 1);
+        for (int m = 0; m < mt && ok; ++m) {
+          ok = mbar_wait_bounded(&q_full[m], n_it[m]++ & 1, a.wait_ns);
+          tc::fence_after_sync();
+          if (ok) qk(m, k, two);
+        }
+        if (ok) tc::mma_commit(&kv_empty[k % C::KVB]);
+        if (ok && two) tc::mma_commit(&kv_empty[(k + 1) % C::KVB]);
+        for (int j = 0; j < it.tiles && ok; ++j, ++n) {
+          const uint32_t v = k + 1 + two, kn = v + 1;
+          const bool more = j + 1 < it.tiles;
+          wait_kv(v);
+          const uint32_t va = smem_addr(kv_s) + (v % C::KVB) * C::KV;
+          for (int m = 0; m < mt && ok; ++m) {
+            ok = mbar_wait_bounded(&p_full[m], n_t[m]++ & 1, a.wait_ns);
+            tc::fence_after_sync();
+            if (!ok) break;
+#pragma unroll
+            for (int t = 0; t < C::NKV / 16; ++t)
+              tc::mma_f16_ts(tmem + kO + m * 128, tmem + m * 128 + t * 8,
+                             tc::sw128_desc(va + (t / 4) * C::D * 128 + (t % 4) * 32), id_pv,
+                             j > 0 || t > 0);
+            issued = true;
+            tc::mma_commit(&pv_done[m]);
+            if (m == mt - 1) tc::mma_commit(&kv_empty[v % C::KVB]);
+            if (more) {
+              if (m == 0) {
+                wait_kv(kn);
+                two = ok && info_two[(n + 1) % C::INFO];
+                if (two) wait_kv(kn + 1);
+              }
+              if (ok) qk(m, kn, two);
+              if (m == mt - 1 && ok) tc::mma_commit(&kv_empty[kn % C::KVB]);
+              if (m == mt - 1 && ok && two) tc::mma_commit(&kv_empty[(kn + 1) % C::KVB]);
+            }
+          }
+          k = kn;
+        }
       }
     }
-    m = m1;
-    __syncthreads();
-  }
-  for (int u = 0; u < (D + 127) / 128; ++u) {
-    const int d = tid + u * 128;
-    if (d < D) out[d] = (uint16_t)pack2<BF16>(l != 0.0f ? acc[u] / l : 0.0f, 0.0f);
-  }
-  if (a.lse && tid == 0)
-    a.lse[(int64_t)row * a.q_heads + qh] = l != 0.0f ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
-}
+    __syncwarp();
+  } else if (warp >= C::EXP_WARP) {
+    // ---------------------------------------------------------------- expand
+    const int et = tid - C::EXP_WARP * 32, ew = et >> 5;
+    uint32_t n = 0, k = 0;  // tiles and operands so far
+    auto wait_free = [&]() {
+      if (k >= C::KVB)
+        ok = ok && mbar_wait_bounded(&kv_empty[k % C::KVB], (k / C::KVB - 1) & 1, a.wait_ns);
+      ok = __all_sync(0xffffffffu, ok);
+    };
+    auto filled = [&]() {
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&kv_full[k % C::KVB]);
+      ++k;
+    };
+    for (int round = 0, i; (i = pre_nth(round)) < items && ok; ++round) {
+      const PreItem it = pre_item<C>(a, pre, i);
+      const int pos_lo = it.pos0 + it.r0 / a.group, pos_hi = it.pos0 + (it.r0 + it.rows - 1) / a.group;
+      ok = __all_sync(0xffffffffu, mbar_wait_bounded(&size_full[round & 1], (round >> 1) & 1, a.wait_ns));
+      if (!ok) break;
+      float size[C::G];
+#pragma unroll
+      for (int q = 0; q < C::G; ++q) {
+        size[q] = 0.0f;
+#pragma unroll
+        for (int w = 0; w < C::SOFT_WARPS; ++w) size[q] = fmaxf(size[q], size_s[round & 1][w][q]);
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&size_empty[round & 1]);
+      for (int j = 0; j < it.tiles && ok; ++j, ++n) {
+        const int st = n & 1, tok0 = it.kv0 + j * C::NKV;
+        const uint8_t* raw = raw_s + st * C::RAW;
+        ok = mbar_wait_bounded(&raw_full[st], (n >> 1) & 1, a.wait_ns);
+        wait_free();
+        if (!ok) break;
+        const uint32_t pages = info_pages[n % C::INFO];
+        // tiles of which some row does not see some token
+        const bool edge = tok0 + C::NKV > it.seq || tok0 + C::NKV > pos_lo + 1 ||
+                          (a.window > 0 && tok0 <= pos_hi - a.window) || pages != (1u << C::TPK) - 1u;
+        // The score's error from keys rounded to 11 bits: each dim's is about
+        // 2^-12.3 |k|, so its variance is 2^-24.6 sum (scale q)^2 k^2, which is
+        // taken as |scale q_g|^2 times the mean k^2 of each group, of one token
+        // a block; 16 makes it 2^-20.6.  (Each of the four warps finds the same.)
+        bool two;
+        {
+          const int c = lane & 3, blk = (lane >> 2) % C::TPK, p = lane / (4 * C::TPK), tt = n & 15;
+          const uint8_t* tile = raw + blk * C::RSTRIDE;
+          float sum = 0.0f;
+#pragma unroll
+          for (int w = 0; w < C::WD; ++w) {
+            const int gq = p * (C::WD / 2) + w / 2;
+            const uint32_t v = *reinterpret_cast<const uint32_t*>(tile + p * 8 * C::W + tt * (C::W / 2) + c * (C::W / 8) + w * 4);
+            const float2 sm = __half22float2(*reinterpret_cast<const __half2*>(tile + 8 * C::D + (tt * C::G + gq) * 4));
+            const uint32_t x = v & 0x0f0f0f0fu, y = (v >> 4) & 0x0f0f0f0fu;
+            const float c2 = (float)__dp4a(x, x, __dp4a(y, y, 0u)), c1 = (float)__dp4a(x, 0x01010101u, __dp4a(y, 0x01010101u, 0u));
+            float sg = size[0];
+#pragma unroll
+            for (int q = 1; q < C::G; ++q) sg = gq == q ? size[q] : sg;
+            sum = fmaf(sg, fmaf(sm.x, fmaf(sm.x, c2, 2.0f * sm.y * c1), 8.0f * sm.y * sm.y), sum);
+          }
+          if (!((pages >> blk) & 1u) || tok0 + blk * kKvTile + tt >= it.hi) sum = 0.0f;
+#pragma unroll
+          for (int d = 1; d < 32; d <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+          two = sum > 16.0f * 64.0f * C::TPK;
+        }
+        if (et == 0) info_two[n % C::INFO] = two;
+        {
+          uint8_t* kb = kv_s + (k % C::KVB) * C::KV;
+#pragma unroll 2
+          for (int s = 0; s < C::NKV * 4 * C::NP / 128; ++s) {
+            const int u = et + 128 * s, p = u / (C::NKV * 4), t = (u / 4) % C::NKV, c = u % 4;
+            const uint8_t* tile = raw + (t / kKvTile) * C::RSTRIDE;
+            const int tt = t % kKvTile;
+            uint32_t w[C::WD];
+            const uint8_t* kp = tile + p * 8 * C::W + tt * (C::W / 2) + c * (C::W / 8);
+            if (C::WD == 4)
+              *reinterpret_cast<uint4*>(w) = *reinterpret_cast<const uint4*>(kp);
+            else
+              *reinterpret_cast<uint2*>(w) = *reinterpret_cast<const uint2*>(kp);
+#pragma unroll
+            for (int q = 0; q < C::WD / 2; ++q) {
+              const int gq = p * (C::WD / 2) + q;
+              const __half2 sm = *reinterpret_cast<const __half2*>(tile + 8 * C::D + (tt * C::G + gq) * 4);
+              const __half2 s2 = __low2half2(sm), m2 = __high2half2(sm);
+#pragma unroll
+              for (int x = 0; x < 2; ++x) {
+                const uint32_t v = w[2 * q + x], v8 = v >> 8;
+                // dims 0 4 1 5 2 6 3 7 of the word, the order that q is laid out in
+                const uint4 o = make_uint4(code_value(code_lo(v), s2, m2), code_value(code_hi(v), s2, m2),
+                                           code_value(code_lo(v8), s2, m2), code_value(code_hi(v8), s2, m2));
+                *reinterpret_cast<uint4*>(kb + gq * C::NKV * 128 + t * 128 + (((2 * c + x) ^ (t & 7)) << 4)) = o;
+              }
+              if (edge && c == 0) {  // values that are not finite: left out, and noted
+                const __half2 vm = *reinterpret_cast<const __half2*>(tile + C::HALF + 8 * C::D + (tt * C::G + gq) * 4);
+                if (!half_finite(__low2half(vm)) || !half_finite(__high2half(vm)))
+                  atomicOr(&info_bad[n % C::INFO][t / 32], 1u << (t % 32));
+              }
+            }
+          }
+          filled();
+        }
+        wait_free();
+        if (!ok) break;
+        if (two) {  // what the keys' rounding left
+          uint8_t* kb = kv_s + (k % C::KVB) * C::KV;
+#pragma unroll 1
+          for (int u = et; u < C::NKV * 4 * C::NP * C::WD; u += 128) {
+            const int w = u % C::WD, c = u / C::WD % 4, t = u / (4 * C::WD) % C::NKV, p = u / (4 * C::WD * C::NKV);
+            const int gq = p * (C::WD / 2) + w / 2, tt = t % kKvTile;
+            const uint8_t* tile = raw + (t / kKvTile) * C::RSTRIDE;
+            const uint32_t v = *reinterpret_cast<const uint32_t*>(tile + p * 8 * C::W + tt * (C::W / 2) + c * (C::W / 8) + w * 4);
+            const __half2 sm = *reinterpret_cast<const __half2*>(tile + 8 * C::D + (tt * C::G + gq) * 4);
+            const float2 f = __half22float2(sm);
+            uint32_t o[4];
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+              const uint32_t code = x % 2 ? code_hi(x > 1 ? v >> 8 : v) : code_lo(x > 1 ? v >> 8 : v);
+              const uint32_t val = code_value(code, __low2half2(sm), __high2half2(sm));
+              const float2 cf = __half22float2(*reinterpret_cast<const __half2*>(&code));
+              const float2 vf = __half22float2(*reinterpret_cast<const __half2*>(&val));
+              o[x] = half2_bits(fmaf(f.x, cf.x, f.y) - vf.x, fmaf(f.x, cf.y, f.y) - vf.y);
+            }
+            *reinterpret_cast<uint4*>(kb + gq * C::NKV * 128 + t * 128 + (((2 * c + w % 2) ^ (t & 7)) << 4)) =
+                make_uint4(o[0], o[1], o[2], o[3]);
+          }
+          filled();
+          wait_free();
+          if (!ok) break;
+        }
+        {
+          uint8_t* vb = kv_s + (k % C::KVB) * C::KV;
+          const int odd = ew & 1, tb = C::NKV == 128 ? ew >> 1 : 0, p = C::NKV == 128 ? 0 : ew >> 1;
+          const int tile4 = lane & 3, u = (lane >> 2) & 1, g = 2 * (lane >> 3) + u, h = u ^ odd;
+          const uint8_t* tile = raw + (tb * 4 + tile4) * C::RSTRIDE + C::HALF;
+          const uint8_t* vp = tile + p * 8 * C::W + h * 4 * C::W + g * (C::W / 2);
+          uint32_t w[4][C::WD];
+          __half2 s2[4][C::WD / 2], m2[4][C::WD / 2];
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            if (C::WD == 4)
+              *reinterpret_cast<uint4*>(w[c]) = *reinterpret_cast<const uint4*>(vp + c * (C::W / 8));
+            else
+              *reinterpret_cast<uint2*>(w[c]) = *reinterpret_cast<const uint2*>(vp + c * (C::W / 8));
+            __half2 sm[2][C::WD / 2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const uint8_t* sp = tile + 8 * C::D + ((8 * h + 2 * c + e) * C::G + p * (C::WD / 2)) * 4;
+              if (C::WD == 4)
+                *reinterpret_cast<uint2*>(sm[e]) = *reinterpret_cast<const uint2*>(sp);
+              else
+                sm[e][0] = *reinterpret_cast<const __half2*>(sp);
+              if (edge) {
+                const int t = tb * 64 + tile4 * 16 + 8 * h + 2 * c + e;
+                bool use = ((pages >> (t / kKvTile)) & 1u) && tok0 + t >= it.lo && tok0 + t < it.hi;
+#pragma unroll
+                for (int q = 0; q < C::WD / 2; ++q)
+                  if (!use || !half_finite(__low2half(sm[e][q])) || !half_finite(__high2half(sm[e][q])))
+                    sm[e][q] = __float2half2_rn(0.0f);
+              }
+            }
+#pragma unroll
+            for (int q = 0; q < C::WD / 2; ++q) {
+              s2[c][q] = __lows2half2(sm[0][q], sm[1][q]);
+              m2[c][q] = __highs2half2(sm[0][q], sm[1][q]);
+            }
+          }
+#pragma unroll
+          for (int x = 0; x < C::WD; ++x) {
+            const int gq = p * (C::WD / 2) + x / 2;
+            const int d0 = gq * 64 + 8 * g + 4 * (x % 2);
+#pragma unroll
+            for (int jj = 0; jj < 4; ++jj) {
+              uint32_t o[4];
+#pragma unroll
+              for (int c = 0; c < 4; ++c) {
+                const uint32_t v = jj >= 2 ? w[c][x] >> 8 : w[c][x];
+                o[c] = code_value(jj % 2 ? code_hi(v) : code_lo(v), s2[c][x / 2], m2[c][x / 2]);
+              }
+              const int d = d0 + jj;
+              *reinterpret_cast<uint4*>(vb + tb * C::D * 128 + d * 128 + (((tile4 * 2 + h) ^ (d & 7)) << 4)) =
+                  make_uint4(o[0], o[1], o[2], o[3]);
+            }
+          }
+          filled();
+          if (lane == 0) mbar_arrive(&raw_empty[st]);
+        }
+      }
+    }
+  } else {
+    // --------------------------------------------------------------- softmax
+    const int m = warp >> 2, wl = warp & 3, r_l = wl * 32 + lane;
+    const uint32_t t_s = tmem + m * 128 + ((uint32_t)(wl * 32) << 16);
+    const uint32_t t_o = tmem + kO + m * 128 + ((uint32_t)(wl * 32) << 16);
+    uint32_t n = 0, n_t = 0;  // tiles of all items; tiles of this half
+    const float sign = a.scale_log2 < 0.0f ? -1.0f : 1.0f;
+    // an item's rows ahead of their turn: the row's largest |q|, returned, and
+    // for the expand warps the largest |scale q_g|^2
+    auto measure = [&](int round) -> float {
+      float top = 0.0f, sq[C::G];
+#pragma unroll
+      for (int q = 0; q < C::G; ++q) sq[q] = 0.0f;
+      const int i = pre_nth(round);
+      if (i >= items) return top;
+      if (round >= 2) {
+        ok = __all_sync(0xffffffffu, mbar_wait_bounded(&size_empty[round & 1], ((round >> 1) - 1) & 1, a.wait_ns));
+        if (!ok) return top;
+      }
+      const PreItem it = pre_item<C>(a, pre, i);
+      const int row = it.r0 + m * 128 + r_l, tok = row / a.group;
+      if (m * 128 + r_l < it.rows) {
+        const uint16_t* qp = reinterpret_cast<const uint16_t*>(a.q) + (int64_t)(it.row0 + tok) * a.ld_q +
+                             (it.h * a.group + row - tok * a.group) * C::D;
+#pragma unroll
+        for (int q = 0; q < C::G; ++q)
+#pragma unroll 4
+          for (int k = 0; k < 8; ++k) {
+            const uint4 v = ldg_nc_v4(qp + q * 64 + k * 8);
+            const uint32_t* w = reinterpret_cast<const uint32_t*>(&v);
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+              const float2 f = unpack2<C::BF16>(w[x]);
+              top = fmaxf(top, fmaxf(fabsf(f.x), fabsf(f.y)));
+              sq[q] = fmaf(f.x, f.x, fmaf(f.y, f.y, sq[q]));
+            }
+          }
+      }
+      const float sc = a.scale_log2 * 0.69314718055994531f;
+#pragma unroll
+      for (int q = 0; q < C::G; ++q) {
+        float x = sq[q] * sc * sc;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, d));
+        if (lane == 0) size_s[round & 1][warp][q] = x;
+      }
+      if (lane == 0) mbar_arrive(&size_full[round & 1]);
+      return top;
+    };
+    float top_next = measure(0);
+    for (int round = 0, i; (i = pre_nth(round)) < items && ok; ++round) {
+      const PreItem it = pre_item<C>(a, pre, i);
+      const float top = top_next;
+      if (m * 128 >= it.rows) {  // this half sits the item out
+        top_next = measure(round + 1);
+        n += it.tiles;
+        continue;
+      }
+      const bool live = m * 128 + r_l < it.rows;
+      const int row = it.r0 + m * 128 + r_l, tok = row / a.group;
+      const int head = it.h * a.group + row - tok * a.group;
+      // q of the row (earlier products with this half's q are done)
+      const uint16_t* qp = reinterpret_cast<const uint16_t*>(a.q) + (int64_t)(it.row0 + tok) * a.ld_q + head * C::D;
+      int e = (int)((__float_as_uint(top) >> 23) & 255u) - 127;
+      e = e < -100 ? -100 : e;
+      const float up = pow2i(14 - e) * sign;
+      const float qa = fabsf(a.scale_log2) * pow2i(e) * (1.0f / 16384.0f);
+#pragma unroll 4
+      for (int k = 0; k < C::D / 8; ++k) {
+        const uint4 v = live ? ldg_nc_v4(qp + k * 8) : make_uint4(0, 0, 0, 0);
+        const uint32_t* w = reinterpret_cast<const uint32_t*>(&v);
+        float f[8];
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          const float2 y = unpack2<C::BF16>(w[x]);
+          f[2 * x] = y.x * up;
+          f[2 * x + 1] = y.y * up;
+        }
+        *reinterpret_cast<uint4*>(q_s + m * 128 * C::D * 2 + (k / 8) * 16384 + r_l * 128 +
+                                  (((k % 8) ^ (r_l & 7)) << 4)) =
+            make_uint4(half2_bits(f[0], f[4]), half2_bits(f[1], f[5]), half2_bits(f[2], f[6]),
+                       half2_bits(f[3], f[7]));
+      }
+      fence_proxy_async_smem();
+      tc::fence_before_sync();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&q_full[m]);
+      top_next = measure(round + 1);
+      if (!ok) break;
 
+      const int pos = it.pos0 + tok;
+      const int see_hi = live ? (pos + 1 < it.seq ? pos + 1 : it.seq) : -1;
+      const int see_lo = a.window > 0 ? pos + 1 - a.window : 0;
+      const int last = it.rows < m * 128 + 128 ? it.rows : m * 128 + 128;
+      const int pos_lo = it.pos0 + (it.r0 + m * 128) / a.group;
+      const int pos_hi = it.pos0 + (it.r0 + last - 1) / a.group;
+      float m_run = kNoMax, l = 0.0f;
+      for (int j = 0; j < it.tiles; ++j, ++n, ++n_t) {
+        ok = __all_sync(0xffffffffu, mbar_wait_bounded(&s_full[m], n_t & 1, a.wait_ns));
+        if (!ok) break;
+        tc::fence_after_sync();
+        const int tok0 = it.kv0 + j * C::NKV;
+        const uint32_t pages = info_pages[n % C::INFO];
+        const bool edge = tok0 + C::NKV > it.seq || tok0 + C::NKV > pos_lo + 1 ||
+                          (a.window > 0 && tok0 <= pos_hi - a.window) || pages != (1u << C::TPK) - 1u;
+        // columns that the row sees, and the blocks of 16 that were not read
+        const int c_lo = see_lo - tok0, c_hi = see_hi - tok0;
+        auto masked = [&](float v, int col) {
+          return col >= c_lo && col < c_hi && ((pages >> (col / kKvTile)) & 1u) ? v * qa : -INFINITY;
+        };
+        // the maximum, O scaled where it grew; true if a wait gave up
+        auto raise = [&](float mx) -> bool {
+          const float m1 = fmaxf(m_run, mx), keep = exp2_fast(m_run - m1);
+          m_run = m1;
+          l *= keep;
+          if (j == 0) return false;
+          if (!__all_sync(0xffffffffu, mbar_wait_bounded(&pv_done[m], (n_t - 1) & 1, a.wait_ns)))
+            return true;
+          tc::fence_after_sync();
+#pragma unroll 1
+          for (int ch = 0; ch < C::D / 32; ++ch) {
+            float v[32];
+            tc::tmem_ld32(t_o + ch * 32, v);
+#pragma unroll
+            for (int x = 0; x < 32; ++x) v[x] *= keep;
+            tc::tmem_st32(t_o + ch * 32, v);
+          }
+          return false;
+        };
+        if (edge || j == 0) {
+          // masks, or no maximum yet: the maximum first, then the weights
+          float mx = -INFINITY;
+#pragma unroll 1
+          for (int ch = 0; ch < C::NKV / 32; ++ch) {
+            float v[32];
+            tc::tmem_ld32(t_s + ch * 32, v);
+#pragma unroll
+            for (int x = 0; x < 32; ++x) mx = fmaxf(mx, masked(v[x], ch * 32 + x));
+          }
+          if (__any_sync(0xffffffffu, mx > m_run + 8.0f) && raise(mx)) {
+            ok = false;
+            break;
+          }
+          const float off = 7.0f - m_run;
+#pragma unroll 1
+          for (int ch = 0; ch < C::NKV / 32; ++ch) {
+            float v[32];
+            uint32_t w[16];
+            tc::tmem_ld32(t_s + ch * 32, v);
+#pragma unroll
+            for (int x = 0; x < 32; ++x) v[x] = exp2_fast(masked(v[x], ch * 32 + x) + off);
+#pragma unroll
+            for (int x = 0; x < 16; ++x) {
+              l += v[2 * x] + v[2 * x + 1];
+              w[x] = half2_bits(v[2 * x], v[2 * x + 1]);
+            }
+            tc::tmem_st16(t_s + ch * 16, w);  // (over columns read already)
+          }
+        } else {
+          // weights by the maximum so far, kept in registers until the tile is
+          // known not to exceed it by 2^8; else once more by the new one
+          uint32_t w[C::NKV / 2];
+          uint64_t l2;
+          float mx;
+          bool again = false;
+          do {
+            const float off = 7.0f - m_run;
+            const uint64_t qa2 = f32x2(qa, qa), off2 = f32x2(off, off);
+            l2 = f32x2(0.0f, 0.0f);
+            mx = -INFINITY;
+#pragma unroll
+            for (int ch = 0; ch < C::NKV / 32; ++ch) {
+              float v[32];
+              tc::tmem_ld32(t_s + ch * 32, v);
+#pragma unroll
+              for (int x = 0; x < 16; ++x) {
+                mx = fmaxf(fmaxf(mx, v[2 * x]), v[2 * x + 1]);
+                float e0, e1;
+                f32x2_split(fma_f32x2(f32x2(v[2 * x], v[2 * x + 1]), qa2, off2), e0, e1);
+                e0 = exp2_fast(e0);
+                e1 = exp2_fast(e1);
+                l2 = add_f32x2(l2, f32x2(e0, e1));
+                w[ch * 16 + x] = half2_bits(e0, e1);
+              }
+            }
+            mx *= qa;
+            again = __any_sync(0xffffffffu, mx > m_run + 8.0f);
+            if (again && raise(mx)) {
+              ok = false;
+              break;
+            }
+          } while (again);
+          if (!ok) break;
+          float l0, l1;
+          f32x2_split(l2, l0, l1);
+          l += l0 + l1;
+#pragma unroll
+          for (int ch = 0; ch < C::NKV / 32; ++ch) tc::tmem_st16(t_s + ch * 16, w + ch * 16);
+        }
+        tc::tmem_wait_st();
+        tc::fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&p_full[m]);
+        if (edge) {
+          for (int w = 0; w < C::NKV / 32; ++w)
+            for (uint32_t bits = info_bad[n % C::INFO][w]; bits; bits &= bits - 1) {
+              const int col = w * 32 + __ffs(bits) - 1;
+              if (masked(1.0f, col) != -INFINITY) l = __int_as_float(0x7fffffff);
+            }
+        }
+      }
+      if (!ok) break;
+      ok = __all_sync(0xffffffffu, mbar_wait_bounded(&pv_done[m], (n_t - 1) & 1, a.wait_ns));
+      if (!ok) break;
+      tc::fence_after_sync();
+      const float inv = l != 0.0f ? 1.0f / l : 0.0f;
+      uint16_t* out = reinterpret_cast<uint16_t*>(a.out) + (int64_t)(it.row0 + tok) * a.ld_out + head * C::D;
+#pragma unroll 1
+      for (int ch = 0; ch < C::D / 32; ++ch) {
+        float v[32];
+        tc::tmem_ld32(t_o + ch * 32, v);
+        if (live) {
+#pragma unroll
+          for (int x = 0; x < 4; ++x)
+            *reinterpret_cast<uint4*>(out + ch * 32 + x * 8) =
+                make_uint4(pack2<C::BF16>(v[8 * x] * inv, v[8 * x + 1] * inv),
+                           pack2<C::BF16>(v[8 * x + 2] * inv, v[8 * x + 3] * inv),
+                           pack2<C::BF16>(v[8 * x + 4] * inv, v[8 * x + 5] * inv),
+                           pack2<C::BF16>(v[8 * x + 6] * inv, v[8 * x + 7] * inv));
+        }
+      }
+      if (live && a.lse)
+        a.lse[(int64_t)(it.row0 + tok) * a.q_heads + head] =
+            l != 0.0f ? (m_run + log2f(l) - 7.0f) * 0.69314718055994531f : -INFINITY;
+      tc::fence_before_sync();
+    }
+  }
+  if (!ok) set_error(a.err, LORA_DEV_ERR_TIMEOUT);
+  // After a time-out the products issued last may still run: one more commit
+  // tracks them, and tensor memory is freed after it has arrived.
+  if (!__syncthreads_and(ok) && warp == C::MMA_WARP && lane == 0 && issued) {
+    tc::mma_commit(&drain_bar);
+    mbar_wait_bounded(&drain_bar, 0, kWaitLimitNs);
+  }
+  tc::fence_before_sync();
+  __syncthreads();
+  if (warp == C::MMA_WARP) tc::tmem_dealloc(tmem, 512);
+}
 
 }  // namespace lora

@@ -43,6 +43,10 @@ int check_rows(const void* p, int64_t ld, int n, int width) {
   return ld % 8 || !aligned16(p) ? LORA_ERR_ALIGN : LORA_OK;
 }
 
+// Dynamic shared memory of an attention CTA: what a CTA may have, less the
+// kernels' own variables.
+constexpr size_t kAttnMaxSmem = 227 * 1024 - 2048;
+
 // f(kernel for head_dim and type)
 template <class F>
 int by_type(int head_dim, int dtype, F f) {
@@ -92,21 +96,40 @@ int rows_call(bool store, const void* k, int64_t ld_k, const void* v, int64_t ld
   });
 }
 
-// Configurations of the decode kernel: warps by the registers of their sums,
-// stages by the shared memory that is left (about 40 KB of copies in flight a
-// CTA cover the latency of HBM).
+// Configurations of the decode kernel: 16 warps where their sums fit 128
+// registers, else 8.
 template <int D, bool BF16, int NT>
-using DecCfg = Dec<D, BF16, NT, (D * NT <= 128 ? 16 : 8),
-                   (D == 64 ? 8 : D == 256 ? (NT == 1 ? 5 : 4) : NT == 1 ? 5 : 8)>;
+using DecCfg = Dec<D, BF16, NT, (D * NT <= 128 ? 16 : 8)>;
 
 template <class C>
 int launch_decode(const AttnArgs& a, cudaStream_t stream) {
-  const int smem = (int)C::smem(a.B);
+  // as many units in flight as shared memory holds
+  int stages = C::MAX_STAGES;
+  while (stages > C::MIN_STAGES && C::smem(a.B, stages) > kAttnMaxSmem) --stages;
+  static_assert(C::smem(kAttnMaxReqs, C::MIN_STAGES) <= kAttnMaxSmem, "a CTA's shared memory");
+  const int smem = (int)C::smem(a.B, stages);
   if (prepare_kernel(kv4_decode_kernel<C>, smem, false) != cudaSuccess) return LORA_ERR_CUDA;
   int ctas = sm_count();
   if (ctas > kAttnMaxCtas) ctas = kAttnMaxCtas;
-  static const int alone = env_int("LORA_ATTN_ALONE", 128);
-  kv4_decode_kernel<C><<<ctas, C::THREADS, smem, stream>>>(a, alone, 1);
+  static const int alone = env_int("LORA_ATTN_ALONE", 64);
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)ctas);
+  cfg.blockDim = dim3(C::THREADS);
+  cfg.dynamicSmemBytes = (size_t)smem;
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = use_pdl() ? 1 : 0;
+  return cuda_status(cudaLaunchKernelEx(&cfg, kv4_decode_kernel<C>, a, stages, alone));
+}
+
+template <class C>
+int launch_prefill(const AttnArgs& a, int min_rows, cudaStream_t stream) {
+  const int smem = (int)C::smem(a.B);
+  if (prepare_kernel(kv4_prefill_kernel<C>, smem, false) != cudaSuccess) return LORA_ERR_CUDA;
+  kv4_prefill_kernel<C><<<sm_count(), C::THREADS, smem, stream>>>(a, min_rows);
   return cuda_status(cudaGetLastError());
 }
 
@@ -141,7 +164,7 @@ int lora_batch_plan(const int32_t* ctx_len, const int32_t* new_len, const int32_
     return LORA_ERR_ARG;
   if (const int rc = check_page_size(page_size)) return rc;
   if (n_reqs > kPlanMaxReqs || (int64_t)n_reqs * max_pages > INT32_MAX ||
-      (int64_t)max_pages * page_size > INT32_MAX)
+      (int64_t)max_pages * page_size > (1 << 29))
     return LORA_ERR_UNSUPPORTED;
   if (n_reqs > 1 && ld_table < max_pages) return LORA_ERR_SHAPE;
   if (!aligned16(row_req) || !aligned16(position) || !aligned16(slot_map) || !aligned16(seq_slot))
@@ -221,14 +244,16 @@ int lora_kv4_attention(void* out, int64_t ld_out, const void* q, int64_t ld_q, i
   if (rc) return rc;
   if (q_heads % kv_heads) return LORA_ERR_SHAPE;
   if (!row_start || (n_reqs > 0 && (!seq_len || !block_table))) return LORA_ERR_ARG;
-  if (n_reqs > kAttnMaxReqs || (int64_t)max_pages * page_size > INT32_MAX || q_heads > 65535)
+  if (n_reqs > kAttnMaxReqs || (int64_t)max_pages * page_size > (1 << 29) || q_heads > 65535)
     return LORA_ERR_UNSUPPORTED;
   if ((rc = check_rows(out, ld_out, n, q_heads * head_dim))) return rc;
   if ((rc = check_rows(q, ld_q, n, q_heads * head_dim))) return rc;
   if (n_reqs > 1 && ld_table < max_pages) return LORA_ERR_SHAPE;
   if (!workspace || ws_bytes < lora_kv4_attention_workspace_size()) return LORA_ERR_WORKSPACE;
   if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return LORA_ERR_ALIGN;
-  if ((int64_t)n_reqs * max_pages * (page_size / kKvTile) > INT32_MAX) return LORA_ERR_UNSUPPORTED;
+  if (n_reqs * ((int64_t)max_pages * (page_size / kKvTile) + kItemCost) * kv_heads > INT32_MAX ||
+      (int64_t)n * (q_heads / kv_heads) > INT32_MAX)
+    return LORA_ERR_UNSUPPORTED;
   AttnArgs a = {};
   a.out = out;
   a.q = q;
@@ -238,12 +263,14 @@ int lora_kv4_attention(void* out, int64_t ld_out, const void* q, int64_t ld_q, i
   a.q_heads = q_heads;
   a.heads = kv_heads;
   a.group = q_heads / kv_heads;
+  a.group_inv = (uint32_t)((65536 + a.group - 1) / a.group);
   a.pages = reinterpret_cast<const uint8_t*>(pages);
   a.num_pages = num_pages;
   a.page_size = page_size;
   a.table = block_table;
   a.ld_table = ld_table;
-  a.max_pages = max_pages;
+  a.cap = max_pages * page_size;
+  a.tpp_inv = (uint32_t)(((1ull << 31) + page_size / kKvTile - 1) / (page_size / kKvTile));
   a.row_start = row_start;
   a.seq_len = seq_len;
   a.B = n_reqs;
@@ -261,11 +288,12 @@ int lora_kv4_attention(void* out, int64_t ld_out, const void* q, int64_t ld_q, i
     constexpr bool BF16 = decltype(bf)::value;
     if (rows <= 8) return launch_decode<DecCfg<D, BF16, 1>>(a, (cudaStream_t)stream);
     if (rows <= 16) return launch_decode<DecCfg<D, BF16, 2>>(a, (cudaStream_t)stream);
-    if constexpr (D < 256)
-      if (rows <= 32) return launch_decode<DecCfg<D, BF16, 4>>(a, (cudaStream_t)stream);
-    kv4_attn_simple_kernel<D, BF16>
-        <<<dim3((unsigned)n, (unsigned)q_heads), 128, 0, (cudaStream_t)stream>>>(a);
-    return cuda_status(cudaGetLastError());
+    // the most rows that the decode kernel takes; requests with more go to the
+    // tensor cores
+    constexpr int NT = D == 256 ? 2 : 4;
+    const int rc = launch_decode<DecCfg<D, BF16, NT>>(a, (cudaStream_t)stream);
+    if (rc || rows <= 8 * NT) return rc;
+    return launch_prefill<Pre<D, BF16>>(a, 8 * NT, (cudaStream_t)stream);
   });
 }
 
