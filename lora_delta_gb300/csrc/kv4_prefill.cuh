@@ -5,7 +5,7 @@
 // key/value head; 128 rows at head_dim 256) and the tokens that they see, in
 // tiles of 128 (64).  Roles of a CTA, handing over through mbarriers:
 //   load warp       bulk copies of the tile's packed 16-token blocks
-//   4 expand warps  codes to f16 values s c + m in the operands' 128-byte
+//   8 expand warps  codes to f16 values s c + m in the operands' 128-byte
 //                   swizzled layout, keys [token][dim], values [dim][token]
 //   MMA warp        S = Q K^T (128 x 128 a row half, in tensor memory), then
 //                   O += P V with P read from tensor memory
@@ -47,7 +47,7 @@ struct Pre {
   static constexpr int Q = ROWS * D * 2;
   static constexpr int INFO = 8;                    // tiles described at once
   static constexpr int SOFT_WARPS = 4 * MT;
-  static constexpr int EXP_WARP = SOFT_WARPS, MMA_WARP = EXP_WARP + 4, LOAD_WARP = MMA_WARP + 1;
+  static constexpr int EXP_WARP = SOFT_WARPS, EXP_WARPS = 8, MMA_WARP = EXP_WARP + EXP_WARPS, LOAD_WARP = MMA_WARP + 1;
   static constexpr int THREADS = (LOAD_WARP + 1) * 32;
   static constexpr size_t smem(int B) {
     return 1024 + (size_t)Q + KVB * KV + 2 * RAW + (size_t)(B + 1) * 4;
@@ -140,6 +140,11 @@ __device__ __forceinline__ uint64_t fma_f32x2(uint64_t a, uint64_t b, uint64_t c
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
   return r;
 }
+__device__ __forceinline__ uint64_t mul_f32x2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
 __device__ __forceinline__ uint64_t add_f32x2(uint64_t a, uint64_t b) {
   uint64_t r;
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
@@ -168,15 +173,15 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_prefill_kernel(const AttnAr
     for (int i = 0; i < 2; ++i) {
       mbar_init(&raw_full[i], 1);
       mbar_init(&size_full[i], C::SOFT_WARPS);
-      mbar_init(&size_empty[i], 4);
-      mbar_init(&raw_empty[i], 4);
+      mbar_init(&size_empty[i], C::EXP_WARPS);
+      mbar_init(&raw_empty[i], C::EXP_WARPS);
       mbar_init(&q_full[i], 4);
       mbar_init(&s_full[i], 1);
       mbar_init(&p_full[i], 4);
       mbar_init(&pv_done[i], 1);
     }
     for (int i = 0; i < C::KVB; ++i) {
-      mbar_init(&kv_full[i], 4);
+      mbar_init(&kv_full[i], C::EXP_WARPS);
       mbar_init(&kv_empty[i], 1);
     }
     mbar_init(&drain_bar, 1);
@@ -269,6 +274,9 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_prefill_kernel(const AttnAr
     // ------------------------------------------------------------------- MMA
     if (lane == 0) {
       const uint32_t id_qk = tc::idesc_f16_f32(128, C::NKV), id_pv = tc::idesc_f16_f32(128, C::D);
+      // (start addresses are in 16-byte units in a descriptor's low bits, and no
+      // sum below carries out of them)
+      const uint64_t q_desc = tc::sw128_desc(smem_addr(q_s)), kv_desc = tc::sw128_desc(smem_addr(kv_s));
       uint32_t k = 0, n = 0;                       // operands and tiles so far
       uint32_t n_it[2] = {0, 0}, n_t[2] = {0, 0};  // items and tiles of each row half
       auto wait_kv = [&](uint32_t x) {
@@ -277,14 +285,15 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_prefill_kernel(const AttnAr
       };
       // S of a half from the keys in operand x, and x + 1 where they are two
       auto qk = [&](int m, uint32_t x, bool two) {
-        const uint32_t qa = smem_addr(q_s) + m * 128 * C::D * 2;
+        const uint64_t qd = q_desc + (uint64_t)(m * 128 * C::D * 2 / 16);
 #pragma unroll 1
         for (int y = 0; y < (two ? 2 : 1); ++y) {
-          const uint32_t ka = smem_addr(kv_s) + ((x + y) % C::KVB) * C::KV;
+          const uint64_t kd = kv_desc + (uint64_t)(((x + y) % C::KVB) * (C::KV / 16));
+          tc::mma_bf16(tmem + m * 128, qd, kd, id_qk, y);
 #pragma unroll
-          for (int d = 0; d < C::D / 16; ++d)
-            tc::mma_bf16(tmem + m * 128, tc::sw128_desc(qa + (d / 4) * 16384 + (d % 4) * 32),
-                         tc::sw128_desc(ka + (d / 4) * C::NKV * 128 + (d % 4) * 32), id_qk, d > 0 || y > 0);
+          for (int d = 1; d < C::D / 16; ++d)
+            tc::mma_bf16(tmem + m * 128, qd + ((d / 4) * 16384 + (d % 4) * 32) / 16,
+                         kd + ((d / 4) * C::NKV * 128 + (d % 4) * 32) / 16, id_qk, 1);
         }
         issued = true;
         tc::mma_commit(&s_full[m]);
@@ -306,16 +315,16 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_prefill_kernel(const AttnAr
           const uint32_t v = k + 1 + two, kn = v + 1;
           const bool more = j + 1 < it.tiles;
           wait_kv(v);
-          const uint32_t va = smem_addr(kv_s) + (v % C::KVB) * C::KV;
+          const uint64_t vd = kv_desc + (uint64_t)((v % C::KVB) * (C::KV / 16));
           for (int m = 0; m < mt && ok; ++m) {
             ok = mbar_wait_bounded(&p_full[m], n_t[m]++ & 1, a.wait_ns);
             tc::fence_after_sync();
             if (!ok) break;
+            tc::mma_f16_ts(tmem + kO + m * 128, tmem + m * 128, vd, id_pv, j > 0);
 #pragma unroll
-            for (int t = 0; t < C::NKV / 16; ++t)
+            for (int t = 1; t < C::NKV / 16; ++t)
               tc::mma_f16_ts(tmem + kO + m * 128, tmem + m * 128 + t * 8,
-                             tc::sw128_desc(va + (t / 4) * C::D * 128 + (t % 4) * 32), id_pv,
-                             j > 0 || t > 0);
+                             vd + ((t / 4) * C::D * 128 + (t % 4) * 32) / 16, id_pv, 1);
             issued = true;
             tc::mma_commit(&pv_done[m]);
             if (m == mt - 1) tc::mma_commit(&kv_empty[v % C::KVB]);
@@ -377,7 +386,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_prefill_kernel(const AttnAr
         // The score's error from keys rounded to 11 bits: each dim's is about
         // 2^-12.3 |k|, so its variance is 2^-24.6 sum (scale q)^2 k^2, which is
         // taken as |scale q_g|^2 times the mean k^2 of each group, of one token
-        // a block; 16 makes it 2^-20.6.  (Each of the four warps finds the same.)
+        // a block; 16 makes it 2^-20.6.  (Each of the warps finds the same.)
         bool two;
         {
           const int c = lane & 3, blk = (lane >> 2) % C::TPK, p = lane / (4 * C::TPK), tt = n & 15;
@@ -403,9 +412,9 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_prefill_kernel(const AttnAr
         if (et == 0) info_two[n % C::INFO] = two;
         {
           uint8_t* kb = kv_s + (k % C::KVB) * C::KV;
-#pragma unroll 2
-          for (int s = 0; s < C::NKV * 4 * C::NP / 128; ++s) {
-            const int u = et + 128 * s, p = u / (C::NKV * 4), t = (u / 4) % C::NKV, c = u % 4;
+#pragma unroll
+          for (int s = 0; s < C::NKV * 4 * C::NP / (32 * C::EXP_WARPS); ++s) {
+            const int u = et + 32 * C::EXP_WARPS * s, p = u / (C::NKV * 4), t = (u / 4) % C::NKV, c = u % 4;
             const uint8_t* tile = raw + (t / kKvTile) * C::RSTRIDE;
             const int tt = t % kKvTile;
             uint32_t w[C::WD];
@@ -441,7 +450,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_prefill_kernel(const AttnAr
         if (two) {  // what the keys' rounding left
           uint8_t* kb = kv_s + (k % C::KVB) * C::KV;
 #pragma unroll 1
-          for (int u = et; u < C::NKV * 4 * C::NP * C::WD; u += 128) {
+          for (int u = et; u < C::NKV * 4 * C::NP * C::WD; u += 32 * C::EXP_WARPS) {
             const int w = u % C::WD, c = u / C::WD % 4, t = u / (4 * C::WD) % C::NKV, p = u / (4 * C::WD * C::NKV);
             const int gq = p * (C::WD / 2) + w / 2, tt = t % kKvTile;
             const uint8_t* tile = raw + (t / kKvTile) * C::RSTRIDE;
@@ -466,55 +475,50 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_prefill_kernel(const AttnAr
         }
         {
           uint8_t* vb = kv_s + (k % C::KVB) * C::KV;
-          const int odd = ew & 1, tb = C::NKV == 128 ? ew >> 1 : 0, p = C::NKV == 128 ? 0 : ew >> 1;
+          // a warp takes 64 tokens' half of the dims of every group's eighths: words
+          // [x0, x0 + WH) of each lane place, all of one group where W is 128
+          constexpr int WH = C::WD / 2;
+          const int odd = ew & 1, tb = C::NKV == 128 ? (ew >> 1) & 1 : 0, p = C::NKV == 128 ? 0 : (ew >> 1) & 1;
+          const int x0 = (ew >> 2) * WH, gq = p * (C::WD / 2) + x0 / 2;
           const int tile4 = lane & 3, u = (lane >> 2) & 1, g = 2 * (lane >> 3) + u, h = u ^ odd;
           const uint8_t* tile = raw + (tb * 4 + tile4) * C::RSTRIDE + C::HALF;
-          const uint8_t* vp = tile + p * 8 * C::W + h * 4 * C::W + g * (C::W / 2);
-          uint32_t w[4][C::WD];
-          __half2 s2[4][C::WD / 2], m2[4][C::WD / 2];
+          const uint8_t* vp = tile + p * 8 * C::W + h * 4 * C::W + g * (C::W / 2) + x0 * 4;
+          uint32_t w[4][WH];
+          __half2 s2[4], m2[4];
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
-            if (C::WD == 4)
-              *reinterpret_cast<uint4*>(w[c]) = *reinterpret_cast<const uint4*>(vp + c * (C::W / 8));
-            else
+            if (WH == 2)
               *reinterpret_cast<uint2*>(w[c]) = *reinterpret_cast<const uint2*>(vp + c * (C::W / 8));
-            __half2 sm[2][C::WD / 2];
+            else
+              w[c][0] = *reinterpret_cast<const uint32_t*>(vp + c * (C::W / 8));
+            __half2 sm[2];
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-              const uint8_t* sp = tile + 8 * C::D + ((8 * h + 2 * c + e) * C::G + p * (C::WD / 2)) * 4;
-              if (C::WD == 4)
-                *reinterpret_cast<uint2*>(sm[e]) = *reinterpret_cast<const uint2*>(sp);
-              else
-                sm[e][0] = *reinterpret_cast<const __half2*>(sp);
+              sm[e] = *reinterpret_cast<const __half2*>(tile + 8 * C::D + ((8 * h + 2 * c + e) * C::G + gq) * 4);
               if (edge) {
                 const int t = tb * 64 + tile4 * 16 + 8 * h + 2 * c + e;
-                bool use = ((pages >> (t / kKvTile)) & 1u) && tok0 + t >= it.lo && tok0 + t < it.hi;
-#pragma unroll
-                for (int q = 0; q < C::WD / 2; ++q)
-                  if (!use || !half_finite(__low2half(sm[e][q])) || !half_finite(__high2half(sm[e][q])))
-                    sm[e][q] = __float2half2_rn(0.0f);
+                const bool use = ((pages >> (t / kKvTile)) & 1u) && tok0 + t >= it.lo && tok0 + t < it.hi;
+                if (!use || !half_finite(__low2half(sm[e])) || !half_finite(__high2half(sm[e])))
+                  sm[e] = __float2half2_rn(0.0f);
               }
             }
-#pragma unroll
-            for (int q = 0; q < C::WD / 2; ++q) {
-              s2[c][q] = __lows2half2(sm[0][q], sm[1][q]);
-              m2[c][q] = __highs2half2(sm[0][q], sm[1][q]);
-            }
+            s2[c] = __lows2half2(sm[0], sm[1]);
+            m2[c] = __highs2half2(sm[0], sm[1]);
           }
+          uint8_t* to = vb + tb * C::D * 128;
 #pragma unroll
-          for (int x = 0; x < C::WD; ++x) {
-            const int gq = p * (C::WD / 2) + x / 2;
-            const int d0 = gq * 64 + 8 * g + 4 * (x % 2);
+          for (int x = 0; x < WH; ++x) {
+            const int d0 = gq * 64 + 8 * g + 4 * ((x0 + x) % 2);
 #pragma unroll
             for (int jj = 0; jj < 4; ++jj) {
               uint32_t o[4];
 #pragma unroll
               for (int c = 0; c < 4; ++c) {
                 const uint32_t v = jj >= 2 ? w[c][x] >> 8 : w[c][x];
-                o[c] = code_value(jj % 2 ? code_hi(v) : code_lo(v), s2[c][x / 2], m2[c][x / 2]);
+                o[c] = code_value(jj % 2 ? code_hi(v) : code_lo(v), s2[c], m2[c]);
               }
               const int d = d0 + jj;
-              *reinterpret_cast<uint4*>(vb + tb * C::D * 128 + d * 128 + (((tile4 * 2 + h) ^ (d & 7)) << 4)) =
+              *reinterpret_cast<uint4*>(to + d * 128 + (((tile4 * 2 + h) ^ (d & 7)) << 4)) =
                   make_uint4(o[0], o[1], o[2], o[3]);
             }
           }
@@ -529,7 +533,8 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_prefill_kernel(const AttnAr
     const uint32_t t_s = tmem + m * 128 + ((uint32_t)(wl * 32) << 16);
     const uint32_t t_o = tmem + kO + m * 128 + ((uint32_t)(wl * 32) << 16);
     uint32_t n = 0, n_t = 0;  // tiles of all items; tiles of this half
-    const float sign = a.scale_log2 < 0.0f ? -1.0f : 1.0f;
+    // (a scale of 0 goes with q too, so that masked scores times qa stay -inf)
+    const float sign = a.scale_log2 < 0.0f ? -1.0f : a.scale_log2 > 0.0f ? 1.0f : 0.0f;
     // an item's rows ahead of their turn: the row's largest |q|, returned, and
     // for the expand warps the largest |scale q_g|^2
     auto measure = [&](int round) -> float {
@@ -589,7 +594,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_prefill_kernel(const AttnAr
       int e = (int)((__float_as_uint(top) >> 23) & 255u) - 127;
       e = e < -100 ? -100 : e;
       const float up = pow2i(14 - e) * sign;
-      const float qa = fabsf(a.scale_log2) * pow2i(e) * (1.0f / 16384.0f);
+      const float qa = sign == 0.0f ? 1.0f : fabsf(a.scale_log2) * pow2i(e) * (1.0f / 16384.0f);
 #pragma unroll 4
       for (int k = 0; k < C::D / 8; ++k) {
         const uint4 v = live ? ldg_nc_v4(qp + k * 8) : make_uint4(0, 0, 0, 0);
@@ -630,98 +635,75 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_prefill_kernel(const AttnAr
                           (a.window > 0 && tok0 <= pos_hi - a.window) || pages != (1u << C::TPK) - 1u;
         // columns that the row sees, and the blocks of 16 that were not read
         const int c_lo = see_lo - tok0, c_hi = see_hi - tok0;
-        auto masked = [&](float v, int col) {
-          return col >= c_lo && col < c_hi && ((pages >> (col / kKvTile)) & 1u) ? v * qa : -INFINITY;
-        };
-        // the maximum, O scaled where it grew; true if a wait gave up
-        auto raise = [&](float mx) -> bool {
-          const float m1 = fmaxf(m_run, mx), keep = exp2_fast(m_run - m1);
-          m_run = m1;
-          l *= keep;
-          if (j == 0) return false;
-          if (!__all_sync(0xffffffffu, mbar_wait_bounded(&pv_done[m], (n_t - 1) & 1, a.wait_ns)))
-            return true;
-          tc::fence_after_sync();
+        auto seen = [&](int col) { return col >= c_lo && col < c_hi && ((pages >> (col / kKvTile)) & 1u); };
+        uint64_t l2 = f32x2(0.0f, 0.0f);
+        const uint64_t qa2 = f32x2(qa, qa);
 #pragma unroll 1
-          for (int ch = 0; ch < C::D / 32; ++ch) {
-            float v[32];
-            tc::tmem_ld32(t_o + ch * 32, v);
+        for (int ch = 0; ch < C::NKV / 32; ++ch) {
+          float v[32];
+          tc::tmem_ld32(t_s + ch * 32, v);
+          if (edge) {
 #pragma unroll
-            for (int x = 0; x < 32; ++x) v[x] *= keep;
-            tc::tmem_st32(t_o + ch * 32, v);
+            for (int x = 0; x < 32; ++x)
+              if (!seen(ch * 32 + x)) v[x] = -INFINITY;
           }
-          return false;
-        };
-        if (edge || j == 0) {
-          // masks, or no maximum yet: the maximum first, then the weights
-          float mx = -INFINITY;
+          float mx = fmaxf(v[0], v[1]);
+#pragma unroll
+          for (int x = 2; x < 32; x += 2) mx = fmaxf(fmaxf(mx, v[x]), v[x + 1]);
+          mx *= qa;
+          if (__any_sync(0xffffffffu, mx > m_run + 8.0f)) {
+            // a new maximum: the sums so far by 2^(old - new), in O after the
+            // product that is under way, and the weights of this tile already
+            // written
+            const float m1 = fmaxf(m_run, mx), keep = exp2_fast(m_run - m1);
+            m_run = m1;
+            l *= keep;
+            l2 = mul_f32x2(l2, f32x2(keep, keep));
+            const __half2 keep2 = __float2half2_rn(keep);
+            tc::tmem_wait_st();
 #pragma unroll 1
-          for (int ch = 0; ch < C::NKV / 32; ++ch) {
-            float v[32];
-            tc::tmem_ld32(t_s + ch * 32, v);
+            for (int x = 0; x < ch; ++x) {
+              float w[16];
+              tc::tmem_ld16(t_s + x * 16, w);
 #pragma unroll
-            for (int x = 0; x < 32; ++x) mx = fmaxf(mx, masked(v[x], ch * 32 + x));
-          }
-          if (__any_sync(0xffffffffu, mx > m_run + 8.0f) && raise(mx)) {
-            ok = false;
-            break;
-          }
-          const float off = 7.0f - m_run;
-#pragma unroll 1
-          for (int ch = 0; ch < C::NKV / 32; ++ch) {
-            float v[32];
-            uint32_t w[16];
-            tc::tmem_ld32(t_s + ch * 32, v);
-#pragma unroll
-            for (int x = 0; x < 32; ++x) v[x] = exp2_fast(masked(v[x], ch * 32 + x) + off);
-#pragma unroll
-            for (int x = 0; x < 16; ++x) {
-              l += v[2 * x] + v[2 * x + 1];
-              w[x] = half2_bits(v[2 * x], v[2 * x + 1]);
+              for (int y = 0; y < 16; ++y) {
+                const __half2 z = __hmul2(*reinterpret_cast<__half2*>(&w[y]), keep2);
+                w[y] = *reinterpret_cast<const float*>(&z);
+              }
+              tc::tmem_st16(t_s + x * 16, reinterpret_cast<const uint32_t*>(w));
             }
-            tc::tmem_st16(t_s + ch * 16, w);  // (over columns read already)
-          }
-        } else {
-          // weights by the maximum so far, kept in registers until the tile is
-          // known not to exceed it by 2^8; else once more by the new one
-          uint32_t w[C::NKV / 2];
-          uint64_t l2;
-          float mx;
-          bool again = false;
-          do {
-            const float off = 7.0f - m_run;
-            const uint64_t qa2 = f32x2(qa, qa), off2 = f32x2(off, off);
-            l2 = f32x2(0.0f, 0.0f);
-            mx = -INFINITY;
+            if (j > 0) {
+              ok = __all_sync(0xffffffffu, mbar_wait_bounded(&pv_done[m], (n_t - 1) & 1, a.wait_ns));
+              if (!ok) break;
+              tc::fence_after_sync();
+#pragma unroll 1
+              for (int x = 0; x < C::D / 16; ++x) {
+                float w[16];
+                tc::tmem_ld16(t_o + x * 16, w);
 #pragma unroll
-            for (int ch = 0; ch < C::NKV / 32; ++ch) {
-              float v[32];
-              tc::tmem_ld32(t_s + ch * 32, v);
-#pragma unroll
-              for (int x = 0; x < 16; ++x) {
-                mx = fmaxf(fmaxf(mx, v[2 * x]), v[2 * x + 1]);
-                float e0, e1;
-                f32x2_split(fma_f32x2(f32x2(v[2 * x], v[2 * x + 1]), qa2, off2), e0, e1);
-                e0 = exp2_fast(e0);
-                e1 = exp2_fast(e1);
-                l2 = add_f32x2(l2, f32x2(e0, e1));
-                w[ch * 16 + x] = half2_bits(e0, e1);
+                for (int y = 0; y < 16; ++y) w[y] *= keep;
+                tc::tmem_st16(t_o + x * 16, reinterpret_cast<const uint32_t*>(w));
               }
             }
-            mx *= qa;
-            again = __any_sync(0xffffffffu, mx > m_run + 8.0f);
-            if (again && raise(mx)) {
-              ok = false;
-              break;
-            }
-          } while (again);
-          if (!ok) break;
-          float l0, l1;
-          f32x2_split(l2, l0, l1);
-          l += l0 + l1;
+          }
+          const float off = 7.0f - m_run;
+          const uint64_t off2 = f32x2(off, off);
+          uint32_t w[16];
 #pragma unroll
-          for (int ch = 0; ch < C::NKV / 32; ++ch) tc::tmem_st16(t_s + ch * 16, w + ch * 16);
+          for (int x = 0; x < 16; ++x) {
+            float e0, e1;
+            f32x2_split(fma_f32x2(f32x2(v[2 * x], v[2 * x + 1]), qa2, off2), e0, e1);
+            e0 = exp2_fast(e0);
+            e1 = exp2_fast(e1);
+            l2 = add_f32x2(l2, f32x2(e0, e1));
+            w[x] = half2_bits(e0, e1);
+          }
+          tc::tmem_st16(t_s + ch * 16, w);  // (over columns read already)
         }
+        if (!ok) break;
+        float l0, l1;
+        f32x2_split(l2, l0, l1);
+        l += l0 + l1;
         tc::tmem_wait_st();
         tc::fence_before_sync();
         __syncwarp();
@@ -730,7 +712,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_prefill_kernel(const AttnAr
           for (int w = 0; w < C::NKV / 32; ++w)
             for (uint32_t bits = info_bad[n % C::INFO][w]; bits; bits &= bits - 1) {
               const int col = w * 32 + __ffs(bits) - 1;
-              if (masked(1.0f, col) != -INFINITY) l = __int_as_float(0x7fffffff);
+              if (seen(col)) l = __int_as_float(0x7fffffff);
             }
         }
       }
