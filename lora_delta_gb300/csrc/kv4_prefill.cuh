@@ -122,10 +122,6 @@ __device__ __forceinline__ uint32_t code_value(uint32_t c, __half2 s, __half2 m)
   const __half2 h = __hfma2(*reinterpret_cast<const __half2*>(&c), s, m);
   return *reinterpret_cast<const uint32_t*>(&h);
 }
-__device__ __forceinline__ bool half_finite(__half x) {
-  return (__half_as_ushort(x) & 0x7c00u) != 0x7c00u;
-}
-
 // Two float32 values worked on by one instruction.
 __device__ __forceinline__ uint64_t f32x2(float lo, float hi) {
   uint64_t r;
@@ -157,6 +153,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_prefill_kernel(const AttnAr
   __shared__ uint64_t raw_full[2], raw_empty[2], kv_full[C::KVB], kv_empty[C::KVB];
   __shared__ uint64_t q_full[2], s_full[2], p_full[2], pv_done[2], size_full[2], size_empty[2], drain_bar;
   __shared__ float size_s[2][C::SOFT_WARPS][C::G];  // of two items: the largest |scale q_g|^2 of a warp's rows
+  __shared__ float size_max_s[C::EXP_WARPS][C::G];  // each expand warp's copy of their largest
   __shared__ uint32_t taddr_s;
   __shared__ uint32_t info_pages[C::INFO];             // blocks of a tile that were copied
   __shared__ uint32_t info_two[C::INFO];               // keys in two operands
@@ -364,18 +361,16 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_prefill_kernel(const AttnAr
       const int pos_lo = it.pos0 + it.r0 / a.group, pos_hi = it.pos0 + (it.r0 + it.rows - 1) / a.group;
       ok = __all_sync(0xffffffffu, mbar_wait_bounded(&size_full[round & 1], (round >> 1) & 1, a.wait_ns));
       if (!ok) break;
-      float size[C::G];
-#pragma unroll
-      for (int q = 0; q < C::G; ++q) {
-        size[q] = 0.0f;
-#pragma unroll
-        for (int w = 0; w < C::SOFT_WARPS; ++w) size[q] = fmaxf(size[q], size_s[round & 1][w][q]);
+      float* size_q = size_max_s[ew];
+      if (lane < C::G) {
+        float x = 0.0f;
+        for (int w = 0; w < C::SOFT_WARPS; ++w) x = fmaxf(x, size_s[round & 1][w][lane]);
+        size_q[lane] = x;
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&size_empty[round & 1]);
       for (int j = 0; j < it.tiles && ok; ++j, ++n) {
         const int st = n & 1, tok0 = it.kv0 + j * C::NKV;
-        const uint8_t* raw = raw_s + st * C::RAW;
         ok = mbar_wait_bounded(&raw_full[st], (n >> 1) & 1, a.wait_ns);
         wait_free();
         if (!ok) break;
@@ -383,31 +378,49 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_prefill_kernel(const AttnAr
         // tiles of which some row does not see some token
         const bool edge = tok0 + C::NKV > it.seq || tok0 + C::NKV > pos_lo + 1 ||
                           (a.window > 0 && tok0 <= pos_hi - a.window) || pages != (1u << C::TPK) - 1u;
+        uint8_t* raw = raw_s + st * C::RAW;
+        if (edge) {
+          // Values' scales of tokens that no row sees may hold anything, and
+          // one that is not finite would reach rows that do not see it: both
+          // are set to 0, the latter noted for the softmax.  (Each warp does it
+          // for what it reads, noting before it clears.)
+          const int tb = C::NKV == 128 ? (ew >> 1) & 1 : 0;
+#pragma unroll 1
+          for (int t = tb * 64 + lane; t < tb * 64 + 64; t += 32) {
+            uint32_t* sp = reinterpret_cast<uint32_t*>(raw + (t / kKvTile) * C::RSTRIDE + C::HALF + 8 * C::D) + (t % kKvTile) * C::G;
+            const bool use = ((pages >> (t / kKvTile)) & 1u) && tok0 + t >= it.lo && tok0 + t < it.hi;
+            bool odd = false;
+#pragma unroll
+            for (int q = 0; q < C::G; ++q)
+              odd |= (sp[q] & 0x7c00u) == 0x7c00u || (sp[q] & 0x7c000000u) == 0x7c000000u;
+            if (use && odd) atomicOr(&info_bad[n % C::INFO][t / 32], 1u << (t % 32));
+            if (!use || odd) {
+#pragma unroll
+              for (int q = 0; q < C::G; ++q) sp[q] = 0;
+            }
+          }
+          fence_proxy_async_smem();  // (the block is next written by a bulk copy)
+          __syncwarp();
+        }
         // The score's error from keys rounded to 11 bits: each dim's is about
         // 2^-12.3 |k|, so its variance is 2^-24.6 sum (scale q)^2 k^2, which is
-        // taken as |scale q_g|^2 times the mean k^2 of each group, of one token
-        // a block; 16 makes it 2^-20.6.  (Each of the warps finds the same.)
+        // taken as |scale q_g|^2 times the mean k^2 of each group, from a word
+        // of 8 dims a lane; 16 makes it 2^-20.6.  (Each of the warps finds the
+        // same.)
         bool two;
         {
           const int c = lane & 3, blk = (lane >> 2) % C::TPK, p = lane / (4 * C::TPK), tt = n & 15;
+          const int w = (lane + n) & (C::WD - 1), gq = p * (C::WD / 2) + w / 2;
           const uint8_t* tile = raw + blk * C::RSTRIDE;
-          float sum = 0.0f;
-#pragma unroll
-          for (int w = 0; w < C::WD; ++w) {
-            const int gq = p * (C::WD / 2) + w / 2;
-            const uint32_t v = *reinterpret_cast<const uint32_t*>(tile + p * 8 * C::W + tt * (C::W / 2) + c * (C::W / 8) + w * 4);
-            const float2 sm = __half22float2(*reinterpret_cast<const __half2*>(tile + 8 * C::D + (tt * C::G + gq) * 4));
-            const uint32_t x = v & 0x0f0f0f0fu, y = (v >> 4) & 0x0f0f0f0fu;
-            const float c2 = (float)__dp4a(x, x, __dp4a(y, y, 0u)), c1 = (float)__dp4a(x, 0x01010101u, __dp4a(y, 0x01010101u, 0u));
-            float sg = size[0];
-#pragma unroll
-            for (int q = 1; q < C::G; ++q) sg = gq == q ? size[q] : sg;
-            sum = fmaf(sg, fmaf(sm.x, fmaf(sm.x, c2, 2.0f * sm.y * c1), 8.0f * sm.y * sm.y), sum);
-          }
+          const uint32_t v = *reinterpret_cast<const uint32_t*>(tile + p * 8 * C::W + tt * (C::W / 2) + c * (C::W / 8) + w * 4);
+          const float2 sm = __half22float2(*reinterpret_cast<const __half2*>(tile + 8 * C::D + (tt * C::G + gq) * 4));
+          const uint32_t x = v & 0x0f0f0f0fu, y = (v >> 4) & 0x0f0f0f0fu;
+          const float c2 = (float)__dp4a(x, x, __dp4a(y, y, 0u)), c1 = (float)__dp4a(x, 0x01010101u, __dp4a(y, 0x01010101u, 0u));
+          float sum = fmaf(sm.x, fmaf(sm.x, c2, 2.0f * sm.y * c1), 8.0f * sm.y * sm.y) * size_q[gq];
           if (!((pages >> blk) & 1u) || tok0 + blk * kKvTile + tt >= it.hi) sum = 0.0f;
 #pragma unroll
           for (int d = 1; d < 32; d <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-          two = sum > 16.0f * 64.0f * C::TPK;
+          two = sum > 16.0f * 8.0f * 32.0f / C::G;  // (the mean over lanes, G groups)
         }
         if (et == 0) info_two[n % C::INFO] = two;
         {
@@ -435,11 +448,6 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_prefill_kernel(const AttnAr
                 const uint4 o = make_uint4(code_value(code_lo(v), s2, m2), code_value(code_hi(v), s2, m2),
                                            code_value(code_lo(v8), s2, m2), code_value(code_hi(v8), s2, m2));
                 *reinterpret_cast<uint4*>(kb + gq * C::NKV * 128 + t * 128 + (((2 * c + x) ^ (t & 7)) << 4)) = o;
-              }
-              if (edge && c == 0) {  // values that are not finite: left out, and noted
-                const __half2 vm = *reinterpret_cast<const __half2*>(tile + C::HALF + 8 * C::D + (tt * C::G + gq) * 4);
-                if (!half_finite(__low2half(vm)) || !half_finite(__high2half(vm)))
-                  atomicOr(&info_bad[n % C::INFO][t / 32], 1u << (t % 32));
               }
             }
           }
@@ -493,15 +501,8 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_prefill_kernel(const AttnAr
               w[c][0] = *reinterpret_cast<const uint32_t*>(vp + c * (C::W / 8));
             __half2 sm[2];
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
+            for (int e = 0; e < 2; ++e)
               sm[e] = *reinterpret_cast<const __half2*>(tile + 8 * C::D + ((8 * h + 2 * c + e) * C::G + gq) * 4);
-              if (edge) {
-                const int t = tb * 64 + tile4 * 16 + 8 * h + 2 * c + e;
-                const bool use = ((pages >> (t / kKvTile)) & 1u) && tok0 + t >= it.lo && tok0 + t < it.hi;
-                if (!use || !half_finite(__low2half(sm[e])) || !half_finite(__high2half(sm[e])))
-                  sm[e] = __float2half2_rn(0.0f);
-              }
-            }
             s2[c] = __lows2half2(sm[0], sm[1]);
             m2[c] = __highs2half2(sm[0], sm[1]);
           }
@@ -554,7 +555,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_prefill_kernel(const AttnAr
                              (it.h * a.group + row - tok * a.group) * C::D;
 #pragma unroll
         for (int q = 0; q < C::G; ++q)
-#pragma unroll 4
+#pragma unroll 2
           for (int k = 0; k < 8; ++k) {
             const uint4 v = ldg_nc_v4(qp + q * 64 + k * 8);
             const uint32_t* w = reinterpret_cast<const uint32_t*>(&v);
@@ -647,10 +648,14 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_prefill_kernel(const AttnAr
             for (int x = 0; x < 32; ++x)
               if (!seen(ch * 32 + x)) v[x] = -INFINITY;
           }
-          float mx = fmaxf(v[0], v[1]);
+          float m4[4];
 #pragma unroll
-          for (int x = 2; x < 32; x += 2) mx = fmaxf(fmaxf(mx, v[x]), v[x + 1]);
-          mx *= qa;
+          for (int y = 0; y < 4; ++y) {
+            m4[y] = fmaxf(v[y], v[4 + y]);
+#pragma unroll
+            for (int x = 8; x < 32; x += 8) m4[y] = fmaxf(fmaxf(m4[y], v[x + y]), v[x + 4 + y]);
+          }
+          const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * qa;
           if (__any_sync(0xffffffffu, mx > m_run + 8.0f)) {
             // a new maximum: the sums so far by 2^(old - new), in O after the
             // product that is under way, and the weights of this tile already
