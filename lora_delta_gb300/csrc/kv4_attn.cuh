@@ -33,7 +33,7 @@ struct AttnArgs {
   const void* q;
   int64_t ld_out, ld_q;
   int n, q_heads, heads, group;  // group = q_heads / heads
-  uint32_t group_inv;            // ceil(2^16 / group): x / group is (x group_inv) >> 16 for x < 32
+  uint32_t group_inv;            // ceil(2^31 / group), for x / group where x group < 2^31
   const uint8_t* pages;
   int64_t num_pages;
   int page_size;
@@ -52,8 +52,10 @@ struct AttnArgs {
   float* partials;     // [kAttnMaxCtas][2] slots, then [kAttnMaxCtas * warps] slots
 };
 
-// Division of a row number below 32 by the group.
-__device__ __forceinline__ int div_group(const AttnArgs& a, int x) { return (int)(((uint32_t)x * a.group_inv) >> 16); }
+// x / group.
+__device__ __forceinline__ int div_group(const AttnArgs& a, int x) {
+  return (int)(((uint64_t)(uint32_t)x * a.group_inv) >> 31);
+}
 
 // The page of a tile of 16 tokens.
 __device__ __forceinline__ int page_of_tile(const AttnArgs& a, int tile) {

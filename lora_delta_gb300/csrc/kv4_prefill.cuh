@@ -38,6 +38,7 @@ struct Pre {
   static constexpr int NKV = D == 256 ? 64 : 128;   // tokens of a tile
   static constexpr int TPK = NKV / kKvTile;
   static constexpr int ROWS = MT * 128;
+  static constexpr int LPR = D / 8, RPL = 32 / LPR;  // lanes a row of q (16 bytes each), rows a load of a warp
   // blocks lie 16 bytes apart modulo 128, so that lanes reading the same place
   // of neighbouring blocks do not meet in a bank
   static constexpr int RSTRIDE = TILE + 16;
@@ -46,17 +47,25 @@ struct Pre {
   static constexpr int KVB = D == 64 ? 6 : 3;       // expanded operands in flight
   static constexpr int Q = ROWS * D * 2;
   static constexpr int INFO = 8;                    // tiles described at once
+  static constexpr int SIZES = 4;                   // items measured at once
   static constexpr int SOFT_WARPS = 4 * MT;
   static constexpr int EXP_WARP = SOFT_WARPS, EXP_WARPS = 8, MMA_WARP = EXP_WARP + EXP_WARPS, LOAD_WARP = MMA_WARP + 1;
   static constexpr int THREADS = (LOAD_WARP + 1) * 32;
+  // Registers a thread: 18 warps start with 96, 1728 by warps.  The expand
+  // warps give 24 each to the softmax warps (8 x 72 + 8 x 120 + 2 x 96 = 1728),
+  // which hold 32 words of weights.  14 warps have 128 each anyway.
+  static constexpr int REGS = MT == 2 ? 96 : 0, SOFT_REGS = 120, EXP_REGS = 72;
+  static_assert(MT != 2 || EXP_WARPS * EXP_REGS + SOFT_WARPS * SOFT_REGS <= (EXP_WARPS + SOFT_WARPS) * REGS,
+                "a split beyond the registers at launch would wait for ever");
   static constexpr size_t smem(int B) {
     return 1024 + (size_t)Q + KVB * KV + 2 * RAW + (size_t)(B + 1) * 4;
   }
 };
 
-// An item: rows [r0, r0 + rows) of the request's (token, head) rows.
+// An item: `rows` of the request's (token, head) rows.
 struct PreItem {
-  int b, h, r0, rows;
+  int b, h, rows;
+  int tok0, rem0;       // the first row's token and place among the heads of its group
   int row0, pos0, seq;  // first row of the batch, its position, visible tokens
   int kv0, lo, hi, tiles;  // first token copied; tokens [lo, hi) are seen by some row
 };
@@ -92,11 +101,13 @@ __device__ __forceinline__ PreItem pre_item(const AttnArgs& a, const int32_t* pr
   const int tokens = a.row_start[lo + 1] - it.row0;
   const int rows = tokens * a.group;
   const int seq = a.seq_len[lo];
-  it.r0 = (rt - pre[lo]) * C::ROWS;
-  it.rows = rows - it.r0 < C::ROWS ? rows - it.r0 : C::ROWS;
+  const int r0 = (rt - pre[lo]) * C::ROWS;
+  it.rows = rows - r0 < C::ROWS ? rows - r0 : C::ROWS;
+  it.tok0 = r0 / a.group;
+  it.rem0 = r0 - it.tok0 * a.group;
   it.pos0 = seq - tokens;
   it.seq = seq < 0 ? 0 : (seq > a.cap ? a.cap : seq);
-  const int pos_lo = it.pos0 + it.r0 / a.group, pos_hi = it.pos0 + (it.r0 + it.rows - 1) / a.group;
+  const int pos_lo = it.pos0 + it.tok0, pos_hi = pos_lo + div_group(a, it.rem0 + it.rows - 1);
   it.lo = a.window > 0 && pos_lo + 1 - a.window > 0 ? pos_lo + 1 - a.window : 0;
   it.hi = pos_hi + 1 < it.seq ? pos_hi + 1 : it.seq;
   it.kv0 = it.lo / kKvTile * kKvTile;
@@ -151,9 +162,9 @@ template <class C>
 __global__ void __launch_bounds__(C::THREADS, 1) kv4_prefill_kernel(const AttnArgs a, int min_rows) {
   extern __shared__ uint8_t pre_smem_raw[];
   __shared__ uint64_t raw_full[2], raw_empty[2], kv_full[C::KVB], kv_empty[C::KVB];
-  __shared__ uint64_t q_full[2], s_full[2], p_full[2], pv_done[2], size_full[2], size_empty[2], drain_bar;
-  __shared__ float size_s[2][C::SOFT_WARPS][C::G];  // of two items: the largest |scale q_g|^2 of a warp's rows
-  __shared__ float size_max_s[C::EXP_WARPS][C::G];  // each expand warp's copy of their largest
+  __shared__ uint64_t q_full[2], s_full[2], p_full[2], pv_done[2], size_full[C::SIZES], size_empty[C::SIZES], drain_bar;
+  __shared__ float size_s[C::SIZES][C::G];         // of some items: the mean |scale q_g|^2 of some rows
+  __shared__ int exp_s[C::SOFT_WARPS][32];         // of q's rows: 2^e <= the largest |q|
   __shared__ uint32_t taddr_s;
   __shared__ uint32_t info_pages[C::INFO];             // blocks of a tile that were copied
   __shared__ uint32_t info_two[C::INFO];               // keys in two operands
@@ -169,13 +180,15 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_prefill_kernel(const AttnAr
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
       mbar_init(&raw_full[i], 1);
-      mbar_init(&size_full[i], C::SOFT_WARPS);
-      mbar_init(&size_empty[i], C::EXP_WARPS);
       mbar_init(&raw_empty[i], C::EXP_WARPS);
       mbar_init(&q_full[i], 4);
       mbar_init(&s_full[i], 1);
       mbar_init(&p_full[i], 4);
       mbar_init(&pv_done[i], 1);
+    }
+    for (int i = 0; i < C::SIZES; ++i) {
+      mbar_init(&size_full[i], 1);
+      mbar_init(&size_empty[i], C::EXP_WARPS);
     }
     for (int i = 0; i < C::KVB; ++i) {
       mbar_init(&kv_full[i], C::EXP_WARPS);
@@ -229,6 +242,37 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_prefill_kernel(const AttnAr
   if (warp == C::LOAD_WARP) {
     // ------------------------------------------------------------------ load
     uint32_t n = 0;  // tiles so far
+    // the size of an item's q, from 4 loads of a lane spread over its rows
+    auto measure = [&](int round) {
+      const int i = pre_nth(round);
+      if (i >= items) return;
+      const PreItem it = pre_item<C>(a, pre, i);
+      if (round >= C::SIZES)
+        ok = __all_sync(0xffffffffu, mbar_wait_bounded(&size_empty[round % C::SIZES], (round / C::SIZES - 1) & 1, a.wait_ns));
+      if (!ok) return;
+      float sq = 0.0f;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int x = it.rem0 + (k * C::RPL + lane / C::LPR) * it.rows / (4 * C::RPL), t = div_group(a, x);
+        const uint4 v = ldg_nc_v4(reinterpret_cast<const uint16_t*>(a.q) + (int64_t)(it.row0 + it.tok0 + t) * a.ld_q +
+                                  (it.h * a.group + x - t * a.group) * C::D + (lane % C::LPR) * 8);
+        const uint32_t* w = reinterpret_cast<const uint32_t*>(&v);
+#pragma unroll
+        for (int y = 0; y < 4; ++y) {
+          const float2 f = unpack2<C::BF16>(w[y]);
+          sq = fmaf(f.x, f.x, fmaf(f.y, f.y, sq));
+        }
+      }
+      // (sums over the lanes of a group of 64 dims, then over the rows)
+#pragma unroll
+      for (int d = 1; d < 8; d <<= 1) sq += __shfl_xor_sync(0xffffffffu, sq, d);
+#pragma unroll
+      for (int d = C::LPR; d < 32; d <<= 1) sq += __shfl_xor_sync(0xffffffffu, sq, d);
+      const float sc = a.scale_log2 * 0.69314718055994531f;
+      if (lane < C::LPR && lane % 8 == 0) size_s[round % C::SIZES][lane / 8] = sq * sc * sc / (4 * C::RPL);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&size_full[round % C::SIZES]);
+    };
     for (int round = 0, i; (i = pre_nth(round)) < items && ok; ++round) {
       const PreItem it = pre_item<C>(a, pre, i);
       const int32_t* table = a.table + (int64_t)it.b * a.ld_table;
@@ -262,6 +306,10 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_prefill_kernel(const AttnAr
           bulk_g2s(raw_s + st * C::RAW + lane * C::RSTRIDE, a.pages + tile * C::TILE, C::TILE,
                    &raw_full[st]);
         }
+        if (j == 0) {  // (behind the first tile's copies; an item ahead)
+          if (round == 0) measure(0);
+          measure(round + 1);
+        }
       }
     }
     // (the copies still in flight write to this CTA's memory)
@@ -274,23 +322,28 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_prefill_kernel(const AttnAr
       // (start addresses are in 16-byte units in a descriptor's low bits, and no
       // sum below carries out of them)
       const uint64_t q_desc = tc::sw128_desc(smem_addr(q_s)), kv_desc = tc::sw128_desc(smem_addr(kv_s));
-      uint32_t k = 0, n = 0;                       // operands and tiles so far
+      uint32_t k = 0, k_ph = 0, n = 0;             // place and parity of the next operand; tiles so far
       uint32_t n_it[2] = {0, 0}, n_t[2] = {0, 0};  // items and tiles of each row half
-      auto wait_kv = [&](uint32_t x) {
-        ok = ok && mbar_wait_bounded(&kv_full[x % C::KVB], (x / C::KVB) & 1, a.wait_ns);
+      auto take = [&]() -> uint32_t {  // waits for the next operand and returns its place
+        ok = ok && mbar_wait_bounded(&kv_full[k], k_ph, a.wait_ns);
         tc::fence_after_sync();
+        const uint32_t x = k;
+        k = k + 1 == C::KVB ? 0 : k + 1;
+        k_ph ^= k == 0;
+        return x;
       };
-      // S of a half from the keys in operand x, and x + 1 where they are two
-      auto qk = [&](int m, uint32_t x, bool two) {
+      // S of a half from the keys in operand x, and y where they are two
+      auto qk = [&](int m, uint32_t x, uint32_t y) {
         const uint64_t qd = q_desc + (uint64_t)(m * 128 * C::D * 2 / 16);
 #pragma unroll 1
-        for (int y = 0; y < (two ? 2 : 1); ++y) {
-          const uint64_t kd = kv_desc + (uint64_t)(((x + y) % C::KVB) * (C::KV / 16));
-          tc::mma_bf16(tmem + m * 128, qd, kd, id_qk, y);
+        for (uint32_t add = 0, z = x;; add = 1, z = y) {
+          const uint64_t kd = kv_desc + (uint64_t)(z * (C::KV / 16));
+          tc::mma_bf16(tmem + m * 128, qd, kd, id_qk, add);
 #pragma unroll
           for (int d = 1; d < C::D / 16; ++d)
             tc::mma_bf16(tmem + m * 128, qd + ((d / 4) * 16384 + (d % 4) * 32) / 16,
                          kd + ((d / 4) * C::NKV * 128 + (d % 4) * 32) / 16, id_qk, 1);
+          if (add || x == y) break;
         }
         issued = true;
         tc::mma_commit(&s_full[m]);
@@ -298,51 +351,50 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_prefill_kernel(const AttnAr
       for (int round = 0, i; (i = pre_nth(round)) < items && ok; ++round) {
         const PreItem it = pre_item<C>(a, pre, i);
         const int mt = it.rows > 128 ? 2 : 1;
-        wait_kv(k);
-        bool two = ok && info_two[n % C::INFO];
-        if (two) wait_kv(k + 1);
-        for (int m = 0; m < mt && ok; ++m) {
-          ok = mbar_wait_bounded(&q_full[m], n_it[m]++ & 1, a.wait_ns);
-          tc::fence_after_sync();
-          if (ok) qk(m, k, two);
-        }
-        if (ok) tc::mma_commit(&kv_empty[k % C::KVB]);
-        if (ok && two) tc::mma_commit(&kv_empty[(k + 1) % C::KVB]);
-        for (int j = 0; j < it.tiles && ok; ++j, ++n) {
-          const uint32_t v = k + 1 + two, kn = v + 1;
+        // step -1: S of the first tile; step j: O of tile j, S of the next
+        for (int j = -1; j < it.tiles && ok; ++j) {
           const bool more = j + 1 < it.tiles;
-          wait_kv(v);
-          const uint64_t vd = kv_desc + (uint64_t)((v % C::KVB) * (C::KV / 16));
+          uint32_t v = 0, x = 0, y = 0;
+          if (j >= 0) v = take();
           for (int m = 0; m < mt && ok; ++m) {
-            ok = mbar_wait_bounded(&p_full[m], n_t[m]++ & 1, a.wait_ns);
-            tc::fence_after_sync();
-            if (!ok) break;
-            tc::mma_f16_ts(tmem + kO + m * 128, tmem + m * 128, vd, id_pv, j > 0);
+            if (j >= 0) {
+              ok = mbar_wait_bounded(&p_full[m], n_t[m]++ & 1, a.wait_ns);
+              tc::fence_after_sync();
+              if (!ok) break;
+              const uint64_t vd = kv_desc + (uint64_t)(v * (C::KV / 16));
+              tc::mma_f16_ts(tmem + kO + m * 128, tmem + m * 128, vd, id_pv, j > 0);
 #pragma unroll
-            for (int t = 1; t < C::NKV / 16; ++t)
-              tc::mma_f16_ts(tmem + kO + m * 128, tmem + m * 128 + t * 8,
-                             vd + ((t / 4) * C::D * 128 + (t % 4) * 32) / 16, id_pv, 1);
-            issued = true;
-            tc::mma_commit(&pv_done[m]);
-            if (m == mt - 1) tc::mma_commit(&kv_empty[v % C::KVB]);
-            if (more) {
-              if (m == 0) {
-                wait_kv(kn);
-                two = ok && info_two[(n + 1) % C::INFO];
-                if (two) wait_kv(kn + 1);
-              }
-              if (ok) qk(m, kn, two);
-              if (m == mt - 1 && ok) tc::mma_commit(&kv_empty[kn % C::KVB]);
-              if (m == mt - 1 && ok && two) tc::mma_commit(&kv_empty[(kn + 1) % C::KVB]);
+              for (int t = 1; t < C::NKV / 16; ++t)
+                tc::mma_f16_ts(tmem + kO + m * 128, tmem + m * 128 + t * 8,
+                               vd + ((t / 4) * C::D * 128 + (t % 4) * 32) / 16, id_pv, 1);
+              issued = true;
+              tc::mma_commit(&pv_done[m]);
+              if (m == mt - 1) tc::mma_commit(&kv_empty[v]);
+            }
+            if (!more) continue;
+            if (m == 0) {
+              x = y = take();
+              if (ok && info_two[(n + (j >= 0)) % C::INFO]) y = take();
+            }
+            if (j < 0) {
+              ok = ok && mbar_wait_bounded(&q_full[m], n_it[m]++ & 1, a.wait_ns);
+              tc::fence_after_sync();
+            }
+            if (!ok) break;
+            qk(m, x, y);
+            if (m == mt - 1) {
+              tc::mma_commit(&kv_empty[x]);
+              if (y != x) tc::mma_commit(&kv_empty[y]);
             }
           }
-          k = kn;
+          n += j >= 0;
         }
       }
     }
     __syncwarp();
   } else if (warp >= C::EXP_WARP) {
     // ---------------------------------------------------------------- expand
+    if constexpr (C::REGS > 0) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::EXP_REGS));
     const int et = tid - C::EXP_WARP * 32, ew = et >> 5;
     uint32_t n = 0, k = 0;  // tiles and operands so far
     auto wait_free = [&]() {
@@ -358,17 +410,9 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_prefill_kernel(const AttnAr
     };
     for (int round = 0, i; (i = pre_nth(round)) < items && ok; ++round) {
       const PreItem it = pre_item<C>(a, pre, i);
-      const int pos_lo = it.pos0 + it.r0 / a.group, pos_hi = it.pos0 + (it.r0 + it.rows - 1) / a.group;
-      ok = __all_sync(0xffffffffu, mbar_wait_bounded(&size_full[round & 1], (round >> 1) & 1, a.wait_ns));
+      const int pos_lo = it.pos0 + it.tok0, pos_hi = pos_lo + div_group(a, it.rem0 + it.rows - 1);
+      ok = __all_sync(0xffffffffu, mbar_wait_bounded(&size_full[round % C::SIZES], (round / C::SIZES) & 1, a.wait_ns));
       if (!ok) break;
-      float* size_q = size_max_s[ew];
-      if (lane < C::G) {
-        float x = 0.0f;
-        for (int w = 0; w < C::SOFT_WARPS; ++w) x = fmaxf(x, size_s[round & 1][w][lane]);
-        size_q[lane] = x;
-      }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&size_empty[round & 1]);
       for (int j = 0; j < it.tiles && ok; ++j, ++n) {
         const int st = n & 1, tok0 = it.kv0 + j * C::NKV;
         ok = mbar_wait_bounded(&raw_full[st], (n >> 1) & 1, a.wait_ns);
@@ -404,9 +448,9 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_prefill_kernel(const AttnAr
         }
         // The score's error from keys rounded to 11 bits: each dim's is about
         // 2^-12.3 |k|, so its variance is 2^-24.6 sum (scale q)^2 k^2, which is
-        // taken as |scale q_g|^2 times the mean k^2 of each group, from a word
-        // of 8 dims a lane; 16 makes it 2^-20.6.  (Each of the warps finds the
-        // same.)
+        // taken as |scale q_g|^2 (of some rows) times the mean k^2 of each group,
+        // from a word of 8 dims a lane; 12 makes it 2^-21.  (Each of the warps
+        // finds the same.)
         bool two;
         {
           const int c = lane & 3, blk = (lane >> 2) % C::TPK, p = lane / (4 * C::TPK), tt = n & 15;
@@ -416,11 +460,11 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_prefill_kernel(const AttnAr
           const float2 sm = __half22float2(*reinterpret_cast<const __half2*>(tile + 8 * C::D + (tt * C::G + gq) * 4));
           const uint32_t x = v & 0x0f0f0f0fu, y = (v >> 4) & 0x0f0f0f0fu;
           const float c2 = (float)__dp4a(x, x, __dp4a(y, y, 0u)), c1 = (float)__dp4a(x, 0x01010101u, __dp4a(y, 0x01010101u, 0u));
-          float sum = fmaf(sm.x, fmaf(sm.x, c2, 2.0f * sm.y * c1), 8.0f * sm.y * sm.y) * size_q[gq];
+          float sum = fmaf(sm.x, fmaf(sm.x, c2, 2.0f * sm.y * c1), 8.0f * sm.y * sm.y) * size_s[round % C::SIZES][gq];
           if (!((pages >> blk) & 1u) || tok0 + blk * kKvTile + tt >= it.hi) sum = 0.0f;
 #pragma unroll
           for (int d = 1; d < 32; d <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-          two = sum > 16.0f * 8.0f * 32.0f / C::G;  // (the mean over lanes, G groups)
+          two = sum > 12.0f * 8.0f * 32.0f / C::G;  // (the mean over lanes, G groups)
         }
         if (et == 0) info_two[n % C::INFO] = two;
         {
@@ -527,104 +571,81 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_prefill_kernel(const AttnAr
           if (lane == 0) mbar_arrive(&raw_empty[st]);
         }
       }
+      if (lane == 0) mbar_arrive(&size_empty[round % C::SIZES]);
     }
   } else {
     // --------------------------------------------------------------- softmax
+    if constexpr (C::REGS > 0) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::SOFT_REGS));
     const int m = warp >> 2, wl = warp & 3, r_l = wl * 32 + lane;
     const uint32_t t_s = tmem + m * 128 + ((uint32_t)(wl * 32) << 16);
     const uint32_t t_o = tmem + kO + m * 128 + ((uint32_t)(wl * 32) << 16);
     uint32_t n = 0, n_t = 0;  // tiles of all items; tiles of this half
     // (a scale of 0 goes with q too, so that masked scores times qa stay -inf)
     const float sign = a.scale_log2 < 0.0f ? -1.0f : a.scale_log2 > 0.0f ? 1.0f : 0.0f;
-    // an item's rows ahead of their turn: the row's largest |q|, returned, and
-    // for the expand warps the largest |scale q_g|^2
-    auto measure = [&](int round) -> float {
-      float top = 0.0f, sq[C::G];
-#pragma unroll
-      for (int q = 0; q < C::G; ++q) sq[q] = 0.0f;
-      const int i = pre_nth(round);
-      if (i >= items) return top;
-      if (round >= 2) {
-        ok = __all_sync(0xffffffffu, mbar_wait_bounded(&size_empty[round & 1], ((round >> 1) - 1) & 1, a.wait_ns));
-        if (!ok) return top;
-      }
-      const PreItem it = pre_item<C>(a, pre, i);
-      const int row = it.r0 + m * 128 + r_l, tok = row / a.group;
-      if (m * 128 + r_l < it.rows) {
-        const uint16_t* qp = reinterpret_cast<const uint16_t*>(a.q) + (int64_t)(it.row0 + tok) * a.ld_q +
-                             (it.h * a.group + row - tok * a.group) * C::D;
-#pragma unroll
-        for (int q = 0; q < C::G; ++q)
-#pragma unroll 2
-          for (int k = 0; k < 8; ++k) {
-            const uint4 v = ldg_nc_v4(qp + q * 64 + k * 8);
-            const uint32_t* w = reinterpret_cast<const uint32_t*>(&v);
-#pragma unroll
-            for (int x = 0; x < 4; ++x) {
-              const float2 f = unpack2<C::BF16>(w[x]);
-              top = fmaxf(top, fmaxf(fabsf(f.x), fabsf(f.y)));
-              sq[q] = fmaf(f.x, f.x, fmaf(f.y, f.y, sq[q]));
-            }
-          }
-      }
-      const float sc = a.scale_log2 * 0.69314718055994531f;
-#pragma unroll
-      for (int q = 0; q < C::G; ++q) {
-        float x = sq[q] * sc * sc;
-#pragma unroll
-        for (int d = 1; d < 32; d <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, d));
-        if (lane == 0) size_s[round & 1][warp][q] = x;
-      }
-      if (lane == 0) mbar_arrive(&size_full[round & 1]);
-      return top;
+    uint8_t* q_half = q_s + m * 128 * C::D * 2;
+    // the place of 16 bytes of a row of q, and of out on its way to memory
+    auto q_place = [&](int row, int chunk) {
+      return reinterpret_cast<uint4*>(q_half + (chunk / 8) * 16384 + row * 128 + (((chunk % 8) ^ (row & 7)) << 4));
     };
-    float top_next = measure(0);
     for (int round = 0, i; (i = pre_nth(round)) < items && ok; ++round) {
       const PreItem it = pre_item<C>(a, pre, i);
-      const float top = top_next;
       if (m * 128 >= it.rows) {  // this half sits the item out
-        top_next = measure(round + 1);
         n += it.tiles;
         continue;
       }
       const bool live = m * 128 + r_l < it.rows;
-      const int row = it.r0 + m * 128 + r_l, tok = row / a.group;
-      const int head = it.h * a.group + row - tok * a.group;
-      // q of the row (earlier products with this half's q are done)
-      const uint16_t* qp = reinterpret_cast<const uint16_t*>(a.q) + (int64_t)(it.row0 + tok) * a.ld_q + head * C::D;
-      int e = (int)((__float_as_uint(top) >> 23) & 255u) - 127;
-      e = e < -100 ? -100 : e;
-      const float up = pow2i(14 - e) * sign;
-      const float qa = sign == 0.0f ? 1.0f : fabsf(a.scale_log2) * pow2i(e) * (1.0f / 16384.0f);
-#pragma unroll 4
-      for (int k = 0; k < C::D / 8; ++k) {
-        const uint4 v = live ? ldg_nc_v4(qp + k * 8) : make_uint4(0, 0, 0, 0);
-        const uint32_t* w = reinterpret_cast<const uint32_t*>(&v);
-        float f[8];
+      const int in_item = it.rem0 + m * 128 + r_l, tok = div_group(a, in_item);  // (tokens from tok0)
+      const int head = it.h * a.group + in_item - tok * a.group;
+      // q of the warp's rows, 16 bytes a lane (earlier products with this
+      // half's q are done), a batch of loads at once
+      const int chunk = lane % C::LPR;
+      constexpr int kBatch = 8;
+#pragma unroll 1
+      for (int y0 = 0; y0 < 32 / C::RPL; y0 += kBatch) {
+        uint4 raw[kBatch];
 #pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          const float2 y = unpack2<C::BF16>(w[x]);
-          f[2 * x] = y.x * up;
-          f[2 * x + 1] = y.y * up;
+        for (int y = 0; y < kBatch; ++y) {
+          const int row = m * 128 + wl * 32 + (y0 + y) * C::RPL + lane / C::LPR;
+          const int x = it.rem0 + row, t = div_group(a, x);
+          raw[y] = row < it.rows ? ldg_nc_v4(reinterpret_cast<const uint16_t*>(a.q) + (int64_t)(it.row0 + it.tok0 + t) * a.ld_q +
+                                             (it.h * a.group + x - t * a.group) * C::D + chunk * 8)
+                                 : make_uint4(0, 0, 0, 0);
         }
-        *reinterpret_cast<uint4*>(q_s + m * 128 * C::D * 2 + (k / 8) * 16384 + r_l * 128 +
-                                  (((k % 8) ^ (r_l & 7)) << 4)) =
-            make_uint4(half2_bits(f[0], f[4]), half2_bits(f[1], f[5]), half2_bits(f[2], f[6]),
-                       half2_bits(f[3], f[7]));
+#pragma unroll
+        for (int y = 0; y < kBatch; ++y) {
+          const uint32_t* w = reinterpret_cast<const uint32_t*>(&raw[y]);
+          float f[8], top = 0.0f;
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            const float2 z = unpack2<C::BF16>(w[x]);
+            f[2 * x] = z.x;
+            f[2 * x + 1] = z.y;
+            top = fmaxf(top, fmaxf(fabsf(z.x), fabsf(z.y)));
+          }
+#pragma unroll
+          for (int d = 1; d < C::LPR; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+          int e = (int)((__float_as_uint(top) >> 23) & 255u) - 127;
+          e = e < -100 ? -100 : e;
+          const float up = pow2i(14 - e) * sign;
+          const int row = (y0 + y) * C::RPL + lane / C::LPR;
+          if (chunk == 0) exp_s[warp][row] = e;
+          // (dims 0 4 1 5 2 6 3 7, as the keys lie)
+          *q_place(wl * 32 + row, chunk) = make_uint4(half2_bits(f[0] * up, f[4] * up), half2_bits(f[1] * up, f[5] * up),
+                                                      half2_bits(f[2] * up, f[6] * up), half2_bits(f[3] * up, f[7] * up));
+        }
       }
       fence_proxy_async_smem();
       tc::fence_before_sync();
       __syncwarp();
       if (lane == 0) mbar_arrive(&q_full[m]);
-      top_next = measure(round + 1);
-      if (!ok) break;
+      const float qa = sign == 0.0f ? 1.0f : fabsf(a.scale_log2) * pow2i(exp_s[warp][lane]) * (1.0f / 16384.0f);
 
-      const int pos = it.pos0 + tok;
+      const int pos = it.pos0 + it.tok0 + tok;
       const int see_hi = live ? (pos + 1 < it.seq ? pos + 1 : it.seq) : -1;
       const int see_lo = a.window > 0 ? pos + 1 - a.window : 0;
       const int last = it.rows < m * 128 + 128 ? it.rows : m * 128 + 128;
-      const int pos_lo = it.pos0 + (it.r0 + m * 128) / a.group;
-      const int pos_hi = it.pos0 + (it.r0 + last - 1) / a.group;
+      const int pos_lo = it.pos0 + it.tok0 + div_group(a, it.rem0 + m * 128);
+      const int pos_hi = it.pos0 + it.tok0 + div_group(a, it.rem0 + last - 1);
       float m_run = kNoMax, l = 0.0f;
       for (int j = 0; j < it.tiles; ++j, ++n, ++n_t) {
         ok = __all_sync(0xffffffffu, mbar_wait_bounded(&s_full[m], n_t & 1, a.wait_ns));
@@ -637,45 +658,58 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_prefill_kernel(const AttnAr
         // columns that the row sees, and the blocks of 16 that were not read
         const int c_lo = see_lo - tok0, c_hi = see_hi - tok0;
         auto seen = [&](int col) { return col >= c_lo && col < c_hi && ((pages >> (col / kKvTile)) & 1u); };
-        uint64_t l2 = f32x2(0.0f, 0.0f);
+        // 64 columns at a time: weights by the maximum so far, kept in
+        // registers until no score is known to exceed it by 2^8, else once
+        // more by a new maximum
         const uint64_t qa2 = f32x2(qa, qa);
 #pragma unroll 1
-        for (int ch = 0; ch < C::NKV / 32; ++ch) {
-          float v[32];
-          tc::tmem_ld32(t_s + ch * 32, v);
-          if (edge) {
+        for (int part = 0; part < C::NKV / 64; ++part) {
+          uint32_t w[32];
+          uint64_t l2;
+          for (;;) {
+            const float off = 7.0f - m_run;
+            const uint64_t off2 = f32x2(off, off);
+            float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+            l2 = f32x2(0.0f, 0.0f);
 #pragma unroll
-            for (int x = 0; x < 32; ++x)
-              if (!seen(ch * 32 + x)) v[x] = -INFINITY;
-          }
-          float m4[4];
+            for (int ch = 0; ch < 2; ++ch) {
+              float v[32];
+              tc::tmem_ld32(t_s + part * 64 + ch * 32, v);
+              if (edge) {
 #pragma unroll
-          for (int y = 0; y < 4; ++y) {
-            m4[y] = fmaxf(v[y], v[4 + y]);
+                for (int x = 0; x < 32; ++x)
+                  if (!seen(part * 64 + ch * 32 + x)) v[x] = -INFINITY;
+              }
 #pragma unroll
-            for (int x = 8; x < 32; x += 8) m4[y] = fmaxf(fmaxf(m4[y], v[x + y]), v[x + 4 + y]);
-          }
-          const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * qa;
-          if (__any_sync(0xffffffffu, mx > m_run + 8.0f)) {
-            // a new maximum: the sums so far by 2^(old - new), in O after the
-            // product that is under way, and the weights of this tile already
-            // written
+              for (int x = 0; x < 16; ++x) {
+                float e0, e1;
+                f32x2_split(fma_f32x2(f32x2(v[2 * x], v[2 * x + 1]), qa2, off2), e0, e1);
+                m4[x % 4] = fmaxf(fmaxf(m4[x % 4], v[2 * x]), v[2 * x + 1]);
+                e0 = exp2_fast(e0);
+                e1 = exp2_fast(e1);
+                l2 = add_f32x2(l2, f32x2(e0, e1));
+                w[ch * 16 + x] = half2_bits(e0, e1);
+              }
+            }
+            const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * qa;
+            if (!__any_sync(0xffffffffu, mx > m_run + 8.0f)) break;
+            // the sums so far by 2^(old - new), in O after the product that is
+            // under way, and the weights of this tile already written
             const float m1 = fmaxf(m_run, mx), keep = exp2_fast(m_run - m1);
             m_run = m1;
             l *= keep;
-            l2 = mul_f32x2(l2, f32x2(keep, keep));
             const __half2 keep2 = __float2half2_rn(keep);
             tc::tmem_wait_st();
 #pragma unroll 1
-            for (int x = 0; x < ch; ++x) {
-              float w[16];
-              tc::tmem_ld16(t_s + x * 16, w);
+            for (int x = 0; x < 2 * part; ++x) {
+              float z[16];
+              tc::tmem_ld16(t_s + x * 16, z);
 #pragma unroll
               for (int y = 0; y < 16; ++y) {
-                const __half2 z = __hmul2(*reinterpret_cast<__half2*>(&w[y]), keep2);
-                w[y] = *reinterpret_cast<const float*>(&z);
+                const __half2 t = __hmul2(*reinterpret_cast<__half2*>(&z[y]), keep2);
+                z[y] = *reinterpret_cast<const float*>(&t);
               }
-              tc::tmem_st16(t_s + x * 16, reinterpret_cast<const uint32_t*>(w));
+              tc::tmem_st16(t_s + x * 16, reinterpret_cast<const uint32_t*>(z));
             }
             if (j > 0) {
               ok = __all_sync(0xffffffffu, mbar_wait_bounded(&pv_done[m], (n_t - 1) & 1, a.wait_ns));
@@ -683,32 +717,22 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_prefill_kernel(const AttnAr
               tc::fence_after_sync();
 #pragma unroll 1
               for (int x = 0; x < C::D / 16; ++x) {
-                float w[16];
-                tc::tmem_ld16(t_o + x * 16, w);
+                float z[16];
+                tc::tmem_ld16(t_o + x * 16, z);
 #pragma unroll
-                for (int y = 0; y < 16; ++y) w[y] *= keep;
-                tc::tmem_st16(t_o + x * 16, reinterpret_cast<const uint32_t*>(w));
+                for (int y = 0; y < 16; ++y) z[y] *= keep;
+                tc::tmem_st16(t_o + x * 16, reinterpret_cast<const uint32_t*>(z));
               }
             }
           }
-          const float off = 7.0f - m_run;
-          const uint64_t off2 = f32x2(off, off);
-          uint32_t w[16];
-#pragma unroll
-          for (int x = 0; x < 16; ++x) {
-            float e0, e1;
-            f32x2_split(fma_f32x2(f32x2(v[2 * x], v[2 * x + 1]), qa2, off2), e0, e1);
-            e0 = exp2_fast(e0);
-            e1 = exp2_fast(e1);
-            l2 = add_f32x2(l2, f32x2(e0, e1));
-            w[x] = half2_bits(e0, e1);
-          }
-          tc::tmem_st16(t_s + ch * 16, w);  // (over columns read already)
+          if (!ok) break;
+          float l0, l1;
+          f32x2_split(l2, l0, l1);
+          l += l0 + l1;
+          tc::tmem_st16(t_s + part * 32, w);  // (over columns read already)
+          tc::tmem_st16(t_s + part * 32 + 16, w + 16);
         }
         if (!ok) break;
-        float l0, l1;
-        f32x2_split(l2, l0, l1);
-        l += l0 + l1;
         tc::tmem_wait_st();
         tc::fence_before_sync();
         __syncwarp();
@@ -726,25 +750,34 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_prefill_kernel(const AttnAr
       if (!ok) break;
       tc::fence_after_sync();
       const float inv = l != 0.0f ? 1.0f / l : 0.0f;
-      uint16_t* out = reinterpret_cast<uint16_t*>(a.out) + (int64_t)(it.row0 + tok) * a.ld_out + head * C::D;
+      // the warp's rows through the place of its rows of q, so that a row's
+      // bytes are stored by neighbouring lanes
 #pragma unroll 1
       for (int ch = 0; ch < C::D / 32; ++ch) {
         float v[32];
         tc::tmem_ld32(t_o + ch * 32, v);
-        if (live) {
 #pragma unroll
-          for (int x = 0; x < 4; ++x)
-            *reinterpret_cast<uint4*>(out + ch * 32 + x * 8) =
-                make_uint4(pack2<C::BF16>(v[8 * x] * inv, v[8 * x + 1] * inv),
-                           pack2<C::BF16>(v[8 * x + 2] * inv, v[8 * x + 3] * inv),
-                           pack2<C::BF16>(v[8 * x + 4] * inv, v[8 * x + 5] * inv),
-                           pack2<C::BF16>(v[8 * x + 6] * inv, v[8 * x + 7] * inv));
-        }
+        for (int x = 0; x < 4; ++x)
+          *q_place(r_l, ch * 4 + x) =
+              make_uint4(pack2<C::BF16>(v[8 * x] * inv, v[8 * x + 1] * inv),
+                         pack2<C::BF16>(v[8 * x + 2] * inv, v[8 * x + 3] * inv),
+                         pack2<C::BF16>(v[8 * x + 4] * inv, v[8 * x + 5] * inv),
+                         pack2<C::BF16>(v[8 * x + 6] * inv, v[8 * x + 7] * inv));
+      }
+      tc::fence_before_sync();
+      __syncwarp();
+#pragma unroll 4
+      for (int y = 0; y < 32 / C::RPL; ++y) {
+        const int row = wl * 32 + y * C::RPL + lane / C::LPR;
+        const int x = it.rem0 + m * 128 + row, t = div_group(a, x);
+        if (m * 128 + row < it.rows)
+          *reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(a.out) + (int64_t)(it.row0 + it.tok0 + t) * a.ld_out +
+                                    (it.h * a.group + x - t * a.group) * C::D + chunk * 8) = *q_place(row, chunk);
       }
       if (live && a.lse)
-        a.lse[(int64_t)(it.row0 + tok) * a.q_heads + head] =
+        a.lse[(int64_t)(it.row0 + it.tok0 + tok) * a.q_heads + head] =
             l != 0.0f ? (m_run + log2f(l) - 7.0f) * 0.69314718055994531f : -INFINITY;
-      tc::fence_before_sync();
+      __syncwarp();  // (before the next item's q goes there)
     }
   }
   if (!ok) set_error(a.err, LORA_DEV_ERR_TIMEOUT);

@@ -129,6 +129,13 @@ template <class C>
 int launch_prefill(const AttnArgs& a, int min_rows, cudaStream_t stream) {
   const int smem = (int)C::smem(a.B);
   if (prepare_kernel(kv4_prefill_kernel<C>, smem, false) != cudaSuccess) return LORA_ERR_CUDA;
+  // (the kernel hands registers from warp to warp, out of those that it was
+  // built to start with)
+  static const bool regs_ok = [] {
+    cudaFuncAttributes fa;
+    return cudaFuncGetAttributes(&fa, kv4_prefill_kernel<C>) == cudaSuccess && fa.numRegs >= C::REGS;
+  }();
+  if (!regs_ok) return LORA_ERR_CUDA;
   kv4_prefill_kernel<C><<<sm_count(), C::THREADS, smem, stream>>>(a, min_rows);
   return cuda_status(cudaGetLastError());
 }
@@ -263,7 +270,7 @@ int lora_kv4_attention(void* out, int64_t ld_out, const void* q, int64_t ld_q, i
   a.q_heads = q_heads;
   a.heads = kv_heads;
   a.group = q_heads / kv_heads;
-  a.group_inv = (uint32_t)((65536 + a.group - 1) / a.group);
+  a.group_inv = (uint32_t)(((1ull << 31) + a.group - 1) / a.group);
   a.pages = reinterpret_cast<const uint8_t*>(pages);
   a.num_pages = num_pages;
   a.page_size = page_size;
