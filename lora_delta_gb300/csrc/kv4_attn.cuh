@@ -28,6 +28,24 @@ namespace lora {
 
 constexpr int kAttnMaxReqs = 4096;
 
+// mbar_wait_bounded for waits that are short and frequent: the global timer,
+// whose reading takes about a microsecond on GB300, is first asked after 64
+// polls (reading it at the first poll that fails cost the prefill kernel a
+// third of its time).
+__device__ __forceinline__ bool mbar_wait_soon(uint64_t* bar, uint32_t parity, uint64_t limit_ns) {
+  if (mbar_try_wait(bar, parity)) return true;
+  if (limit_ns == 0) return false;
+  uint64_t t0 = 0;
+  for (uint32_t it = 1;; ++it) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if ((it & 63u) == 0) {
+      const uint64_t t = globaltimer_ns();
+      if (t0 == 0) t0 = t;
+      else if (t - t0 > limit_ns) return false;
+    }
+  }
+}
+
 struct AttnArgs {
   void* out;
   const void* q;
@@ -865,13 +883,13 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_decode_kernel(const AttnArg
         const uint32_t got = (have >> (2 * stage)) & 3u;
         if (got) {
           if (!__all_sync(0xffffffffu,
-                          mbar_wait_bounded(&bars[warp][stage], (phase >> stage) & 1u, a.wait_ns))) {
+                          mbar_wait_soon(&bars[warp][stage], (phase >> stage) & 1u, a.wait_ns))) {
             // given up: the copies in flight still write to this CTA's memory,
             // so they are waited for; the rest of the part is not read
             if (lane == 0) {
               set_error(a.err, LORA_DEV_ERR_TIMEOUT);
               for (int x = 0; x < stages; ++x)
-                if ((have >> (2 * x)) & 3u) mbar_wait_bounded(&bars[warp][x], (phase >> x) & 1u, kWaitLimitNs);
+                if ((have >> (2 * x)) & 3u) mbar_wait_soon(&bars[warp][x], (phase >> x) & 1u, kWaitLimitNs);
             }
             __syncwarp();
             have = 0;

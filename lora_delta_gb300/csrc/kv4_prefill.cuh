@@ -7,8 +7,10 @@
 //   load warp       bulk copies of the tile's packed 16-token blocks
 //   8 expand warps  codes to f16 values s c + m in the operands' 128-byte
 //                   swizzled layout, keys [token][dim], values [dim][token]
-//   MMA warp        S = Q K^T (128 x 128 a row half, in tensor memory), then
-//                   O += P V with P read from tensor memory
+//   an MMA warp     a row half: S = Q K^T (128 x 128, in tensor memory), then
+//                   O += P V with P read from tensor memory.  A warp each,
+//                   since the tensor cores idle while an issuing thread waits
+//                   or commits (one thread for both halves: 1.3 times the time)
 //   4 softmax warps a row half: a thread a row; scores to weights in place of
 //                   S, running maximum (followed lazily: O is scaled only when
 //                   a row's maximum grew by 2^8), denominator, the final O / l
@@ -48,12 +50,14 @@ struct Pre {
   static constexpr int Q = ROWS * D * 2;
   static constexpr int INFO = 8;                    // tiles described at once
   static constexpr int SIZES = 4;                   // items measured at once
-  static constexpr int SOFT_WARPS = 4 * MT;
-  static constexpr int EXP_WARP = SOFT_WARPS, EXP_WARPS = 8, MMA_WARP = EXP_WARP + EXP_WARPS, LOAD_WARP = MMA_WARP + 1;
-  static constexpr int THREADS = (LOAD_WARP + 1) * 32;
-  // Registers a thread: 18 warps start with 96, 1728 by warps.  The expand
-  // warps give 24 each to the softmax warps (8 x 72 + 8 x 120 + 2 x 96 = 1728),
-  // which hold 32 words of weights.  14 warps have 128 each anyway.
+  // Warps: MMA 0 (and 1), load 2, then softmax and expand; the first are waited
+  // for most and come first where a scheduler has a choice.
+  static constexpr int SOFT_WARPS = 4 * MT, EXP_WARPS = 8;
+  static constexpr int MMA_WARP = 0, LOAD_WARP = 2, SOFT_WARP = 4, EXP_WARP = SOFT_WARP + SOFT_WARPS;
+  static constexpr int THREADS = (EXP_WARP + EXP_WARPS) * 32;
+  // Registers a thread: 20 warps start with 96.  The expand warps give 24 each
+  // to the softmax warps (8 x 72 + 8 x 120 = 16 x 96), which hold 32 words of
+  // weights.  16 warps have 128 each anyway.
   static constexpr int REGS = MT == 2 ? 96 : 0, SOFT_REGS = 120, EXP_REGS = 72;
   static_assert(MT != 2 || EXP_WARPS * EXP_REGS + SOFT_WARPS * SOFT_REGS <= (EXP_WARPS + SOFT_WARPS) * REGS,
                 "a split beyond the registers at launch would wait for ever");
@@ -162,7 +166,7 @@ template <class C>
 __global__ void __launch_bounds__(C::THREADS, 1) kv4_prefill_kernel(const AttnArgs a, int min_rows) {
   extern __shared__ uint8_t pre_smem_raw[];
   __shared__ uint64_t raw_full[2], raw_empty[2], kv_full[C::KVB], kv_empty[C::KVB];
-  __shared__ uint64_t q_full[2], s_full[2], p_full[2], pv_done[2], size_full[C::SIZES], size_empty[C::SIZES], drain_bar;
+  __shared__ uint64_t q_full[2], s_full[2], p_full[2], pv_done[2], size_full[C::SIZES], size_empty[C::SIZES], turn[2], drain_bar[2];
   __shared__ float size_s[C::SIZES][C::G];         // of some items: the mean |scale q_g|^2 of some rows
   __shared__ int exp_s[C::SOFT_WARPS][32];         // of q's rows: 2^e <= the largest |q|
   __shared__ uint32_t taddr_s;
@@ -170,7 +174,8 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_prefill_kernel(const AttnAr
   __shared__ uint32_t info_two[C::INFO];               // keys in two operands
   __shared__ uint32_t info_bad[C::INFO][C::NKV / 32];  // tokens whose values are not finite
   __shared__ int scan_s[32];
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);  // (known to be the same in a warp)
   uint8_t* smem = pre_smem_raw + ((1024 - (smem_addr(pre_smem_raw) & 1023)) & 1023);
   uint8_t* q_s = smem;
   uint8_t* kv_s = smem + C::Q;
@@ -185,6 +190,8 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_prefill_kernel(const AttnAr
       mbar_init(&s_full[i], 1);
       mbar_init(&p_full[i], 4);
       mbar_init(&pv_done[i], 1);
+      mbar_init(&turn[i], 1);
+      mbar_init(&drain_bar[i], 1);
     }
     for (int i = 0; i < C::SIZES; ++i) {
       mbar_init(&size_full[i], 1);
@@ -192,9 +199,8 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_prefill_kernel(const AttnAr
     }
     for (int i = 0; i < C::KVB; ++i) {
       mbar_init(&kv_full[i], C::EXP_WARPS);
-      mbar_init(&kv_empty[i], 1);
+      mbar_init(&kv_empty[i], C::MT);
     }
-    mbar_init(&drain_bar, 1);
     fence_barrier_init();
   }
   // row tiles of the requests, summed
@@ -237,7 +243,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_prefill_kernel(const AttnAr
   const int items = pre[a.B] * a.heads;
   constexpr uint32_t kO = 256;  // first tensor-memory column of the sums
   bool ok = true;
-  bool issued = false;
+  bool issued = false;  // (by an MMA warp)
 
   if (warp == C::LOAD_WARP) {
     // ------------------------------------------------------------------ load
@@ -248,7 +254,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_prefill_kernel(const AttnAr
       if (i >= items) return;
       const PreItem it = pre_item<C>(a, pre, i);
       if (round >= C::SIZES)
-        ok = __all_sync(0xffffffffu, mbar_wait_bounded(&size_empty[round % C::SIZES], (round / C::SIZES - 1) & 1, a.wait_ns));
+        ok = __all_sync(0xffffffffu, mbar_wait_soon(&size_empty[round % C::SIZES], (round / C::SIZES - 1) & 1, a.wait_ns));
       if (!ok) return;
       float sq = 0.0f;
 #pragma unroll
@@ -287,7 +293,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_prefill_kernel(const AttnAr
             page = -1;
           }
         }
-        if (n >= 2) ok = mbar_wait_bounded(&raw_empty[st], ((n >> 1) - 1) & 1, a.wait_ns);
+        if (n >= 2) ok = mbar_wait_soon(&raw_empty[st], ((n >> 1) - 1) & 1, a.wait_ns);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         const uint32_t got = __ballot_sync(0xffffffffu, page >= 0);
@@ -314,84 +320,102 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_prefill_kernel(const AttnAr
     }
     // (the copies still in flight write to this CTA's memory)
     for (uint32_t k = n >= 2 ? n - 2 : 0; k < n; ++k)
-      if (!mbar_wait_bounded(&raw_full[k & 1], (k >> 1) & 1, kWaitLimitNs)) ok = false;
-  } else if (warp == C::MMA_WARP) {
+      if (!mbar_wait_soon(&raw_full[k & 1], (k >> 1) & 1, kWaitLimitNs)) ok = false;
+  } else if (warp < C::MMA_WARP + C::MT) {
     // ------------------------------------------------------------------- MMA
-    if (lane == 0) {
-      const uint32_t id_qk = tc::idesc_f16_f32(128, C::NKV), id_pv = tc::idesc_f16_f32(128, C::D);
-      // (start addresses are in 16-byte units in a descriptor's low bits, and no
-      // sum below carries out of them)
-      const uint64_t q_desc = tc::sw128_desc(smem_addr(q_s)), kv_desc = tc::sw128_desc(smem_addr(kv_s));
-      uint32_t k = 0, k_ph = 0, n = 0;             // place and parity of the next operand; tiles so far
-      uint32_t n_it[2] = {0, 0}, n_t[2] = {0, 0};  // items and tiles of each row half
-      auto take = [&]() -> uint32_t {  // waits for the next operand and returns its place
-        ok = ok && mbar_wait_bounded(&kv_full[k], k_ph, a.wait_ns);
-        tc::fence_after_sync();
-        const uint32_t x = k;
-        k = k + 1 == C::KVB ? 0 : k + 1;
-        k_ph ^= k == 0;
-        return x;
-      };
-      // S of a half from the keys in operand x, and y where they are two
-      auto qk = [&](int m, uint32_t x, uint32_t y) {
-        const uint64_t qd = q_desc + (uint64_t)(m * 128 * C::D * 2 / 16);
-#pragma unroll 1
-        for (uint32_t add = 0, z = x;; add = 1, z = y) {
-          const uint64_t kd = kv_desc + (uint64_t)(z * (C::KV / 16));
-          tc::mma_bf16(tmem + m * 128, qd, kd, id_qk, add);
-#pragma unroll
-          for (int d = 1; d < C::D / 16; ++d)
-            tc::mma_bf16(tmem + m * 128, qd + ((d / 4) * 16384 + (d % 4) * 32) / 16,
-                         kd + ((d / 4) * C::NKV * 128 + (d % 4) * 32) / 16, id_qk, 1);
-          if (add || x == y) break;
-        }
-        issued = true;
-        tc::mma_commit(&s_full[m]);
-      };
-      for (int round = 0, i; (i = pre_nth(round)) < items && ok; ++round) {
-        const PreItem it = pre_item<C>(a, pre, i);
-        const int mt = it.rows > 128 ? 2 : 1;
-        // step -1: S of the first tile; step j: O of tile j, S of the next
-        for (int j = -1; j < it.tiles && ok; ++j) {
-          const bool more = j + 1 < it.tiles;
-          uint32_t v = 0, x = 0, y = 0;
-          if (j >= 0) v = take();
-          for (int m = 0; m < mt && ok; ++m) {
-            if (j >= 0) {
-              ok = mbar_wait_bounded(&p_full[m], n_t[m]++ & 1, a.wait_ns);
-              tc::fence_after_sync();
-              if (!ok) break;
-              const uint64_t vd = kv_desc + (uint64_t)(v * (C::KV / 16));
-              tc::mma_f16_ts(tmem + kO + m * 128, tmem + m * 128, vd, id_pv, j > 0);
-#pragma unroll
-              for (int t = 1; t < C::NKV / 16; ++t)
-                tc::mma_f16_ts(tmem + kO + m * 128, tmem + m * 128 + t * 8,
-                               vd + ((t / 4) * C::D * 128 + (t % 4) * 32) / 16, id_pv, 1);
-              issued = true;
-              tc::mma_commit(&pv_done[m]);
-              if (m == mt - 1) tc::mma_commit(&kv_empty[v]);
-            }
-            if (!more) continue;
-            if (m == 0) {
-              x = y = take();
-              if (ok && info_two[(n + (j >= 0)) % C::INFO]) y = take();
-            }
-            if (j < 0) {
-              ok = ok && mbar_wait_bounded(&q_full[m], n_it[m]++ & 1, a.wait_ns);
-              tc::fence_after_sync();
-            }
-            if (!ok) break;
-            qk(m, x, y);
-            if (m == mt - 1) {
-              tc::mma_commit(&kv_empty[x]);
-              if (y != x) tc::mma_commit(&kv_empty[y]);
-            }
-          }
+    // The warp runs whole, so that descriptors stay in uniform registers; one
+    // lane is elected at each product and commit.
+    const int m = warp - C::MMA_WARP;  // the row half
+    const uint32_t id_qk = tc::idesc_f16_f32(128, C::NKV), id_pv = tc::idesc_f16_f32(128, C::D);
+    const uint32_t t_s = tmem + m * 128, t_o = tmem + kO + m * 128;
+    // (start addresses are in 16-byte units in a descriptor's low bits, and no
+    // sum below carries out of them)
+    const uint64_t q_desc = tc::sw128_desc(smem_addr(q_s) + m * 128 * C::D * 2), kv_desc = tc::sw128_desc(smem_addr(kv_s));
+    uint32_t k = 0, k_ph = 0, n = 0;         // place and parity of the next operand; tiles so far
+    uint32_t n_it = 0, n_t = 0, n_turn = 0;  // items, tiles and turns of this half
+    auto wait = [&](uint64_t* bar, uint32_t parity) {
+      ok = __all_sync(0xffffffffu, mbar_wait_soon(bar, parity, a.wait_ns));
+    };
+    auto take = [&]() -> uint32_t {  // waits for the next operand and returns its place
+      if (ok) wait(&kv_full[k], k_ph);
+      const uint32_t x = k;
+      k = k + 1 == C::KVB ? 0 : k + 1;
+      k_ph ^= k == 0;
+      return x;
+    };
+    auto commit = [&](uint64_t* bar) {
+      if (tc::elect_one()) tc::mma_commit(bar);
+    };
+    for (int round = 0, i; (i = pre_nth(round)) < items && ok; ++round) {
+      const PreItem it = pre_item<C>(a, pre, i);
+      const bool active = it.rows > m * 128;
+      const bool both = C::MT == 2 && it.rows > 128;
+      // step -1: S of the first tile; step j: O of tile j, S of the next
+      for (int j = -1; j < it.tiles && ok; ++j) {
+        const bool more = j + 1 < it.tiles;
+        uint32_t v = 0, x = 0, y = 0;
+        auto take_keys = [&]() {  // the keys in operand x, and y where they are two
+          x = y = take();
+          if (ok && __shfl_sync(0xffffffffu, info_two[(n + (j >= 0)) % C::INFO], 0)) y = take();
+        };
+        if (j >= 0) v = take();
+        if (!active) {  // (no product of this half reads them)
+          if (more) take_keys();
           n += j >= 0;
+          if (ok && lane == 0) {
+            if (j >= 0) mbar_arrive(&kv_empty[v]);
+            if (more) mbar_arrive(&kv_empty[x]);
+            if (y != x) mbar_arrive(&kv_empty[y]);
+          }
+          __syncwarp();
+          continue;
         }
+        if (ok) {
+          if (j < 0)
+            wait(&q_full[m], n_it++ & 1);
+          else
+            wait(&p_full[m], n_t++ & 1);
+        }
+        // The halves take turns, so that one's products run while the other's
+        // weights are computed: together they would do both in step.
+        if (both) {
+          if (ok && (m == 1 || n_turn > 0)) wait(&turn[m], (n_turn - (m == 0)) & 1);
+          ++n_turn;
+        }
+        if (!ok) break;
+        tc::fence_after_sync();
+        issued = true;
+        if (j >= 0) {
+          const uint64_t vd = kv_desc + (uint64_t)(v * (C::KV / 16));
+#pragma unroll
+          for (int t = 0; t < C::NKV / 16; ++t)
+            if (tc::elect_one())
+              tc::mma_f16_ts(t_o, t_s + t * 8, vd + ((t / 4) * C::D * 128 + (t % 4) * 32) / 16, id_pv, t > 0 || j > 0);
+          commit(&pv_done[m]);
+          commit(&kv_empty[v]);
+        }
+        if (more) {
+          take_keys();
+          if (!ok) break;
+#pragma unroll 1
+          for (uint32_t add = 0, z = x;; add = 1, z = y) {
+            const uint64_t kd = kv_desc + (uint64_t)(z * (C::KV / 16));
+#pragma unroll
+            for (int d = 0; d < C::D / 16; ++d)
+              if (tc::elect_one())
+                tc::mma_bf16(t_s, q_desc + ((d / 4) * 16384 + (d % 4) * 32) / 16,
+                             kd + ((d / 4) * C::NKV * 128 + (d % 4) * 32) / 16, id_qk, d > 0 || add);
+            if (add || x == y) break;
+          }
+          commit(&s_full[m]);
+          commit(&kv_empty[x]);
+          if (y != x) commit(&kv_empty[y]);
+        }
+        n += j >= 0;
+        if (both && lane == 0) mbar_arrive(&turn[m ^ 1]);
+        __syncwarp();
       }
     }
-    __syncwarp();
   } else if (warp >= C::EXP_WARP) {
     // ---------------------------------------------------------------- expand
     if constexpr (C::REGS > 0) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::EXP_REGS));
@@ -399,7 +423,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_prefill_kernel(const AttnAr
     uint32_t n = 0, k = 0;  // tiles and operands so far
     auto wait_free = [&]() {
       if (k >= C::KVB)
-        ok = ok && mbar_wait_bounded(&kv_empty[k % C::KVB], (k / C::KVB - 1) & 1, a.wait_ns);
+        ok = ok && mbar_wait_soon(&kv_empty[k % C::KVB], (k / C::KVB - 1) & 1, a.wait_ns);
       ok = __all_sync(0xffffffffu, ok);
     };
     auto filled = [&]() {
@@ -411,11 +435,11 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_prefill_kernel(const AttnAr
     for (int round = 0, i; (i = pre_nth(round)) < items && ok; ++round) {
       const PreItem it = pre_item<C>(a, pre, i);
       const int pos_lo = it.pos0 + it.tok0, pos_hi = pos_lo + div_group(a, it.rem0 + it.rows - 1);
-      ok = __all_sync(0xffffffffu, mbar_wait_bounded(&size_full[round % C::SIZES], (round / C::SIZES) & 1, a.wait_ns));
+      ok = __all_sync(0xffffffffu, mbar_wait_soon(&size_full[round % C::SIZES], (round / C::SIZES) & 1, a.wait_ns));
       if (!ok) break;
       for (int j = 0; j < it.tiles && ok; ++j, ++n) {
         const int st = n & 1, tok0 = it.kv0 + j * C::NKV;
-        ok = mbar_wait_bounded(&raw_full[st], (n >> 1) & 1, a.wait_ns);
+        ok = mbar_wait_soon(&raw_full[st], (n >> 1) & 1, a.wait_ns);
         wait_free();
         if (!ok) break;
         const uint32_t pages = info_pages[n % C::INFO];
@@ -573,10 +597,10 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_prefill_kernel(const AttnAr
       }
       if (lane == 0) mbar_arrive(&size_empty[round % C::SIZES]);
     }
-  } else {
+  } else if (warp >= C::SOFT_WARP) {
     // --------------------------------------------------------------- softmax
     if constexpr (C::REGS > 0) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::SOFT_REGS));
-    const int m = warp >> 2, wl = warp & 3, r_l = wl * 32 + lane;
+    const int m = (warp - C::SOFT_WARP) >> 2, wl = warp & 3, r_l = wl * 32 + lane;
     const uint32_t t_s = tmem + m * 128 + ((uint32_t)(wl * 32) << 16);
     const uint32_t t_o = tmem + kO + m * 128 + ((uint32_t)(wl * 32) << 16);
     uint32_t n = 0, n_t = 0;  // tiles of all items; tiles of this half
@@ -628,7 +652,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_prefill_kernel(const AttnAr
           e = e < -100 ? -100 : e;
           const float up = pow2i(14 - e) * sign;
           const int row = (y0 + y) * C::RPL + lane / C::LPR;
-          if (chunk == 0) exp_s[warp][row] = e;
+          if (chunk == 0) exp_s[warp - C::SOFT_WARP][row] = e;
           // (dims 0 4 1 5 2 6 3 7, as the keys lie)
           *q_place(wl * 32 + row, chunk) = make_uint4(half2_bits(f[0] * up, f[4] * up), half2_bits(f[1] * up, f[5] * up),
                                                       half2_bits(f[2] * up, f[6] * up), half2_bits(f[3] * up, f[7] * up));
@@ -638,7 +662,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_prefill_kernel(const AttnAr
       tc::fence_before_sync();
       __syncwarp();
       if (lane == 0) mbar_arrive(&q_full[m]);
-      const float qa = sign == 0.0f ? 1.0f : fabsf(a.scale_log2) * pow2i(exp_s[warp][lane]) * (1.0f / 16384.0f);
+      const float qa = sign == 0.0f ? 1.0f : fabsf(a.scale_log2) * pow2i(exp_s[warp - C::SOFT_WARP][lane]) * (1.0f / 16384.0f);
 
       const int pos = it.pos0 + it.tok0 + tok;
       const int see_hi = live ? (pos + 1 < it.seq ? pos + 1 : it.seq) : -1;
@@ -648,7 +672,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_prefill_kernel(const AttnAr
       const int pos_hi = it.pos0 + it.tok0 + div_group(a, it.rem0 + last - 1);
       float m_run = kNoMax, l = 0.0f;
       for (int j = 0; j < it.tiles; ++j, ++n, ++n_t) {
-        ok = __all_sync(0xffffffffu, mbar_wait_bounded(&s_full[m], n_t & 1, a.wait_ns));
+        ok = __all_sync(0xffffffffu, mbar_wait_soon(&s_full[m], n_t & 1, a.wait_ns));
         if (!ok) break;
         tc::fence_after_sync();
         const int tok0 = it.kv0 + j * C::NKV;
@@ -712,7 +736,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_prefill_kernel(const AttnAr
               tc::tmem_st16(t_s + x * 16, reinterpret_cast<const uint32_t*>(z));
             }
             if (j > 0) {
-              ok = __all_sync(0xffffffffu, mbar_wait_bounded(&pv_done[m], (n_t - 1) & 1, a.wait_ns));
+              ok = __all_sync(0xffffffffu, mbar_wait_soon(&pv_done[m], (n_t - 1) & 1, a.wait_ns));
               if (!ok) break;
               tc::fence_after_sync();
 #pragma unroll 1
@@ -746,7 +770,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_prefill_kernel(const AttnAr
         }
       }
       if (!ok) break;
-      ok = __all_sync(0xffffffffu, mbar_wait_bounded(&pv_done[m], (n_t - 1) & 1, a.wait_ns));
+      ok = __all_sync(0xffffffffu, mbar_wait_soon(&pv_done[m], (n_t - 1) & 1, a.wait_ns));
       if (!ok) break;
       tc::fence_after_sync();
       const float inv = l != 0.0f ? 1.0f / l : 0.0f;
@@ -781,11 +805,11 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_prefill_kernel(const AttnAr
     }
   }
   if (!ok) set_error(a.err, LORA_DEV_ERR_TIMEOUT);
-  // After a time-out the products issued last may still run: one more commit
-  // tracks them, and tensor memory is freed after it has arrived.
-  if (!__syncthreads_and(ok) && warp == C::MMA_WARP && lane == 0 && issued) {
-    tc::mma_commit(&drain_bar);
-    mbar_wait_bounded(&drain_bar, 0, kWaitLimitNs);
+  // After a time-out the products issued last may still run: one more commit of
+  // each issuing thread tracks them, and tensor memory is freed after it has arrived.
+  if (!__syncthreads_and(ok) && issued && tc::elect_one()) {  // (an MMA warp)
+    tc::mma_commit(&drain_bar[warp - C::MMA_WARP]);
+    mbar_wait_soon(&drain_bar[warp - C::MMA_WARP], 0, kWaitLimitNs);
   }
   tc::fence_before_sync();
   __syncthreads();
