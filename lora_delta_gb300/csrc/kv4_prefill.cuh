@@ -275,6 +275,13 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_prefill_kernel(const AttnAr
 #pragma unroll
       for (int d = C::LPR; d < 32; d <<= 1) sq += __shfl_xor_sync(0xffffffffu, sq, d);
       const float sc = a.scale_log2 * 0.69314718055994531f;
+      // and all of it on its way to L2
+      for (int x = lane; x < it.rows * (C::D / 64); x += 32) {
+        const int y = it.rem0 + x / (C::D / 64), t = div_group(a, y);
+        asm volatile("prefetch.global.L2 [%0];" ::"l"(
+            reinterpret_cast<const uint16_t*>(a.q) + (int64_t)(it.row0 + it.tok0 + t) * a.ld_q +
+            (it.h * a.group + y - t * a.group) * C::D + x % (C::D / 64) * 64));
+      }
       if (lane < C::LPR && lane % 8 == 0) size_s[round % C::SIZES][lane / 8] = sq * sc * sc / (4 * C::RPL);
       __syncwarp();
       if (lane == 0) mbar_arrive(&size_full[round % C::SIZES]);
@@ -623,7 +630,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_prefill_kernel(const AttnAr
       // q of the warp's rows, 16 bytes a lane (earlier products with this
       // half's q are done), a batch of loads at once
       const int chunk = lane % C::LPR;
-      constexpr int kBatch = 8;
+      constexpr int kBatch = C::LPR < 16 ? 8 : 16;
 #pragma unroll 1
       for (int y0 = 0; y0 < 32 / C::RPL; y0 += kBatch) {
         uint4 raw[kBatch];
@@ -681,42 +688,61 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_prefill_kernel(const AttnAr
                           (a.window > 0 && tok0 <= pos_hi - a.window) || pages != (1u << C::TPK) - 1u;
         // columns that the row sees, and the blocks of 16 that were not read
         const int c_lo = see_lo - tok0, c_hi = see_hi - tok0;
-        auto seen = [&](int col) { return col >= c_lo && col < c_hi && ((pages >> (col / kKvTile)) & 1u); };
+        auto seen32 = [&](int col) -> uint32_t {  // of the 32 columns from col
+          const int lo = c_lo - col > 0 ? c_lo - col : 0, hi = c_hi - col < 32 ? c_hi - col : 32;
+          uint32_t s = hi > lo ? (0xffffffffu >> (32 - (hi - lo))) << lo : 0u;
+          const uint32_t two_blocks = pages >> (col / kKvTile);
+          if (!(two_blocks & 1u)) s &= 0xffff0000u;
+          if (!(two_blocks & 2u)) s &= 0x0000ffffu;
+          return s;
+        };
         // 64 columns at a time: weights by the maximum so far, kept in
-        // registers until no score is known to exceed it by 2^8, else once
-        // more by a new maximum
+        // registers until their sum shows that none is above 2^15, which f16
+        // holds (64 at the maximum make 2^13); else once more by a new maximum
         const uint64_t qa2 = f32x2(qa, qa);
+        auto scores = [&](int col, float* v) {
+          tc::tmem_ld32(t_s + col, v);
+          if (edge) {
+            __syncwarp();  // (a branch, not 32 selections each time)
+            const uint32_t s = seen32(col);
+#pragma unroll
+            for (int x = 0; x < 32; ++x)
+              if (!(s & (1u << x))) v[x] = -INFINITY;
+          }
+        };
 #pragma unroll 1
         for (int part = 0; part < C::NKV / 64; ++part) {
           uint32_t w[32];
-          uint64_t l2;
+          float l0, l1;
           for (;;) {
             const float off = 7.0f - m_run;
             const uint64_t off2 = f32x2(off, off);
-            float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-            l2 = f32x2(0.0f, 0.0f);
+            uint64_t l2 = f32x2(0.0f, 0.0f);
 #pragma unroll
             for (int ch = 0; ch < 2; ++ch) {
               float v[32];
-              tc::tmem_ld32(t_s + part * 64 + ch * 32, v);
-              if (edge) {
-#pragma unroll
-                for (int x = 0; x < 32; ++x)
-                  if (!seen(part * 64 + ch * 32 + x)) v[x] = -INFINITY;
-              }
+              scores(part * 64 + ch * 32, v);
 #pragma unroll
               for (int x = 0; x < 16; ++x) {
                 float e0, e1;
                 f32x2_split(fma_f32x2(f32x2(v[2 * x], v[2 * x + 1]), qa2, off2), e0, e1);
-                m4[x % 4] = fmaxf(fmaxf(m4[x % 4], v[2 * x]), v[2 * x + 1]);
                 e0 = exp2_fast(e0);
                 e1 = exp2_fast(e1);
                 l2 = add_f32x2(l2, f32x2(e0, e1));
                 w[ch * 16 + x] = half2_bits(e0, e1);
               }
             }
-            const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * qa;
-            if (!__any_sync(0xffffffffu, mx > m_run + 8.0f)) break;
+            f32x2_split(l2, l0, l1);
+            if (!__any_sync(0xffffffffu, l0 + l1 > 32768.0f)) break;
+            float mx = -INFINITY;
+#pragma unroll 1
+            for (int ch = 0; ch < 2; ++ch) {
+              float v[32];
+              scores(part * 64 + ch * 32, v);
+#pragma unroll
+              for (int x = 0; x < 32; ++x) mx = fmaxf(mx, v[x]);
+            }
+            mx *= qa;
             // the sums so far by 2^(old - new), in O after the product that is
             // under way, and the weights of this tile already written
             const float m1 = fmaxf(m_run, mx), keep = exp2_fast(m_run - m1);
@@ -750,8 +776,6 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_prefill_kernel(const AttnAr
             }
           }
           if (!ok) break;
-          float l0, l1;
-          f32x2_split(l2, l0, l1);
           l += l0 + l1;
           tc::tmem_st16(t_s + part * 32, w);  // (over columns read already)
           tc::tmem_st16(t_s + part * 32 + 16, w + 16);
@@ -763,10 +787,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_prefill_kernel(const AttnAr
         if (lane == 0) mbar_arrive(&p_full[m]);
         if (edge) {
           for (int w = 0; w < C::NKV / 32; ++w)
-            for (uint32_t bits = info_bad[n % C::INFO][w]; bits; bits &= bits - 1) {
-              const int col = w * 32 + __ffs(bits) - 1;
-              if (seen(col)) l = __int_as_float(0x7fffffff);
-            }
+            if (info_bad[n % C::INFO][w] & seen32(w * 32)) l = __int_as_float(0x7fffffff);
         }
       }
       if (!ok) break;
