@@ -15,10 +15,21 @@ from ._lib import lib
 _DTYPES = {torch.bfloat16: 0, torch.float16: 1}
 
 
-def _call(name, *args):
-    rc = getattr(lib(), name)(*args)
+def _check(name, rc):
     if rc:
         raise LoraError(name, rc)
+
+
+class _Functions:
+    """The library's functions, looked up once (``lib()`` loads it on the first call)."""
+
+    def __getattr__(self, name):
+        fn = getattr(lib(), name)
+        setattr(self, name, fn)
+        return fn
+
+
+_fn = _Functions()
 
 
 def _at(t):
@@ -26,32 +37,40 @@ def _at(t):
 
 
 def _raw_stream(stream):
-    return (torch.cuda.current_stream() if stream is None else stream).cuda_stream
+    # (torch.cuda.current_stream() builds a Stream object, a third of a small call's time)
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+    return stream.cuda_stream
 
 
-def _i32(t, name, size=None):
-    _dev(t, name, torch.int32)
-    if size is not None and t.numel() < size:
+def _i32(t, name, size=0):
+    if not t.is_cuda or t.dtype is not torch.int32 or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous int32 CUDA tensor")
+    if t.numel() < size:
         raise ValueError(f"{name} must have {size} entries, got {t.numel()}")
     return t.data_ptr()
 
 
 def _table(t, n_reqs):
-    if not t.is_cuda or t.dtype != torch.int32 or t.dim() != 2 or t.shape[0] < n_reqs or \
-            (t.shape[1] > 1 and t.stride(1) != 1 and n_reqs > 0):
-        raise ValueError("block_table must be an int32 CUDA tensor [n_reqs, max_pages] with adjacent entries")
-    return t.data_ptr(), t.stride(0), t.shape[1]
+    """Pointer, row stride and pages a request of a block table."""
+    if t.is_cuda and t.dtype is torch.int32 and t.dim() == 2:
+        rows, pages = t.shape
+        ld, step = t.stride()
+        if rows >= n_reqs and (step == 1 or pages <= 1 or n_reqs == 0):
+            return t.data_ptr(), ld, pages
+    raise ValueError("block_table must be an int32 CUDA tensor [n_reqs, max_pages] with adjacent entries")
 
 
 def _rows(t, name, heads, head_dim, dtype):
     """Pointer and row stride of a [n, heads, head_dim] tensor whose rows may lie apart."""
-    if not t.is_cuda or t.dtype != dtype:
+    if not t.is_cuda or t.dtype is not dtype:
         raise ValueError(f"{name} must be a {dtype} CUDA tensor")
-    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != head_dim:
+    if t.dim() != 3 or t.shape[1:] != (heads, head_dim):
         raise ValueError(f"{name} must be [n, {heads}, {head_dim}], got {tuple(t.shape)}")
-    if t.stride(2) != 1 or (heads > 1 and t.stride(1) != head_dim):
+    ld, head, step = t.stride()
+    if step != 1 or (head != head_dim and heads > 1):
         raise ValueError(f"{name}'s heads must lie next to one another")
-    return t.data_ptr(), t.stride(0) if t.shape[0] > 1 else heads * head_dim
+    return t.data_ptr(), ld if t.shape[0] > 1 else heads * head_dim
 
 
 class BatchPlan:
@@ -78,14 +97,15 @@ def lora_batch_plan(plan: BatchPlan, ctx_len, new_len, block_table, req_slot=Non
     ``free_pages`` / ``free_count`` [1] are the stack of free pages; the height that is left goes to
     ``free_left`` [1], or back into ``free_count`` where none is given."""
     B = plan.n_reqs
-    if free_pages is not None and free_left is None:
-        free_left = free_count
-    _call("lora_batch_plan", _i32(ctx_len, "ctx_len", B), _i32(new_len, "new_len", B),
-          None if req_slot is None else _i32(req_slot, "req_slot", B), B, plan.n_rows,
-          plan.page_size, *_table(block_table, B),
-          *(None if t is None else _i32(t, name) for t, name in (
-              (free_pages, "free_pages"), (free_count, "free_count"), (free_left, "free_left"))),
-          *plan._out, _at(err), _raw_stream(stream))
+    table, ld, pages = _table(block_table, B)
+    free = count = left = None
+    if free_pages is not None:
+        free, count = _i32(free_pages, "free_pages"), _i32(free_count, "free_count", 1)
+        left = count if free_left is None else _i32(free_left, "free_left", 1)
+    _check("lora_batch_plan", _fn.lora_batch_plan(
+        _i32(ctx_len, "ctx_len", B), _i32(new_len, "new_len", B),
+        None if req_slot is None else _i32(req_slot, "req_slot", B), B, plan.n_rows, plan.page_size,
+        table, ld, pages, free, count, left, *plan._out, _at(err), _raw_stream(stream)))
     return plan
 
 
@@ -93,9 +113,11 @@ def lora_pages_release(done, seq_len, block_table, page_size: int, free_pages, f
                        stream=None):
     """The pages of the requests with ``done[b] != 0`` back onto the stack of free pages."""
     B = done.numel()
-    _call("lora_pages_release", _i32(done, "done"), _i32(seq_len, "seq_len", B), B, int(page_size),
-          *_table(block_table, B), _i32(free_pages, "free_pages"), free_pages.numel(),
-          _i32(free_count, "free_count"), _at(err), _raw_stream(stream))
+    table, ld, pages = _table(block_table, B)
+    _check("lora_pages_release", _fn.lora_pages_release(
+        _i32(done, "done"), _i32(seq_len, "seq_len", B), B, int(page_size), table, ld, pages,
+        _i32(free_pages, "free_pages"), free_pages.numel(), _i32(free_count, "free_count", 1), _at(err),
+        _raw_stream(stream)))
 
 
 def lora_kv4_page_bytes(page_size: int, kv_heads: int, head_dim: int) -> int:
@@ -134,32 +156,29 @@ class Kv4Cache:
                                dtype=torch.uint8, device=device), page_size, head_dim, dtype)
 
 
-def _slots(slot_map, n):
-    _dev(slot_map, "slot_map", torch.int64)
+def _store_or_read(name, cache, k, v, slot_map, err, stream):
+    n, H, D = k.shape[0], cache.kv_heads, cache.head_dim
+    if v.shape[0] != n:
+        raise ValueError("k and v must have the same number of rows")
+    if not slot_map.is_cuda or slot_map.dtype is not torch.int64 or not slot_map.is_contiguous():
+        raise ValueError("slot_map must be a contiguous int64 CUDA tensor")
     if slot_map.numel() != n:
         raise ValueError(f"slot_map must have {n} entries, got {slot_map.numel()}")
-    return slot_map.data_ptr()
+    k_at, ld_k = _rows(k, "k", H, D, cache.dtype)
+    v_at, ld_v = _rows(v, "v", H, D, cache.dtype)
+    _check(name, getattr(_fn, name)(*cache._args, k_at, ld_k, v_at, ld_v, slot_map.data_ptr(), n, _at(err),
+                                    _raw_stream(stream)))
 
 
 def lora_kv4_append(cache: Kv4Cache, k, v, slot_map, err=None, stream=None):
     """Quantise the rows ``k``, ``v`` [n, kv_heads, head_dim] and store row i at ``slot_map[i]``
     (a negative slot is not stored).  The rows may be slices of a fused projection's output."""
-    n = k.shape[0]
-    if v.shape[0] != n:
-        raise ValueError("k and v must have the same number of rows")
-    _call("lora_kv4_append", *cache._args, *_rows(k, "k", cache.kv_heads, cache.head_dim, cache.dtype),
-          *_rows(v, "v", cache.kv_heads, cache.head_dim, cache.dtype), _slots(slot_map, n), n,
-          _at(err), _raw_stream(stream))
+    _store_or_read("lora_kv4_append", cache, k, v, slot_map, err, stream)
 
 
 def lora_kv4_read(cache: Kv4Cache, k, v, slot_map, err=None, stream=None):
     """The values that stored rows stand for, into ``k``, ``v`` [n, kv_heads, head_dim]."""
-    n = k.shape[0]
-    if v.shape[0] != n:
-        raise ValueError("k and v must have the same number of rows")
-    _call("lora_kv4_read", *cache._args, *_rows(k, "k", cache.kv_heads, cache.head_dim, cache.dtype),
-          *_rows(v, "v", cache.kv_heads, cache.head_dim, cache.dtype), _slots(slot_map, n), n,
-          _at(err), _raw_stream(stream))
+    _store_or_read("lora_kv4_read", cache, k, v, slot_map, err, stream)
 
 
 def lora_kv4_attention_workspace(device="cuda") -> torch.Tensor:
@@ -175,17 +194,15 @@ def lora_kv4_attention_workspace(device="cuda") -> torch.Tensor:
 _ATTN_WS: dict = {}
 
 
-def _attn_workspace(device, stream):
-    s = torch.cuda.current_stream(device) if stream is None else stream
-    key = (device.index, s.cuda_stream)
-    ws = _ATTN_WS.get(key)
+def _attn_workspace(device, stream, raw):
+    ws = _ATTN_WS.get((device.index, raw))
     if ws is None:
-        with torch.cuda.stream(s):
+        with torch.cuda.stream(torch.cuda.current_stream(device) if stream is None else stream):
             ws = lora_kv4_attention_workspace(device)
             if torch.cuda.is_current_stream_capturing():
-                return ws, s.cuda_stream  # the graph's own, zeroed by each replay
-        _ATTN_WS[key] = ws
-    return ws, s.cuda_stream
+                return ws  # the graph's own, zeroed by each replay
+        _ATTN_WS[(device.index, raw)] = ws
+    return ws
 
 
 def lora_kv4_attention(out, q, cache: Kv4Cache, block_table, row_start, seq_len, max_q_len: int,
@@ -197,20 +214,22 @@ def lora_kv4_attention(out, q, cache: Kv4Cache, block_table, row_start, seq_len,
     keys must be stored before.  ``max_q_len``: the most rows of one request.  ``scale`` defaults to
     head_dim ** -0.5; ``window`` > 0 limits a row to the last ``window`` tokens up to its own.  ``lse``
     [n, q_heads] float32 receives the log of the softmax's denominator."""
-    n, q_heads = q.shape[0], q.shape[1]
+    n, q_heads, D = q.shape
     B = seq_len.numel()
-    if out.shape != q.shape:
-        raise ValueError("out and q must have the same shape")
+    if out.shape[0] != n:
+        raise ValueError("out and q must have the same number of rows")
     if lse is not None:
         _dev(lse, "lse", torch.float32)
         if lse.numel() != n * q_heads:
             raise ValueError("lse must be [n, q_heads]")
+    raw = _raw_stream(stream)
     if workspace is None:
-        workspace, raw = _attn_workspace(q.device, stream)
-    else:
-        raw = _raw_stream(stream)
-    _call("lora_kv4_attention", *_rows(out, "out", q_heads, cache.head_dim, cache.dtype),
-          *_rows(q, "q", q_heads, cache.head_dim, cache.dtype), n, q_heads, *cache._args,
-          *_table(block_table, B), _i32(row_start, "row_start", B + 1), _i32(seq_len, "seq_len"), B,
-          max_q_len, cache.head_dim ** -0.5 if scale is None else scale, window, _at(lse),
-          workspace.data_ptr(), workspace.numel(), _at(err), raw)
+        workspace = _attn_workspace(q.device, stream, raw)
+    out_at, ld_out = _rows(out, "out", q_heads, cache.head_dim, cache.dtype)
+    q_at, ld_q = _rows(q, "q", q_heads, cache.head_dim, cache.dtype)
+    table, ld, pages = _table(block_table, B)
+    _check("lora_kv4_attention", _fn.lora_kv4_attention(
+        out_at, ld_out, q_at, ld_q, n, q_heads, *cache._args, table, ld, pages,
+        _i32(row_start, "row_start", B + 1), _i32(seq_len, "seq_len"), B, max_q_len,
+        D ** -0.5 if scale is None else scale, window, _at(lse), workspace.data_ptr(),
+        workspace.numel(), _at(err), raw))
