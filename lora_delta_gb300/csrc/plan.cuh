@@ -76,14 +76,15 @@ __device__ __forceinline__ void block_scan2(int64_t a, int b, int64_t& ex_a, int
   ex_b = base_b + sb - b;
 }
 
-// One thread-block cluster.  Every CTA scans all requests (12 bytes each, in
-// L2 after the first), so no CTA waits for another's sums; the rows are then
-// shared out in contiguous chunks and each row finds its request by binary
-// search in shared memory.  Table entries below ceil(ctx / P) are only read
-// and the others only written, and the free count is read before the cluster
-// barrier and stored after it, so free_left may be free_count itself.
+// Every CTA scans all requests (12 bytes each, in L2 after the first), so no CTA
+// waits for another's sums; the rows are then shared out in contiguous chunks
+// and each row finds its request by binary search in shared memory.  Table
+// entries below ceil(ctx / P) are only read and the others only written.  Where
+// free_left is free_count itself, the count is stored behind a barrier of one
+// thread-block cluster (`cluster`), after every CTA has read it; else there are
+// CTAs for all rows.
 // Bound: latency (20 bytes a row; three dependent round trips to L2/HBM).
-__global__ void __launch_bounds__(kPlanThreads) batch_plan_kernel(const PlanArgs a, int n_ctas) {
+__global__ void __launch_bounds__(kPlanThreads) batch_plan_kernel(const PlanArgs a, int cluster) {
   extern __shared__ int32_t plan_smem[];
   int32_t* start_s = plan_smem;           // [B + 1] first row, clipped to n
   int32_t* ctx_s = plan_smem + a.B + 1;   // [B]
@@ -91,7 +92,8 @@ __global__ void __launch_bounds__(kPlanThreads) batch_plan_kernel(const PlanArgs
   __shared__ int64_t buf_a[kPlanThreads / 32];
   __shared__ int buf_b[kPlanThreads / 32];
   __shared__ int used_s;
-  const int rank = blockIdx.x, P = a.page_size;
+  const int rank = blockIdx.x, n_ctas = gridDim.x, P = a.page_size;
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // (what the kernel before wrote is read from here on)
   const int64_t cap = (int64_t)a.max_pages * P;
   const int count = a.free_pages ? *a.free_count : 0;
   if (threadIdx.x == 0) used_s = 0;
@@ -198,7 +200,7 @@ __global__ void __launch_bounds__(kPlanThreads) batch_plan_kernel(const PlanArgs
     }
   }
   if (bad) set_error(a.err, bad);
-  if (n_ctas > 1) {
+  if (cluster) {
     cluster_arrive();
     cluster_wait();
   }

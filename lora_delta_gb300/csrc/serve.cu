@@ -47,6 +47,23 @@ int check_rows(const void* p, int64_t ld, int n, int width) {
 // kernels' own variables.
 constexpr size_t kAttnMaxSmem = 227 * 1024 - 2048;
 
+// Launch of a kernel that waits for the one before it by griddepcontrol.
+template <class... P, class... A>
+int launch_after(void (*kernel)(P...), unsigned grid, int threads, size_t smem, cudaStream_t stream,
+                 const A&... args) {
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = use_pdl() ? 1 : 0;
+  return cuda_status(cudaLaunchKernelEx(&cfg, kernel, P(args)...));
+}
+
 // f(kernel for head_dim and type)
 template <class F>
 int by_type(int head_dim, int dtype, F f) {
@@ -82,17 +99,24 @@ int rows_call(bool store, const void* k, int64_t ld_k, const void* v, int64_t ld
   a.slot_map = slot_map;
   a.n = n;
   a.err = err;
-  const int64_t items = (int64_t)n * 2 * heads * (head_dim / 8);
-  const int64_t want = (items + 255) / 256, most = (int64_t)sm_count() * 32;
+  a.page_shift = -1;
+  for (int x = 4; x <= 10; ++x)
+    if (page_size == 1 << x) a.page_shift = x;
+  // a head a task until there are 128 warps for an SM
+  const int64_t blocks = ((int64_t)n + 7) / 8, fill = (int64_t)sm_count() * 128;
+  int64_t per = blocks * 2 * heads / fill;
+  per = per < 1 ? 1 : (per > heads ? heads : per);
+  a.task_heads = (int)per;
+  const int64_t tasks = blocks * 2 * ((heads + per - 1) / per);
+  if (tasks > INT32_MAX) return LORA_ERR_UNSUPPORTED;
+  constexpr int kWarps = kKvThreads / 32;
+  const int64_t want = (tasks + kWarps - 1) / kWarps, most = (int64_t)sm_count() * 32;
   const unsigned grid = (unsigned)(want < most ? want : most);
   return by_type(head_dim, dtype, [&](auto d, auto bf) {
     constexpr int D = decltype(d)::value;
     constexpr bool BF16 = decltype(bf)::value;
-    if (store)
-      kv4_append_kernel<D, BF16><<<grid, 256, 0, stream>>>(a);
-    else
-      kv4_read_kernel<D, BF16><<<grid, 256, 0, stream>>>(a);
-    return cuda_status(cudaGetLastError());
+    return store ? launch_after(kv4_rows_kernel<D, BF16, true>, grid, kKvThreads, 0, stream, a)
+                 : launch_after(kv4_rows_kernel<D, BF16, false>, grid, kKvThreads, 0, stream, a);
   });
 }
 
@@ -112,17 +136,7 @@ int launch_decode(const AttnArgs& a, cudaStream_t stream) {
   int ctas = sm_count();
   if (ctas > kAttnMaxCtas) ctas = kAttnMaxCtas;
   static const int alone = env_int("LORA_ATTN_ALONE", 64);
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)ctas);
-  cfg.blockDim = dim3(C::THREADS);
-  cfg.dynamicSmemBytes = (size_t)smem;
-  cfg.stream = stream;
-  cfg.attrs = attr;
-  cfg.numAttrs = use_pdl() ? 1 : 0;
-  return cuda_status(cudaLaunchKernelEx(&cfg, kv4_decode_kernel<C>, a, stages, alone));
+  return launch_after(kv4_decode_kernel<C>, (unsigned)ctas, C::THREADS, (size_t)smem, stream, a, stages, alone);
 }
 
 template <class C>
@@ -182,21 +196,25 @@ int lora_batch_plan(const int32_t* ctx_len, const int32_t* new_len, const int32_
   const int smem = (int)plan_smem_bytes(n_reqs);
   if (prepare_kernel(batch_plan_kernel, smem, false) != cudaSuccess) return LORA_ERR_CUDA;
   const int64_t per_cta = kPlanThreads * kPlanRowsPerThread;
-  int ctas = 1;
-  while (ctas < kPlanMaxCluster && ctas * per_cta < n_rows) ctas *= 2;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = (unsigned)ctas;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
+  // (one cluster where the free count is replaced in place)
+  const bool cluster = free_left != nullptr && free_left == free_count;
+  const int64_t want = (n_rows + per_cta - 1) / per_cta, most = cluster ? kPlanMaxCluster : sm_count();
+  const int ctas = want < 1 ? 1 : (int)(want < most ? want : most);
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = (unsigned)ctas;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)ctas);
   cfg.blockDim = dim3(kPlanThreads);
   cfg.dynamicSmemBytes = (size_t)smem;
   cfg.stream = (cudaStream_t)stream;
-  cfg.attrs = attr;
-  cfg.numAttrs = ctas > 1 ? 1 : 0;
-  return cuda_status(cudaLaunchKernelEx(&cfg, batch_plan_kernel, (const PlanArgs)a, ctas));
+  cfg.attrs = use_pdl() ? attr : attr + 1;
+  cfg.numAttrs = (use_pdl() ? 1 : 0) + (cluster && ctas > 1 ? 1 : 0);
+  return cuda_status(cudaLaunchKernelEx(&cfg, batch_plan_kernel, (const PlanArgs)a, cluster && ctas > 1 ? 1 : 0));
 }
 
 int lora_pages_release(const int32_t* done, const int32_t* seq_len, int n_reqs, int page_size,
