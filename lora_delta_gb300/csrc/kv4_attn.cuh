@@ -133,8 +133,10 @@ struct Dec {
   // numbers) queue behind them.
   static constexpr int MIN_STAGES = (SLOT * 4 + 2 * TILE - 1) / (2 * TILE) < 2 ? 2 : (SLOT * 4 + 2 * TILE - 1) / (2 * TILE);
   static constexpr int MAX_STAGES = MIN_STAGES > (D == 64 ? 4 : 3) ? MIN_STAGES : (D == 64 ? 4 : 3);
-  static constexpr size_t smem(int B, int stages) {
-    return (size_t)NW * (stages * 2 * TILE + QROW + QBYTES) + (size_t)(B + 1) * 4 + 16;
+  // (with the requests' row starts and lengths beside the sums of their work,
+  // or without)
+  static constexpr size_t smem(int B, int stages, bool cached) {
+    return (size_t)NW * (stages * 2 * TILE + QROW + QBYTES) + (size_t)(B + 1) * (cached ? 12 : 4) + 16;
   }
 };
 
@@ -201,13 +203,13 @@ __device__ __forceinline__ void dec_save(const DecState<C>& st, float* slot, int
     p[C::F4 + n * 32] = make_float4(st.m[n][0], st.m[n][1], st.l[n][0], st.l[n][1]);
   }
 }
-// (o, ml) += (o2, ml2), each sums relative to its own maxima.
+// (o, ml) += (o2, ml2), the latter relative to its own maxima, ml.x and ml.y
+// being the largest already.
 __device__ __forceinline__ void dec_join(float4& o, float4& ml, const float4& o2, const float4& ml2) {
-  const float m0 = fmaxf(ml.x, ml2.x), m1 = fmaxf(ml.y, ml2.y);
-  const float a0 = exp2_fast(ml.x - m0), a1 = exp2_fast(ml.y - m1);
-  const float b0 = exp2_fast(ml2.x - m0), b1 = exp2_fast(ml2.y - m1);
-  ml = make_float4(m0, m1, ml.z * a0 + ml2.z * b0, ml.w * a1 + ml2.w * b1);
-  o = make_float4(o.x * a0 + o2.x * b0, o.y * a1 + o2.y * b1, o.z * a0 + o2.z * b0, o.w * a1 + o2.w * b1);
+  const float b0 = exp2_fast(ml2.x - ml.x), b1 = exp2_fast(ml2.y - ml.y);
+  ml.z = fmaf(ml2.z, b0, ml.z);
+  ml.w = fmaf(ml2.w, b1, ml.w);
+  o = make_float4(fmaf(o2.x, b0, o.x), fmaf(o2.y, b1, o.y), fmaf(o2.z, b0, o.z), fmaf(o2.w, b1, o.w));
 }
 
 // What a (request, head) is: its rows, and the tiles that they see.
@@ -218,10 +220,10 @@ struct DecReq {
   int tile0, units;   // first tile and number of units, 0 for a request without rows here
 };
 
-__device__ __forceinline__ DecReq dec_request(const AttnArgs& a, int b, int max_rows, uint32_t& bad) {
+// (start, end: its first row and the next request's; seq: its length)
+__device__ __forceinline__ DecReq dec_request(const AttnArgs& a, int start, int end, int seq, int max_rows,
+                                              uint32_t& bad) {
   DecReq r;
-  const int start = a.row_start[b], end = a.row_start[b + 1];
-  const int seq = a.seq_len[b];
   r.row0 = start;
   r.rows = 0;
   r.pos0 = 0;
@@ -581,15 +583,20 @@ constexpr int kItemCost = 2;
 
 template <class C>
 __global__ void __launch_bounds__(C::THREADS, 1) kv4_decode_kernel(const AttnArgs a, int stages,
-                                                                   int min_units) {
+                                                                   int cached, int min_units) {
   extern __shared__ __align__(128) uint8_t dec_smem[];
   __shared__ uint64_t bars[C::NW][C::MAX_STAGES];
   __shared__ int scan_s[C::NW];
-  __shared__ int max_s, over_s, last_s, chains_s;
+  __shared__ int max_s, over_s, last_s[2], chains_s;
   // segments of items that cross the warps' parts: [0] the warp's first, [1]
   // its last (b -1: none), and the items' first and last + 1 unit
   __shared__ int seg_b[C::NW][2], seg_h[C::NW][2], seg_lo[C::NW][2], seg_hi[C::NW][2];
   __shared__ int chain_s[2 * C::NW];
+  struct Cross {  // an item that crosses CTAs: the first and last, its place in the first
+    int c0, c1, into, h;
+    DecReq r;
+  };
+  __shared__ Cross cross_s[2];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, c = lane & 3;
   const int ring_bytes = stages * 2 * C::TILE;
   uint8_t* ring = dec_smem + warp * ring_bytes;
@@ -597,6 +604,10 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_decode_kernel(const AttnArg
   uint32_t* q_s = reinterpret_cast<uint32_t*>(dec_smem + C::NW * (ring_bytes + C::QROW) + warp * C::QBYTES) + lane;
   int32_t* pre = reinterpret_cast<int32_t*>(dec_smem + C::NW * (ring_bytes + C::QROW + C::QBYTES));
   const int cta = blockIdx.x, n_ctas = gridDim.x;
+  // the requests' row starts and lengths, in shared memory where there is room
+  int32_t* const copy = pre + a.B + 1;
+  const int32_t* const starts = cached ? copy : a.row_start;
+  const int32_t* const seqs = cached ? copy + a.B + 1 : a.seq_len;
 
   if (lane < stages) mbar_init(&bars[warp][lane], 1);
   if (lane < 2) seg_b[warp][lane] = -1;
@@ -613,7 +624,13 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_decode_kernel(const AttnArg
     for (int i = 0; i < per; ++i) {
       const int b = tid * per + i;
       if (b >= a.B) break;
-      const int units = dec_request(a, b, C::ROWS, bad).units;
+      const int start = a.row_start[b], end = a.row_start[b + 1], seq = a.seq_len[b];
+      if (cached) {
+        copy[b] = start;
+        if (b == a.B - 1) copy[a.B] = end;
+        copy[a.B + 1 + b] = seq;
+      }
+      const int units = dec_request(a, start, end, seq, C::ROWS, bad).units;
       pre[b] = units ? units + kItemCost : 0;
       sum += pre[b];
       most = most > units ? most : units;
@@ -644,7 +661,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_decode_kernel(const AttnArg
   if (cta == 0 && bad) set_error(a.err, bad);
   // rows that no request covers, and requests that are refused
   uint16_t* const out = reinterpret_cast<uint16_t*>(a.out);
-  const int first_row = a.B > 0 ? a.row_start[0] : a.n, last_row = a.B > 0 ? a.row_start[a.B] : a.n;
+  const int first_row = a.B > 0 ? starts[0] : a.n, last_row = a.B > 0 ? starts[a.B] : a.n;
   if (first_row > 0 || last_row < a.n || over_s) {
 #pragma unroll 1
     for (int b = over_s ? -1 : a.B - 1; b <= a.B; ++b) {
@@ -657,8 +674,8 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_decode_kernel(const AttnArg
         hi = a.n;
       } else {
         if (pre[b + 1] != pre[b]) continue;
-        lo = a.row_start[b];
-        hi = a.row_start[b + 1];
+        lo = starts[b];
+        hi = starts[b + 1];
       }
       zero_rows<C>(out, a.ld_out, a.q_heads, a.lse, lo < 0 ? 0 : lo, hi < a.n ? hi : a.n, cta, n_ctas);
     }
@@ -707,19 +724,20 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_decode_kernel(const AttnArg
     do ++p.b; while (pre[p.b + 1] == pre[p.b]);
   };
 
-  DecState<C> st;
   uint32_t unused = 0;
+  auto request = [&](int b) { return dec_request(a, starts[b], starts[b + 1], seqs[b], C::ROWS, unused); };
+  DecState<C> st;
   int f = w0;
   Place at = {0, 0, 0};
   DecReq r = {};
   if (f < w1) {
     at = find(f);
-    r = dec_request(a, at.b, C::ROWS, unused);
+    r = request(at.b);
     if (at.u >= r.units) {  // the part begins in the cost of an item's end
       f += r.units + kItemCost - at.u;
       if (f < w1) {
         next_item(at);
-        r = dec_request(a, at.b, C::ROWS, unused);
+        r = request(at.b);
       }
     }
   }
@@ -773,7 +791,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_decode_kernel(const AttnArg
         fresh = true;
         if (pf < w1) {
           next_item(pp);
-          pr = dec_request(a, pp.b, C::ROWS, unused);
+          pr = request(pp.b);
         }
       }
     };
@@ -864,13 +882,11 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_decode_kernel(const AttnArg
       }
       __syncwarp();
       // the item after this one
-      Place nx = at;
-      DecReq rn = r;
       const int f_next = item1 + kItemCost;
       if (f_next < w1) {
+        Place nx = at;
         next_item(nx);
-        rn = dec_request(a, nx.b, C::ROWS, unused);
-        fetch_q(rn, nx.h);
+        fetch_q(request(nx.b), nx.h);
       }
       dec_reset(st);
       // every row sees the tokens [see0, see1)
@@ -909,7 +925,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_decode_kernel(const AttnArg
       }
       dec_finish(st);
       if (item0 >= w0 && item1 <= w1) {
-        dec_write(a, r, at.h, st, lane);
+        dec_write(a, request(at.b), at.h, st, lane);
       } else {
         // a part of an item: the warp's first goes to memory, where its ring
         // is still in use; its last to the ring, which has served
@@ -924,8 +940,10 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_decode_kernel(const AttnArg
                           : a.partials + (2 * kAttnMaxCtas + cta * C::NW + warp) * (int64_t)C::SLOT, lane);
       }
       f = f_next;
-      at = nx;
-      r = rn;
+      if (f < w1) {
+        next_item(at);
+        r = request(at.b);
+      }
     }
   }
   __syncthreads();
@@ -947,16 +965,32 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_decode_kernel(const AttnArg
     const int to = ((hi < t1 ? hi : t1) - t0 + part - 1) / part;
     const int mlx = C::F4 + x / (32 * C::MM) * 32 + (x & 31);
     float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f), ml = make_float4(kNoMax, kNoMax, 0.0f, 0.0f);
-#pragma unroll 4
-    for (int i = w; i < to; ++i) {
-      const bool first = i == w ? which == 0 : seg_b[i][0] >= 0 && seg_lo[i][0] == lo;
-      const float4* slot = reinterpret_cast<const float4*>(
-          first ? a.partials + (2 * kAttnMaxCtas + cta * C::NW + i) * (int64_t)C::SLOT
-                : reinterpret_cast<const float*>(dec_smem + i * ring_bytes));
-      dec_join(o, ml, slot[x], slot[mlx]);
+    // All but the last warp's segment are those warps' last ones, in the rings;
+    // the last warp's, or a single one, may be a first one, in memory.  First
+    // the largest maxima, then the sums.
+    const bool far = to - 1 == w ? which == 0 : seg_b[to - 1][0] >= 0 && seg_lo[to - 1][0] == lo;
+    const int near_to = far ? to - 1 : to;
+    const float4* mem = reinterpret_cast<const float4*>(a.partials + (2 * kAttnMaxCtas + cta * C::NW + to - 1) * (int64_t)C::SLOT);
+    const float4* slots = reinterpret_cast<const float4*>(dec_smem);
+    const int stride = ring_bytes / 16;
+    float4 far_o, far_ml;
+    if (far) {
+      far_o = mem[x];
+      far_ml = mem[mlx];
+      ml.x = far_ml.x;
+      ml.y = far_ml.y;
     }
+#pragma unroll 4
+    for (int i = w; i < near_to; ++i) {
+      const float2 m2 = *reinterpret_cast<const float2*>(slots + i * stride + mlx);
+      ml.x = fmaxf(ml.x, m2.x);
+      ml.y = fmaxf(ml.y, m2.y);
+    }
+#pragma unroll 4
+    for (int i = w; i < near_to; ++i) dec_join(o, ml, slots[i * stride + x], slots[i * stride + mlx]);
+    if (far) dec_join(o, ml, far_o, far_ml);
     if (lo >= t0 && hi <= t1) {
-      const DecReq rq = dec_request(a, seg_b[w][which], C::ROWS, unused);
+      const DecReq rq = request(seg_b[w][which]);
       dec_write_part<C>(a, rq, seg_h[w][which], x, o, ml);
     } else {
       float4* slot = reinterpret_cast<float4*>(a.partials + (2 * cta + (lo > t0 ? 1 : 0)) * (int64_t)C::SLOT);
@@ -970,38 +1004,81 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_decode_kernel(const AttnArg
   // part of and the one that its last is part of.  Where the threads are more
   // than a result's float4s, each group of threads adds some of the CTAs.
   constexpr int PAR = C::THREADS > C::F4 ? C::THREADS / C::F4 : 1;
+  // (One thread arrives for the CTA: the barrier orders the others' writes
+  // before its fence.)
+  auto crossing = [&](int side, Place& p, DecReq& rq, int& lo) {
+    const int ref = side == 0 ? t0 : t1 - 1;
+    p = find(ref);
+    rq = request(p.b);
+    lo = ref - p.u;
+    const int hi = lo + rq.units;
+    // (not an item that lies in the CTA, or whose cost alone reaches into it,
+    // or that side 0 has seen)
+    return !((lo >= t0 && hi <= t1) || hi <= t0 || (side == 1 && lo <= t0));
+  };
+  __syncthreads();
+  if (tid < 2) {
+    Place p;
+    DecReq rq;
+    int lo;
+    bool last = false;
+    if (crossing(tid, p, rq, lo)) {
+      const int c0 = lo / chunk, c1 = (lo + rq.units - 1) / chunk;
+      __threadfence();
+      last = atomicAdd(&a.counters[c0], 1u) == (uint32_t)(c1 - c0);
+      if (last) {
+        a.counters[c0] = 0;
+        __threadfence();
+        cross_s[tid] = Cross{c0, c1, lo - c0 * chunk, p.h, rq};
+      }
+    }
+    last_s[tid] = last;
+  }
+  __syncthreads();
 #pragma unroll 1
   for (int side = 0; side < 2; ++side) {
-    const int ref = side == 0 ? t0 : t1 - 1;
-    const Place p = find(ref);
-    const DecReq rq = dec_request(a, p.b, C::ROWS, unused);
-    const int lo = ref - p.u, hi = lo + rq.units;
-    // (not an item that lies in the CTA, or whose cost alone reaches into it)
-    if ((lo >= t0 && hi <= t1) || hi <= t0 || (side == 1 && lo <= t0)) continue;
-    const int c0 = lo / chunk, c1 = (hi - 1) / chunk;
-    __threadfence();
-    __syncthreads();
-    if (tid == 0) {
-      const uint32_t before = atomicAdd(&a.counters[c0], 1u);
-      last_s = before == (uint32_t)(c1 - c0);
-      if (last_s) a.counters[c0] = 0;
-    }
-    __syncthreads();
-    if (!last_s) continue;
-    __threadfence();
+    if (!last_s[side]) continue;
+    __syncthreads();  // (side 0's shares are read)
+    const Cross cr = cross_s[side];
+    const int c0 = cr.c0, c1 = cr.c1;
+    const DecReq rq = cr.r;
     float4* share = reinterpret_cast<float4*>(dec_smem);  // [PAR][F4][2], PAR * F4 <= THREADS
 #pragma unroll 1
     for (int x = tid % C::F4, k = tid / C::F4; x < C::F4 && k < PAR; x += C::THREADS) {
       const int mlx = C::F4 + x / (32 * C::MM) * 32 + (x & 31);
       float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f), ml = make_float4(kNoMax, kNoMax, 0.0f, 0.0f);
-#pragma unroll 4
-      for (int i = c0 + k; i <= c1; i += PAR) {
-        const float4* slot = reinterpret_cast<const float4*>(
-            a.partials + (2 * i + (lo > i * chunk ? 1 : 0)) * (int64_t)C::SLOT);
-        dec_join(o, ml, __ldcg(slot + x), __ldcg(slot + mlx));
+      // eight at once, as their latency is what this costs
+#pragma unroll 1
+      for (int i0 = c0 + k; i0 <= c1; i0 += 8 * PAR) {
+        float4 o2[8], ml2[8];
+#pragma unroll
+        for (int y = 0; y < 8; ++y) {
+          const int i = i0 + y * PAR;
+          ml2[y] = make_float4(kNoMax, kNoMax, 0.0f, 0.0f);
+          o2[y] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+          if (i <= c1) {
+            // (the second of a CTA's two slots only where the item began within it)
+            const float4* slot = reinterpret_cast<const float4*>(
+                a.partials + (2 * i + (i == c0 && cr.into > 0 ? 1 : 0)) * (int64_t)C::SLOT);
+            ml2[y] = __ldcg(slot + mlx);
+            o2[y] = __ldcg(slot + x);
+          }
+        }
+        const float4 old = ml;
+#pragma unroll
+        for (int y = 0; y < 8; ++y) {
+          ml.x = fmaxf(ml.x, ml2[y].x);
+          ml.y = fmaxf(ml.y, ml2[y].y);
+        }
+        const float4 o1 = o;
+        o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        ml.z = ml.w = 0.0f;
+        dec_join(o, ml, o1, old);
+#pragma unroll
+        for (int y = 0; y < 8; ++y) dec_join(o, ml, o2[y], ml2[y]);
       }
       if (PAR == 1) {
-        dec_write_part<C>(a, rq, p.h, x, o, ml);
+        dec_write_part<C>(a, rq, cr.h, x, o, ml);
       } else {
         share[(k * C::F4 + x) * 2] = o;
         share[(k * C::F4 + x) * 2 + 1] = ml;
@@ -1010,11 +1087,17 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_decode_kernel(const AttnArg
     if (PAR > 1) {
       __syncthreads();
       if (tid < C::F4) {
-        float4 o = share[tid * 2], ml = share[tid * 2 + 1];
+        float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f), ml = make_float4(kNoMax, kNoMax, 0.0f, 0.0f);
 #pragma unroll
-        for (int k = 1; k < PAR; ++k)
+        for (int k = 0; k < PAR; ++k) {
+          const float4 m2 = share[(k * C::F4 + tid) * 2 + 1];
+          ml.x = fmaxf(ml.x, m2.x);
+          ml.y = fmaxf(ml.y, m2.y);
+        }
+#pragma unroll
+        for (int k = 0; k < PAR; ++k)
           dec_join(o, ml, share[(k * C::F4 + tid) * 2], share[(k * C::F4 + tid) * 2 + 1]);
-        dec_write_part<C>(a, rq, p.h, tid, o, ml);
+        dec_write_part<C>(a, rq, cr.h, tid, o, ml);
       }
     }
   }

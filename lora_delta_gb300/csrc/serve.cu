@@ -129,14 +129,15 @@ template <class C>
 int launch_decode(const AttnArgs& a, cudaStream_t stream) {
   // as many units in flight as shared memory holds
   int stages = C::MAX_STAGES;
-  while (stages > C::MIN_STAGES && C::smem(a.B, stages) > kAttnMaxSmem) --stages;
-  static_assert(C::smem(kAttnMaxReqs, C::MIN_STAGES) <= kAttnMaxSmem, "a CTA's shared memory");
-  const int smem = (int)C::smem(a.B, stages);
+  while (stages > C::MIN_STAGES && C::smem(a.B, stages, false) > kAttnMaxSmem) --stages;
+  static_assert(C::smem(kAttnMaxReqs, C::MIN_STAGES, false) <= kAttnMaxSmem, "a CTA's shared memory");
+  const int cached = C::smem(a.B, stages, true) <= kAttnMaxSmem;
+  const int smem = (int)C::smem(a.B, stages, cached != 0);
   if (prepare_kernel(kv4_decode_kernel<C>, smem, false) != cudaSuccess) return LORA_ERR_CUDA;
   int ctas = sm_count();
   if (ctas > kAttnMaxCtas) ctas = kAttnMaxCtas;
   static const int alone = env_int("LORA_ATTN_ALONE", 64);
-  return launch_after(kv4_decode_kernel<C>, (unsigned)ctas, C::THREADS, (size_t)smem, stream, a, stages, alone);
+  return launch_after(kv4_decode_kernel<C>, (unsigned)ctas, C::THREADS, (size_t)smem, stream, a, stages, cached, alone);
 }
 
 template <class C>
