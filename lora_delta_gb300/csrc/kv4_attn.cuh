@@ -579,24 +579,207 @@ __device__ __forceinline__ void dec_unit(const AttnArgs& a, const DecReq& r, Dec
 // lies inside a warp's part it is written; what crosses parts is joined over
 // the CTA's warps, and over CTAs by the last of them to arrive, in the order of
 // the units (so results do not depend on the order of events).
-constexpr int kItemCost = 2;
+constexpr int kItemCost = 3;
+
+// A place in the work: request, head, unit (up to units + kItemCost).
+struct DecPlace {
+  int b, h, u;
+};
+__device__ __forceinline__ DecPlace dec_find(const AttnArgs& a, const int32_t* pre, int f) {
+  int lo = 0, hi = a.B;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (pre[mid] * a.heads <= f) lo = mid; else hi = mid;
+  }
+  const int cost = pre[lo + 1] - pre[lo], rest = f - pre[lo] * a.heads, h = rest / cost;
+  return DecPlace{lo, h, rest - h * cost};
+}
+
+struct DecCross {  // an item that crosses CTAs: the first and last, its place in the first
+  int c0, c1, into, h;
+  DecReq r;
+};
+template <class C>
+struct DecShared {
+  // segments of items that cross the warps' parts: [0] the warp's first, [1]
+  // its last (b -1: none), and the items' first and last + 1 unit
+  int seg_b[C::NW][2], seg_h[C::NW][2], seg_lo[C::NW][2], seg_hi[C::NW][2];
+  int chain_s[2 * C::NW], chains_s, last_s[2];
+  DecCross cross_s[2];
+};
+
+// The end of a CTA: its warps' and the CTAs' parts of items put together.  Of
+// its own, so that its registers do not weigh on the units' loop.
+template <class C>
+__device__ __noinline__ void dec_join_all(const AttnArgs& a, DecShared<C>& sh, uint8_t* dec_smem, int ring_bytes,
+                                          const int32_t* starts, const int32_t* seqs, const int32_t* pre, int t0,
+                                          int t1, int part, int chunk) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, cta = blockIdx.x;
+  uint32_t unused = 0;
+  auto request = [&](int b) { return dec_request(a, starts[b], starts[b + 1], seqs[b], C::ROWS, unused); };
+  // Joining in the CTA.  An item's segments are those of adjacent warps; its
+  // first one here stands for it: warp w's, where the item began in w's part
+  // or before the CTA's range.
+  if (warp == 0) {
+    const int w = lane >> 1, which = lane & 1;
+    const bool head = w < C::NW && sh.seg_b[w][which] >= 0 && (sh.seg_lo[w][which] >= t0 + w * part || w == 0);
+    const uint32_t heads = __ballot_sync(0xffffffffu, head);
+    if (head) sh.chain_s[__popc(heads & ((1u << lane) - 1u))] = lane;
+    if (lane == 0) sh.chains_s = __popc(heads);
+  }
+  __syncthreads();
+  for (int y = tid; y < sh.chains_s * C::F4; y += C::THREADS) {
+    const int x = y % C::F4, w = sh.chain_s[y / C::F4] >> 1, which = sh.chain_s[y / C::F4] & 1;
+    const int lo = sh.seg_lo[w][which], hi = sh.seg_hi[w][which];
+    const int to = ((hi < t1 ? hi : t1) - t0 + part - 1) / part;
+    const int mlx = C::F4 + x / (32 * C::MM) * 32 + (x & 31);
+    float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f), ml = make_float4(kNoMax, kNoMax, 0.0f, 0.0f);
+    // All but the last warp's segment are those warps' last ones, in the rings;
+    // the last warp's, or a single one, may be a first one, in memory.  First
+    // the largest maxima, then the sums.
+    const bool far = to - 1 == w ? which == 0 : sh.seg_b[to - 1][0] >= 0 && sh.seg_lo[to - 1][0] == lo;
+    const int near_to = far ? to - 1 : to;
+    const float4* mem = reinterpret_cast<const float4*>(a.partials + (2 * kAttnMaxCtas + cta * C::NW + to - 1) * (int64_t)C::SLOT);
+    const float4* slots = reinterpret_cast<const float4*>(dec_smem);
+    const int stride = ring_bytes / 16;
+    float4 far_o, far_ml;
+    if (far) {
+      far_o = mem[x];
+      far_ml = mem[mlx];
+      ml.x = far_ml.x;
+      ml.y = far_ml.y;
+    }
+#pragma unroll 4
+    for (int i = w; i < near_to; ++i) {
+      const float2 m2 = *reinterpret_cast<const float2*>(slots + i * stride + mlx);
+      ml.x = fmaxf(ml.x, m2.x);
+      ml.y = fmaxf(ml.y, m2.y);
+    }
+#pragma unroll 4
+    for (int i = w; i < near_to; ++i) dec_join(o, ml, slots[i * stride + x], slots[i * stride + mlx]);
+    if (far) dec_join(o, ml, far_o, far_ml);
+    if (lo >= t0 && hi <= t1) {
+      const DecReq rq = request(sh.seg_b[w][which]);
+      dec_write_part<C>(a, rq, sh.seg_h[w][which], x, o, ml);
+    } else {
+      float4* slot = reinterpret_cast<float4*>(a.partials + (2 * cta + (lo > t0 ? 1 : 0)) * (int64_t)C::SLOT);
+      slot[x] = o;
+      if (x / 32 % C::MM == 0) slot[mlx] = ml;
+    }
+  }
+  if (chunk == 0) return;
+
+  // Joining over CTAs: at most two items, the one that the CTA's first unit is
+  // part of and the one that its last is part of.  Where the threads are more
+  // than a result's float4s, each group of threads adds some of the CTAs.
+  constexpr int PAR = C::THREADS > C::F4 ? C::THREADS / C::F4 : 1;
+  // (One thread arrives for the CTA: the barrier orders the others' writes
+  // before its fence.)
+  auto crossing = [&](int side, DecPlace& p, DecReq& rq, int& lo) {
+    const int ref = side == 0 ? t0 : t1 - 1;
+    p = dec_find(a, pre, ref);
+    rq = request(p.b);
+    lo = ref - p.u;
+    const int hi = lo + rq.units;
+    // (not an item that lies in the CTA, or whose cost alone reaches into it,
+    // or that side 0 has seen)
+    return !((lo >= t0 && hi <= t1) || hi <= t0 || (side == 1 && lo <= t0));
+  };
+  __syncthreads();
+  if (tid < 2) {
+    DecPlace p;
+    DecReq rq;
+    int lo;
+    bool last = false;
+    if (crossing(tid, p, rq, lo)) {
+      const int c0 = lo / chunk, c1 = (lo + rq.units - 1) / chunk;
+      __threadfence();
+      last = atomicAdd(&a.counters[c0], 1u) == (uint32_t)(c1 - c0);
+      if (last) {
+        a.counters[c0] = 0;
+        __threadfence();
+        sh.cross_s[tid] = DecCross{c0, c1, lo - c0 * chunk, p.h, rq};
+      }
+    }
+    sh.last_s[tid] = last;
+  }
+  __syncthreads();
+#pragma unroll 1
+  for (int side = 0; side < 2; ++side) {
+    if (!sh.last_s[side]) continue;
+    __syncthreads();  // (side 0's shares are read)
+    const DecCross cr = sh.cross_s[side];
+    const int c0 = cr.c0, c1 = cr.c1;
+    const DecReq rq = cr.r;
+    float4* share = reinterpret_cast<float4*>(dec_smem);  // [PAR][F4][2], PAR * F4 <= THREADS
+#pragma unroll 1
+    for (int x = tid % C::F4, k = tid / C::F4; x < C::F4 && k < PAR; x += C::THREADS) {
+      const int mlx = C::F4 + x / (32 * C::MM) * 32 + (x & 31);
+      float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f), ml = make_float4(kNoMax, kNoMax, 0.0f, 0.0f);
+      // eight at once, as their latency is what this costs
+#pragma unroll 1
+      for (int i0 = c0 + k; i0 <= c1; i0 += 8 * PAR) {
+        float4 o2[8], ml2[8];
+#pragma unroll
+        for (int y = 0; y < 8; ++y) {
+          const int i = i0 + y * PAR;
+          ml2[y] = make_float4(kNoMax, kNoMax, 0.0f, 0.0f);
+          o2[y] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+          if (i <= c1) {
+            // (the second of a CTA's two slots only where the item began within it)
+            const float4* slot = reinterpret_cast<const float4*>(
+                a.partials + (2 * i + (i == c0 && cr.into > 0 ? 1 : 0)) * (int64_t)C::SLOT);
+            ml2[y] = __ldcg(slot + mlx);
+            o2[y] = __ldcg(slot + x);
+          }
+        }
+        const float4 old = ml;
+#pragma unroll
+        for (int y = 0; y < 8; ++y) {
+          ml.x = fmaxf(ml.x, ml2[y].x);
+          ml.y = fmaxf(ml.y, ml2[y].y);
+        }
+        const float4 o1 = o;
+        o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        ml.z = ml.w = 0.0f;
+        dec_join(o, ml, o1, old);
+#pragma unroll
+        for (int y = 0; y < 8; ++y) dec_join(o, ml, o2[y], ml2[y]);
+      }
+      if (PAR == 1) {
+        dec_write_part<C>(a, rq, cr.h, x, o, ml);
+      } else {
+        share[(k * C::F4 + x) * 2] = o;
+        share[(k * C::F4 + x) * 2 + 1] = ml;
+      }
+    }
+    if (PAR > 1) {
+      __syncthreads();
+      if (tid < C::F4) {
+        float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f), ml = make_float4(kNoMax, kNoMax, 0.0f, 0.0f);
+#pragma unroll
+        for (int k = 0; k < PAR; ++k) {
+          const float4 m2 = share[(k * C::F4 + tid) * 2 + 1];
+          ml.x = fmaxf(ml.x, m2.x);
+          ml.y = fmaxf(ml.y, m2.y);
+        }
+#pragma unroll
+        for (int k = 0; k < PAR; ++k)
+          dec_join(o, ml, share[(k * C::F4 + tid) * 2], share[(k * C::F4 + tid) * 2 + 1]);
+        dec_write_part<C>(a, rq, cr.h, tid, o, ml);
+      }
+    }
+  }
+}
 
 template <class C>
-__global__ void __launch_bounds__(C::THREADS, 1) kv4_decode_kernel(const AttnArgs a, int stages,
+__global__ void __launch_bounds__(C::THREADS, 1) kv4_decode_kernel(const __grid_constant__ AttnArgs a, int stages,
                                                                    int cached, int min_units) {
   extern __shared__ __align__(128) uint8_t dec_smem[];
   __shared__ uint64_t bars[C::NW][C::MAX_STAGES];
   __shared__ int scan_s[C::NW];
-  __shared__ int max_s, over_s, last_s[2], chains_s;
-  // segments of items that cross the warps' parts: [0] the warp's first, [1]
-  // its last (b -1: none), and the items' first and last + 1 unit
-  __shared__ int seg_b[C::NW][2], seg_h[C::NW][2], seg_lo[C::NW][2], seg_hi[C::NW][2];
-  __shared__ int chain_s[2 * C::NW];
-  struct Cross {  // an item that crosses CTAs: the first and last, its place in the first
-    int c0, c1, into, h;
-    DecReq r;
-  };
-  __shared__ Cross cross_s[2];
+  __shared__ int max_s, over_s;
+  __shared__ DecShared<C> sh;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, c = lane & 3;
   const int ring_bytes = stages * 2 * C::TILE;
   uint8_t* ring = dec_smem + warp * ring_bytes;
@@ -610,7 +793,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_decode_kernel(const AttnArg
   const int32_t* const seqs = cached ? copy + a.B + 1 : a.seq_len;
 
   if (lane < stages) mbar_init(&bars[warp][lane], 1);
-  if (lane < 2) seg_b[warp][lane] = -1;
+  if (lane < 2) sh.seg_b[warp][lane] = -1;
   if (tid == 0) max_s = over_s = 0;
   fence_barrier_init();
   // (what the kernel before wrote is read from here on)
@@ -704,20 +887,8 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_decode_kernel(const AttnArg
   const int w0 = t0 + warp * part < t1 ? t0 + warp * part : t1;
   const int w1 = w0 + part < t1 ? w0 + part : t1;
 
-  // a place in the work: request, head, unit (up to units + kItemCost)
-  struct Place {
-    int b, h, u;
-  };
-  auto find = [&](int f) {
-    int lo = 0, hi = a.B;
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (pre[mid] * a.heads <= f) lo = mid; else hi = mid;
-    }
-    const int cost = pre[lo + 1] - pre[lo], rest = f - pre[lo] * a.heads, h = rest / cost;
-    return Place{lo, h, rest - h * cost};
-  };
-  auto next_item = [&](Place& p) {  // (there is one)
+  auto find = [&](int f) { return dec_find(a, pre, f); };
+  auto next_item = [&](DecPlace& p) {  // (there is one)
     p.u = 0;
     if (++p.h < a.heads) return;
     p.h = 0;
@@ -728,7 +899,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_decode_kernel(const AttnArg
   auto request = [&](int b) { return dec_request(a, starts[b], starts[b + 1], seqs[b], C::ROWS, unused); };
   DecState<C> st;
   int f = w0;
-  Place at = {0, 0, 0};
+  DecPlace at = {0, 0, 0};
   DecReq r = {};
   if (f < w1) {
     at = find(f);
@@ -754,7 +925,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_decode_kernel(const AttnArg
     };
     fetch_q(r, at.h);
     // the producer's place; the addresses of its next 32 tiles, one a lane
-    Place pp = at;
+    DecPlace pp = at;
     DecReq pr = r;
     int pf = f, pblk = 0;
     const uint8_t* src = nullptr;
@@ -884,7 +1055,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_decode_kernel(const AttnArg
       // the item after this one
       const int f_next = item1 + kItemCost;
       if (f_next < w1) {
-        Place nx = at;
+        DecPlace nx = at;
         next_item(nx);
         fetch_q(request(nx.b), nx.h);
       }
@@ -931,10 +1102,10 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_decode_kernel(const AttnArg
         // is still in use; its last to the ring, which has served
         const bool last = f_next >= w1;
         if (lane == 0) {
-          seg_b[warp][last] = at.b;
-          seg_h[warp][last] = at.h;
-          seg_lo[warp][last] = item0;
-          seg_hi[warp][last] = item1;
+          sh.seg_b[warp][last] = at.b;
+          sh.seg_h[warp][last] = at.h;
+          sh.seg_lo[warp][last] = item0;
+          sh.seg_hi[warp][last] = item1;
         }
         dec_save(st, last ? reinterpret_cast<float*>(ring)
                           : a.partials + (2 * kAttnMaxCtas + cta * C::NW + warp) * (int64_t)C::SLOT, lane);
@@ -948,159 +1119,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_decode_kernel(const AttnArg
   }
   __syncthreads();
 
-  // Joining in the CTA.  An item's segments are those of adjacent warps; its
-  // first one here stands for it: warp w's, where the item began in w's part
-  // or before the CTA's range.
-  if (warp == 0) {
-    const int w = lane >> 1, which = lane & 1;
-    const bool head = w < C::NW && seg_b[w][which] >= 0 && (seg_lo[w][which] >= t0 + w * part || w == 0);
-    const uint32_t heads = __ballot_sync(0xffffffffu, head);
-    if (head) chain_s[__popc(heads & ((1u << lane) - 1u))] = lane;
-    if (lane == 0) chains_s = __popc(heads);
-  }
-  __syncthreads();
-  for (int y = tid; y < chains_s * C::F4; y += C::THREADS) {
-    const int x = y % C::F4, w = chain_s[y / C::F4] >> 1, which = chain_s[y / C::F4] & 1;
-    const int lo = seg_lo[w][which], hi = seg_hi[w][which];
-    const int to = ((hi < t1 ? hi : t1) - t0 + part - 1) / part;
-    const int mlx = C::F4 + x / (32 * C::MM) * 32 + (x & 31);
-    float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f), ml = make_float4(kNoMax, kNoMax, 0.0f, 0.0f);
-    // All but the last warp's segment are those warps' last ones, in the rings;
-    // the last warp's, or a single one, may be a first one, in memory.  First
-    // the largest maxima, then the sums.
-    const bool far = to - 1 == w ? which == 0 : seg_b[to - 1][0] >= 0 && seg_lo[to - 1][0] == lo;
-    const int near_to = far ? to - 1 : to;
-    const float4* mem = reinterpret_cast<const float4*>(a.partials + (2 * kAttnMaxCtas + cta * C::NW + to - 1) * (int64_t)C::SLOT);
-    const float4* slots = reinterpret_cast<const float4*>(dec_smem);
-    const int stride = ring_bytes / 16;
-    float4 far_o, far_ml;
-    if (far) {
-      far_o = mem[x];
-      far_ml = mem[mlx];
-      ml.x = far_ml.x;
-      ml.y = far_ml.y;
-    }
-#pragma unroll 4
-    for (int i = w; i < near_to; ++i) {
-      const float2 m2 = *reinterpret_cast<const float2*>(slots + i * stride + mlx);
-      ml.x = fmaxf(ml.x, m2.x);
-      ml.y = fmaxf(ml.y, m2.y);
-    }
-#pragma unroll 4
-    for (int i = w; i < near_to; ++i) dec_join(o, ml, slots[i * stride + x], slots[i * stride + mlx]);
-    if (far) dec_join(o, ml, far_o, far_ml);
-    if (lo >= t0 && hi <= t1) {
-      const DecReq rq = request(seg_b[w][which]);
-      dec_write_part<C>(a, rq, seg_h[w][which], x, o, ml);
-    } else {
-      float4* slot = reinterpret_cast<float4*>(a.partials + (2 * cta + (lo > t0 ? 1 : 0)) * (int64_t)C::SLOT);
-      slot[x] = o;
-      if (x / 32 % C::MM == 0) slot[mlx] = ml;
-    }
-  }
-  if (chunk == 0) return;
-
-  // Joining over CTAs: at most two items, the one that the CTA's first unit is
-  // part of and the one that its last is part of.  Where the threads are more
-  // than a result's float4s, each group of threads adds some of the CTAs.
-  constexpr int PAR = C::THREADS > C::F4 ? C::THREADS / C::F4 : 1;
-  // (One thread arrives for the CTA: the barrier orders the others' writes
-  // before its fence.)
-  auto crossing = [&](int side, Place& p, DecReq& rq, int& lo) {
-    const int ref = side == 0 ? t0 : t1 - 1;
-    p = find(ref);
-    rq = request(p.b);
-    lo = ref - p.u;
-    const int hi = lo + rq.units;
-    // (not an item that lies in the CTA, or whose cost alone reaches into it,
-    // or that side 0 has seen)
-    return !((lo >= t0 && hi <= t1) || hi <= t0 || (side == 1 && lo <= t0));
-  };
-  __syncthreads();
-  if (tid < 2) {
-    Place p;
-    DecReq rq;
-    int lo;
-    bool last = false;
-    if (crossing(tid, p, rq, lo)) {
-      const int c0 = lo / chunk, c1 = (lo + rq.units - 1) / chunk;
-      __threadfence();
-      last = atomicAdd(&a.counters[c0], 1u) == (uint32_t)(c1 - c0);
-      if (last) {
-        a.counters[c0] = 0;
-        __threadfence();
-        cross_s[tid] = Cross{c0, c1, lo - c0 * chunk, p.h, rq};
-      }
-    }
-    last_s[tid] = last;
-  }
-  __syncthreads();
-#pragma unroll 1
-  for (int side = 0; side < 2; ++side) {
-    if (!last_s[side]) continue;
-    __syncthreads();  // (side 0's shares are read)
-    const Cross cr = cross_s[side];
-    const int c0 = cr.c0, c1 = cr.c1;
-    const DecReq rq = cr.r;
-    float4* share = reinterpret_cast<float4*>(dec_smem);  // [PAR][F4][2], PAR * F4 <= THREADS
-#pragma unroll 1
-    for (int x = tid % C::F4, k = tid / C::F4; x < C::F4 && k < PAR; x += C::THREADS) {
-      const int mlx = C::F4 + x / (32 * C::MM) * 32 + (x & 31);
-      float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f), ml = make_float4(kNoMax, kNoMax, 0.0f, 0.0f);
-      // eight at once, as their latency is what this costs
-#pragma unroll 1
-      for (int i0 = c0 + k; i0 <= c1; i0 += 8 * PAR) {
-        float4 o2[8], ml2[8];
-#pragma unroll
-        for (int y = 0; y < 8; ++y) {
-          const int i = i0 + y * PAR;
-          ml2[y] = make_float4(kNoMax, kNoMax, 0.0f, 0.0f);
-          o2[y] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-          if (i <= c1) {
-            // (the second of a CTA's two slots only where the item began within it)
-            const float4* slot = reinterpret_cast<const float4*>(
-                a.partials + (2 * i + (i == c0 && cr.into > 0 ? 1 : 0)) * (int64_t)C::SLOT);
-            ml2[y] = __ldcg(slot + mlx);
-            o2[y] = __ldcg(slot + x);
-          }
-        }
-        const float4 old = ml;
-#pragma unroll
-        for (int y = 0; y < 8; ++y) {
-          ml.x = fmaxf(ml.x, ml2[y].x);
-          ml.y = fmaxf(ml.y, ml2[y].y);
-        }
-        const float4 o1 = o;
-        o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        ml.z = ml.w = 0.0f;
-        dec_join(o, ml, o1, old);
-#pragma unroll
-        for (int y = 0; y < 8; ++y) dec_join(o, ml, o2[y], ml2[y]);
-      }
-      if (PAR == 1) {
-        dec_write_part<C>(a, rq, cr.h, x, o, ml);
-      } else {
-        share[(k * C::F4 + x) * 2] = o;
-        share[(k * C::F4 + x) * 2 + 1] = ml;
-      }
-    }
-    if (PAR > 1) {
-      __syncthreads();
-      if (tid < C::F4) {
-        float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f), ml = make_float4(kNoMax, kNoMax, 0.0f, 0.0f);
-#pragma unroll
-        for (int k = 0; k < PAR; ++k) {
-          const float4 m2 = share[(k * C::F4 + tid) * 2 + 1];
-          ml.x = fmaxf(ml.x, m2.x);
-          ml.y = fmaxf(ml.y, m2.y);
-        }
-#pragma unroll
-        for (int k = 0; k < PAR; ++k)
-          dec_join(o, ml, share[(k * C::F4 + tid) * 2], share[(k * C::F4 + tid) * 2 + 1]);
-        dec_write_part<C>(a, rq, cr.h, tid, o, ml);
-      }
-    }
-  }
+  dec_join_all<C>(a, sh, dec_smem, ring_bytes, starts, seqs, pre, t0, t1, part, chunk);
 }
 
 }  // namespace lora

@@ -570,3 +570,73 @@ def test_binding_refuses_wrong_tensors(ld):
         ld.lora_kv4_attention(q.cpu(), q, cache, table, one, one[:1], 1)
     with pytest.raises(ValueError):
         ld.lora_kv4_attention(q, q, cache, table.long(), one, one[:1], 1)
+
+
+@gpu
+@pytest.mark.parametrize("lens", [DECODE, [(3000, 1), (10, 1)], CHUNKS], ids=["decode", "split", "chunks"])
+def test_attention_that_gives_up_waiting_reports_it_and_leaves_all_usable(ld, lens):
+    """With a wait limit of 0 a wait gives up at its first poll that finds its phase incomplete: the call
+    sets the time-out bit (or no poll did, and the result is right), and the workspace and the device
+    serve the next call as before."""
+    rng = np.random.default_rng(23)
+    c = attention_case(rng, lens, 128, 2, 4, 16, torch.bfloat16)
+    ws = ld.lora_kv4_attention_workspace()
+    want = run_attention(ld, c, workspace=ws)[0]
+    prev = ld.lora_set_wait_limit_ns(0)
+    try:
+        out, _, err = run_attention(ld, c, workspace=ws)
+    finally:
+        ld.lora_set_wait_limit_ns(prev)
+    assert err == 8 or (err == 0 and torch.equal(out, want))
+    torch.cuda.synchronize()
+    assert not ws[:int(ld.lib().lora_kv4_attention_zeroed_bytes())].any()
+    for _ in range(2):
+        out, _, err = run_attention(ld, c, workspace=ws)
+        assert err == 0 and torch.equal(out, want)
+
+
+@gpu
+def test_example_steps_match_the_plain_forms(ld, oracle):
+    """The example's steps: plan, projections with adapters, store and attention together."""
+    from examples.serve_step import D, HIDDEN, KV_HEADS, PAGE, Q_HEADS, WIDTHS, Server
+    slots = [0, 2, -1, 1, 1]
+    server = Server(slots, max_tokens=128, num_pages=40)
+    cache = server.cache
+    cache.pages.zero_()
+    pages = host(cache.pages)
+    g = torch.Generator(device="cuda").manual_seed(5)
+    A, Bm = [[t.double().cpu().numpy() for t in x] for x in (server.pool.A, server.pool.B)]
+    scale = server.pool.scale_table.double().cpu().numpy()
+    table, free, count, ctx = host(server.table), host(server.free), 40, np.zeros(5, int)
+    for new in ([37, 5, 64, 1, 0], [1, 1, 1, 1, 1], [1, 3, 1, 0, 2]):
+        n, new = sum(new) + 2, np.array(new)  # two padding rows
+        x = torch.randn(n, HIDDEN, device="cuda", generator=g).bfloat16()
+        out, plan, qkv = server.step(x, dev(new), int(new.max()))
+        want = ref.plan(ctx, new, slots, n, PAGE, table, table.shape[1], free, count)
+        assert want["err"] == 0
+        table, count, ctx = want["table"], want["left"], want["seq_len"]
+        for name in ("row_req", "position", "slot_map", "seq_slot", "seq_len", "row_start"):
+            assert np.array_equal(host(getattr(plan, name)), want[name]), name
+        assert np.array_equal(host(server.table), table) and int(server.free_count[0]) == count
+        # the delta on the rows' adapters
+        base = (x @ server.weight).double().cpu().numpy()
+        xs, s = x.double().cpu().numpy(), want["seq_slot"]
+        at = 0
+        for j, w in enumerate(WIDTHS):
+            for i in np.nonzero(s >= 0)[0]:
+                base[i, at:at + w] += scale[s[i]] * (xs[i] @ A[j][s[i]].T) @ Bm[j][s[i]].T
+            at += w
+        got = qkv.double().cpu().numpy()
+        assert (np.abs(got - base) <= 2.0 ** -7 * np.abs(base) + 2.0 ** -7).all()
+        # what was stored, from the projections as they are
+        k, v = (got[:, a:a + KV_HEADS * D].reshape(n, KV_HEADS, D) for a in (WIDTHS[0], WIDTHS[0] + WIDTHS[1]))
+        ref.append(pages, k, v, want["slot_map"], PAGE)
+        assert np.array_equal(host(cache.pages), pages)
+        q = got[:, :WIDTHS[0]].reshape(n, Q_HEADS, D)
+        exact, _, big, err = ref.attend(q, pages, PAGE, table, want["row_start"], want["seq_len"], D ** -0.5, 0)
+        off = np.abs(out.double().cpu().numpy() - exact)
+        assert err == 0 and (off <= 2.0 ** -8 * np.abs(exact) + 2.0 ** -9 * big[..., None]).all()
+    server.release(dev([1, 0, 1, 0, 0]))
+    freed = ref.release([1, 0, 1, 0, 0], ctx, PAGE, table, table.shape[1], free, count)
+    assert np.array_equal(host(server.table), freed[0]) and int(server.free_count[0]) == freed[2]
+    assert ld.lora_get_error(server.err) == 0
