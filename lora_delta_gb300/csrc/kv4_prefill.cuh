@@ -166,7 +166,7 @@ template <class C>
 __global__ void __launch_bounds__(C::THREADS, 1) kv4_prefill_kernel(const AttnArgs a, int min_rows) {
   extern __shared__ uint8_t pre_smem_raw[];
   __shared__ uint64_t raw_full[2], raw_empty[2], kv_full[C::KVB], kv_empty[C::KVB];
-  __shared__ uint64_t q_full[2], s_full[2], p_full[2], pv_done[2], size_full[C::SIZES], size_empty[C::SIZES], turn[2], drain_bar[2];
+  __shared__ uint64_t q_full[2], s_full[2], p_full[2], pv_done[2], size_full[C::SIZES], size_empty[C::SIZES], drain_bar;
   __shared__ float size_s[C::SIZES][C::G];         // of some items: the mean |scale q_g|^2 of some rows
   __shared__ int exp_s[C::SOFT_WARPS][32];         // of q's rows: 2^e <= the largest |q|
   __shared__ uint32_t taddr_s;
@@ -190,16 +190,15 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_prefill_kernel(const AttnAr
       mbar_init(&s_full[i], 1);
       mbar_init(&p_full[i], 4);
       mbar_init(&pv_done[i], 1);
-      mbar_init(&turn[i], 1);
-      mbar_init(&drain_bar[i], 1);
     }
+    mbar_init(&drain_bar, 1);
     for (int i = 0; i < C::SIZES; ++i) {
       mbar_init(&size_full[i], 1);
       mbar_init(&size_empty[i], C::EXP_WARPS);
     }
     for (int i = 0; i < C::KVB; ++i) {
       mbar_init(&kv_full[i], C::EXP_WARPS);
-      mbar_init(&kv_empty[i], C::MT);
+      mbar_init(&kv_empty[i], 1);
     }
     fence_barrier_init();
   }
@@ -328,23 +327,21 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_prefill_kernel(const AttnAr
     // (the copies still in flight write to this CTA's memory)
     for (uint32_t k = n >= 2 ? n - 2 : 0; k < n; ++k)
       if (!mbar_wait_soon(&raw_full[k & 1], (k >> 1) & 1, kWaitLimitNs)) ok = false;
-  } else if (warp < C::MMA_WARP + C::MT) {
+  } else if (warp == C::MMA_WARP) {
     // ------------------------------------------------------------------- MMA
     // The warp runs whole, so that descriptors stay in uniform registers; one
     // lane is elected at each product and commit.
-    const int m = warp - C::MMA_WARP;  // the row half
     const uint32_t id_qk = tc::idesc_f16_f32(128, C::NKV), id_pv = tc::idesc_f16_f32(128, C::D);
-    const uint32_t t_s = tmem + m * 128, t_o = tmem + kO + m * 128;
     // (start addresses are in 16-byte units in a descriptor's low bits, and no
     // sum below carries out of them)
-    const uint64_t q_desc = tc::sw128_desc(smem_addr(q_s) + m * 128 * C::D * 2), kv_desc = tc::sw128_desc(smem_addr(kv_s));
-    uint32_t k = 0, k_ph = 0, n = 0;         // place and parity of the next operand; tiles so far
-    uint32_t n_it = 0, n_t = 0, n_turn = 0;  // items, tiles and turns of this half
+    const uint64_t q_desc = tc::sw128_desc(smem_addr(q_s)), kv_desc = tc::sw128_desc(smem_addr(kv_s));
+    uint32_t k = 0, k_ph = 0, n = 0;  // place and parity of the next operand; tiles so far
+    uint32_t q_ph = 0, p_ph = 0;      // a bit a half: parities of q_full and p_full
     auto wait = [&](uint64_t* bar, uint32_t parity) {
-      ok = __all_sync(0xffffffffu, mbar_wait_soon(bar, parity, a.wait_ns));
+      if (ok) ok = __all_sync(0xffffffffu, mbar_wait_soon(bar, parity, a.wait_ns));
     };
     auto take = [&]() -> uint32_t {  // waits for the next operand and returns its place
-      if (ok) wait(&kv_full[k], k_ph);
+      wait(&kv_full[k], k_ph);
       const uint32_t x = k;
       k = k + 1 == C::KVB ? 0 : k + 1;
       k_ph ^= k == 0;
@@ -355,72 +352,61 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_prefill_kernel(const AttnAr
     };
     for (int round = 0, i; (i = pre_nth(round)) < items && ok; ++round) {
       const PreItem it = pre_item<C>(a, pre, i);
-      const bool active = it.rows > m * 128;
-      const bool both = C::MT == 2 && it.rows > 128;
-      // step -1: S of the first tile; step j: O of tile j, S of the next
+      const int mt = it.rows > 128 ? 2 : 1;
+      // step -1: S of the first tile; step j: O of tile j, S of the next.  The
+      // halves take turns, so that one's products run while the other's weights
+      // are computed.
       for (int j = -1; j < it.tiles && ok; ++j) {
         const bool more = j + 1 < it.tiles;
         uint32_t v = 0, x = 0, y = 0;
-        auto take_keys = [&]() {  // the keys in operand x, and y where they are two
-          x = y = take();
-          if (ok && __shfl_sync(0xffffffffu, info_two[(n + (j >= 0)) % C::INFO], 0)) y = take();
-        };
         if (j >= 0) v = take();
-        if (!active) {  // (no product of this half reads them)
-          if (more) take_keys();
-          n += j >= 0;
-          if (ok && lane == 0) {
-            if (j >= 0) mbar_arrive(&kv_empty[v]);
-            if (more) mbar_arrive(&kv_empty[x]);
-            if (y != x) mbar_arrive(&kv_empty[y]);
-          }
-          __syncwarp();
-          continue;
-        }
-        if (ok) {
-          if (j < 0)
-            wait(&q_full[m], n_it++ & 1);
-          else
-            wait(&p_full[m], n_t++ & 1);
-        }
-        // The halves take turns, so that one's products run while the other's
-        // weights are computed: together they would do both in step.
-        if (both) {
-          if (ok && (m == 1 || n_turn > 0)) wait(&turn[m], (n_turn - (m == 0)) & 1);
-          ++n_turn;
-        }
-        if (!ok) break;
-        tc::fence_after_sync();
-        issued = true;
-        if (j >= 0) {
-          const uint64_t vd = kv_desc + (uint64_t)(v * (C::KV / 16));
-#pragma unroll
-          for (int t = 0; t < C::NKV / 16; ++t)
-            if (tc::elect_one())
-              tc::mma_f16_ts(t_o, t_s + t * 8, vd + ((t / 4) * C::D * 128 + (t % 4) * 32) / 16, id_pv, t > 0 || j > 0);
-          commit(&pv_done[m]);
-          commit(&kv_empty[v]);
-        }
-        if (more) {
-          take_keys();
-          if (!ok) break;
 #pragma unroll 1
-          for (uint32_t add = 0, z = x;; add = 1, z = y) {
-            const uint64_t kd = kv_desc + (uint64_t)(z * (C::KV / 16));
-#pragma unroll
-            for (int d = 0; d < C::D / 16; ++d)
-              if (tc::elect_one())
-                tc::mma_bf16(t_s, q_desc + ((d / 4) * 16384 + (d % 4) * 32) / 16,
-                             kd + ((d / 4) * C::NKV * 128 + (d % 4) * 32) / 16, id_qk, d > 0 || add);
-            if (add || x == y) break;
+        for (int m = 0; m < mt; ++m) {
+          const uint32_t t_s = tmem + m * 128, t_o = tmem + kO + m * 128;
+          if (j < 0) {
+            wait(&q_full[m], (q_ph >> m) & 1);
+            q_ph ^= 1u << m;
+          } else {
+            wait(&p_full[m], (p_ph >> m) & 1);
+            p_ph ^= 1u << m;
           }
-          commit(&s_full[m]);
-          commit(&kv_empty[x]);
-          if (y != x) commit(&kv_empty[y]);
+          if (!ok) break;
+          tc::fence_after_sync();
+          issued = true;
+          if (j >= 0) {
+            const uint64_t vd = kv_desc + (uint64_t)(v * (C::KV / 16));
+#pragma unroll
+            for (int t = 0; t < C::NKV / 16; ++t)
+              if (tc::elect_one())
+                tc::mma_f16_ts(t_o, t_s + t * 8, vd + ((t / 4) * C::D * 128 + (t % 4) * 32) / 16, id_pv, t > 0 || j > 0);
+            commit(&pv_done[m]);
+            if (m == mt - 1) commit(&kv_empty[v]);
+          }
+          if (more) {
+            if (m == 0) {  // the keys in operand x, and y where they are two
+              x = y = take();
+              if (ok && __shfl_sync(0xffffffffu, info_two[(n + (j >= 0)) % C::INFO], 0)) y = take();
+              if (!ok) break;
+            }
+            const uint64_t qd = q_desc + (uint64_t)(m * 128 * C::D * 2 / 16);
+#pragma unroll 1
+            for (uint32_t add = 0, z = x;; add = 1, z = y) {
+              const uint64_t kd = kv_desc + (uint64_t)(z * (C::KV / 16));
+#pragma unroll
+              for (int d = 0; d < C::D / 16; ++d)
+                if (tc::elect_one())
+                  tc::mma_bf16(t_s, qd + ((d / 4) * 16384 + (d % 4) * 32) / 16,
+                               kd + ((d / 4) * C::NKV * 128 + (d % 4) * 32) / 16, id_qk, d > 0 || add);
+              if (add || x == y) break;
+            }
+            commit(&s_full[m]);
+            if (m == mt - 1) {
+              commit(&kv_empty[x]);
+              if (y != x) commit(&kv_empty[y]);
+            }
+          }
         }
         n += j >= 0;
-        if (both && lane == 0) mbar_arrive(&turn[m ^ 1]);
-        __syncwarp();
       }
     }
   } else if (warp >= C::EXP_WARP) {
@@ -829,8 +815,8 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_prefill_kernel(const AttnAr
   // After a time-out the products issued last may still run: one more commit of
   // each issuing thread tracks them, and tensor memory is freed after it has arrived.
   if (!__syncthreads_and(ok) && issued && tc::elect_one()) {  // (an MMA warp)
-    tc::mma_commit(&drain_bar[warp - C::MMA_WARP]);
-    mbar_wait_soon(&drain_bar[warp - C::MMA_WARP], 0, kWaitLimitNs);
+    tc::mma_commit(&drain_bar);
+    mbar_wait_soon(&drain_bar, 0, kWaitLimitNs);
   }
   tc::fence_before_sync();
   __syncthreads();
