@@ -7,10 +7,9 @@
 //   load warp       bulk copies of the tile's packed 16-token blocks
 //   8 expand warps  codes to f16 values s c + m in the operands' 128-byte
 //                   swizzled layout, keys [token][dim], values [dim][token]
-//   an MMA warp     a row half: S = Q K^T (128 x 128, in tensor memory), then
-//                   O += P V with P read from tensor memory.  A warp each,
-//                   since the tensor cores idle while an issuing thread waits
-//                   or commits (one thread for both halves: 1.3 times the time)
+//   an MMA warp     for each row half in turn: O += P V with P read from tensor
+//                   memory, then S = Q K^T of the next tile (128 x 128) in its
+//                   place
 //   4 softmax warps a row half: a thread a row; scores to weights in place of
 //                   S, running maximum (followed lazily: O is scaled only when
 //                   a row's maximum grew by 2^8), denominator, the final O / l
@@ -50,8 +49,8 @@ struct Pre {
   static constexpr int Q = ROWS * D * 2;
   static constexpr int INFO = 8;                    // tiles described at once
   static constexpr int SIZES = 4;                   // items measured at once
-  // Warps: MMA 0 (and 1), load 2, then softmax and expand; the first are waited
-  // for most and come first where a scheduler has a choice.
+  // Warps: MMA 0, load 2, then softmax and expand from whole warpgroups on (1 and
+  // 3 only help at the start).
   static constexpr int SOFT_WARPS = 4 * MT, EXP_WARPS = 8;
   static constexpr int MMA_WARP = 0, LOAD_WARP = 2, SOFT_WARP = 4, EXP_WARP = SOFT_WARP + SOFT_WARPS;
   static constexpr int THREADS = (EXP_WARP + EXP_WARPS) * 32;
@@ -242,7 +241,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_prefill_kernel(const AttnAr
   const int items = pre[a.B] * a.heads;
   constexpr uint32_t kO = 256;  // first tensor-memory column of the sums
   bool ok = true;
-  bool issued = false;  // (by an MMA warp)
+  bool issued = false;  // (by the MMA warp)
 
   if (warp == C::LOAD_WARP) {
     // ------------------------------------------------------------------ load
@@ -360,6 +359,11 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_prefill_kernel(const AttnAr
         const bool more = j + 1 < it.tiles;
         uint32_t v = 0, x = 0, y = 0;
         if (j >= 0) v = take();
+        // (operands are waited for ahead of the weights: 573 -> 542 us)
+        if (more) {  // the keys in operand x, and y where they are two
+          x = y = take();
+          if (ok && __shfl_sync(0xffffffffu, info_two[(n + (j >= 0)) % C::INFO], 0)) y = take();
+        }
 #pragma unroll 1
         for (int m = 0; m < mt; ++m) {
           const uint32_t t_s = tmem + m * 128, t_o = tmem + kO + m * 128;
@@ -383,11 +387,6 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_prefill_kernel(const AttnAr
             if (m == mt - 1) commit(&kv_empty[v]);
           }
           if (more) {
-            if (m == 0) {  // the keys in operand x, and y where they are two
-              x = y = take();
-              if (ok && __shfl_sync(0xffffffffu, info_two[(n + (j >= 0)) % C::INFO], 0)) y = take();
-              if (!ok) break;
-            }
             const uint64_t qd = q_desc + (uint64_t)(m * 128 * C::D * 2 / 16);
 #pragma unroll 1
             for (uint32_t add = 0, z = x;; add = 1, z = y) {
@@ -552,14 +551,9 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_prefill_kernel(const AttnAr
           const int tile4 = lane & 3, u = (lane >> 2) & 1, g = 2 * (lane >> 3) + u, h = u ^ odd;
           const uint8_t* tile = raw + (tb * 4 + tile4) * C::RSTRIDE + C::HALF;
           const uint8_t* vp = tile + p * 8 * C::W + h * 4 * C::W + g * (C::W / 2) + x0 * 4;
-          uint32_t w[4][WH];
           __half2 s2[4], m2[4];
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
-            if (WH == 2)
-              *reinterpret_cast<uint2*>(w[c]) = *reinterpret_cast<const uint2*>(vp + c * (C::W / 8));
-            else
-              w[c][0] = *reinterpret_cast<const uint32_t*>(vp + c * (C::W / 8));
             __half2 sm[2];
 #pragma unroll
             for (int e = 0; e < 2; ++e)
@@ -568,15 +562,18 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_prefill_kernel(const AttnAr
             m2[c] = __highs2half2(sm[0], sm[1]);
           }
           uint8_t* to = vb + tb * C::D * 128;
-#pragma unroll
+#pragma unroll 1
           for (int x = 0; x < WH; ++x) {
+            uint32_t w[4];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) w[c] = *reinterpret_cast<const uint32_t*>(vp + c * (C::W / 8) + x * 4);
             const int d0 = gq * 64 + 8 * g + 4 * ((x0 + x) % 2);
 #pragma unroll
             for (int jj = 0; jj < 4; ++jj) {
               uint32_t o[4];
 #pragma unroll
               for (int c = 0; c < 4; ++c) {
-                const uint32_t v = jj >= 2 ? w[c][x] >> 8 : w[c][x];
+                const uint32_t v = jj >= 2 ? w[c] >> 8 : w[c];
                 o[c] = code_value(jj % 2 ? code_hi(v) : code_lo(v), s2[c], m2[c]);
               }
               const int d = d0 + jj;
@@ -682,9 +679,11 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_prefill_kernel(const AttnAr
           if (!(two_blocks & 2u)) s &= 0x0000ffffu;
           return s;
         };
-        // 64 columns at a time: weights by the maximum so far, kept in
-        // registers until their sum shows that none is above 2^15, which f16
-        // holds (64 at the maximum make 2^13); else once more by a new maximum
+        // 32 columns at a time: weights by the maximum so far, kept in registers
+        // until their sum shows that none is above 2^15, which f16 holds (32 at
+        // the maximum make 2^12); else once more by a new maximum.  (64 at a
+        // time, with one wait for more loads but twice the instructions to
+        // fetch: 32 prompts 108.5 us for 105.7, one of 8192 tokens as long.)
         const uint64_t qa2 = f32x2(qa, qa);
         auto scores = [&](int col, float* v) {
           tc::tmem_ld32(t_s + col, v);
@@ -697,37 +696,29 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_prefill_kernel(const AttnAr
           }
         };
 #pragma unroll 1
-        for (int part = 0; part < C::NKV / 64; ++part) {
-          uint32_t w[32];
-          float l0, l1;
+        for (int part = 0; part < C::NKV / 32; ++part) {
+          uint32_t w[16];
+          float v[32], l0, l1;
           for (;;) {
             const float off = 7.0f - m_run;
             const uint64_t off2 = f32x2(off, off);
             uint64_t l2 = f32x2(0.0f, 0.0f);
+            scores(part * 32, v);
 #pragma unroll
-            for (int ch = 0; ch < 2; ++ch) {
-              float v[32];
-              scores(part * 64 + ch * 32, v);
-#pragma unroll
-              for (int x = 0; x < 16; ++x) {
-                float e0, e1;
-                f32x2_split(fma_f32x2(f32x2(v[2 * x], v[2 * x + 1]), qa2, off2), e0, e1);
-                e0 = exp2_fast(e0);
-                e1 = exp2_fast(e1);
-                l2 = add_f32x2(l2, f32x2(e0, e1));
-                w[ch * 16 + x] = half2_bits(e0, e1);
-              }
+            for (int x = 0; x < 16; ++x) {
+              float e0, e1;
+              f32x2_split(fma_f32x2(f32x2(v[2 * x], v[2 * x + 1]), qa2, off2), e0, e1);
+              e0 = exp2_fast(e0);
+              e1 = exp2_fast(e1);
+              l2 = add_f32x2(l2, f32x2(e0, e1));
+              w[x] = half2_bits(e0, e1);
             }
             f32x2_split(l2, l0, l1);
             if (!__any_sync(0xffffffffu, l0 + l1 > 32768.0f)) break;
             float mx = -INFINITY;
-#pragma unroll 1
-            for (int ch = 0; ch < 2; ++ch) {
-              float v[32];
-              scores(part * 64 + ch * 32, v);
+            scores(part * 32, v);
 #pragma unroll
-              for (int x = 0; x < 32; ++x) mx = fmaxf(mx, v[x]);
-            }
+            for (int x = 0; x < 32; ++x) mx = fmaxf(mx, v[x]);
             mx *= qa;
             // the sums so far by 2^(old - new), in O after the product that is
             // under way, and the weights of this tile already written
@@ -737,7 +728,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_prefill_kernel(const AttnAr
             const __half2 keep2 = __float2half2_rn(keep);
             tc::tmem_wait_st();
 #pragma unroll 1
-            for (int x = 0; x < 2 * part; ++x) {
+            for (int x = 0; x < part; ++x) {
               float z[16];
               tc::tmem_ld16(t_s + x * 16, z);
 #pragma unroll
@@ -763,8 +754,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_prefill_kernel(const AttnAr
           }
           if (!ok) break;
           l += l0 + l1;
-          tc::tmem_st16(t_s + part * 32, w);  // (over columns read already)
-          tc::tmem_st16(t_s + part * 32 + 16, w + 16);
+          tc::tmem_st16(t_s + part * 16, w);  // (over columns read already)
         }
         if (!ok) break;
         tc::tmem_wait_st();
@@ -812,9 +802,9 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_prefill_kernel(const AttnAr
     }
   }
   if (!ok) set_error(a.err, LORA_DEV_ERR_TIMEOUT);
-  // After a time-out the products issued last may still run: one more commit of
-  // each issuing thread tracks them, and tensor memory is freed after it has arrived.
-  if (!__syncthreads_and(ok) && issued && tc::elect_one()) {  // (an MMA warp)
+  // After a time-out the products issued last may still run: one more commit
+  // tracks them, and tensor memory is freed after it has arrived.
+  if (!__syncthreads_and(ok) && issued && tc::elect_one()) {
     tc::mma_commit(&drain_bar);
     mbar_wait_soon(&drain_bar, 0, kWaitLimitNs);
   }
