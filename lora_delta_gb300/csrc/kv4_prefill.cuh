@@ -478,9 +478,10 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_prefill_kernel(const AttnAr
           const float c2 = (float)__dp4a(x, x, __dp4a(y, y, 0u)), c1 = (float)__dp4a(x, 0x01010101u, __dp4a(y, 0x01010101u, 0u));
           float sum = fmaf(sm.x, fmaf(sm.x, c2, 2.0f * sm.y * c1), 8.0f * sm.y * sm.y) * size_s[round % C::SIZES][gq];
           if (!((pages >> blk) & 1u) || tok0 + blk * kKvTile + tt >= it.hi) sum = 0.0f;
-#pragma unroll
-          for (int d = 1; d < 32; d <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-          two = sum > 12.0f * 8.0f * 32.0f / C::G;  // (the mean over lanes, G groups)
+          // (the mean over lanes, G groups; summed in units of 2^-4, a lane's part
+          // bounded, and what is not a number counts as large)
+          const uint32_t part = (uint32_t)fminf(sum * 16.0f, 67108864.0f);
+          two = __reduce_add_sync(0xffffffffu, part) > (uint32_t)(16.0f * 12.0f * 8.0f * 32.0f / C::G);
         }
         if (et == 0) info_two[n % C::INFO] = two;
         {
