@@ -49,10 +49,10 @@ struct Pre {
   static constexpr int Q = ROWS * D * 2;
   static constexpr int INFO = 8;                    // tiles described at once
   static constexpr int SIZES = 4;                   // items measured at once
-  // Warps: MMA 0, load 2, then softmax and expand from whole warpgroups on (1 and
-  // 3 only help at the start).
+  // Warps: load 2, MMA 3, then softmax and expand from whole warpgroups on (0 and
+  // 1 only help at the start).
   static constexpr int SOFT_WARPS = 4 * MT, EXP_WARPS = 8;
-  static constexpr int MMA_WARP = 0, LOAD_WARP = 2, SOFT_WARP = 4, EXP_WARP = SOFT_WARP + SOFT_WARPS;
+  static constexpr int MMA_WARP = 3, LOAD_WARP = 2, SOFT_WARP = 4, EXP_WARP = SOFT_WARP + SOFT_WARPS;
   static constexpr int THREADS = (EXP_WARP + EXP_WARPS) * 32;
   // Registers a thread: 20 warps start with 96.  The expand warps give 24 each
   // to the softmax warps (8 x 72 + 8 x 120 = 16 x 96), which hold 32 words of
@@ -431,8 +431,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_prefill_kernel(const AttnAr
       if (!ok) break;
       for (int j = 0; j < it.tiles && ok; ++j, ++n) {
         const int st = n & 1, tok0 = it.kv0 + j * C::NKV;
-        ok = mbar_wait_soon(&raw_full[st], (n >> 1) & 1, a.wait_ns);
-        wait_free();
+        ok = __all_sync(0xffffffffu, mbar_wait_soon(&raw_full[st], (n >> 1) & 1, a.wait_ns));
         if (!ok) break;
         const uint32_t pages = info_pages[n % C::INFO];
         // tiles of which some row does not see some token
@@ -484,6 +483,9 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_prefill_kernel(const AttnAr
           two = __reduce_add_sync(0xffffffffu, part) > (uint32_t)(16.0f * 12.0f * 8.0f * 32.0f / C::G);
         }
         if (et == 0) info_two[n % C::INFO] = two;
+        // (not waited for earlier: the tensor cores' next step waits for these keys)
+        wait_free();
+        if (!ok) break;
         {
           uint8_t* kb = kv_s + (k % C::KVB) * C::KV;
 #pragma unroll
