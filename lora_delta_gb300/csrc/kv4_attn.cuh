@@ -10,8 +10,14 @@
 // laid out with 2^-4 on the dims they meet.  Values: the odd pairs are rows
 // 8-15 of the product, which take 2^-4 at the end.  Scales and least values:
 //   s_t,g sum_d q_d c_d + m_t,g sum_d q_d    per group g of 64 dims (float32)
-//   sum_t (p_t s_t,g) c_t + sum_t p_t m_t,g
-// where the last sum and the denominator sum_t p_t are one more product, with
+//   sum_t (p_t s_t,g) (c_t - 8) + sum_t p_t (m_t,g + 8 s_t,g)
+// Values' codes less 8 (one exact subtraction a register) and least values with
+// 8 s (rounded to f16 once) keep both sums near the result's size: with c and m
+// as they are they grow over a long context and cancel, and what the matrix
+// unit's float32 sums drop of them shows (f16, 60 thousand tokens a warp's part:
+// 1.1e-2 of the result's norm for 5.6e-4; 300 tokens 4.5e-4 for 2.9e-4; the
+// price is 1 to 5% of the time, a product with the constant 8 was dearer).
+// The last sum and the denominator sum_t p_t are one more product, with
 // the m of each group and ones as its rows.  q is brought to f16 by a power of
 // two of its row (exact: 8 or 11 significant bits).  p is 2^6 exp2(s - max)
 // with a running maximum that follows lazily (p <= 2^14), rounded to f16 once;
@@ -20,6 +26,14 @@
 //
 // A warp works on units of two tiles, so that waits, votes and page look-ups
 // are paid once for 32 tokens.
+//
+// Bound: HBM for the cache's bytes, then what surrounds the stream.  bf16, 8
+// heads of 128, 4 query heads each: one context of 131072 tokens 44 us (151 MB,
+// 3.4 TB/s), of which its copies alone take 29 us, the arithmetic that they do
+// not cover 8 us and the joins of the 152 CTAs' parts 7 us; 64 requests of 256 to
+// 8192 tokens 51 us (170 MB, 3.3 TB/s); 256 of 17 to 2048 with 40 heads and as many
+// query heads 150 us (624 MB, 4.1 TB/s, where the instructions of the units' loop
+// count: a matrix product's 8 columns hold one row).
 #pragma once
 
 #include "kv4.cuh"
@@ -28,10 +42,9 @@ namespace lora {
 
 constexpr int kAttnMaxReqs = 4096;
 
-// mbar_wait_bounded for waits that are short and frequent: the global timer,
-// whose reading takes about a microsecond on GB300, is first asked after 64
-// polls (reading it at the first poll that fails cost the prefill kernel a
-// third of its time).
+// mbar_wait_bounded for waits that are short and frequent: the global timer is
+// first asked after 64 polls, and a poll sleeps no longer than the hardware's
+// own limit (sleeps of a microsecond as there: 1% slower prompts).
 __device__ __forceinline__ bool mbar_wait_soon(uint64_t* bar, uint32_t parity, uint64_t limit_ns) {
   if (mbar_try_wait(bar, parity)) return true;
   if (limit_ns == 0) return false;
@@ -105,6 +118,11 @@ __device__ __forceinline__ float exp2_fast(float x) {
 }
 __device__ __forceinline__ uint32_t half2_bits(float lo, float hi) {
   const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+// Two f16 less two others.
+__device__ __forceinline__ uint32_t sub2(uint32_t a, uint32_t b) {
+  const __half2 h = __hsub2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 // 2^e for -126 <= e <= 127.
@@ -452,7 +470,7 @@ __device__ __forceinline__ void dec_unit(const AttnArgs& a, const DecReq& r, Dec
       for (int q = 0; q < C::G; ++q) {
         const uint32_t lo = __byte_perm(x[0][q], x[1][q], 0x5410), hi = __byte_perm(x[0][q], x[1][q], 0x7632);
         vs[t][u][q] = *reinterpret_cast<const __half2*>(&lo);
-        vm[t][u][q] = *reinterpret_cast<const __half2*>(&hi);
+        vm[t][u][q] = __hfma2(vs[t][u][q], __float2half2_rn(8.0f), *reinterpret_cast<const __half2*>(&hi));
       }
     }
   __half2 top2 = vs[0][0][0];
@@ -560,8 +578,8 @@ __device__ __forceinline__ void dec_unit(const AttnArgs& a, const DecReq& r, Dec
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
           const uint32_t x0 = u ? v0[w] >> 8 : v0[w], x1 = u ? v1[w] >> 8 : v1[w];
-          const uint32_t a0 = x0 & 0x000f000fu, a1 = x0 & 0x00f000f0u;
-          const uint32_t a2 = x1 & 0x000f000fu, a3 = x1 & 0x00f000f0u;
+          const uint32_t a0 = sub2(x0 & 0x000f000fu, 0x00080008u), a1 = sub2(x0 & 0x00f000f0u, 0x00800080u);
+          const uint32_t a2 = sub2(x1 & 0x000f000fu, 0x00080008u), a3 = sub2(x1 & 0x00f000f0u, 0x00800080u);
           const int q = (p * C::WD + w) / 2;
 #pragma unroll
           for (int n = 0; n < C::NT; ++n)
@@ -573,7 +591,9 @@ __device__ __forceinline__ void dec_unit(const AttnArgs& a, const DecReq& r, Dec
 
 // The work of all (request, head)s, laid end to end, is shared out evenly: a
 // CTA takes a contiguous range and its warps contiguous parts of that.  An item
-// counts its units and kItemCost more, for what its beginning and end take.  A
+// counts its units and kItemCost more, for what its beginning and end take
+// (with 1, 2, 3, 4: 64 requests 55.1, 51.7, 51, 50.1 us; 256 requests of 40 heads
+// 167, 146, 151, 158).  A
 // warp streams its units through a ring of bulk copies of its own; the next
 // item's q comes by asynchronous copies meanwhile.  Where a (request, head)
 // lies inside a warp's part it is written; what crosses parts is joined over

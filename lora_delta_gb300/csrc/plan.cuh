@@ -83,7 +83,8 @@ __device__ __forceinline__ void block_scan2(int64_t a, int b, int64_t& ex_a, int
 // free_left is free_count itself, the count is stored behind a barrier of one
 // thread-block cluster (`cluster`), after every CTA has read it; else there are
 // CTAs for all rows.
-// Bound: latency (20 bytes a row; three dependent round trips to L2/HBM).
+// Bound: latency (20 bytes a row; three dependent round trips to L2/HBM): 64
+// single tokens 4.7 us, 512 requests with 75 thousand rows 5.9 us.
 __global__ void __launch_bounds__(kPlanThreads) batch_plan_kernel(const PlanArgs a, int cluster) {
   extern __shared__ int32_t plan_smem[];
   int32_t* start_s = plan_smem;           // [B + 1] first row, clipped to n

@@ -136,6 +136,7 @@ int launch_decode(const AttnArgs& a, cudaStream_t stream) {
   if (prepare_kernel(kv4_decode_kernel<C>, smem, false) != cudaSuccess) return LORA_ERR_CUDA;
   int ctas = sm_count();
   if (ctas > kAttnMaxCtas) ctas = kAttnMaxCtas;
+  // items of at most this many units stay whole where there is a CTA for each
   static const int alone = env_int("LORA_ATTN_ALONE", 64);
   return launch_after(kv4_decode_kernel<C>, (unsigned)ctas, C::THREADS, (size_t)smem, stream, a, stages, cached, alone);
 }

@@ -382,6 +382,24 @@ def test_attention_over_long_contexts(ld, lens, H, group, window):
 
 
 @gpu
+def test_attention_sums_of_long_contexts_do_not_drift(ld):
+    """Requests of 8192 tokens, enough of them that a warp sums whole ones.  Three roundings to
+    f16 (a weight, its product with a scale, the result), each of at most 2^-11 / sqrt(3) on the
+    average, make 2^-11 of the result's norm."""
+    rng = np.random.default_rng(21)
+    c, B, part = attention_case(rng, [(8191, 1)], 64, 1, 1, 64, torch.float16), 4096, 64
+    c["table"] = np.repeat(c["table"], B, 0)
+    c["start"], c["seq"] = np.arange(B + 1), np.repeat(c["seq"], B)
+    c["q"] = to_rows(rng.standard_normal((B, 1, 64)), torch.float16)
+    out, _, err = run_attention(ld, c)
+    assert err == 0
+    want = ref.attend(c["q"][:part].double().cpu().numpy(), c["pages"], 64, c["table"][:part], c["start"][:part + 1],
+                      c["seq"][:part], 64 ** -0.5, 0)[0]
+    off = out[:part].double().cpu().numpy() - want
+    assert np.sqrt((off ** 2).sum() / (want ** 2).sum()) <= 2.0 ** -11
+
+
+@gpu
 @pytest.mark.parametrize("B", [300, 4096])
 def test_attention_of_many_requests(ld, B):
     rng = np.random.default_rng(B)
