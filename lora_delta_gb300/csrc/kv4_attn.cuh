@@ -79,7 +79,7 @@ struct AttnArgs {
   float* lse;
   uint32_t* err;
   uint64_t wait_ns;
-  uint32_t* counters;  // [kAttnMaxCtas], zero between calls
+  uint32_t* counters;  // [4 kAttnMaxCtas], zero between calls
   float* partials;     // [kAttnMaxCtas][2] slots, then [kAttnMaxCtas * warps] slots
 };
 

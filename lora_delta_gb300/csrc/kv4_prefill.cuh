@@ -80,6 +80,7 @@ struct PreItem {
   int tok0, rem0;       // the first row's token and place among the heads of its group
   int row0, pos0, seq;  // first row of the batch, its position, visible tokens
   int kv0, lo, hi, tiles;  // first token copied; tokens [lo, hi) are seen by some row
+  int parts;  // of the item, this one among them if sp.part is below
 };
 
 __device__ __forceinline__ int pre_rows(const AttnArgs& a, int b, int min_rows, uint32_t& bad) {
@@ -91,14 +92,25 @@ __device__ __forceinline__ int pre_rows(const AttnArgs& a, int b, int min_rows, 
   return (int)(end - start);
 }
 
+// SPLIT: where items are so few that half the CTAs or more had none, each item's
+// tiles are shared out over `parts` CTAs, whose results the last of them joins (48
+// rows over 65536 tokens: 939 -> 101 us; 512 tokens over 16384: 272 -> 171).  A
+// kernel of its own, since what it adds costs the other 15%.
+struct PreSplit {
+  int parts, part;
+};
+constexpr int kPartTiles = 4;  // tiles of a part, at least (fewer gain less than the join takes)
+
 // A CTA's items: one of each gridDim.x in turn, forwards and backwards
-// alternately, since a prompt's items come by falling work.
-__device__ __forceinline__ int pre_nth(int round) {
+// alternately, since a prompt's items come by falling work; or a part of one.
+template <bool SPLIT>
+__device__ __forceinline__ int pre_nth(const PreSplit& sp, int round) {
+  if (SPLIT && sp.parts > 1) return round == 0 ? blockIdx.x / sp.parts : INT32_MAX;
   return round * gridDim.x + (round & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
 }
 
-template <class C>
-__device__ __forceinline__ PreItem pre_item(const AttnArgs& a, const int32_t* pre, int item) {
+template <class C, bool SPLIT>
+__device__ __forceinline__ PreItem pre_item(const AttnArgs& a, const int32_t* pre, const PreSplit& sp, int item) {
   PreItem it;
   const int total = pre[a.B];
   it.h = item % a.heads;
@@ -125,6 +137,14 @@ __device__ __forceinline__ PreItem pre_item(const AttnArgs& a, const int32_t* pr
   it.kv0 = it.lo / kKvTile * kKvTile;
   // (rows that see nothing keep one tile, all of it masked)
   it.tiles = it.hi > it.kv0 ? (it.hi - it.kv0 + C::NKV - 1) / C::NKV : 1;
+  it.parts = 1;
+  if (SPLIT && sp.parts > 1) {
+    it.parts = it.tiles / kPartTiles;
+    it.parts = it.parts < 1 ? 1 : (it.parts < sp.parts ? it.parts : sp.parts);
+    const int t0 = sp.part * it.tiles / it.parts;
+    it.tiles = (sp.part + 1) * it.tiles / it.parts - t0;
+    it.kv0 += t0 * C::NKV;
+  }
   return it;
 }
 
@@ -170,7 +190,7 @@ __device__ __forceinline__ uint64_t add_f32x2(uint64_t a, uint64_t b) {
   return r;
 }
 
-template <class C>
+template <class C, bool SPLIT>
 __global__ void __launch_bounds__(C::THREADS, 1) kv4_prefill_kernel(const AttnArgs a, int min_rows) {
   extern __shared__ uint8_t pre_smem_raw[];
   __shared__ uint64_t raw_full[2], raw_empty[2], kv_full[C::KVB], kv_empty[C::KVB];
@@ -247,7 +267,13 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_prefill_kernel(const AttnAr
   tc::fence_after_sync();
   if (bad && blockIdx.x == 0) set_error(a.err, bad);
   const uint32_t tmem = taddr_s;
-  const int items = pre[a.B] * a.heads;
+  int items = pre[a.B] * a.heads;
+  PreSplit sp = {1, 0};
+  if (SPLIT && items > 0 && 2 * items <= (int)gridDim.x) {
+    sp.parts = gridDim.x / items;
+    sp.part = blockIdx.x % sp.parts;
+    if ((int)blockIdx.x >= items * sp.parts || sp.part >= pre_item<C, SPLIT>(a, pre, sp, blockIdx.x / sp.parts).parts) items = 0;
+  }
   constexpr uint32_t kO = 256;  // first tensor-memory column of the sums
   bool ok = true;
   bool issued = false;  // (by the MMA warp)
@@ -257,9 +283,9 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_prefill_kernel(const AttnAr
     uint32_t n = 0;  // tiles so far
     // the size of an item's q, from 4 loads of a lane spread over its rows
     auto measure = [&](int round) {
-      const int i = pre_nth(round);
+      const int i = pre_nth<SPLIT>(sp, round);
       if (i >= items) return;
-      const PreItem it = pre_item<C>(a, pre, i);
+      const PreItem it = pre_item<C, SPLIT>(a, pre, sp, i);
       if (round >= C::SIZES)
         ok = __all_sync(0xffffffffu, mbar_wait_soon(&size_empty[round % C::SIZES], (round / C::SIZES - 1) & 1, a.wait_ns));
       if (!ok) return;
@@ -293,8 +319,8 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_prefill_kernel(const AttnAr
       __syncwarp();
       if (lane == 0) mbar_arrive(&size_full[round % C::SIZES]);
     };
-    for (int round = 0, i; (i = pre_nth(round)) < items && ok; ++round) {
-      const PreItem it = pre_item<C>(a, pre, i);
+    for (int round = 0, i; (i = pre_nth<SPLIT>(sp, round)) < items && ok; ++round) {
+      const PreItem it = pre_item<C, SPLIT>(a, pre, sp, i);
       const int32_t* table = a.table + (int64_t)it.b * a.ld_table;
       for (int j = 0; j < it.tiles && ok; ++j, ++n) {
         const int st = n & 1;
@@ -358,8 +384,8 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_prefill_kernel(const AttnAr
     auto commit = [&](uint64_t* bar) {
       if (tc::elect_one()) tc::mma_commit(bar);
     };
-    for (int round = 0, i; (i = pre_nth(round)) < items && ok; ++round) {
-      const PreItem it = pre_item<C>(a, pre, i);
+    for (int round = 0, i; (i = pre_nth<SPLIT>(sp, round)) < items && ok; ++round) {
+      const PreItem it = pre_item<C, SPLIT>(a, pre, sp, i);
       const int mt = it.rows > 128 ? 2 : 1;
       // step -1: S of the first tile; step j: O of tile j, S of the next.  The
       // halves take turns, so that one's products run while the other's weights
@@ -433,8 +459,8 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_prefill_kernel(const AttnAr
       if (lane == 0) mbar_arrive(&kv_full[k % C::KVB]);
       ++k;
     };
-    for (int round = 0, i; (i = pre_nth(round)) < items && ok; ++round) {
-      const PreItem it = pre_item<C>(a, pre, i);
+    for (int round = 0, i; (i = pre_nth<SPLIT>(sp, round)) < items && ok; ++round) {
+      const PreItem it = pre_item<C, SPLIT>(a, pre, sp, i);
       const int pos_lo = it.pos0 + it.tok0, pos_hi = pos_lo + div_group(a, it.rem0 + it.rows - 1);
       ok = __all_sync(0xffffffffu, mbar_wait_soon(&size_full[round % C::SIZES], (round / C::SIZES) & 1, a.wait_ns));
       if (!ok) break;
@@ -613,8 +639,24 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_prefill_kernel(const AttnAr
     auto q_place = [&](int row, int chunk) {
       return reinterpret_cast<uint4*>(q_half + (chunk / 8) * 16384 + row * 128 + (((chunk % 8) ^ (row & 7)) << 4));
     };
-    for (int round = 0, i; (i = pre_nth(round)) < items && ok; ++round) {
-      const PreItem it = pre_item<C>(a, pre, i);
+    // (of a part: to be counted in, whatever happens, so that the count returns to 0)
+    uint32_t* count = nullptr;
+    int parts = 1;
+    [[maybe_unused]] auto arrive = [&]() -> bool {  // whether all the others had
+      bool last = false;
+      if (lane == 0) {
+        last = atomicAdd(count, 1u) == (uint32_t)parts - 1u;
+        if (last) *count = 0;
+      }
+      count = nullptr;
+      return __shfl_sync(0xffffffffu, last, 0);
+    };
+    for (int round = 0, i; (i = pre_nth<SPLIT>(sp, round)) < items && ok; ++round) {
+      const PreItem it = pre_item<C, SPLIT>(a, pre, sp, i);
+      if (SPLIT && it.parts > 1 && m * 128 < it.rows) {
+        parts = it.parts;
+        count = a.counters + i * C::SOFT_WARPS + (warp - C::SOFT_WARP);
+      }
       if (m * 128 >= it.rows) {  // this half sits the item out
         n += it.tiles;
         continue;
@@ -782,13 +824,63 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_prefill_kernel(const AttnAr
       ok = __all_sync(0xffffffffu, mbar_wait_soon(&pv_done[m], (n_t - 1) & 1, a.wait_ns));
       if (!ok) break;
       tc::fence_after_sync();
+      // a part's sums, (m, l) first, four columns of the rows side by side; the
+      // parts' in their order by whoever comes last
+      const float4* from = nullptr;
+      if (SPLIT && it.parts > 1) {
+        constexpr int kSlot = C::ROWS * (1 + C::D / 4);  // float4s
+        float4* slot = reinterpret_cast<float4*>(a.partials) + (int64_t)blockIdx.x * kSlot + m * 128 + r_l;
+        __stcg(slot, make_float4(m_run, l, 0.0f, 0.0f));
+#pragma unroll 1
+        for (int ch = 0; ch < C::D / 16; ++ch) {
+          float v[16];
+          tc::tmem_ld16(t_o + ch * 16, v);
+#pragma unroll
+          for (int x = 0; x < 4; ++x)
+            __stcg(slot + (1 + ch * 4 + x) * C::ROWS, make_float4(v[4 * x], v[4 * x + 1], v[4 * x + 2], v[4 * x + 3]));
+        }
+        __threadfence();
+        __syncwarp();
+        if (!arrive()) {
+          __syncwarp();
+          continue;
+        }
+        __threadfence();
+        from = reinterpret_cast<const float4*>(a.partials) + (int64_t)(blockIdx.x - sp.part) * kSlot + m * 128 + r_l;
+        m_run = kNoMax;
+        for (int s = 0; s < it.parts; ++s) m_run = fmaxf(m_run, __ldcg(from + (int64_t)s * kSlot).x);
+        l = 0.0f;
+        for (int s = 0; s < it.parts; ++s) {
+          const float4 ml = __ldcg(from + (int64_t)s * kSlot);
+          l = fmaf(exp2_fast(ml.x - m_run), ml.y, l);
+        }
+      }
       const float inv = l != 0.0f ? 1.0f / l : 0.0f;
       // the warp's rows through the place of its rows of q, so that a row's
       // bytes are stored by neighbouring lanes
 #pragma unroll 1
       for (int ch = 0; ch < C::D / 32; ++ch) {
         float v[32];
-        tc::tmem_ld32(t_o + ch * 32, v);
+        if (SPLIT && from) {
+          constexpr int kSlot = C::ROWS * (1 + C::D / 4);
+#pragma unroll
+          for (int x = 0; x < 32; ++x) v[x] = 0.0f;
+#pragma unroll 1
+          for (int s = 0; s < it.parts; ++s) {
+            const float4* f = from + (int64_t)s * kSlot;
+            const float w = exp2_fast(__ldcg(f).x - m_run);
+#pragma unroll
+            for (int x = 0; x < 8; ++x) {
+              const float4 z = __ldcg(f + (1 + ch * 8 + x) * C::ROWS);
+              v[4 * x] = fmaf(w, z.x, v[4 * x]);
+              v[4 * x + 1] = fmaf(w, z.y, v[4 * x + 1]);
+              v[4 * x + 2] = fmaf(w, z.z, v[4 * x + 2]);
+              v[4 * x + 3] = fmaf(w, z.w, v[4 * x + 3]);
+            }
+          }
+        } else {
+          tc::tmem_ld32(t_o + ch * 32, v);
+        }
 #pragma unroll
         for (int x = 0; x < 4; ++x)
           *q_place(r_l, ch * 4 + x) =
@@ -812,6 +904,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_prefill_kernel(const AttnAr
             l != 0.0f ? (m_run + log2f(l) - 7.0f) * 0.69314718055994531f : -INFINITY;
       __syncwarp();  // (before the next item's q goes there)
     }
+    if (SPLIT && count) arrive();
   }
   if (!ok) set_error(a.err, LORA_DEV_ERR_TIMEOUT);
   // After a time-out the products issued last may still run: one more commit

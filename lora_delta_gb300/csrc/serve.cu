@@ -141,19 +141,30 @@ int launch_decode(const AttnArgs& a, cudaStream_t stream) {
   return launch_after(kv4_decode_kernel<C>, (unsigned)ctas, C::THREADS, (size_t)smem, stream, a, stages, cached, alone);
 }
 
-template <class C>
-int launch_prefill(const AttnArgs& a, int min_rows, cudaStream_t stream) {
+template <class C, bool SPLIT>
+int launch_prefill_as(const AttnArgs& a, int min_rows, cudaStream_t stream) {
   const int smem = (int)C::smem(a.B);
-  if (prepare_kernel(kv4_prefill_kernel<C>, smem, false) != cudaSuccess) return LORA_ERR_CUDA;
+  if (prepare_kernel(kv4_prefill_kernel<C, SPLIT>, smem, false) != cudaSuccess) return LORA_ERR_CUDA;
   // (the kernel hands registers from warp to warp, out of those that it was
   // built to start with)
   static const bool regs_ok = [] {
     cudaFuncAttributes fa;
-    return cudaFuncGetAttributes(&fa, kv4_prefill_kernel<C>) == cudaSuccess && fa.numRegs >= C::REGS;
+    return cudaFuncGetAttributes(&fa, kv4_prefill_kernel<C, SPLIT>) == cudaSuccess && fa.numRegs >= C::REGS;
   }();
   if (!regs_ok) return LORA_ERR_CUDA;
-  kv4_prefill_kernel<C><<<sm_count(), C::THREADS, smem, stream>>>(a, min_rows);
+  const int ctas = sm_count() < kAttnMaxCtas ? sm_count() : kAttnMaxCtas;
+  kv4_prefill_kernel<C, SPLIT><<<ctas, C::THREADS, smem, stream>>>(a, min_rows);
   return cuda_status(cudaGetLastError());
+}
+
+// Items are split along the tokens where, by the rows of the batch, there are
+// at most half as many as CTAs, and contexts may be long enough for two parts.
+template <class C>
+int launch_prefill(const AttnArgs& a, int min_rows, cudaStream_t stream) {
+  const int64_t rows = (int64_t)a.n * a.group, reqs = rows / (min_rows + 1);
+  const int64_t items = (rows / C::ROWS + (reqs < a.B ? reqs : a.B)) * a.heads;
+  const bool split = 2 * items <= sm_count() && a.cap >= 2 * kPartTiles * C::NKV;
+  return split ? launch_prefill_as<C, true>(a, min_rows, stream) : launch_prefill_as<C, false>(a, min_rows, stream);
 }
 
 // Floats of the partial results of every configuration.
@@ -167,7 +178,11 @@ constexpr size_t kPartialFloats =
               max2(dec_partials<DecCfg<64, true, 4>>(), dec_partials<DecCfg<128, true, 1>>())),
          max2(max2(dec_partials<DecCfg<128, true, 2>>(), dec_partials<DecCfg<128, true, 4>>()),
               max2(dec_partials<DecCfg<256, true, 1>>(), dec_partials<DecCfg<256, true, 2>>())));
-constexpr size_t kCounterBytes = (size_t)kAttnMaxCtas * 4;
+constexpr size_t kCounterBytes = (size_t)kAttnMaxCtas * 16;
+// (a part of a prefill item a CTA; a count for each of 8 warps of at most half as
+// many items)
+static_assert(kPartialFloats >= (size_t)kAttnMaxCtas * 256 * (128 + 4) && kPartialFloats >= (size_t)kAttnMaxCtas * 128 * (256 + 4),
+              "the parts of the prefill kernel's items");
 
 }  // namespace
 
