@@ -382,6 +382,22 @@ def test_attention_over_long_contexts(ld, lens, H, group, window):
 
 
 @gpu
+@pytest.mark.parametrize("D,H,group,dtype,lens,window", [
+    (64, 2, 4, torch.float16, [(5000, 40)], 0), (256, 1, 3, torch.bfloat16, [(3000, 90), (700, 1)], 0),
+    (128, 1, 1, torch.bfloat16, [(2000, 300), (0, 1100), (1500, 33)], 900)])
+def test_attention_of_few_rows_over_long_contexts(ld, D, H, group, dtype, lens, window):
+    """Items that share their tokens out; twice with one workspace, and after a call that gave up."""
+    c = attention_case(np.random.default_rng(D), lens, D, H, group, 32, dtype)
+    first = check_attention(ld, c, window)
+    prev = ld.lora_set_wait_limit_ns(0)
+    try:
+        run_attention(ld, c, window)
+    finally:
+        ld.lora_set_wait_limit_ns(prev)
+    assert torch.equal(first, check_attention(ld, c, window))
+
+
+@gpu
 def test_attention_sums_of_long_contexts_do_not_drift(ld):
     """Requests of 8192 tokens, enough of them that a warp sums whole ones.  Three roundings to
     f16 (a weight, its product with a scale, the result), each of at most 2^-11 / sqrt(3) on the
