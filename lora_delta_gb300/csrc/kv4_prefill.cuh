@@ -24,13 +24,12 @@
 // by a power of two of their row (exact), weights are 2^7 p with p <= 2^8.
 //
 // Bound: the chain of a half's softmax, its two products and the expansion that
-// refills their operands, and the fetch of the roles' instructions (issue slots
-// half full); the tensor cores work a third of the time.  bf16, 8 heads of 128, 4
+// refills their operands; issue slots are 60% full, the tensor cores 40%.  bf16, 8 heads of 128, 4
 // query heads each: one prompt of 8192 tokens 490 us (1120 TFLOP/s), 32 prompts
 // 104 us, chunks behind 16 thousand tokens 253 us (670 TFLOP/s).  Two places of
 // 64 columns of scores a half, so that its softmax need not wait, took 650 us of
-// the first: more roles at once only thin out the fetch; an MMA warp a half, or
-// one each for S and O, no less; four operands in flight 600 us against 575.
+// the first: with more roles at once a third of the warps waited for instructions;
+// an MMA warp a half, or one each for S and O, took no less; four operands in flight 600 us against 575.
 #pragma once
 
 #include "kv4_attn.cuh"
