@@ -31,8 +31,8 @@
 // heads of 128, 4 query heads each: one context of 131072 tokens 44 us (151 MB,
 // 3.4 TB/s), of which its copies alone take 29 us, the arithmetic that they do
 // not cover 8 us and the joins of the 152 CTAs' parts 7 us; 64 requests of 256 to
-// 8192 tokens 51 us (170 MB, 3.3 TB/s); 256 of 17 to 2048 with 40 heads and as many
-// query heads 150 us (624 MB, 4.1 TB/s, where the instructions of the units' loop
+// 8192 tokens 52 us (170 MB, 3.3 TB/s); 256 of 17 to 2048 with 40 heads and as many
+// query heads 159 us (624 MB, 3.9 TB/s, where the instructions of the units' loop
 // count: a matrix product's 8 columns hold one row).
 #pragma once
 
