@@ -73,6 +73,28 @@ struct Pre {
   }
 };
 
+// A row's frame: its weights and their sums are exp2((score - base) qa + off), in
+// log2 units qa score.  base is 0 and off 7 less the row's maximum, as one product
+// and sum a score is least, until the maximum passes 2^12, of which float32 keeps
+// too little; then base is that score itself and off 7, so that its weight is 2^7
+// at any size.  Kept as the largest score of the frame and `off`, which is
+// kNoOffset for a row that takes a base and for one that has seen no token: it makes
+// the common pass overflow, so that such rows take the other.
+constexpr float kNoOffset = 3e38f;
+constexpr float kFarScore = 4096.0f;
+struct PreFrame {
+  float top, off;
+};
+__device__ __forceinline__ float2 frame_terms(const PreFrame& f) {  // (base, off)
+  const bool far = f.off == kNoOffset && f.top > -INFINITY;
+  return make_float2(far ? f.top : 0.0f, far ? 7.0f : f.off);
+}
+// What a weight of frame `from` is in frame `to`.
+__device__ __forceinline__ float frame_ratio(const PreFrame& from, const PreFrame& to, float qa) {
+  const float2 a = frame_terms(from), b = frame_terms(to);
+  return exp2_fast(fmaf(a.x - b.x, qa, b.y - a.y));
+}
+
 // An item: `rows` of the request's (token, head) rows.
 struct PreItem {
   int b, h, rows;
@@ -713,7 +735,8 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_prefill_kernel(const AttnAr
       const int last = it.rows < m * 128 + 128 ? it.rows : m * 128 + 128;
       const int pos_lo = it.pos0 + it.tok0 + div_group(a, it.rem0 + m * 128);
       const int pos_hi = it.pos0 + it.tok0 + div_group(a, it.rem0 + last - 1);
-      float m_run = kNoMax, l = 0.0f;
+      PreFrame fr = {-INFINITY, kNoOffset};
+      float l = 0.0f;
       for (int j = 0; j < it.tiles; ++j, ++n, ++n_t) {
         ok = __all_sync(0xffffffffu, mbar_wait_soon(&s_full[m], n_t & 1, a.wait_ns));
         if (!ok) break;
@@ -734,7 +757,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_prefill_kernel(const AttnAr
         };
         // 32 columns at a time: weights by the maximum so far, kept in registers
         // until their sum shows that none is above 2^15, which f16 holds (32 at
-        // the maximum make 2^12); else once more by a new maximum.  (64 at a
+        // the maximum make 2^12); else once more in a new frame.  (64 at a
         // time, with one wait for more loads but twice the instructions to
         // fetch: 32 prompts 108.5 us for 105.7, one of 8192 tokens as long.)
         const uint64_t qa2 = f32x2(qa, qa);
@@ -752,60 +775,73 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_prefill_kernel(const AttnAr
         for (int part = 0; part < C::NKV / 32; ++part) {
           uint32_t w[16];
           float v[32], l0, l1;
-          for (;;) {
-            const float off = 7.0f - m_run;
-            const uint64_t off2 = f32x2(off, off);
-            uint64_t l2 = f32x2(0.0f, 0.0f);
-            scores(part * 32, v);
+          const uint64_t off2 = f32x2(fr.off, fr.off);
+          uint64_t l2 = f32x2(0.0f, 0.0f);
+          scores(part * 32, v);
 #pragma unroll
-            for (int x = 0; x < 16; ++x) {
-              float e0, e1;
-              f32x2_split(fma_f32x2(f32x2(v[2 * x], v[2 * x + 1]), qa2, off2), e0, e1);
-              e0 = exp2_fast(e0);
-              e1 = exp2_fast(e1);
-              l2 = add_f32x2(l2, f32x2(e0, e1));
-              w[x] = half2_bits(e0, e1);
-            }
-            f32x2_split(l2, l0, l1);
-            if (!__any_sync(0xffffffffu, l0 + l1 > 32768.0f)) break;
+          for (int x = 0; x < 16; ++x) {
+            float e0, e1;
+            f32x2_split(fma_f32x2(f32x2(v[2 * x], v[2 * x + 1]), qa2, off2), e0, e1);
+            e0 = exp2_fast(e0);
+            e1 = exp2_fast(e1);
+            l2 = add_f32x2(l2, f32x2(e0, e1));
+            w[x] = half2_bits(e0, e1);
+          }
+          f32x2_split(l2, l0, l1);
+          if (__any_sync(0xffffffffu, l0 + l1 > 32768.0f)) {
             float mx = -INFINITY;
             scores(part * 32, v);
 #pragma unroll
             for (int x = 0; x < 32; ++x) mx = fmaxf(mx, v[x]);
-            mx *= qa;
-            // the sums so far by 2^(old - new), in O after the product that is
-            // under way, and the weights of this tile already written
-            const float m1 = fmaxf(m_run, mx), keep = exp2_fast(m_run - m1);
-            m_run = m1;
-            l *= keep;
-            const __half2 keep2 = __float2half2_rn(keep);
-            tc::tmem_wait_st();
-#pragma unroll 1
-            for (int x = 0; x < part; ++x) {
-              float z[16];
-              tc::tmem_ld16(t_s + x * 16, z);
-#pragma unroll
-              for (int y = 0; y < 16; ++y) {
-                const __half2 t = __hmul2(*reinterpret_cast<__half2*>(&z[y]), keep2);
-                z[y] = *reinterpret_cast<const float*>(&t);
-              }
-              tc::tmem_st16(t_s + x * 16, reinterpret_cast<const uint32_t*>(z));
+            const PreFrame old = fr;
+            if (mx > fr.top) {
+              fr.top = mx;
+              fr.off = fabsf(mx * qa) > kFarScore ? kNoOffset : 7.0f - mx * qa;
             }
-            if (j > 0) {
-              ok = __all_sync(0xffffffffu, mbar_wait_soon(&pv_done[m], (n_t - 1) & 1, a.wait_ns));
-              if (!ok) break;
-              tc::fence_after_sync();
+            const float keep = frame_ratio(old, fr, qa);
+            if (__any_sync(0xffffffffu, keep != 1.0f)) {
+              // the sums so far by that, in O after the product that is under way,
+              // and the weights of this tile already written
+              l *= keep;
+              const __half2 keep2 = __float2half2_rn(keep);
+              tc::tmem_wait_st();
 #pragma unroll 1
-              for (int x = 0; x < C::D / 16; ++x) {
+              for (int x = 0; x < part; ++x) {
                 float z[16];
-                tc::tmem_ld16(t_o + x * 16, z);
+                tc::tmem_ld16(t_s + x * 16, z);
 #pragma unroll
-                for (int y = 0; y < 16; ++y) z[y] *= keep;
-                tc::tmem_st16(t_o + x * 16, reinterpret_cast<const uint32_t*>(z));
+                for (int y = 0; y < 16; ++y) {
+                  const __half2 t = __hmul2(*reinterpret_cast<__half2*>(&z[y]), keep2);
+                  z[y] = *reinterpret_cast<const float*>(&t);
+                }
+                tc::tmem_st16(t_s + x * 16, reinterpret_cast<const uint32_t*>(z));
               }
+              if (j > 0) {
+                ok = __all_sync(0xffffffffu, mbar_wait_soon(&pv_done[m], (n_t - 1) & 1, a.wait_ns));
+                if (!ok) break;
+                tc::fence_after_sync();
+#pragma unroll 1
+                for (int x = 0; x < C::D / 16; ++x) {
+                  float z[16];
+                  tc::tmem_ld16(t_o + x * 16, z);
+#pragma unroll
+                  for (int y = 0; y < 16; ++y) z[y] *= keep;
+                  tc::tmem_st16(t_o + x * 16, reinterpret_cast<const uint32_t*>(z));
+                }
+              }
+            }
+            // no weight is above 2^8 now
+            const float2 f = frame_terms(fr);
+            scores(part * 32, v);
+            l0 = l1 = 0.0f;
+#pragma unroll
+            for (int x = 0; x < 16; ++x) {
+              const float e0 = exp2_fast(fmaf(v[2 * x] - f.x, qa, f.y)), e1 = exp2_fast(fmaf(v[2 * x + 1] - f.x, qa, f.y));
+              l0 += e0;
+              l1 += e1;
+              w[x] = half2_bits(e0, e1);
             }
           }
-          if (!ok) break;
           l += l0 + l1;
           tc::tmem_st16(t_s + part * 16, w);  // (over columns read already)
         }
@@ -823,13 +859,13 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_prefill_kernel(const AttnAr
       ok = __all_sync(0xffffffffu, mbar_wait_soon(&pv_done[m], (n_t - 1) & 1, a.wait_ns));
       if (!ok) break;
       tc::fence_after_sync();
-      // a part's sums, (m, l) first, four columns of the rows side by side; the
-      // parts' in their order by whoever comes last
+      // a part's sums, its frame and l first, four columns of the rows side by side;
+      // the parts' in their order by whoever comes last
       const float4* from = nullptr;
       if (SPLIT && it.parts > 1) {
         constexpr int kSlot = C::ROWS * (1 + C::D / 4);  // float4s
         float4* slot = reinterpret_cast<float4*>(a.partials) + (int64_t)blockIdx.x * kSlot + m * 128 + r_l;
-        __stcg(slot, make_float4(m_run, l, 0.0f, 0.0f));
+        __stcg(slot, make_float4(fr.top, fr.off, l, 0.0f));
 #pragma unroll 1
         for (int ch = 0; ch < C::D / 16; ++ch) {
           float v[16];
@@ -846,12 +882,14 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_prefill_kernel(const AttnAr
         }
         __threadfence();
         from = reinterpret_cast<const float4*>(a.partials) + (int64_t)(blockIdx.x - sp.part) * kSlot + m * 128 + r_l;
-        m_run = kNoMax;
-        for (int s = 0; s < it.parts; ++s) m_run = fmaxf(m_run, __ldcg(from + (int64_t)s * kSlot).x);
+        for (int s = 0; s < it.parts; ++s) {
+          const float4 f = __ldcg(from + (int64_t)s * kSlot);
+          if (f.x > fr.top) fr = PreFrame{f.x, f.y};
+        }
         l = 0.0f;
         for (int s = 0; s < it.parts; ++s) {
-          const float4 ml = __ldcg(from + (int64_t)s * kSlot);
-          l = fmaf(exp2_fast(ml.x - m_run), ml.y, l);
+          const float4 f = __ldcg(from + (int64_t)s * kSlot);
+          l = fmaf(frame_ratio(PreFrame{f.x, f.y}, fr, qa), f.z, l);
         }
       }
       const float inv = l != 0.0f ? 1.0f / l : 0.0f;
@@ -867,7 +905,8 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_prefill_kernel(const AttnAr
 #pragma unroll 1
           for (int s = 0; s < it.parts; ++s) {
             const float4* f = from + (int64_t)s * kSlot;
-            const float w = exp2_fast(__ldcg(f).x - m_run);
+            const float4 first = __ldcg(f);
+            const float w = frame_ratio(PreFrame{first.x, first.y}, fr, qa);
 #pragma unroll
             for (int x = 0; x < 8; ++x) {
               const float4 z = __ldcg(f + (1 + ch * 8 + x) * C::ROWS);
@@ -898,9 +937,11 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_prefill_kernel(const AttnAr
           *reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(a.out) + (int64_t)(it.row0 + it.tok0 + t) * a.ld_out +
                                     (it.h * a.group + x - t * a.group) * C::D + chunk * 8) = *q_place(row, chunk);
       }
-      if (live && a.lse)
+      if (live && a.lse) {
+        const float2 f = frame_terms(fr);
         a.lse[(int64_t)(it.row0 + it.tok0 + tok) * a.q_heads + head] =
-            l != 0.0f ? (m_run + log2f(l) - 7.0f) * 0.69314718055994531f : -INFINITY;
+            l != 0.0f ? (fmaf(f.x, qa, -f.y) + log2f(l)) * 0.69314718055994531f : -INFINITY;
+      }
       __syncwarp();  // (before the next item's q goes there)
     }
     if (SPLIT && count) arrive();

@@ -1,0 +1,116 @@
+"""Attention over the 4-bit cache where numbers are large, not finite or badly spread, against plain
+64-bit numpy forms.
+
+Tolerance of an output: as in ``tests/test_serve.py``, two roundings of the row type and 2^-9 of the largest
+|v| that the row sees; and what the float32 sum of a score can move.  A score is off by at most
+e = 2^-20 scale sum_d |q_d k_d| (products of up to 22 bits, sums of at most 256 of them in float32, a few
+roundings after them), so weights change by factors of at most exp(2 e), and where 1 - r is the weight of the
+row's largest score (and of tokens with the same key), the result moves by at most
+2 max|v| min(1, r (exp(2 e) - 1)) and the logarithm of the denominator by e.
+"""
+from __future__ import annotations
+
+import numpy as np
+import pytest
+import torch
+
+from tests import serve_ref as ref
+from tests.test_serve import NP_TYPE, attention_case, dev, host, ld, run_attention  # noqa: F401
+
+gpu = pytest.mark.gpu
+
+
+def rows_of(c, b):
+    """Of a request: its rows, the positions they stand at and what its pages hold."""
+    a, e, seq = int(c["start"][b]), int(c["start"][b + 1]), int(c["seq"][b])
+    t = np.arange(seq)
+    page = c["table"][b, t // c["P"]].astype(np.int64)
+    k, v = ref.read(c["pages"], page * c["P"] + t % c["P"], c["P"], c["D"])
+    return a, e, seq - (e - a) + np.arange(e - a), k, v
+
+
+def score_room(c, scale, window=0):
+    """For each row and head [n, Q]: min(1, r (exp(2 e) - 1)), and e."""
+    q = c["q"].double().cpu().numpy()
+    room, off = np.zeros(q.shape[:2]), np.zeros(q.shape[:2])
+    for b in range(len(c["seq"])):
+        a, e, pos, k, _ = rows_of(c, b)
+        t = np.arange(len(k))
+        for h in range(k.shape[1]):
+            g = q.shape[1] // k.shape[1]
+            rows = q[a:e, h * g:(h + 1) * g]
+            s = np.einsum("ngd,td->ngt", rows, k[:, h]) * scale
+            err = 2.0 ** -20 * abs(scale) * np.einsum("ngd,td->ngt", np.abs(rows), np.abs(k[:, h]))
+            seen = (t <= pos[:, None]) & ((t > pos[:, None] - window) if window else True)
+            s = np.where(seen[:, None], s, -np.inf)
+            most = np.where(seen[:, None], err, 0).max(-1)
+            top = s.max(-1, keepdims=True)
+            p = np.exp(s - top)
+            tied = s > top - 1e-10 * np.abs(top)  # (the same key, so the same error)
+            rest = np.where(tied, 0, p).sum(-1) / p.sum(-1)
+            with np.errstate(over="ignore", invalid="ignore"):
+                grown = np.where(rest > 0, np.exp(np.log(np.maximum(rest, 1e-300)) + 2 * most) - rest, 0)
+            room[a:e, h * g:(h + 1) * g], off[a:e, h * g:(h + 1) * g] = np.minimum(1, grown), most
+    return room, off
+
+
+def check_large(ld, c, scale, window=0):  # noqa: F811
+    out, lse, err = run_attention(ld, c, window, scale)
+    want, want_lse, big, _ = ref.attend(c["q"].double().cpu().numpy(), c["pages"], c["P"], c["table"], c["start"],
+                                        c["seq"], scale, window)
+    assert err == 0
+    got, (room, off) = out.double().cpu().numpy(), score_room(c, scale, window)
+    bound = NP_TYPE[c["dtype"]] * np.abs(want) + (2.0 ** -9 + 2 * room[..., None]) * big[..., None]
+    assert np.isfinite(got).all()
+    assert (np.abs(got - want) <= bound).all(), float((np.abs(got - want) - bound).max())
+    got_lse = lse.double().cpu().numpy()
+    assert (np.abs(got_lse - want_lse) <= 2.0 ** -9 + off + 2.0 ** -20 * np.abs(want_lse)).all()
+    return room
+
+
+MANY_ROWS = [(0, 70), (100, 33), (17, 129), (40, 200)]
+# (type, size of q, of k, scale): scores of 2^12 to 2^40
+LARGE = [(torch.bfloat16, 1.0, 1.0, 2.0 ** 12), (torch.bfloat16, 2.0 ** 18, 1000.0, None),
+         (torch.bfloat16, 1.0, 1.0, -2.0 ** 27), (torch.float16, 1.0, 1.0, 2.0 ** 29),
+         (torch.float16, 3000.0, 3000.0, 2.0 ** 17), (torch.bfloat16, 2.0 ** -30, 1.0, 2.0 ** 56)]
+
+
+def large_case(seed, lens, D, group, kind):
+    dtype, q_size, k_size, scale = kind
+    c = attention_case(np.random.default_rng(seed), lens, D, 1, group, 32, dtype, k_std=k_size)
+    c["q"] = (c["q"].float() * q_size).to(dtype)
+    return c, D ** -0.5 if scale is None else scale
+
+
+@gpu
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("kind", LARGE)
+def test_large_scores_of_many_rows(ld, D, kind):  # noqa: F811
+    """The largest score takes all but a few rows whole, at any size."""
+    c, scale = large_case(D, MANY_ROWS, D, 4, kind)
+    room = check_large(ld, c, scale)
+    assert (room < 2.0 ** -9).mean() > 0.75
+    check_large(ld, c, scale, window=40)
+
+
+@gpu
+@pytest.mark.parametrize("kind", LARGE)
+def test_large_scores_of_a_split_item(ld, kind):  # noqa: F811
+    c, scale = large_case(3, [(5000, 40)], 128, 2, kind)
+    check_large(ld, c, scale)
+
+
+@gpu
+@pytest.mark.parametrize("scale", [2.0 ** 5, 2.0 ** 15, 2.0 ** 30])
+def test_equal_large_scores_of_many_rows_share_the_weight(ld, scale):  # noqa: F811
+    """Tokens 16 to 31 have the keys of 0 to 15: a row that sees both gives them the same weights."""
+    c = attention_case(np.random.default_rng(5), [(16, 64), (16, 200)], 128, 1, 4, 32, torch.bfloat16)
+    half = ref.tile_bytes(128) // 2
+    for b in range(2):
+        page = c["pages"][c["table"][b, 0]]
+        page[:, 1, :half] = page[:, 0, :half]
+    c["seq"] = np.array([32, 32])       # rows 16 to 31 of the positions; the rows before them see less
+    c["start"] = np.array([0, 16, 32])
+    c["q"] = c["q"][:32].contiguous()
+    c["max_q"] = 16
+    check_large(ld, c, scale)
