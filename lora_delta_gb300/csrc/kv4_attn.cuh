@@ -94,7 +94,12 @@ __device__ __forceinline__ int page_of_tile(const AttnArgs& a, int tile) {
 }
 
 constexpr int kAttnMaxCtas = 256;
-constexpr float kNoMax = -1e30f;  // running maximum before any token
+constexpr float kNoMax = -3e38f;    // running maximum before any token
+constexpr float kNoOffset = 3e38f;  // and what weights' exponents take for it
+// Maxima (log2) past this are far: of their scores' products with the scale
+// float32 keeps too little, so a row subtracts its largest score before it scales,
+// and that score's weight is the planned one at any size.
+constexpr float kFarScore = 4096.0f;
 
 // d += a(16 x 16, row) * b(16 x 8, col), f16 operands.
 __device__ __forceinline__ void mma_f16(float* c, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
@@ -159,13 +164,15 @@ struct Dec {
 };
 
 // Running state of one (request, head): O^T sums, the sums of p m (lanes of
-// row group g < G) and of p (g == G), and the maxima (log2) of the lane's
-// columns, 2 c and 2 c + 1 of each column tile.
+// row group g < G) and of p (g == G), and what the weights' exponents take, of the
+// lane's columns, 2 c and 2 c + 1 of each column tile: 6 less the maximum (log2), or
+// 6 where the bit of `far` is set and scores are taken less the largest, `thr`.
 template <class C>
 struct DecState {
   float o[C::NT][C::MM][4];
   float z[C::NT][4];
-  float l[C::NT][2], m[C::NT][2];
+  float l[C::NT][2], off[C::NT][2], m[C::NT][2];  // (l and m once finished)
+  uint32_t far;
   int sexp;  // scales are taken as s 2^-sexp
 };
 constexpr int kMinSexp = -14, kMaxSexp = 15;
@@ -180,21 +187,22 @@ __device__ __forceinline__ void dec_reset(DecState<C>& st) {
       for (int j = 0; j < 4; ++j) st.o[n][i][j] = 0.0f;
 #pragma unroll
     for (int j = 0; j < 4; ++j) st.z[n][j] = 0.0f;
-    st.l[n][0] = st.l[n][1] = 0.0f;
-    st.m[n][0] = st.m[n][1] = kNoMax;
+    st.off[n][0] = st.off[n][1] = kNoOffset;
   }
+  st.far = 0;
   st.sexp = kMinSexp;
 }
 
 // The sums of p m and p to every lane; o becomes the sum of p v in float32.
 template <class C>
-__device__ __forceinline__ void dec_finish(DecState<C>& st) {
+__device__ __forceinline__ void dec_finish(DecState<C>& st, const float (&qa)[C::NT][2], const float (&thr)[C::NT][2]) {
   const int c = threadIdx.x & 3;
   const float f0 = pow2i(18 + st.sexp), f1 = f0 * 0.0625f;  // 2^24 for the codes, 2^-6 for p
 #pragma unroll
   for (int n = 0; n < C::NT; ++n)
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
+      st.m[n][e] = (st.far >> (2 * n + e)) & 1u ? thr[n][e] * qa[n][e] : 6.0f - st.off[n][e];
       st.l[n][e] = __shfl_sync(0xffffffffu, st.z[n][e], C::G * 4 + c) * 0.015625f;
 #pragma unroll
       for (int g = 0; g < C::G; ++g) {
@@ -481,10 +489,10 @@ __device__ __forceinline__ void dec_unit(const AttnArgs& a, const DecReq& r, Dec
 #pragma unroll
       for (int q = 0; q < C::G; ++q) top2 = __hmax2(top2, vs[t][u][q]);
   const float stop = __half2float(__hmax(__low2half(top2), __high2half(top2)));
-  up |= stop >= pow2i(st.sexp + 1);
+  up |= stop >= pow2i(st.sexp + 1) || st.far;
 
   // new maxima only where a score is 2^8 above the old one, or a scale 2^1
-  // above its unit
+  // above its unit; and what far maxima take
   if (__any_sync(0xffffffffu, up)) {
     float smax = 0.0f;  // (a scale that is not finite poisons its own rows only)
 #pragma unroll
@@ -510,9 +518,20 @@ __device__ __forceinline__ void dec_unit(const AttnArgs& a, const DecReq& r, Dec
         float top = fmaxf(fmaxf(s[0][n][k], s[0][n][2 + k]), fmaxf(s[1][n][k], s[1][n][2 + k]));
 #pragma unroll
         for (int d = 4; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-        const float m1 = fmaxf(st.m[n][k], top * qa[n][k]), keep = exp2_fast(st.m[n][k] - m1);
-        st.m[n][k] = m1;
-        thr[n][k] = __fdividef(m1 + 8.0f, qa[n][k]);
+        // (the sums move from one base and offset to the other)
+        const uint32_t bit = 1u << (2 * n + k);
+        const bool far0 = st.far & bit;
+        const float base0 = far0 ? thr[n][k] : 0.0f, off0 = st.off[n][k];
+        if (far0) top = fmaxf(top, base0);
+        const float m0 = far0 ? kNoMax : 6.0f - off0, m1 = fmaxf(m0, top * qa[n][k]);
+        const bool far1 = fabsf(m1) > kFarScore && m1 > kNoMax;
+        const float base1 = far1 ? top : 0.0f, off1 = far1 ? 6.0f : m1 > m0 ? 6.0f - m1 : off0;
+        const float keep = exp2_fast(fmaf(base0 - base1, qa[n][k], off1 - off0));
+        st.far = far1 ? st.far | bit : st.far & ~bit;
+        st.off[n][k] = off1;
+        thr[n][k] = far1 ? top : __fdividef(m1 + 8.0f, qa[n][k]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) s[i >> 1][n][2 * (i & 1) + k] -= base1;
         st.z[n][k] *= keep;
         const float ko = keep * fold;
 #pragma unroll
@@ -535,7 +554,7 @@ __device__ __forceinline__ void dec_unit(const AttnArgs& a, const DecReq& r, Dec
         float p[2];
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-          p[k] = exp2_fast(fmaf(s[t][n][2 * u + k], qa[n][k], 6.0f - st.m[n][k]));
+          p[k] = exp2_fast(fmaf(s[t][n][2 * u + k], qa[n][k], st.off[n][k]));
           if (edge && s[t][n][2 * u + k] == -INFINITY) p[k] = 0.0f;
         }
         pt[n][u] = transpose8(half2_bits(p[0], p[1]));
@@ -1114,7 +1133,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_decode_kernel(const __grid_
         issue(stage);
         stage = stage + 1 == stages ? 0 : stage + 1;
       }
-      dec_finish(st);
+      dec_finish(st, qa, thr);
       if (item0 >= w0 && item1 <= w1) {
         dec_write(a, request(at.b), at.h, st, lane);
       } else {

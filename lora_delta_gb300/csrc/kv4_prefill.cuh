@@ -80,8 +80,6 @@ struct Pre {
 // at any size.  Kept as the largest score of the frame and `off`, which is
 // kNoOffset for a row that takes a base and for one that has seen no token: it makes
 // the common pass overflow, so that such rows take the other.
-constexpr float kNoOffset = 3e38f;
-constexpr float kFarScore = 4096.0f;
 struct PreFrame {
   float top, off;
 };

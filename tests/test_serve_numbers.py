@@ -114,3 +114,51 @@ def test_equal_large_scores_of_many_rows_share_the_weight(ld, scale):  # noqa: F
     c["q"] = c["q"][:32].contiguous()
     c["max_q"] = 16
     check_large(ld, c, scale)
+
+
+FEW_ROWS = [(0, 1), (16, 1), (17, 1), (300, 1), (95, 1), (1000, 1)]
+
+
+@gpu
+@pytest.mark.parametrize("D,group", [(64, 1), (64, 20), (128, 4), (128, 16), (256, 5), (256, 16)])
+@pytest.mark.parametrize("kind", LARGE)
+def test_large_scores_of_few_rows(ld, D, group, kind):  # noqa: F811
+    c, scale = large_case(D + group, FEW_ROWS, D, group, kind)
+    check_large(ld, c, scale)
+    check_large(ld, c, scale, window=40)
+
+
+@gpu
+@pytest.mark.parametrize("kind", LARGE)
+def test_large_scores_of_few_rows_over_a_long_context(ld, kind):  # noqa: F811
+    """Parts of many CTAs, each with a largest score of its own."""
+    c, scale = large_case(7, [(9000, 2), (400, 1)], 128, 4, kind)
+    check_large(ld, c, scale)
+
+
+@gpu
+@pytest.mark.parametrize("scale", [2.0 ** 5, 2.0 ** 15, 2.0 ** 30])
+def test_equal_large_scores_of_few_rows_share_the_weight(ld, scale):  # noqa: F811
+    c = attention_case(np.random.default_rng(5), [(31, 1), (40, 1)], 128, 1, 4, 32, torch.bfloat16)
+    half = ref.tile_bytes(128) // 2
+    for b in range(2):
+        page = c["pages"][c["table"][b, 0]]
+        page[:, 1, :half] = page[:, 0, :half]
+    check_large(ld, c, scale)
+
+
+@gpu
+@pytest.mark.parametrize("lens", [FEW_ROWS, MANY_ROWS], ids=["few", "many"])
+def test_scores_grow_and_fall_across_the_limit_along_a_context(ld, lens):  # noqa: F811
+    """Keys that grow from 2^-4 to 2^10 along the tokens, and ones that fall: the largest score moves from
+    ordinary sizes to large ones, and a row's first large one stays."""
+    for flip in (False, True):
+        c = attention_case(np.random.default_rng(9), lens, 128, 1, 4, 32, torch.bfloat16)
+        half = ref.tile_bytes(128) // 2
+        for b, s in enumerate(c["seq"]):
+            size = 2.0 ** np.linspace(-4, 10, s)[::-1 if flip else 1]
+            for t in range(s):
+                pair = c["pages"][c["table"][b, t // 32], 0, t % 32 // 16, 8 * 128:half].view(np.float16).reshape(16, 4)
+                pair[t % 16] = pair[t % 16] * size[t]
+        check_large(ld, c, 16.0)
+        check_large(ld, c, -16.0)
