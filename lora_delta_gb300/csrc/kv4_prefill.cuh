@@ -848,7 +848,12 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_prefill_kernel(const AttnAr
         tc::fence_before_sync();
         __syncwarp();
         if (lane == 0) mbar_arrive(&p_full[m]);
-        if (edge) {
+        // (tokens noted where the tile is an edge of the item, be it one of this
+        // half's rows or not)
+        uint32_t noted = 0;
+#pragma unroll
+        for (int w = 0; w < C::NKV / 32; ++w) noted |= info_bad[n % C::INFO][w];
+        if (noted) {
           for (int w = 0; w < C::NKV / 32; ++w)
             if (info_bad[n % C::INFO][w] & seen32(w * 32)) l = __int_as_float(0x7fffffff);
         }

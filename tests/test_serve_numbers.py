@@ -162,3 +162,44 @@ def test_scores_grow_and_fall_across_the_limit_along_a_context(ld, lens):  # noq
                 pair[t % 16] = pair[t % 16] * size[t]
         check_large(ld, c, 16.0)
         check_large(ld, c, -16.0)
+
+
+def spoil_value(c, b, t, group, fill):
+    """A token's value pair of one group becomes (fill, fill)."""
+    D, half = c["D"], ref.tile_bytes(c["D"]) // 2
+    tile = c["pages"][c["table"][b, t // c["P"]], :, t % c["P"] // 16, half + 8 * D:]
+    pairs = np.ascontiguousarray(tile).view(np.float16).reshape(len(tile), 16, D // 64, 2)
+    pairs[:, t % 16, group] = fill
+    tile[:] = pairs.reshape(len(tile), -1).view(np.uint8)
+
+
+def spoiled(c, places, window, fill):
+    """The case with values that are not finite, which outputs [n, Q, D] see them, and what the rest should be."""
+    q, scale = c["q"].double().cpu().numpy(), c["D"] ** -0.5
+    want, want_lse, big, _ = ref.attend(q, c["pages"], c["P"], c["table"], c["start"], c["seq"], scale, window)
+    hit = np.zeros(want.shape, bool)
+    for b, t, group in places:
+        spoil_value(c, b, t, group, fill)
+        a, e, seq = int(c["start"][b]), int(c["start"][b + 1]), int(c["seq"][b])
+        pos = seq - (e - a) + np.arange(e - a)
+        sees = (t <= pos) & ((t > pos - window) if window else True)
+        hit[a:e, :, 64 * group:64 * (group + 1)] |= sees[:, None, None]
+    return hit, want, want_lse, big
+
+
+@gpu
+@pytest.mark.parametrize("fill", [np.nan, np.inf])
+@pytest.mark.parametrize("D,group,lens,window,places", [
+    (128, 1, [(0, 256)], 0, [(0, 5, 0)]), (64, 1, [(0, 300), (0, 256)], 0, [(0, 130, 0), (1, 100, 0)]),
+    (128, 1, [(0, 256)], 60, [(0, 5, 1), (0, 140, 0)]), (128, 4, [(10, 64), (0, 40)], 0, [(0, 20, 1), (1, 0, 0)]),
+    (256, 2, [(3, 130)], 0, [(0, 40, 3), (0, 70, 1)]), (128, 1, [(3000, 256)], 0, [(0, 2990, 1), (0, 3100, 0), (0, 100, 0)]),
+    (128, 1, [(0, 256)], 130, [(0, 0, 0), (0, 255, 1)])])
+def test_many_rows_that_see_a_value_that_is_not_finite_show_it(ld, D, group, lens, window, places, fill):  # noqa: F811
+    """A tile may be hidden from some rows of one half of an item's rows and seen by all of the other."""
+    c = attention_case(np.random.default_rng(D + window), lens, D, 1, group, 32, torch.bfloat16)
+    hit = spoiled(c, places, window, fill)[0]
+    got = run_attention(ld, c, window)[0].float().cpu().numpy()
+    # (steps and least values that are infinities stand for inf * code + inf, an infinity or a NaN)
+    assert not np.isfinite(got[hit]).any() and (np.isinf(fill) or np.isnan(got[hit]).all())
+    sees = hit.any(-1)
+    assert np.isfinite(got[~sees]).all()
