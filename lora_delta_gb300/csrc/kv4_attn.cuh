@@ -356,24 +356,21 @@ __device__ __forceinline__ void dec_unit(const AttnArgs& a, const DecReq& r, Dec
     return tok <= pos && (a.window <= 0 || tok > pos - a.window);
   };
   if (edge) {
-    // values' scales of tokens that no row sees may hold anything; one that is
-    // not finite is left out here and makes the rows that do see it NaN
+    // values' scales of tokens that no row sees may hold anything; a group's that
+    // is not finite is left out here and makes its dims NaN of rows that do see it
     uint32_t* sp = reinterpret_cast<uint32_t*>(unit + (lane >> 4) * C::TILE + C::HALF + 8 * C::D) + (lane & 15) * C::G;
     const bool any = seen_by_any(lane >> 4, tok0 + lane);
-    bool odd = false;
+#pragma unroll 1
+    for (int q = 0; q < C::G; ++q) {
+      const bool odd = (sp[q] & 0x7c00u) == 0x7c00u || (sp[q] & 0x7c000000u) == 0x7c000000u;
+      if (!any || odd) sp[q] = 0;
+      for (uint32_t lost = __ballot_sync(0xffffffffu, any && odd); lost; lost &= lost - 1)
 #pragma unroll
-    for (int q = 0; q < C::G; ++q)
-      odd |= (sp[q] & 0x7c00u) == 0x7c00u || (sp[q] & 0x7c000000u) == 0x7c000000u;
-    if (!any || odd) {
+        for (int n = 0; n < C::NT; ++n)
 #pragma unroll
-      for (int q = 0; q < C::G; ++q) sp[q] = 0;
+          for (int k = 0; k < 2; ++k)
+            if (g == q && seen_by(tok0 + __ffs(lost) - 1, n * 8 + 2 * c + k)) st.z[n][k] = __int_as_float(0x7fffffff);
     }
-    for (uint32_t lost = __ballot_sync(0xffffffffu, any && odd); lost; lost &= lost - 1)
-#pragma unroll
-      for (int n = 0; n < C::NT; ++n)
-#pragma unroll
-        for (int k = 0; k < 2; ++k)
-          if (seen_by(tok0 + __ffs(lost) - 1, n * 8 + 2 * c + k)) st.z[n][k] = __int_as_float(0x7fffffff);
     fence_proxy_async_smem();  // (the stage is next written by a bulk copy)
     __syncwarp();
   }

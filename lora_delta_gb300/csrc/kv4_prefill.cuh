@@ -219,7 +219,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_prefill_kernel(const AttnAr
   __shared__ uint32_t taddr_s;
   __shared__ uint32_t info_pages[C::INFO];             // blocks of a tile that were copied
   __shared__ uint32_t info_two[C::INFO];               // keys in two operands
-  __shared__ uint32_t info_bad[C::INFO][C::NKV / 32];  // tokens whose values are not finite
+  __shared__ uint32_t info_bad[C::INFO][C::G][C::NKV / 32];  // tokens whose values are not finite, by group
   __shared__ int scan_s[32];
   const int tid = threadIdx.x, lane = tid & 31;
   const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);  // (known to be the same in a warp)
@@ -358,7 +358,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_prefill_kernel(const AttnAr
         const uint32_t got = __ballot_sync(0xffffffffu, page >= 0);
         if (lane == 0) {
           info_pages[n % C::INFO] = got;
-          for (int w = 0; w < C::NKV / 32; ++w) info_bad[n % C::INFO][w] = 0;
+          for (int w = 0; w < C::G * C::NKV / 32; ++w) (&info_bad[n % C::INFO][0][0])[w] = 0;
           if (got)
             mbar_arrive_expect_tx(&raw_full[st], __popc(got) * C::TILE);
           else
@@ -493,8 +493,8 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_prefill_kernel(const AttnAr
                           (a.window > 0 && tok0 <= pos_hi - a.window) || pages != (1u << C::TPK) - 1u;
         uint8_t* raw = raw_s + st * C::RAW;
         if (edge) {
-          // Values' scales of tokens that no row sees may hold anything, and
-          // one that is not finite would reach rows that do not see it: both
+          // Values' scales of tokens that no row sees may hold anything, and a
+          // group's that is not finite would reach rows that do not see it: both
           // are set to 0, the latter noted for the softmax.  (Each warp does it
           // for what it reads, noting before it clears.)
           const int tb = C::NKV == 128 ? (ew >> 1) & 1 : 0;
@@ -502,14 +502,11 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_prefill_kernel(const AttnAr
           for (int t = tb * 64 + lane; t < tb * 64 + 64; t += 32) {
             uint32_t* sp = reinterpret_cast<uint32_t*>(raw + (t / kKvTile) * C::RSTRIDE + C::HALF + 8 * C::D) + (t % kKvTile) * C::G;
             const bool use = ((pages >> (t / kKvTile)) & 1u) && tok0 + t >= it.lo && tok0 + t < it.hi;
-            bool odd = false;
 #pragma unroll
-            for (int q = 0; q < C::G; ++q)
-              odd |= (sp[q] & 0x7c00u) == 0x7c00u || (sp[q] & 0x7c000000u) == 0x7c000000u;
-            if (use && odd) atomicOr(&info_bad[n % C::INFO][t / 32], 1u << (t % 32));
-            if (!use || odd) {
-#pragma unroll
-              for (int q = 0; q < C::G; ++q) sp[q] = 0;
+            for (int q = 0; q < C::G; ++q) {
+              const bool odd = (sp[q] & 0x7c00u) == 0x7c00u || (sp[q] & 0x7c000000u) == 0x7c000000u;
+              if (use && odd) atomicOr(&info_bad[n % C::INFO][q][t / 32], 1u << (t % 32));
+              if (!use || odd) sp[q] = 0;
             }
           }
           fence_proxy_async_smem();  // (the block is next written by a bulk copy)
@@ -735,6 +732,14 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_prefill_kernel(const AttnAr
       const int pos_hi = it.pos0 + it.tok0 + div_group(a, it.rem0 + last - 1);
       PreFrame fr = {-INFINITY, kNoOffset};
       float l = 0.0f;
+      uint32_t lost = 0;  // groups of 64 dims of which the row has seen a value that is not finite
+      auto spoil = [&](auto& v, int group) {
+        if (__any_sync(0xffffffffu, lost)) {
+          const float add = (lost >> group) & 1u ? __int_as_float(0x7fffffff) : 0.0f;
+#pragma unroll
+          for (float& x : v) x += add;
+        }
+      };
       for (int j = 0; j < it.tiles; ++j, ++n, ++n_t) {
         ok = __all_sync(0xffffffffu, mbar_wait_soon(&s_full[m], n_t & 1, a.wait_ns));
         if (!ok) break;
@@ -852,10 +857,10 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_prefill_kernel(const AttnAr
         // half's rows or not)
         uint32_t noted = 0;
 #pragma unroll
-        for (int w = 0; w < C::NKV / 32; ++w) noted |= info_bad[n % C::INFO][w];
+        for (int w = 0; w < C::G * C::NKV / 32; ++w) noted |= (&info_bad[n % C::INFO][0][0])[w];
         if (noted) {
-          for (int w = 0; w < C::NKV / 32; ++w)
-            if (info_bad[n % C::INFO][w] & seen32(w * 32)) l = __int_as_float(0x7fffffff);
+          for (int w = 0; w < C::G * C::NKV / 32; ++w)
+            if ((&info_bad[n % C::INFO][0][0])[w] & seen32(w % (C::NKV / 32) * 32)) lost |= 1u << w / (C::NKV / 32);
         }
       }
       if (!ok) break;
@@ -873,6 +878,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_prefill_kernel(const AttnAr
         for (int ch = 0; ch < C::D / 16; ++ch) {
           float v[16];
           tc::tmem_ld16(t_o + ch * 16, v);
+          spoil(v, ch / 4);
 #pragma unroll
           for (int x = 0; x < 4; ++x)
             __stcg(slot + (1 + ch * 4 + x) * C::ROWS, make_float4(v[4 * x], v[4 * x + 1], v[4 * x + 2], v[4 * x + 3]));
@@ -921,6 +927,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_prefill_kernel(const AttnAr
           }
         } else {
           tc::tmem_ld32(t_o + ch * 32, v);
+          spoil(v, ch / 2);
         }
 #pragma unroll
         for (int x = 0; x < 4; ++x)

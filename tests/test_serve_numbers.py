@@ -203,3 +203,23 @@ def test_many_rows_that_see_a_value_that_is_not_finite_show_it(ld, D, group, len
     assert not np.isfinite(got[hit]).any() and (np.isinf(fill) or np.isnan(got[hit]).all())
     sees = hit.any(-1)
     assert np.isfinite(got[~sees]).all()
+
+
+@gpu
+@pytest.mark.parametrize("D,group,lens,window,places", [
+    (128, 1, [(0, 256)], 60, [(0, 5, 1), (0, 140, 0)]), (128, 4, [(10, 64), (0, 40)], 0, [(0, 20, 1), (1, 0, 0)]),
+    (256, 2, [(3, 130)], 0, [(0, 40, 3), (0, 70, 1)]), (128, 1, [(3000, 256)], 0, [(0, 2990, 1), (0, 3100, 0), (0, 100, 0)]),
+    (128, 4, [(30, 1), (64, 1), (40, 1)], 0, [(0, 29, 0), (1, 3, 1), (2, 40, 1)]), (256, 2, [(50, 8)], 20, [(0, 40, 2), (0, 55, 0)]),
+    (64, 1, [(90, 5)], 0, [(0, 92, 0)]), (128, 8, [(5000, 1)], 0, [(0, 5000, 1), (0, 77, 0)])])
+def test_a_value_that_is_not_finite_shows_in_its_group_only(ld, D, group, lens, window, places):  # noqa: F811
+    """The result's dims of other groups, and the logarithm of the denominator, do not depend on it."""
+    c = attention_case(np.random.default_rng(D + group), lens, D, 1, group, 32, torch.bfloat16)
+    hit, want, want_lse, big = spoiled(c, places, window, np.nan)
+    out, lse, err = run_attention(ld, c, window)
+    assert err == 0
+    got, got_lse = out.double().cpu().numpy(), lse.double().cpu().numpy()
+    assert np.array_equal(np.isnan(got), hit)
+    # (a row's weights are its own, so the rest is as it was before)
+    bound = NP_TYPE[c["dtype"]] * np.abs(want) + 2.0 ** -9 * big[..., None]
+    assert (np.abs(got - want) <= bound)[~hit].all()
+    assert (np.abs(got_lse - want_lse) <= 2.0 ** -9 + 2.0 ** -20 * np.abs(want_lse)).all()
