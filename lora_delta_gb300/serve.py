@@ -190,18 +190,20 @@ def lora_kv4_attention_workspace(device="cuda") -> torch.Tensor:
 
 
 # One workspace per (device, stream) for callers that pass none: calls on one
-# stream run in order and may share it.
+# stream run in order and may share it.  A graph gets its own, since its replays
+# may run on any stream, beside calls on the one that it was captured on.
 _ATTN_WS: dict = {}
 
 
 def _attn_workspace(device, stream, raw):
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return _attn_workspace(device, None, raw)
+    if torch.cuda.is_current_stream_capturing():
+        return lora_kv4_attention_workspace(device)  # zeroed by each replay
     ws = _ATTN_WS.get((device.index, raw))
     if ws is None:
-        with torch.cuda.stream(torch.cuda.current_stream(device) if stream is None else stream):
-            ws = lora_kv4_attention_workspace(device)
-            if torch.cuda.is_current_stream_capturing():
-                return ws  # the graph's own, zeroed by each replay
-        _ATTN_WS[(device.index, raw)] = ws
+        ws = _ATTN_WS[(device.index, raw)] = lora_kv4_attention_workspace(device)
     return ws
 
 
