@@ -445,12 +445,16 @@ int lora_delta_fused_noalloc(void *out, int64_t ld_out, const void *x, int n, in
  *   free_pages, free_count (in), free_left (out): a stack of free pages and its
  *               height; page k of all the step's new pages, in request order,
  *               is free_pages[*free_count - 1 - k], and *free_left is the height
- *               left.  free_left may be free_count.  With a free_left of its own
- *               the call changes nothing that it reads, and can be repeated.
+ *               left.  free_left may be free_count.  With a free_left and a seq_len
+ *               of its own the call changes nothing that it reads, and can be repeated.
  *               All three NULL: the tables hold every page already.
+ *               (In place, of these or of the lengths below, the call runs on at
+ *               most 8 SMs.)
  *   row_start   [n_reqs + 1] int32 (out): request b's rows are row_start[b] ..
  *               row_start[b + 1] - 1.
- *   seq_len     [n_reqs] int32 (out): ctx + new.
+ *   seq_len     [n_reqs] int32 (out): ctx + new.  It may be ctx_len itself, which
+ *               then holds the next step's lengths; no other output may share
+ *               memory with an input (LORA_ERR_ARG).
  *   row_req, position, seq_slot [n_rows] int32, slot_map [n_rows] int64 (out):
  *               the row's request, its token's position, its adapter slot and
  *               its cache slot page * page_size + position % page_size.  Rows

@@ -18,6 +18,11 @@ using namespace lora;
 
 namespace {
 
+// Whether two arrays share bytes (a NULL one has none).
+inline bool overlap(const void* p, size_t np, const void* q, size_t nq) {
+  const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
+  return p && q && np && nq && a < b + nq && b < a + np;
+}
 inline bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 inline bool aligned8(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 7u) == 0; }
 
@@ -207,14 +212,26 @@ int lora_batch_plan(const int32_t* ctx_len, const int32_t* new_len, const int32_
   if (n_reqs > 1 && ld_table < max_pages) return LORA_ERR_SHAPE;
   if (!aligned16(row_req) || !aligned16(position) || !aligned16(slot_map) || !aligned16(seq_slot))
     return LORA_ERR_ALIGN;
+  // the one input that may be replaced is ctx_len, by seq_len
+  const size_t reqs = (size_t)n_reqs * 4, rows = (size_t)n_rows * 4;
+  const struct {
+    const void* p;
+    size_t bytes;
+  } ins[] = {{ctx_len, reqs}, {new_len, reqs}, {req_slot, reqs}, {free_count, 4}},
+    outs[] = {{row_start, reqs + 4}, {seq_len, reqs}, {row_req, rows}, {position, rows}, {seq_slot, rows}, {slot_map, 2 * rows}};
+  for (const auto& in : ins)
+    for (const auto& out : outs)
+      if (overlap(in.p, in.bytes, out.p, out.bytes) && !(in.p == ctx_len && out.p == seq_len && in.p == out.p)) return LORA_ERR_ARG;
+  for (int i = 0; i < 3; ++i)
+    if (overlap(ins[i].p, ins[i].bytes, free_left, 4)) return LORA_ERR_ARG;
   PlanArgs a = {ctx_len,    new_len,   req_slot, n_reqs,   n_rows,   page_size, max_pages,
                 block_table, ld_table, free_pages, free_count, free_left, row_start, seq_len,
                 row_req,    position,  slot_map, seq_slot, err_word};
   const int smem = (int)plan_smem_bytes(n_reqs);
   if (prepare_kernel(batch_plan_kernel, smem, false) != cudaSuccess) return LORA_ERR_CUDA;
   const int64_t per_cta = kPlanThreads * kPlanRowsPerThread;
-  // (one cluster where the free count is replaced in place)
-  const bool cluster = free_left != nullptr && free_left == free_count;
+  // (one cluster where the free count or the lengths are replaced in place)
+  const bool cluster = (free_left != nullptr && free_left == free_count) || (n_reqs > 0 && seq_len == ctx_len);
   const int64_t want = (n_rows + per_cta - 1) / per_cta, most = cluster ? kPlanMaxCluster : sm_count();
   const int ctas = want < 1 ? 1 : (int)(want < most ? want : most);
   cudaLaunchAttribute attr[2];

@@ -94,6 +94,7 @@ def lora_batch_plan(plan: BatchPlan, ctx_len, new_len, block_table, req_slot=Non
                     free_count=None, free_left=None, err=None, stream=None) -> BatchPlan:
     """The step's maps and new pages from the requests' lengths, into ``plan``'s tensors.
 
+    ``ctx_len`` may be ``plan.seq_len``, the lengths that the plan's last step left.
     ``free_pages`` / ``free_count`` [1] are the stack of free pages; the height that is left goes to
     ``free_left`` [1], or back into ``free_count`` where none is given."""
     B = plan.n_reqs

@@ -48,3 +48,61 @@ def test_graphs_do_not_share_a_workspace_with_calls_or_one_another(ld, monkeypat
     torch.cuda.synchronize()
     for out in outs[:3]:
         assert torch.equal(out, want)
+
+
+@gpu
+@pytest.mark.parametrize("B,top,in_place", [(700, 9, False), (700, 9, True), (4096, 3, False), (40, 2, True), (600, 1, False)])
+def test_plan_steps_on_its_own_lengths(ld, B, top, in_place):  # noqa: F811
+    """The lengths that a step leaves are the next one's: the same tensor in and out, with one CTA's rows and more."""
+    from tests import serve_ref as ref
+    rng, P, max_pages = np.random.default_rng(B + top), 16, 6
+    ctx, slots = rng.integers(0, 40, B), rng.integers(-1, 9, B)
+    table = np.full((B, max_pages), -1)
+    order = rng.permutation(B * max_pages)
+    held = -(-ctx // P)
+    at = np.concatenate([[0], np.cumsum(held)])
+    for b in range(B):
+        table[b, :held[b]] = order[at[b]:at[b + 1]]
+    free, count = order[at[-1]:], len(order) - at[-1]
+    n = B * top + 3
+    p, d_table, d_free, d_count = ld.BatchPlan(B, n, P), dev(table), dev(free), dev([count])
+    left = None if in_place else dev([0])
+    p.seq_len.copy_(dev(ctx))
+    for _ in range(3):
+        new, err = rng.integers(0, top + 1, B), ld.new_error_word()
+        want = ref.plan(ctx, new, slots, n, P, table, max_pages, free, count)
+        ld.lora_batch_plan(p, p.seq_len, dev(new), d_table, req_slot=dev(slots), free_pages=d_free, free_count=d_count,
+                           free_left=left, err=err)
+        assert ld.lora_get_error(err) == want["err"] == 0
+        for name in ("row_start", "seq_len", "row_req", "position", "seq_slot", "slot_map"):
+            assert np.array_equal(host(getattr(p, name)), want[name]), name
+        assert np.array_equal(host(d_table), want["table"])
+        ctx, table, count = want["seq_len"], want["table"], want["left"]
+        if not in_place:
+            d_count.copy_(left)
+        assert int(d_count[0]) == count
+
+
+def test_plan_refuses_outputs_that_share_memory_with_inputs():
+    import ctypes
+
+    import lora_delta_gb300 as ld
+    from lora_delta_gb300.build import build
+    build()
+    at = [0x100000 * (i + 1) for i in range(16)]  # never dereferenced: the checks come first
+    names = ["ctx", "new", "slot", "table", "free", "count", "left", "start", "seq", "req", "pos", "map", "aslot"]
+
+    def plan(**kw):
+        p = {**dict(zip(names, at)), **kw}
+        v = {k: ctypes.c_void_p(x) for k, x in p.items()}
+        return ld.lib().lora_batch_plan(v["ctx"], v["new"], v["slot"], 8, 40, 16, v["table"], 4, 4, v["free"], v["count"],
+                                        v["left"], v["start"], v["seq"], v["req"], v["pos"], v["map"], v["aslot"], None, None)
+
+    by = dict(zip(names, at))
+    for name in ("new", "slot", "count"):
+        for out in ("start", "seq", "req", "pos", "map", "aslot"):
+            assert plan(**{out: by[name]}) == 1, (name, out)
+    for out in ("start", "req", "pos", "map", "aslot", "left"):
+        assert plan(**{out: by["ctx"]}) == 1, out
+    assert plan(seq=by["ctx"] + 4) == 1 and plan(seq=by["ctx"] - 28) == 1
+    assert plan(map=by["new"] - 8 * 40 + 16) == 1
