@@ -228,6 +228,8 @@ def lora_kv4_attention(out, q, cache: Kv4Cache, block_table, row_start, seq_len,
     raw = _raw_stream(stream)
     if workspace is None:
         workspace = _attn_workspace(q.device, stream, raw)
+    else:
+        _dev(workspace, "workspace")
     out_at, ld_out = _rows(out, "out", q_heads, cache.head_dim, cache.dtype)
     q_at, ld_q = _rows(q, "q", q_heads, cache.head_dim, cache.dtype)
     table, ld, pages = _table(block_table, B)
@@ -235,4 +237,4 @@ def lora_kv4_attention(out, q, cache: Kv4Cache, block_table, row_start, seq_len,
         out_at, ld_out, q_at, ld_q, n, q_heads, *cache._args, table, ld, pages,
         _i32(row_start, "row_start", B + 1), _i32(seq_len, "seq_len"), B, max_q_len,
         D ** -0.5 if scale is None else scale, window, _at(lse), workspace.data_ptr(),
-        workspace.numel(), _at(err), raw))
+        workspace.numel() * workspace.element_size(), _at(err), raw))

@@ -106,3 +106,18 @@ def test_plan_refuses_outputs_that_share_memory_with_inputs():
         assert plan(**{out: by["ctx"]}) == 1, out
     assert plan(seq=by["ctx"] + 4) == 1 and plan(seq=by["ctx"] - 28) == 1
     assert plan(map=by["new"] - 8 * 40 + 16) == 1
+
+
+@gpu
+def test_attention_refuses_workspaces_that_it_cannot_use(ld):  # noqa: F811
+    c = attention_case(np.random.default_rng(1), [(20, 1)], 64, 1, 2, 16, torch.bfloat16)
+    want = run_attention(ld, c)[0]
+    nbytes = int(ld.lib().lora_kv4_attention_workspace_size())
+    for ws in (torch.zeros(nbytes, dtype=torch.uint8), torch.zeros(nbytes, 2, dtype=torch.uint8, device="cuda")[:, 0]):
+        with pytest.raises(ValueError):
+            run_attention(ld, c, workspace=ws)
+    with pytest.raises(ld.LoraError) as e:
+        run_attention(ld, c, workspace=torch.zeros(nbytes // 4 - 1, dtype=torch.int32, device="cuda"))
+    assert e.value.code == 5
+    # bytes count, not entries
+    assert torch.equal(run_attention(ld, c, workspace=torch.zeros(nbytes // 4 + 1, dtype=torch.int32, device="cuda"))[0], want)
