@@ -36,6 +36,14 @@ def _at(t):
     return None if t is None else t.data_ptr()
 
 
+def _err_at(t):
+    if t is None:
+        return None
+    if not t.is_cuda or t.dtype not in (torch.int32, torch.uint32) or t.numel() < 1:
+        raise ValueError("err must be an int32 CUDA tensor, as new_error_word() makes it")
+    return t.data_ptr()
+
+
 def _raw_stream(stream):
     # (torch.cuda.current_stream() builds a Stream object, a third of a small call's time)
     if stream is None:
@@ -106,7 +114,7 @@ def lora_batch_plan(plan: BatchPlan, ctx_len, new_len, block_table, req_slot=Non
     _check("lora_batch_plan", _fn.lora_batch_plan(
         _i32(ctx_len, "ctx_len", B), _i32(new_len, "new_len", B),
         None if req_slot is None else _i32(req_slot, "req_slot", B), B, plan.n_rows, plan.page_size,
-        table, ld, pages, free, count, left, *plan._out, _at(err), _raw_stream(stream)))
+        table, ld, pages, free, count, left, *plan._out, _err_at(err), _raw_stream(stream)))
     return plan
 
 
@@ -117,7 +125,7 @@ def lora_pages_release(done, seq_len, block_table, page_size: int, free_pages, f
     table, ld, pages = _table(block_table, B)
     _check("lora_pages_release", _fn.lora_pages_release(
         _i32(done, "done"), _i32(seq_len, "seq_len", B), B, int(page_size), table, ld, pages,
-        _i32(free_pages, "free_pages"), free_pages.numel(), _i32(free_count, "free_count", 1), _at(err),
+        _i32(free_pages, "free_pages"), free_pages.numel(), _i32(free_count, "free_count", 1), _err_at(err),
         _raw_stream(stream)))
 
 
@@ -167,7 +175,7 @@ def _store_or_read(name, cache, k, v, slot_map, err, stream):
         raise ValueError(f"slot_map must have {n} entries, got {slot_map.numel()}")
     k_at, ld_k = _rows(k, "k", H, D, cache.dtype)
     v_at, ld_v = _rows(v, "v", H, D, cache.dtype)
-    _check(name, getattr(_fn, name)(*cache._args, k_at, ld_k, v_at, ld_v, slot_map.data_ptr(), n, _at(err),
+    _check(name, getattr(_fn, name)(*cache._args, k_at, ld_k, v_at, ld_v, slot_map.data_ptr(), n, _err_at(err),
                                     _raw_stream(stream)))
 
 
@@ -237,4 +245,4 @@ def lora_kv4_attention(out, q, cache: Kv4Cache, block_table, row_start, seq_len,
         out_at, ld_out, q_at, ld_q, n, q_heads, *cache._args, table, ld, pages,
         _i32(row_start, "row_start", B + 1), _i32(seq_len, "seq_len"), B, max_q_len,
         D ** -0.5 if scale is None else scale, window, _at(lse), workspace.data_ptr(),
-        workspace.numel() * workspace.element_size(), _at(err), raw))
+        workspace.numel() * workspace.element_size(), _err_at(err), raw))

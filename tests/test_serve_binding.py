@@ -121,3 +121,18 @@ def test_attention_refuses_workspaces_that_it_cannot_use(ld):  # noqa: F811
     assert e.value.code == 5
     # bytes count, not entries
     assert torch.equal(run_attention(ld, c, workspace=torch.zeros(nbytes // 4 + 1, dtype=torch.int32, device="cuda"))[0], want)
+
+
+@gpu
+def test_error_words_are_checked(ld):  # noqa: F811
+    c = attention_case(np.random.default_rng(1), [(20, 1)], 64, 1, 2, 16, torch.bfloat16)
+    cache = ld.Kv4Cache(dev(c["pages"], np.uint8), 16, 64)
+    k, slots, one = torch.zeros(1, 1, 64, device="cuda").bfloat16(), torch.zeros(1, dtype=torch.int64, device="cuda"), dev([1])
+    p, table = ld.BatchPlan(1, 1, 16), dev(c["table"])
+    args = c["q"], c["q"], cache, table, dev(c["start"]), dev(c["seq"]), 1
+    for err in (torch.zeros(1, dtype=torch.int32), torch.zeros(1, device="cuda"), torch.zeros(0, dtype=torch.int32, device="cuda")):
+        for call in (lambda: ld.lora_batch_plan(p, one, one, table, err=err), lambda: ld.lora_kv4_append(cache, k, k, slots, err=err),
+                     lambda: ld.lora_kv4_read(cache, k, k, slots, err=err), lambda: ld.lora_kv4_attention(*args, err=err),
+                     lambda: ld.lora_pages_release(one, one, table, 16, one, one, err=err)):
+            with pytest.raises(ValueError):
+                call()
