@@ -81,7 +81,16 @@ def _rows(t, name, heads, head_dim, dtype):
     return t.data_ptr(), ld if t.shape[0] > 1 else heads * head_dim
 
 
-class BatchPlan:
+class _Fixed:
+    """An object whose attributes are set once: it keeps their tensors' addresses."""
+
+    def __setattr__(self, name, value):
+        if name in self.__dict__:
+            raise AttributeError(f"{type(self).__name__}.{name} is fixed: write into it, or make another")
+        super().__setattr__(name, value)
+
+
+class BatchPlan(_Fixed):
     """What ``lora_batch_plan`` writes for a batch of up to ``n_reqs`` requests padded to ``n_rows``
     rows: ``row_start`` [n_reqs + 1], ``seq_len`` [n_reqs], ``row_req``, ``position``, ``seq_slot``
     [n_rows] int32 and ``slot_map`` [n_rows] int64."""
@@ -133,7 +142,7 @@ def lora_kv4_page_bytes(page_size: int, kv_heads: int, head_dim: int) -> int:
     return int(lib().lora_kv4_page_bytes(int(page_size), int(kv_heads), int(head_dim)))
 
 
-class Kv4Cache:
+class Kv4Cache(_Fixed):
     """A key/value cache held in 4 bits.
 
     ``pages`` is its memory, uint8 [num_pages, kv_heads, page_size / 16, tile bytes]; ``dtype``

@@ -136,3 +136,14 @@ def test_error_words_are_checked(ld):  # noqa: F811
                      lambda: ld.lora_pages_release(one, one, table, 16, one, one, err=err)):
             with pytest.raises(ValueError):
                 call()
+
+
+@gpu
+def test_plans_and_caches_keep_the_tensors_that_they_were_made_with(ld):  # noqa: F811
+    """Their addresses are taken once, so a tensor put in another's place would not be written."""
+    p, cache = ld.BatchPlan(2, 4, 16), ld.Kv4Cache.empty(2, 16, 1, 64)
+    for obj, names in ((p, ("row_start", "seq_len", "row_req", "position", "slot_map", "seq_slot", "n_rows", "page_size")),
+                       (cache, ("pages", "page_size", "head_dim", "dtype", "num_pages", "kv_heads"))):
+        for name in names:
+            with pytest.raises(AttributeError):
+                setattr(obj, name, getattr(obj, name))
