@@ -474,6 +474,20 @@ int lora_batch_plan(const int32_t *ctx_len, const int32_t *new_len, const int32_
                     lora_stream_t stream);
 
 /*
+ * lora_batch_plan_bounded -- lora_batch_plan with the number of entries of
+ * free_pages: a *free_count above free_cap counts as free_cap and one below 0 as
+ * 0, with LORA_DEV_ERR_PAGE.  lora_batch_plan takes *free_count as it is, so there
+ * the stack must have that many entries.
+ */
+int lora_batch_plan_bounded(const int32_t *ctx_len, const int32_t *new_len,
+                            const int32_t *req_slot, int n_reqs, int n_rows, int page_size,
+                            int32_t *block_table, int64_t ld_table, int max_pages,
+                            const int32_t *free_pages, int free_cap, const int32_t *free_count,
+                            int32_t *free_left, int32_t *row_start, int32_t *seq_len,
+                            int32_t *row_req, int32_t *position, int64_t *slot_map,
+                            int32_t *seq_slot, uint32_t *err_word, lora_stream_t stream);
+
+/*
  * lora_pages_release -- the pages of finished requests back onto the free
  * stack: for every b with done[b] != 0, the entries >= 0 among its first
  * ceil(seq_len[b] / page_size), in (request, page) order, are stored from

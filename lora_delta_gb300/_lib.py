@@ -55,6 +55,8 @@ SIGNATURES = {
                                       _i, _i, _i, _vp, _vp]),
     "lora_batch_plan": (_i, [_vp, _vp, _vp, _i, _i, _i, _vp, _i64, _i, _vp, _vp, _vp, _vp, _vp,
                              _vp, _vp, _vp, _vp, _vp, _vp]),
+    "lora_batch_plan_bounded": (_i, [_vp, _vp, _vp, _i, _i, _i, _vp, _i64, _i, _vp, _i, _vp, _vp, _vp,
+                                     _vp, _vp, _vp, _vp, _vp, _vp, _vp]),
     "lora_pages_release": (_i, [_vp, _vp, _i, _i, _vp, _i64, _i, _vp, _i, _vp, _vp, _vp]),
     "lora_kv4_page_bytes": (_sz, [_i, _i, _i]),
     "lora_kv4_append": (_i, [_vp, _i64, _i, _i, _i, _i, _vp, _i64, _vp, _i64, _vp, _i, _vp, _vp]),

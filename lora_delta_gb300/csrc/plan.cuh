@@ -20,6 +20,7 @@ struct PlanArgs {
   int32_t* table;
   int64_t ld_table;
   const int32_t* free_pages;  // NULL: the tables hold every page already
+  int free_cap;               // entries of free_pages
   const int32_t* free_count;
   int32_t* free_left;
   int32_t* row_start;
@@ -96,9 +97,10 @@ __global__ void __launch_bounds__(kPlanThreads) batch_plan_kernel(const PlanArgs
   const int rank = blockIdx.x, n_ctas = gridDim.x, P = a.page_size;
   asm volatile("griddepcontrol.wait;" ::: "memory");  // (what the kernel before wrote is read from here on)
   const int64_t cap = (int64_t)a.max_pages * P;
-  const int count = a.free_pages ? *a.free_count : 0;
+  const int told = a.free_pages ? *a.free_count : 0;
+  const int count = told < 0 ? 0 : (told < a.free_cap ? told : a.free_cap);
   if (threadIdx.x == 0) used_s = 0;
-  uint32_t bad = 0;
+  uint32_t bad = a.free_pages && told != count ? LORA_DEV_ERR_PAGE : 0u;
   int64_t carry_rows = 0;
   int carry_pages = 0;
   for (int b0 = 0; b0 < a.B; b0 += kPlanThreads) {

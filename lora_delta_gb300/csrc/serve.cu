@@ -193,13 +193,14 @@ static_assert(kPartialFloats >= (size_t)kAttnMaxCtas * 256 * (128 + 4) && kParti
 
 extern "C" {
 
-int lora_batch_plan(const int32_t* ctx_len, const int32_t* new_len, const int32_t* req_slot,
-                    int n_reqs, int n_rows, int page_size, int32_t* block_table, int64_t ld_table,
-                    int max_pages, const int32_t* free_pages, const int32_t* free_count,
-                    int32_t* free_left, int32_t* row_start, int32_t* seq_len, int32_t* row_req,
-                    int32_t* position, int64_t* slot_map, int32_t* seq_slot, uint32_t* err_word,
-                    lora_stream_t stream) {
-  if (n_reqs < 0 || n_rows < 0 || max_pages < 0 || !row_start) return LORA_ERR_ARG;
+int lora_batch_plan_bounded(const int32_t* ctx_len, const int32_t* new_len, const int32_t* req_slot,
+                            int n_reqs, int n_rows, int page_size, int32_t* block_table,
+                            int64_t ld_table, int max_pages, const int32_t* free_pages, int free_cap,
+                            const int32_t* free_count, int32_t* free_left, int32_t* row_start,
+                            int32_t* seq_len, int32_t* row_req, int32_t* position,
+                            int64_t* slot_map, int32_t* seq_slot, uint32_t* err_word,
+                            lora_stream_t stream) {
+  if (n_reqs < 0 || n_rows < 0 || max_pages < 0 || free_cap < 0 || !row_start) return LORA_ERR_ARG;
   if (n_reqs > 0 && (!ctx_len || !new_len || !block_table || !seq_len)) return LORA_ERR_ARG;
   if (n_rows > 0 && (!row_req || !position || !slot_map || !seq_slot)) return LORA_ERR_ARG;
   if ((free_pages != nullptr) != (free_count != nullptr) ||
@@ -225,7 +226,7 @@ int lora_batch_plan(const int32_t* ctx_len, const int32_t* new_len, const int32_
   for (int i = 0; i < 3; ++i)
     if (overlap(ins[i].p, ins[i].bytes, free_left, 4)) return LORA_ERR_ARG;
   PlanArgs a = {ctx_len,    new_len,   req_slot, n_reqs,   n_rows,   page_size, max_pages,
-                block_table, ld_table, free_pages, free_count, free_left, row_start, seq_len,
+                block_table, ld_table, free_pages, free_cap, free_count, free_left, row_start, seq_len,
                 row_req,    position,  slot_map, seq_slot, err_word};
   const int smem = (int)plan_smem_bytes(n_reqs);
   if (prepare_kernel(batch_plan_kernel, smem, false) != cudaSuccess) return LORA_ERR_CUDA;
@@ -249,6 +250,18 @@ int lora_batch_plan(const int32_t* ctx_len, const int32_t* new_len, const int32_
   cfg.attrs = use_pdl() ? attr : attr + 1;
   cfg.numAttrs = (use_pdl() ? 1 : 0) + (cluster && ctas > 1 ? 1 : 0);
   return cuda_status(cudaLaunchKernelEx(&cfg, batch_plan_kernel, (const PlanArgs)a, cluster && ctas > 1 ? 1 : 0));
+}
+
+int lora_batch_plan(const int32_t* ctx_len, const int32_t* new_len, const int32_t* req_slot,
+                    int n_reqs, int n_rows, int page_size, int32_t* block_table, int64_t ld_table,
+                    int max_pages, const int32_t* free_pages, const int32_t* free_count,
+                    int32_t* free_left, int32_t* row_start, int32_t* seq_len, int32_t* row_req,
+                    int32_t* position, int64_t* slot_map, int32_t* seq_slot, uint32_t* err_word,
+                    lora_stream_t stream) {
+  return lora_batch_plan_bounded(ctx_len, new_len, req_slot, n_reqs, n_rows, page_size, block_table,
+                                 ld_table, max_pages, free_pages, INT32_MAX, free_count, free_left,
+                                 row_start, seq_len, row_req, position, slot_map, seq_slot,
+                                 err_word, stream);
 }
 
 int lora_pages_release(const int32_t* done, const int32_t* seq_len, int n_reqs, int page_size,

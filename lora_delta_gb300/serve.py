@@ -111,19 +111,22 @@ def lora_batch_plan(plan: BatchPlan, ctx_len, new_len, block_table, req_slot=Non
                     free_count=None, free_left=None, err=None, stream=None) -> BatchPlan:
     """The step's maps and new pages from the requests' lengths, into ``plan``'s tensors.
 
-    ``ctx_len`` may be ``plan.seq_len``, the lengths that the plan's last step left.
-    ``free_pages`` / ``free_count`` [1] are the stack of free pages; the height that is left goes to
-    ``free_left`` [1], or back into ``free_count`` where none is given."""
+    ``ctx_len`` may be ``plan.seq_len``, the lengths that the plan's last step left.  ``free_pages`` /
+    ``free_count`` [1] are the stack of free pages (a count past its entries is cut and reported in
+    ``err``); the height that is left goes to ``free_left`` [1], or back into ``free_count`` where none
+    is given."""
     B = plan.n_reqs
     table, ld, pages = _table(block_table, B)
     free = count = left = None
+    cap = 0
     if free_pages is not None:
+        cap = free_pages.numel()
         free, count = _i32(free_pages, "free_pages"), _i32(free_count, "free_count", 1)
         left = count if free_left is None else _i32(free_left, "free_left", 1)
-    _check("lora_batch_plan", _fn.lora_batch_plan(
+    _check("lora_batch_plan", _fn.lora_batch_plan_bounded(
         _i32(ctx_len, "ctx_len", B), _i32(new_len, "new_len", B),
         None if req_slot is None else _i32(req_slot, "req_slot", B), B, plan.n_rows, plan.page_size,
-        table, ld, pages, free, count, left, *plan._out, _err_at(err), _raw_stream(stream)))
+        table, ld, pages, free, cap, count, left, *plan._out, _err_at(err), _raw_stream(stream)))
     return plan
 
 

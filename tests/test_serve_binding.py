@@ -147,3 +147,24 @@ def test_plans_and_caches_keep_the_tensors_that_they_were_made_with(ld):  # noqa
         for name in names:
             with pytest.raises(AttributeError):
                 setattr(obj, name, getattr(obj, name))
+
+
+@gpu
+@pytest.mark.parametrize("count", [6, 1000, 2 ** 31 - 1, -1, -2 ** 31])
+@pytest.mark.parametrize("in_place", [False, True])
+def test_plan_does_not_take_pages_past_the_stack(ld, count, in_place):  # noqa: F811
+    """A height above the stack's entries counts as full, one below 0 as empty; both are reported."""
+    from tests import serve_ref as ref
+    ctx, new, P, free = np.array([3, 0]), np.array([30, 9]), 16, np.array([11, 12, 13, 14, 15])
+    table = np.full((2, 4), -1)
+    table[0, 0] = 2
+    want = ref.plan(ctx, new, None, 40, P, table, 4, free, min(max(count, 0), 5))
+    p, err, left = ld.BatchPlan(2, 40, P), ld.new_error_word(), dev([77])
+    d_table, d_count = dev(table), dev([count])
+    ld.lora_batch_plan(p, dev(ctx), dev(new), d_table, free_pages=dev(free), free_count=d_count,
+                       free_left=None if in_place else left, err=err)
+    assert ld.lora_get_error(err) == ref.ERR_PAGE
+    for name in ("row_start", "seq_len", "row_req", "position", "slot_map"):
+        assert np.array_equal(host(getattr(p, name)), want[name]), name
+    assert np.array_equal(host(d_table), want["table"])
+    assert int((d_count if in_place else left)[0]) == want["left"]
