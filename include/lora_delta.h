@@ -505,9 +505,11 @@ int lora_pages_release(const int32_t *done, const int32_t *seq_len, int n_reqs, 
  * head_dim is 64, 128 or 256, in groups of 64.  A (token, head, group) keeps
  * m = f16(min), s = f16((max - min) * (1 / 15)) and codes
  * c = clamp(rint((x - m) * (1 / s)), 0, 15) (0 where s is 0), each step rounded
- * to float32, and stands for s * c + m.  Magnitudes up to 65504 are held (attention
- * wants them up to 2^15, since it may round s * c + m to float16); a group with
- * an infinity, a NaN or more reads as NaN.  The bytes of a tile, W = min(D, 128):
+ * to float32, and stands for s * c + m.  Magnitudes up to 65504 are held (above
+ * 65440 the top of a group may read as an infinity in float16 rows, and attention
+ * wants magnitudes up to 2^15, since it may round s * c + m to float16); a group with
+ * an infinity, a NaN or more keeps NaNs for s and m, and reads as NaN.  The bytes of
+ * a tile, W = min(D, 128):
  *   key codes [D / W][16 tokens][4 c][W / 32 words]: nibble i of word w is dim
  *     64 (w / 2) + 16 c + 8 (w % 2) + i of the plane; key pairs [16][D / 64] of f16 (s, m);
  *   value codes [D / W][2 h][8 g][4 c][W / 32 words]: nibble j of the low (high) half of

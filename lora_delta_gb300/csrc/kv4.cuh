@@ -5,7 +5,8 @@
 // keeps m = f16(min), s = f16((max - min) * (1 / 15)) and codes
 // c = clamp(rint((x - m) * (1 / s)), 0, 15), each step rounded to float32, and
 // stands for s * c + m.  Rounding s and m to f16 before the codes are taken
-// makes the codes the nearest ones on the grid that is read back.
+// makes the codes the nearest ones on the grid that is read back.  A group that
+// f16 does not hold (an infinity, a NaN, a magnitude above 65504) keeps NaNs.
 //
 // Pages are [num_pages][kv_heads][page_size / 16] tiles of 16 tokens, so one
 // (page, head) is contiguous and a bulk copy brings a tile whole:
@@ -84,8 +85,10 @@ __device__ __forceinline__ Kv4Scale kv4_scale(uint32_t lo2, uint32_t hi2) {
   lo2 = min2<BF16>(lo2, lo2 >> 16 | lo2 << 16);
   hi2 = max2<BF16>(hi2, hi2 >> 16 | hi2 << 16);
   const float lo = unpack2<BF16>(lo2).x, hi = unpack2<BF16>(hi2).x;
-  const __half m = __float2half_rn(__fadd_rn(lo, 0.0f));
-  const __half s = __float2half_rn(__fmul_rn(__fsub_rn(hi, lo), 1.0f / 15.0f));
+  // (beyond f16, or not a number: neither is kept, and the group reads as NaN)
+  const bool held = fabsf(lo) <= 65504.0f && fabsf(hi) <= 65504.0f;
+  const __half m = held ? __float2half_rn(__fadd_rn(lo, 0.0f)) : __ushort_as_half(0x7fff);
+  const __half s = held ? __float2half_rn(__fmul_rn(__fsub_rn(hi, lo), 1.0f / 15.0f)) : m;
   const float sf = __half2float(s);
   Kv4Scale q;
   q.m = __half2float(m);

@@ -223,3 +223,51 @@ def test_a_value_that_is_not_finite_shows_in_its_group_only(ld, D, group, lens, 
     bound = NP_TYPE[c["dtype"]] * np.abs(want) + 2.0 ** -9 * big[..., None]
     assert (np.abs(got - want) <= bound)[~hit].all()
     assert (np.abs(got_lse - want_lse) <= 2.0 ** -9 + 2.0 ** -20 * np.abs(want_lse)).all()
+
+
+@gpu
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+def test_groups_beyond_f16_read_as_nan_and_ones_up_to_it_do_not(ld, dtype):  # noqa: F811
+    D, n = 128, 16
+    x = torch.randn(n, 1, D, device="cuda").to(dtype)
+    limit = 65280.0 if dtype == torch.bfloat16 else 65440.0  # (65280 is the last of bfloat16)
+    x[0, 0, 3], x[1, 0, 70], x[2, 0, :64] = limit, -limit, limit
+    x[3, 0, 64], x[3, 0, 65] = limit, -limit
+    held = torch.ones(n, 2, dtype=torch.bool, device="cuda")
+    if dtype == torch.bfloat16:
+        x[5, 0, 3], x[6, 0, 127], x[7, 0, :64], x[8, 0, 64:] = 65536.0, -70000.0, 1e5, -1e30
+        x[9, 0, :64], x[10, 0, 0], x[10, 0, 1] = torch.linspace(0, 5e5, 64, device="cuda").to(dtype), 3e38, -3e38
+        held[5, 0] = held[6, 1] = held[7, 0] = held[8, 1] = held[9, 0] = held[10, 0] = False
+    x[11, 0, :64], x[12, 0, 64:], x[13, 0, 9] = float("inf"), -float("inf"), float("nan")
+    held[11, 0] = held[12, 1] = held[13, 0] = False
+    cache, err = ld.Kv4Cache.empty(1, 16, 1, D, dtype), ld.new_error_word()
+    slots = torch.arange(n, device="cuda")
+    k, v = torch.empty(2, n, 1, D, device="cuda", dtype=dtype)
+    ld.lora_kv4_append(cache, x, x, slots, err=err)
+    ld.lora_kv4_read(cache, k, v, slots, err=err)
+    assert ld.lora_get_error(err) == 0
+    for got in (k, v):
+        g, w = got.float().view(n, 2, 64), x.float().view(n, 2, 64)
+        assert torch.equal(torch.isnan(g).all(-1), ~held) and torch.equal(torch.isfinite(g).all(-1), held)
+        # half a step, the step's rounding 15 times over, and the row type's
+        step = (w.amax(-1) - w.amin(-1)) / 15
+        bound = 0.5 * step + 16 * step * 2.0 ** -11 + w.abs().amax(-1) * (2.0 ** -10 + NP_TYPE[dtype])
+        assert ((g - w).abs() <= bound[..., None])[held].all()
+
+
+@gpu
+@pytest.mark.parametrize("lens", [FEW_ROWS, MANY_ROWS], ids=["few", "many"])
+def test_attention_over_groups_beyond_f16(ld, lens):  # noqa: F811
+    """Rows that see a key or value which the cache does not hold are NaN, be it read by either kernel."""
+    c = attention_case(np.random.default_rng(4), lens, 64, 1, 4, 32, torch.bfloat16)
+    cache = ld.Kv4Cache(dev(c["pages"], np.uint8), 32, 64)
+    b = 1
+    at = int(c["seq"][b]) - 1
+    slot = dev([int(c["table"][b, at // 32]) * 32 + at % 32], np.int64)
+    x = torch.zeros(1, 1, 64, device="cuda").bfloat16()
+    x[0, 0, 5] = 1e5
+    for k, v in ((torch.zeros_like(x), x), (x, torch.zeros_like(x))):
+        ld.lora_kv4_append(cache, k, v, slot)
+        out = run_attention(ld, c, cache=cache)[0].float()
+        last = int(c["start"][b + 1]) - 1
+        assert torch.isnan(out[last]).all() and torch.isfinite(out[:last]).all() and torch.isfinite(out[last + 1:]).all()
