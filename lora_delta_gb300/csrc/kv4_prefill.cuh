@@ -5,6 +5,7 @@
 // key/value head; 128 rows at head_dim 256) and the tokens that they see, in
 // tiles of 128 (64).  Roles of a CTA, handing over through mbarriers:
 //   load warp       bulk copies of the tile's packed 16-token blocks
+//   guard warp      whether the tile's keys need two operands
 //   8 expand warps  codes to f16 values s c + m in the operands' 128-byte
 //                   swizzled layout, keys [token][dim], values [dim][token]
 //   an MMA warp     for each row half in turn: O += P V with P read from tensor
@@ -17,10 +18,17 @@
 // weights are computed; tiles are expanded once for both.
 // Keys and values are rounded to f16 (2^-12 relative) where tiles are expanded:
 // two packed instructions a pair of codes.  Scaling S instead would cost one
-// per score, group and query row.  Where that rounding could show (scores of
-// large keys and queries: an estimated error of a score above 2^-10), a tile's
-// keys come in two operands, the second holding what the first lost, and S is
-// the sum of two products; ordinary tiles do without.  Queries are brought to f16
+// per score, group and query row.  Where that rounding could show, a tile's
+// keys come in two operands, the second holding what the first lost, and S is the
+// sum of two products; ordinary tiles do without.  A rounding is some 2^-12.3 |k|, so
+// a score's error has the variance 2^-24.6 sum_d (scale q_d k_d)^2, at most the sum
+// over groups of 64 dims of |scale q_g|^2 max k_g^2.  The guard bounds that for
+// every row of the item and every token of the tile that some row sees: above 2^8
+// the keys are two, so that no score is off by more than 2^-8.3 (one standard
+// deviation), whatever the data; of normal keys with a few strong dims that bound is
+// about 85 and the largest true sum about 8, an error of 2^-10.8.  (A limit
+// of 2^7 would take a quarter of such tiles, 2^6 most of them: one prompt of 8192
+// tokens 720 and 990 us for 477; two operands always take 1057.)  Queries are brought to f16
 // by a power of two of their row (exact), weights are 2^7 p with p <= 2^8.
 //
 // Bound: the chain of a half's softmax, its two products and the expansion that
@@ -56,11 +64,10 @@ struct Pre {
   static constexpr int KVB = D == 64 ? 6 : 3;       // expanded operands in flight
   static constexpr int Q = ROWS * D * 2;
   static constexpr int INFO = 8;                    // tiles described at once
-  static constexpr int SIZES = 4;                   // items measured at once
-  // Warps: load 2, MMA 3, then softmax and expand from whole warpgroups on (0 and
-  // 1 only help at the start).
+  // Warps: guard 1, load 2, MMA 3, then softmax and expand from whole warpgroups on
+  // (0 only helps at the start).
   static constexpr int SOFT_WARPS = 4 * MT, EXP_WARPS = 8;
-  static constexpr int MMA_WARP = 3, LOAD_WARP = 2, SOFT_WARP = 4, EXP_WARP = SOFT_WARP + SOFT_WARPS;
+  static constexpr int MMA_WARP = 3, LOAD_WARP = 2, GUARD_WARP = 1, SOFT_WARP = 4, EXP_WARP = SOFT_WARP + SOFT_WARPS;
   static constexpr int THREADS = (EXP_WARP + EXP_WARPS) * 32;
   // Registers a thread: 20 warps start with 96.  The expand warps give 24 each
   // to the softmax warps (8 x 72 + 8 x 120 = 16 x 96), which hold 32 words of
@@ -72,6 +79,8 @@ struct Pre {
     return 1024 + (size_t)Q + KVB * KV + 2 * RAW + (size_t)(B + 1) * 4;
   }
 };
+
+constexpr float kKeyLimit = 256.0f;  // of the guard's bound, as above
 
 // A row's frame: its weights and their sums are exp2((score - base) qa + off), in
 // log2 units qa score.  base is 0 and off 7 less the row's maximum, as one product
@@ -213,8 +222,8 @@ template <class C, bool SPLIT>
 __global__ void __launch_bounds__(C::THREADS, 1) kv4_prefill_kernel(const AttnArgs a, int min_rows) {
   extern __shared__ uint8_t pre_smem_raw[];
   __shared__ uint64_t raw_full[2], raw_empty[2], kv_full[C::KVB], kv_empty[C::KVB];
-  __shared__ uint64_t q_full[2], s_full[2], p_full[2], pv_done[2], size_full[C::SIZES], size_empty[C::SIZES], drain_bar;
-  __shared__ float size_s[C::SIZES][C::G];         // of some items: the mean |scale q_g|^2 of some rows
+  __shared__ uint64_t q_full[2], s_full[2], p_full[2], pv_done[2], two_full[2], drain_bar;
+  __shared__ float size_s[C::SOFT_WARPS][C::G];    // of a warp's rows of q: the largest |scale q_g|^2
   __shared__ int exp_s[C::SOFT_WARPS][32];         // of q's rows: 2^e <= the largest |q|
   __shared__ uint32_t taddr_s;
   __shared__ uint32_t info_pages[C::INFO];             // blocks of a tile that were copied
@@ -237,12 +246,9 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_prefill_kernel(const AttnAr
       mbar_init(&s_full[i], 1);
       mbar_init(&p_full[i], 4);
       mbar_init(&pv_done[i], 1);
+      mbar_init(&two_full[i], 1);
     }
     mbar_init(&drain_bar, 1);
-    for (int i = 0; i < C::SIZES; ++i) {
-      mbar_init(&size_full[i], 1);
-      mbar_init(&size_empty[i], C::EXP_WARPS);
-    }
     for (int i = 0; i < C::KVB; ++i) {
       mbar_init(&kv_full[i], C::EXP_WARPS);
       mbar_init(&kv_empty[i], 1);
@@ -300,43 +306,16 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_prefill_kernel(const AttnAr
   if (warp == C::LOAD_WARP) {
     // ------------------------------------------------------------------ load
     uint32_t n = 0;  // tiles so far
-    // the size of an item's q, from 4 loads of a lane spread over its rows
-    auto measure = [&](int round) {
+    auto prefetch = [&](int round) {  // an item's q on its way to L2
       const int i = pre_nth<SPLIT>(sp, round);
       if (i >= items) return;
       const PreItem it = pre_item<C, SPLIT>(a, pre, sp, i);
-      if (round >= C::SIZES)
-        ok = __all_sync(0xffffffffu, mbar_wait_soon(&size_empty[round % C::SIZES], (round / C::SIZES - 1) & 1, a.wait_ns));
-      if (!ok) return;
-      float sq = 0.0f;
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const int x = it.rem0 + (k * C::RPL + lane / C::LPR) * it.rows / (4 * C::RPL), t = div_group(a, x);
-        const uint4 v = ldg_nc_v4(reinterpret_cast<const uint16_t*>(a.q) + (int64_t)(it.row0 + it.tok0 + t) * a.ld_q +
-                                  (it.h * a.group + x - t * a.group) * C::D + (lane % C::LPR) * 8);
-        const uint32_t* w = reinterpret_cast<const uint32_t*>(&v);
-#pragma unroll
-        for (int y = 0; y < 4; ++y) {
-          const float2 f = unpack2<C::BF16>(w[y]);
-          sq = fmaf(f.x, f.x, fmaf(f.y, f.y, sq));
-        }
-      }
-      // (sums over the lanes of a group of 64 dims, then over the rows)
-#pragma unroll
-      for (int d = 1; d < 8; d <<= 1) sq += __shfl_xor_sync(0xffffffffu, sq, d);
-#pragma unroll
-      for (int d = C::LPR; d < 32; d <<= 1) sq += __shfl_xor_sync(0xffffffffu, sq, d);
-      const float sc = a.scale_log2 * 0.69314718055994531f;
-      // and all of it on its way to L2
       for (int x = lane; x < it.rows * (C::D / 64); x += 32) {
         const int y = it.rem0 + x / (C::D / 64), t = div_group(a, y);
         asm volatile("prefetch.global.L2 [%0];" ::"l"(
             reinterpret_cast<const uint16_t*>(a.q) + (int64_t)(it.row0 + it.tok0 + t) * a.ld_q +
             (it.h * a.group + y - t * a.group) * C::D + x % (C::D / 64) * 64));
       }
-      if (lane < C::LPR && lane % 8 == 0) size_s[round % C::SIZES][lane / 8] = sq * sc * sc / (4 * C::RPL);
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&size_full[round % C::SIZES]);
     };
     for (int round = 0, i; (i = pre_nth<SPLIT>(sp, round)) < items && ok; ++round) {
       const PreItem it = pre_item<C, SPLIT>(a, pre, sp, i);
@@ -371,15 +350,65 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_prefill_kernel(const AttnAr
           bulk_g2s(raw_s + st * C::RAW + lane * C::RSTRIDE, a.pages + tile * C::TILE, C::TILE,
                    &raw_full[st]);
         }
-        if (j == 0) {  // (behind the first tile's copies; an item ahead)
-          if (round == 0) measure(0);
-          measure(round + 1);
-        }
+        if (j == 0) prefetch(round + 1);  // (behind the first tile's copies)
       }
     }
     // (the copies still in flight write to this CTA's memory)
     for (uint32_t k = n >= 2 ? n - 2 : 0; k < n; ++k)
       if (!mbar_wait_soon(&raw_full[k & 1], (k >> 1) & 1, kWaitLimitNs)) ok = false;
+  } else if (warp == C::GUARD_WARP) {
+    // ----------------------------------------------------------------- guard
+    uint32_t n = 0, q_ph = 0;
+    auto wait = [&](uint64_t* bar, uint32_t parity) {
+      if (ok) ok = __all_sync(0xffffffffu, mbar_wait_soon(bar, parity, a.wait_ns));
+    };
+    for (int round = 0, i; (i = pre_nth<SPLIT>(sp, round)) < items && ok; ++round) {
+      const PreItem it = pre_item<C, SPLIT>(a, pre, sp, i);
+      const int mt = it.rows > 128 ? 2 : 1;
+      float size[C::G];
+      for (int j = 0; j < it.tiles && ok; ++j, ++n) {
+        const int st = n & 1, tok0 = it.kv0 + j * C::NKV;
+        wait(&raw_full[st], (n >> 1) & 1);
+        if (!ok) break;
+        const uint32_t pages = info_pages[n % C::INFO];
+        float k2[C::NKV / 32][C::G];  // the largest k^2 of each group, of tokens that some row sees
+#pragma unroll
+        for (int x = 0; x < C::NKV / 32; ++x) {
+          const int t = x * 32 + lane;
+          const uint8_t* pairs = raw_s + st * C::RAW + (t / kKvTile) * C::RSTRIDE + 8 * C::D + (t % kKvTile) * C::G * 4;
+          const bool use = ((pages >> (t / kKvTile)) & 1u) && tok0 + t >= it.lo && tok0 + t < it.hi;
+#pragma unroll
+          for (int q = 0; q < C::G; ++q) {
+            const float2 f = __half22float2(*reinterpret_cast<const __half2*>(pairs + 4 * q));
+            const float k = fmaxf(fabsf(f.y), fabsf(fmaf(15.0f, f.x, f.y)));
+            k2[x][q] = use ? k * k : 0.0f;
+          }
+        }
+        if (j == 0) {  // (as late as can be: the rows' warps load q after the last item's end)
+          for (int m = 0; m < mt; ++m) {
+            wait(&q_full[m], (q_ph >> m) & 1);
+            q_ph ^= 1u << m;
+          }
+          if (!ok) break;
+#pragma unroll
+          for (int q = 0; q < C::G; ++q)
+            size[q] = __uint_as_float(__reduce_max_sync(0xffffffffu, lane < 4 * mt ? __float_as_uint(size_s[lane][q]) : 0u));
+        }
+        bool large = false;
+#pragma unroll
+        for (int x = 0; x < C::NKV / 32; ++x) {
+          float sum = 0.0f;
+#pragma unroll
+          for (int q = 0; q < C::G; ++q) sum = fmaf(size[q], k2[x][q], sum);
+          large |= !(sum <= kKeyLimit);  // (and what is not a number)
+        }
+        large = __any_sync(0xffffffffu, large);
+        if (lane == 0) {
+          info_two[n % C::INFO] = large;
+          mbar_arrive(&two_full[st]);
+        }
+      }
+    }
   } else if (warp == C::MMA_WARP) {
     // ------------------------------------------------------------------- MMA
     // The warp runs whole, so that descriptors stay in uniform registers; one
@@ -481,8 +510,6 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_prefill_kernel(const AttnAr
     for (int round = 0, i; (i = pre_nth<SPLIT>(sp, round)) < items && ok; ++round) {
       const PreItem it = pre_item<C, SPLIT>(a, pre, sp, i);
       const int pos_lo = it.pos0 + it.tok0, pos_hi = pos_lo + div_group(a, it.rem0 + it.rows - 1);
-      ok = __all_sync(0xffffffffu, mbar_wait_soon(&size_full[round % C::SIZES], (round / C::SIZES) & 1, a.wait_ns));
-      if (!ok) break;
       for (int j = 0; j < it.tiles && ok; ++j, ++n) {
         const int st = n & 1, tok0 = it.kv0 + j * C::NKV;
         ok = __all_sync(0xffffffffu, mbar_wait_soon(&raw_full[st], (n >> 1) & 1, a.wait_ns));
@@ -512,31 +539,9 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_prefill_kernel(const AttnAr
           fence_proxy_async_smem();  // (the block is next written by a bulk copy)
           __syncwarp();
         }
-        // The score's error from keys rounded to 11 bits: each dim's is about
-        // 2^-12.3 |k|, so its variance is 2^-24.6 sum (scale q)^2 k^2, which is
-        // taken as |scale q_g|^2 (of some rows) times the mean k^2 of each group,
-        // from a word of 8 dims a lane; 12 makes it 2^-21.  (Each of the warps
-        // finds the same.)
-        bool two;
-        {
-          const int c = lane & 3, blk = (lane >> 2) % C::TPK, p = lane / (4 * C::TPK), tt = n & 15;
-          const int w = (lane + n) & (C::WD - 1), gq = p * (C::WD / 2) + w / 2;
-          const uint8_t* tile = raw + blk * C::RSTRIDE;
-          const uint32_t v = *reinterpret_cast<const uint32_t*>(tile + p * 8 * C::W + tt * (C::W / 2) + c * (C::W / 8) + w * 4);
-          const float2 sm = __half22float2(*reinterpret_cast<const __half2*>(tile + 8 * C::D + (tt * C::G + gq) * 4));
-          const uint32_t x = v & 0x0f0f0f0fu, y = (v >> 4) & 0x0f0f0f0fu;
-          const float c2 = (float)__dp4a(x, x, __dp4a(y, y, 0u)), c1 = (float)__dp4a(x, 0x01010101u, __dp4a(y, 0x01010101u, 0u));
-          float sum = fmaf(sm.x, fmaf(sm.x, c2, 2.0f * sm.y * c1), 8.0f * sm.y * sm.y) * size_s[round % C::SIZES][gq];
-          if (!((pages >> blk) & 1u) || tok0 + blk * kKvTile + tt >= it.hi) sum = 0.0f;
-          // (the mean over lanes, G groups; summed in units of 2^-4, a lane's part
-          // bounded, and what is not a number counts as large)
-          const uint32_t part = (uint32_t)fminf(sum * 16.0f, 67108864.0f);
-          two = __reduce_add_sync(0xffffffffu, part) > (uint32_t)(16.0f * 12.0f * 8.0f * 32.0f / C::G);
-        }
-        if (et == 0) info_two[n % C::INFO] = two;
-        // (not waited for earlier: the tensor cores' next step waits for these keys)
         wait_free();
         if (!ok) break;
+        bool two;
         {
           uint8_t* kb = kv_s + (k % C::KVB) * C::KV;
 #pragma unroll
@@ -565,6 +570,10 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_prefill_kernel(const AttnAr
               }
             }
           }
+          // (the MMA warp reads the guard's word too, by way of these keys)
+          ok = __all_sync(0xffffffffu, mbar_wait_soon(&two_full[st], (n >> 1) & 1, a.wait_ns));
+          if (!ok) break;
+          two = info_two[n % C::INFO];
           filled();
         }
         wait_free();
@@ -639,7 +648,6 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_prefill_kernel(const AttnAr
           if (lane == 0) mbar_arrive(&raw_empty[st]);
         }
       }
-      if (lane == 0) mbar_arrive(&size_empty[round % C::SIZES]);
     }
   } else if (warp >= C::SOFT_WARP) {
     // --------------------------------------------------------------- softmax
@@ -684,6 +692,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_prefill_kernel(const AttnAr
       // half's q are done), a batch of loads at once
       const int chunk = lane % C::LPR;
       constexpr int kBatch = C::LPR < 16 ? 8 : 16;
+      float largest = 0.0f;  // |q_g|^2 of the lane's group of dims
 #pragma unroll 1
       for (int y0 = 0; y0 < 32 / C::RPL; y0 += kBatch) {
         uint4 raw[kBatch];
@@ -698,14 +707,18 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_prefill_kernel(const AttnAr
 #pragma unroll
         for (int y = 0; y < kBatch; ++y) {
           const uint32_t* w = reinterpret_cast<const uint32_t*>(&raw[y]);
-          float f[8], top = 0.0f;
+          float f[8], top = 0.0f, sq = 0.0f;
 #pragma unroll
           for (int x = 0; x < 4; ++x) {
             const float2 z = unpack2<C::BF16>(w[x]);
             f[2 * x] = z.x;
             f[2 * x + 1] = z.y;
             top = fmaxf(top, fmaxf(fabsf(z.x), fabsf(z.y)));
+            sq = fmaf(z.x, z.x, fmaf(z.y, z.y, sq));
           }
+#pragma unroll
+          for (int d = 1; d < 8; d <<= 1) sq += __shfl_xor_sync(0xffffffffu, sq, d);
+          largest = fmaxf(largest, sq);
 #pragma unroll
           for (int d = 1; d < C::LPR; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
           int e = (int)((__float_as_uint(top) >> 23) & 255u) - 127;
@@ -718,6 +731,10 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_prefill_kernel(const AttnAr
                                                       half2_bits(f[2] * up, f[6] * up), half2_bits(f[3] * up, f[7] * up));
         }
       }
+#pragma unroll
+      for (int d = C::LPR; d < 32; d <<= 1) largest = fmaxf(largest, __shfl_xor_sync(0xffffffffu, largest, d));
+      const float sc = a.scale_log2 * 0.69314718055994531f;
+      if (lane < C::LPR && lane % 8 == 0) size_s[warp - C::SOFT_WARP][lane / 8] = largest * (sc * sc);
       fence_proxy_async_smem();
       tc::fence_before_sync();
       __syncwarp();

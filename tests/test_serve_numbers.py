@@ -271,3 +271,84 @@ def test_attention_over_groups_beyond_f16(ld, lens):  # noqa: F811
         out = run_attention(ld, c, cache=cache)[0].float()
         last = int(c["start"][b + 1]) - 1
         assert torch.isnan(out[last]).all() and torch.isfinite(out[:last]).all() and torch.isfinite(out[last + 1:]).all()
+
+
+def keys_case(seed, lens, D, group, dtype, key_of, q_of):
+    """A case whose keys and queries are changed before they are stored: key_of(k [s, D]), q_of(q [n, Q, D])."""
+    rng = np.random.default_rng(seed)
+    c = attention_case(rng, lens, D, 1, group, 32, dtype)
+    for b, s in enumerate(c["seq"]):
+        t = np.arange(s)
+        k, v = rng.standard_normal((2, s, 1, D))
+        k = key_of(k[:, 0])[:, None]
+        k, v = (torch.from_numpy(x).to(dtype).double().numpy() for x in (k, v))
+        ref.append(c["pages"], k, v, c["table"][b, t // 32].astype(np.int64) * 32 + t % 32, 32)
+    c["q"] = torch.from_numpy(q_of(rng.standard_normal(c["q"].shape))).to(dtype).cuda()
+    return c
+
+
+def check_scores(ld, c):  # noqa: F811
+    """The logarithm of the denominator is as exact as the scores: e, and 2^-9 for weights rounded to 16 bits."""
+    out, lse, err = run_attention(ld, c)
+    want, want_lse, big, _ = ref.attend(c["q"].double().cpu().numpy(), c["pages"], c["P"], c["table"], c["start"],
+                                        c["seq"], c["D"] ** -0.5, 0)
+    assert err == 0
+    got, got_lse = out.double().cpu().numpy(), lse.double().cpu().numpy()
+    room, off = score_room(c, c["D"] ** -0.5)
+    assert (np.abs(got_lse - want_lse) <= 2.0 ** -9 + off).all(), float((np.abs(got_lse - want_lse) - off).max())
+    bound = NP_TYPE[c["dtype"]] * np.abs(want) + (2.0 ** -9 + 2 * room[..., None]) * big[..., None]
+    assert (np.abs(got - want) <= bound).all()
+
+
+def times(x, at, by):
+    x = x.copy()
+    x[at] *= by
+    return x
+
+
+@gpu
+@pytest.mark.parametrize("D,group,head", [(128, 4, 3), (128, 4, 1), (64, 8, 5), (256, 2, 1)])
+def test_scores_of_a_head_with_large_queries(ld, D, group, head):  # noqa: F811
+    """One query head of a group is 30 times the others."""
+    c = keys_case(D, [(0, 300), (200, 90)], D, group, torch.bfloat16, lambda k: k, lambda q: times(q, np.s_[:, head], 30.0))
+    check_scores(ld, c)
+
+
+@gpu
+def test_scores_of_one_row_with_a_large_query(ld):  # noqa: F811
+    for row in (0, 1, 77, 128, 255, 299):
+        c = keys_case(row, [(0, 300)], 128, 4, torch.bfloat16, lambda k: k, lambda q: times(q, np.s_[row, 2], 100.0))
+        check_scores(ld, c)
+
+
+@gpu
+@pytest.mark.parametrize("at", range(16))
+def test_scores_of_one_large_key_in_each_place_of_a_block(ld, at):  # noqa: F811
+    """One token in 300 has a key 60 times the others' size."""
+    c = keys_case(at, [(0, 300), (100, 60)], 128, 2, torch.bfloat16, lambda k: times(k, 64 + at, 60.0), lambda q: q)
+    check_scores(ld, c)
+
+
+@gpu
+@pytest.mark.parametrize("D,size", [(128, 10.0), (64, 8.0), (256, 12.0), (128, 30.0)])
+def test_scores_of_a_dim_that_is_strong_in_queries_and_keys(ld, D, size):  # noqa: F811
+    for dim in (0, 13, D - 1):
+        c = keys_case(dim, [(0, 300), (500, 70)], D, 4, torch.bfloat16, lambda k: times(k, np.s_[:, dim], size),
+                      lambda q: times(q, np.s_[..., dim], size))
+        check_scores(ld, c)
+
+
+@gpu
+def test_requests_of_many_rows_do_not_depend_on_their_neighbours(ld):  # noqa: F811
+    """The same requests in another order, with keys about the size from which two operands are taken."""
+    rng = np.random.default_rng(17)
+    lens = [(int(a), int(b)) for a, b in zip(rng.integers(0, 300, 40), rng.integers(33, 200, 40))]
+    c = keys_case(1, lens, 128, 4, torch.bfloat16, lambda k: k * np.exp(rng.standard_normal((len(k), 1)) * 0.5), lambda q: q * 2.5)
+    out, lse, _ = run_attention(ld, c)
+    order = rng.permutation(40)
+    rows = np.concatenate([np.arange(c["start"][b], c["start"][b + 1]) for b in order])
+    d = dict(c, table=c["table"][order], seq=c["seq"][order], q=c["q"][torch.from_numpy(rows).cuda()].contiguous(),
+             start=np.concatenate([[0], np.cumsum([lens[b][1] for b in order])]))
+    out2, lse2, _ = run_attention(ld, d)
+    at = torch.from_numpy(rows).cuda()
+    assert torch.equal(out[at], out2) and torch.equal(lse[at], lse2)
