@@ -99,6 +99,8 @@ class BatchPlan(_Fixed):
         def ints(n):
             return torch.empty(n, dtype=torch.int32, device=device)
 
+        if torch.device(device).type != "cuda":
+            raise ValueError(f"a plan's tensors are the GPU's, not {device}'s")
         self.n_reqs, self.n_rows, self.page_size = int(n_reqs), int(n_rows), int(page_size)
         self.row_start, self.seq_len = ints(n_reqs + 1), ints(n_reqs)
         self.row_req, self.position, self.seq_slot = ints(n_rows), ints(n_rows), ints(n_rows)

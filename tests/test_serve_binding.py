@@ -168,3 +168,11 @@ def test_plan_does_not_take_pages_past_the_stack(ld, count, in_place):  # noqa: 
         assert np.array_equal(host(getattr(p, name)), want[name]), name
     assert np.array_equal(host(d_table), want["table"])
     assert int((d_count if in_place else left)[0]) == want["left"]
+
+
+def test_plans_are_made_on_the_gpu():
+    """The kernel writes to their addresses, which must not be the host's."""
+    import lora_delta_gb300 as ld
+    for device in ("cpu", torch.device("cpu")):
+        with pytest.raises(ValueError):
+            ld.BatchPlan(2, 4, 16, device=device)
