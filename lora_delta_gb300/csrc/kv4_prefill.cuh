@@ -23,13 +23,15 @@
 // sum of two products; ordinary tiles do without.  A rounding is some 2^-12.3 |k|, so
 // a score's error has the variance 2^-24.6 sum_d (scale q_d k_d)^2, at most the sum
 // over groups of 64 dims of |scale q_g|^2 max k_g^2.  The guard bounds that for
-// every row of the item and every token of the tile that some row sees: above 2^8
-// the keys are two, so that no score is off by more than 2^-8.3 (one standard
+// every row of the item and every token of the tile that some row sees: above 384
+// the keys are two, so that no score is off by more than 2^-8 (one standard
 // deviation), whatever the data; of normal keys with a few strong dims that bound is
-// about 85 and the largest true sum about 8, an error of 2^-10.8.  (A limit
-// of 2^7 would take a quarter of such tiles, 2^6 most of them: one prompt of 8192
-// tokens 720 and 990 us for 477; two operands always take 1057.)  Queries are brought to f16
-// by a power of two of their row (exact), weights are 2^7 p with p <= 2^8.
+// about 85 and the largest true sum about 8, an error of 2^-10.8.  (384 takes one
+// such tile in 3000, and one in 200 at head_dim 64; 2^8 one in 140 and one in 23,
+// and 271 us where a prompt's chunks have such a head for 247; 2^7 a quarter, 2^6 most:
+// one prompt of 8192 tokens 720 and 990 us for 477; two operands always take 1057.)
+// Queries are brought to f16 by a power of two of their row (exact), weights are
+// 2^7 p with p <= 2^8.
 //
 // Bound: the chain of a half's softmax, its two products and the expansion that
 // refills their operands; issue slots are 60% full, the tensor cores 40%.  bf16, 8 heads of 128, 4
@@ -80,7 +82,7 @@ struct Pre {
   }
 };
 
-constexpr float kKeyLimit = 256.0f;  // of the guard's bound, as above
+constexpr float kKeyLimit = 384.0f;  // of the guard's bound, as above
 
 // A row's frame: its weights and their sums are exp2((score - base) qa + off), in
 // log2 units qa score.  base is 0 and off 7 less the row's maximum, as one product
