@@ -222,7 +222,7 @@ def _attn_workspace(device, stream, raw):
     if stream is not None:
         with torch.cuda.stream(stream):
             return _attn_workspace(device, None, raw)
-    if torch.cuda.is_current_stream_capturing():
+    if torch._C._cuda_isCurrentStreamCapturing():
         return lora_kv4_attention_workspace(device)  # zeroed by each replay
     ws = _ATTN_WS.get((device.index, raw))
     if ws is None:
