@@ -554,9 +554,11 @@ int lora_kv4_read(const void *pages, int64_t num_pages, int page_size, int kv_he
  * past the table are not seen (LORA_DEV_ERR_PAGE / LORA_DEV_ERR_LENGTH).  A row
  * that sees nothing, and rows outside every request, get zeros (lse -inf).
  * What the cache holds at tokens that are not seen has no influence.
- * workspace: lora_kv4_attention_workspace_size() bytes, 256-byte aligned.  Its
- * first lora_kv4_attention_zeroed_bytes() bytes must be zero before its first
- * use and are left zero; calls that may overlap need workspaces of their own.
+ * Magnitudes of q are taken up to 2^100; scores of any size are.
+ * workspace: lora_kv4_attention_workspace_size() bytes (some 47 MB, for any batch),
+ * 256-byte aligned.  Its first lora_kv4_attention_zeroed_bytes() bytes must be
+ * zero before its first use and are left zero; calls that may overlap (a graph's
+ * replays among them) need workspaces of their own.
  */
 size_t lora_kv4_attention_workspace_size(void);
 size_t lora_kv4_attention_zeroed_bytes(void);

@@ -153,9 +153,11 @@ struct Kv4Rows {
 // plane), so rows may lie anywhere.  Values: a lane has rows 2 c and 2 c + 1 and
 // 8 dims of each group; where the two are one pair of a tile, as in a prompt
 // begun at an even place, its words are whole, else they go by halves.
-// Bound: HBM (2 bytes a value against 0.56 of the cache) and the instructions of
-// the quantisation, about 8 a value; 8192 rows of 8 heads of 128 stored and read
-// back: 27.6 us, 3.1 TB/s of the 86 MB that both move (12 CTAs an SM; at 8: 29.7).
+// Bound: the chain of a task (slots, rows, their shuffles, stores) and its
+// instructions, 23 a value stored and 14 a value read: issue slots are two thirds
+// full while an SM is active, half of the whole time, and most other cycles wait for
+// rows.  HBM would allow 12.8 us of 8192 rows of 8 heads of 128 stored and read back:
+// 27.7 us, 3.1 TB/s of the 86 MB that both move (12 CTAs an SM; at 8: 29.7).
 template <int D, bool BF16, bool STORE>
 __global__ void __launch_bounds__(kKvThreads, 12) kv4_rows_kernel(const Kv4Rows a) {
   constexpr int W = D < 128 ? D : 128, NP = D / W, WD = W / 32, GP = WD / 2;  // GP groups a plane

@@ -21,17 +21,20 @@
 // the m of each group and ones as its rows.  q is brought to f16 by a power of
 // two of its row (exact: 8 or 11 significant bits).  p is 2^6 exp2(s - max)
 // with a running maximum that follows lazily (p <= 2^14), rounded to f16 once;
-// p s is rounded to f16 with s taken relative to the largest so far.  Both
-// keep 11 bits down to 2^-20 of the largest weight.  Sums are float32.
+// p s is rounded to f16 with s taken relative to the largest so far of all groups of
+// the head.  Both keep 11 bits down to 2^-20 of the largest weight (p s where the
+// group's steps are as large as the largest; of one whose steps are 2^-k of
+// that, down to 2^(k - 20)).  Sums are float32.
 //
 // A warp works on units of two tiles, so that waits, votes and page look-ups
 // are paid once for 32 tokens.
 //
 // Bound: HBM for the cache's bytes, then what surrounds the stream.  bf16, 8
 // heads of 128, 4 query heads each: one context of 131072 tokens 44 us (151 MB,
-// 3.4 TB/s), of which its copies alone take 29 us, the arithmetic that they do
-// not cover 8 us and the joins of the 152 CTAs' parts 7 us; 64 requests of 256 to
-// 8192 tokens 52 us (170 MB, 3.3 TB/s); 256 of 17 to 2048 with 40 heads and as many
+// 3.4 TB/s; by the clocks of an instrumented copy of the kernel its copies alone take
+// 29 us, the arithmetic that they do not cover 8 us and the joins of the 152 CTAs'
+// parts 7 us; issue slots are 55% full while an SM is active); 64 requests of 256 to
+// 8192 tokens 52 us (170 MB, 3.2 TB/s); 256 of 17 to 2048 with 40 heads and as many
 // query heads 159 us (624 MB, 3.9 TB/s, where the instructions of the units' loop
 // count: a matrix product's 8 columns hold one row).
 #pragma once

@@ -34,12 +34,16 @@
 // 2^7 p with p <= 2^8.
 //
 // Bound: the chain of a half's softmax, its two products and the expansion that
-// refills their operands; issue slots are 60% full, the tensor cores 40%.  bf16, 8 heads of 128, 4
-// query heads each: one prompt of 8192 tokens 490 us (1120 TFLOP/s), 32 prompts
-// 104 us, chunks behind 16 thousand tokens 253 us (670 TFLOP/s).  Two places of
-// 64 columns of scores a half, so that its softmax need not wait, took 650 us of
-// the first: with more roles at once a third of the warps waited for instructions;
-// an MMA warp a half, or one each for S and O, took no less; four operands in flight 600 us against 575.
+// refills their operands; issue slots are 60% full, the tensor cores 40%.  bf16, 8
+// heads of 128, 4 query heads each: one prompt of 8192 tokens 479 us (1148
+// TFLOP/s), 32 prompts 110 us, chunks behind 16 thousand tokens 247 us (687 TFLOP/s).
+// An item's first keys wait for the guard and so for its q, about 1 us an item (32
+// prompts 104 us without); the MMA warp's first product ahead of the guard's word took
+// 590 us of the first case, its loop no longer uniform.  Two places of 64 columns of
+// scores a half, so that its softmax need not wait, took 650 us of the first where this
+// took 531: with more roles at once a third of the warps waited for instructions; an
+// MMA warp a half, or one each for S and O, took no less; four operands in flight 600
+// us against 575.
 #pragma once
 
 #include "kv4_attn.cuh"
@@ -124,7 +128,7 @@ __device__ __forceinline__ int pre_rows(const AttnArgs& a, int b, int min_rows, 
 
 // SPLIT: where items are so few that half the CTAs or more had none, each item's
 // tiles are shared out over `parts` CTAs, whose results the last of them joins (48
-// rows over 65536 tokens: 939 -> 101 us; 512 tokens over 16384: 272 -> 171).  A
+// rows over 65536 tokens: 939 -> 101 us; 512 tokens over 16384: 272 -> 162).  A
 // kernel of its own, since what it adds costs the other 15%.
 struct PreSplit {
   int parts, part;
