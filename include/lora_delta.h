@@ -570,6 +570,108 @@ int lora_kv4_attention(void *out, int64_t ld_out, const void *q, int64_t ld_q, i
                        size_t ws_bytes, uint32_t *err_word, lora_stream_t stream);
 
 /*
+ * The routed-expert layer around the deltas.  A pair p = t * top_k + j sends
+ * token t to expert topk_ids[t, j].  A layer's order is lora_moe_dispatch,
+ * lora_moe_linear (with the delta that lora_moe_fc1_delta leaves for the sorted
+ * rows: T = their number, top_k = 1, topk_ids = row_expert, lora_ids =
+ * row_lora), lora_moe_linear again, lora_moe_w2_delta likewise, lora_moe_combine.
+ * None of the pages has these calls.  Matrices hold 16-bit values, row-major
+ * with row strides ld in elements, multiples of 8 (of one row it does not
+ * matter), 16-byte aligned; H, k_in, n_out are multiples of 8 (LORA_ERR_ALIGN).
+ * No output may share memory with another argument (LORA_ERR_ARG), but for
+ * `out` with `residual` as stated.  Columns of one buffer may interleave.
+ * Limits: E <= 2048, top_k <= 64, T * top_k < 2^30 (LORA_ERR_UNSUPPORTED).
+ */
+#define LORA_MOE_MAX_TOP_K 64
+
+/*
+ * lora_moe_dispatch -- the tokens' rows sorted by expert, stable in p, and the
+ * plan that leads back.
+ *   topk_ids [T, top_k] int32: -1 is no expert (a padded token), silently; an id
+ *     outside [0, E) gets no row either, with LORA_DEV_ERR_EXPERT.
+ *   expert_map [n_global_experts] int32 or NULL: as in lora_moe_w13_delta, global
+ *     expert id -> this rank's id, -1 = not on this rank (no row).
+ *   lora_ids [T] int32 or NULL (all -1): the token's adapter.
+ *   seg_start [E + 1] int32 (out): expert e's rows are seg_start[e] ..
+ *     seg_start[e + 1] - 1; seg_start[0] is 0.
+ *   pair_row [T, top_k] int32 (out): the pair's row, -1: none.
+ *   row_pair, row_expert, row_lora [T * top_k] int32 (out): the row's pair, expert
+ *     and its token's adapter; -1 from row seg_start[E] on.
+ *   rows [T * top_k, H] (out): rows[pair_row[t, j]] = x[t]; rows from seg_start[E]
+ *     on are left as they were.
+ * The gradient for x is lora_moe_combine of the rows' gradients without weights.
+ */
+int lora_moe_dispatch(void *rows, int64_t ld_rows, int32_t *seg_start, int32_t *row_pair,
+                      int32_t *pair_row, int32_t *row_expert, int32_t *row_lora, const void *x,
+                      int64_t ld_x, const int32_t *topk_ids, const int32_t *lora_ids,
+                      const int32_t *expert_map, int n_global_experts, int T, int top_k, int E,
+                      int H, uint32_t *err_word, lora_stream_t stream);
+
+/*
+ * lora_moe_combine -- the rows back at their tokens:
+ *   out[t] = RN(residual[t] + sum_j weights[t, j] * rows[pair_row[t, j]])
+ * over the pairs that have a row (pair_row inside [0, T * top_k)), in float32 and
+ * in the order of j.  weights [T, top_k] float32 or NULL (1); residual [T, H] or
+ * NULL (0), which may be `out` itself with the same row stride.  A token without a
+ * row gets its residual.  dtype: LORA_BF16 or LORA_F16.
+ */
+int lora_moe_combine(void *out, int64_t ld_out, const void *rows, int64_t ld_rows,
+                     const int32_t *pair_row, const float *weights, const void *residual,
+                     int64_t ld_residual, int T, int top_k, int H, int dtype,
+                     lora_stream_t stream);
+
+/*
+ * lora_moe_combine_grad -- the gradient of lora_moe_combine for its rows and
+ * weights (that for the residual is grad_out itself):
+ *   grad_rows[pair_row[t, j]] = RN(weights[t, j] * grad_out[t])
+ *   grad_weights[t, j] = grad_out[t] . rows[pair_row[t, j]]   (float32; 0 without a row)
+ * grad_weights [T, top_k] float32 or NULL.  Rows that no pair has are left as
+ * they were.
+ */
+int lora_moe_combine_grad(void *grad_rows, int64_t ld_grad_rows, float *grad_weights,
+                          const void *grad_out, int64_t ld_grad_out, const void *rows,
+                          int64_t ld_rows, const int32_t *pair_row, const float *weights, int T,
+                          int top_k, int H, int dtype, lora_stream_t stream);
+
+/* activations of the products below */
+#define LORA_ACT_NONE 0
+#define LORA_ACT_RELU 1
+#define LORA_ACT_SILU 2
+#define LORA_ACT_GELU 3      /* 0.5 z (1 + erf(z / sqrt 2)) */
+#define LORA_ACT_GELU_TANH 4 /* 0.5 z (1 + tanh(sqrt(2 / pi) (z + 0.044715 z^3))) */
+
+/*
+ * lora_linear -- the base layer that a delta belongs to: x [n, k_in] times
+ * w [n_out, k_in] transposed, with everything after it in one pass:
+ *   z = x w^T + bias + delta                        (float32)
+ *   out = RN(act(z) + residual)                     gated == 0: [n, n_out]
+ *   out = RN(act(z[:, :I]) * z[:, I:] + residual)   gated == 1: [n, I], I = n_out / 2
+ * bias [n_out], delta [n, n_out], residual (as out) or NULL, of x's type; the
+ * residual may be `out` itself with the same row stride.  delta is added ahead
+ * of the activation, where an adapter's part belongs.  gated == 1 needs n_out a
+ * multiple of 16.
+ */
+int lora_linear(void *out, int64_t ld_out, const void *x, int64_t ld_x, int n, int k_in,
+                const void *w, int64_t ld_w, int n_out, const void *bias, const void *delta,
+                int64_t ld_delta, const void *residual, int64_t ld_residual, int activation,
+                int gated, int dtype, uint32_t *err_word, lora_stream_t stream);
+
+/*
+ * lora_moe_linear -- lora_linear for sorted rows, each expert's with its own
+ * weights: rows seg_start[e] .. seg_start[e + 1] - 1 take w + e * stride_w
+ * elements and bias [E, n_out].  seg_start [E + 1] int32 (device), as
+ * lora_moe_dispatch writes it, must be nondecreasing within [0, n]; starts outside
+ * are clamped with LORA_DEV_ERR_SEGMENT, and what rows get then is not specified.
+ * Rows outside every segment are left as they were, and what x, delta and residual
+ * hold there has no influence.
+ */
+int lora_moe_linear(void *out, int64_t ld_out, const void *rows, int64_t ld_rows, int n, int k_in,
+                    const int32_t *seg_start, int E, const void *w, int64_t ld_w,
+                    int64_t stride_w, int n_out, const void *bias, const void *delta,
+                    int64_t ld_delta, const void *residual, int64_t ld_residual, int activation,
+                    int gated, int dtype, uint32_t *err_word, lora_stream_t stream);
+
+/*
  * lora_get_error -- copy the device error word to *host_out after all work
  * queued on `stream` so far has finished (this call synchronizes `stream`),
  * then clear it on the device when `clear` is nonzero.

@@ -65,6 +65,14 @@ SIGNATURES = {
     "lora_kv4_attention_zeroed_bytes": (_sz, []),
     "lora_kv4_attention": (_i, [_vp, _i64, _vp, _i64, _i, _i, _vp, _i64, _i, _i, _i, _i, _vp, _i64,
                                 _i, _vp, _vp, _i, _i, _f, _i, _vp, _vp, _sz, _vp, _vp]),
+    "lora_moe_dispatch": (_i, [_vp, _i64, _vp, _vp, _vp, _vp, _vp, _vp, _i64, _vp, _vp, _vp, _i, _i, _i,
+                               _i, _i, _vp, _vp]),
+    "lora_moe_combine": (_i, [_vp, _i64, _vp, _i64, _vp, _vp, _vp, _i64, _i, _i, _i, _i, _vp]),
+    "lora_moe_combine_grad": (_i, [_vp, _i64, _vp, _vp, _i64, _vp, _i64, _vp, _vp, _i, _i, _i, _i, _vp]),
+    "lora_linear": (_i, [_vp, _i64, _vp, _i64, _i, _i, _vp, _i64, _i, _vp, _vp, _i64, _vp, _i64, _i, _i,
+                         _i, _vp, _vp]),
+    "lora_moe_linear": (_i, [_vp, _i64, _vp, _i64, _i, _i, _vp, _i, _vp, _i64, _i64, _i, _vp, _vp, _i64,
+                             _vp, _i64, _i, _i, _i, _vp, _vp]),
 }
 
 _LIB = None

@@ -1,0 +1,175 @@
+"""The routed-expert layer around the deltas: tokens sorted by expert and back, and matrix products with bias, delta,
+activation and residual in one pass, dense or over the experts' rows.
+
+As in the rest of the binding, every function only marshals tensors into the C ABI of ``include/lora_delta.h`` (where
+layouts, limits and errors are stated) on torch's current CUDA stream, and turns a nonzero status into ``LoraError``.
+Tensors must be on the current device.
+"""
+from __future__ import annotations
+
+import torch
+
+from .serve import _DTYPES, _check, _err_at, _Fixed, _fn, _raw_stream
+
+_ACTIVATIONS = {"none": 0, None: 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4}
+
+
+def _here(t, name):
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.get_device() != torch._C._cuda_getDevice():
+        raise ValueError(f"{name} is on {t.device}, not on the current device")
+
+
+def _matrix(t, name, dtype, rows, width):
+    """Pointer and row stride of a [rows, width] tensor with adjacent columns; rows may lie apart."""
+    _here(t, name)
+    if t.dtype is not dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.dim() != 2 or t.shape[0] != rows or t.shape[1] != width:
+        raise ValueError(f"{name} must be [{rows}, {width}], got {tuple(t.shape)}")
+    ld, step = t.stride()
+    if step != 1 and width > 1:
+        raise ValueError(f"{name}'s columns must be adjacent")
+    return t.data_ptr(), (ld if rows > 1 else width)
+
+
+def _whole(t, name, dtype, shape):
+    """Pointer of a contiguous tensor of this shape, or None."""
+    if t is None:
+        return None
+    _here(t, name)
+    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor {tuple(shape)}, got {t.dtype} {tuple(t.shape)}")
+    return t.data_ptr()
+
+
+def _rows_dtype(t, name):
+    if t.dtype not in _DTYPES:
+        raise ValueError(f"{name} must be bfloat16 or float16, not {t.dtype}")
+    return t.dtype
+
+
+class MoePlan(_Fixed):
+    """What ``lora_moe_dispatch`` writes for ``T`` tokens of ``top_k`` experts among ``E``: ``seg_start`` [E + 1], ``pair_row``
+    [T, top_k], ``row_pair``, ``row_expert`` and ``row_lora`` [T * top_k], all int32.  Until then no pair has a row."""
+
+    def __init__(self, T: int, top_k: int, E: int, device="cuda"):
+        if torch.device(device).type != "cuda":
+            raise ValueError(f"a plan's tensors are the GPU's, not {device}'s")
+        if T < 0 or top_k < 1 or E < 1:
+            raise ValueError(f"a plan of {T} tokens, {top_k} experts each of {E}")
+        self.T, self.top_k, self.E, self.n_rows = int(T), int(top_k), int(E), int(T) * int(top_k)
+
+        def ints(*shape, value=-1):
+            return torch.full(shape, value, dtype=torch.int32, device=device)
+
+        self.seg_start, self.pair_row = ints(self.E + 1, value=0), ints(self.T, self.top_k)
+        self.row_pair, self.row_expert, self.row_lora = (ints(self.n_rows) for _ in range(3))
+        self._seg, self._pair = self.seg_start.data_ptr(), self.pair_row.data_ptr()
+        self._out = (self._seg, self.row_pair.data_ptr(), self._pair, self.row_expert.data_ptr(), self.row_lora.data_ptr())
+
+
+def lora_moe_dispatch(rows, x, topk_ids, plan: MoePlan, lora_ids=None, expert_map=None, err=None, stream=None) -> MoePlan:
+    """Sort the tokens by expert into ``plan`` and their rows ``x`` [T, H] into ``rows`` [T * top_k, H].
+
+    ``topk_ids`` [T, top_k] int32, -1 for a padded token; ``lora_ids`` [T] int32 the tokens' adapters; ``expert_map`` int32 the
+    global experts' numbers on this rank, -1 elsewhere.  The gradient for x is ``lora_moe_combine(grad_x, grad_rows, plan)``."""
+    T, k = plan.T, plan.top_k
+    H, dtype = x.shape[-1], _rows_dtype(x, "x")
+    _here(plan.seg_start, "plan")
+    x_at, ld_x = _matrix(x, "x", dtype, T, H)
+    rows_at, ld_rows = _matrix(rows, "rows", dtype, plan.n_rows, H)
+    n_map = 0
+    if expert_map is not None:
+        n_map = expert_map.numel()
+        expert_map = _whole(expert_map, "expert_map", torch.int32, (n_map,))
+    _check("lora_moe_dispatch", _fn.lora_moe_dispatch(
+        rows_at, ld_rows, *plan._out, x_at, ld_x, _whole(topk_ids, "topk_ids", torch.int32, (T, k)),
+        _whole(lora_ids, "lora_ids", torch.int32, (T,)), expert_map, n_map, T, k, plan.E, H, _err_at(err), _raw_stream(stream)))
+    return plan
+
+
+def lora_moe_combine(out, rows, plan: MoePlan, weights=None, residual=None, stream=None):
+    """``out[t] = residual[t] + sum_j weights[t, j] rows[plan.pair_row[t, j]]``, over the pairs that have a row.
+
+    ``weights`` [T, top_k] float32 (1 without); ``residual`` [T, H] may be ``out`` itself.  Without either it is the gradient
+    of ``lora_moe_dispatch``."""
+    T, H, dtype = plan.T, out.shape[-1], _rows_dtype(out, "out")
+    _here(plan.seg_start, "plan")
+    out_at, ld_out = _matrix(out, "out", dtype, T, H)
+    rows_at, ld_rows = _matrix(rows, "rows", dtype, plan.n_rows, H)
+    res_at, ld_res = (None, 0) if residual is None else _matrix(residual, "residual", dtype, T, H)
+    _check("lora_moe_combine", _fn.lora_moe_combine(
+        out_at, ld_out, rows_at, ld_rows, plan._pair, _whole(weights, "weights", torch.float32, (T, plan.top_k)), res_at, ld_res,
+        T, plan.top_k, H, _DTYPES[dtype], _raw_stream(stream)))
+
+
+def lora_moe_combine_grad(grad_rows, grad_weights, grad_out, rows, plan: MoePlan, weights=None, stream=None):
+    """The gradient of ``lora_moe_combine`` for its rows, into ``grad_rows`` (rows that no pair has stay as they were), and for
+    its weights, into ``grad_weights`` [T, top_k] float32 or None.  That for the residual is ``grad_out`` itself."""
+    T, H, dtype = plan.T, grad_out.shape[-1], _rows_dtype(grad_out, "grad_out")
+    _here(plan.seg_start, "plan")
+    go_at, ld_go = _matrix(grad_out, "grad_out", dtype, T, H)
+    rows_at, ld_rows = _matrix(rows, "rows", dtype, plan.n_rows, H)
+    gr_at, ld_gr = _matrix(grad_rows, "grad_rows", dtype, plan.n_rows, H)
+    _check("lora_moe_combine_grad", _fn.lora_moe_combine_grad(
+        gr_at, ld_gr, _whole(grad_weights, "grad_weights", torch.float32, (T, plan.top_k)), go_at, ld_go, rows_at, ld_rows,
+        plan._pair, _whole(weights, "weights", torch.float32, (T, plan.top_k)), T, plan.top_k, H, _DTYPES[dtype],
+        _raw_stream(stream)))
+
+
+def _activation(name):
+    if name not in _ACTIVATIONS:
+        raise ValueError(f"activation must be one of {sorted(k for k in _ACTIVATIONS if k)}, got {name!r}")
+    return _ACTIVATIONS[name]
+
+
+def _epilogue(delta, residual, dtype, n, N, width):
+    d = (None, 0) if delta is None else _matrix(delta, "delta", dtype, n, N)
+    r = (None, 0) if residual is None else _matrix(residual, "residual", dtype, n, width)
+    return *d, *r
+
+
+def lora_linear(out, x, weight, bias=None, delta=None, residual=None, activation="none", gated: bool = False, err=None,
+                stream=None):
+    """``out = act(x weight^T + bias + delta) + residual``; gated: ``act(z[:, :I]) * z[:, I:] + residual`` of z [n, 2 I].
+
+    ``x`` [n, k_in], ``weight`` [n_out, k_in], ``bias`` [n_out], ``delta`` [n, n_out] (what the LoRA calls leave: it goes
+    ahead of the activation), all bfloat16 or all float16, and ``residual`` as ``out``, which it may be itself.  ``activation``:
+    "none", "relu", "silu", "gelu" (by erf) or "gelu_tanh"."""
+    dtype, n = _rows_dtype(x, "x"), x.shape[0]
+    if weight.dim() != 2:
+        raise ValueError(f"weight must be [n_out, k_in], got {tuple(weight.shape)}")
+    N, K = weight.shape
+    width = N // 2 if gated else N
+    x_at, ld_x = _matrix(x, "x", dtype, n, K)
+    w_at, ld_w = _matrix(weight, "weight", dtype, N, K)
+    out_at, ld_out = _matrix(out, "out", dtype, n, width)
+    _check("lora_linear", _fn.lora_linear(
+        out_at, ld_out, x_at, ld_x, n, K, w_at, ld_w, N, _whole(bias, "bias", dtype, (N,)),
+        *_epilogue(delta, residual, dtype, n, N, width), _activation(activation), 1 if gated else 0, _DTYPES[dtype],
+        _err_at(err), _raw_stream(stream)))
+
+
+def lora_moe_linear(out, rows, weight, plan: MoePlan, bias=None, delta=None, residual=None, activation="none",
+                    gated: bool = False, err=None, stream=None):
+    """``lora_linear`` of the sorted ``rows`` [T * top_k, k_in] of ``plan``, expert e's with ``weight[e]`` of [E, n_out, k_in] and
+    ``bias[e]`` of [E, n_out].  ``delta`` and ``residual`` are in the rows' order.  Rows behind the last expert's are left as
+    they were."""
+    dtype, n = _rows_dtype(rows, "rows"), plan.n_rows
+    _here(weight, "weight")
+    _here(plan.seg_start, "plan")
+    if weight.dtype is not dtype or weight.dim() != 3 or weight.shape[0] != plan.E:
+        raise ValueError(f"weight must be {dtype} [{plan.E}, n_out, k_in], got {weight.dtype} {tuple(weight.shape)}")
+    E, N, K = weight.shape
+    stride_w, ld_w, step = weight.stride()
+    if step != 1 and K > 1:
+        raise ValueError("weight's columns must be adjacent")
+    width = N // 2 if gated else N
+    x_at, ld_x = _matrix(rows, "rows", dtype, n, K)
+    out_at, ld_out = _matrix(out, "out", dtype, n, width)
+    _check("lora_moe_linear", _fn.lora_moe_linear(
+        out_at, ld_out, x_at, ld_x, n, K, plan._seg, E, weight.data_ptr(), ld_w if N > 1 else K, stride_w, N,
+        _whole(bias, "bias", dtype, (E, N)), *_epilogue(delta, residual, dtype, n, N, width), _activation(activation),
+        1 if gated else 0, _DTYPES[dtype], _err_at(err), _raw_stream(stream)))
