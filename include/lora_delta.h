@@ -659,7 +659,7 @@ int lora_linear(void *out, int64_t ld_out, const void *x, int64_t ld_x, int n, i
 /*
  * lora_moe_linear -- lora_linear for sorted rows, each expert's with its own
  * weights: rows seg_start[e] .. seg_start[e + 1] - 1 take w + e * stride_w
- * elements and bias [E, n_out].  seg_start [E + 1] int32 (device), as
+ * elements (a multiple of ld_w) and bias [E, n_out].  seg_start [E + 1] int32 (device), as
  * lora_moe_dispatch writes it, must be nondecreasing within [0, n]; starts outside
  * are clamped with LORA_DEV_ERR_SEGMENT, and what rows get then is not specified.
  * Rows outside every segment are left as they were, and what x, delta and residual

@@ -444,22 +444,7 @@ int prepare_rows(DeltaArgs& a, const int32_t* seq_slot, int n, int max_loras, in
 }
 
 // 2-D tensor maps for TMA loads of row blocks (128 rows x 64 columns, bf16,
-// 128-byte swizzle) of a row-major [rows, cols] matrix with leading dimension
-// ld; the encoder comes from the driver through the runtime, looked up once.
-PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
-  static const PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
-    void* p = nullptr;
-    cudaDriverEntryPointQueryResult q = cudaDriverEntryPointSymbolNotFound;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault,
-                                         &q) != cudaSuccess ||
-        q != cudaDriverEntryPointSuccess) {
-      cudaGetLastError();
-      p = nullptr;
-    }
-    return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
-  }();
-  return fn;
-}
+// 128-byte swizzle) of a row-major [rows, cols] matrix with leading dimension ld.
 bool encode_row_blocks(CUtensorMap* m, const void* base, int64_t rows, int64_t cols, int64_t ld) {
   const PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
   if (!enc || rows < 1 || cols < 1) return false;

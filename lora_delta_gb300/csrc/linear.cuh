@@ -3,10 +3,20 @@
 //   z = x[r] W^T + bias + delta[r]
 //   out[r] = act(z) + residual[r], or act(z[0:I]) * z[I:2I] + residual[r]
 // summed in float32 and rounded once.
+//
+// W's rows are the M side of the tensor cores' products (128 a CTA) and x's rows
+// the N side, whose size a product takes as it comes: a segment of 40 rows costs
+// 48 columns, not a tile of 128.  Gated, a CTA's 128 rows are 64 of each half.
+// The sums go through shared memory to the threads that finish 8 columns of a
+// row of out, where delta and residual are read and out is written whole sectors
+// at a time.
 #pragma once
+
+#include <cuda.h>
 
 #include "common.cuh"
 #include "moe.cuh"
+#include "tc.cuh"
 
 namespace lora {
 
@@ -48,62 +58,459 @@ __device__ __forceinline__ float activate(float z, int act) {
   }
 }
 
-template <bool BF16>
-__device__ __forceinline__ float elem(const void* base, int64_t i) {
-  return BF16 ? __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(base)[i])
-              : __half2float(reinterpret_cast<const __half*>(base)[i]);
+// -------------------------------------------------------------- epilogue --
+// 8 columns of a row of out: what is read for them, ahead of the sums, and what
+// becomes of the sums z (and up, the second half's).
+struct LinearTail {
+  uint4 bias[2], delta[2], residual;
+};
+
+__device__ __forceinline__ LinearTail linear_tail(const LinearArgs& a, int g, int64_t row, int col, bool ok) {
+  LinearTail t;
+  const uint4 none = make_uint4(0, 0, 0, 0);
+  t.bias[0] = t.bias[1] = t.delta[0] = t.delta[1] = t.residual = none;
+  if (!ok) return t;
+  const uint16_t* b = reinterpret_cast<const uint16_t*>(a.bias) + (int64_t)g * a.N + col;
+  if (a.bias) t.bias[0] = *reinterpret_cast<const uint4*>(b);
+  if (a.delta) t.delta[0] = load8(a.delta, a.ld_delta, row, col);
+  if (a.gated) {
+    if (a.bias) t.bias[1] = *reinterpret_cast<const uint4*>(b + a.n_out);
+    if (a.delta) t.delta[1] = load8(a.delta, a.ld_delta, row, a.n_out + col);
+  }
+  if (a.residual) t.residual = load8(a.residual, a.ld_residual, row, col);
+  return t;
 }
 
-// A tile of 64 rows x 64 columns a CTA, 4 x 4 a thread.
 template <bool BF16>
-__global__ void __launch_bounds__(256) linear_simple_kernel(const LinearArgs a) {
-  __shared__ float xs[16][65], ws[2][16][65];
+__device__ __forceinline__ void add8(float* z, const uint4& v) {
+  float f[8];
+  unpack8<BF16>(v, f);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) z[i] += f[i];
+}
+
+template <bool BF16>
+__device__ __forceinline__ void linear_finish(const LinearArgs& a, const LinearTail& t, int64_t row, int col, float* z, float* up) {
+  if (a.bias) add8<BF16>(z, t.bias[0]);
+  if (a.delta) add8<BF16>(z, t.delta[0]);
+  if (a.act != LORA_ACT_NONE) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) z[i] = activate(z[i], a.act);
+  }
+  if (a.gated) {
+    if (a.bias) add8<BF16>(up, t.bias[1]);
+    if (a.delta) add8<BF16>(up, t.delta[1]);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) z[i] *= up[i];
+  }
+  if (a.residual) add8<BF16>(z, t.residual);
+  store8(a.out, a.ld_out, row, col, pack8<BF16>(z));
+}
+
+// ------------------------------------------------------------- few rows --
+// A tile is 128 rows of W and up to NT of x.  The CTAs of a cluster share a
+// tile's K out, so that few tiles still read W at the card's full rate; their
+// parts are added in the order of K through distributed shared memory, each CTA
+// finishing its share of the tile.  Grid: (feature tile, part of K), group, and
+// row tiles in turn.  Two CTAs fit an SM.
+template <int NT_>
+struct Few {
+  static constexpr int NT = NT_;
+  static constexpr int W = 128 * 128, X = NT * 128, STAGE = W + X;
+  static constexpr int STAGES = 106 * 1024 / STAGE < 8 ? 106 * 1024 / STAGE : 8;
+  static constexpr int PAD = 132;  // floats between rows of a part
+  static constexpr int THREADS = 192;
+  static constexpr uint32_t COLS = NT < 32 ? 32 : NT;  // of tensor memory
+  static constexpr size_t smem() { return 1024 + (size_t)STAGES * STAGE; }
+  static_assert(NT * PAD * 4 <= STAGES * STAGE, "a part lies where the operands were");
+};
+
+template <bool BF16, class C>
+__global__ void __launch_bounds__(C::THREADS) linear_few_kernel(const LinearArgs a, const __grid_constant__ CUtensorMap map_w,
+                                                               const __grid_constant__ CUtensorMap map_x, int split) {
+  extern __shared__ uint8_t few_smem_raw[];
+  __shared__ uint64_t full[C::STAGES], empty[C::STAGES], done;
+  __shared__ uint32_t taddr_s;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  uint8_t* smem = few_smem_raw + ((1024 - (smem_addr(few_smem_raw) & 1023)) & 1023);
+  const int part = blockIdx.x % split, ft = blockIdx.x / split, g = blockIdx.y;
+  const int blocks = (a.K + 63) / 64;
+  const int kb0 = (int)((int64_t)blocks * part / split), nkb = (int)((int64_t)blocks * (part + 1) / split) - kb0;
+  if (tid == 0) {
+    for (int i = 0; i < C::STAGES; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], 1);
+    }
+    mbar_init(&done, 1);
+    fence_barrier_init();
+  }
   cudaGridDependencySynchronize();
-  const int tid = threadIdx.x, tr = tid / 16, tc = tid % 16, c0 = blockIdx.x * 64, g = blockIdx.y;
+  if (warp == 1) tc::tmem_alloc(&taddr_s, C::COLS);
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  const uint32_t tmem = taddr_s;
   uint32_t bad = 0;
   const int2 seg = group_rows(a, g, bad);
   if (bad && tid == 0) set_error(a.err, bad);
-  const int halves = a.gated ? 2 : 1;
-  for (int r0 = seg.x + blockIdx.z * 64; r0 < seg.y; r0 += gridDim.z * 64) {
-    float acc[2][4][4] = {};
-    for (int k0 = 0; k0 < a.K; k0 += 16) {
-      for (int i = tid; i < 16 * 64; i += 256) {
-        const int r = i / 16, k = k0 + i % 16;
-        xs[i % 16][r] = r0 + r < seg.y && k < a.K ? elem<BF16>(a.x, (int64_t)(r0 + r) * a.ld_x + k) : 0.0f;
-        for (int h = 0; h < halves; ++h)
-          ws[h][i % 16][r] = c0 + r < a.n_out && k < a.K
-                                 ? elem<BF16>(a.w, (int64_t)g * a.stride_w + (int64_t)(h * a.n_out + c0 + r) * a.ld_w + k)
-                                 : 0.0f;
-      }
-      __syncthreads();
-      for (int k = 0; k < 16; ++k)
-        for (int h = 0; h < halves; ++h)
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) acc[h][i][j] = fmaf(xs[k][tr * 4 + i], ws[h][k][tc + 16 * j], acc[h][i][j]);
-      __syncthreads();
-    }
-    for (int i = 0; i < 4; ++i)
-      for (int j = 0; j < 4; ++j) {
-        const int64_t r = r0 + tr * 4 + i;
-        const int c = c0 + tc + 16 * j;
-        if (r >= seg.y || c >= a.n_out) continue;
-        float z[2];
-        for (int h = 0; h < halves; ++h) {
-          z[h] = acc[h][i][j];
-          if (a.bias) z[h] += elem<BF16>(a.bias, (int64_t)g * a.N + h * a.n_out + c);
-          if (a.delta) z[h] += elem<BF16>(a.delta, r * a.ld_delta + h * a.n_out + c);
+  bool ok = true, dead = false;  // (dead: known to all threads of the CTA)
+  uint32_t it = 0;               // steps of K so far
+  uint32_t tiles = 0;
+  for (int r0 = seg.x + (int)blockIdx.z * C::NT; r0 < seg.y; r0 += (int)gridDim.z * C::NT, ++tiles) {
+    const int rows = min(C::NT, seg.y - r0), boxes = (rows + 15) / 16;
+    if (!dead) {
+      if (warp == 0) {
+        if (lane == 0) {
+          for (int i = 0; i < nkb; ++i, ++it) {
+            const int s = it % C::STAGES;
+            if (it >= C::STAGES && !mbar_wait_bounded(&empty[s], (it / C::STAGES - 1) & 1, a.wait_ns)) {
+              ok = false;
+              break;
+            }
+            mbar_arrive_expect_tx(&full[s], C::W + boxes * 2048);
+            uint8_t* st = smem + s * C::STAGE;
+            if (a.gated) {
+              tma_load_3d(st, &map_w, (kb0 + i) * 64, ft * 64, g, &full[s]);
+              tma_load_3d(st + 64 * 128, &map_w, (kb0 + i) * 64, a.n_out + ft * 64, g, &full[s]);
+            } else {
+              tma_load_3d(st, &map_w, (kb0 + i) * 64, ft * 128, g, &full[s]);
+            }
+            for (int b = 0; b < boxes; ++b) tma_load_2d(st + C::W + b * 2048, &map_x, (kb0 + i) * 64, r0 + b * 16, &full[s]);
+          }
         }
-        float y = activate(z[0], a.act);
-        if (a.gated) y *= z[1];
-        if (a.residual) y += elem<BF16>(a.residual, r * a.ld_residual + c);
-        if (BF16)
-          reinterpret_cast<__nv_bfloat16*>(a.out)[r * a.ld_out + c] = __float2bfloat16_rn(y);
-        else
-          reinterpret_cast<__half*>(a.out)[r * a.ld_out + c] = __float2half_rn(y);
+      } else if (warp == 1) {
+        if (lane == 0) {
+          const uint32_t id = BF16 ? tc::idesc_bf16_f32(128, boxes * 16) : tc::idesc_f16_f32(128, boxes * 16);
+          for (int i = 0; i < nkb; ++i, ++it) {
+            const int s = it % C::STAGES;
+            if (!mbar_wait_bounded(&full[s], (it / C::STAGES) & 1, a.wait_ns)) {
+              ok = false;
+              break;
+            }
+            tc::fence_after_sync();
+            const uint32_t at = smem_addr(smem + s * C::STAGE);
+            const uint64_t wd = tc::sw128_desc(at), xd = tc::sw128_desc(at + C::W);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) tc::mma_bf16(tmem, wd + q * 2, xd + q * 2, id, i > 0 || q > 0);
+            tc::mma_commit(&empty[s]);
+          }
+          // (every product issued is awaited, a failed loop's too)
+          tc::mma_commit(&done);
+          if (!mbar_wait_bounded(&done, tiles & 1, ok ? a.wait_ns : kWaitLimitNs)) ok = false;
+        }
       }
+      dead = !__syncthreads_and(ok);
+      if (dead && tid == 0) {
+        set_error(a.err, LORA_DEV_ERR_TIMEOUT);
+        // (this thread's copies in flight write to the CTA's memory)
+        for (uint32_t j = it > C::STAGES ? it - C::STAGES : 0; j < it; ++j)
+          mbar_wait_bounded(&full[j % C::STAGES], (j / C::STAGES) & 1, kWaitLimitNs);
+      }
+    }
+    float* own = reinterpret_cast<float*>(smem);  // [rows][PAD]: this CTA's part of the sums
+    if (!dead && warp >= 2) {
+      tc::fence_after_sync();
+      const int q = warp & 3;
+      for (int c = 0; c < rows; c += 16) {
+        float v[16];
+        tc::tmem_ld16(tmem + ((uint32_t)(q * 32) << 16) + c, v);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) own[(c + i) * C::PAD + q * 32 + lane] = v[i];
+      }
+      tc::fence_before_sync();
+    }
+    __syncwarp();
+    cluster_arrive_release_smem();
+    cluster_wait();
+    if (!dead) {
+      const int width = a.gated ? 8 : 16, items = rows * width;  // (8 columns of out each)
+      for (int i = part * C::THREADS + tid; i < items; i += split * C::THREADS) {
+        const int r = i / width, b = i % width, col = (ft * width + b) * 8;
+        const bool use = col < a.n_out;
+        const LinearTail t = linear_tail(a, g, r0 + r, col, use);
+        float z[16] = {};
+        const uint32_t at = smem_addr(own + r * C::PAD + b * 8);
+        for (int p = 0; p < split; ++p) {
+          const uint32_t from = dsmem_map(at, p);
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            if (j < 2 || a.gated) {
+              const float4 f = dsmem_ld_f32x4(from + (j < 2 ? 16 * j : 256 + 16 * (j - 2)));
+              z[4 * j] += f.x;
+              z[4 * j + 1] += f.y;
+              z[4 * j + 2] += f.z;
+              z[4 * j + 3] += f.w;
+            }
+        }
+        if (use) linear_finish<BF16>(a, t, r0 + r, col, z, z + 8);
+      }
+    }
+    fence_proxy_async_smem();  // (the memory is next written by copies)
+    __syncwarp();
+    cluster_arrive();
+    cluster_wait();
   }
+  tc::fence_before_sync();
+  __syncthreads();
+  if (warp == 1) tc::tmem_dealloc(tmem, C::COLS);
+}
+
+// ------------------------------------------------------------ many rows --
+// A pair of CTAs works on a tile of 256 rows of W and up to 256 of x: each holds
+// half of both (cta_group::2), so that a step of 64 of K costs an SM 32 KB of
+// copies for 512 cycles of products.  Persistent: a load warp, an MMA warp (of
+// the even CTA) and 8 epilogue warps, the sums of one tile in one half of tensor
+// memory while the epilogue reads the other's.
+struct Pair {
+  static constexpr int W = 128 * 128, X = 128 * 128, STAGE = W + X, STAGES = 6;
+  static constexpr int EPI = 8, EPI_WARP = 4, THREADS = (EPI_WARP + EPI) * 32;
+  static constexpr int PAD = 36, BUF = 16 * PAD;  // floats: 16 rows of 32 sums
+  static constexpr int UNIT = 64;                 // rows that tiles are made of
+  static constexpr size_t smem(int groups) { return 1024 + (size_t)STAGES * STAGE + EPI * BUF * 4 + (size_t)(groups + 1) * 4; }
+};
+// AND of a predicate over the `threads` threads that meet at barrier `id`.
+__device__ __forceinline__ bool barrier_and(int id, int threads, bool v) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 p, %3, 0;\n\t"
+      "barrier.cta.red.and.pred q, %1, %2, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"(id), "r"(threads), "r"((uint32_t)v)
+      : "memory");
+  return r != 0;
+}
+__device__ __forceinline__ void barrier_sync(int id, int threads) {
+  asm volatile("barrier.cta.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+
+struct PairTile {
+  int g, row0, rows, ft;
+};
+
+// Tile t of all: row tiles in blocks of `band`, in a block by feature tile.
+__device__ __forceinline__ PairTile pair_tile(const LinearArgs& a, const int32_t* pre, int t, int features, int band) {
+  const int total = pre[a.groups], b = t / (band * features), in = t - b * band * features;
+  const int width = min(band, total - b * band);
+  PairTile p;
+  p.ft = in / width;
+  const int rt = b * band + in - p.ft * width;
+  int lo = 0, hi = a.groups;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (pre[mid] <= rt) lo = mid; else hi = mid;
+  }
+  p.g = lo;
+  uint32_t bad = 0;
+  const int2 seg = group_rows(a, lo, bad);
+  const int units = (seg.y - seg.x + Pair::UNIT - 1) / Pair::UNIT, tiles = pre[lo + 1] - pre[lo], i = rt - pre[lo];
+  const int u0 = (int)((int64_t)units * i / tiles), u1 = (int)((int64_t)units * (i + 1) / tiles);
+  p.row0 = seg.x + u0 * Pair::UNIT;
+  p.rows = min(seg.y, seg.x + u1 * Pair::UNIT) - p.row0;
+  return p;
+}
+
+template <bool BF16>
+__global__ void __launch_bounds__(Pair::THREADS, 1) linear_pair_kernel(const LinearArgs a, const __grid_constant__ CUtensorMap map_w,
+                                                                       const __grid_constant__ CUtensorMap map_x, int tile_units, int band) {
+  using C = Pair;
+  extern __shared__ uint8_t pair_smem_raw[];
+  __shared__ uint64_t full[C::STAGES], empty[C::STAGES], acc_full[2], acc_empty[2], drain;
+  __shared__ uint32_t taddr_s, issued_s, tx_s[C::STAGES];  // (steps copied by this CTA, their bytes)
+  __shared__ int scan_s[C::THREADS / 32];
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
+  const uint32_t rank = cluster_rank();
+  uint8_t* smem = pair_smem_raw + ((1024 - (smem_addr(pair_smem_raw) & 1023)) & 1023);
+  float* epi_s = reinterpret_cast<float*>(smem + C::STAGES * C::STAGE);
+  int32_t* pre = reinterpret_cast<int32_t*>(epi_s + C::EPI * C::BUF);  // row tiles of the groups, summed
+  if (tid == 0) {
+    for (int i = 0; i < C::STAGES; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&acc_full[i], 1);
+      mbar_init(&acc_empty[i], 2 * C::EPI);
+    }
+    mbar_init(&drain, 1);
+    fence_barrier_init();
+  }
+  cudaGridDependencySynchronize();
+  if (warp == 2) tc::tmem_alloc_pair(&taddr_s, 512);
+  {
+    uint32_t bad = 0;
+    const int per = (a.groups + C::THREADS - 1) / C::THREADS;
+    int sum = 0;
+    for (int i = 0; i < per; ++i) {
+      const int g = tid * per + i;
+      if (g >= a.groups) break;
+      const int2 seg = group_rows(a, g, bad);
+      const int units = (seg.y - seg.x + C::UNIT - 1) / C::UNIT;
+      pre[g] = (units + tile_units - 1) / tile_units;
+      sum += pre[g];
+    }
+    if (bad && blockIdx.x == 0) set_error(a.err, bad);
+    int inc = sum;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int u = __shfl_up_sync(0xffffffffu, inc, d);
+      if (lane >= d) inc += u;
+    }
+    if (lane == 31) scan_s[warp] = inc;
+    __syncthreads();
+    int base = inc - sum;
+    for (int w = 0; w < warp; ++w) base += scan_s[w];
+    for (int i = 0; i < per; ++i) {
+      const int g = tid * per + i;
+      if (g >= a.groups) break;
+      const int x = pre[g];
+      pre[g] = base;
+      base += x;
+    }
+    if (tid == C::THREADS - 1) pre[a.groups] = base;
+  }
+  tc::fence_before_sync();
+  __syncthreads();
+  cluster_arrive();  // (the barriers of both are ready)
+  cluster_wait();
+  tc::fence_after_sync();
+  const uint32_t tmem = taddr_s;
+  const int per_pair = a.gated ? 128 : 256, features = (a.n_out + per_pair - 1) / per_pair;
+  const int total = pre[a.groups] * features, first = blockIdx.x / 2, step = gridDim.x / 2;
+  const int blocks = (a.K + 63) / 64;
+  bool ok = true;
+  if (warp == 0) {
+    // ------------------------------------------------------------------ load
+    if (lane == 0) {
+      uint32_t it = 0;
+      const uint32_t leader_full = dsmem_map(smem_addr(full), 0);
+      for (int t = first; t < total && ok; t += step) {
+        const PairTile p = pair_tile(a, pre, t, features, band);
+        const int half = (p.rows + 63) / 64 * 32, boxes = half / 32;
+        for (int kb = 0; kb < blocks; ++kb, ++it) {
+          const int s = it % C::STAGES;
+          if (it >= C::STAGES && !mbar_wait_bounded(&empty[s], (it / C::STAGES - 1) & 1, a.wait_ns)) {
+            ok = false;
+            break;
+          }
+          tx_s[s] = C::W + boxes * 4096;
+          if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * (C::W + boxes * 4096));
+          const uint32_t bar = leader_full + s * 8;
+          uint8_t* st = smem + s * C::STAGE;
+          if (a.gated) {
+            tma_load_3d_pair(st, &map_w, kb * 64, p.ft * 128 + (int)rank * 64, p.g, bar);
+            tma_load_3d_pair(st + 64 * 128, &map_w, kb * 64, a.n_out + p.ft * 128 + (int)rank * 64, p.g, bar);
+          } else {
+            tma_load_3d_pair(st, &map_w, kb * 64, p.ft * 256 + (int)rank * 128, p.g, bar);
+          }
+          for (int b = 0; b < boxes; ++b)
+            tma_load_2d_pair(st + C::W + b * 4096, &map_x, kb * 64, p.row0 + (int)rank * half + b * 32, bar);
+        }
+      }
+      issued_s = it;
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------------------------- MMA
+    if (rank == 0 && lane == 0) {
+      uint32_t it = 0, n = 0;
+      for (int t = first; t < total && ok; t += step, ++n) {
+        const PairTile p = pair_tile(a, pre, t, features, band);
+        const int cols = (p.rows + 63) / 64 * 64;
+        const uint32_t id = BF16 ? tc::idesc_bf16_f32(256, cols) : tc::idesc_f16_f32(256, cols);
+        const uint32_t acc = tmem + (n & 1) * 256;
+        if (n >= 2 && !mbar_wait_bounded(&acc_empty[n & 1], (n / 2 - 1) & 1, a.wait_ns)) {
+          ok = false;
+          break;
+        }
+        tc::fence_after_sync();
+        for (int kb = 0; kb < blocks; ++kb, ++it) {
+          const int s = it % C::STAGES;
+          if (!mbar_wait_bounded(&full[s], (it / C::STAGES) & 1, a.wait_ns)) {
+            ok = false;
+            break;
+          }
+          tc::fence_after_sync();
+          const uint32_t at = smem_addr(smem + s * C::STAGE);
+          const uint64_t wd = tc::sw128_desc(at), xd = tc::sw128_desc(at + C::W);
+#pragma unroll
+          for (int q = 0; q < 4; ++q) tc::mma_pair(acc, wd + q * 2, xd + q * 2, id, kb > 0 || q > 0);
+          tc::mma_commit_pair(&empty[s], 3);
+        }
+        if (ok) tc::mma_commit_pair(&acc_full[n & 1], 3);
+      }
+      // (every product issued is awaited before tensor memory is freed)
+      tc::mma_commit_pair(&drain, 1);
+      if (!mbar_wait_bounded(&drain, 0, kWaitLimitNs)) ok = false;
+    }
+  } else if (warp >= C::EPI_WARP) {
+    // -------------------------------------------------------------- epilogue
+    // A warp reads 32 rows of W of half of the tile's columns.  Gated, the warps
+    // of a half's first and second 32 rows work with those of the other half's.
+    const int q = warp & 3, side = (warp - C::EPI_WARP) / 4, bar = 1 + side * 2 + (q & 1);
+    float* buf = epi_s + (warp - C::EPI_WARP) * C::BUF;
+    const float *first_half = epi_s + (side * 4 + (a.gated ? q & 1 : q)) * C::BUF, *second_half = epi_s + (side * 4 + 2 + (q & 1)) * C::BUF;
+    const int block = lane % 4, row_1 = (a.gated ? q >> 1 : 0) * 8 + lane / 4, rows_1 = a.gated ? 16 : 8;  // (of 16 rows: one or two a lane)
+    const uint32_t leader_empty = dsmem_map(smem_addr(acc_empty), 0);
+    uint32_t n = 0;
+    for (int t = first; t < total; t += step, ++n) {
+      const PairTile p = pair_tile(a, pre, t, features, band);
+      const int cols = (p.rows + 63) / 64 * 64, c0 = side * cols / 2, c1 = min(c0 + cols / 2, p.rows);
+      const int col = p.ft * per_pair + (int)rank * (per_pair / 2) + (a.gated ? q & 1 : q) * 32 + block * 8;
+      ok = mbar_wait_bounded(&acc_full[n & 1], (n / 2) & 1, a.wait_ns);
+      ok = barrier_and(bar, 64, ok);  // (the warps that work together go on together)
+      if (!ok) break;
+      tc::fence_after_sync();
+      const uint32_t acc = tmem + (n & 1) * 256 + ((uint32_t)(q * 32) << 16);
+      for (int c = c0; c < c1; c += 16) {
+        float v[16];
+        tc::tmem_ld16(acc + c, v);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) buf[i * C::PAD + lane] = v[i];
+        if (a.gated) barrier_sync(bar, 64); else __syncwarp();
+        for (int r = row_1; r < 16; r += rows_1) {
+          const bool use = c + r < c1 && col < a.n_out;
+          const int64_t row = p.row0 + c + r;
+          const LinearTail tail = linear_tail(a, p.g, row, col, use);
+          float z[16];
+          const int at = r * C::PAD + block * 8;
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            *reinterpret_cast<float4*>(z + 4 * j) = *reinterpret_cast<const float4*>(first_half + at + 4 * j);
+            *reinterpret_cast<float4*>(z + 8 + 4 * j) = *reinterpret_cast<const float4*>(second_half + at + 4 * j);
+          }
+          if (use) linear_finish<BF16>(a, tail, row, col, z, z + 8);
+        }
+        if (a.gated) barrier_sync(bar, 64); else __syncwarp();
+      }
+      tc::fence_before_sync();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster(leader_empty + (n & 1) * 8);
+    }
+  }
+  if (!ok) set_error(a.err, LORA_DEV_ERR_TIMEOUT);
+  __syncwarp();
+  tc::fence_before_sync();
+  __syncthreads();
+  cluster_arrive();  // (neither CTA leaves while the other's products or copies use its memory)
+  cluster_wait();
+  if (tid == 0 && rank == 0) {
+    // Copies still in flight, after a wait gave up: both CTAs' complete the even
+    // one's barriers, which here come to expect what each has copied.
+    const uint32_t mine = issued_s, other = dsmem_ld_u32(dsmem_map(smem_addr(&issued_s), 1)), most = max(mine, other);
+    for (uint32_t j = mine; j < other; ++j)
+      mbar_arrive_expect_tx(&full[j % C::STAGES], dsmem_ld_u32(dsmem_map(smem_addr(&tx_s[j % C::STAGES]), 1)));
+    for (uint32_t j = other; j < mine; ++j) mbar_complete_tx(&full[j % C::STAGES], tx_s[j % C::STAGES]);
+    for (uint32_t j = most > C::STAGES ? most - C::STAGES : 0; j < most; ++j)
+      if (!mbar_wait_bounded(&full[j % C::STAGES], (j / C::STAGES) & 1, kWaitLimitNs)) set_error(a.err, LORA_DEV_ERR_INTERNAL);
+  }
+  __syncthreads();
+  cluster_arrive();
+  cluster_wait();
+  if (warp == 2) tc::tmem_dealloc_pair(tmem, 512);
+  cluster_arrive();
+  cluster_wait();
 }
 
 }  // namespace lora

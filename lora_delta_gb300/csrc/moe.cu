@@ -76,6 +76,85 @@ int check_moe(int T, int top_k, int H) {
 
 int check_dtype(int dtype) { return dtype == LORA_BF16 || dtype == LORA_F16 ? LORA_OK : LORA_ERR_ARG; }
 
+// Tensor maps of 64 columns of K (128 bytes, swizzled): rows of x, and the rows
+// of W that a CTA's tile has of the matrix or, gated, of a half.
+bool encode_map(CUtensorMap* m, bool bf16, int dims, const void* base, const cuuint64_t* size, const cuuint64_t* stride,
+                const cuuint32_t* box) {
+  const PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
+  const cuuint32_t one[5] = {1, 1, 1, 1, 1};
+  return enc && enc(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, (cuuint32_t)dims,
+                    const_cast<void*>(base), size, stride, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+bool encode_x(CUtensorMap* m, const LinearArgs& a, bool bf16, int box_rows) {
+  const cuuint64_t size[2] = {(cuuint64_t)a.K, (cuuint64_t)a.n}, stride[1] = {(cuuint64_t)(a.n > 1 ? a.ld_x : a.K) * 2};
+  const cuuint32_t box[2] = {64, (cuuint32_t)box_rows};
+  return encode_map(m, bf16, 2, a.x, size, stride, box);
+}
+bool encode_w(CUtensorMap* m, const LinearArgs& a, bool bf16) {
+  const cuuint64_t K = (cuuint64_t)a.K, row = (cuuint64_t)a.ld_w * 2, groups = (cuuint64_t)a.groups;
+  const cuuint64_t group = a.groups > 1 ? (cuuint64_t)a.stride_w * 2 : row * (cuuint64_t)a.N;
+  const cuuint64_t size[3] = {K, (cuuint64_t)a.N, groups}, stride[2] = {row, group};
+  const cuuint32_t box[3] = {64, a.gated ? 64u : 128u, 1};
+  return encode_map(m, bf16, 3, a.w, size, stride, box);
+}
+
+template <bool BF16, int NT>
+int launch_few(const LinearArgs& a, cudaStream_t stream) {
+  using C = Few<NT>;
+  CUtensorMap map_w, map_x;
+  if (!encode_w(&map_w, a, BF16) || !encode_x(&map_x, a, BF16, 16)) return LORA_ERR_CUDA;
+  if (prepare_kernel(linear_few_kernel<BF16, C>, (int)C::smem(), false) != cudaSuccess) return LORA_ERR_CUDA;
+  const int per = a.gated ? 64 : 128, features = (a.n_out + per - 1) / per, blocks = (a.K + 63) / 64;
+  const int64_t row_tiles = ((int64_t)a.n + NT - 1) / NT;
+  const int z = (int)(a.seg_start ? (row_tiles < 2 ? row_tiles : 2) : (row_tiles < 65535 ? row_tiles : 65535));
+  // K in as many parts as leave the tiles' clusters room at two CTAs an SM
+  const int64_t tiles = (int64_t)features * a.groups * (a.seg_start ? 1 : z);
+  static const int force = env_int("LORA_LINEAR_SPLIT", 0);
+  int split = (int)(2 * (int64_t)sm_count() / tiles);
+  split = force ? force : (split < 1 ? 1 : (split > 8 ? 8 : split));
+  if (split > blocks) split = blocks;
+  return launch(linear_few_kernel<BF16, C>, dim3((unsigned)(features * split), (unsigned)a.groups, (unsigned)z), C::THREADS,
+                C::smem(), stream, split, a, map_w, map_x, split);
+}
+
+template <bool BF16>
+int launch_pair(const LinearArgs& a, cudaStream_t stream) {
+  CUtensorMap map_w, map_x;
+  if (!encode_w(&map_w, a, BF16) || !encode_x(&map_x, a, BF16, 32)) return LORA_ERR_CUDA;
+  const size_t smem = Pair::smem(a.groups);
+  if (prepare_kernel(linear_pair_kernel<BF16>, (int)smem, false) != cudaSuccess) return LORA_ERR_CUDA;
+  const int per = a.gated ? 128 : 256, pairs = sm_count() / 2;
+  const int64_t features = (a.n_out + per - 1) / per, units = ((int64_t)a.n + Pair::UNIT - 1) / Pair::UNIT;
+  int best = 4;
+  if (!a.seg_start) {  // the height of a tile that leaves the last round fullest
+    int64_t least = INT64_MAX;
+    for (int u = 4; u >= 1; --u) {
+      const int64_t tiles = features * ((units + u - 1) / u), rounds = (tiles + pairs - 1) / pairs, cost = rounds * (u * 8 + 3);
+      if (cost < least) {
+        least = cost;
+        best = u;
+      }
+    }
+  }
+  const int64_t tiles = features * (a.seg_start ? units / best + a.groups : (units + best - 1) / best);
+  if (tiles > INT32_MAX) return LORA_ERR_UNSUPPORTED;
+  const unsigned ctas = 2u * (unsigned)(tiles < pairs ? tiles : pairs);
+  return launch(linear_pair_kernel<BF16>, dim3(ctas), Pair::THREADS, smem, stream, 2, a, map_w, map_x, best, 16);
+}
+
+template <bool BF16>
+int linear_launch(const LinearArgs& a, cudaStream_t stream) {
+  const int64_t rows = a.seg_start ? ((int64_t)a.n + a.groups - 1) / a.groups : a.n;  // of a group, on average
+  static const int few = env_int("LORA_LINEAR_FEW", 64);
+  if (rows > few) return launch_pair<BF16>(a, stream);
+  const int64_t want = a.seg_start && a.groups > 1 ? 2 * rows : rows;
+  if (want <= 16) return launch_few<BF16, 16>(a, stream);
+  if (want <= 32) return launch_few<BF16, 32>(a, stream);
+  if (want <= 64) return launch_few<BF16, 64>(a, stream);
+  return launch_few<BF16, 128>(a, stream);
+}
+
 int linear_call(LinearArgs& a, int dtype, cudaStream_t stream) {
   if (a.n < 0 || a.K < 1 || a.N < 1 || a.groups < 1) return LORA_ERR_ARG;
   if (a.act < LORA_ACT_NONE || a.act > LORA_ACT_GELU_TANH || (a.gated != 0 && a.gated != 1)) return LORA_ERR_ARG;
@@ -91,7 +170,7 @@ int linear_call(LinearArgs& a, int dtype, cudaStream_t stream) {
   if (a.delta && (rc = check_mat(delta))) return rc;
   if (a.residual && (rc = check_mat(res))) return rc;
   if (a.groups > 1 && a.stride_w < (int64_t)(a.N - 1) * a.ld_w + a.K) return LORA_ERR_SHAPE;
-  if (a.groups > 1 && a.stride_w % 8) return LORA_ERR_ALIGN;
+  if (a.groups > 1 && a.stride_w % a.ld_w) return LORA_ERR_SHAPE;
   if (!aligned16(a.bias) || !aligned4(a.seg_start) || !aligned4(a.err)) return LORA_ERR_ALIGN;
   const bool in_place = a.residual == a.out && (a.ld_residual == a.ld_out || a.n == 1);
   const Mat all_w = {a.w, 0, 1, (int64_t)(a.groups - 1) * a.stride_w + (int64_t)(a.N - 1) * a.ld_w + a.K};
@@ -100,10 +179,7 @@ int linear_call(LinearArgs& a, int dtype, cudaStream_t stream) {
       (a.bias && share(out, Mat{a.bias, 0, 1, (int64_t)a.groups * a.N})) || shares_words(out, a.seg_start, a.groups + 1))
     return LORA_ERR_ARG;
   a.wait_ns = g_wait_limit_ns.load(std::memory_order_relaxed);
-  const int64_t tiles = ((int64_t)a.n + 63) / 64;
-  const dim3 grid((unsigned)((a.n_out + 63) / 64), (unsigned)a.groups, (unsigned)(tiles < 32768 ? tiles : 32768));
-  return dtype == LORA_BF16 ? launch(linear_simple_kernel<true>, grid, 256, 0, stream, 1, a)
-                            : launch(linear_simple_kernel<false>, grid, 256, 0, stream, 1, a);
+  return dtype == LORA_BF16 ? linear_launch<true>(a, stream) : linear_launch<false>(a, stream);
 }
 
 }  // namespace

@@ -117,7 +117,7 @@ def test_refusals_on_the_host():
         assert linear(E=E, x=at[0]) == arg and linear(E=E, w=at[0]) == arg and linear(E=E, delta=at[0]) == arg
         assert linear(E=E, bias=at[0]) == arg and linear(E=E, res=at[0], ld_res=56) == arg
         assert linear(E=E, res=ctypes.c_void_p(0x10000000 + 96)) == arg
-    assert linear(E=3, seg=None) == arg and linear(E=3, stride=47 * 64) == shape and linear(E=3, stride=48 * 64 + 4) == align
+    assert linear(E=3, seg=None) == arg and linear(E=3, stride=47 * 64) == shape and linear(E=3, stride=48 * 64 + 8) == shape
     assert linear(E=2049) == unsup and linear(E=3, seg=at[0]) == arg
 
 
@@ -554,3 +554,23 @@ def test_results_repeat_and_do_not_depend_on_neighbours(ld):
     y[32:] = 0
     ld.lora_linear(b, y, w)
     assert torch.equal(a[:32], b[:32])
+
+
+@gpu
+@pytest.mark.parametrize("n,gated", [(5, False), (64, True), (300, False), (700, True)])
+def test_a_wait_that_gives_up_is_reported(ld, n, gated):
+    """With a limit of 0 a wait gives up at its first look; the call reports it, and the next call is whole."""
+    rng = np.random.default_rng(60)
+    x, w = normal(rng, torch.bfloat16, n, 2048), normal(rng, torch.bfloat16, 512, 2048)
+    want, out = torch.empty(2, n, 256 if gated else 512, device="cuda").bfloat16()
+    ld.lora_linear(want, x, w, gated=gated)
+    err = ld.new_error_word()
+    torch.cuda.synchronize()
+    old = ld.lora_set_wait_limit_ns(0)
+    try:
+        ld.lora_linear(out, x, w, gated=gated, err=err)
+        assert ld.lora_get_error(err) == 8
+    finally:
+        ld.lora_set_wait_limit_ns(old)
+    ld.lora_linear(out, x, w, gated=gated, err=err)
+    assert ld.lora_get_error(err) == 0 and torch.equal(out, want)
