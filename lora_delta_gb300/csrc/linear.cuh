@@ -15,6 +15,7 @@
 #include <cuda.h>
 
 #include "common.cuh"
+#include "kv4_attn.cuh"
 #include "moe.cuh"
 #include "tc.cuh"
 
@@ -57,6 +58,14 @@ __device__ __forceinline__ float activate(float z, int act) {
     default: return z;
   }
 }
+
+// Tensor maps of x for boxes of 16, 32, 64 and 128 rows: one copy a step, of the
+// least box that holds the rows.  (Copies of 32 rows took the place of one of 128 in
+// 1440 us where this takes 1205, 8192 x 4096 by 28672: what bounds them is their number.)
+struct RowMaps {
+  CUtensorMap box[4];
+};
+__host__ __device__ __forceinline__ int row_box(int rows) { return rows <= 16 ? 0 : (rows <= 32 ? 1 : (rows <= 64 ? 2 : 3)); }
 
 // -------------------------------------------------------------- epilogue --
 // 8 columns of a row of out: what is read for them, ahead of the sums, and what
@@ -127,7 +136,7 @@ struct Few {
 
 template <bool BF16, class C>
 __global__ void __launch_bounds__(C::THREADS) linear_few_kernel(const LinearArgs a, const __grid_constant__ CUtensorMap map_w,
-                                                               const __grid_constant__ CUtensorMap map_x, int split) {
+                                                               const __grid_constant__ RowMaps maps_x, int split) {
   extern __shared__ uint8_t few_smem_raw[];
   __shared__ uint64_t full[C::STAGES], empty[C::STAGES], done;
   __shared__ uint32_t taddr_s;
@@ -157,17 +166,17 @@ __global__ void __launch_bounds__(C::THREADS) linear_few_kernel(const LinearArgs
   uint32_t it = 0;               // steps of K so far
   uint32_t tiles = 0;
   for (int r0 = seg.x + (int)blockIdx.z * C::NT; r0 < seg.y; r0 += (int)gridDim.z * C::NT, ++tiles) {
-    const int rows = min(C::NT, seg.y - r0), boxes = (rows + 15) / 16;
+    const int rows = min(C::NT, seg.y - r0), cols = (rows + 15) / 16 * 16, box = row_box(rows);
     if (!dead) {
       if (warp == 0) {
         if (lane == 0) {
           for (int i = 0; i < nkb; ++i, ++it) {
             const int s = it % C::STAGES;
-            if (it >= C::STAGES && !mbar_wait_bounded(&empty[s], (it / C::STAGES - 1) & 1, a.wait_ns)) {
+            if (it >= C::STAGES && !mbar_wait_soon(&empty[s], (it / C::STAGES - 1) & 1, a.wait_ns)) {
               ok = false;
               break;
             }
-            mbar_arrive_expect_tx(&full[s], C::W + boxes * 2048);
+            mbar_arrive_expect_tx(&full[s], C::W + (2048 << box));
             uint8_t* st = smem + s * C::STAGE;
             if (a.gated) {
               tma_load_3d(st, &map_w, (kb0 + i) * 64, ft * 64, g, &full[s]);
@@ -175,15 +184,15 @@ __global__ void __launch_bounds__(C::THREADS) linear_few_kernel(const LinearArgs
             } else {
               tma_load_3d(st, &map_w, (kb0 + i) * 64, ft * 128, g, &full[s]);
             }
-            for (int b = 0; b < boxes; ++b) tma_load_2d(st + C::W + b * 2048, &map_x, (kb0 + i) * 64, r0 + b * 16, &full[s]);
+            tma_load_2d(st + C::W, &maps_x.box[box], (kb0 + i) * 64, r0, &full[s]);
           }
         }
       } else if (warp == 1) {
         if (lane == 0) {
-          const uint32_t id = BF16 ? tc::idesc_bf16_f32(128, boxes * 16) : tc::idesc_f16_f32(128, boxes * 16);
+          const uint32_t id = BF16 ? tc::idesc_bf16_f32(128, cols) : tc::idesc_f16_f32(128, cols);
           for (int i = 0; i < nkb; ++i, ++it) {
             const int s = it % C::STAGES;
-            if (!mbar_wait_bounded(&full[s], (it / C::STAGES) & 1, a.wait_ns)) {
+            if (!mbar_wait_soon(&full[s], (it / C::STAGES) & 1, a.wait_ns)) {
               ok = false;
               break;
             }
@@ -196,7 +205,7 @@ __global__ void __launch_bounds__(C::THREADS) linear_few_kernel(const LinearArgs
           }
           // (every product issued is awaited, a failed loop's too)
           tc::mma_commit(&done);
-          if (!mbar_wait_bounded(&done, tiles & 1, ok ? a.wait_ns : kWaitLimitNs)) ok = false;
+          if (!mbar_wait_soon(&done, tiles & 1, ok ? a.wait_ns : kWaitLimitNs)) ok = false;
         }
       }
       dead = !__syncthreads_and(ok);
@@ -313,7 +322,7 @@ __device__ __forceinline__ PairTile pair_tile(const LinearArgs& a, const int32_t
 
 template <bool BF16>
 __global__ void __launch_bounds__(Pair::THREADS, 1) linear_pair_kernel(const LinearArgs a, const __grid_constant__ CUtensorMap map_w,
-                                                                       const __grid_constant__ CUtensorMap map_x, int tile_units, int band) {
+                                                                       const __grid_constant__ RowMaps maps_x, int tile_units, int band) {
   using C = Pair;
   extern __shared__ uint8_t pair_smem_raw[];
   __shared__ uint64_t full[C::STAGES], empty[C::STAGES], acc_full[2], acc_empty[2], drain;
@@ -388,15 +397,16 @@ __global__ void __launch_bounds__(Pair::THREADS, 1) linear_pair_kernel(const Lin
       const uint32_t leader_full = dsmem_map(smem_addr(full), 0);
       for (int t = first; t < total && ok; t += step) {
         const PairTile p = pair_tile(a, pre, t, features, band);
-        const int half = (p.rows + 63) / 64 * 32, boxes = half / 32;
+        const int half = (p.rows + 63) / 64 * 32, box = row_box(half);
+        const uint32_t bytes = C::W + (2048u << box);
         for (int kb = 0; kb < blocks; ++kb, ++it) {
           const int s = it % C::STAGES;
-          if (it >= C::STAGES && !mbar_wait_bounded(&empty[s], (it / C::STAGES - 1) & 1, a.wait_ns)) {
+          if (it >= C::STAGES && !mbar_wait_soon(&empty[s], (it / C::STAGES - 1) & 1, a.wait_ns)) {
             ok = false;
             break;
           }
-          tx_s[s] = C::W + boxes * 4096;
-          if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * (C::W + boxes * 4096));
+          tx_s[s] = bytes;
+          if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * bytes);
           const uint32_t bar = leader_full + s * 8;
           uint8_t* st = smem + s * C::STAGE;
           if (a.gated) {
@@ -405,8 +415,7 @@ __global__ void __launch_bounds__(Pair::THREADS, 1) linear_pair_kernel(const Lin
           } else {
             tma_load_3d_pair(st, &map_w, kb * 64, p.ft * 256 + (int)rank * 128, p.g, bar);
           }
-          for (int b = 0; b < boxes; ++b)
-            tma_load_2d_pair(st + C::W + b * 4096, &map_x, kb * 64, p.row0 + (int)rank * half + b * 32, bar);
+          tma_load_2d_pair(st + C::W, &maps_x.box[box], kb * 64, p.row0 + (int)rank * half, bar);
         }
       }
       issued_s = it;
@@ -420,14 +429,14 @@ __global__ void __launch_bounds__(Pair::THREADS, 1) linear_pair_kernel(const Lin
         const int cols = (p.rows + 63) / 64 * 64;
         const uint32_t id = BF16 ? tc::idesc_bf16_f32(256, cols) : tc::idesc_f16_f32(256, cols);
         const uint32_t acc = tmem + (n & 1) * 256;
-        if (n >= 2 && !mbar_wait_bounded(&acc_empty[n & 1], (n / 2 - 1) & 1, a.wait_ns)) {
+        if (n >= 2 && !mbar_wait_soon(&acc_empty[n & 1], (n / 2 - 1) & 1, a.wait_ns)) {
           ok = false;
           break;
         }
         tc::fence_after_sync();
         for (int kb = 0; kb < blocks; ++kb, ++it) {
           const int s = it % C::STAGES;
-          if (!mbar_wait_bounded(&full[s], (it / C::STAGES) & 1, a.wait_ns)) {
+          if (!mbar_wait_soon(&full[s], (it / C::STAGES) & 1, a.wait_ns)) {
             ok = false;
             break;
           }

@@ -86,10 +86,13 @@ bool encode_map(CUtensorMap* m, bool bf16, int dims, const void* base, const cuu
                     const_cast<void*>(base), size, stride, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                     CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
-bool encode_x(CUtensorMap* m, const LinearArgs& a, bool bf16, int box_rows) {
+bool encode_x(RowMaps* m, const LinearArgs& a, bool bf16, int first, int last) {
   const cuuint64_t size[2] = {(cuuint64_t)a.K, (cuuint64_t)a.n}, stride[1] = {(cuuint64_t)(a.n > 1 ? a.ld_x : a.K) * 2};
-  const cuuint32_t box[2] = {64, (cuuint32_t)box_rows};
-  return encode_map(m, bf16, 2, a.x, size, stride, box);
+  for (int i = first; i <= last; ++i) {
+    const cuuint32_t box[2] = {64, 16u << i};
+    if (!encode_map(&m->box[i], bf16, 2, a.x, size, stride, box)) return false;
+  }
+  return true;
 }
 bool encode_w(CUtensorMap* m, const LinearArgs& a, bool bf16) {
   const cuuint64_t K = (cuuint64_t)a.K, row = (cuuint64_t)a.ld_w * 2, groups = (cuuint64_t)a.groups;
@@ -102,8 +105,9 @@ bool encode_w(CUtensorMap* m, const LinearArgs& a, bool bf16) {
 template <bool BF16, int NT>
 int launch_few(const LinearArgs& a, cudaStream_t stream) {
   using C = Few<NT>;
-  CUtensorMap map_w, map_x;
-  if (!encode_w(&map_w, a, BF16) || !encode_x(&map_x, a, BF16, 16)) return LORA_ERR_CUDA;
+  CUtensorMap map_w;
+  RowMaps maps_x = {};
+  if (!encode_w(&map_w, a, BF16) || !encode_x(&maps_x, a, BF16, 0, row_box(NT))) return LORA_ERR_CUDA;
   if (prepare_kernel(linear_few_kernel<BF16, C>, (int)C::smem(), false) != cudaSuccess) return LORA_ERR_CUDA;
   const int per = a.gated ? 64 : 128, features = (a.n_out + per - 1) / per, blocks = (a.K + 63) / 64;
   const int64_t row_tiles = ((int64_t)a.n + NT - 1) / NT;
@@ -115,13 +119,14 @@ int launch_few(const LinearArgs& a, cudaStream_t stream) {
   split = force ? force : (split < 1 ? 1 : (split > 8 ? 8 : split));
   if (split > blocks) split = blocks;
   return launch(linear_few_kernel<BF16, C>, dim3((unsigned)(features * split), (unsigned)a.groups, (unsigned)z), C::THREADS,
-                C::smem(), stream, split, a, map_w, map_x, split);
+                C::smem(), stream, split, a, map_w, maps_x, split);
 }
 
 template <bool BF16>
 int launch_pair(const LinearArgs& a, cudaStream_t stream) {
-  CUtensorMap map_w, map_x;
-  if (!encode_w(&map_w, a, BF16) || !encode_x(&map_x, a, BF16, 32)) return LORA_ERR_CUDA;
+  CUtensorMap map_w;
+  RowMaps maps_x = {};
+  if (!encode_w(&map_w, a, BF16) || !encode_x(&maps_x, a, BF16, 1, 3)) return LORA_ERR_CUDA;
   const size_t smem = Pair::smem(a.groups);
   if (prepare_kernel(linear_pair_kernel<BF16>, (int)smem, false) != cudaSuccess) return LORA_ERR_CUDA;
   const int per = a.gated ? 128 : 256, pairs = sm_count() / 2;
@@ -140,7 +145,7 @@ int launch_pair(const LinearArgs& a, cudaStream_t stream) {
   const int64_t tiles = features * (a.seg_start ? units / best + a.groups : (units + best - 1) / best);
   if (tiles > INT32_MAX) return LORA_ERR_UNSUPPORTED;
   const unsigned ctas = 2u * (unsigned)(tiles < pairs ? tiles : pairs);
-  return launch(linear_pair_kernel<BF16>, dim3(ctas), Pair::THREADS, smem, stream, 2, a, map_w, map_x, best, 16);
+  return launch(linear_pair_kernel<BF16>, dim3(ctas), Pair::THREADS, smem, stream, 2, a, map_w, maps_x, best, 16);
 }
 
 template <bool BF16>
