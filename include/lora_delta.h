@@ -650,11 +650,19 @@ int lora_moe_combine_grad(void *grad_rows, int64_t ld_grad_rows, float *grad_wei
  * residual may be `out` itself with the same row stride.  delta is added ahead
  * of the activation, where an adapter's part belongs.  gated == 1 needs n_out a
  * multiple of 16.
+ * workspace: lora_linear_workspace_size(n, 1) bytes (0, or some 42 MB at any size),
+ * 256-byte aligned, or NULL: with it, tiles may be shared by several SMs along k_in
+ * where there are not enough for all.  Its first lora_linear_zeroed_bytes() bytes must be
+ * zero before its first use and are left zero; calls that may overlap (a graph's
+ * replays among them) need workspaces of their own.
  */
+size_t lora_linear_workspace_size(int n, int groups);
+size_t lora_linear_zeroed_bytes(void);
 int lora_linear(void *out, int64_t ld_out, const void *x, int64_t ld_x, int n, int k_in,
                 const void *w, int64_t ld_w, int n_out, const void *bias, const void *delta,
                 int64_t ld_delta, const void *residual, int64_t ld_residual, int activation,
-                int gated, int dtype, uint32_t *err_word, lora_stream_t stream);
+                int gated, int dtype, void *workspace, size_t ws_bytes, uint32_t *err_word,
+                lora_stream_t stream);
 
 /*
  * lora_moe_linear -- lora_linear for sorted rows, each expert's with its own
@@ -663,13 +671,15 @@ int lora_linear(void *out, int64_t ld_out, const void *x, int64_t ld_x, int n, i
  * lora_moe_dispatch writes it, must be nondecreasing within [0, n]; starts outside
  * are clamped with LORA_DEV_ERR_SEGMENT, and what rows get then is not specified.
  * Rows outside every segment are left as they were, and what x, delta and residual
- * hold there has no influence.
+ * hold there has no influence.  workspace: lora_linear_workspace_size(n, E) bytes, as
+ * for lora_linear.
  */
 int lora_moe_linear(void *out, int64_t ld_out, const void *rows, int64_t ld_rows, int n, int k_in,
                     const int32_t *seg_start, int E, const void *w, int64_t ld_w,
                     int64_t stride_w, int n_out, const void *bias, const void *delta,
                     int64_t ld_delta, const void *residual, int64_t ld_residual, int activation,
-                    int gated, int dtype, uint32_t *err_word, lora_stream_t stream);
+                    int gated, int dtype, void *workspace, size_t ws_bytes, uint32_t *err_word,
+                    lora_stream_t stream);
 
 /*
  * lora_get_error -- copy the device error word to *host_out after all work

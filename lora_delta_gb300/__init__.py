@@ -33,7 +33,7 @@ __all__ = [
     "BatchPlan", "Kv4Cache", "lora_batch_plan", "lora_pages_release", "lora_kv4_page_bytes",
     "lora_kv4_append", "lora_kv4_read", "lora_kv4_attention", "lora_kv4_attention_workspace",
     "MoePlan", "lora_moe_dispatch", "lora_moe_combine", "lora_moe_combine_grad", "lora_linear",
-    "lora_moe_linear",
+    "lora_moe_linear", "lora_linear_workspace",
 ]
 
 # Default limit of the kernels' bounded waits (2 s of the GPU's global timer).
@@ -490,5 +490,5 @@ def lora_get_error(err: torch.Tensor, clear: bool = True, stream=None) -> int:
 from .serve import (BatchPlan, Kv4Cache, lora_batch_plan, lora_kv4_append,  # noqa: E402
                     lora_kv4_attention, lora_kv4_attention_workspace, lora_kv4_page_bytes,
                     lora_kv4_read, lora_pages_release)
-from .moe import (MoePlan, lora_linear, lora_moe_combine, lora_moe_combine_grad,  # noqa: E402
+from .moe import (MoePlan, lora_linear, lora_linear_workspace, lora_moe_combine, lora_moe_combine_grad,  # noqa: E402
                   lora_moe_dispatch, lora_moe_linear)

@@ -69,10 +69,12 @@ SIGNATURES = {
                                _i, _i, _vp, _vp]),
     "lora_moe_combine": (_i, [_vp, _i64, _vp, _i64, _vp, _vp, _vp, _i64, _i, _i, _i, _i, _vp]),
     "lora_moe_combine_grad": (_i, [_vp, _i64, _vp, _vp, _i64, _vp, _i64, _vp, _vp, _i, _i, _i, _i, _vp]),
+    "lora_linear_workspace_size": (_sz, [_i, _i]),
+    "lora_linear_zeroed_bytes": (_sz, []),
     "lora_linear": (_i, [_vp, _i64, _vp, _i64, _i, _i, _vp, _i64, _i, _vp, _vp, _i64, _vp, _i64, _i, _i,
-                         _i, _vp, _vp]),
+                         _i, _vp, _sz, _vp, _vp]),
     "lora_moe_linear": (_i, [_vp, _i64, _vp, _i64, _i, _i, _vp, _i, _vp, _i64, _i64, _i, _vp, _vp, _i64,
-                             _vp, _i64, _i, _i, _i, _vp, _vp]),
+                             _vp, _i64, _i, _i, _i, _vp, _sz, _vp, _vp]),
 }
 
 _LIB = None

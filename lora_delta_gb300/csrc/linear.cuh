@@ -38,6 +38,8 @@ struct LinearArgs {
   int act, gated;
   uint32_t* err;
   uint64_t wait_ns;
+  uint32_t* counters;  // of shared tiles, zero between calls; or null: no tile is shared
+  float* parts;
 };
 
 // Rows [start, end) of a group.
@@ -71,21 +73,29 @@ __host__ __device__ __forceinline__ int row_box(int rows) { return rows <= 16 ? 
 // 8 columns of a row of out: what is read for them, ahead of the sums, and what
 // becomes of the sums z (and up, the second half's).
 struct LinearTail {
-  uint4 bias[2], delta[2], residual;
+  uint4 delta[2], residual;
+};
+struct LinearBias {
+  uint4 half[2];
 };
 
-__device__ __forceinline__ LinearTail linear_tail(const LinearArgs& a, int g, int64_t row, int col, bool ok) {
-  LinearTail t;
-  const uint4 none = make_uint4(0, 0, 0, 0);
-  t.bias[0] = t.bias[1] = t.delta[0] = t.delta[1] = t.residual = none;
-  if (!ok) return t;
-  const uint16_t* b = reinterpret_cast<const uint16_t*>(a.bias) + (int64_t)g * a.N + col;
-  if (a.bias) t.bias[0] = *reinterpret_cast<const uint4*>(b);
-  if (a.delta) t.delta[0] = load8(a.delta, a.ld_delta, row, col);
-  if (a.gated) {
-    if (a.bias) t.bias[1] = *reinterpret_cast<const uint4*>(b + a.n_out);
-    if (a.delta) t.delta[1] = load8(a.delta, a.ld_delta, row, a.n_out + col);
+__device__ __forceinline__ LinearBias linear_bias(const LinearArgs& a, int g, int col) {
+  LinearBias b;
+  b.half[0] = b.half[1] = make_uint4(0, 0, 0, 0);
+  if (a.bias && col < a.n_out) {
+    const uint16_t* at = reinterpret_cast<const uint16_t*>(a.bias) + (int64_t)g * a.N + col;
+    b.half[0] = *reinterpret_cast<const uint4*>(at);
+    if (a.gated) b.half[1] = *reinterpret_cast<const uint4*>(at + a.n_out);
   }
+  return b;
+}
+
+__device__ __forceinline__ LinearTail linear_tail(const LinearArgs& a, int64_t row, int col, bool use) {
+  LinearTail t;
+  t.delta[0] = t.delta[1] = t.residual = make_uint4(0, 0, 0, 0);
+  if (!use) return t;
+  if (a.delta) t.delta[0] = load8(a.delta, a.ld_delta, row, col);
+  if (a.delta && a.gated) t.delta[1] = load8(a.delta, a.ld_delta, row, a.n_out + col);
   if (a.residual) t.residual = load8(a.residual, a.ld_residual, row, col);
   return t;
 }
@@ -99,15 +109,16 @@ __device__ __forceinline__ void add8(float* z, const uint4& v) {
 }
 
 template <bool BF16>
-__device__ __forceinline__ void linear_finish(const LinearArgs& a, const LinearTail& t, int64_t row, int col, float* z, float* up) {
-  if (a.bias) add8<BF16>(z, t.bias[0]);
+__device__ __forceinline__ void linear_finish(const LinearArgs& a, const LinearBias& b, const LinearTail& t, int64_t row, int col,
+                                              float* z, float* up) {
+  if (a.bias) add8<BF16>(z, b.half[0]);
   if (a.delta) add8<BF16>(z, t.delta[0]);
   if (a.act != LORA_ACT_NONE) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) z[i] = activate(z[i], a.act);
   }
   if (a.gated) {
-    if (a.bias) add8<BF16>(up, t.bias[1]);
+    if (a.bias) add8<BF16>(up, b.half[1]);
     if (a.delta) add8<BF16>(up, t.delta[1]);
 #pragma unroll
     for (int i = 0; i < 8; ++i) z[i] *= up[i];
@@ -236,7 +247,8 @@ __global__ void __launch_bounds__(C::THREADS) linear_few_kernel(const LinearArgs
       for (int i = part * C::THREADS + tid; i < items; i += split * C::THREADS) {
         const int r = i / width, b = i % width, col = (ft * width + b) * 8;
         const bool use = col < a.n_out;
-        const LinearTail t = linear_tail(a, g, r0 + r, col, use);
+        const LinearBias bias = linear_bias(a, g, col);
+        const LinearTail t = linear_tail(a, r0 + r, col, use);
         float z[16] = {};
         const uint32_t at = smem_addr(own + r * C::PAD + b * 8);
         for (int p = 0; p < split; ++p) {
@@ -251,7 +263,7 @@ __global__ void __launch_bounds__(C::THREADS) linear_few_kernel(const LinearArgs
               z[4 * j + 3] += f.w;
             }
         }
-        if (use) linear_finish<BF16>(a, t, r0 + r, col, z, z + 8);
+        if (use) linear_finish<BF16>(a, bias, t, r0 + r, col, z, z + 8);
       }
     }
     fence_proxy_async_smem();  // (the memory is next written by copies)
@@ -274,9 +286,168 @@ struct Pair {
   static constexpr int W = 128 * 128, X = 128 * 128, STAGE = W + X, STAGES = 6;
   static constexpr int EPI = 8, EPI_WARP = 4, THREADS = (EPI_WARP + EPI) * 32;
   static constexpr int PAD = 36, BUF = 16 * PAD;  // floats: 16 rows of 32 sums
-  static constexpr int UNIT = 64;                 // rows that tiles are made of
+  static constexpr int UNIT = 64, UNITS = 4;      // a tile is 1 to 4 units of rows
+  static constexpr int BAND = 16;                 // row tiles that a feature tile is used for in turn
+  static constexpr int MAX = 80;                  // pairs that share tiles
+  static constexpr int PART = 128 * 256;          // floats of a CTA's part of a tile
   static constexpr size_t smem(int groups) { return 1024 + (size_t)STAGES * STAGE + EPI * BUF * 4 + (size_t)(groups + 1) * 4; }
 };
+constexpr size_t kLinearCounterBytes = (size_t)Pair::MAX * 8 * 4;
+constexpr size_t kLinearPartFloats = (size_t)Pair::MAX * 2 * 2 * Pair::PART;
+
+// What a step of 64 of K costs by a tile's units of rows: copies and products.
+__device__ __forceinline__ int unit_cost(int units) { return units == 4 ? 16 : 7 + 2 * units; }
+
+// A pair's work: steps [kb0, kb1) of a tile's K.  A tile that several pairs share
+// is finished by the last of them, which adds the others' parts in the order of K.
+struct PairItem {
+  int g, row0, rows, ft, kb0, kb1;
+  int head, parts, part;  // the pair that has the tile's first steps, how many share it, which this one is
+};
+
+// The pairs' items.  Tiles lie end to end: by group (of a dense product, by band
+// of rows), feature tile, row tile.  Whole rounds of tiles are taken in turns (of a
+// dense product, whose pairs then use the same bands at the same time); the rest is
+// cut into equal shares of cost, within tiles where need be.
+struct PairWalk {
+  const LinearArgs& a;
+  const int32_t* pre;  // of the groups: cost so far, a step of K
+  int features, blocks, pairs, me, groups;
+  int t, t_end;              // next tile in turn
+  int g, ft, rt, rts, units, cost;  // the tile of the shares
+  int2 seg;
+  int64_t at, base, total;   // its position; of all shares: first position, cost (a step of K)
+  int sharers;
+
+  __device__ __forceinline__ PairWalk(const LinearArgs& a, const int32_t* pre, int features, int groups, int pairs, int me)
+      : a(a), pre(pre), features(features), blocks((a.K + 63) / 64), pairs(pairs), me(me), groups(groups) {
+    t = me;
+    t_end = 0;
+    base = 0;
+    if (a.seg_start) {
+      total = pre[groups];
+    } else {
+      enter(groups - 1);
+      const int64_t tiles = (int64_t)features * ((int64_t)(groups - 1) * Pair::BAND + rts);
+      total = (int64_t)(groups - 1) * features * Pair::BAND * 16 + (int64_t)features * cost;
+      int64_t turns = tiles / pairs;
+      if (tiles % pairs && turns) --turns;
+      if (!a.counters) turns = (tiles + pairs - 1) / pairs;
+      t_end = (int)(turns * pairs < tiles ? turns * pairs : tiles);
+      if (t_end < tiles) {
+        locate_tile(t_end);
+        base = at;
+        total -= base;
+      } else {
+        total = 0;
+      }
+    }
+    // a share is at least 8 steps of a full tile
+    const int64_t most = total * blocks / 128;
+    sharers = (int)(most < 1 ? 1 : (most < pairs ? most : pairs));
+    if (me < sharers && total > 0) locate(edge(me) / blocks);
+  }
+  __device__ __forceinline__ int64_t edge(int i) const { return base * blocks + total * blocks * i / sharers; }
+  __device__ __forceinline__ void enter(int group) {  // the rows of a group
+    g = group;
+    if (a.seg_start) {
+      uint32_t bad = 0;
+      seg = group_rows(a, g, bad);
+    } else {
+      constexpr int rows = Pair::BAND * Pair::UNITS * Pair::UNIT;
+      seg = make_int2(g * rows, min(a.n, (g + 1) * rows));
+    }
+    units = (seg.y - seg.x + Pair::UNIT - 1) / Pair::UNIT;
+    rts = (units + Pair::UNITS - 1) / Pair::UNITS;
+    cost = rts ? (rts - 1) * 16 + unit_cost(units - (rts - 1) * Pair::UNITS) : 0;
+  }
+  __device__ __forceinline__ void locate_tile(int tile) {  // of a dense product
+    enter(min(tile / (features * Pair::BAND), groups - 1));
+    const int in = tile - g * features * Pair::BAND;
+    ft = in / rts;
+    rt = in - ft * rts;
+    at = (int64_t)g * features * Pair::BAND * 16 + (int64_t)ft * cost + rt * 16;
+  }
+  __device__ __forceinline__ void locate(int64_t x) {  // the tile at a position
+    int64_t start;
+    if (a.seg_start) {
+      int lo = 0, hi = groups;
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (pre[mid] <= x) lo = mid; else hi = mid;
+      }
+      enter(lo);
+      start = pre[lo];
+    } else {
+      const int64_t band = (int64_t)features * Pair::BAND * 16;
+      enter((int)(x / band < groups - 1 ? x / band : groups - 1));
+      start = g * band;
+    }
+    ft = (int)((x - start) / cost);
+    const int in = (int)(x - start - (int64_t)ft * cost);
+    rt = min(in / 16, rts - 1);
+    at = start + (int64_t)ft * cost + rt * 16;
+  }
+  // Where share i begins in the tile at `at`; near an end, there.
+  __device__ __forceinline__ int bound(int i, int per_step) const {
+    const int64_t d = edge(i) - at * blocks;
+    const int least = a.counters ? 4 : blocks;
+    if (d <= 0) return 0;
+    if (d >= (int64_t)per_step * blocks) return blocks;
+    const int kb = (int)(d / per_step);
+    return kb < least ? 0 : (blocks - kb < least ? blocks : kb);
+  }
+  __device__ __forceinline__ void rows_of(PairItem& p) const {
+    p.row0 = seg.x + rt * Pair::UNITS * Pair::UNIT;
+    p.rows = min(seg.y - p.row0, Pair::UNITS * Pair::UNIT);
+    p.g = a.seg_start ? g : 0;
+    p.ft = ft;
+  }
+  __device__ __forceinline__ bool next(PairItem& p) {
+    if (t < t_end) {
+      locate_tile(t);
+      rows_of(p);
+      p.kb0 = 0;
+      p.kb1 = blocks;
+      p.parts = 1;
+      p.head = p.part = 0;
+      t += pairs;
+      if (t >= t_end && me < sharers && total > 0) locate(edge(me) / blocks);
+      return true;
+    }
+    if (me >= sharers || total <= 0) return false;
+    const int64_t end = edge(me + 1);
+    while (g < groups && at * blocks < end) {
+      const int per_step = rt + 1 < rts ? 16 : unit_cost(units - rt * Pair::UNITS);
+      const int lo = bound(me, per_step), hi = bound(me + 1, per_step);
+      const bool mine = lo < hi;
+      if (mine) {
+        rows_of(p);
+        p.kb0 = lo;
+        p.kb1 = hi;
+        int first = me, last = me;
+        while (first > 0 && bound(first, per_step) > 0) --first;
+        while (last + 1 < sharers && bound(last + 1, per_step) < blocks) ++last;
+        p.head = first;
+        p.parts = last - first + 1;
+        p.part = me - first;
+      }
+      at += per_step;
+      if (++rt == rts) {
+        rt = 0;
+        if (++ft == features) {
+          ft = 0;
+          do {
+            if (++g < groups) enter(g);
+          } while (g < groups && rts == 0);
+        }
+      }
+      if (mine) return true;
+    }
+    return false;
+  }
+};
+
 // AND of a predicate over the `threads` threads that meet at barrier `id`.
 __device__ __forceinline__ bool barrier_and(int id, int threads, bool v) {
   uint32_t r;
@@ -320,9 +491,16 @@ __device__ __forceinline__ PairTile pair_tile(const LinearArgs& a, const int32_t
   return p;
 }
 
+// Where part x of a shared tile lies: [2 slots][2 CTAs][8 warps][128 columns][32
+// rows of W] a pair; a pair has the first steps of one shared tile at most (slot 1)
+// and later ones of one (slot 0).
+__device__ __forceinline__ float* part_of(const LinearArgs& a, const PairItem& p, int x, uint32_t rank, int warp) {
+  return a.parts + ((int64_t)((p.head + x) * 2 + (x == 0)) * 2 + rank) * Pair::PART + warp * 128 * 32;
+}
+
 template <bool BF16>
 __global__ void __launch_bounds__(Pair::THREADS, 1) linear_pair_kernel(const LinearArgs a, const __grid_constant__ CUtensorMap map_w,
-                                                                       const __grid_constant__ RowMaps maps_x, int tile_units, int band) {
+                                                                       const __grid_constant__ RowMaps maps_x, int groups) {
   using C = Pair;
   extern __shared__ uint8_t pair_smem_raw[];
   __shared__ uint64_t full[C::STAGES], empty[C::STAGES], acc_full[2], acc_empty[2], drain;
@@ -333,7 +511,7 @@ __global__ void __launch_bounds__(Pair::THREADS, 1) linear_pair_kernel(const Lin
   const uint32_t rank = cluster_rank();
   uint8_t* smem = pair_smem_raw + ((1024 - (smem_addr(pair_smem_raw) & 1023)) & 1023);
   float* epi_s = reinterpret_cast<float*>(smem + C::STAGES * C::STAGE);
-  int32_t* pre = reinterpret_cast<int32_t*>(epi_s + C::EPI * C::BUF);  // row tiles of the groups, summed
+  int32_t* pre = reinterpret_cast<int32_t*>(epi_s + C::EPI * C::BUF);  // the experts' costs, summed
   if (tid == 0) {
     for (int i = 0; i < C::STAGES; ++i) {
       mbar_init(&full[i], 1);
@@ -348,7 +526,8 @@ __global__ void __launch_bounds__(Pair::THREADS, 1) linear_pair_kernel(const Lin
   }
   cudaGridDependencySynchronize();
   if (warp == 2) tc::tmem_alloc_pair(&taddr_s, 512);
-  {
+  const int per_pair = a.gated ? 128 : 256, features = (a.n_out + per_pair - 1) / per_pair;
+  if (a.seg_start) {
     uint32_t bad = 0;
     const int per = (a.groups + C::THREADS - 1) / C::THREADS;
     int sum = 0;
@@ -356,8 +535,8 @@ __global__ void __launch_bounds__(Pair::THREADS, 1) linear_pair_kernel(const Lin
       const int g = tid * per + i;
       if (g >= a.groups) break;
       const int2 seg = group_rows(a, g, bad);
-      const int units = (seg.y - seg.x + C::UNIT - 1) / C::UNIT;
-      pre[g] = (units + tile_units - 1) / tile_units;
+      const int units = (seg.y - seg.x + C::UNIT - 1) / C::UNIT, whole = units / C::UNITS, rest = units % C::UNITS;
+      pre[g] = features * (whole * 16 + (rest ? unit_cost(rest) : 0));
       sum += pre[g];
     }
     if (bad && blockIdx.x == 0) set_error(a.err, bad);
@@ -386,20 +565,18 @@ __global__ void __launch_bounds__(Pair::THREADS, 1) linear_pair_kernel(const Lin
   cluster_wait();
   tc::fence_after_sync();
   const uint32_t tmem = taddr_s;
-  const int per_pair = a.gated ? 128 : 256, features = (a.n_out + per_pair - 1) / per_pair;
-  const int total = pre[a.groups] * features, first = blockIdx.x / 2, step = gridDim.x / 2;
-  const int blocks = (a.K + 63) / 64;
+  PairWalk walk(a, pre, features, groups, gridDim.x / 2, blockIdx.x / 2);
+  PairItem p;
   bool ok = true;
   if (warp == 0) {
     // ------------------------------------------------------------------ load
     if (lane == 0) {
       uint32_t it = 0;
       const uint32_t leader_full = dsmem_map(smem_addr(full), 0);
-      for (int t = first; t < total && ok; t += step) {
-        const PairTile p = pair_tile(a, pre, t, features, band);
+      while (ok && walk.next(p)) {
         const int half = (p.rows + 63) / 64 * 32, box = row_box(half);
         const uint32_t bytes = C::W + (2048u << box);
-        for (int kb = 0; kb < blocks; ++kb, ++it) {
+        for (int kb = p.kb0; kb < p.kb1; ++kb, ++it) {
           const int s = it % C::STAGES;
           if (it >= C::STAGES && !mbar_wait_soon(&empty[s], (it / C::STAGES - 1) & 1, a.wait_ns)) {
             ok = false;
@@ -422,35 +599,37 @@ __global__ void __launch_bounds__(Pair::THREADS, 1) linear_pair_kernel(const Lin
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------------- MMA
-    if (rank == 0 && lane == 0) {
-      uint32_t it = 0, n = 0;
-      for (int t = first; t < total && ok; t += step, ++n) {
-        const PairTile p = pair_tile(a, pre, t, features, band);
+    // The warp runs whole, so that descriptors stay in uniform registers; one
+    // lane is elected at each product and commit.
+    if (rank == 0) {
+      uint32_t s = 0, ph = 0, n = 0;  // place and parity of the next step; tiles so far
+      const uint64_t base = tc::sw128_desc(smem_addr(smem));
+      auto commit = [&](uint64_t* bar, uint16_t mask) {
+        if (tc::elect_one()) tc::mma_commit_pair(bar, mask);
+      };
+      for (; ok && walk.next(p); ++n) {
         const int cols = (p.rows + 63) / 64 * 64;
         const uint32_t id = BF16 ? tc::idesc_bf16_f32(256, cols) : tc::idesc_f16_f32(256, cols);
         const uint32_t acc = tmem + (n & 1) * 256;
-        if (n >= 2 && !mbar_wait_soon(&acc_empty[n & 1], (n / 2 - 1) & 1, a.wait_ns)) {
-          ok = false;
-          break;
-        }
+        if (n >= 2) ok = __all_sync(0xffffffffu, mbar_wait_soon(&acc_empty[n & 1], (n / 2 - 1) & 1, a.wait_ns));
+        if (!ok) break;
         tc::fence_after_sync();
-        for (int kb = 0; kb < blocks; ++kb, ++it) {
-          const int s = it % C::STAGES;
-          if (!mbar_wait_soon(&full[s], (it / C::STAGES) & 1, a.wait_ns)) {
-            ok = false;
-            break;
-          }
+        for (int kb = p.kb0; kb < p.kb1; ++kb) {
+          ok = __all_sync(0xffffffffu, mbar_wait_soon(&full[s], ph, a.wait_ns));
+          if (!ok) break;
           tc::fence_after_sync();
-          const uint32_t at = smem_addr(smem + s * C::STAGE);
-          const uint64_t wd = tc::sw128_desc(at), xd = tc::sw128_desc(at + C::W);
+          const uint64_t wd = base + (uint64_t)(s * (C::STAGE / 16)), xd = wd + C::W / 16;
 #pragma unroll
-          for (int q = 0; q < 4; ++q) tc::mma_pair(acc, wd + q * 2, xd + q * 2, id, kb > 0 || q > 0);
-          tc::mma_commit_pair(&empty[s], 3);
+          for (int q = 0; q < 4; ++q)
+            if (tc::elect_one()) tc::mma_pair(acc, wd + q * 2, xd + q * 2, id, kb > p.kb0 || q > 0);
+          commit(&empty[s], 3);
+          s = s + 1 == C::STAGES ? 0 : s + 1;
+          ph ^= s == 0;
         }
-        if (ok) tc::mma_commit_pair(&acc_full[n & 1], 3);
+        if (ok) commit(&acc_full[n & 1], 3);
       }
       // (every product issued is awaited before tensor memory is freed)
-      tc::mma_commit_pair(&drain, 1);
+      commit(&drain, 1);
       if (!mbar_wait_bounded(&drain, 0, kWaitLimitNs)) ok = false;
     }
   } else if (warp >= C::EPI_WARP) {
@@ -460,38 +639,83 @@ __global__ void __launch_bounds__(Pair::THREADS, 1) linear_pair_kernel(const Lin
     const int q = warp & 3, side = (warp - C::EPI_WARP) / 4, bar = 1 + side * 2 + (q & 1);
     float* buf = epi_s + (warp - C::EPI_WARP) * C::BUF;
     const float *first_half = epi_s + (side * 4 + (a.gated ? q & 1 : q)) * C::BUF, *second_half = epi_s + (side * 4 + 2 + (q & 1)) * C::BUF;
-    const int block = lane % 4, row_1 = (a.gated ? q >> 1 : 0) * 8 + lane / 4, rows_1 = a.gated ? 16 : 8;  // (of 16 rows: one or two a lane)
+    const int block = lane % 4, row_1 = (a.gated ? q >> 1 : 0) * 8 + lane / 4;  // (of 16 rows: this and, not gated, 8 on)
     const uint32_t leader_empty = dsmem_map(smem_addr(acc_empty), 0);
-    uint32_t n = 0;
-    for (int t = first; t < total; t += step, ++n) {
-      const PairTile p = pair_tile(a, pre, t, features, band);
+    // (after a wait that gave up, shared tiles are still counted, so that the
+    // counters end at zero)
+    for (uint32_t n = 0; walk.next(p); ++n) {
       const int cols = (p.rows + 63) / 64 * 64, c0 = side * cols / 2, c1 = min(c0 + cols / 2, p.rows);
       const int col = p.ft * per_pair + (int)rank * (per_pair / 2) + (a.gated ? q & 1 : q) * 32 + block * 8;
-      ok = mbar_wait_bounded(&acc_full[n & 1], (n / 2) & 1, a.wait_ns);
+      if (ok) ok = mbar_wait_soon(&acc_full[n & 1], (n / 2) & 1, a.wait_ns);
       ok = barrier_and(bar, 64, ok);  // (the warps that work together go on together)
-      if (!ok) break;
       tc::fence_after_sync();
       const uint32_t acc = tmem + (n & 1) * 256 + ((uint32_t)(q * 32) << 16);
-      for (int c = c0; c < c1; c += 16) {
-        float v[16];
-        tc::tmem_ld16(acc + c, v);
+      bool finish = ok;
+      if (p.parts > 1) {
+        float* own = part_of(a, p, p.part, rank, warp - C::EPI_WARP) + lane;
+        if (ok)
+          for (int c = c0; c < c1; c += 16) {
+            float v[16];
+            tc::tmem_ld16(acc + c, v);
 #pragma unroll
-        for (int i = 0; i < 16; ++i) buf[i * C::PAD + lane] = v[i];
-        if (a.gated) barrier_sync(bar, 64); else __syncwarp();
-        for (int r = row_1; r < 16; r += rows_1) {
-          const bool use = c + r < c1 && col < a.n_out;
-          const int64_t row = p.row0 + c + r;
-          const LinearTail tail = linear_tail(a, p.g, row, col, use);
-          float z[16];
-          const int at = r * C::PAD + block * 8;
-#pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            *reinterpret_cast<float4*>(z + 4 * j) = *reinterpret_cast<const float4*>(first_half + at + 4 * j);
-            *reinterpret_cast<float4*>(z + 8 + 4 * j) = *reinterpret_cast<const float4*>(second_half + at + 4 * j);
+            for (int i = 0; i < 16; ++i) __stcg(own + (c - c0 + i) * 32, v[i]);
           }
-          if (use) linear_finish<BF16>(a, tail, row, col, z, z + 8);
+        __threadfence();
+        barrier_sync(bar, 64);
+        bool last = true;
+        if (q < 2 && lane == 0) {
+          uint32_t* count = a.counters + (p.head * 2 + (int)rank) * 4 + bar - 1;
+          last = atomicAdd(count, 1u) + 1 == (uint32_t)p.parts;
+          if (last) *count = 0;
+          __threadfence();
         }
-        if (a.gated) barrier_sync(bar, 64); else __syncwarp();
+        finish = barrier_and(bar, 64, last) && ok;
+      }
+      if (finish) {
+        const LinearBias bias = linear_bias(a, p.g, col);
+        LinearTail tail[2];
+        auto fetch = [&](int c) {
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+            if (i == 0 || !a.gated) {
+              const int r = c + row_1 + 8 * i;
+              tail[i] = linear_tail(a, p.row0 + r, col, r < c1 && col < a.n_out);
+            }
+        };
+        fetch(c0);
+        for (int c = c0; c < c1; c += 16) {
+          float v[16];
+          if (p.parts == 1) {
+            tc::tmem_ld16(acc + c, v);
+          } else {  // in the order of K, whoever adds
+            const float* from = part_of(a, p, 0, rank, warp - C::EPI_WARP) + (c - c0) * 32 + lane;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) v[i] = __ldcg(from + i * 32);
+            for (int x = 1; x < p.parts; ++x) {
+              from = part_of(a, p, x, rank, warp - C::EPI_WARP) + (c - c0) * 32 + lane;
+#pragma unroll
+              for (int i = 0; i < 16; ++i) v[i] += __ldcg(from + i * 32);
+            }
+          }
+#pragma unroll
+          for (int i = 0; i < 16; ++i) buf[i * C::PAD + lane] = v[i];
+          if (a.gated) barrier_sync(bar, 64); else __syncwarp();
+          const LinearTail now[2] = {tail[0], tail[1]};
+          if (c + 16 < c1) fetch(c + 16);  // (ahead of this part's work)
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+            if (i == 0 || !a.gated) {
+              const int r = row_1 + 8 * i, at = r * C::PAD + block * 8;
+              float z[16];
+#pragma unroll
+              for (int j = 0; j < 2; ++j) {
+                *reinterpret_cast<float4*>(z + 4 * j) = *reinterpret_cast<const float4*>(first_half + at + 4 * j);
+                *reinterpret_cast<float4*>(z + 8 + 4 * j) = *reinterpret_cast<const float4*>(second_half + at + 4 * j);
+              }
+              if (c + r < c1 && col < a.n_out) linear_finish<BF16>(a, bias, now[i], p.row0 + c + r, col, z, z + 8);
+            }
+          if (a.gated) barrier_sync(bar, 64); else __syncwarp();
+        }
       }
       tc::fence_before_sync();
       __syncwarp();

@@ -129,30 +129,24 @@ int launch_pair(const LinearArgs& a, cudaStream_t stream) {
   if (!encode_w(&map_w, a, BF16) || !encode_x(&maps_x, a, BF16, 1, 3)) return LORA_ERR_CUDA;
   const size_t smem = Pair::smem(a.groups);
   if (prepare_kernel(linear_pair_kernel<BF16>, (int)smem, false) != cudaSuccess) return LORA_ERR_CUDA;
-  const int per = a.gated ? 128 : 256, pairs = sm_count() / 2;
-  const int64_t features = (a.n_out + per - 1) / per, units = ((int64_t)a.n + Pair::UNIT - 1) / Pair::UNIT;
-  int best = 4;
-  if (!a.seg_start) {  // the height of a tile that leaves the last round fullest
-    int64_t least = INT64_MAX;
-    for (int u = 4; u >= 1; --u) {
-      const int64_t tiles = features * ((units + u - 1) / u), rounds = (tiles + pairs - 1) / pairs, cost = rounds * (u * 8 + 3);
-      if (cost < least) {
-        least = cost;
-        best = u;
-      }
-    }
-  }
-  const int64_t tiles = features * (a.seg_start ? units / best + a.groups : (units + best - 1) / best);
-  if (tiles > INT32_MAX) return LORA_ERR_UNSUPPORTED;
-  const unsigned ctas = 2u * (unsigned)(tiles < pairs ? tiles : pairs);
-  return launch(linear_pair_kernel<BF16>, dim3(ctas), Pair::THREADS, smem, stream, 2, a, map_w, maps_x, best, 16);
+  int pairs = sm_count() / 2;
+  if (pairs > Pair::MAX) pairs = Pair::MAX;
+  constexpr int band = Pair::BAND * Pair::UNITS * Pair::UNIT;
+  const int groups = a.seg_start ? a.groups : (int)(((int64_t)a.n + band - 1) / band);
+  return launch(linear_pair_kernel<BF16>, dim3(2u * (unsigned)pairs), Pair::THREADS, smem, stream, 2, a, map_w, maps_x, groups);
+}
+
+// Rows of a group on average, and up to how many the kernel for few rows takes.
+int64_t mean_rows(int n, int groups) { return ((int64_t)n + groups - 1) / groups; }
+int few_rows() {
+  static const int few = env_int("LORA_LINEAR_FEW", 64);
+  return few;
 }
 
 template <bool BF16>
 int linear_launch(const LinearArgs& a, cudaStream_t stream) {
-  const int64_t rows = a.seg_start ? ((int64_t)a.n + a.groups - 1) / a.groups : a.n;  // of a group, on average
-  static const int few = env_int("LORA_LINEAR_FEW", 64);
-  if (rows > few) return launch_pair<BF16>(a, stream);
+  const int64_t rows = mean_rows(a.n, a.groups);
+  if (rows > few_rows()) return launch_pair<BF16>(a, stream);
   const int64_t want = a.seg_start && a.groups > 1 ? 2 * rows : rows;
   if (want <= 16) return launch_few<BF16, 16>(a, stream);
   if (want <= 32) return launch_few<BF16, 32>(a, stream);
@@ -160,7 +154,7 @@ int linear_launch(const LinearArgs& a, cudaStream_t stream) {
   return launch_few<BF16, 128>(a, stream);
 }
 
-int linear_call(LinearArgs& a, int dtype, cudaStream_t stream) {
+int linear_call(LinearArgs& a, int dtype, void* workspace, size_t ws_bytes, cudaStream_t stream) {
   if (a.n < 0 || a.K < 1 || a.N < 1 || a.groups < 1) return LORA_ERR_ARG;
   if (a.act < LORA_ACT_NONE || a.act > LORA_ACT_GELU_TANH || (a.gated != 0 && a.gated != 1)) return LORA_ERR_ARG;
   int rc = check_dtype(dtype);
@@ -183,6 +177,12 @@ int linear_call(LinearArgs& a, int dtype, cudaStream_t stream) {
       (a.residual && !in_place && share(out, res)) ||
       (a.bias && share(out, Mat{a.bias, 0, 1, (int64_t)a.groups * a.N})) || shares_words(out, a.seg_start, a.groups + 1))
     return LORA_ERR_ARG;
+  if (workspace) {
+    if (ws_bytes < lora_linear_workspace_size(a.n, a.groups)) return LORA_ERR_WORKSPACE;
+    if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return LORA_ERR_ALIGN;
+    a.counters = reinterpret_cast<uint32_t*>(workspace);
+    a.parts = reinterpret_cast<float*>(reinterpret_cast<char*>(workspace) + kLinearCounterBytes);
+  }
   a.wait_ns = g_wait_limit_ns.load(std::memory_order_relaxed);
   return dtype == LORA_BF16 ? linear_launch<true>(a, stream) : linear_launch<false>(a, stream);
 }
@@ -300,22 +300,28 @@ int lora_moe_combine_grad(void* grad_rows, int64_t ld_grad_rows, float* grad_wei
              : launch(moe_combine_grad_kernel<false>, dim3((unsigned)T), kMoeThreads, 0, (cudaStream_t)stream, 1, a);
 }
 
+size_t lora_linear_workspace_size(int n, int groups) {
+  return groups < 1 || mean_rows(n, groups) <= few_rows() ? 0 : kLinearCounterBytes + kLinearPartFloats * 4;
+}
+size_t lora_linear_zeroed_bytes(void) { return kLinearCounterBytes; }
+
 int lora_linear(void* out, int64_t ld_out, const void* x, int64_t ld_x, int n, int k_in, const void* w, int64_t ld_w,
                 int n_out, const void* bias, const void* delta, int64_t ld_delta, const void* residual,
-                int64_t ld_residual, int activation, int gated, int dtype, uint32_t* err_word, lora_stream_t stream) {
+                int64_t ld_residual, int activation, int gated, int dtype, void* workspace, size_t ws_bytes,
+                uint32_t* err_word, lora_stream_t stream) {
   LinearArgs a = {out, ld_out, x, ld_x, w, ld_w, 0, bias, delta, ld_delta, residual, ld_residual, nullptr, 1, n, k_in, n_out,
-                  0, activation, gated, err_word, 0};
-  return linear_call(a, dtype, (cudaStream_t)stream);
+                  0, activation, gated, err_word, 0, nullptr, nullptr};
+  return linear_call(a, dtype, workspace, ws_bytes, (cudaStream_t)stream);
 }
 
 int lora_moe_linear(void* out, int64_t ld_out, const void* rows, int64_t ld_rows, int n, int k_in, const int32_t* seg_start,
                     int E, const void* w, int64_t ld_w, int64_t stride_w, int n_out, const void* bias, const void* delta,
                     int64_t ld_delta, const void* residual, int64_t ld_residual, int activation, int gated, int dtype,
-                    uint32_t* err_word, lora_stream_t stream) {
+                    void* workspace, size_t ws_bytes, uint32_t* err_word, lora_stream_t stream) {
   if (!seg_start) return LORA_ERR_ARG;
   LinearArgs a = {out, ld_out, rows, ld_rows, w, ld_w, stride_w, bias, delta, ld_delta, residual, ld_residual, seg_start, E, n,
-                  k_in, n_out, 0, activation, gated, err_word, 0};
-  return linear_call(a, dtype, (cudaStream_t)stream);
+                  k_in, n_out, 0, activation, gated, err_word, 0, nullptr, nullptr};
+  return linear_call(a, dtype, workspace, ws_bytes, (cudaStream_t)stream);
 }
 
 }  // extern "C"

@@ -7,8 +7,11 @@ Tensors must be on the current device.
 """
 from __future__ import annotations
 
+import functools
+
 import torch
 
+from ._lib import lib
 from .serve import _DTYPES, _check, _err_at, _Fixed, _fn, _raw_stream
 
 _ACTIVATIONS = {"none": 0, None: 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4}
@@ -131,8 +134,46 @@ def _epilogue(delta, residual, dtype, n, N, width):
     return *d, *r
 
 
-def lora_linear(out, x, weight, bias=None, delta=None, residual=None, activation="none", gated: bool = False, err=None,
-                stream=None):
+@functools.lru_cache(maxsize=4096)
+def _linear_bytes(n, groups):
+    return int(lib().lora_linear_workspace_size(n, groups))
+
+
+def lora_linear_workspace(device="cuda") -> torch.Tensor:
+    """A workspace for ``lora_linear`` and ``lora_moe_linear`` of any size, ready for its first use."""
+    L = lib()
+    ws = torch.empty(int(L.lora_linear_workspace_size(2 ** 31 - 1, 1)), dtype=torch.uint8, device=device)
+    ws[:int(L.lora_linear_zeroed_bytes())].zero_()
+    return ws
+
+
+# One workspace per (device, stream) for callers that pass none, as for the attention: calls on one stream run in order
+# and may share it.  A graph gets its own, since its replays may run beside calls on the stream of its capture.
+_LINEAR_WS: dict = {}
+
+
+def _linear_workspace(workspace, n, groups, device, stream, raw):
+    """Pointer and bytes of the workspace of a call."""
+    if workspace is not None:
+        _here(workspace, "workspace")
+        if not workspace.is_contiguous():
+            raise ValueError("workspace must be contiguous")
+    elif not _linear_bytes(n, groups):
+        return None, 0
+    elif stream is not None:
+        with torch.cuda.stream(stream):
+            return _linear_workspace(None, n, groups, device, None, raw)
+    elif torch._C._cuda_isCurrentStreamCapturing():
+        workspace = lora_linear_workspace(torch.device("cuda", device))  # zeroed by each replay
+    else:
+        workspace = _LINEAR_WS.get((device, raw))
+        if workspace is None:
+            workspace = _LINEAR_WS[(device, raw)] = lora_linear_workspace(torch.device("cuda", device))
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size()
+
+
+def lora_linear(out, x, weight, bias=None, delta=None, residual=None, activation="none", gated: bool = False,
+                workspace=None, err=None, stream=None):
     """``out = act(x weight^T + bias + delta) + residual``; gated: ``act(z[:, :I]) * z[:, I:] + residual`` of z [n, 2 I].
 
     ``x`` [n, k_in], ``weight`` [n_out, k_in], ``bias`` [n_out], ``delta`` [n, n_out] (what the LoRA calls leave: it goes
@@ -146,14 +187,16 @@ def lora_linear(out, x, weight, bias=None, delta=None, residual=None, activation
     x_at, ld_x = _matrix(x, "x", dtype, n, K)
     w_at, ld_w = _matrix(weight, "weight", dtype, N, K)
     out_at, ld_out = _matrix(out, "out", dtype, n, width)
+    raw = _raw_stream(stream)
+    ws, ws_bytes = _linear_workspace(workspace, n, 1, x.get_device(), stream, raw)
     _check("lora_linear", _fn.lora_linear(
         out_at, ld_out, x_at, ld_x, n, K, w_at, ld_w, N, _whole(bias, "bias", dtype, (N,)),
         *_epilogue(delta, residual, dtype, n, N, width), _activation(activation), 1 if gated else 0, _DTYPES[dtype],
-        _err_at(err), _raw_stream(stream)))
+        ws, ws_bytes, _err_at(err), raw))
 
 
 def lora_moe_linear(out, rows, weight, plan: MoePlan, bias=None, delta=None, residual=None, activation="none",
-                    gated: bool = False, err=None, stream=None):
+                    gated: bool = False, workspace=None, err=None, stream=None):
     """``lora_linear`` of the sorted ``rows`` [T * top_k, k_in] of ``plan``, expert e's with ``weight[e]`` of [E, n_out, k_in] and
     ``bias[e]`` of [E, n_out].  ``delta`` and ``residual`` are in the rows' order.  Rows behind the last expert's are left as
     they were."""
@@ -169,7 +212,9 @@ def lora_moe_linear(out, rows, weight, plan: MoePlan, bias=None, delta=None, res
     width = N // 2 if gated else N
     x_at, ld_x = _matrix(rows, "rows", dtype, n, K)
     out_at, ld_out = _matrix(out, "out", dtype, n, width)
+    raw = _raw_stream(stream)
+    ws, ws_bytes = _linear_workspace(workspace, n, E, rows.get_device(), stream, raw)
     _check("lora_moe_linear", _fn.lora_moe_linear(
         out_at, ld_out, x_at, ld_x, n, K, plan._seg, E, weight.data_ptr(), ld_w if N > 1 else K, stride_w, N,
         _whole(bias, "bias", dtype, (E, N)), *_epilogue(delta, residual, dtype, n, N, width), _activation(activation),
-        1 if gated else 0, _DTYPES[dtype], _err_at(err), _raw_stream(stream)))
+        1 if gated else 0, _DTYPES[dtype], ws, ws_bytes, _err_at(err), raw))

@@ -100,11 +100,11 @@ def test_refusals_on_the_host():
     assert grad(H=4) == align and grad(ld_gr=56) == shape and grad(t=-1) == arg
 
     def linear(out=at[0], ld_out=48, x=at[1], ld_x=64, n=5, K=64, w=at[2], ld_w=64, N=48, bias=at[3], delta=at[4], ld_delta=48,
-               res=at[5], ld_res=48, act=0, gated=0, t=0, E=0, seg=at[6], stride=48 * 64):
+               res=at[5], ld_res=48, act=0, gated=0, t=0, E=0, seg=at[6], stride=48 * 64, work=None, wsb=0):
         if E:
             return L.lora_moe_linear(out, ld_out, x, ld_x, n, K, seg, E, w, ld_w, stride, N, bias, delta, ld_delta, res, ld_res,
-                                     act, gated, t, None, None)
-        return L.lora_linear(out, ld_out, x, ld_x, n, K, w, ld_w, N, bias, delta, ld_delta, res, ld_res, act, gated, t, None, None)
+                                     act, gated, t, work, wsb, None, None)
+        return L.lora_linear(out, ld_out, x, ld_x, n, K, w, ld_w, N, bias, delta, ld_delta, res, ld_res, act, gated, t, work, wsb, None, None)
 
     for E in (0, 3):
         assert linear(E=E, n=0, out=None) == ok
@@ -117,6 +117,7 @@ def test_refusals_on_the_host():
         assert linear(E=E, x=at[0]) == arg and linear(E=E, w=at[0]) == arg and linear(E=E, delta=at[0]) == arg
         assert linear(E=E, bias=at[0]) == arg and linear(E=E, res=at[0], ld_res=56) == arg
         assert linear(E=E, res=ctypes.c_void_p(0x10000000 + 96)) == arg
+        assert linear(E=E, n=1000, work=at[7], wsb=1000) == 5 and linear(E=E, work=odd, wsb=1 << 30) == align
     assert linear(E=3, seg=None) == arg and linear(E=3, stride=47 * 64) == shape and linear(E=3, stride=48 * 64 + 8) == shape
     assert linear(E=2049) == unsup and linear(E=3, seg=at[0]) == arg
 
@@ -559,7 +560,8 @@ def test_results_repeat_and_do_not_depend_on_neighbours(ld):
 @gpu
 @pytest.mark.parametrize("n,gated", [(5, False), (64, True), (300, False), (700, True)])
 def test_a_wait_that_gives_up_is_reported(ld, n, gated):
-    """With a limit of 0 a wait gives up at its first look; the call reports it, and the next call is whole."""
+    """With a limit of 0 a wait gives up at its first look, which may itself block for a while: the call reports it, or no
+    wait was too long and it is whole.  The next call is whole, its workspace's counters at zero."""
     rng = np.random.default_rng(60)
     x, w = normal(rng, torch.bfloat16, n, 2048), normal(rng, torch.bfloat16, 512, 2048)
     want, out = torch.empty(2, n, 256 if gated else 512, device="cuda").bfloat16()
@@ -569,8 +571,11 @@ def test_a_wait_that_gives_up_is_reported(ld, n, gated):
     old = ld.lora_set_wait_limit_ns(0)
     try:
         ld.lora_linear(out, x, w, gated=gated, err=err)
-        assert ld.lora_get_error(err) == 8
+        bits = ld.lora_get_error(err)
+        assert bits == 8 or (bits == 0 and torch.equal(out, want))
     finally:
         ld.lora_set_wait_limit_ns(old)
-    ld.lora_linear(out, x, w, gated=gated, err=err)
-    assert ld.lora_get_error(err) == 0 and torch.equal(out, want)
+    for _ in range(2):
+        out.fill_(3)
+        ld.lora_linear(out, x, w, gated=gated, err=err)
+        assert ld.lora_get_error(err) == 0 and torch.equal(out, want)
