@@ -279,9 +279,9 @@ __global__ void __launch_bounds__(C::THREADS) linear_few_kernel(const LinearArgs
 // ------------------------------------------------------------ many rows --
 // A pair of CTAs works on a tile of 256 rows of W and up to 256 of x: each holds
 // half of both (cta_group::2), so that a step of 64 of K costs an SM 32 KB of
-// copies for 512 cycles of products.  Persistent: a load warp, an MMA warp (of
-// the even CTA) and 8 epilogue warps, the sums of one tile in one half of tensor
-// memory while the epilogue reads the other's.
+// copies for 512 cycles of products.  Persistent: a warp that lays out the pair's
+// items ahead, a load warp, an MMA warp (of the even CTA) and 8 epilogue warps, the
+// sums of one tile in one half of tensor memory while the epilogue reads the other's.
 struct Pair {
   static constexpr int W = 128 * 128, X = 128 * 128, STAGE = W + X, STAGES = 6;
   static constexpr int EPI = 8, EPI_WARP = 4, THREADS = (EPI_WARP + EPI) * 32;
@@ -290,6 +290,7 @@ struct Pair {
   static constexpr int BAND = 16;                 // row tiles that a feature tile is used for in turn
   static constexpr int MAX = 80;                  // pairs that share tiles
   static constexpr int PART = 128 * 256;          // floats of a CTA's part of a tile
+  static constexpr int ITEMS = 4;                 // items laid out ahead
   static constexpr size_t smem(int groups) { return 1024 + (size_t)STAGES * STAGE + EPI * BUF * 4 + (size_t)(groups + 1) * 4; }
 };
 constexpr size_t kLinearCounterBytes = (size_t)Pair::MAX * 8 * 4;
@@ -503,7 +504,8 @@ __global__ void __launch_bounds__(Pair::THREADS, 1) linear_pair_kernel(const Lin
                                                                        const __grid_constant__ RowMaps maps_x, int groups) {
   using C = Pair;
   extern __shared__ uint8_t pair_smem_raw[];
-  __shared__ uint64_t full[C::STAGES], empty[C::STAGES], acc_full[2], acc_empty[2], drain;
+  __shared__ uint64_t full[C::STAGES], empty[C::STAGES], acc_full[2], acc_empty[2], item_full[C::ITEMS], item_empty[C::ITEMS], drain;
+  __shared__ PairItem items[C::ITEMS];
   __shared__ uint32_t taddr_s, issued_s, tx_s[C::STAGES];  // (steps copied by this CTA, their bytes)
   __shared__ int scan_s[C::THREADS / 32];
   const int tid = threadIdx.x, lane = tid & 31;
@@ -520,6 +522,10 @@ __global__ void __launch_bounds__(Pair::THREADS, 1) linear_pair_kernel(const Lin
     for (int i = 0; i < 2; ++i) {
       mbar_init(&acc_full[i], 1);
       mbar_init(&acc_empty[i], 2 * C::EPI);
+    }
+    for (int i = 0; i < C::ITEMS; ++i) {
+      mbar_init(&item_full[i], 1);
+      mbar_init(&item_empty[i], 1 + (rank == 0) + C::EPI);  // load, MMA and epilogue warps
     }
     mbar_init(&drain, 1);
     fence_barrier_init();
@@ -565,18 +571,30 @@ __global__ void __launch_bounds__(Pair::THREADS, 1) linear_pair_kernel(const Lin
   cluster_wait();
   tc::fence_after_sync();
   const uint32_t tmem = taddr_s;
-  PairWalk walk(a, pre, features, groups, gridDim.x / 2, blockIdx.x / 2);
+  // An item from the warp that lays them out (false: there are no more) and, once
+  // it is no longer needed, back.  After a wait that gave up a role passes on
+  // without work; these waits end since every role's do.
   PairItem p;
+  uint32_t n = 0;  // items so far
+  auto take = [&]() -> bool {
+    if (!mbar_wait_soon(&item_full[n % C::ITEMS], (n / C::ITEMS) & 1, 4 * kWaitLimitNs)) return false;
+    p = items[n % C::ITEMS];
+    return p.parts > 0;
+  };
+  auto pass = [&]() {  // (by one thread)
+    mbar_arrive(&item_empty[n % C::ITEMS]);
+  };
   bool ok = true;
   if (warp == 0) {
     // ------------------------------------------------------------------ load
     if (lane == 0) {
       uint32_t it = 0;
       const uint32_t leader_full = dsmem_map(smem_addr(full), 0);
-      while (ok && walk.next(p)) {
+      for (; take(); ++n) {
+        pass();
         const int half = (p.rows + 63) / 64 * 32, box = row_box(half);
         const uint32_t bytes = C::W + (2048u << box);
-        for (int kb = p.kb0; kb < p.kb1; ++kb, ++it) {
+        for (int kb = p.kb0; kb < p.kb1 && ok; ++kb, ++it) {
           const int s = it % C::STAGES;
           if (it >= C::STAGES && !mbar_wait_soon(&empty[s], (it / C::STAGES - 1) & 1, a.wait_ns)) {
             ok = false;
@@ -602,17 +620,20 @@ __global__ void __launch_bounds__(Pair::THREADS, 1) linear_pair_kernel(const Lin
     // The warp runs whole, so that descriptors stay in uniform registers; one
     // lane is elected at each product and commit.
     if (rank == 0) {
-      uint32_t s = 0, ph = 0, n = 0;  // place and parity of the next step; tiles so far
+      uint32_t s = 0, ph = 0;  // place and parity of the next step
       const uint64_t base = tc::sw128_desc(smem_addr(smem));
       auto commit = [&](uint64_t* bar, uint16_t mask) {
         if (tc::elect_one()) tc::mma_commit_pair(bar, mask);
       };
-      for (; ok && walk.next(p); ++n) {
+      for (; __all_sync(0xffffffffu, take()); ++n) {
+        __syncwarp();
+        if (lane == 0) pass();
+        if (!ok) continue;
         const int cols = (p.rows + 63) / 64 * 64;
         const uint32_t id = BF16 ? tc::idesc_bf16_f32(256, cols) : tc::idesc_f16_f32(256, cols);
         const uint32_t acc = tmem + (n & 1) * 256;
         if (n >= 2) ok = __all_sync(0xffffffffu, mbar_wait_soon(&acc_empty[n & 1], (n / 2 - 1) & 1, a.wait_ns));
-        if (!ok) break;
+        if (!ok) continue;
         tc::fence_after_sync();
         for (int kb = p.kb0; kb < p.kb1; ++kb) {
           ok = __all_sync(0xffffffffu, mbar_wait_soon(&full[s], ph, a.wait_ns));
@@ -632,6 +653,21 @@ __global__ void __launch_bounds__(Pair::THREADS, 1) linear_pair_kernel(const Lin
       commit(&drain, 1);
       if (!mbar_wait_bounded(&drain, 0, kWaitLimitNs)) ok = false;
     }
+  } else if (warp == 3) {
+    // ----------------------------------------------------------------- items
+    if (lane == 0) {
+      PairWalk walk(a, pre, features, groups, gridDim.x / 2, blockIdx.x / 2);
+      for (bool more = true; more; ++n) {
+        more = walk.next(p);
+        if (!more) p.parts = 0;
+        if (n >= C::ITEMS && !mbar_wait_bounded(&item_empty[n % C::ITEMS], (n / C::ITEMS - 1) & 1, 4 * kWaitLimitNs)) {
+          ok = false;
+          break;
+        }
+        items[n % C::ITEMS] = p;
+        mbar_arrive(&item_full[n % C::ITEMS]);
+      }
+    }
   } else if (warp >= C::EPI_WARP) {
     // -------------------------------------------------------------- epilogue
     // A warp reads 32 rows of W of half of the tile's columns.  Gated, the warps
@@ -643,7 +679,9 @@ __global__ void __launch_bounds__(Pair::THREADS, 1) linear_pair_kernel(const Lin
     const uint32_t leader_empty = dsmem_map(smem_addr(acc_empty), 0);
     // (after a wait that gave up, shared tiles are still counted, so that the
     // counters end at zero)
-    for (uint32_t n = 0; walk.next(p); ++n) {
+    for (; __all_sync(0xffffffffu, take()); ++n) {
+      __syncwarp();
+      if (lane == 0) pass();
       const int cols = (p.rows + 63) / 64 * 64, c0 = side * cols / 2, c1 = min(c0 + cols / 2, p.rows);
       const int col = p.ft * per_pair + (int)rank * (per_pair / 2) + (a.gated ? q & 1 : q) * 32 + block * 8;
       if (ok) ok = mbar_wait_soon(&acc_full[n & 1], (n / 2) & 1, a.wait_ns);
