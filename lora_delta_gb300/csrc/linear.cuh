@@ -288,10 +288,11 @@ struct Pair {
   static constexpr int PAD = 36, BUF = 16 * PAD;  // floats: 16 rows of 32 sums
   static constexpr int UNIT = 64, UNITS = 4;      // a tile is 1 to 4 units of rows
   static constexpr int BAND = 16;                 // row tiles that a feature tile is used for in turn
+  static constexpr int BAND_COST = BAND * 16;
   static constexpr int MAX = 80;                  // pairs that share tiles
   static constexpr int PART = 128 * 256;          // floats of a CTA's part of a tile
   static constexpr int ITEMS = 4;                 // items laid out ahead
-  static constexpr size_t smem(int groups) { return 1024 + (size_t)STAGES * STAGE + EPI * BUF * 4 + (size_t)(groups + 1) * 4; }
+  static constexpr size_t smem(int groups) { return 1024 + (size_t)STAGES * STAGE + EPI * BUF * 4 + (size_t)(groups + 1) * 8; }
 };
 constexpr size_t kLinearCounterBytes = (size_t)Pair::MAX * 8 * 4;
 constexpr size_t kLinearPartFloats = (size_t)Pair::MAX * 2 * 2 * Pair::PART;
@@ -306,124 +307,120 @@ struct PairItem {
   int head, parts, part;  // the pair that has the tile's first steps, how many share it, which this one is
 };
 
-// The pairs' items.  Tiles lie end to end: by group (of a dense product, by band
-// of rows), feature tile, row tile.  Whole rounds of tiles are taken in turns (of a
-// dense product, whose pairs then use the same bands at the same time); the rest is
-// cut into equal shares of cost, within tiles where need be.
+// The pairs' items.  Tiles lie end to end: by group, band of 16 row tiles, feature
+// tile, row tile.  Whole rounds of tiles are taken in turns, so that the pairs use
+// the same rows and weights at the same time (contiguous shares of all: 16384 rows
+// of 64 experts 197 us for 148, x read from memory again); the last rounds are cut
+// into equal shares of cost, within tiles where need be.
 struct PairWalk {
   const LinearArgs& a;
-  const int32_t* pre;  // of the groups: cost so far, a step of K
-  int features, blocks, pairs, me, groups;
-  int t, t_end;              // next tile in turn
-  int g, ft, rt, rts, units, cost;  // the tile of the shares
+  const int2* pre;  // of the groups: tiles and cost (a step of K) so far
+  int features, blocks, pairs, me;
+  int t, t_end;                              // next tile in turn
+  int g, units, rts, band, width, ft, rt;    // the tile of the shares; row tiles of its band
   int2 seg;
-  int64_t at, base, total;   // its position; of all shares: first position, cost (a step of K)
+  int64_t at, base, total;                   // its position; of the shares: first position, cost (a step of K)
   int sharers;
 
-  __device__ __forceinline__ PairWalk(const LinearArgs& a, const int32_t* pre, int features, int groups, int pairs, int me)
-      : a(a), pre(pre), features(features), blocks((a.K + 63) / 64), pairs(pairs), me(me), groups(groups) {
+  __device__ __forceinline__ PairWalk(const LinearArgs& a, const int2* pre, int features, int pairs, int me)
+      : a(a), pre(pre), features(features), blocks((a.K + 63) / 64), pairs(pairs), me(me) {
+    const int tiles = pre[a.groups].x;
     t = me;
-    t_end = 0;
-    base = 0;
-    if (a.seg_start) {
-      total = pre[groups];
-    } else {
-      enter(groups - 1);
-      const int64_t tiles = (int64_t)features * ((int64_t)(groups - 1) * Pair::BAND + rts);
-      total = (int64_t)(groups - 1) * features * Pair::BAND * 16 + (int64_t)features * cost;
-      int64_t turns = tiles / pairs;
-      if (tiles % pairs && turns) --turns;
-      if (!a.counters) turns = (tiles + pairs - 1) / pairs;
-      t_end = (int)(turns * pairs < tiles ? turns * pairs : tiles);
-      if (t_end < tiles) {
-        locate_tile(t_end);
-        base = at;
-        total -= base;
-      } else {
-        total = 0;
-      }
+    int turns = tiles / pairs;
+    if (tiles % pairs && turns) --turns;
+    t_end = a.counters ? turns * pairs : tiles;
+    base = total = 0;
+    if (t_end < tiles) {
+      locate_tile(t_end);
+      base = at;
+      total = pre[a.groups].y - base;
     }
     // a share is at least 8 steps of a full tile
     const int64_t most = total * blocks / 128;
     sharers = (int)(most < 1 ? 1 : (most < pairs ? most : pairs));
+    if (t >= t_end) begin();
+  }
+  __device__ __forceinline__ void begin() {
     if (me < sharers && total > 0) locate(edge(me) / blocks);
   }
   __device__ __forceinline__ int64_t edge(int i) const { return base * blocks + total * blocks * i / sharers; }
-  __device__ __forceinline__ void enter(int group) {  // the rows of a group
+  __device__ __forceinline__ int cost_of(int row_tile) const {
+    return row_tile + 1 < rts ? 16 : unit_cost(units - row_tile * Pair::UNITS);
+  }
+  __device__ __forceinline__ void enter(int group) {
     g = group;
-    if (a.seg_start) {
-      uint32_t bad = 0;
-      seg = group_rows(a, g, bad);
-    } else {
-      constexpr int rows = Pair::BAND * Pair::UNITS * Pair::UNIT;
-      seg = make_int2(g * rows, min(a.n, (g + 1) * rows));
-    }
+    uint32_t bad = 0;
+    seg = group_rows(a, g, bad);
     units = (seg.y - seg.x + Pair::UNIT - 1) / Pair::UNIT;
     rts = (units + Pair::UNITS - 1) / Pair::UNITS;
-    cost = rts ? (rts - 1) * 16 + unit_cost(units - (rts - 1) * Pair::UNITS) : 0;
   }
-  __device__ __forceinline__ void locate_tile(int tile) {  // of a dense product
-    enter(min(tile / (features * Pair::BAND), groups - 1));
-    const int in = tile - g * features * Pair::BAND;
-    ft = in / rts;
-    rt = in - ft * rts;
-    at = (int64_t)g * features * Pair::BAND * 16 + (int64_t)ft * cost + rt * 16;
+  __device__ __forceinline__ void enter_band(int b) {
+    band = b;
+    width = min(Pair::BAND, rts - b * Pair::BAND);
+  }
+  __device__ __forceinline__ int band_cost() const { return (width - 1) * 16 + cost_of(band * Pair::BAND + width - 1); }
+  template <class F>
+  __device__ __forceinline__ int group_of(F before) const {  // the last group before which it holds
+    int lo = 0, hi = a.groups;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (before(pre[mid])) lo = mid; else hi = mid;
+    }
+    return lo;
+  }
+  __device__ __forceinline__ void locate_tile(int tile) {
+    enter(group_of([&](int2 v) { return v.x <= tile; }));
+    int in = tile - pre[g].x;
+    enter_band(in / (features * Pair::BAND));
+    in -= band * features * Pair::BAND;
+    ft = in / width;
+    rt = band * Pair::BAND + in - ft * width;
+    at = pre[g].y + (int64_t)band * features * Pair::BAND_COST + (int64_t)ft * band_cost() + (rt - band * Pair::BAND) * 16;
   }
   __device__ __forceinline__ void locate(int64_t x) {  // the tile at a position
-    int64_t start;
-    if (a.seg_start) {
-      int lo = 0, hi = groups;
-      while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (pre[mid] <= x) lo = mid; else hi = mid;
-      }
-      enter(lo);
-      start = pre[lo];
-    } else {
-      const int64_t band = (int64_t)features * Pair::BAND * 16;
-      enter((int)(x / band < groups - 1 ? x / band : groups - 1));
-      start = g * band;
-    }
-    ft = (int)((x - start) / cost);
-    const int in = (int)(x - start - (int64_t)ft * cost);
-    rt = min(in / 16, rts - 1);
-    at = start + (int64_t)ft * cost + rt * 16;
+    enter(group_of([&](int2 v) { return v.y <= x; }));
+    int64_t in = x - pre[g].y;
+    const int64_t whole = (int64_t)features * Pair::BAND_COST;
+    const int bands = (rts + Pair::BAND - 1) / Pair::BAND;
+    enter_band((int)(in / whole < bands - 1 ? in / whole : bands - 1));
+    in -= band * whole;
+    ft = (int)(in / band_cost());
+    in -= (int64_t)ft * band_cost();
+    rt = band * Pair::BAND + min((int)in / 16, width - 1);
+    at = pre[g].y + band * whole + (int64_t)ft * band_cost() + (rt - band * Pair::BAND) * 16;
   }
   // Where share i begins in the tile at `at`; near an end, there.
   __device__ __forceinline__ int bound(int i, int per_step) const {
     const int64_t d = edge(i) - at * blocks;
-    const int least = a.counters ? 4 : blocks;
     if (d <= 0) return 0;
     if (d >= (int64_t)per_step * blocks) return blocks;
     const int kb = (int)(d / per_step);
-    return kb < least ? 0 : (blocks - kb < least ? blocks : kb);
+    return kb < 4 ? 0 : (blocks - kb < 4 ? blocks : kb);
   }
-  __device__ __forceinline__ void rows_of(PairItem& p) const {
+  __device__ __forceinline__ void fill(PairItem& p) const {
+    p.g = g;
+    p.ft = ft;
     p.row0 = seg.x + rt * Pair::UNITS * Pair::UNIT;
     p.rows = min(seg.y - p.row0, Pair::UNITS * Pair::UNIT);
-    p.g = a.seg_start ? g : 0;
-    p.ft = ft;
+    p.kb0 = 0;
+    p.kb1 = blocks;
+    p.parts = 1;
+    p.head = p.part = 0;
   }
   __device__ __forceinline__ bool next(PairItem& p) {
     if (t < t_end) {
       locate_tile(t);
-      rows_of(p);
-      p.kb0 = 0;
-      p.kb1 = blocks;
-      p.parts = 1;
-      p.head = p.part = 0;
+      fill(p);
       t += pairs;
-      if (t >= t_end && me < sharers && total > 0) locate(edge(me) / blocks);
+      if (t >= t_end) begin();
       return true;
     }
     if (me >= sharers || total <= 0) return false;
     const int64_t end = edge(me + 1);
-    while (g < groups && at * blocks < end) {
-      const int per_step = rt + 1 < rts ? 16 : unit_cost(units - rt * Pair::UNITS);
-      const int lo = bound(me, per_step), hi = bound(me + 1, per_step);
-      const bool mine = lo < hi;
-      if (mine) {
-        rows_of(p);
+    while (g < a.groups && at * blocks < end) {
+      const int per_step = cost_of(rt), lo = bound(me, per_step), hi = bound(me + 1, per_step);
+      if (lo < hi) {
+        fill(p);
         p.kb0 = lo;
         p.kb1 = hi;
         int first = me, last = me;
@@ -434,16 +431,21 @@ struct PairWalk {
         p.part = me - first;
       }
       at += per_step;
-      if (++rt == rts) {
-        rt = 0;
+      if (++rt == band * Pair::BAND + width) {
         if (++ft == features) {
           ft = 0;
-          do {
-            if (++g < groups) enter(g);
-          } while (g < groups && rts == 0);
+          if ((band + 1) * Pair::BAND < rts) {
+            enter_band(band + 1);
+          } else {
+            do {
+              if (++g < a.groups) enter(g);
+            } while (g < a.groups && rts == 0);
+            if (g < a.groups) enter_band(0);
+          }
         }
+        rt = band * Pair::BAND;
       }
-      if (mine) return true;
+      if (lo < hi) return true;
     }
     return false;
   }
@@ -501,19 +503,19 @@ __device__ __forceinline__ float* part_of(const LinearArgs& a, const PairItem& p
 
 template <bool BF16>
 __global__ void __launch_bounds__(Pair::THREADS, 1) linear_pair_kernel(const LinearArgs a, const __grid_constant__ CUtensorMap map_w,
-                                                                       const __grid_constant__ RowMaps maps_x, int groups) {
+                                                                       const __grid_constant__ RowMaps maps_x) {
   using C = Pair;
   extern __shared__ uint8_t pair_smem_raw[];
   __shared__ uint64_t full[C::STAGES], empty[C::STAGES], acc_full[2], acc_empty[2], item_full[C::ITEMS], item_empty[C::ITEMS], drain;
   __shared__ PairItem items[C::ITEMS];
   __shared__ uint32_t taddr_s, issued_s, tx_s[C::STAGES];  // (steps copied by this CTA, their bytes)
-  __shared__ int scan_s[C::THREADS / 32];
+  __shared__ int2 scan_s[C::THREADS / 32];
   const int tid = threadIdx.x, lane = tid & 31;
   const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
   const uint32_t rank = cluster_rank();
   uint8_t* smem = pair_smem_raw + ((1024 - (smem_addr(pair_smem_raw) & 1023)) & 1023);
   float* epi_s = reinterpret_cast<float*>(smem + C::STAGES * C::STAGE);
-  int32_t* pre = reinterpret_cast<int32_t*>(epi_s + C::EPI * C::BUF);  // the experts' costs, summed
+  int2* pre = reinterpret_cast<int2*>(epi_s + C::EPI * C::BUF);  // the groups' tiles and costs, summed
   if (tid == 0) {
     for (int i = 0; i < C::STAGES; ++i) {
       mbar_init(&full[i], 1);
@@ -533,37 +535,46 @@ __global__ void __launch_bounds__(Pair::THREADS, 1) linear_pair_kernel(const Lin
   cudaGridDependencySynchronize();
   if (warp == 2) tc::tmem_alloc_pair(&taddr_s, 512);
   const int per_pair = a.gated ? 128 : 256, features = (a.n_out + per_pair - 1) / per_pair;
-  if (a.seg_start) {
+  {
     uint32_t bad = 0;
     const int per = (a.groups + C::THREADS - 1) / C::THREADS;
-    int sum = 0;
+    int2 sum = make_int2(0, 0);
     for (int i = 0; i < per; ++i) {
       const int g = tid * per + i;
       if (g >= a.groups) break;
       const int2 seg = group_rows(a, g, bad);
       const int units = (seg.y - seg.x + C::UNIT - 1) / C::UNIT, whole = units / C::UNITS, rest = units % C::UNITS;
-      pre[g] = features * (whole * 16 + (rest ? unit_cost(rest) : 0));
-      sum += pre[g];
+      const int2 v = make_int2(features * (whole + (rest != 0)), features * (whole * 16 + (rest ? unit_cost(rest) : 0)));
+      pre[g] = v;
+      sum.x += v.x;
+      sum.y += v.y;
     }
     if (bad && blockIdx.x == 0) set_error(a.err, bad);
-    int inc = sum;
+    int2 inc = sum;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
-      const int u = __shfl_up_sync(0xffffffffu, inc, d);
-      if (lane >= d) inc += u;
+      const int x = __shfl_up_sync(0xffffffffu, inc.x, d), y = __shfl_up_sync(0xffffffffu, inc.y, d);
+      if (lane >= d) {
+        inc.x += x;
+        inc.y += y;
+      }
     }
     if (lane == 31) scan_s[warp] = inc;
     __syncthreads();
-    int base = inc - sum;
-    for (int w = 0; w < warp; ++w) base += scan_s[w];
+    int2 run = make_int2(inc.x - sum.x, inc.y - sum.y);
+    for (int w = 0; w < warp; ++w) {
+      run.x += scan_s[w].x;
+      run.y += scan_s[w].y;
+    }
     for (int i = 0; i < per; ++i) {
       const int g = tid * per + i;
       if (g >= a.groups) break;
-      const int x = pre[g];
-      pre[g] = base;
-      base += x;
+      const int2 v = pre[g];
+      pre[g] = run;
+      run.x += v.x;
+      run.y += v.y;
     }
-    if (tid == C::THREADS - 1) pre[a.groups] = base;
+    if (tid == C::THREADS - 1) pre[a.groups] = run;
   }
   tc::fence_before_sync();
   __syncthreads();
@@ -656,7 +667,7 @@ __global__ void __launch_bounds__(Pair::THREADS, 1) linear_pair_kernel(const Lin
   } else if (warp == 3) {
     // ----------------------------------------------------------------- items
     if (lane == 0) {
-      PairWalk walk(a, pre, features, groups, gridDim.x / 2, blockIdx.x / 2);
+      PairWalk walk(a, pre, features, gridDim.x / 2, blockIdx.x / 2);
       for (bool more = true; more; ++n) {
         more = walk.next(p);
         if (!more) p.parts = 0;

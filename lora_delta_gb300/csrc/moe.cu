@@ -131,9 +131,7 @@ int launch_pair(const LinearArgs& a, cudaStream_t stream) {
   if (prepare_kernel(linear_pair_kernel<BF16>, (int)smem, false) != cudaSuccess) return LORA_ERR_CUDA;
   int pairs = sm_count() / 2;
   if (pairs > Pair::MAX) pairs = Pair::MAX;
-  constexpr int band = Pair::BAND * Pair::UNITS * Pair::UNIT;
-  const int groups = a.seg_start ? a.groups : (int)(((int64_t)a.n + band - 1) / band);
-  return launch(linear_pair_kernel<BF16>, dim3(2u * (unsigned)pairs), Pair::THREADS, smem, stream, 2, a, map_w, maps_x, groups);
+  return launch(linear_pair_kernel<BF16>, dim3(2u * (unsigned)pairs), Pair::THREADS, smem, stream, 2, a, map_w, maps_x);
 }
 
 // Rows of a group on average, and up to how many the kernel for few rows takes.

@@ -13,7 +13,7 @@
 
 namespace lora {
 
-constexpr int kMoeMaxExperts = 2048;
+constexpr int kMoeMaxExperts = 1024;
 constexpr int kMoeSortCluster = 16;
 constexpr int kMoeThreads = 256;
 

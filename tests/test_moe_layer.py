@@ -79,7 +79,7 @@ def test_refusals_on_the_host():
     assert dispatch(H=60) == align and dispatch(ld_x=68) == align and dispatch(rows=odd) == align
     assert dispatch(ids=ctypes.c_void_p(0x50000002)) == align
     assert dispatch(ld_rows=56) == shape and dispatch(ld_x=56) == shape
-    assert dispatch(E=2049) == unsup and dispatch(k=65) == unsup and dispatch(T=1 << 30) == unsup
+    assert dispatch(E=1025) == unsup and dispatch(k=65) == unsup and dispatch(T=1 << 30) == unsup
     assert dispatch(x=at[0]) == arg and dispatch(x=ctypes.c_void_p(0x10000000 + 2 * 64 * 15)) == arg
     assert dispatch(ids=at[2]) == arg and dispatch(seg=at[2]) == arg and dispatch(pair=at[0]) == arg and dispatch(row_pair=at[3]) == arg
 
@@ -119,7 +119,7 @@ def test_refusals_on_the_host():
         assert linear(E=E, res=ctypes.c_void_p(0x10000000 + 96)) == arg
         assert linear(E=E, n=1000, work=at[7], wsb=1000) == 5 and linear(E=E, work=odd, wsb=1 << 30) == align
     assert linear(E=3, seg=None) == arg and linear(E=3, stride=47 * 64) == shape and linear(E=3, stride=48 * 64 + 8) == shape
-    assert linear(E=2049) == unsup and linear(E=3, seg=at[0]) == arg
+    assert linear(E=1025) == unsup and linear(E=3, seg=at[0]) == arg
 
 
 def test_plans_are_made_on_the_gpu():
@@ -187,7 +187,7 @@ def check_plan(plan, want):
 
 
 @gpu
-@pytest.mark.parametrize("T,k,E,H", [(1, 1, 1, 8), (1, 8, 64, 72), (64, 8, 64, 2048), (63, 3, 7, 264), (130, 16, 256, 4104), (300, 7, 2048, 16),
+@pytest.mark.parametrize("T,k,E,H", [(1, 1, 1, 8), (1, 8, 64, 72), (64, 8, 64, 2048), (63, 3, 7, 264), (130, 16, 256, 4104), (300, 7, 1024, 16),
                                      (2500, 8, 64, 136), (9000, 4, 40, 8), (70001, 2, 33, 8), (20000, 16, 300, 24)])
 def test_dispatch(ld, T, k, E, H):
     rng = np.random.default_rng(T + k)
