@@ -51,13 +51,25 @@ __device__ __forceinline__ int2 group_rows(const LinearArgs& a, int g, uint32_t&
   return make_int2(s1, min(max(e, s1), a.n));
 }
 
-__device__ __forceinline__ float activate(float z, int act) {
-  switch (act) {
-    case LORA_ACT_RELU: return z > 0.0f ? z : (z != z ? z : 0.0f);
-    case LORA_ACT_SILU: return z / (1.0f + expf(-z));
-    case LORA_ACT_GELU: return 0.5f * z * (1.0f + erff(z * 0.70710678f));
-    case LORA_ACT_GELU_TANH: return 0.5f * z * (1.0f + tanhf(0.79788456f * (z + 0.044715f * z * z * z)));
-    default: return z;
+// Of 8 values.  gelu by tanh is z / (1 + exp(-2 u)), as silu with 2 u for z.  (Few
+// instructions matter more than the time they take: the roles of a CTA run at once
+// and fetch theirs side by side.)
+__device__ __forceinline__ void activate8(float* z, int act) {
+  if (act == LORA_ACT_NONE) return;
+  if (act == LORA_ACT_RELU) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) z[i] = z[i] < 0.0f ? 0.0f : z[i];
+  } else if (act == LORA_ACT_GELU) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) z[i] = 0.5f * z[i] * (1.0f + erff(z[i] * 0.70710678f));
+  } else {
+    const float cubic = act == LORA_ACT_SILU ? 0.0f : 2.0f * 0.79788456f * 0.044715f;
+    const float linear = act == LORA_ACT_SILU ? 1.0f : 2.0f * 0.79788456f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float t = z[i] * (cubic == 0.0f ? linear : fmaf(cubic * z[i], z[i], linear));
+      z[i] = __fdividef(z[i], 1.0f + __expf(-t));
+    }
   }
 }
 
@@ -79,24 +91,27 @@ struct LinearBias {
   uint4 half[2];
 };
 
+template <bool GATED>
 __device__ __forceinline__ LinearBias linear_bias(const LinearArgs& a, int g, int col) {
   LinearBias b;
   b.half[0] = b.half[1] = make_uint4(0, 0, 0, 0);
   if (a.bias && col < a.n_out) {
     const uint16_t* at = reinterpret_cast<const uint16_t*>(a.bias) + (int64_t)g * a.N + col;
     b.half[0] = *reinterpret_cast<const uint4*>(at);
-    if (a.gated) b.half[1] = *reinterpret_cast<const uint4*>(at + a.n_out);
+    if (GATED) b.half[1] = *reinterpret_cast<const uint4*>(at + a.n_out);
   }
   return b;
 }
 
+template <bool GATED>
 __device__ __forceinline__ LinearTail linear_tail(const LinearArgs& a, int64_t row, int col, bool use) {
   LinearTail t;
   t.delta[0] = t.delta[1] = t.residual = make_uint4(0, 0, 0, 0);
-  if (!use) return t;
-  if (a.delta) t.delta[0] = load8(a.delta, a.ld_delta, row, col);
-  if (a.delta && a.gated) t.delta[1] = load8(a.delta, a.ld_delta, row, a.n_out + col);
-  if (a.residual) t.residual = load8(a.residual, a.ld_residual, row, col);
+  if (use && a.delta) {
+    t.delta[0] = load8(a.delta, a.ld_delta, row, col);
+    if (GATED) t.delta[1] = load8(a.delta, a.ld_delta, row, a.n_out + col);
+  }
+  if (use && a.residual) t.residual = load8(a.residual, a.ld_residual, row, col);
   return t;
 }
 
@@ -108,23 +123,20 @@ __device__ __forceinline__ void add8(float* z, const uint4& v) {
   for (int i = 0; i < 8; ++i) z[i] += f[i];
 }
 
-template <bool BF16>
-__device__ __forceinline__ void linear_finish(const LinearArgs& a, const LinearBias& b, const LinearTail& t, int64_t row, int col,
-                                              float* z, float* up) {
+// EXTRA: with a delta or a residual.
+template <bool BF16, bool GATED, bool EXTRA>
+__device__ __forceinline__ uint4 linear_finish(const LinearArgs& a, const LinearBias& b, const LinearTail& t, float* z, float* up) {
   if (a.bias) add8<BF16>(z, b.half[0]);
-  if (a.delta) add8<BF16>(z, t.delta[0]);
-  if (a.act != LORA_ACT_NONE) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) z[i] = activate(z[i], a.act);
-  }
-  if (a.gated) {
+  if (EXTRA && a.delta) add8<BF16>(z, t.delta[0]);
+  activate8(z, a.act);
+  if (GATED) {
     if (a.bias) add8<BF16>(up, b.half[1]);
-    if (a.delta) add8<BF16>(up, t.delta[1]);
+    if (EXTRA && a.delta) add8<BF16>(up, t.delta[1]);
 #pragma unroll
     for (int i = 0; i < 8; ++i) z[i] *= up[i];
   }
-  if (a.residual) add8<BF16>(z, t.residual);
-  store8(a.out, a.ld_out, row, col, pack8<BF16>(z));
+  if (EXTRA && a.residual) add8<BF16>(z, t.residual);
+  return pack8<BF16>(z);
 }
 
 // ------------------------------------------------------------- few rows --
@@ -132,18 +144,44 @@ __device__ __forceinline__ void linear_finish(const LinearArgs& a, const LinearB
 // tile's K out, so that few tiles still read W at the card's full rate; their
 // parts are added in the order of K through distributed shared memory, each CTA
 // finishing its share of the tile.  Grid: (feature tile, part of K), group, and
-// row tiles in turn.  Two CTAs fit an SM.
+// row tiles in turn.  Two CTAs fit an SM (one where NT is 256).
 template <int NT_>
 struct Few {
   static constexpr int NT = NT_;
   static constexpr int W = 128 * 128, X = NT * 128, STAGE = W + X;
-  static constexpr int STAGES = 106 * 1024 / STAGE < 8 ? 106 * 1024 / STAGE : 8;
+  static constexpr int STAGES = (NT == 256 ? 208 : 106) * 1024 / STAGE;
   static constexpr int PAD = 132;  // floats between rows of a part
   static constexpr int THREADS = 192;
   static constexpr uint32_t COLS = NT < 32 ? 32 : NT;  // of tensor memory
   static constexpr size_t smem() { return 1024 + (size_t)STAGES * STAGE; }
   static_assert(NT * PAD * 4 <= STAGES * STAGE, "a part lies where the operands were");
 };
+
+// A CTA's share of a tile, from all parts.
+template <bool BF16, bool GATED, class C>
+__device__ __forceinline__ void linear_few_finish(const LinearArgs& a, const float* own, int g, int ft, int r0, int rows, int part, int split) {
+  constexpr int width = GATED ? 8 : 16;  // blocks of 8 columns of out
+  for (int i = part * C::THREADS + (int)threadIdx.x; i < rows * width; i += split * C::THREADS) {
+    const int r = i / width, b = i % width, col = (ft * width + b) * 8;
+    const bool use = col < a.n_out;
+    const LinearBias bias = linear_bias<GATED>(a, g, col);
+    const LinearTail t = linear_tail<GATED>(a, r0 + r, col, use);
+    float z[16] = {};
+    const uint32_t at = smem_addr(own + r * C::PAD + b * 8);
+    for (int p = 0; p < split; ++p) {
+      const uint32_t from = dsmem_map(at, p);
+#pragma unroll
+      for (int j = 0; j < (GATED ? 4 : 2); ++j) {
+        const float4 f = dsmem_ld_f32x4(from + (j < 2 ? 16 * j : 256 + 16 * (j - 2)));
+        z[4 * j] += f.x;
+        z[4 * j + 1] += f.y;
+        z[4 * j + 2] += f.z;
+        z[4 * j + 3] += f.w;
+      }
+    }
+    if (use) store8(a.out, a.ld_out, r0 + r, col, linear_finish<BF16, GATED, true>(a, bias, t, z, z + 8));
+  }
+}
 
 template <bool BF16, class C>
 __global__ void __launch_bounds__(C::THREADS) linear_few_kernel(const LinearArgs a, const __grid_constant__ CUtensorMap map_w,
@@ -187,7 +225,7 @@ __global__ void __launch_bounds__(C::THREADS) linear_few_kernel(const LinearArgs
               ok = false;
               break;
             }
-            mbar_arrive_expect_tx(&full[s], C::W + (2048 << box));
+            mbar_arrive_expect_tx(&full[s], C::W + (2048 << box) + (rows > 128 ? 16384 : 0));
             uint8_t* st = smem + s * C::STAGE;
             if (a.gated) {
               tma_load_3d(st, &map_w, (kb0 + i) * 64, ft * 64, g, &full[s]);
@@ -196,6 +234,7 @@ __global__ void __launch_bounds__(C::THREADS) linear_few_kernel(const LinearArgs
               tma_load_3d(st, &map_w, (kb0 + i) * 64, ft * 128, g, &full[s]);
             }
             tma_load_2d(st + C::W, &maps_x.box[box], (kb0 + i) * 64, r0, &full[s]);
+            if (rows > 128) tma_load_2d(st + C::W + 128 * 128, &maps_x.box[3], (kb0 + i) * 64, r0 + 128, &full[s]);
           }
         }
       } else if (warp == 1) {
@@ -243,28 +282,10 @@ __global__ void __launch_bounds__(C::THREADS) linear_few_kernel(const LinearArgs
     cluster_arrive_release_smem();
     cluster_wait();
     if (!dead) {
-      const int width = a.gated ? 8 : 16, items = rows * width;  // (8 columns of out each)
-      for (int i = part * C::THREADS + tid; i < items; i += split * C::THREADS) {
-        const int r = i / width, b = i % width, col = (ft * width + b) * 8;
-        const bool use = col < a.n_out;
-        const LinearBias bias = linear_bias(a, g, col);
-        const LinearTail t = linear_tail(a, r0 + r, col, use);
-        float z[16] = {};
-        const uint32_t at = smem_addr(own + r * C::PAD + b * 8);
-        for (int p = 0; p < split; ++p) {
-          const uint32_t from = dsmem_map(at, p);
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-            if (j < 2 || a.gated) {
-              const float4 f = dsmem_ld_f32x4(from + (j < 2 ? 16 * j : 256 + 16 * (j - 2)));
-              z[4 * j] += f.x;
-              z[4 * j + 1] += f.y;
-              z[4 * j + 2] += f.z;
-              z[4 * j + 3] += f.w;
-            }
-        }
-        if (use) linear_finish<BF16>(a, bias, t, r0 + r, col, z, z + 8);
-      }
+      if (a.gated)
+        linear_few_finish<BF16, true, C>(a, own, g, ft, r0, rows, part, split);
+      else
+        linear_few_finish<BF16, false, C>(a, own, g, ft, r0, rows, part, split);
     }
     fence_proxy_async_smem();  // (the memory is next written by copies)
     __syncwarp();
@@ -283,15 +304,16 @@ __global__ void __launch_bounds__(C::THREADS) linear_few_kernel(const LinearArgs
 // items ahead, a load warp, an MMA warp (of the even CTA) and 8 epilogue warps, the
 // sums of one tile in one half of tensor memory while the epilogue reads the other's.
 struct Pair {
-  static constexpr int W = 128 * 128, X = 128 * 128, STAGE = W + X, STAGES = 6;
+  static constexpr int W = 128 * 128, X = 128 * 128, STAGE = W + X, STAGES = 5;
   static constexpr int EPI = 8, EPI_WARP = 4, THREADS = (EPI_WARP + EPI) * 32;
-  static constexpr int PAD = 36, BUF = 16 * PAD;  // floats: 16 rows of 32 sums
+  static constexpr int PAD = 36, BUF = 32 * PAD;  // floats: 32 rows of 32 sums
   static constexpr int UNIT = 64, UNITS = 4;      // a tile is 1 to 4 units of rows
   static constexpr int BAND = 16;                 // row tiles that a feature tile is used for in turn
   static constexpr int BAND_COST = BAND * 16;
   static constexpr int MAX = 80;                  // pairs that share tiles
   static constexpr int PART = 128 * 256;          // floats of a CTA's part of a tile
   static constexpr int ITEMS = 4;                 // items laid out ahead
+  static constexpr int SHARE = 512;               // what sharing tiles costs a pair, as 32 steps of a full tile
   static constexpr size_t smem(int groups) { return 1024 + (size_t)STAGES * STAGE + EPI * BUF * 4 + (size_t)(groups + 1) * 8; }
 };
 constexpr size_t kLinearCounterBytes = (size_t)Pair::MAX * 8 * 4;
@@ -305,18 +327,21 @@ __device__ __forceinline__ int unit_cost(int units) { return units == 4 ? 16 : 7
 struct PairItem {
   int g, row0, rows, ft, kb0, kb1;
   int head, parts, part;  // the pair that has the tile's first steps, how many share it, which this one is
+  int last;               // of the pair's items
 };
 
 // The pairs' items.  Tiles lie end to end: by group, band of 16 row tiles, feature
 // tile, row tile.  Whole rounds of tiles are taken in turns, so that the pairs use
 // the same rows and weights at the same time (contiguous shares of all: 16384 rows
 // of 64 experts 197 us for 148, x read from memory again); the last rounds are cut
-// into equal shares of cost, within tiles where need be.
+// into equal shares of cost, within tiles where need be.  A pair's place moves on by
+// 13 a round: full and ragged row tiles alternate, and 76 pairs would meet the same
+// of them each time (16384 rows of 64 experts, 768 by 2048: 158 us for 100).
 struct PairWalk {
   const LinearArgs& a;
   const int2* pre;  // of the groups: tiles and cost (a step of K) so far
   int features, blocks, pairs, me;
-  int t, t_end;                              // next tile in turn
+  int round, t_end;                          // of the tiles in turn
   int g, units, rts, band, width, ft, rt;    // the tile of the shares; row tiles of its band
   int2 seg;
   int64_t at, base, total;                   // its position; of the shares: first position, cost (a step of K)
@@ -325,7 +350,7 @@ struct PairWalk {
   __device__ __forceinline__ PairWalk(const LinearArgs& a, const int2* pre, int features, int pairs, int me)
       : a(a), pre(pre), features(features), blocks((a.K + 63) / 64), pairs(pairs), me(me) {
     const int tiles = pre[a.groups].x;
-    t = me;
+    round = 0;
     int turns = tiles / pairs;
     if (tiles % pairs && turns) --turns;
     t_end = a.counters ? turns * pairs : tiles;
@@ -334,12 +359,18 @@ struct PairWalk {
       locate_tile(t_end);
       base = at;
       total = pre[a.groups].y - base;
+      const int64_t whole = (int64_t)((tiles - t_end + pairs - 1) / pairs) * 16 * blocks;  // a pair's cost without
+      if (total * blocks + (int64_t)Pair::SHARE * pairs >= whole * pairs) {
+        t_end = tiles;
+        total = 0;
+      }
     }
     // a share is at least 8 steps of a full tile
     const int64_t most = total * blocks / 128;
     sharers = (int)(most < 1 ? 1 : (most < pairs ? most : pairs));
-    if (t >= t_end) begin();
+    if (turn() >= t_end) begin();
   }
+  __device__ __forceinline__ int turn() const { return round * pairs + (int)((me + 13ll * round) % pairs); }
   __device__ __forceinline__ void begin() {
     if (me < sharers && total > 0) locate(edge(me) / blocks);
   }
@@ -408,11 +439,11 @@ struct PairWalk {
     p.head = p.part = 0;
   }
   __device__ __forceinline__ bool next(PairItem& p) {
-    if (t < t_end) {
-      locate_tile(t);
+    if (turn() < t_end) {
+      locate_tile(turn());
       fill(p);
-      t += pairs;
-      if (t >= t_end) begin();
+      ++round;
+      if (turn() >= t_end) begin();
       return true;
     }
     if (me >= sharers || total <= 0) return false;
@@ -501,12 +532,13 @@ __device__ __forceinline__ float* part_of(const LinearArgs& a, const PairItem& p
   return a.parts + ((int64_t)((p.head + x) * 2 + (x == 0)) * 2 + rank) * Pair::PART + warp * 128 * 32;
 }
 
-template <bool BF16>
+template <bool BF16, bool GATED, bool EXTRA>
 __global__ void __launch_bounds__(Pair::THREADS, 1) linear_pair_kernel(const LinearArgs a, const __grid_constant__ CUtensorMap map_w,
                                                                        const __grid_constant__ RowMaps maps_x) {
   using C = Pair;
   extern __shared__ uint8_t pair_smem_raw[];
   __shared__ uint64_t full[C::STAGES], empty[C::STAGES], acc_full[2], acc_empty[2], item_full[C::ITEMS], item_empty[C::ITEMS], drain;
+  __shared__ uint64_t part_full[C::EPI];
   __shared__ PairItem items[C::ITEMS];
   __shared__ uint32_t taddr_s, issued_s, tx_s[C::STAGES];  // (steps copied by this CTA, their bytes)
   __shared__ int2 scan_s[C::THREADS / 32];
@@ -529,12 +561,14 @@ __global__ void __launch_bounds__(Pair::THREADS, 1) linear_pair_kernel(const Lin
       mbar_init(&item_full[i], 1);
       mbar_init(&item_empty[i], 1 + (rank == 0) + C::EPI);  // load, MMA and epilogue warps
     }
+    for (int i = 0; i < C::EPI; ++i) mbar_init(&part_full[i], 1);
     mbar_init(&drain, 1);
     fence_barrier_init();
   }
   cudaGridDependencySynchronize();
   if (warp == 2) tc::tmem_alloc_pair(&taddr_s, 512);
-  const int per_pair = a.gated ? 128 : 256, features = (a.n_out + per_pair - 1) / per_pair;
+  constexpr int per_pair = GATED ? 128 : 256;
+  const int features = (a.n_out + per_pair - 1) / per_pair;
   {
     uint32_t bad = 0;
     const int per = (a.groups + C::THREADS - 1) / C::THREADS;
@@ -615,7 +649,7 @@ __global__ void __launch_bounds__(Pair::THREADS, 1) linear_pair_kernel(const Lin
           if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * bytes);
           const uint32_t bar = leader_full + s * 8;
           uint8_t* st = smem + s * C::STAGE;
-          if (a.gated) {
+          if (GATED) {
             tma_load_3d_pair(st, &map_w, kb * 64, p.ft * 128 + (int)rank * 64, p.g, bar);
             tma_load_3d_pair(st + 64 * 128, &map_w, kb * 64, a.n_out + p.ft * 128 + (int)rank * 64, p.g, bar);
           } else {
@@ -668,9 +702,13 @@ __global__ void __launch_bounds__(Pair::THREADS, 1) linear_pair_kernel(const Lin
     // ----------------------------------------------------------------- items
     if (lane == 0) {
       PairWalk walk(a, pre, features, gridDim.x / 2, blockIdx.x / 2);
-      for (bool more = true; more; ++n) {
-        more = walk.next(p);
+      PairItem ahead;
+      bool more = walk.next(ahead);
+      for (p.parts = 1; p.parts; ++n) {
+        p = ahead;
         if (!more) p.parts = 0;
+        if (more) more = walk.next(ahead);
+        p.last = !more;
         if (n >= C::ITEMS && !mbar_wait_bounded(&item_empty[n % C::ITEMS], (n / C::ITEMS - 1) & 1, 4 * kWaitLimitNs)) {
           ok = false;
           break;
@@ -683,10 +721,11 @@ __global__ void __launch_bounds__(Pair::THREADS, 1) linear_pair_kernel(const Lin
     // -------------------------------------------------------------- epilogue
     // A warp reads 32 rows of W of half of the tile's columns.  Gated, the warps
     // of a half's first and second 32 rows work with those of the other half's.
-    const int q = warp & 3, side = (warp - C::EPI_WARP) / 4, bar = 1 + side * 2 + (q & 1);
-    float* buf = epi_s + (warp - C::EPI_WARP) * C::BUF;
-    const float *first_half = epi_s + (side * 4 + (a.gated ? q & 1 : q)) * C::BUF, *second_half = epi_s + (side * 4 + 2 + (q & 1)) * C::BUF;
-    const int block = lane % 4, row_1 = (a.gated ? q >> 1 : 0) * 8 + lane / 4;  // (of 16 rows: this and, not gated, 8 on)
+    const int ew = warp - C::EPI_WARP, q = warp & 3, side = ew / 4, bar = 1 + side * 2 + (q & 1);
+    float* buf = epi_s + ew * C::BUF;
+    const float *first_half = epi_s + (side * 4 + (GATED ? q & 1 : q)) * C::BUF, *second_half = epi_s + (side * 4 + 2 + (q & 1)) * C::BUF;
+    constexpr int MINE = GATED ? 2 : 4;  // of 32 rows, a lane's, 8 apart
+    const int block = lane % 4, my_row = (GATED ? (q >> 1) * 16 : 0) + lane / 4;
     const uint32_t leader_empty = dsmem_map(smem_addr(acc_empty), 0);
     // (after a wait that gave up, shared tiles are still counted, so that the
     // counters end at zero)
@@ -694,76 +733,123 @@ __global__ void __launch_bounds__(Pair::THREADS, 1) linear_pair_kernel(const Lin
       __syncwarp();
       if (lane == 0) pass();
       const int cols = (p.rows + 63) / 64 * 64, c0 = side * cols / 2, c1 = min(c0 + cols / 2, p.rows);
-      const int col = p.ft * per_pair + (int)rank * (per_pair / 2) + (a.gated ? q & 1 : q) * 32 + block * 8;
+      const int col = p.ft * per_pair + (int)rank * (per_pair / 2) + (GATED ? q & 1 : q) * 32 + block * 8;
       if (ok) ok = mbar_wait_soon(&acc_full[n & 1], (n / 2) & 1, a.wait_ns);
       ok = barrier_and(bar, 64, ok);  // (the warps that work together go on together)
       tc::fence_after_sync();
       const uint32_t acc = tmem + (n & 1) * 256 + ((uint32_t)(q * 32) << 16);
       bool finish = ok;
       if (p.parts > 1) {
-        float* own = part_of(a, p, p.part, rank, warp - C::EPI_WARP) + lane;
-        if (ok)
-          for (int c = c0; c < c1; c += 16) {
-            float v[16];
-            tc::tmem_ld16(acc + c, v);
-#pragma unroll
-            for (int i = 0; i < 16; ++i) __stcg(own + (c - c0 + i) * 32, v[i]);
-          }
-        __threadfence();
-        barrier_sync(bar, 64);
+        // The last to come finishes the tile.  Who finds all others there need
+        // not write a part; else it writes, and may be the last all the same.
+        uint32_t* count = a.counters + (p.head * 2 + (int)rank) * 4 + bar - 1;
+        const bool counts = q < 2 && lane == 0;
         bool last = true;
-        if (q < 2 && lane == 0) {
-          uint32_t* count = a.counters + (p.head * 2 + (int)rank) * 4 + bar - 1;
-          last = atomicAdd(count, 1u) + 1 == (uint32_t)p.parts;
-          if (last) *count = 0;
+        if (counts) {
+          last = atomicAdd(count, 0u) + 1 == (uint32_t)p.parts;
           __threadfence();
         }
-        finish = barrier_and(bar, 64, last) && ok;
+        if (!barrier_and(bar, 64, last)) {
+          float* own = part_of(a, p, p.part, rank, ew) + lane;
+          if (ok)
+            for (int c = c0; c < c1; c += 32) {
+              float v[32];
+              tc::tmem_ld32(acc + c, v);
+#pragma unroll
+              for (int i = 0; i < 32; ++i) __stcg(own + (c - c0 + i) * 32, v[i]);
+            }
+          __threadfence();
+          barrier_sync(bar, 64);
+          last = true;
+          if (counts) {
+            last = atomicAdd(count, 1u) + 1 == (uint32_t)p.parts;
+            __threadfence();
+          }
+          last = barrier_and(bar, 64, last);
+        } else {
+          last = true;
+        }
+        if (last && counts) *count = 0;
+        finish = last && ok;
+        if (finish) {
+          // The others' parts are added in the order of K, whoever adds, and the sums
+          // go back to tensor memory.  Where this is the pair's last item, as it mostly
+          // is, the operands' memory is free, and the parts come there by bulk copies,
+          // `step` columns at once.
+          const int others = p.parts - 1, step = C::STAGES * C::STAGE / (C::EPI * 128 * others) / 32 * 32;
+          const bool copy = p.last && step > 0;
+          float* room = reinterpret_cast<float*>(smem) + ew * (C::STAGES * C::STAGE / (C::EPI * 4));
+          for (int c = c0, from_c = c0, ready = c0; c < c1; c += 32) {
+            if (copy && c == ready) {
+              const int count = min(step, c0 + cols / 2 - c);
+              __syncwarp();
+              if (lane == 0) {
+                mbar_arrive_expect_tx(&part_full[ew], others * count * 128);
+                for (int x = 0, at = 0; x < p.parts; ++x)
+                  if (x != p.part) bulk_g2s(room + at++ * step * 32, part_of(a, p, x, rank, ew) + (c - c0) * 32, count * 128, &part_full[ew]);
+              }
+              ok = __all_sync(0xffffffffu, mbar_wait_soon(&part_full[ew], ((c - c0) / step) & 1, 4 * kWaitLimitNs)) && ok;
+              from_c = c;
+              ready += step;
+            }
+            float own[32], sum[32];
+            tc::tmem_ld32(acc + c, own);
+            for (int x = 0, at = 0; x < p.parts; ++x) {
+              if (x == p.part) {
+#pragma unroll
+                for (int i = 0; i < 32; ++i) sum[i] = x ? sum[i] + own[i] : own[i];
+                continue;
+              }
+              const float* from = copy ? room + (at * step + c - from_c) * 32 + lane : part_of(a, p, x, rank, ew) + (c - c0) * 32 + lane;
+              ++at;
+              float part[32];
+              if (copy) {
+#pragma unroll
+                for (int i = 0; i < 32; ++i) part[i] = from[i * 32];
+              } else {
+#pragma unroll
+                for (int i = 0; i < 32; ++i) part[i] = __ldcg(from + i * 32);
+              }
+#pragma unroll
+              for (int i = 0; i < 32; ++i) sum[i] = x ? sum[i] + part[i] : part[i];
+            }
+            tc::tmem_st16(acc + c, reinterpret_cast<const uint32_t*>(sum));
+            tc::tmem_st16(acc + c + 16, reinterpret_cast<const uint32_t*>(sum + 16));
+          }
+          tc::tmem_wait_st();
+        }
       }
       if (finish) {
-        const LinearBias bias = linear_bias(a, p.g, col);
-        LinearTail tail[2];
-        auto fetch = [&](int c) {
-#pragma unroll
-          for (int i = 0; i < 2; ++i)
-            if (i == 0 || !a.gated) {
-              const int r = c + row_1 + 8 * i;
-              tail[i] = linear_tail(a, p.row0 + r, col, r < c1 && col < a.n_out);
-            }
+        const LinearBias bias = linear_bias<GATED>(a, p.g, col);
+        LinearTail tail[MINE];
+        auto fetch = [&](int c, int i) {
+          const int r = c + my_row + 8 * i;
+          if (EXTRA) tail[i] = linear_tail<GATED>(a, p.row0 + r, col, r < c1 && col < a.n_out);
         };
-        fetch(c0);
-        for (int c = c0; c < c1; c += 16) {
-          float v[16];
-          if (p.parts == 1) {
-            tc::tmem_ld16(acc + c, v);
-          } else {  // in the order of K, whoever adds
-            const float* from = part_of(a, p, 0, rank, warp - C::EPI_WARP) + (c - c0) * 32 + lane;
 #pragma unroll
-            for (int i = 0; i < 16; ++i) v[i] = __ldcg(from + i * 32);
-            for (int x = 1; x < p.parts; ++x) {
-              from = part_of(a, p, x, rank, warp - C::EPI_WARP) + (c - c0) * 32 + lane;
+        for (int i = 0; i < MINE; ++i) fetch(c0, i);
+        uint32_t sums[32];
+        if (c0 < c1) tc::tmem_ld32_start(acc + c0, sums);
+        for (int c = c0; c < c1; c += 32) {
+          tc::tmem_ld32_wait(sums);
 #pragma unroll
-              for (int i = 0; i < 16; ++i) v[i] += __ldcg(from + i * 32);
+          for (int i = 0; i < 32; ++i) buf[i * C::PAD + lane] = __uint_as_float(sums[i]);
+          if (GATED) barrier_sync(bar, 64); else __syncwarp();
+          if (c + 32 < c1) tc::tmem_ld32_start(acc + c + 32, sums);  // (ahead, as each row's delta and residual)
+#pragma unroll
+          for (int i = 0; i < MINE; ++i) {
+            const int r = my_row + 8 * i, at = r * C::PAD + block * 8;
+            float z[16];
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              *reinterpret_cast<float4*>(z + 4 * j) = *reinterpret_cast<const float4*>(first_half + at + 4 * j);
+              if (GATED) *reinterpret_cast<float4*>(z + 8 + 4 * j) = *reinterpret_cast<const float4*>(second_half + at + 4 * j);
             }
+            const uint4 y = linear_finish<BF16, GATED, EXTRA>(a, bias, tail[i], z, z + 8);
+            fetch(c + 32, i);
+            if (c + r < c1 && col < a.n_out) store8(a.out, a.ld_out, p.row0 + c + r, col, y);
           }
-#pragma unroll
-          for (int i = 0; i < 16; ++i) buf[i * C::PAD + lane] = v[i];
-          if (a.gated) barrier_sync(bar, 64); else __syncwarp();
-          const LinearTail now[2] = {tail[0], tail[1]};
-          if (c + 16 < c1) fetch(c + 16);  // (ahead of this part's work)
-#pragma unroll
-          for (int i = 0; i < 2; ++i)
-            if (i == 0 || !a.gated) {
-              const int r = row_1 + 8 * i, at = r * C::PAD + block * 8;
-              float z[16];
-#pragma unroll
-              for (int j = 0; j < 2; ++j) {
-                *reinterpret_cast<float4*>(z + 4 * j) = *reinterpret_cast<const float4*>(first_half + at + 4 * j);
-                *reinterpret_cast<float4*>(z + 8 + 4 * j) = *reinterpret_cast<const float4*>(second_half + at + 4 * j);
-              }
-              if (c + r < c1 && col < a.n_out) linear_finish<BF16>(a, bias, now[i], p.row0 + c + r, col, z, z + 8);
-            }
-          if (a.gated) barrier_sync(bar, 64); else __syncwarp();
+          if (GATED) barrier_sync(bar, 64); else __syncwarp();
         }
       }
       tc::fence_before_sync();

@@ -112,26 +112,28 @@ int launch_few(const LinearArgs& a, cudaStream_t stream) {
   const int per = a.gated ? 64 : 128, features = (a.n_out + per - 1) / per, blocks = (a.K + 63) / 64;
   const int64_t row_tiles = ((int64_t)a.n + NT - 1) / NT;
   const int z = (int)(a.seg_start ? (row_tiles < 2 ? row_tiles : 2) : (row_tiles < 65535 ? row_tiles : 65535));
-  // K in as many parts as leave the tiles' clusters room at two CTAs an SM
+  // K in as many parts as give an SM 1.6 CTAs (48 tiles of 1 row and K = 4096, parts
+  // of K: 1 23.2 us, 2 14.9, 3 13.2, 4 12.7, 5 13.0, 6 19.2; 32 tiles of 64 rows and
+  // K = 14336: 1 93.8, 4 29.7, 5 28.3, 8 28.3)
   const int64_t tiles = (int64_t)features * a.groups * (a.seg_start ? 1 : z);
-  static const int force = env_int("LORA_LINEAR_SPLIT", 0);
-  int split = (int)(2 * (int64_t)sm_count() / tiles);
-  split = force ? force : (split < 1 ? 1 : (split > 8 ? 8 : split));
+  int64_t split = sm_count() * 8 / 5 / tiles;
+  split = split < 1 ? 1 : (split > 8 ? 8 : split);
   if (split > blocks) split = blocks;
   return launch(linear_few_kernel<BF16, C>, dim3((unsigned)(features * split), (unsigned)a.groups, (unsigned)z), C::THREADS,
-                C::smem(), stream, split, a, map_w, maps_x, split);
+                C::smem(), stream, (int)split, a, map_w, maps_x, (int)split);
 }
 
-template <bool BF16>
+template <bool BF16, bool GATED, bool EXTRA>
 int launch_pair(const LinearArgs& a, cudaStream_t stream) {
   CUtensorMap map_w;
   RowMaps maps_x = {};
   if (!encode_w(&map_w, a, BF16) || !encode_x(&maps_x, a, BF16, 1, 3)) return LORA_ERR_CUDA;
   const size_t smem = Pair::smem(a.groups);
-  if (prepare_kernel(linear_pair_kernel<BF16>, (int)smem, false) != cudaSuccess) return LORA_ERR_CUDA;
+  const auto kernel = linear_pair_kernel<BF16, GATED, EXTRA>;
+  if (prepare_kernel(kernel, (int)smem, false) != cudaSuccess) return LORA_ERR_CUDA;
   int pairs = sm_count() / 2;
   if (pairs > Pair::MAX) pairs = Pair::MAX;
-  return launch(linear_pair_kernel<BF16>, dim3(2u * (unsigned)pairs), Pair::THREADS, smem, stream, 2, a, map_w, maps_x);
+  return launch(kernel, dim3(2u * (unsigned)pairs), Pair::THREADS, smem, stream, 2, a, map_w, maps_x);
 }
 
 // Rows of a group on average, and up to how many the kernel for few rows takes.
@@ -144,12 +146,17 @@ int few_rows() {
 template <bool BF16>
 int linear_launch(const LinearArgs& a, cudaStream_t stream) {
   const int64_t rows = mean_rows(a.n, a.groups);
-  if (rows > few_rows()) return launch_pair<BF16>(a, stream);
+  if (rows > few_rows()) {
+    const bool extra = a.delta || a.residual;
+    if (a.gated) return extra ? launch_pair<BF16, true, true>(a, stream) : launch_pair<BF16, true, false>(a, stream);
+    return extra ? launch_pair<BF16, false, true>(a, stream) : launch_pair<BF16, false, false>(a, stream);
+  }
   const int64_t want = a.seg_start && a.groups > 1 ? 2 * rows : rows;
   if (want <= 16) return launch_few<BF16, 16>(a, stream);
   if (want <= 32) return launch_few<BF16, 32>(a, stream);
   if (want <= 64) return launch_few<BF16, 64>(a, stream);
-  return launch_few<BF16, 128>(a, stream);
+  if (want <= 128) return launch_few<BF16, 128>(a, stream);
+  return launch_few<BF16, 256>(a, stream);
 }
 
 int linear_call(LinearArgs& a, int dtype, void* workspace, size_t ws_bytes, cudaStream_t stream) {
