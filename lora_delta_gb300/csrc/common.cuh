@@ -189,6 +189,10 @@ __device__ __forceinline__ void tma_load_3d(void* dst, const void* map, int c0, 
       "l"(map), "r"(c0), "r"(c1), "r"(c2), "r"(smem_addr(bar))
       : "memory");
 }
+// The same box into L2 only.
+__device__ __forceinline__ void tma_prefetch_3d(const void* map, int c0, int c1, int c2) {
+  asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global.tile [%0, {%1, %2, %3}];" ::"l"(map), "r"(c0), "r"(c1), "r"(c2) : "memory");
+}
 // Of a pair of CTAs: into this CTA's memory, completing a barrier of either CTA
 // (`bar`: its address in the cluster).
 __device__ __forceinline__ void tma_load_2d_pair(void* dst, const void* map, int c0, int c1, uint32_t bar) {

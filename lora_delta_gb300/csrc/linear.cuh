@@ -151,40 +151,63 @@ struct Few {
   static constexpr int W = 128 * 128, X = NT * 128, STAGE = W + X;
   static constexpr int STAGES = (NT == 256 ? 208 : 106) * 1024 / STAGE;
   static constexpr int PAD = 132;  // floats between rows of a part
-  static constexpr int THREADS = 192;
+  static constexpr int THREADS = 256;  // load, MMA, 4 warps that read the sums; all finish
   static constexpr uint32_t COLS = NT < 32 ? 32 : NT;  // of tensor memory
   static constexpr size_t smem() { return 1024 + (size_t)STAGES * STAGE; }
   static_assert(NT * PAD * 4 <= STAGES * STAGE, "a part lies where the operands were");
 };
 
-// A CTA's share of a tile, from all parts.
+// A CTA's share of a tile, from all parts: 8 columns of out a thread.  What is read
+// from global memory for the first of them is on its way while the parts are awaited.
 template <bool BF16, bool GATED, class C>
-__device__ __forceinline__ void linear_few_finish(const LinearArgs& a, const float* own, int g, int ft, int r0, int rows, int part, int split) {
-  constexpr int width = GATED ? 8 : 16;  // blocks of 8 columns of out
-  for (int i = part * C::THREADS + (int)threadIdx.x; i < rows * width; i += split * C::THREADS) {
+__device__ __forceinline__ void linear_few_finish(const LinearArgs& a, const float* own, int g, int ft, int r0, int rows, int part,
+                                                  int split, bool use) {
+  constexpr int width = GATED ? 8 : 16;
+  LinearBias bias;
+  LinearTail t;
+  auto fetch = [&](int i) {
+    const int col = (ft * width + i % width) * 8;
+    bias = linear_bias<GATED>(a, g, use ? col : a.n_out);
+    t = linear_tail<GATED>(a, r0 + i / width, col, use && i < rows * width && col < a.n_out);
+  };
+  int i = part * C::THREADS + (int)threadIdx.x;
+  fetch(i);
+  cluster_wait();
+  for (; use && i < rows * width; i += split * C::THREADS) {
     const int r = i / width, b = i % width, col = (ft * width + b) * 8;
-    const bool use = col < a.n_out;
-    const LinearBias bias = linear_bias<GATED>(a, g, col);
-    const LinearTail t = linear_tail<GATED>(a, r0 + r, col, use);
     float z[16] = {};
     const uint32_t at = smem_addr(own + r * C::PAD + b * 8);
-    for (int p = 0; p < split; ++p) {
-      const uint32_t from = dsmem_map(at, p);
+    constexpr int AT_ONCE = GATED ? 2 : 4;
+#pragma unroll 1
+    for (int p = 0; p < split; p += AT_ONCE) {
+      float4 f[AT_ONCE][GATED ? 4 : 2];
 #pragma unroll
-      for (int j = 0; j < (GATED ? 4 : 2); ++j) {
-        const float4 f = dsmem_ld_f32x4(from + (j < 2 ? 16 * j : 256 + 16 * (j - 2)));
-        z[4 * j] += f.x;
-        z[4 * j + 1] += f.y;
-        z[4 * j + 2] += f.z;
-        z[4 * j + 3] += f.w;
-      }
+      for (int x = 0; x < AT_ONCE; ++x)
+        if (p + x < split) {
+          const uint32_t from = dsmem_map(at, p + x);
+#pragma unroll
+          for (int j = 0; j < (GATED ? 4 : 2); ++j) f[x][j] = dsmem_ld_f32x4(from + (j < 2 ? 16 * j : 256 + 16 * (j - 2)));
+        }
+#pragma unroll
+      for (int x = 0; x < AT_ONCE; ++x)
+        if (p + x < split) {
+#pragma unroll
+          for (int j = 0; j < (GATED ? 4 : 2); ++j) {
+            z[4 * j] += f[x][j].x;
+            z[4 * j + 1] += f[x][j].y;
+            z[4 * j + 2] += f[x][j].z;
+            z[4 * j + 3] += f[x][j].w;
+          }
+        }
     }
-    if (use) store8(a.out, a.ld_out, r0 + r, col, linear_finish<BF16, GATED, true>(a, bias, t, z, z + 8));
+    const uint4 y = linear_finish<BF16, GATED, true>(a, bias, t, z, z + 8);
+    if (col < a.n_out) store8(a.out, a.ld_out, r0 + r, col, y);
+    if (i + split * C::THREADS < rows * width) fetch(i + split * C::THREADS);
   }
 }
 
 template <bool BF16, class C>
-__global__ void __launch_bounds__(C::THREADS) linear_few_kernel(const LinearArgs a, const __grid_constant__ CUtensorMap map_w,
+__global__ void __launch_bounds__(C::THREADS, C::NT == 256 ? 1 : 2) linear_few_kernel(const LinearArgs a, const __grid_constant__ CUtensorMap map_w,
                                                                const __grid_constant__ RowMaps maps_x, int split) {
   extern __shared__ uint8_t few_smem_raw[];
   __shared__ uint64_t full[C::STAGES], empty[C::STAGES], done;
@@ -201,6 +224,16 @@ __global__ void __launch_bounds__(C::THREADS) linear_few_kernel(const LinearArgs
     }
     mbar_init(&done, 1);
     fence_barrier_init();
+  }
+  // What the call before writes is not read ahead of the wait, but W may come to L2
+  // (a product of one group knows its part; up to 48 MB of all CTAs' parts).
+  cudaTriggerProgrammaticLaunchCompletion();
+  if (warp == 0 && !a.seg_start && blockIdx.z == 0) {
+    const int most = max(1, (48 << 20) / (int)(gridDim.x * C::W));
+    for (int i = lane; i < min(nkb, most); i += 32) {
+      tma_prefetch_3d(&map_w, (kb0 + i) * 64, ft * (a.gated ? 64 : 128), 0);
+      if (a.gated) tma_prefetch_3d(&map_w, (kb0 + i) * 64, a.n_out + ft * 64, 0);
+    }
   }
   cudaGridDependencySynchronize();
   if (warp == 1) tc::tmem_alloc(&taddr_s, C::COLS);
@@ -267,9 +300,10 @@ __global__ void __launch_bounds__(C::THREADS) linear_few_kernel(const LinearArgs
       }
     }
     float* own = reinterpret_cast<float*>(smem);  // [rows][PAD]: this CTA's part of the sums
-    if (!dead && warp >= 2) {
+    if (!dead && warp >= 2 && warp < 6) {
       tc::fence_after_sync();
       const int q = warp & 3;
+#pragma unroll 2
       for (int c = 0; c < rows; c += 16) {
         float v[16];
         tc::tmem_ld16(tmem + ((uint32_t)(q * 32) << 16) + c, v);
@@ -280,13 +314,10 @@ __global__ void __launch_bounds__(C::THREADS) linear_few_kernel(const LinearArgs
     }
     __syncwarp();
     cluster_arrive_release_smem();
-    cluster_wait();
-    if (!dead) {
-      if (a.gated)
-        linear_few_finish<BF16, true, C>(a, own, g, ft, r0, rows, part, split);
-      else
-        linear_few_finish<BF16, false, C>(a, own, g, ft, r0, rows, part, split);
-    }
+    if (a.gated)
+      linear_few_finish<BF16, true, C>(a, own, g, ft, r0, rows, part, split, !dead);
+    else
+      linear_few_finish<BF16, false, C>(a, own, g, ft, r0, rows, part, split, !dead);
     fence_proxy_async_smem();  // (the memory is next written by copies)
     __syncwarp();
     cluster_arrive();
@@ -565,6 +596,7 @@ __global__ void __launch_bounds__(Pair::THREADS, 1) linear_pair_kernel(const Lin
     mbar_init(&drain, 1);
     fence_barrier_init();
   }
+  cudaTriggerProgrammaticLaunchCompletion();
   cudaGridDependencySynchronize();
   if (warp == 2) tc::tmem_alloc_pair(&taddr_s, 512);
   constexpr int per_pair = GATED ? 128 : 256;

@@ -56,6 +56,7 @@ inline size_t moe_sort_smem(int E) { return sizeof(uint32_t) * ((size_t)kRouteWa
 __global__ void __launch_bounds__(kRouteThreads) moe_sort_kernel(const MoePlanArgs a) {
   extern __shared__ uint32_t cnt[];  // [kRouteWarps][E + 1], then mine, before, total
   __shared__ uint32_t warp_sums[kRouteWarps];
+  cudaTriggerProgrammaticLaunchCompletion();
   cudaGridDependencySynchronize();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int E = a.key.E, nkb = E + 1, nblk = (int)gridDim.x, blk = (int)blockIdx.x;
@@ -182,6 +183,7 @@ __device__ __forceinline__ void store8(void* base, int64_t ld, int64_t row, int 
 
 // rows[pair_row[t, j]] = x[t]
 __global__ void __launch_bounds__(kMoeThreads) moe_scatter_kernel(const MoveArgs a) {
+  cudaTriggerProgrammaticLaunchCompletion();
   cudaGridDependencySynchronize();
   const int t = blockIdx.x;
   for (int c = threadIdx.x * 8; c < a.H; c += kMoeThreads * 8) {
@@ -196,6 +198,7 @@ __global__ void __launch_bounds__(kMoeThreads) moe_scatter_kernel(const MoveArgs
 // out[t] = residual[t] + sum_j w[t, j] rows[pair_row[t, j]], in the order of j
 template <bool BF16>
 __global__ void __launch_bounds__(kMoeThreads) moe_combine_kernel(const MoveArgs a) {
+  cudaTriggerProgrammaticLaunchCompletion();
   cudaGridDependencySynchronize();
   const int t = blockIdx.x;
   for (int c = threadIdx.x * 8; c < a.H; c += kMoeThreads * 8) {
@@ -224,6 +227,7 @@ __global__ void __launch_bounds__(kMoeThreads) moe_combine_kernel(const MoveArgs
 template <bool BF16>
 __global__ void __launch_bounds__(kMoeThreads) moe_combine_grad_kernel(const MoveArgs a) {
   __shared__ float part[kMoeThreads / 32];
+  cudaTriggerProgrammaticLaunchCompletion();
   cudaGridDependencySynchronize();
   const int t = blockIdx.x;
   for (int j = 0; j < a.top_k; ++j) {
