@@ -123,19 +123,19 @@ __device__ __forceinline__ void add8(float* z, const uint4& v) {
   for (int i = 0; i < 8; ++i) z[i] += f[i];
 }
 
-// EXTRA: with a delta or a residual.
-template <bool BF16, bool GATED, bool EXTRA>
+// EXTRA: with a delta (1), a residual (2).
+template <bool BF16, bool GATED, int EXTRA>
 __device__ __forceinline__ uint4 linear_finish(const LinearArgs& a, const LinearBias& b, const LinearTail& t, float* z, float* up) {
   if (a.bias) add8<BF16>(z, b.half[0]);
-  if (EXTRA && a.delta) add8<BF16>(z, t.delta[0]);
+  if ((EXTRA & 1) && a.delta) add8<BF16>(z, t.delta[0]);
   activate8(z, a.act);
   if (GATED) {
     if (a.bias) add8<BF16>(up, b.half[1]);
-    if (EXTRA && a.delta) add8<BF16>(up, t.delta[1]);
+    if ((EXTRA & 1) && a.delta) add8<BF16>(up, t.delta[1]);
 #pragma unroll
     for (int i = 0; i < 8; ++i) z[i] *= up[i];
   }
-  if (EXTRA && a.residual) add8<BF16>(z, t.residual);
+  if ((EXTRA & 2) && a.residual) add8<BF16>(z, t.residual);
   return pack8<BF16>(z);
 }
 
@@ -144,12 +144,12 @@ __device__ __forceinline__ uint4 linear_finish(const LinearArgs& a, const Linear
 // tile's K out, so that few tiles still read W at the card's full rate; their
 // parts are added in the order of K through distributed shared memory, each CTA
 // finishing its share of the tile.  Grid: (feature tile, part of K), group, and
-// row tiles in turn.  Two CTAs fit an SM (one where NT is 256).
+// row tiles in turn.  Two CTAs fit an SM.
 template <int NT_>
 struct Few {
   static constexpr int NT = NT_;
   static constexpr int W = 128 * 128, X = NT * 128, STAGE = W + X;
-  static constexpr int STAGES = (NT == 256 ? 208 : 106) * 1024 / STAGE;
+  static constexpr int STAGES = 106 * 1024 / STAGE;
   static constexpr int PAD = 132;  // floats between rows of a part
   static constexpr int THREADS = 256;  // load, MMA, 4 warps that read the sums; all finish
   static constexpr uint32_t COLS = NT < 32 ? 32 : NT;  // of tensor memory
@@ -200,14 +200,14 @@ __device__ __forceinline__ void linear_few_finish(const LinearArgs& a, const flo
           }
         }
     }
-    const uint4 y = linear_finish<BF16, GATED, true>(a, bias, t, z, z + 8);
+    const uint4 y = linear_finish<BF16, GATED, 3>(a, bias, t, z, z + 8);
     if (col < a.n_out) store8(a.out, a.ld_out, r0 + r, col, y);
     if (i + split * C::THREADS < rows * width) fetch(i + split * C::THREADS);
   }
 }
 
 template <bool BF16, class C>
-__global__ void __launch_bounds__(C::THREADS, C::NT == 256 ? 1 : 2) linear_few_kernel(const LinearArgs a, const __grid_constant__ CUtensorMap map_w,
+__global__ void __launch_bounds__(C::THREADS, 2) linear_few_kernel(const LinearArgs a, const __grid_constant__ CUtensorMap map_w,
                                                                const __grid_constant__ RowMaps maps_x, int split) {
   extern __shared__ uint8_t few_smem_raw[];
   __shared__ uint64_t full[C::STAGES], empty[C::STAGES], done;
@@ -258,7 +258,7 @@ __global__ void __launch_bounds__(C::THREADS, C::NT == 256 ? 1 : 2) linear_few_k
               ok = false;
               break;
             }
-            mbar_arrive_expect_tx(&full[s], C::W + (2048 << box) + (rows > 128 ? 16384 : 0));
+            mbar_arrive_expect_tx(&full[s], C::W + (2048 << box));
             uint8_t* st = smem + s * C::STAGE;
             if (a.gated) {
               tma_load_3d(st, &map_w, (kb0 + i) * 64, ft * 64, g, &full[s]);
@@ -267,7 +267,6 @@ __global__ void __launch_bounds__(C::THREADS, C::NT == 256 ? 1 : 2) linear_few_k
               tma_load_3d(st, &map_w, (kb0 + i) * 64, ft * 128, g, &full[s]);
             }
             tma_load_2d(st + C::W, &maps_x.box[box], (kb0 + i) * 64, r0, &full[s]);
-            if (rows > 128) tma_load_2d(st + C::W + 128 * 128, &maps_x.box[3], (kb0 + i) * 64, r0 + 128, &full[s]);
           }
         }
       } else if (warp == 1) {
@@ -350,8 +349,9 @@ struct Pair {
 constexpr size_t kLinearCounterBytes = (size_t)Pair::MAX * 8 * 4;
 constexpr size_t kLinearPartFloats = (size_t)Pair::MAX * 2 * 2 * Pair::PART;
 
-// What a step of 64 of K costs by a tile's units of rows: copies and products.
-__device__ __forceinline__ int unit_cost(int units) { return units == 4 ? 16 : 7 + 2 * units; }
+// What a step of 64 of K costs by a tile's units of rows (measured: 0.22, 0.23, 0.26,
+// 0.31 us).
+__device__ __forceinline__ int unit_cost(int units) { return units == 4 ? 16 : 10 + units; }
 
 // A pair's work: steps [kb0, kb1) of a tile's K.  A tile that several pairs share
 // is finished by the last of them, which adds the others' parts in the order of K.
@@ -373,13 +373,16 @@ struct PairWalk {
   const int2* pre;  // of the groups: tiles and cost (a step of K) so far
   int features, blocks, pairs, me;
   int round, t_end;                          // of the tiles in turn
+  bool moved;
   int g, units, rts, band, width, ft, rt;    // the tile of the shares; row tiles of its band
   int2 seg;
-  int64_t at, base, total;                   // its position; of the shares: first position, cost (a step of K)
-  int sharers;
+  int at, base, total;                       // its position; of the shares: first position, cost (a step of K)
+  int sharers, rest;                         // pairs that share, and what is left over of equal shares
+  int64_t share;                             // a pair's cost
 
   __device__ __forceinline__ PairWalk(const LinearArgs& a, const int2* pre, int features, int pairs, int me)
-      : a(a), pre(pre), features(features), blocks((a.K + 63) / 64), pairs(pairs), me(me) {
+      : a(a), pre(pre), features(features), blocks((a.K + 63) / 64), pairs(pairs), me(me) {}
+  __device__ __forceinline__ void start() {
     const int tiles = pre[a.groups].x;
     round = 0;
     int turns = tiles / pairs;
@@ -390,22 +393,32 @@ struct PairWalk {
       locate_tile(t_end);
       base = at;
       total = pre[a.groups].y - base;
-      const int64_t whole = (int64_t)((tiles - t_end + pairs - 1) / pairs) * 16 * blocks;  // a pair's cost without
-      if (total * blocks + (int64_t)Pair::SHARE * pairs >= whole * pairs) {
+      const int64_t whole = (int64_t)((unsigned)(tiles - t_end + pairs - 1) / (unsigned)pairs) * 16 * blocks;  // a pair's cost without
+      // Shared, row tiles that use the same weights are no longer at the same place in
+      // K, and weights that L2 does not hold meanwhile are read again (600 rows of 13824
+      // by 5120: 71 us whole, 97 shared; 1023 rows, just above one tile a pair, 135 and 98).
+      const int left = tiles - t_end;
+      const bool again = a.groups == 1 && width > 1 && (int64_t)(left / width) * (256 * 2) * a.K > (64 << 20) &&
+                         (left < pairs || left * 8 > pairs * 9);
+      if (again || (int64_t)total * blocks + (int64_t)Pair::SHARE * pairs >= whole * pairs) {
         t_end = tiles;
         total = 0;
       }
     }
     // a share is at least 8 steps of a full tile
-    const int64_t most = total * blocks / 128;
+    const int64_t all = (int64_t)total * blocks, most = all >> 7;
     sharers = (int)(most < 1 ? 1 : (most < pairs ? most : pairs));
-    if (turn() >= t_end) begin();
+    share = all / sharers;
+    rest = (int)(all - share * sharers);
+    moved = true;  // (`next` begins the shares)
   }
-  __device__ __forceinline__ int turn() const { return round * pairs + (int)((me + 13ll * round) % pairs); }
+  __device__ __forceinline__ int turn() const { return round * pairs + (int)((unsigned)(me + 13 * round) % (unsigned)pairs); }
   __device__ __forceinline__ void begin() {
-    if (me < sharers && total > 0) locate(edge(me) / blocks);
+    if (me < sharers && total > 0) locate((int)(edge(me) / blocks));
   }
-  __device__ __forceinline__ int64_t edge(int i) const { return base * blocks + total * blocks * i / sharers; }
+  __device__ __forceinline__ int64_t edge(int i) const {
+    return (int64_t)base * blocks + share * i + (unsigned)(rest * i) / (unsigned)sharers;
+  }
   __device__ __forceinline__ int cost_of(int row_tile) const {
     return row_tile + 1 < rts ? 16 : unit_cost(units - row_tile * Pair::UNITS);
   }
@@ -432,31 +445,34 @@ struct PairWalk {
   }
   __device__ __forceinline__ void locate_tile(int tile) {
     enter(group_of([&](int2 v) { return v.x <= tile; }));
-    int in = tile - pre[g].x;
-    enter_band(in / (features * Pair::BAND));
+    unsigned in = (unsigned)(tile - pre[g].x);
+    enter_band((int)(in / (unsigned)(features * Pair::BAND)));
     in -= band * features * Pair::BAND;
-    ft = in / width;
-    rt = band * Pair::BAND + in - ft * width;
-    at = pre[g].y + (int64_t)band * features * Pair::BAND_COST + (int64_t)ft * band_cost() + (rt - band * Pair::BAND) * 16;
+    ft = (int)(in / (unsigned)width);
+    rt = band * Pair::BAND + (int)in - ft * width;
+    place();
   }
-  __device__ __forceinline__ void locate(int64_t x) {  // the tile at a position
+  __device__ __forceinline__ void place() {
+    at = pre[g].y + band * features * Pair::BAND_COST + ft * band_cost() + (rt - band * Pair::BAND) * 16;
+  }
+  __device__ __forceinline__ void locate(int x) {  // the tile at a position
     enter(group_of([&](int2 v) { return v.y <= x; }));
-    int64_t in = x - pre[g].y;
-    const int64_t whole = (int64_t)features * Pair::BAND_COST;
-    const int bands = (rts + Pair::BAND - 1) / Pair::BAND;
-    enter_band((int)(in / whole < bands - 1 ? in / whole : bands - 1));
+    unsigned in = (unsigned)(x - pre[g].y);
+    const unsigned whole = (unsigned)(features * Pair::BAND_COST);
+    enter_band(min((int)(in / whole), (rts + Pair::BAND - 1) / Pair::BAND - 1));
     in -= band * whole;
-    ft = (int)(in / band_cost());
-    in -= (int64_t)ft * band_cost();
+    const unsigned row = (unsigned)band_cost();
+    ft = (int)(in / row);
+    in -= ft * row;
     rt = band * Pair::BAND + min((int)in / 16, width - 1);
-    at = pre[g].y + band * whole + (int64_t)ft * band_cost() + (rt - band * Pair::BAND) * 16;
+    place();
   }
   // Where share i begins in the tile at `at`; near an end, there.
   __device__ __forceinline__ int bound(int i, int per_step) const {
-    const int64_t d = edge(i) - at * blocks;
+    const int64_t d = edge(i) - (int64_t)at * blocks;
     if (d <= 0) return 0;
     if (d >= (int64_t)per_step * blocks) return blocks;
-    const int kb = (int)(d / per_step);
+    const int kb = (int)((unsigned)d / (unsigned)per_step);
     return kb < 4 ? 0 : (blocks - kb < 4 ? blocks : kb);
   }
   __device__ __forceinline__ void fill(PairItem& p) const {
@@ -467,19 +483,21 @@ struct PairWalk {
     p.kb0 = 0;
     p.kb1 = blocks;
     p.parts = 1;
-    p.head = p.part = 0;
+    p.head = p.part = p.last = 0;
   }
   __device__ __forceinline__ bool next(PairItem& p) {
     if (turn() < t_end) {
       locate_tile(turn());
       fill(p);
       ++round;
-      if (turn() >= t_end) begin();
+      moved = true;
       return true;
     }
+    if (moved) begin();
+    moved = false;
     if (me >= sharers || total <= 0) return false;
     const int64_t end = edge(me + 1);
-    while (g < a.groups && at * blocks < end) {
+    while (g < a.groups && (int64_t)at * blocks < end) {
       const int per_step = cost_of(rt), lo = bound(me, per_step), hi = bound(me + 1, per_step);
       if (lo < hi) {
         fill(p);
@@ -491,6 +509,7 @@ struct PairWalk {
         p.head = first;
         p.parts = last - first + 1;
         p.part = me - first;
+        p.last = hi < blocks || (int64_t)(at + per_step) * blocks >= end;
       }
       at += per_step;
       if (++rt == band * Pair::BAND + width) {
@@ -563,7 +582,7 @@ __device__ __forceinline__ float* part_of(const LinearArgs& a, const PairItem& p
   return a.parts + ((int64_t)((p.head + x) * 2 + (x == 0)) * 2 + rank) * Pair::PART + warp * 128 * 32;
 }
 
-template <bool BF16, bool GATED, bool EXTRA>
+template <bool BF16, bool GATED, int EXTRA>
 __global__ void __launch_bounds__(Pair::THREADS, 1) linear_pair_kernel(const LinearArgs a, const __grid_constant__ CUtensorMap map_w,
                                                                        const __grid_constant__ RowMaps maps_x) {
   using C = Pair;
@@ -571,7 +590,7 @@ __global__ void __launch_bounds__(Pair::THREADS, 1) linear_pair_kernel(const Lin
   __shared__ uint64_t full[C::STAGES], empty[C::STAGES], acc_full[2], acc_empty[2], item_full[C::ITEMS], item_empty[C::ITEMS], drain;
   __shared__ uint64_t part_full[C::EPI];
   __shared__ PairItem items[C::ITEMS];
-  __shared__ uint32_t taddr_s, issued_s, tx_s[C::STAGES];  // (steps copied by this CTA, their bytes)
+  __shared__ uint32_t taddr_s, failed_s, issued_s, tx_s[C::STAGES];  // (steps copied by this CTA, their bytes)
   __shared__ int2 scan_s[C::THREADS / 32];
   const int tid = threadIdx.x, lane = tid & 31;
   const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
@@ -594,11 +613,14 @@ __global__ void __launch_bounds__(Pair::THREADS, 1) linear_pair_kernel(const Lin
     }
     for (int i = 0; i < C::EPI; ++i) mbar_init(&part_full[i], 1);
     mbar_init(&drain, 1);
+    failed_s = 0;
     fence_barrier_init();
   }
+  __syncwarp();
+  cluster_arrive();  // (the barriers of both are ready at the wait)
   cudaTriggerProgrammaticLaunchCompletion();
-  cudaGridDependencySynchronize();
-  if (warp == 2) tc::tmem_alloc_pair(&taddr_s, 512);
+  // (a product of one group lays out its work ahead of the wait for the call before)
+  if (a.seg_start) cudaGridDependencySynchronize();
   constexpr int per_pair = GATED ? 128 : 256;
   const int features = (a.n_out + per_pair - 1) / per_pair;
   {
@@ -642,16 +664,24 @@ __global__ void __launch_bounds__(Pair::THREADS, 1) linear_pair_kernel(const Lin
     }
     if (tid == C::THREADS - 1) pre[a.groups] = run;
   }
+  __syncthreads();
+  PairWalk walk(a, pre, features, gridDim.x / 2, blockIdx.x / 2);
+  PairItem p;
+  if (warp == 3 && lane == 0) {
+    walk.start();
+    if (!walk.next(p)) p.parts = 0;
+  }
+  __syncwarp();
+  if (!a.seg_start) cudaGridDependencySynchronize();
+  if (warp == 2) tc::tmem_alloc_pair(&taddr_s, 512);
   tc::fence_before_sync();
   __syncthreads();
-  cluster_arrive();  // (the barriers of both are ready)
   cluster_wait();
   tc::fence_after_sync();
   const uint32_t tmem = taddr_s;
   // An item from the warp that lays them out (false: there are no more) and, once
   // it is no longer needed, back.  After a wait that gave up a role passes on
   // without work; these waits end since every role's do.
-  PairItem p;
   uint32_t n = 0;  // items so far
   auto take = [&]() -> bool {
     if (!mbar_wait_soon(&item_full[n % C::ITEMS], (n / C::ITEMS) & 1, 4 * kWaitLimitNs)) return false;
@@ -733,14 +763,9 @@ __global__ void __launch_bounds__(Pair::THREADS, 1) linear_pair_kernel(const Lin
   } else if (warp == 3) {
     // ----------------------------------------------------------------- items
     if (lane == 0) {
-      PairWalk walk(a, pre, features, gridDim.x / 2, blockIdx.x / 2);
-      PairItem ahead;
-      bool more = walk.next(ahead);
-      for (p.parts = 1; p.parts; ++n) {
-        p = ahead;
-        if (!more) p.parts = 0;
-        if (more) more = walk.next(ahead);
-        p.last = !more;
+      for (bool more = true; more; ++n) {  // (the first is laid out already)
+        if (n > 0 && !walk.next(p)) p.parts = 0;
+        more = p.parts > 0;
         if (n >= C::ITEMS && !mbar_wait_bounded(&item_empty[n % C::ITEMS], (n / C::ITEMS - 1) & 1, 4 * kWaitLimitNs)) {
           ok = false;
           break;
@@ -854,34 +879,48 @@ __global__ void __launch_bounds__(Pair::THREADS, 1) linear_pair_kernel(const Lin
       if (finish) {
         const LinearBias bias = linear_bias<GATED>(a, p.g, col);
         LinearTail tail[MINE];
+        // (columns and rows past the tile's are read as the last, and not written)
+        const int from_col = min(col, a.n_out - 8);
         auto fetch = [&](int c, int i) {
-          const int r = c + my_row + 8 * i;
-          if (EXTRA) tail[i] = linear_tail<GATED>(a, p.row0 + r, col, r < c1 && col < a.n_out);
+          const int64_t row = p.row0 + min(c + my_row + 8 * i, c1 - 1);
+          if (EXTRA & 1) {
+            tail[i].delta[0] = load8(a.delta, a.ld_delta, row, from_col);
+            if (GATED) tail[i].delta[1] = load8(a.delta, a.ld_delta, row, a.n_out + from_col);
+          }
+          if (EXTRA & 2) tail[i].residual = load8(a.residual, a.ld_residual, row, from_col);
         };
-#pragma unroll
-        for (int i = 0; i < MINE; ++i) fetch(c0, i);
+        // the next columns come from tensor memory ahead, where registers suffice
+        constexpr bool AHEAD = EXTRA != 3;
         uint32_t sums[32];
-        if (c0 < c1) tc::tmem_ld32_start(acc + c0, sums);
+        if (c0 < c1) {
+          if (AHEAD) tc::tmem_ld32_start(acc + c0, sums);
+#pragma unroll
+          for (int i = 0; i < MINE; ++i) fetch(c0, i);
+        }
         for (int c = c0; c < c1; c += 32) {
+          if (!AHEAD) tc::tmem_ld32_start(acc + c, sums);
           tc::tmem_ld32_wait(sums);
 #pragma unroll
           for (int i = 0; i < 32; ++i) buf[i * C::PAD + lane] = __uint_as_float(sums[i]);
           if (GATED) barrier_sync(bar, 64); else __syncwarp();
-          if (c + 32 < c1) tc::tmem_ld32_start(acc + c + 32, sums);  // (ahead, as each row's delta and residual)
+          float z[MINE][GATED ? 16 : 8];
 #pragma unroll
-          for (int i = 0; i < MINE; ++i) {
-            const int r = my_row + 8 * i, at = r * C::PAD + block * 8;
-            float z[16];
+          for (int i = 0; i < MINE; ++i)
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-              *reinterpret_cast<float4*>(z + 4 * j) = *reinterpret_cast<const float4*>(first_half + at + 4 * j);
-              if (GATED) *reinterpret_cast<float4*>(z + 8 + 4 * j) = *reinterpret_cast<const float4*>(second_half + at + 4 * j);
+              const int at = (my_row + 8 * i) * C::PAD + block * 8 + 4 * j;
+              *reinterpret_cast<float4*>(z[i] + 4 * j) = *reinterpret_cast<const float4*>(first_half + at);
+              if (GATED) *reinterpret_cast<float4*>(z[i] + 8 + 4 * j) = *reinterpret_cast<const float4*>(second_half + at);
             }
-            const uint4 y = linear_finish<BF16, GATED, EXTRA>(a, bias, tail[i], z, z + 8);
-            fetch(c + 32, i);
-            if (c + r < c1 && col < a.n_out) store8(a.out, a.ld_out, p.row0 + c + r, col, y);
-          }
           if (GATED) barrier_sync(bar, 64); else __syncwarp();
+          if (AHEAD && c + 32 < c1) tc::tmem_ld32_start(acc + c + 32, sums);
+#pragma unroll
+          for (int i = 0; i < MINE; ++i) {
+            const uint4 y = linear_finish<BF16, GATED, EXTRA>(a, bias, tail[i], z[i], z[i] + 8);
+            if (EXTRA && c + 32 < c1) fetch(c + 32, i);  // (ahead)
+            const int r = c + my_row + 8 * i;
+            if (r < c1 && col < a.n_out) store8(a.out, a.ld_out, p.row0 + r, col, y);
+          }
         }
       }
       tc::fence_before_sync();
@@ -889,25 +928,30 @@ __global__ void __launch_bounds__(Pair::THREADS, 1) linear_pair_kernel(const Lin
       if (lane == 0) mbar_arrive_cluster(leader_empty + (n & 1) * 8);
     }
   }
-  if (!ok) set_error(a.err, LORA_DEV_ERR_TIMEOUT);
+  if (!ok) {
+    set_error(a.err, LORA_DEV_ERR_TIMEOUT);
+    for (int r = 0; r < 2; ++r) dsmem_st_f32(dsmem_map(smem_addr(&failed_s), r), 1.0f);
+  }
   __syncwarp();
   tc::fence_before_sync();
   __syncthreads();
   cluster_arrive();  // (neither CTA leaves while the other's products or copies use its memory)
   cluster_wait();
-  if (tid == 0 && rank == 0) {
-    // Copies still in flight, after a wait gave up: both CTAs' complete the even
-    // one's barriers, which here come to expect what each has copied.
-    const uint32_t mine = issued_s, other = dsmem_ld_u32(dsmem_map(smem_addr(&issued_s), 1)), most = max(mine, other);
-    for (uint32_t j = mine; j < other; ++j)
-      mbar_arrive_expect_tx(&full[j % C::STAGES], dsmem_ld_u32(dsmem_map(smem_addr(&tx_s[j % C::STAGES]), 1)));
-    for (uint32_t j = other; j < mine; ++j) mbar_complete_tx(&full[j % C::STAGES], tx_s[j % C::STAGES]);
-    for (uint32_t j = most > C::STAGES ? most - C::STAGES : 0; j < most; ++j)
-      if (!mbar_wait_bounded(&full[j % C::STAGES], (j / C::STAGES) & 1, kWaitLimitNs)) set_error(a.err, LORA_DEV_ERR_INTERNAL);
+  if (*reinterpret_cast<volatile uint32_t*>(&failed_s)) {
+    // After a wait that gave up, copies are still in flight: both CTAs' complete the
+    // even one's barriers, which here come to expect what each has copied.
+    if (tid == 0 && rank == 0) {
+      const uint32_t mine = issued_s, other = dsmem_ld_u32(dsmem_map(smem_addr(&issued_s), 1)), most = max(mine, other);
+      for (uint32_t j = mine; j < other; ++j)
+        mbar_arrive_expect_tx(&full[j % C::STAGES], dsmem_ld_u32(dsmem_map(smem_addr(&tx_s[j % C::STAGES]), 1)));
+      for (uint32_t j = other; j < mine; ++j) mbar_complete_tx(&full[j % C::STAGES], tx_s[j % C::STAGES]);
+      for (uint32_t j = most > C::STAGES ? most - C::STAGES : 0; j < most; ++j)
+        if (!mbar_wait_bounded(&full[j % C::STAGES], (j / C::STAGES) & 1, kWaitLimitNs)) set_error(a.err, LORA_DEV_ERR_INTERNAL);
+    }
+    __syncthreads();
+    cluster_arrive();
+    cluster_wait();
   }
-  __syncthreads();
-  cluster_arrive();
-  cluster_wait();
   if (warp == 2) tc::tmem_dealloc_pair(tmem, 512);
   cluster_arrive();
   cluster_wait();

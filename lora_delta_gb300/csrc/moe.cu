@@ -123,7 +123,7 @@ int launch_few(const LinearArgs& a, cudaStream_t stream) {
                 C::smem(), stream, (int)split, a, map_w, maps_x, (int)split);
 }
 
-template <bool BF16, bool GATED, bool EXTRA>
+template <bool BF16, bool GATED, int EXTRA>
 int launch_pair(const LinearArgs& a, cudaStream_t stream) {
   CUtensorMap map_w;
   RowMaps maps_x = {};
@@ -136,27 +136,31 @@ int launch_pair(const LinearArgs& a, cudaStream_t stream) {
   return launch(kernel, dim3(2u * (unsigned)pairs), Pair::THREADS, smem, stream, 2, a, map_w, maps_x);
 }
 
-// Rows of a group on average, and up to how many the kernel for few rows takes.
-int64_t mean_rows(int n, int groups) { return ((int64_t)n + groups - 1) / groups; }
-int few_rows() {
-  static const int few = env_int("LORA_LINEAR_FEW", 64);
-  return few;
+template <bool BF16, bool GATED>
+int launch_pair_form(const LinearArgs& a, cudaStream_t stream) {
+  if (a.delta && a.residual) return launch_pair<BF16, GATED, 3>(a, stream);
+  if (a.residual) return launch_pair<BF16, GATED, 2>(a, stream);
+  return a.delta ? launch_pair<BF16, GATED, 1>(a, stream) : launch_pair<BF16, GATED, 0>(a, stream);
 }
+
+// Up to how many rows of a group, on average, the kernel for few rows takes.  Few rows,
+// many rows: 128 by 4096 x 28672 47 us, 59; 128 by 4096 x 6144 21, 28; experts of 64
+// rows (2048 x 1536 gated) 80, 83; of 80 rows 109, 84.
+constexpr int kFewRows = 64, kFewRowsAlone = 128;
+int64_t mean_rows(int n, int groups) { return ((int64_t)n + groups - 1) / groups; }
 
 template <bool BF16>
 int linear_launch(const LinearArgs& a, cudaStream_t stream) {
   const int64_t rows = mean_rows(a.n, a.groups);
-  if (rows > few_rows()) {
-    const bool extra = a.delta || a.residual;
-    if (a.gated) return extra ? launch_pair<BF16, true, true>(a, stream) : launch_pair<BF16, true, false>(a, stream);
-    return extra ? launch_pair<BF16, false, true>(a, stream) : launch_pair<BF16, false, false>(a, stream);
+  const bool few = rows <= (a.groups > 1 ? kFewRows : kFewRowsAlone);
+  if (!few) {
+    return a.gated ? launch_pair_form<BF16, true>(a, stream) : launch_pair_form<BF16, false>(a, stream);
   }
-  const int64_t want = a.seg_start && a.groups > 1 ? 2 * rows : rows;
+  const int64_t want = a.groups > 1 ? 2 * rows : rows;
   if (want <= 16) return launch_few<BF16, 16>(a, stream);
   if (want <= 32) return launch_few<BF16, 32>(a, stream);
   if (want <= 64) return launch_few<BF16, 64>(a, stream);
-  if (want <= 128) return launch_few<BF16, 128>(a, stream);
-  return launch_few<BF16, 256>(a, stream);
+  return launch_few<BF16, 128>(a, stream);
 }
 
 int linear_call(LinearArgs& a, int dtype, void* workspace, size_t ws_bytes, cudaStream_t stream) {
@@ -306,7 +310,8 @@ int lora_moe_combine_grad(void* grad_rows, int64_t ld_grad_rows, float* grad_wei
 }
 
 size_t lora_linear_workspace_size(int n, int groups) {
-  return groups < 1 || mean_rows(n, groups) <= few_rows() ? 0 : kLinearCounterBytes + kLinearPartFloats * 4;
+  const bool few = groups < 1 || mean_rows(n, groups) <= (groups > 1 ? kFewRows : kFewRowsAlone);
+  return few ? 0 : kLinearCounterBytes + kLinearPartFloats * 4;
 }
 size_t lora_linear_zeroed_bytes(void) { return kLinearCounterBytes; }
 
