@@ -226,11 +226,6 @@ int lora_moe_dispatch(void* rows, int64_t ld_rows, int32_t* seg_start, int32_t* 
   if (T > 0 && share(Mat{rows, ld_rows, P, H}, Mat{x, ld_x, T, H})) return LORA_ERR_ARG;
   const MoePlanArgs p = {{topk_ids, expert_map, n_global_experts, E}, lora_ids, P, top_k, seg_start, row_pair, pair_row,
                          row_expert, row_lora, err_word};
-  const int smem = (int)moe_sort_smem(E);
-  if (prepare_kernel(moe_sort_kernel, smem, true) != cudaSuccess) return LORA_ERR_CUDA;
-  const int want = P / 2048 + 1, ctas = want < kMoeSortCluster ? want : kMoeSortCluster;
-  if ((rc = launch(moe_sort_kernel, dim3((unsigned)ctas), kRouteThreads, (size_t)smem, (cudaStream_t)stream, ctas, p))) return rc;
-  if (T == 0) return LORA_OK;
   MoveArgs a = {};
   a.out = rows;
   a.ld_out = ld_rows;
@@ -241,6 +236,16 @@ int lora_moe_dispatch(void* rows, int64_t ld_rows, int32_t* seg_start, int32_t* 
   a.top_k = top_k;
   a.H = H;
   a.P = P;
+  static const int few = env_int("LORA_MOE_FEW", kMoeFewPairs);
+  if (T > 0 && P <= few && P <= kMoeFewPairs) {
+    const size_t smem = (size_t)(E + 1) * 4 + (size_t)P * 2;
+    return launch(moe_dispatch_few_kernel, dim3((unsigned)T), kMoeThreads, smem, (cudaStream_t)stream, 1, p, a);
+  }
+  const int smem = (int)moe_sort_smem(E);
+  if (prepare_kernel(moe_sort_kernel, smem, true) != cudaSuccess) return LORA_ERR_CUDA;
+  const int want = P / 2048 + 1, ctas = want < kMoeSortCluster ? want : kMoeSortCluster;
+  if ((rc = launch(moe_sort_kernel, dim3((unsigned)ctas), kRouteThreads, (size_t)smem, (cudaStream_t)stream, ctas, p))) return rc;
+  if (T == 0) return LORA_OK;
   return launch(moe_scatter_kernel, dim3((unsigned)T), kMoeThreads, 0, (cudaStream_t)stream, 1, a);
 }
 

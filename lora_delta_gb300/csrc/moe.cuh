@@ -49,6 +49,15 @@ struct MoePlanArgs {
   uint32_t* err;
 };
 
+// Pair p of an expert (E: none) at row `at`.
+__device__ __forceinline__ void place_pair(const MoePlanArgs& a, int p, int key, int lora, int at) {
+  const bool there = key < a.key.E;
+  a.pair_row[p] = there ? at : -1;
+  a.row_pair[at] = there ? p : -1;
+  a.row_expert[at] = there ? key : -1;
+  a.row_lora[at] = there ? lora : -1;
+}
+
 inline size_t moe_sort_smem(int E) { return sizeof(uint32_t) * ((size_t)kRouteWarps + 3) * (size_t)(E + 1); }
 
 // One cluster; a contiguous block of pairs a CTA and within it a warp, counted
@@ -104,22 +113,25 @@ __global__ void __launch_bounds__(kRouteThreads) moe_sort_kernel(const MoePlanAr
     run += total[k];
   }
   __syncthreads();
-  for (int base = b0; base < b1; base += 32) {
-    const int p = base + lane;
-    uint32_t dummy = 0;
-    const int key = p < b1 ? a.key(p, dummy) : -1;
-    const unsigned peers = __match_any_sync(0xffffffffu, key);
-    if (key >= 0) {
-      const uint32_t at = my[key] + __popc(peers & ((1u << lane) - 1u));
-      const bool there = key < E;
-      a.pair_row[p] = there ? (int32_t)at : -1;
-      a.row_pair[at] = there ? p : -1;
-      a.row_expert[at] = there ? key : -1;
-      a.row_lora[at] = there && a.lora_ids ? a.lora_ids[p / a.top_k] : -1;
+  // (8 pairs' keys and adapters a lane at a time, so that their loads overlap)
+  for (int base = b0; base < b1; base += 256) {
+    int key[8], lora[8];
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      const int p = base + u * 32 + lane;
+      uint32_t dummy = 0;
+      key[u] = p < b1 ? a.key(p, dummy) : -1;
+      lora[u] = p < b1 && a.lora_ids ? a.lora_ids[p / a.top_k] : -1;
     }
-    __syncwarp();
-    if (key >= 0 && lane == __ffs(peers) - 1) my[key] += __popc(peers);
-    __syncwarp();
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      if (base + u * 32 >= b1) break;
+      const unsigned peers = __match_any_sync(0xffffffffu, key[u]);
+      if (key[u] >= 0) place_pair(a, base + u * 32 + lane, key[u], lora[u], (int)my[key[u]] + __popc(peers & ((1u << lane) - 1u)));
+      __syncwarp();
+      if (key[u] >= 0 && lane == __ffs(peers) - 1) my[key[u]] += __popc(peers);
+      __syncwarp();
+    }
   }
   cluster_wait();  // the peers have read this CTA's totals
 }
@@ -181,41 +193,126 @@ __device__ __forceinline__ void store8(void* base, int64_t ld, int64_t row, int 
   *reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(base) + row * ld + col) = v;
 }
 
-// rows[pair_row[t, j]] = x[t]
+// A token's row into its pairs' rows.
+__device__ __forceinline__ void scatter_row(const MoveArgs& a, int t, const int* row) {
+  for (int c = threadIdx.x * 8; c < a.H; c += kMoeThreads * 8) {
+    const uint4 v = load8(a.x, a.ld_x, t, c);
+#pragma unroll 4
+    for (int j = 0; j < a.top_k; ++j)
+      if (row[j] >= 0) store8(a.out, a.ld_out, row[j], c, v);
+  }
+}
+
+// rows[pair_row[t, j]] = x[t].  A CTA a token: x is read once, each row written once.
+// Bound: the rows' bytes (65536 rows of 4096: 98 us, 6.2 TB/s).
 __global__ void __launch_bounds__(kMoeThreads) moe_scatter_kernel(const MoveArgs a) {
+  __shared__ int row[LORA_MOE_MAX_TOP_K];
   cudaTriggerProgrammaticLaunchCompletion();
   cudaGridDependencySynchronize();
   const int t = blockIdx.x;
-  for (int c = threadIdx.x * 8; c < a.H; c += kMoeThreads * 8) {
-    const uint4 v = load8(a.x, a.ld_x, t, c);
-    for (int j = 0; j < a.top_k; ++j) {
-      const int r = row_of(a, (int64_t)t * a.top_k + j);
-      if (r >= 0) store8(a.out, a.ld_out, r, c, v);
+  if ((int)threadIdx.x < a.top_k) row[threadIdx.x] = row_of(a, (int64_t)t * a.top_k + threadIdx.x);
+  __syncthreads();
+  scatter_row(a, t, row);
+}
+
+// Sort and scatter of few pairs in one launch: every token's CTA counts, among all
+// pairs' keys, those that come before each of its own.  (64 tokens of 8 experts, rows
+// of 2048: see the launch.)
+constexpr int kMoeFewPairs = 4096;
+__global__ void __launch_bounds__(kMoeThreads) moe_dispatch_few_kernel(const MoePlanArgs a, const MoveArgs m) {
+  extern __shared__ uint32_t few_s[];  // hist[E + 1] (of CTA 0), then the pairs' keys
+  __shared__ int row[LORA_MOE_MAX_TOP_K];
+  __shared__ uint32_t warp_sums[kMoeThreads / 32];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, t = blockIdx.x;
+  const int E = a.key.E, nkb = E + 1;
+  uint32_t* hist = few_s;
+  uint16_t* key = reinterpret_cast<uint16_t*>(few_s + nkb);
+  cudaTriggerProgrammaticLaunchCompletion();
+  cudaGridDependencySynchronize();
+  uint32_t bad = 0;
+  if (t == 0)
+    for (int k = tid; k < nkb; k += kMoeThreads) hist[k] = 0;
+#pragma unroll 4
+  for (int p = tid; p < a.P; p += kMoeThreads) key[p] = (uint16_t)a.key(p, bad);
+  if (bad && t == 0) set_error(a.err, bad);
+  __syncthreads();
+  for (int j = warp; j < a.top_k; j += kMoeThreads / 32) {
+    const int p = t * a.top_k + j, e = key[p];
+    int before = 0;
+    for (int q = lane; q < a.P; q += 32) {
+      const int k = key[q];
+      before += k < e || (k == e && q < p);
+    }
+    before = __reduce_add_sync(0xffffffffu, before);
+    if (lane == 0) {
+      place_pair(a, p, e, a.lora_ids ? a.lora_ids[t] : -1, before);
+      row[j] = e < E ? before : -1;
+    }
+  }
+  __syncthreads();
+  scatter_row(m, t, row);
+  if (t == 0) {  // the experts' first rows
+    for (int p = tid; p < a.P; p += kMoeThreads) atomicAdd(&hist[key[p]], 1u);
+    __syncthreads();
+    uint32_t carry = 0;
+    for (int k0 = 0; k0 < nkb; k0 += kMoeThreads) {
+      const uint32_t v = k0 + tid < nkb ? hist[k0 + tid] : 0u;
+      uint32_t inc = v;
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const uint32_t u = __shfl_up_sync(0xffffffffu, inc, d);
+        if (lane >= d) inc += u;
+      }
+      if (lane == 31) warp_sums[warp] = inc;
+      __syncthreads();
+      uint32_t base = carry;
+      for (int w = 0; w < kMoeThreads / 32; ++w) {
+        base += w < warp ? warp_sums[w] : 0u;
+        carry += warp_sums[w];
+      }
+      if (k0 + tid < nkb) a.seg_start[k0 + tid] = (int32_t)(base + inc - v);
+      __syncthreads();
     }
   }
 }
 
-// out[t] = residual[t] + sum_j w[t, j] rows[pair_row[t, j]], in the order of j
+// out[t] = residual[t] + sum_j w[t, j] rows[pair_row[t, j]], in the order of j, 8 rows
+// on their way at once.  A CTA a token.  Bound: the rows' bytes (65536 rows of 4096
+// into 8192: 97 us, 6.2 TB/s).
 template <bool BF16>
 __global__ void __launch_bounds__(kMoeThreads) moe_combine_kernel(const MoveArgs a) {
+  __shared__ int row[LORA_MOE_MAX_TOP_K];
+  __shared__ float weight[LORA_MOE_MAX_TOP_K];
   cudaTriggerProgrammaticLaunchCompletion();
   cudaGridDependencySynchronize();
   const int t = blockIdx.x;
+  if ((int)threadIdx.x < a.top_k) {
+    const int64_t p = (int64_t)t * a.top_k + threadIdx.x;
+    row[threadIdx.x] = row_of(a, p);
+    weight[threadIdx.x] = a.weights ? a.weights[p] : 1.0f;
+  }
+  __syncthreads();
   for (int c = threadIdx.x * 8; c < a.H; c += kMoeThreads * 8) {
     float sum[8] = {};
-    for (int j = 0; j < a.top_k; ++j) {
-      const int64_t p = (int64_t)t * a.top_k + j;
-      const int r = row_of(a, p);
-      if (r < 0) continue;
-      const float w = a.weights ? a.weights[p] : 1.0f;
-      float y[8];
-      unpack8<BF16>(load8(a.rows, a.ld_rows, r, c), y);
+    uint4 res = make_uint4(0, 0, 0, 0);
+    if (a.residual) res = load8(a.residual, a.ld_residual, t, c);
+    for (int j0 = 0; j0 < a.top_k; j0 += 8) {
+      uint4 v[8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) sum[i] = fmaf(w, y[i], sum[i]);
+      for (int u = 0; u < 8; ++u)
+        if (j0 + u < a.top_k && row[j0 + u] >= 0) v[u] = load8(a.rows, a.ld_rows, row[j0 + u], c);
+#pragma unroll
+      for (int u = 0; u < 8; ++u)
+        if (j0 + u < a.top_k && row[j0 + u] >= 0) {
+          float y[8];
+          unpack8<BF16>(v[u], y);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) sum[i] = fmaf(weight[j0 + u], y[i], sum[i]);
+        }
     }
     if (a.residual) {
       float y[8];
-      unpack8<BF16>(load8(a.residual, a.ld_residual, t, c), y);
+      unpack8<BF16>(res, y);
 #pragma unroll
       for (int i = 0; i < 8; ++i) sum[i] += y[i];
     }
@@ -223,37 +320,62 @@ __global__ void __launch_bounds__(kMoeThreads) moe_combine_kernel(const MoveArgs
   }
 }
 
-// grad_rows[pair_row[t, j]] = w[t, j] grad_out[t]; grad_weights[t, j] = grad_out[t] . rows[pair_row[t, j]]
+// grad_rows[pair_row[t, j]] = w[t, j] grad_out[t]; grad_weights[t, j] = grad_out[t] .
+// rows[pair_row[t, j]].  A CTA a token; 4 pairs at a time, so that grad_out is read
+// from L1 after the first and their rows are on their way together; dots are summed
+// in a fixed order (a thread's columns, a warp's lanes, the warps).  Bound: the rows'
+// bytes, once in and once out (65536 rows of 2048: 96 us, 5.9 TB/s).
+constexpr int kGradPairs = 4;
 template <bool BF16>
 __global__ void __launch_bounds__(kMoeThreads) moe_combine_grad_kernel(const MoveArgs a) {
-  __shared__ float part[kMoeThreads / 32];
+  __shared__ float part[kMoeThreads / 32][kGradPairs];
+  __shared__ int row[LORA_MOE_MAX_TOP_K];
+  __shared__ float weight[LORA_MOE_MAX_TOP_K];
   cudaTriggerProgrammaticLaunchCompletion();
   cudaGridDependencySynchronize();
-  const int t = blockIdx.x;
-  for (int j = 0; j < a.top_k; ++j) {
-    const int64_t p = (int64_t)t * a.top_k + j;
-    const int r = row_of(a, p);
-    const float w = a.weights ? a.weights[p] : 1.0f;
-    float dot = 0.0f;
-    if (r >= 0)
-      for (int c = threadIdx.x * 8; c < a.H; c += kMoeThreads * 8) {
-        float g[8], y[8];
-        unpack8<BF16>(load8(a.x, a.ld_x, t, c), g);
-        unpack8<BF16>(load8(a.rows, a.ld_rows, r, c), y);
+  const int t = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  if ((int)threadIdx.x < a.top_k) {
+    const int64_t p = (int64_t)t * a.top_k + threadIdx.x;
+    row[threadIdx.x] = row_of(a, p);
+    weight[threadIdx.x] = a.weights ? a.weights[p] : 1.0f;
+  }
+  __syncthreads();
+  for (int j0 = 0; j0 < a.top_k; j0 += kGradPairs) {
+    float dot[kGradPairs] = {};
+    for (int c = threadIdx.x * 8; c < a.H; c += kMoeThreads * 8) {
+      uint4 v[kGradPairs];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) dot = fmaf(g[i], y[i], dot);
+      for (int u = 0; u < kGradPairs; ++u)
+        if (j0 + u < a.top_k && row[j0 + u] >= 0 && a.grad_weights) v[u] = load8(a.rows, a.ld_rows, row[j0 + u], c);
+      float g[8];
+      unpack8<BF16>(load8(a.x, a.ld_x, t, c), g);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) g[i] *= w;
-        store8(a.out, a.ld_out, r, c, pack8<BF16>(g));
-      }
+      for (int u = 0; u < kGradPairs; ++u)
+        if (j0 + u < a.top_k && row[j0 + u] >= 0) {
+          float y[8];
+          if (a.grad_weights) {
+            unpack8<BF16>(v[u], y);
 #pragma unroll
-    for (int d = 16; d; d >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, d);
-    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = dot;
+            for (int i = 0; i < 8; ++i) dot[u] = fmaf(g[i], y[i], dot[u]);
+          }
+#pragma unroll
+          for (int i = 0; i < 8; ++i) y[i] = g[i] * weight[j0 + u];
+          store8(a.out, a.ld_out, row[j0 + u], c, pack8<BF16>(y));
+        }
+    }
+    if (!a.grad_weights) continue;
+#pragma unroll
+    for (int u = 0; u < kGradPairs; ++u) {
+#pragma unroll
+      for (int d = 16; d; d >>= 1) dot[u] += __shfl_xor_sync(0xffffffffu, dot[u], d);
+      if (lane == 0) part[warp][u] = dot[u];
+    }
     __syncthreads();
-    if (threadIdx.x == 0 && a.grad_weights) {
+    if ((int)threadIdx.x < kGradPairs && j0 + (int)threadIdx.x < a.top_k) {
+      const int j = j0 + threadIdx.x;
       float sum = 0.0f;
-      for (int i = 0; i < kMoeThreads / 32; ++i) sum += part[i];
-      a.grad_weights[p] = r >= 0 ? sum : 0.0f;
+      for (int w = 0; w < kMoeThreads / 32; ++w) sum += part[w][threadIdx.x];
+      a.grad_weights[(int64_t)t * a.top_k + j] = row[j] >= 0 ? sum : 0.0f;
     }
     __syncthreads();
   }

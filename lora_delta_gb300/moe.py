@@ -26,25 +26,22 @@ def _here(t, name):
 
 def _matrix(t, name, dtype, rows, width):
     """Pointer and row stride of a [rows, width] tensor with adjacent columns; rows may lie apart."""
+    if t.dtype is dtype and t.get_device() == torch._C._cuda_getDevice() and t.shape == (rows, width):
+        ld, step = t.stride()
+        if step == 1 or width <= 1:
+            return t.data_ptr(), ld
     _here(t, name)
-    if t.dtype is not dtype:
-        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.dim() != 2 or t.shape[0] != rows or t.shape[1] != width:
-        raise ValueError(f"{name} must be [{rows}, {width}], got {tuple(t.shape)}")
-    ld, step = t.stride()
-    if step != 1 and width > 1:
-        raise ValueError(f"{name}'s columns must be adjacent")
-    return t.data_ptr(), (ld if rows > 1 else width)
+    raise ValueError(f"{name} must be {dtype} [{rows}, {width}] with adjacent columns, got {t.dtype} {tuple(t.shape)}")
 
 
 def _whole(t, name, dtype, shape):
     """Pointer of a contiguous tensor of this shape, or None."""
     if t is None:
         return None
+    if t.dtype is dtype and t.get_device() == torch._C._cuda_getDevice() and t.shape == shape and t.is_contiguous():
+        return t.data_ptr()
     _here(t, name)
-    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor {tuple(shape)}, got {t.dtype} {tuple(t.shape)}")
-    return t.data_ptr()
+    raise ValueError(f"{name} must be a contiguous {dtype} tensor {tuple(shape)}, got {t.dtype} {tuple(t.shape)}")
 
 
 def _rows_dtype(t, name):
@@ -69,8 +66,14 @@ class MoePlan(_Fixed):
 
         self.seg_start, self.pair_row = ints(self.E + 1, value=0), ints(self.T, self.top_k)
         self.row_pair, self.row_expert, self.row_lora = (ints(self.n_rows) for _ in range(3))
+        self._device = self.seg_start.get_device()
         self._seg, self._pair = self.seg_start.data_ptr(), self.pair_row.data_ptr()
         self._out = (self._seg, self.row_pair.data_ptr(), self._pair, self.row_expert.data_ptr(), self.row_lora.data_ptr())
+
+
+def _plan_here(plan):
+    if plan._device != torch._C._cuda_getDevice():
+        raise ValueError(f"the plan is on device {plan._device}, not on the current one")
 
 
 def lora_moe_dispatch(rows, x, topk_ids, plan: MoePlan, lora_ids=None, expert_map=None, err=None, stream=None) -> MoePlan:
@@ -80,7 +83,7 @@ def lora_moe_dispatch(rows, x, topk_ids, plan: MoePlan, lora_ids=None, expert_ma
     global experts' numbers on this rank, -1 elsewhere.  The gradient for x is ``lora_moe_combine(grad_x, grad_rows, plan)``."""
     T, k = plan.T, plan.top_k
     H, dtype = x.shape[-1], _rows_dtype(x, "x")
-    _here(plan.seg_start, "plan")
+    _plan_here(plan)
     x_at, ld_x = _matrix(x, "x", dtype, T, H)
     rows_at, ld_rows = _matrix(rows, "rows", dtype, plan.n_rows, H)
     n_map = 0
@@ -99,7 +102,7 @@ def lora_moe_combine(out, rows, plan: MoePlan, weights=None, residual=None, stre
     ``weights`` [T, top_k] float32 (1 without); ``residual`` [T, H] may be ``out`` itself.  Without either it is the gradient
     of ``lora_moe_dispatch``."""
     T, H, dtype = plan.T, out.shape[-1], _rows_dtype(out, "out")
-    _here(plan.seg_start, "plan")
+    _plan_here(plan)
     out_at, ld_out = _matrix(out, "out", dtype, T, H)
     rows_at, ld_rows = _matrix(rows, "rows", dtype, plan.n_rows, H)
     res_at, ld_res = (None, 0) if residual is None else _matrix(residual, "residual", dtype, T, H)
@@ -112,7 +115,7 @@ def lora_moe_combine_grad(grad_rows, grad_weights, grad_out, rows, plan: MoePlan
     """The gradient of ``lora_moe_combine`` for its rows, into ``grad_rows`` (rows that no pair has stay as they were), and for
     its weights, into ``grad_weights`` [T, top_k] float32 or None.  That for the residual is ``grad_out`` itself."""
     T, H, dtype = plan.T, grad_out.shape[-1], _rows_dtype(grad_out, "grad_out")
-    _here(plan.seg_start, "plan")
+    _plan_here(plan)
     go_at, ld_go = _matrix(grad_out, "grad_out", dtype, T, H)
     rows_at, ld_rows = _matrix(rows, "rows", dtype, plan.n_rows, H)
     gr_at, ld_gr = _matrix(grad_rows, "grad_rows", dtype, plan.n_rows, H)
@@ -202,7 +205,7 @@ def lora_moe_linear(out, rows, weight, plan: MoePlan, bias=None, delta=None, res
     they were."""
     dtype, n = _rows_dtype(rows, "rows"), plan.n_rows
     _here(weight, "weight")
-    _here(plan.seg_start, "plan")
+    _plan_here(plan)
     if weight.dtype is not dtype or weight.dim() != 3 or weight.shape[0] != plan.E:
         raise ValueError(f"weight must be {dtype} [{plan.E}, n_out, k_in], got {weight.dtype} {tuple(weight.shape)}")
     E, N, K = weight.shape
