@@ -227,7 +227,6 @@ __global__ void __launch_bounds__(C::THREADS, 2) linear_few_kernel(const LinearA
   }
   // What the call before writes is not read ahead of the wait, but W may come to L2
   // (a product of one group knows its part; up to 48 MB of all CTAs' parts).
-  cudaTriggerProgrammaticLaunchCompletion();
   if (warp == 0 && !a.seg_start && blockIdx.z == 0) {
     const int most = max(1, (48 << 20) / (int)(gridDim.x * C::W));
     for (int i = lane; i < min(nkb, most); i += 32) {
@@ -235,7 +234,8 @@ __global__ void __launch_bounds__(C::THREADS, 2) linear_few_kernel(const LinearA
       if (a.gated) tma_prefetch_3d(&map_w, (kb0 + i) * 64, a.n_out + ft * 64, 0);
     }
   }
-  cudaGridDependencySynchronize();
+  // (tensor memory after the wait: the call before may still need all of it)
+  after_previous_call();
   if (warp == 1) tc::tmem_alloc(&taddr_s, C::COLS);
   tc::fence_before_sync();
   __syncthreads();
@@ -618,9 +618,8 @@ __global__ void __launch_bounds__(Pair::THREADS, 1) linear_pair_kernel(const Lin
   }
   __syncwarp();
   cluster_arrive();  // (the barriers of both are ready at the wait)
-  cudaTriggerProgrammaticLaunchCompletion();
   // (a product of one group lays out its work ahead of the wait for the call before)
-  if (a.seg_start) cudaGridDependencySynchronize();
+  if (a.seg_start) after_previous_call();
   constexpr int per_pair = GATED ? 128 : 256;
   const int features = (a.n_out + per_pair - 1) / per_pair;
   {
@@ -672,7 +671,7 @@ __global__ void __launch_bounds__(Pair::THREADS, 1) linear_pair_kernel(const Lin
     if (!walk.next(p)) p.parts = 0;
   }
   __syncwarp();
-  if (!a.seg_start) cudaGridDependencySynchronize();
+  if (!a.seg_start) after_previous_call();
   if (warp == 2) tc::tmem_alloc_pair(&taddr_s, 512);
   tc::fence_before_sync();
   __syncthreads();

@@ -236,8 +236,7 @@ int lora_moe_dispatch(void* rows, int64_t ld_rows, int32_t* seg_start, int32_t* 
   a.top_k = top_k;
   a.H = H;
   a.P = P;
-  static const int few = env_int("LORA_MOE_FEW", kMoeFewPairs);
-  if (T > 0 && P <= few && P <= kMoeFewPairs) {
+  if (T > 0 && P <= kMoeFewPairs) {
     const size_t smem = (size_t)(E + 1) * 4 + (size_t)P * 2;
     return launch(moe_dispatch_few_kernel, dim3((unsigned)T), kMoeThreads, smem, (cudaStream_t)stream, 1, p, a);
   }

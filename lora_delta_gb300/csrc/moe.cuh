@@ -13,6 +13,14 @@
 
 namespace lora {
 
+// The wait for the call before, and leave for the next one's CTAs to come: in this
+// order, so that what those do ahead of their own wait finds the calls before this
+// one done.
+__device__ __forceinline__ void after_previous_call() {
+  cudaGridDependencySynchronize();
+  cudaTriggerProgrammaticLaunchCompletion();
+}
+
 constexpr int kMoeMaxExperts = 1024;
 constexpr int kMoeSortCluster = 16;
 constexpr int kMoeThreads = 256;
@@ -65,8 +73,7 @@ inline size_t moe_sort_smem(int E) { return sizeof(uint32_t) * ((size_t)kRouteWa
 __global__ void __launch_bounds__(kRouteThreads) moe_sort_kernel(const MoePlanArgs a) {
   extern __shared__ uint32_t cnt[];  // [kRouteWarps][E + 1], then mine, before, total
   __shared__ uint32_t warp_sums[kRouteWarps];
-  cudaTriggerProgrammaticLaunchCompletion();
-  cudaGridDependencySynchronize();
+  after_previous_call();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int E = a.key.E, nkb = E + 1, nblk = (int)gridDim.x, blk = (int)blockIdx.x;
   uint32_t *mine = cnt + kRouteWarps * nkb, *before = mine + nkb, *total = before + nkb;
@@ -76,7 +83,25 @@ __global__ void __launch_bounds__(kRouteThreads) moe_sort_kernel(const MoePlanAr
   const int b0 = (int)(a.P * part / parts), b1 = (int)(a.P * (part + 1) / parts);
   uint32_t errbits = 0;
   uint32_t* my = cnt + warp * nkb;
-  warp_count<4>(a.key, b0, b1, nkb, my, errbits);
+  // The first 256 pairs' keys and adapters of a warp stay in registers for the
+  // placing below (65536 pairs: all of them).
+  int key[8], lora[8];
+  auto load = [&](int base, uint32_t& err) {
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      const int p = base + u * 32 + lane;
+      key[u] = p < b1 ? a.key(p, err) : -1;
+      lora[u] = p < b1 && a.lora_ids ? a.lora_ids[p / a.top_k] : -1;
+    }
+  };
+  load(b0, errbits);
+#pragma unroll
+  for (int u = 0; u < 8; ++u) {
+    const unsigned peers = __match_any_sync(0xffffffffu, key[u]);
+    if (key[u] >= 0 && lane == __ffs(peers) - 1) my[key[u]] += __popc(peers);
+    __syncwarp();
+  }
+  warp_count<4>(a.key, b0 + 256, b1, nkb, my, errbits);
   errbits = __reduce_or_sync(0xffffffffu, errbits);
   if (lane == 0 && errbits) set_error(a.err, errbits);
   __syncthreads();
@@ -113,16 +138,9 @@ __global__ void __launch_bounds__(kRouteThreads) moe_sort_kernel(const MoePlanAr
     run += total[k];
   }
   __syncthreads();
-  // (8 pairs' keys and adapters a lane at a time, so that their loads overlap)
   for (int base = b0; base < b1; base += 256) {
-    int key[8], lora[8];
-#pragma unroll
-    for (int u = 0; u < 8; ++u) {
-      const int p = base + u * 32 + lane;
-      uint32_t dummy = 0;
-      key[u] = p < b1 ? a.key(p, dummy) : -1;
-      lora[u] = p < b1 && a.lora_ids ? a.lora_ids[p / a.top_k] : -1;
-    }
+    uint32_t dummy = 0;
+    if (base > b0) load(base, dummy);
 #pragma unroll
     for (int u = 0; u < 8; ++u) {
       if (base + u * 32 >= b1) break;
@@ -204,12 +222,11 @@ __device__ __forceinline__ void scatter_row(const MoveArgs& a, int t, const int*
 }
 
 // rows[pair_row[t, j]] = x[t].  A CTA a token: x is read once, each row written once.
-// Bound: the rows' bytes (65536 rows of 4096: 98 us, 6.2 TB/s).
+// Bound: the rows' bytes.
 __global__ void __launch_bounds__(kMoeThreads) moe_scatter_kernel(const MoveArgs a) {
   __shared__ int row[LORA_MOE_MAX_TOP_K];
-  cudaTriggerProgrammaticLaunchCompletion();
-  cudaGridDependencySynchronize();
   const int t = blockIdx.x;
+  after_previous_call();
   if ((int)threadIdx.x < a.top_k) row[threadIdx.x] = row_of(a, (int64_t)t * a.top_k + threadIdx.x);
   __syncthreads();
   scatter_row(a, t, row);
@@ -227,8 +244,7 @@ __global__ void __launch_bounds__(kMoeThreads) moe_dispatch_few_kernel(const Moe
   const int E = a.key.E, nkb = E + 1;
   uint32_t* hist = few_s;
   uint16_t* key = reinterpret_cast<uint16_t*>(few_s + nkb);
-  cudaTriggerProgrammaticLaunchCompletion();
-  cudaGridDependencySynchronize();
+  after_previous_call();
   uint32_t bad = 0;
   if (t == 0)
     for (int k = tid; k < nkb; k += kMoeThreads) hist[k] = 0;
@@ -283,8 +299,7 @@ template <bool BF16>
 __global__ void __launch_bounds__(kMoeThreads) moe_combine_kernel(const MoveArgs a) {
   __shared__ int row[LORA_MOE_MAX_TOP_K];
   __shared__ float weight[LORA_MOE_MAX_TOP_K];
-  cudaTriggerProgrammaticLaunchCompletion();
-  cudaGridDependencySynchronize();
+  after_previous_call();
   const int t = blockIdx.x;
   if ((int)threadIdx.x < a.top_k) {
     const int64_t p = (int64_t)t * a.top_k + threadIdx.x;
@@ -331,8 +346,7 @@ __global__ void __launch_bounds__(kMoeThreads) moe_combine_grad_kernel(const Mov
   __shared__ float part[kMoeThreads / 32][kGradPairs];
   __shared__ int row[LORA_MOE_MAX_TOP_K];
   __shared__ float weight[LORA_MOE_MAX_TOP_K];
-  cudaTriggerProgrammaticLaunchCompletion();
-  cudaGridDependencySynchronize();
+  after_previous_call();
   const int t = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   if ((int)threadIdx.x < a.top_k) {
     const int64_t p = (int64_t)t * a.top_k + threadIdx.x;

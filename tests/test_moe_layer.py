@@ -285,7 +285,10 @@ LINEAR = [  # n, K, N, act, gated, bias, delta, residual
     (65, 64, 128, "gelu_tanh", False, False, True, False), (100, 520, 48, "gelu", True, True, False, True),
     (129, 256, 640, "gelu_tanh", True, False, False, False), (200, 1032, 1000, "none", False, False, True, True),
     (255, 392, 272, "relu", True, True, True, False), (257, 128, 512, "silu", False, True, True, True),
-    (700, 328, 1296, "silu", True, False, True, True), (1500, 904, 776, "none", False, True, False, True)]
+    (700, 328, 1296, "silu", True, False, True, True), (1500, 904, 776, "none", False, True, False, True),
+    # tiles shared along K by two pairs of CTAs and by more, whole rounds of tiles, no rows but one past a tile's
+    (300, 8192, 512, "none", False, True, True, True), (1090, 4096, 1296, "silu", True, False, True, False),
+    (5000, 72, 2064, "relu", False, False, False, True), (257, 5000, 272, "gelu", True, True, False, True)]
 
 
 @gpu
@@ -329,7 +332,8 @@ def test_linear_on_columns_of_larger_tensors(ld):
     (1, 1, 1, 64, 16, "none", False, True, False, True), (1, 8, 64, 256, 160, "silu", True, False, True, False),
     (64, 8, 64, 512, 272, "silu", True, True, True, True), (40, 2, 3, 72, 392, "gelu", False, True, True, False),
     (200, 4, 8, 264, 128, "relu", False, False, False, True), (300, 8, 16, 136, 528, "gelu_tanh", True, True, False, False),
-    (700, 3, 5, 128, 264, "none", False, False, True, True), (30, 2, 600, 64, 24, "silu", False, True, True, True)])
+    (700, 3, 5, 128, 264, "none", False, False, True, True), (30, 2, 600, 64, 24, "silu", False, True, True, True),
+    (2000, 4, 64, 64, 528, "silu", True, False, True, False), (400, 2, 3, 4096, 128, "none", False, True, False, True)])
 def test_experts(ld, dtype, T, k, E, K, N, act, gated, bias, delta, residual):
     rng = np.random.default_rng(T + E)
     width, P = N // 2 if gated else N, T * k
@@ -579,3 +583,103 @@ def test_a_wait_that_gives_up_is_reported(ld, n, gated):
         out.fill_(3)
         ld.lora_linear(out, x, w, gated=gated, err=err)
         assert ld.lora_get_error(err) == 0 and torch.equal(out, want)
+
+
+@gpu
+def test_workspaces_of_products(ld):
+    """One's own or none given: the same result; left ready; refused where it cannot be used."""
+    rng = np.random.default_rng(70)
+    x, w = normal(rng, torch.bfloat16, 300, 8192), normal(rng, torch.bfloat16, 512, 8192, std=1 / 90)
+    want, out, ws = *torch.empty(2, 300, 512, device="cuda").bfloat16(), ld.lora_linear_workspace()
+    ld.lora_linear(want, x, w)
+    for _ in range(3):
+        ld.lora_linear(out, x, w, workspace=ws)
+        assert torch.equal(out, want)
+    assert not ws[:int(ld.lib().lora_linear_zeroed_bytes())].any()
+    for bad in (ws.cpu(), ws[::2]):
+        with pytest.raises(ValueError):
+            ld.lora_linear(out, x, w, workspace=bad)
+    with pytest.raises(ld.LoraError) as e:
+        ld.lora_linear(out, x, w, workspace=ws[:-256])
+    assert e.value.code == 5
+    assert int(ld.lib().lora_linear_workspace_size(1, 1)) == 0 and int(ld.lib().lora_linear_workspace_size(2000, 64)) == 0
+    # none at all, by the C call: whole tiles only
+    import ctypes
+    p = [ctypes.c_void_p(t.data_ptr()) for t in (out, x, w)]
+    out.zero_()
+    s = ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+    assert ld.lib().lora_linear(p[0], 512, p[1], 8192, 300, 8192, p[2], 8192, 512, None, None, 0, None, 0, 0, 0, 0, None, 0, None, s) == 0
+    reference, bound = ref.linear(host(x), host(w))
+    close(host(out), reference, bound, torch.bfloat16)
+
+
+@gpu
+def test_graphs_of_products_have_workspaces_of_their_own(ld):
+    """Two graphs and eager calls of shared tiles, side by side on three streams."""
+    rng = np.random.default_rng(71)
+    x, w = normal(rng, torch.bfloat16, 300, 8192), normal(rng, torch.bfloat16, 512, 8192, std=1 / 90)
+    outs, graphs, streams = [torch.empty(300, 512, device="cuda").bfloat16() for _ in range(3)], [], [torch.cuda.Stream() for _ in range(3)]
+    want = torch.empty_like(outs[0])
+    ld.lora_linear(want, x, w)
+    torch.cuda.synchronize()
+    for i in range(2):
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1], stream=streams[i]):
+            ld.lora_linear(outs[i], x, w)
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for g, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                g.replay()
+        ld.lora_linear(outs[2], x, w, stream=streams[2])
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, want) for o in outs)
+
+
+@gpu
+@pytest.mark.parametrize("T", [1, 50])
+def test_example_of_a_layer(ld, T):
+    from examples.moe_layer import MoeLayer
+    layer, rng = MoeLayer(), np.random.default_rng(T)
+    x, lora = normal(rng, torch.bfloat16, T, layer.H), dev(rng.integers(-1, layer.L, T))
+    weights, ids = layer.route(x)
+    out, plan = layer.forward(x, weights, ids, lora)
+    c = {"ids": host(ids), "lora": host(lora), "x": x, "w": weights, "w13": layer.w13, "w2": layer.w2, "a13": layer.a13, "b13": layer.b13,
+         "a2": layer.a2, "b2": layer.b2, "E": layer.E, "I": layer.I, "rank": layer.rank, "L": layer.L, "H": layer.H, "k": layer.top_k, "T": T}
+    assert ld.lora_get_error(layer.err) == 0 and torch.equal(out, run_layer(ld, c)["out"])
+    check_plan(plan, ref.plan(c["ids"], layer.E, c["lora"]))
+
+
+@gpu
+def test_gradients_of_a_loss_through_dispatch_and_combine(ld):
+    """The calls' gradients of sum(combine(c * dispatch(x)) * g) against differences of the 64-bit form."""
+    rng, T, k, E, H = np.random.default_rng(80), 20, 3, 5, 16
+    ids = route(rng, T, k, E, none=0.1)
+    x, c, g = normal(rng, torch.bfloat16, T, H), normal(rng, torch.bfloat16, T * k, H), normal(rng, torch.bfloat16, T, H)
+    w = dev(rng.random((T, k)), np.float32)
+    plan, rows, _ = dispatched(ld, ids, E, x)
+    y = (rows.float() * c.float()).bfloat16()
+    grad_y, grad_w = torch.zeros_like(y), torch.empty(T, k, device="cuda")
+    ld.lora_moe_combine_grad(grad_y, grad_w, g, y, plan, weights=w)
+    grad_rows, grad_x = (grad_y.float() * c.float()).bfloat16(), torch.empty_like(x)
+    ld.lora_moe_combine(grad_x, grad_rows, plan)
+    p, c64, g64, w64 = ref.plan(ids, E), host(c), host(g), host(w)
+
+    def loss(x, w):
+        moved = np.where(p["row_pair"][:, None] >= 0, x[p["row_pair"] // k], 0.0)
+        return (ref.combine(moved * c64, p["pair_row"], w)[0] * g64).sum()
+
+    x64, step = host(x), 1e-4
+    for i in [(0, 0), (3, 7), (11, 15), (19, 2)]:
+        d = np.zeros_like(x64)
+        d[i] = step
+        size = sum(abs(w64[i[0], j] * g64[i] * c64[r, i[1]]) for j, r in enumerate(p["pair_row"][i[0]]) if r >= 0)
+        # three roundings to bf16 (grad_y, grad_rows, grad_x), half a step each, of terms and of their sum
+        assert abs((loss(x64 + d, w64) - loss(x64 - d, w64)) / (2 * step) - host(grad_x)[i]) <= 3.1 * 2.0 ** -8 * size + 1e-6
+    for i in [(0, 0), (5, 2), (17, 1)]:
+        d = np.zeros_like(w64)
+        d[i] = step
+        r = p["pair_row"][i]
+        size = np.abs(g64[i[0]] * x64[i[0]] * c64[r]).sum() if r >= 0 else 0.0
+        # one rounding to bf16, of y
+        assert abs((loss(x64, w64 + d) - loss(x64, w64 - d)) / (2 * step) - host(grad_w)[i]) <= 1.1 * 2.0 ** -8 * size + 1e-6
