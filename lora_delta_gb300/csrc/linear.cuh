@@ -9,7 +9,8 @@
 // 48 columns, not a tile of 128.  Gated, a CTA's 128 rows are 64 of each half.
 // The sums go through shared memory to the threads that finish 8 columns of a
 // row of out, where delta and residual are read and out is written whole sectors
-// at a time.
+// at a time.  Two kernels: few rows a group stream W and are bound by its bytes, many
+// rows by the tensor cores (64 FLOP and more a byte of W).
 #pragma once
 
 #include <cuda.h>
@@ -145,6 +146,11 @@ __device__ __forceinline__ uint4 linear_finish(const LinearArgs& a, const Linear
 // parts are added in the order of K through distributed shared memory, each CTA
 // finishing its share of the tile.  Grid: (feature tile, part of K), group, and
 // row tiles in turn.  Two CTAs fit an SM.
+// Bound: W's bytes.  1 row of 4096 by 6144 11.6 us (4.3 TB/s, of which the copies take
+// 8.9), 64 rows 16.3, where the parts' way through distributed shared memory costs 3.3
+// (read from the CTA's own instead: 13.0); 64 tokens of 8 experts, 2048 by 1536 gated,
+// 70.8 us (5.8 TB/s).  Tiles of 256 rows of x in this form lose to the pairs below: the
+// parts' way grows with the rows (192 rows of 2048 by 2048 26 us, 17 there).
 template <int NT_>
 struct Few {
   static constexpr int NT = NT_;
@@ -333,6 +339,15 @@ __global__ void __launch_bounds__(C::THREADS, 2) linear_few_kernel(const LinearA
 // copies for 512 cycles of products.  Persistent: a warp that lays out the pair's
 // items ahead, a load warp, an MMA warp (of the even CTA) and 8 epilogue warps, the
 // sums of one tile in one half of tensor memory while the epilogue reads the other's.
+// Bound: the tensor cores while K is long (8192 x 4096 by 28672 1045 to 1075 us, 1790
+// to 1840 TFLOP/s; gated with silu and delta 1060 to 1110; products without copies or an
+// epilogue 1000, copies alone 875), W's bytes for the experts of few tokens (16384 rows
+// of 64 experts, 2048 by 1536 gated with delta: 106.5 us, 5.1 TB/s; without an epilogue
+// 88), and the epilogue where K is short (768 by 2048: 64 us, without one 48).  Tried:
+// descriptors from one lane 1086 us where the whole warp takes 1000 (products alone); six
+// stages and 16 columns of the epilogue at once, with flags instead of forms of the
+// kernel, 154 us for the experts' 106; erf and tanh inlined for every value 376 us where
+// 65536 rows of the experts now take 270, by what the roles then fetch of instructions.
 struct Pair {
   static constexpr int W = 128 * 128, X = 128 * 128, STAGE = W + X, STAGES = 5;
   static constexpr int EPI = 8, EPI_WARP = 4, THREADS = (EPI_WARP + EPI) * 32;
