@@ -580,7 +580,8 @@ int lora_kv4_attention(void *out, int64_t ld_out, const void *q, int64_t ld_q, i
  * matter), 16-byte aligned; H, k_in, n_out are multiples of 8 (LORA_ERR_ALIGN).
  * No output may share memory with another argument (LORA_ERR_ARG), but for
  * `out` with `residual` as stated.  Columns of one buffer may interleave.
- * Limits: E <= 1024, top_k <= 64, T * top_k < 2^30 (LORA_ERR_UNSUPPORTED).
+ * Limits: E <= 1024, top_k <= 64, T * top_k < 2^30, n <= 2^30 rows of a product
+ * (LORA_ERR_UNSUPPORTED).
  */
 #define LORA_MOE_MAX_TOP_K 64
 

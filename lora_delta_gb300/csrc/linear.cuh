@@ -652,6 +652,9 @@ __global__ void __launch_bounds__(Pair::THREADS, 1) linear_pair_kernel(const Lin
       sum.y += v.y;
     }
     if (bad && blockIdx.x == 0) set_error(a.err, bad);
+    // (segments that overlap could be more rows than there are: nothing is done then)
+    const bool none = __syncthreads_or(bad != 0);
+    if (none) sum = make_int2(0, 0);
     int2 inc = sum;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
@@ -671,7 +674,7 @@ __global__ void __launch_bounds__(Pair::THREADS, 1) linear_pair_kernel(const Lin
     for (int i = 0; i < per; ++i) {
       const int g = tid * per + i;
       if (g >= a.groups) break;
-      const int2 v = pre[g];
+      const int2 v = none ? make_int2(0, 0) : pre[g];
       pre[g] = run;
       run.x += v.x;
       run.y += v.y;

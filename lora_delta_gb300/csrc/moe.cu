@@ -169,7 +169,7 @@ int linear_call(LinearArgs& a, int dtype, void* workspace, size_t ws_bytes, cuda
   int rc = check_dtype(dtype);
   if (rc) return rc;
   if (a.K % 8 || a.N % (a.gated ? 16 : 8)) return LORA_ERR_ALIGN;
-  if (a.groups > kMoeMaxExperts || a.K > (1 << 24) || a.N > (1 << 24) || (int64_t)a.groups * a.N > INT32_MAX) return LORA_ERR_UNSUPPORTED;
+  if (a.groups > kMoeMaxExperts || a.n > (1 << 30) || a.K > (1 << 24) || a.N > (1 << 24) || (int64_t)a.groups * a.N > INT32_MAX) return LORA_ERR_UNSUPPORTED;
   if (a.n == 0) return LORA_OK;
   a.n_out = a.gated ? a.N / 2 : a.N;
   const Mat out = {a.out, a.ld_out, a.n, a.n_out}, x = {a.x, a.ld_x, a.n, a.K}, w = {a.w, a.ld_w, a.N, a.K},

@@ -119,7 +119,7 @@ def test_refusals_on_the_host():
         assert linear(E=E, res=ctypes.c_void_p(0x10000000 + 96)) == arg
         assert linear(E=E, n=1000, work=at[7], wsb=1000) == 5 and linear(E=E, work=odd, wsb=1 << 30) == align
     assert linear(E=3, seg=None) == arg and linear(E=3, stride=47 * 64) == shape and linear(E=3, stride=48 * 64 + 8) == shape
-    assert linear(E=1025) == unsup and linear(E=3, seg=at[0]) == arg
+    assert linear(n=2 ** 30 + 1) == unsup and linear(E=1025) == unsup and linear(E=3, seg=at[0]) == arg
 
 
 def test_plans_are_made_on_the_gpu():
@@ -368,13 +368,16 @@ def test_experts_of_all_rows_at_one(ld):
 @gpu
 def test_experts_report_segments_outside_the_rows(ld):
     rng = np.random.default_rng(9)
-    for seg in ([0, 50, 30, 90], [-4, 10, 20, 40], [0, 10, 20, 2 ** 31 - 1], [70, 80, 90, 100]):
-        plan, err = ld.MoePlan(40, 1, 3), ld.new_error_word()
-        plan.seg_start.copy_(dev(seg))
-        big = torch.full((60, 24), 5.0, device="cuda").bfloat16()
-        ld.lora_moe_linear(big[10:50], normal(rng, torch.bfloat16, 40, 64), normal(rng, torch.bfloat16, 3, 24, 64), plan, err=err)
-        assert ld.lora_get_error(err) == 64
-        assert (big[:10] == 5).all() and (big[50:] == 5).all()
+    for n in (40, 400):  # few rows an expert, and many
+        for seg in ([0, 50, 30, 90], [-4, 10, 20, 40], [0, 10, 20, 2 ** 31 - 1], [70, 80, 90, 100], [0, n, 0, n], [2 ** 31 - 1, -1, n, 0]):
+            if all(0 <= a <= b <= n for a, b in zip(seg, seg[1:])):
+                continue
+            plan, err = ld.MoePlan(n, 1, 3), ld.new_error_word()
+            plan.seg_start.copy_(dev(seg))
+            big = torch.full((n + 20, 24), 5.0, device="cuda").bfloat16()
+            ld.lora_moe_linear(big[10:n + 10], normal(rng, torch.bfloat16, n, 64), normal(rng, torch.bfloat16, 3, 24, 64), plan, err=err)
+            assert ld.lora_get_error(err) == 64
+            assert (big[:10] == 5).all() and (big[n + 10:] == 5).all()
 
 
 @gpu
