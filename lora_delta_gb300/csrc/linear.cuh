@@ -7,8 +7,8 @@
 // W's rows are the M side of the tensor cores' products (128 a CTA) and x's rows
 // the N side, whose size a product takes as it comes: a segment of 40 rows costs
 // 48 columns, not a tile of 128.  Gated, a CTA's 128 rows are 64 of each half.
-// The sums go through shared memory to the threads that finish 8 columns of a
-// row of out, where delta and residual are read and out is written whole sectors
+// The sums go through shared memory to the threads that finish 4 or 8 columns of
+// a row of out, where delta and residual are read and out is written whole sectors
 // at a time.  Two kernels: few rows a group stream W and are bound by its bytes, many
 // rows by the tensor cores (64 FLOP and more a byte of W).
 #pragma once
@@ -52,22 +52,23 @@ __device__ __forceinline__ int2 group_rows(const LinearArgs& a, int g, uint32_t&
   return make_int2(s1, min(max(e, s1), a.n));
 }
 
-// Of 8 values.  gelu by tanh is z / (1 + exp(-2 u)), as silu with 2 u for z.  (Few
+// Of N values.  gelu by tanh is z / (1 + exp(-2 u)), as silu with 2 u for z.  (Few
 // instructions matter more than the time they take: the roles of a CTA run at once
 // and fetch theirs side by side.)
-__device__ __forceinline__ void activate8(float* z, int act) {
+template <int N>
+__device__ __forceinline__ void activate(float* z, int act) {
   if (act == LORA_ACT_NONE) return;
   if (act == LORA_ACT_RELU) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) z[i] = z[i] < 0.0f ? 0.0f : z[i];
+    for (int i = 0; i < N; ++i) z[i] = z[i] < 0.0f ? 0.0f : z[i];
   } else if (act == LORA_ACT_GELU) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) z[i] = 0.5f * z[i] * (1.0f + erff(z[i] * 0.70710678f));
+    for (int i = 0; i < N; ++i) z[i] = 0.5f * z[i] * (1.0f + erff(z[i] * 0.70710678f));
   } else {
     const float cubic = act == LORA_ACT_SILU ? 0.0f : 2.0f * 0.79788456f * 0.044715f;
     const float linear = act == LORA_ACT_SILU ? 1.0f : 2.0f * 0.79788456f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
+    for (int i = 0; i < N; ++i) {
       const float t = z[i] * (cubic == 0.0f ? linear : fmaf(cubic * z[i], z[i], linear));
       z[i] = __fdividef(z[i], 1.0f + __expf(-t));
     }
@@ -83,61 +84,73 @@ struct RowMaps {
 __host__ __device__ __forceinline__ int row_box(int rows) { return rows <= 16 ? 0 : (rows <= 32 ? 1 : (rows <= 64 ? 2 : 3)); }
 
 // -------------------------------------------------------------- epilogue --
-// 8 columns of a row of out: what is read for them, ahead of the sums, and what
-// becomes of the sums z (and up, the second half's).
+// 8 (V: uint4) or 4 (uint2) columns of a row of out: what is read for them, ahead of
+// the sums, and what becomes of the sums z (and up, the second half's).
+template <class V>
 struct LinearTail {
-  uint4 delta[2], residual;
+  V delta[2], residual;
 };
+template <class V>
 struct LinearBias {
-  uint4 half[2];
+  V half[2];
 };
 
-template <bool GATED>
-__device__ __forceinline__ LinearBias linear_bias(const LinearArgs& a, int g, int col) {
-  LinearBias b;
-  b.half[0] = b.half[1] = make_uint4(0, 0, 0, 0);
+template <class V>
+__device__ __forceinline__ V load_v(const void* base, int64_t at) {
+  return *reinterpret_cast<const V*>(reinterpret_cast<const uint16_t*>(base) + at);
+}
+
+template <bool GATED, class V>
+__device__ __forceinline__ LinearBias<V> linear_bias(const LinearArgs& a, int g, int col) {
+  LinearBias<V> b = {};
   if (a.bias && col < a.n_out) {
-    const uint16_t* at = reinterpret_cast<const uint16_t*>(a.bias) + (int64_t)g * a.N + col;
-    b.half[0] = *reinterpret_cast<const uint4*>(at);
-    if (GATED) b.half[1] = *reinterpret_cast<const uint4*>(at + a.n_out);
+    b.half[0] = load_v<V>(a.bias, (int64_t)g * a.N + col);
+    if (GATED) b.half[1] = load_v<V>(a.bias, (int64_t)g * a.N + a.n_out + col);
   }
   return b;
 }
 
-template <bool GATED>
-__device__ __forceinline__ LinearTail linear_tail(const LinearArgs& a, int64_t row, int col, bool use) {
-  LinearTail t;
-  t.delta[0] = t.delta[1] = t.residual = make_uint4(0, 0, 0, 0);
+template <bool GATED, class V>
+__device__ __forceinline__ LinearTail<V> linear_tail(const LinearArgs& a, int64_t row, int col, bool use) {
+  LinearTail<V> t = {};
   if (use && a.delta) {
-    t.delta[0] = load8(a.delta, a.ld_delta, row, col);
-    if (GATED) t.delta[1] = load8(a.delta, a.ld_delta, row, a.n_out + col);
+    t.delta[0] = load_v<V>(a.delta, row * a.ld_delta + col);
+    if (GATED) t.delta[1] = load_v<V>(a.delta, row * a.ld_delta + a.n_out + col);
   }
-  if (use && a.residual) t.residual = load8(a.residual, a.ld_residual, row, col);
+  if (use && a.residual) t.residual = load_v<V>(a.residual, row * a.ld_residual + col);
   return t;
 }
 
-template <bool BF16>
-__device__ __forceinline__ void add8(float* z, const uint4& v) {
-  float f[8];
-  unpack8<BF16>(v, f);
+template <bool BF16, class V>
+__device__ __forceinline__ void add_v(float* z, const V& v) {
+  const uint32_t* w = reinterpret_cast<const uint32_t*>(&v);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) z[i] += f[i];
+  for (int i = 0; i < (int)(sizeof(V) / 4); ++i) {
+    const float2 f = unpack2<BF16>(w[i]);
+    z[2 * i] += f.x;
+    z[2 * i + 1] += f.y;
+  }
 }
 
 // EXTRA: with a delta (1), a residual (2).
-template <bool BF16, bool GATED, int EXTRA>
-__device__ __forceinline__ uint4 linear_finish(const LinearArgs& a, const LinearBias& b, const LinearTail& t, float* z, float* up) {
-  if (a.bias) add8<BF16>(z, b.half[0]);
-  if ((EXTRA & 1) && a.delta) add8<BF16>(z, t.delta[0]);
-  activate8(z, a.act);
+template <bool BF16, bool GATED, int EXTRA, class V>
+__device__ __forceinline__ V linear_finish(const LinearArgs& a, const LinearBias<V>& b, const LinearTail<V>& t, float* z, float* up) {
+  constexpr int N = sizeof(V) / 2;
+  if (a.bias) add_v<BF16>(z, b.half[0]);
+  if ((EXTRA & 1) && a.delta) add_v<BF16>(z, t.delta[0]);
+  activate<N>(z, a.act);
   if (GATED) {
-    if (a.bias) add8<BF16>(up, b.half[1]);
-    if ((EXTRA & 1) && a.delta) add8<BF16>(up, t.delta[1]);
+    if (a.bias) add_v<BF16>(up, b.half[1]);
+    if ((EXTRA & 1) && a.delta) add_v<BF16>(up, t.delta[1]);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) z[i] *= up[i];
+    for (int i = 0; i < N; ++i) z[i] *= up[i];
   }
-  if ((EXTRA & 2) && a.residual) add8<BF16>(z, t.residual);
-  return pack8<BF16>(z);
+  if ((EXTRA & 2) && a.residual) add_v<BF16>(z, t.residual);
+  V y;
+  uint32_t* w = reinterpret_cast<uint32_t*>(&y);
+#pragma unroll
+  for (int i = 0; i < N / 2; ++i) w[i] = pack2<BF16>(z[2 * i], z[2 * i + 1]);
+  return y;
 }
 
 // ------------------------------------------------------------- few rows --
@@ -146,11 +159,12 @@ __device__ __forceinline__ uint4 linear_finish(const LinearArgs& a, const Linear
 // parts are added in the order of K through distributed shared memory, each CTA
 // finishing its share of the tile.  Grid: (feature tile, part of K), group, and
 // row tiles in turn.  Two CTAs fit an SM.
-// Bound: W's bytes.  1 row of 4096 by 6144 11.6 us (4.3 TB/s, of which the copies take
-// 8.9), 64 rows 16.3, where the parts' way through distributed shared memory costs 3.3
-// (read from the CTA's own instead: 13.0); 64 tokens of 8 experts, 2048 by 1536 gated,
-// 70.8 us (5.8 TB/s).  Tiles of 256 rows of x in this form lose to the pairs below: the
-// parts' way grows with the rows (192 rows of 2048 by 2048 26 us, 17 there).
+// Bound: W's bytes, and launch, first copies and the parts' way where they are few.  1 row
+// of 4096 by 6144 11.5 us (4.4 TB/s), 64 rows 14.3, 128 rows 17.0; 64 tokens of 8 experts,
+// 2048 by 1536 gated, 70.3 us (5.8 TB/s).  Parts read 32 bytes a thread instead of 16, so
+// that a warp's lie apart: 64 rows 16.3, 128 rows 21.0 (from the CTA's own memory 13.0).
+// Tiles of 256 rows of x in this form lost to the pairs below, as the parts' way grows
+// with the rows (192 rows of 2048 by 2048 26 us, 17 there).
 template <int NT_>
 struct Few {
   static constexpr int NT = NT_;
@@ -163,42 +177,43 @@ struct Few {
   static_assert(NT * PAD * 4 <= STAGES * STAGE, "a part lies where the operands were");
 };
 
-// A CTA's share of a tile, from all parts: 8 columns of out a thread.  What is read
-// from global memory for the first of them is on its way while the parts are awaited.
+// A CTA's share of a tile, from all parts: 4 columns of out a thread, so that a warp
+// reads a part's 512 bytes in a row.  What is read from global memory for the first of
+// them is on its way while the parts are awaited.
 template <bool BF16, bool GATED, class C>
 __device__ __forceinline__ void linear_few_finish(const LinearArgs& a, const float* own, int g, int ft, int r0, int rows, int part,
                                                   int split, bool use) {
-  constexpr int width = GATED ? 8 : 16;
-  LinearBias bias;
-  LinearTail t;
+  constexpr int width = GATED ? 16 : 32;
+  LinearBias<uint2> bias;
+  LinearTail<uint2> t;
   auto fetch = [&](int i) {
-    const int col = (ft * width + i % width) * 8;
-    bias = linear_bias<GATED>(a, g, use ? col : a.n_out);
-    t = linear_tail<GATED>(a, r0 + i / width, col, use && i < rows * width && col < a.n_out);
+    const int col = (ft * width + i % width) * 4;
+    bias = linear_bias<GATED, uint2>(a, g, use ? col : a.n_out);
+    t = linear_tail<GATED, uint2>(a, r0 + i / width, col, use && i < rows * width && col < a.n_out);
   };
   int i = part * C::THREADS + (int)threadIdx.x;
   fetch(i);
   cluster_wait();
   for (; use && i < rows * width; i += split * C::THREADS) {
-    const int r = i / width, b = i % width, col = (ft * width + b) * 8;
-    float z[16] = {};
-    const uint32_t at = smem_addr(own + r * C::PAD + b * 8);
-    constexpr int AT_ONCE = GATED ? 2 : 4;
+    const int r = i / width, b = i % width, col = (ft * width + b) * 4;
+    float z[8] = {};
+    const uint32_t at = smem_addr(own + r * C::PAD + b * 4);
+    constexpr int AT_ONCE = GATED ? 4 : 8;
 #pragma unroll 1
     for (int p = 0; p < split; p += AT_ONCE) {
-      float4 f[AT_ONCE][GATED ? 4 : 2];
+      float4 f[AT_ONCE][GATED ? 2 : 1];
 #pragma unroll
       for (int x = 0; x < AT_ONCE; ++x)
         if (p + x < split) {
           const uint32_t from = dsmem_map(at, p + x);
-#pragma unroll
-          for (int j = 0; j < (GATED ? 4 : 2); ++j) f[x][j] = dsmem_ld_f32x4(from + (j < 2 ? 16 * j : 256 + 16 * (j - 2)));
+          f[x][0] = dsmem_ld_f32x4(from);
+          if (GATED) f[x][GATED ? 1 : 0] = dsmem_ld_f32x4(from + 256);
         }
 #pragma unroll
       for (int x = 0; x < AT_ONCE; ++x)
         if (p + x < split) {
 #pragma unroll
-          for (int j = 0; j < (GATED ? 4 : 2); ++j) {
+          for (int j = 0; j < (GATED ? 2 : 1); ++j) {
             z[4 * j] += f[x][j].x;
             z[4 * j + 1] += f[x][j].y;
             z[4 * j + 2] += f[x][j].z;
@@ -206,8 +221,8 @@ __device__ __forceinline__ void linear_few_finish(const LinearArgs& a, const flo
           }
         }
     }
-    const uint4 y = linear_finish<BF16, GATED, 3>(a, bias, t, z, z + 8);
-    if (col < a.n_out) store8(a.out, a.ld_out, r0 + r, col, y);
+    const uint2 y = linear_finish<BF16, GATED, 3>(a, bias, t, z, z + 4);
+    if (col < a.n_out) *reinterpret_cast<uint2*>(reinterpret_cast<uint16_t*>(a.out) + (int64_t)(r0 + r) * a.ld_out + col) = y;
     if (i + split * C::THREADS < rows * width) fetch(i + split * C::THREADS);
   }
 }
@@ -907,8 +922,8 @@ __global__ void __launch_bounds__(Pair::THREADS, 1) linear_pair_kernel(const Lin
         }
       }
       if (finish) {
-        const LinearBias bias = linear_bias<GATED>(a, p.g, col);
-        LinearTail tail[MINE];
+        const LinearBias<uint4> bias = linear_bias<GATED, uint4>(a, p.g, col);
+        LinearTail<uint4> tail[MINE];
         // (columns and rows past the tile's are read as the last, and not written)
         const int from_col = min(col, a.n_out - 8);
         auto fetch = [&](int c, int i) {

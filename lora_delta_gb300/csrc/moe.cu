@@ -144,7 +144,7 @@ int launch_pair_form(const LinearArgs& a, cudaStream_t stream) {
 }
 
 // Up to how many rows of a group, on average, the kernel for few rows takes.  Few rows,
-// many rows: 128 by 4096 x 28672 47 us, 59; 128 by 4096 x 6144 21, 28; experts of 64
+// many rows: 128 by 4096 x 28672 47 us, 59; 128 by 4096 x 6144 17, 28; experts of 64
 // rows (2048 x 1536 gated) 80, 83; of 80 rows 109, 84.
 constexpr int kFewRows = 64, kFewRowsAlone = 128;
 int64_t mean_rows(int n, int groups) { return ((int64_t)n + groups - 1) / groups; }

@@ -9,6 +9,7 @@
 #include <cuda_fp16.h>
 
 #include "common.cuh"
+#include "kv4.cuh"
 #include "route.cuh"
 
 namespace lora {
@@ -182,29 +183,14 @@ __device__ __forceinline__ void unpack8(const uint4& v, float* f) {
   const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    if (BF16) {
-      f[2 * i] = bf16lo(w[i]);
-      f[2 * i + 1] = bf16hi(w[i]);
-    } else {
-      const float2 h = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
-      f[2 * i] = h.x;
-      f[2 * i + 1] = h.y;
-    }
+    const float2 x = unpack2<BF16>(w[i]);
+    f[2 * i] = x.x;
+    f[2 * i + 1] = x.y;
   }
 }
 template <bool BF16>
 __device__ __forceinline__ uint4 pack8(const float* f) {
-  uint32_t w[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    if (BF16) {
-      w[i] = pack_bf16x2(f[2 * i], f[2 * i + 1]);
-    } else {
-      const __half2 h = __floats2half2_rn(f[2 * i], f[2 * i + 1]);
-      w[i] = *reinterpret_cast<const uint32_t*>(&h);
-    }
-  }
-  return make_uint4(w[0], w[1], w[2], w[3]);
+  return make_uint4(pack2<BF16>(f[0], f[1]), pack2<BF16>(f[2], f[3]), pack2<BF16>(f[4], f[5]), pack2<BF16>(f[6], f[7]));
 }
 __device__ __forceinline__ uint4 load8(const void* base, int64_t ld, int64_t row, int col) {
   return *reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(base) + row * ld + col);
