@@ -24,9 +24,9 @@ def _here(t, name):
         raise ValueError(f"{name} is on {t.device}, not on the current device")
 
 
-def _matrix(t, name, dtype, rows, width):
-    """Pointer and row stride of a [rows, width] tensor with adjacent columns; rows may lie apart."""
-    if t.dtype is dtype and t.get_device() == torch._C._cuda_getDevice() and t.shape == (rows, width):
+def _matrix(t, name, dtype, rows, width, here):
+    """Pointer and row stride of a [rows, width] tensor with adjacent columns on device `here`; rows may lie apart."""
+    if t.dtype is dtype and t.get_device() == here and t.shape == (rows, width):
         ld, step = t.stride()
         if step == 1 or width <= 1:
             return t.data_ptr(), ld
@@ -34,11 +34,11 @@ def _matrix(t, name, dtype, rows, width):
     raise ValueError(f"{name} must be {dtype} [{rows}, {width}] with adjacent columns, got {t.dtype} {tuple(t.shape)}")
 
 
-def _whole(t, name, dtype, shape):
-    """Pointer of a contiguous tensor of this shape, or None."""
+def _whole(t, name, dtype, shape, here):
+    """Pointer of a contiguous tensor of this shape on device `here`, or None."""
     if t is None:
         return None
-    if t.dtype is dtype and t.get_device() == torch._C._cuda_getDevice() and t.shape == shape and t.is_contiguous():
+    if t.dtype is dtype and t.get_device() == here and t.shape == shape and t.is_contiguous():
         return t.data_ptr()
     _here(t, name)
     raise ValueError(f"{name} must be a contiguous {dtype} tensor {tuple(shape)}, got {t.dtype} {tuple(t.shape)}")
@@ -72,8 +72,11 @@ class MoePlan(_Fixed):
 
 
 def _plan_here(plan):
-    if plan._device != torch._C._cuda_getDevice():
+    """The current device, which the plan has to be on."""
+    here = torch._C._cuda_getDevice()
+    if plan._device != here:
         raise ValueError(f"the plan is on device {plan._device}, not on the current one")
+    return here
 
 
 def lora_moe_dispatch(rows, x, topk_ids, plan: MoePlan, lora_ids=None, expert_map=None, err=None, stream=None) -> MoePlan:
@@ -83,16 +86,16 @@ def lora_moe_dispatch(rows, x, topk_ids, plan: MoePlan, lora_ids=None, expert_ma
     global experts' numbers on this rank, -1 elsewhere.  The gradient for x is ``lora_moe_combine(grad_x, grad_rows, plan)``."""
     T, k = plan.T, plan.top_k
     H, dtype = x.shape[-1], _rows_dtype(x, "x")
-    _plan_here(plan)
-    x_at, ld_x = _matrix(x, "x", dtype, T, H)
-    rows_at, ld_rows = _matrix(rows, "rows", dtype, plan.n_rows, H)
+    here = _plan_here(plan)
+    x_at, ld_x = _matrix(x, "x", dtype, T, H, here)
+    rows_at, ld_rows = _matrix(rows, "rows", dtype, plan.n_rows, H, here)
     n_map = 0
     if expert_map is not None:
         n_map = expert_map.numel()
-        expert_map = _whole(expert_map, "expert_map", torch.int32, (n_map,))
+        expert_map = _whole(expert_map, "expert_map", torch.int32, (n_map,), here)
     _check("lora_moe_dispatch", _fn.lora_moe_dispatch(
-        rows_at, ld_rows, *plan._out, x_at, ld_x, _whole(topk_ids, "topk_ids", torch.int32, (T, k)),
-        _whole(lora_ids, "lora_ids", torch.int32, (T,)), expert_map, n_map, T, k, plan.E, H, _err_at(err), _raw_stream(stream)))
+        rows_at, ld_rows, *plan._out, x_at, ld_x, _whole(topk_ids, "topk_ids", torch.int32, (T, k), here),
+        _whole(lora_ids, "lora_ids", torch.int32, (T,), here), expert_map, n_map, T, k, plan.E, H, _err_at(err), _raw_stream(stream)))
     return plan
 
 
@@ -102,12 +105,12 @@ def lora_moe_combine(out, rows, plan: MoePlan, weights=None, residual=None, stre
     ``weights`` [T, top_k] float32 (1 without); ``residual`` [T, H] may be ``out`` itself.  Without either it is the gradient
     of ``lora_moe_dispatch``."""
     T, H, dtype = plan.T, out.shape[-1], _rows_dtype(out, "out")
-    _plan_here(plan)
-    out_at, ld_out = _matrix(out, "out", dtype, T, H)
-    rows_at, ld_rows = _matrix(rows, "rows", dtype, plan.n_rows, H)
-    res_at, ld_res = (None, 0) if residual is None else _matrix(residual, "residual", dtype, T, H)
+    here = _plan_here(plan)
+    out_at, ld_out = _matrix(out, "out", dtype, T, H, here)
+    rows_at, ld_rows = _matrix(rows, "rows", dtype, plan.n_rows, H, here)
+    res_at, ld_res = (None, 0) if residual is None else _matrix(residual, "residual", dtype, T, H, here)
     _check("lora_moe_combine", _fn.lora_moe_combine(
-        out_at, ld_out, rows_at, ld_rows, plan._pair, _whole(weights, "weights", torch.float32, (T, plan.top_k)), res_at, ld_res,
+        out_at, ld_out, rows_at, ld_rows, plan._pair, _whole(weights, "weights", torch.float32, (T, plan.top_k), here), res_at, ld_res,
         T, plan.top_k, H, _DTYPES[dtype], _raw_stream(stream)))
 
 
@@ -115,13 +118,13 @@ def lora_moe_combine_grad(grad_rows, grad_weights, grad_out, rows, plan: MoePlan
     """The gradient of ``lora_moe_combine`` for its rows, into ``grad_rows`` (rows that no pair has stay as they were), and for
     its weights, into ``grad_weights`` [T, top_k] float32 or None.  That for the residual is ``grad_out`` itself."""
     T, H, dtype = plan.T, grad_out.shape[-1], _rows_dtype(grad_out, "grad_out")
-    _plan_here(plan)
-    go_at, ld_go = _matrix(grad_out, "grad_out", dtype, T, H)
-    rows_at, ld_rows = _matrix(rows, "rows", dtype, plan.n_rows, H)
-    gr_at, ld_gr = _matrix(grad_rows, "grad_rows", dtype, plan.n_rows, H)
+    here = _plan_here(plan)
+    go_at, ld_go = _matrix(grad_out, "grad_out", dtype, T, H, here)
+    rows_at, ld_rows = _matrix(rows, "rows", dtype, plan.n_rows, H, here)
+    gr_at, ld_gr = _matrix(grad_rows, "grad_rows", dtype, plan.n_rows, H, here)
     _check("lora_moe_combine_grad", _fn.lora_moe_combine_grad(
-        gr_at, ld_gr, _whole(grad_weights, "grad_weights", torch.float32, (T, plan.top_k)), go_at, ld_go, rows_at, ld_rows,
-        plan._pair, _whole(weights, "weights", torch.float32, (T, plan.top_k)), T, plan.top_k, H, _DTYPES[dtype],
+        gr_at, ld_gr, _whole(grad_weights, "grad_weights", torch.float32, (T, plan.top_k), here), go_at, ld_go, rows_at, ld_rows,
+        plan._pair, _whole(weights, "weights", torch.float32, (T, plan.top_k), here), T, plan.top_k, H, _DTYPES[dtype],
         _raw_stream(stream)))
 
 
@@ -131,9 +134,9 @@ def _activation(name):
     return _ACTIVATIONS[name]
 
 
-def _epilogue(delta, residual, dtype, n, N, width):
-    d = (None, 0) if delta is None else _matrix(delta, "delta", dtype, n, N)
-    r = (None, 0) if residual is None else _matrix(residual, "residual", dtype, n, width)
+def _epilogue(delta, residual, dtype, n, N, width, here):
+    d = (None, 0) if delta is None else _matrix(delta, "delta", dtype, n, N, here)
+    r = (None, 0) if residual is None else _matrix(residual, "residual", dtype, n, width, here)
     return *d, *r
 
 
@@ -182,19 +185,20 @@ def lora_linear(out, x, weight, bias=None, delta=None, residual=None, activation
     ``x`` [n, k_in], ``weight`` [n_out, k_in], ``bias`` [n_out], ``delta`` [n, n_out] (what the LoRA calls leave: it goes
     ahead of the activation), all bfloat16 or all float16, and ``residual`` as ``out``, which it may be itself.  ``activation``:
     "none", "relu", "silu", "gelu" (by erf) or "gelu_tanh"."""
+    here = torch._C._cuda_getDevice()
     dtype, n = _rows_dtype(x, "x"), x.shape[0]
     if weight.dim() != 2:
         raise ValueError(f"weight must be [n_out, k_in], got {tuple(weight.shape)}")
     N, K = weight.shape
     width = N // 2 if gated else N
-    x_at, ld_x = _matrix(x, "x", dtype, n, K)
-    w_at, ld_w = _matrix(weight, "weight", dtype, N, K)
-    out_at, ld_out = _matrix(out, "out", dtype, n, width)
+    x_at, ld_x = _matrix(x, "x", dtype, n, K, here)
+    w_at, ld_w = _matrix(weight, "weight", dtype, N, K, here)
+    out_at, ld_out = _matrix(out, "out", dtype, n, width, here)
     raw = _raw_stream(stream)
-    ws, ws_bytes = _linear_workspace(workspace, n, 1, x.get_device(), stream, raw)
+    ws, ws_bytes = _linear_workspace(workspace, n, 1, here, stream, raw)
     _check("lora_linear", _fn.lora_linear(
-        out_at, ld_out, x_at, ld_x, n, K, w_at, ld_w, N, _whole(bias, "bias", dtype, (N,)),
-        *_epilogue(delta, residual, dtype, n, N, width), _activation(activation), 1 if gated else 0, _DTYPES[dtype],
+        out_at, ld_out, x_at, ld_x, n, K, w_at, ld_w, N, _whole(bias, "bias", dtype, (N,), here),
+        *_epilogue(delta, residual, dtype, n, N, width, here), _activation(activation), 1 if gated else 0, _DTYPES[dtype],
         ws, ws_bytes, _err_at(err), raw))
 
 
@@ -205,7 +209,7 @@ def lora_moe_linear(out, rows, weight, plan: MoePlan, bias=None, delta=None, res
     they were."""
     dtype, n = _rows_dtype(rows, "rows"), plan.n_rows
     _here(weight, "weight")
-    _plan_here(plan)
+    here = _plan_here(plan)
     if weight.dtype is not dtype or weight.dim() != 3 or weight.shape[0] != plan.E:
         raise ValueError(f"weight must be {dtype} [{plan.E}, n_out, k_in], got {weight.dtype} {tuple(weight.shape)}")
     E, N, K = weight.shape
@@ -213,11 +217,11 @@ def lora_moe_linear(out, rows, weight, plan: MoePlan, bias=None, delta=None, res
     if step != 1 and K > 1:
         raise ValueError("weight's columns must be adjacent")
     width = N // 2 if gated else N
-    x_at, ld_x = _matrix(rows, "rows", dtype, n, K)
-    out_at, ld_out = _matrix(out, "out", dtype, n, width)
+    x_at, ld_x = _matrix(rows, "rows", dtype, n, K, here)
+    out_at, ld_out = _matrix(out, "out", dtype, n, width, here)
     raw = _raw_stream(stream)
-    ws, ws_bytes = _linear_workspace(workspace, n, E, rows.get_device(), stream, raw)
+    ws, ws_bytes = _linear_workspace(workspace, n, E, here, stream, raw)
     _check("lora_moe_linear", _fn.lora_moe_linear(
         out_at, ld_out, x_at, ld_x, n, K, plan._seg, E, weight.data_ptr(), ld_w if N > 1 else K, stride_w, N,
-        _whole(bias, "bias", dtype, (E, N)), *_epilogue(delta, residual, dtype, n, N, width), _activation(activation),
+        _whole(bias, "bias", dtype, (E, N), here), *_epilogue(delta, residual, dtype, n, N, width, here), _activation(activation),
         1 if gated else 0, _DTYPES[dtype], ws, ws_bytes, _err_at(err), raw))
