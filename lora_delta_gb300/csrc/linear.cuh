@@ -249,7 +249,7 @@ __global__ void __launch_bounds__(C::THREADS, 2) linear_few_kernel(const LinearA
   // What the call before writes is not read ahead of the wait, but W may come to L2
   // (a product of one group knows its part; up to 48 MB of all CTAs' parts).
   if (warp == 0 && !a.seg_start && blockIdx.z == 0) {
-    const int most = max(1, (48 << 20) / (int)(gridDim.x * C::W));
+    const int most = max(1, (int)((48ll << 20) / ((int64_t)gridDim.x * C::W)));
     for (int i = lane; i < min(nkb, most); i += 32) {
       tma_prefetch_3d(&map_w, (kb0 + i) * 64, ft * (a.gated ? 64 : 128), 0);
       if (a.gated) tma_prefetch_3d(&map_w, (kb0 + i) * 64, a.n_out + ft * 64, 0);
@@ -579,32 +579,6 @@ __device__ __forceinline__ void barrier_sync(int id, int threads) {
   asm volatile("barrier.cta.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
 
-struct PairTile {
-  int g, row0, rows, ft;
-};
-
-// Tile t of all: row tiles in blocks of `band`, in a block by feature tile.
-__device__ __forceinline__ PairTile pair_tile(const LinearArgs& a, const int32_t* pre, int t, int features, int band) {
-  const int total = pre[a.groups], b = t / (band * features), in = t - b * band * features;
-  const int width = min(band, total - b * band);
-  PairTile p;
-  p.ft = in / width;
-  const int rt = b * band + in - p.ft * width;
-  int lo = 0, hi = a.groups;
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (pre[mid] <= rt) lo = mid; else hi = mid;
-  }
-  p.g = lo;
-  uint32_t bad = 0;
-  const int2 seg = group_rows(a, lo, bad);
-  const int units = (seg.y - seg.x + Pair::UNIT - 1) / Pair::UNIT, tiles = pre[lo + 1] - pre[lo], i = rt - pre[lo];
-  const int u0 = (int)((int64_t)units * i / tiles), u1 = (int)((int64_t)units * (i + 1) / tiles);
-  p.row0 = seg.x + u0 * Pair::UNIT;
-  p.rows = min(seg.y, seg.x + u1 * Pair::UNIT) - p.row0;
-  return p;
-}
-
 // Where part x of a shared tile lies: [2 slots][2 CTAs][8 warps][128 columns][32
 // rows of W] a pair; a pair has the first steps of one shared tile at most (slot 1)
 // and later ones of one (slot 0).
@@ -715,15 +689,15 @@ __global__ void __launch_bounds__(Pair::THREADS, 1) linear_pair_kernel(const Lin
   // it is no longer needed, back.  After a wait that gave up a role passes on
   // without work; these waits end since every role's do.
   uint32_t n = 0;  // items so far
+  bool ok = true;
   auto take = [&]() -> bool {
-    if (!mbar_wait_soon(&item_full[n % C::ITEMS], (n / C::ITEMS) & 1, 4 * kWaitLimitNs)) return false;
+    if (!mbar_wait_soon(&item_full[n % C::ITEMS], (n / C::ITEMS) & 1, 4 * kWaitLimitNs)) return ok = false;
     p = items[n % C::ITEMS];
     return p.parts > 0;
   };
   auto pass = [&]() {  // (by one thread)
     mbar_arrive(&item_empty[n % C::ITEMS]);
   };
-  bool ok = true;
   if (warp == 0) {
     // ------------------------------------------------------------------ load
     if (lane == 0) {
@@ -824,7 +798,8 @@ __global__ void __launch_bounds__(Pair::THREADS, 1) linear_pair_kernel(const Lin
       const int cols = (p.rows + 63) / 64 * 64, c0 = side * cols / 2, c1 = min(c0 + cols / 2, p.rows);
       const int col = p.ft * per_pair + (int)rank * (per_pair / 2) + (GATED ? q & 1 : q) * 32 + block * 8;
       // delta and residual on their way to L2 while the products run: 64 bytes a row,
-      // half of the rows for the warps that work together (1023 rows down 109 -> 98 us)
+      // half of the rows for the warps that work together (read from there as each part
+      // begins; into registers a part ahead instead, 1023 rows down 111 us for 103)
       if (EXTRA) {
         const int first = col - block * 8;
         for (int r = c0 + lane + (GATED ? (q >> 1) * 32 : 0); r < c1 && first < a.n_out; r += GATED ? 64 : 32) {
@@ -861,6 +836,7 @@ __global__ void __launch_bounds__(Pair::THREADS, 1) linear_pair_kernel(const Lin
               for (int i = 0; i < 32; ++i) __stcg(own + (c - c0 + i) * 32, v[i]);
             }
           __threadfence();
+          fence_proxy_async_global();  // (the part may be read by a bulk copy)
           barrier_sync(bar, 64);
           last = true;
           if (counts) {
@@ -886,6 +862,7 @@ __global__ void __launch_bounds__(Pair::THREADS, 1) linear_pair_kernel(const Lin
               const int count = min(step, c0 + cols / 2 - c);
               __syncwarp();
               if (lane == 0) {
+                fence_proxy_async_global();
                 mbar_arrive_expect_tx(&part_full[ew], others * count * 128);
                 for (int x = 0, at = 0; x < p.parts; ++x)
                   if (x != p.part) bulk_g2s(room + at++ * step * 32, part_of(a, p, x, rank, ew) + (c - c0) * 32, count * 128, &part_full[ew]);
