@@ -306,9 +306,13 @@ __global__ void __launch_bounds__(C::THREADS, 2) linear_few_kernel(const LinearA
             for (int q = 0; q < 4; ++q) tc::mma_bf16(tmem, wd + q * 2, xd + q * 2, id, i > 0 || q > 0);
             tc::mma_commit(&empty[s]);
           }
-          // (every product issued is awaited, a failed loop's too)
+          // (every product issued is awaited, after a wait that gave up too: they write
+          // to the tensor memory that is freed below)
           tc::mma_commit(&done);
-          if (!mbar_wait_soon(&done, tiles & 1, ok ? a.wait_ns : kWaitLimitNs)) ok = false;
+          if (!ok || !mbar_wait_soon(&done, tiles & 1, a.wait_ns)) {
+            ok = false;
+            mbar_wait_bounded(&done, tiles & 1, kWaitLimitNs);
+          }
         }
       }
       dead = !__syncthreads_and(ok);

@@ -686,3 +686,29 @@ def test_gradients_of_a_loss_through_dispatch_and_combine(ld):
         size = np.abs(g64[i[0]] * x64[i[0]] * c64[r]).sum() if r >= 0 else 0.0
         # one rounding to bf16, of y
         assert abs((loss(x64, w64 + d) - loss(x64, w64 - d)) / (2 * step) - host(grad_w)[i]) <= 1.1 * 2.0 ** -8 * size + 1e-6
+
+
+@gpu
+@pytest.mark.parametrize("n,K,gated", [(1, 64, False), (16, 128, True), (128, 64, False)])
+def test_products_are_awaited_after_a_wait_that_gave_up(ld, n, K, gated):
+    """Sums so short that the wait for the last products is the likeliest to give up: it is reported, they are awaited all the
+    same before their tensor memory is freed, and the calls that take it next are whole."""
+    rng = np.random.default_rng(61)
+    x, w = normal(rng, torch.bfloat16, n, K), normal(rng, torch.bfloat16, 2048, K)
+    want, out = torch.empty(2, n, 1024 if gated else 2048, device="cuda").bfloat16()
+    ld.lora_linear(want, x, w, gated=gated)
+    reference, bound = ref.linear(host(x), host(w), gated=gated)
+    close(host(want), reference, bound, torch.bfloat16)
+    err = ld.new_error_word()
+    for limit in (0, 0, 0, 1, 1000, 5000):
+        old = ld.lora_set_wait_limit_ns(limit)
+        try:
+            ld.lora_linear(out, x, w, gated=gated, err=err)
+        finally:
+            ld.lora_set_wait_limit_ns(old)
+        bits = ld.lora_get_error(err)
+        assert bits == 8 or (bits == 0 and torch.equal(out, want))
+        for _ in range(3):
+            out.fill_(3)
+            ld.lora_linear(out, x, w, gated=gated, err=err)
+        assert ld.lora_get_error(err) == 0 and torch.equal(out, want)
