@@ -589,9 +589,27 @@ __device__ __forceinline__ void barrier_sync(int id, int threads) {
 __device__ __forceinline__ float* part_of(const LinearArgs& a, const PairItem& p, int x, uint32_t rank, int warp) {
   return a.parts + ((int64_t)((p.head + x) * 2 + (x == 0)) * 2 + rank) * Pair::PART + warp * 128 * 32;
 }
+// How many pairs have come to a shared tile, of the warps that meet at barrier `bar`.
+__device__ __forceinline__ uint32_t* count_of(const LinearArgs& a, const PairItem& p, uint32_t rank, int bar) {
+  return a.counters + (p.head * 2 + (int)rank) * 4 + bar - 1;
+}
+
+// Counts a pair's shared tiles from item `n` on, without finishing any: for warps that
+// leave after a wait for an item gave up, so that the counters end at zero all the same.
+// (Not inlined: it is reached after a failure only, and the epilogue has no registers left.)
+__device__ __noinline__ void count_rest(const LinearArgs& a, const int2* pre, int features, uint32_t n, uint32_t rank, int bar) {
+  PairWalk walk(a, pre, features, gridDim.x / 2, blockIdx.x / 2);
+  walk.start();
+  PairItem p;
+  for (uint32_t i = 0; walk.next(p); ++i) {
+    if (i < n || p.parts < 2) continue;
+    uint32_t* count = count_of(a, p, rank, bar);
+    if (atomicAdd(count, 1u) + 1 == (uint32_t)p.parts) *count = 0;
+  }
+}
 
 template <bool BF16, bool GATED, int EXTRA>
-__global__ void __launch_bounds__(Pair::THREADS, 1) linear_pair_kernel(const LinearArgs a, const __grid_constant__ CUtensorMap map_w,
+__global__ void __launch_bounds__(Pair::THREADS, 1) linear_pair_kernel(const __grid_constant__ LinearArgs a, const __grid_constant__ CUtensorMap map_w,
                                                                        const __grid_constant__ RowMaps maps_x) {
   using C = Pair;
   extern __shared__ uint8_t pair_smem_raw[];
@@ -691,11 +709,12 @@ __global__ void __launch_bounds__(Pair::THREADS, 1) linear_pair_kernel(const Lin
   const uint32_t tmem = taddr_s;
   // An item from the warp that lays them out (false: there are no more) and, once
   // it is no longer needed, back.  After a wait that gave up a role passes on
-  // without work; these waits end since every role's do.
+  // without work, and leaves where it was one for an item.
   uint32_t n = 0;  // items so far
   bool ok = true;
+  auto come = [&]() -> bool { return mbar_wait_soon(&item_full[n % C::ITEMS], (n / C::ITEMS) & 1, a.wait_ns); };
   auto take = [&]() -> bool {
-    if (!mbar_wait_soon(&item_full[n % C::ITEMS], (n / C::ITEMS) & 1, 4 * kWaitLimitNs)) return ok = false;
+    if (!come()) return ok = false;
     p = items[n % C::ITEMS];
     return p.parts > 0;
   };
@@ -776,7 +795,7 @@ __global__ void __launch_bounds__(Pair::THREADS, 1) linear_pair_kernel(const Lin
       for (bool more = true; more; ++n) {  // (the first is laid out already)
         if (n > 0 && !walk.next(p)) p.parts = 0;
         more = p.parts > 0;
-        if (n >= C::ITEMS && !mbar_wait_bounded(&item_empty[n % C::ITEMS], (n / C::ITEMS - 1) & 1, 4 * kWaitLimitNs)) {
+        if (n >= C::ITEMS && !mbar_wait_bounded(&item_empty[n % C::ITEMS], (n / C::ITEMS - 1) & 1, a.wait_ns)) {
           ok = false;
           break;
         }
@@ -794,9 +813,19 @@ __global__ void __launch_bounds__(Pair::THREADS, 1) linear_pair_kernel(const Lin
     constexpr int MINE = GATED ? 2 : 4;  // of 32 rows, a lane's, 8 apart
     const int block = lane % 4, my_row = (GATED ? (q >> 1) * 16 : 0) + lane / 4;
     const uint32_t leader_empty = dsmem_map(smem_addr(acc_empty), 0);
+    const bool counts = q < 2 && lane == 0;  // (one thread of the warps that work together)
     // (after a wait that gave up, shared tiles are still counted, so that the
     // counters end at zero)
-    for (; __all_sync(0xffffffffu, take()); ++n) {
+    for (;; ++n) {
+      // (the warps that work together take an item, or leave, together: one alone
+      // would wait for the other without end)
+      if (!barrier_and(bar, 64, come())) {
+        ok = false;
+        if (counts && a.counters) count_rest(a, pre, features, n, rank, bar);
+        break;
+      }
+      p = items[n % C::ITEMS];
+      if (p.parts == 0) break;
       __syncwarp();
       if (lane == 0) pass();
       const int cols = (p.rows + 63) / 64 * 64, c0 = side * cols / 2, c1 = min(c0 + cols / 2, p.rows);
@@ -823,8 +852,7 @@ __global__ void __launch_bounds__(Pair::THREADS, 1) linear_pair_kernel(const Lin
       if (p.parts > 1) {
         // The last to come finishes the tile.  Who finds all others there need
         // not write a part; else it writes, and may be the last all the same.
-        uint32_t* count = a.counters + (p.head * 2 + (int)rank) * 4 + bar - 1;
-        const bool counts = q < 2 && lane == 0;
+        uint32_t* count = count_of(a, p, rank, bar);
         bool last = true;
         if (counts) {
           last = atomicAdd(count, 0u) + 1 == (uint32_t)p.parts;

@@ -712,3 +712,49 @@ def test_products_are_awaited_after_a_wait_that_gave_up(ld, n, K, gated):
             out.fill_(3)
             ld.lora_linear(out, x, w, gated=gated, err=err)
         assert ld.lora_get_error(err) == 0 and torch.equal(out, want)
+
+
+@gpu
+@pytest.mark.parametrize("n,K,N,gated", [(300, 8192, 512, False), (1090, 4096, 1296, True), (5000, 72, 2064, False), (3000, 1024, 4096, True)])
+def test_counters_end_at_zero_after_waits_that_gave_up(ld, n, K, N, gated):
+    """Limits so short that any wait of a product may give up, those for the next item of work among them: the call ends, reports
+    it or is whole, leaves the counters of shared tiles at zero, and the next call with the same workspace is whole."""
+    rng = np.random.default_rng(62)
+    x, w, ws = normal(rng, torch.bfloat16, n, K), normal(rng, torch.bfloat16, N, K), ld.lora_linear_workspace()
+    want, out = torch.empty(2, n, N // 2 if gated else N, device="cuda").bfloat16()
+    ld.lora_linear(want, x, w, gated=gated, workspace=ws)
+    counters, err = ws[:int(ld.lib().lora_linear_zeroed_bytes())], ld.new_error_word()
+    for limit in (0, 0, 1, 2000, 5000, 20000, 50000):
+        old = ld.lora_set_wait_limit_ns(limit)
+        try:
+            ld.lora_linear(out, x, w, gated=gated, workspace=ws, err=err)
+        finally:
+            ld.lora_set_wait_limit_ns(old)
+        bits = ld.lora_get_error(err)
+        assert bits == 8 or (bits == 0 and torch.equal(out, want))
+        assert not counters.any()
+        out.fill_(3)
+        ld.lora_linear(out, x, w, gated=gated, workspace=ws, err=err)
+        assert ld.lora_get_error(err) == 0 and torch.equal(out, want)
+
+
+@gpu
+def test_experts_after_waits_that_gave_up(ld):
+    """The same over experts of uneven sizes."""
+    rng, T, k, E, K, N = np.random.default_rng(63), 900, 4, 12, 1024, 784
+    plan, x, _ = dispatched(ld, route(rng, T, k, E, none=0.1, skew=True), E, normal(rng, torch.bfloat16, T, K))
+    w, ws, err = normal(rng, torch.bfloat16, E, N, K), ld.lora_linear_workspace(), ld.new_error_word()
+    want, out = torch.zeros(2, T * k, N, device="cuda").bfloat16()
+    ld.lora_moe_linear(want, x, w, plan, workspace=ws, err=err)
+    for limit in (0, 0, 1, 2000, 5000, 20000):
+        old = ld.lora_set_wait_limit_ns(limit)
+        try:
+            ld.lora_moe_linear(out, x, w, plan, workspace=ws, err=err)
+        finally:
+            ld.lora_set_wait_limit_ns(old)
+        bits = ld.lora_get_error(err)
+        assert bits == 8 or (bits == 0 and torch.equal(out, want))
+        assert not ws[:int(ld.lib().lora_linear_zeroed_bytes())].any()
+        out.zero_()
+        ld.lora_moe_linear(out, x, w, plan, workspace=ws, err=err)
+        assert ld.lora_get_error(err) == 0 and torch.equal(out, want)
