@@ -785,9 +785,9 @@ __global__ void __launch_bounds__(Pair::THREADS, 1) linear_pair_kernel(const __g
         }
         if (ok) commit(&acc_full[n & 1], 3);
       }
-      // (every product issued is awaited before tensor memory is freed)
+      // (every product issued is awaited before tensor memory is freed, whatever the limit)
       commit(&drain, 1);
-      if (!mbar_wait_bounded(&drain, 0, kWaitLimitNs)) ok = false;
+      if (!mbar_wait_bounded(&drain, 0, max(a.wait_ns, (uint64_t)kWaitLimitNs))) ok = false;
     }
   } else if (warp == 3) {
     // ----------------------------------------------------------------- items
@@ -899,7 +899,12 @@ __global__ void __launch_bounds__(Pair::THREADS, 1) linear_pair_kernel(const __g
                 for (int x = 0, at = 0; x < p.parts; ++x)
                   if (x != p.part) bulk_g2s(room + at++ * step * 32, part_of(a, p, x, rank, ew) + (c - c0) * 32, count * 128, &part_full[ew]);
               }
-              ok = __all_sync(0xffffffffu, mbar_wait_soon(&part_full[ew], ((c - c0) / step) & 1, 4 * kWaitLimitNs)) && ok;
+              const uint32_t parity = ((c - c0) / step) & 1;
+              ok = __all_sync(0xffffffffu, mbar_wait_soon(&part_full[ew], parity, a.wait_ns));
+              if (!ok) {  // (what is on its way to the CTA's memory is awaited all the same)
+                mbar_wait_bounded(&part_full[ew], parity, kWaitLimitNs);
+                break;
+              }
               from_c = c;
               ready += step;
             }
@@ -928,6 +933,7 @@ __global__ void __launch_bounds__(Pair::THREADS, 1) linear_pair_kernel(const __g
             tc::tmem_st16(acc + c + 16, reinterpret_cast<const uint32_t*>(sum + 16));
           }
           tc::tmem_wait_st();
+          finish = barrier_and(bar, 64, ok);
         }
       }
       if (finish) {

@@ -758,3 +758,31 @@ def test_experts_after_waits_that_gave_up(ld):
         out.zero_()
         ld.lora_moe_linear(out, x, w, plan, workspace=ws, err=err)
         assert ld.lora_get_error(err) == 0 and torch.equal(out, want)
+
+
+@gpu
+@pytest.mark.parametrize("n,K,N", [(300, 8192, 512), (1023, 6144, 2560), (256, 16384, 512), (8192, 4096, 4096)])
+def test_waits_for_parts_of_shared_tiles_follow_the_limit(ld, n, K, N):
+    """Tiles shared by two pairs of CTAs, by a few and by many, and behind whole rounds of tiles, with limits down to none: a
+    call that does not report a wait is whole, one that does leaves the counters at zero."""
+    rng = np.random.default_rng(64)
+    x, w, ws = normal(rng, torch.float16, n, K), normal(rng, torch.float16, N, K, std=K ** -0.5), ld.lora_linear_workspace()
+    want, out = torch.empty(2, n, N, device="cuda").half()
+    err = ld.new_error_word()
+    ld.lora_linear(want, x, w, workspace=ws, err=err)
+    assert ld.lora_get_error(err) == 0
+    if n < 2000:
+        reference, bound = ref.linear(host(x), host(w))
+        close(host(want), reference, bound, torch.float16)
+    for limit in [0] + [300 * 2 ** (i / 2) for i in range(20)]:
+        out.fill_(3)
+        old = ld.lora_set_wait_limit_ns(int(limit))
+        try:
+            ld.lora_linear(out, x, w, workspace=ws, err=err)
+        finally:
+            ld.lora_set_wait_limit_ns(old)
+        bits = ld.lora_get_error(err)
+        assert bits == 8 or (bits == 0 and torch.equal(out, want))
+        assert not ws[:int(ld.lib().lora_linear_zeroed_bytes())].any()
+    ld.lora_linear(out, x, w, workspace=ws, err=err)
+    assert ld.lora_get_error(err) == 0 and torch.equal(out, want)
