@@ -52,9 +52,36 @@ __device__ __forceinline__ int2 group_rows(const LinearArgs& a, int g, uint32_t&
   return make_int2(s1, min(max(e, s1), a.n));
 }
 
-// Of N values.  gelu by tanh is z / (1 + exp(-2 u)), as silu with 2 u for z.  (Few
-// instructions matter more than the time they take: the roles of a CTA run at once
-// and fetch theirs side by side.)
+// 1 / x for x in [1, 8]: within 2^-23 of it.
+__device__ __forceinline__ float rcp_near(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// gelu of a value: z / 2 erfc(-z / sqrt 2) = max(z, 0) - a G e^(-a^2 / 2) with a = |z| and
+// G = erfcx(a / sqrt 2) / 2, so that nothing cancels in the lower tail, where z / 2 (1 + erf)
+// keeps no digit from -5.5 on.  G is a polynomial in t = 1 / (1 + 0.3 a), fitted by weighted
+// least squares to within 1.5e-7 of it from 0 to 14, where the result leaves float32.  The
+// power is the square of that of half its exponent, so that its underflow is the result's.
+// With CUDA's erfcf in its place 8192 rows of 4096 by 28672 took 1255 us for 1139 to 1181,
+// gated 1155 for 1114.
+__device__ __forceinline__ float gelu_erf(float z) {
+  const float a = fminf(fabsf(z), 20.0f), t = rcp_near(fmaf(a, 0.3f, 1.0f));
+  float g = 0.03567515f;
+  g = fmaf(g, t, -0.15720464f);
+  g = fmaf(g, t, 0.20635618f);
+  g = fmaf(g, t, -0.053686097f);
+  g = fmaf(g, t, 0.12856292f);
+  g = fmaf(g, t, 0.099913100f);
+  g = fmaf(g, t, 0.12075402f);
+  g = fmaf(g, t, 0.11962929f);
+  const float h = exp2_fast(a * a * -0.36067376f);  // e^(-a^2 / 4)
+  return fmaf(-(a * (g * t) * h), h, z < 0.0f ? 0.0f * z : z);
+}
+
+// Of N values.  (Few instructions matter more than the time they take: the roles of a
+// CTA run at once and fetch theirs side by side.)
 template <int N>
 __device__ __forceinline__ void activate(float* z, int act) {
   if (act == LORA_ACT_NONE) return;
@@ -63,7 +90,7 @@ __device__ __forceinline__ void activate(float* z, int act) {
     for (int i = 0; i < N; ++i) z[i] = z[i] < 0.0f ? 0.0f : z[i];
   } else if (act == LORA_ACT_GELU) {
 #pragma unroll
-    for (int i = 0; i < N; ++i) z[i] = 0.5f * z[i] * (1.0f + erff(z[i] * 0.70710678f));
+    for (int i = 0; i < N; ++i) z[i] = gelu_erf(z[i]);
   } else {
     const float cubic = act == LORA_ACT_SILU ? 0.0f : 2.0f * 0.79788456f * 0.044715f;
     const float linear = act == LORA_ACT_SILU ? 1.0f : 2.0f * 0.79788456f;

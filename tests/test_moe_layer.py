@@ -9,6 +9,7 @@ products as ``moe_ref.linear`` derives it.  Below the normal range a step is abs
 from __future__ import annotations
 
 import ctypes
+import math
 
 import numpy as np
 import pytest
@@ -786,3 +787,38 @@ def test_waits_for_parts_of_shared_tiles_follow_the_limit(ld, n, K, N):
         assert not ws[:int(ld.lib().lora_linear_zeroed_bytes())].any()
     ld.lora_linear(out, x, w, workspace=ws, err=err)
     assert ld.lora_get_error(err) == 0 and torch.equal(out, want)
+
+
+def activation_alone(z, act):
+    """An activation in 64 bits with nothing that cancels, and how far float32 may be from it relative to it.
+
+    Of 2^-19: two powers 2^-22 each, a reciprocal 2^-23, a polynomial's fit and some ten roundings 2^-24 each.  The power's
+    exponent is rounded 2^-24 relative, twice and in its constant, so that its value is off by the exponent times 2^-23 at most."""
+    if act == "gelu":
+        return 0.5 * z * np.vectorize(math.erfc)(-z / math.sqrt(2)), 2.0 ** -19 + z * z * 2.0 ** -23
+    raise ValueError(act)
+
+
+@gpu
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("act", ["gelu"])
+@pytest.mark.parametrize("n", [1, 130])
+@pytest.mark.parametrize("gated", [False, True])
+def test_activations_of_every_number(ld, dtype, act, n, gated):
+    """An activation of each 16-bit number, brought by the bias, to its own rounding: in the tails too, down to where the result
+    leaves its type."""
+    z = torch.arange(-2 ** 15, 2 ** 15, dtype=torch.int32, device="cuda").to(torch.int16).view(dtype)
+    bias = torch.cat([z, torch.ones_like(z)]) if gated else z
+    x, w = torch.zeros(n, 8, device="cuda", dtype=dtype), torch.zeros(len(bias), 8, device="cuda", dtype=dtype)
+    out, err = torch.empty(n, len(z), device="cuda", dtype=dtype), ld.new_error_word()
+    ld.lora_linear(out, x, w, bias=bias, activation=act, gated=gated, err=err)
+    assert ld.lora_get_error(err) == 0
+    assert torch.equal(out.view(torch.int16), out[:1].view(torch.int16).expand_as(out))
+    got, z = host(out[0]), host(z)
+    assert np.isnan(got[np.isnan(z)]).all() and (got[z == np.inf] == np.inf).all()
+    there = np.isfinite(z)
+    want, off = activation_alone(z[there], act)
+    # (what float32 itself may be off by below its normal range is less than a tenth of a step of bf16 there)
+    tiny = 2.0 ** -25 if dtype is torch.float16 else 1.1 * 2.0 ** -134
+    worst = np.abs(got[there] - want) - (STEP[dtype] * (1 + off) + off) * np.abs(want) - tiny
+    assert (worst <= 0).all(), (z[there][worst.argmax()], got[there][worst.argmax()], want[worst.argmax()])
