@@ -80,6 +80,15 @@ __device__ __forceinline__ float gelu_erf(float z) {
   return fmaf(-(a * (g * t) * h), h, z < 0.0f ? 0.0f * z : z);
 }
 
+// z / (1 + e^-t), where t has z's sign: silu (t = z) and gelu by tanh (t = 2 u).  With
+// e = e^-|t| it is z / (1 + e) or z e / (1 + e), so that the divisor is 1 to 2 and, for far
+// negative t, the value leaves float32 no earlier than it has to (z / (1 + e^-t) is 0 from
+// -87.4 on, where bf16 holds it to -97).
+__device__ __forceinline__ float times_sigmoid(float z, float t) {
+  const float h = exp2_fast(fabsf(t) * -0.72134752f);  // e^(-|t| / 2)
+  return (t < 0.0f ? z * h * h : z) * rcp_near(fmaf(h, h, 1.0f));
+}
+
 // Of N values.  (Few instructions matter more than the time they take: the roles of a
 // CTA run at once and fetch theirs side by side.)
 template <int N>
@@ -95,10 +104,7 @@ __device__ __forceinline__ void activate(float* z, int act) {
     const float cubic = act == LORA_ACT_SILU ? 0.0f : 2.0f * 0.79788456f * 0.044715f;
     const float linear = act == LORA_ACT_SILU ? 1.0f : 2.0f * 0.79788456f;
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const float t = z[i] * (cubic == 0.0f ? linear : fmaf(cubic * z[i], z[i], linear));
-      z[i] = __fdividef(z[i], 1.0f + __expf(-t));
-    }
+    for (int i = 0; i < N; ++i) z[i] = times_sigmoid(z[i], z[i] * (cubic == 0.0f ? linear : fmaf(cubic * z[i], z[i], linear)));
   }
 }
 

@@ -796,12 +796,15 @@ def activation_alone(z, act):
     exponent is rounded 2^-24 relative, twice and in its constant, so that its value is off by the exponent times 2^-23 at most."""
     if act == "gelu":
         return 0.5 * z * np.vectorize(math.erfc)(-z / math.sqrt(2)), 2.0 ** -19 + z * z * 2.0 ** -23
-    raise ValueError(act)
+    # z / (1 + e^-t), t for gelu_tanh of four roundings 2^-24 and constants' 2^-24 more, which the exponent takes whole
+    t = z if act == "silu" else 2 * math.sqrt(2 / math.pi) * (z + 0.044715 * z ** 3)
+    e = np.exp(-np.abs(t))
+    return np.where(t < 0, z * e, z) / (1 + e), 2.0 ** -19 + np.abs(t) * (2.0 ** -23 if act == "silu" else 2.0 ** -21)
 
 
 @gpu
 @pytest.mark.parametrize("dtype", TYPES)
-@pytest.mark.parametrize("act", ["gelu"])
+@pytest.mark.parametrize("act", ["gelu", "silu", "gelu_tanh"])
 @pytest.mark.parametrize("n", [1, 130])
 @pytest.mark.parametrize("gated", [False, True])
 def test_activations_of_every_number(ld, dtype, act, n, gated):
