@@ -182,13 +182,19 @@ int linear_call(LinearArgs& a, int dtype, void* workspace, size_t ws_bytes, cuda
   if (!aligned16(a.bias) || !aligned4(a.seg_start) || !aligned4(a.err)) return LORA_ERR_ALIGN;
   const bool in_place = a.residual == a.out && (a.ld_residual == a.ld_out || a.n == 1);
   const Mat all_w = {a.w, 0, 1, (int64_t)(a.groups - 1) * a.stride_w + (int64_t)(a.N - 1) * a.ld_w + a.K};
-  if (share(out, x) || share(out, a.groups > 1 ? all_w : w) || (a.delta && share(out, delta)) ||
-      (a.residual && !in_place && share(out, res)) ||
-      (a.bias && share(out, Mat{a.bias, 0, 1, (int64_t)a.groups * a.N})) || shares_words(out, a.seg_start, a.groups + 1))
-    return LORA_ERR_ARG;
+  const Mat in[] = {x, a.groups > 1 ? all_w : w, delta, {a.bias, 0, 1, (int64_t)a.groups * a.N}, {a.seg_start, 0, 1, 2 * (a.groups + 1)}};
+  const Mat err = {a.err, 0, 1, 2};
+  for (const Mat& m : in)
+    if (share(out, m) || share(err, m)) return LORA_ERR_ARG;
+  if ((!in_place && share(out, res)) || share(err, res) || share(err, out)) return LORA_ERR_ARG;
   if (workspace) {
-    if (ws_bytes < lora_linear_workspace_size(a.n, a.groups)) return LORA_ERR_WORKSPACE;
+    const size_t need = lora_linear_workspace_size(a.n, a.groups);
+    if (ws_bytes < need) return LORA_ERR_WORKSPACE;
     if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return LORA_ERR_ALIGN;
+    const Mat ws = {workspace, 0, need > 0, (int64_t)(need / 2)};
+    for (const Mat& m : in)
+      if (share(ws, m)) return LORA_ERR_ARG;
+    if (share(ws, res) || share(ws, out) || share(ws, err)) return LORA_ERR_ARG;
     a.counters = reinterpret_cast<uint32_t*>(workspace);
     a.parts = reinterpret_cast<float*>(reinterpret_cast<char*>(workspace) + kLinearCounterBytes);
   }
@@ -218,10 +224,10 @@ int lora_moe_dispatch(void* rows, int64_t ld_rows, int32_t* seg_start, int32_t* 
   for (int i = 0; i < 9; ++i) {
     if (!aligned4(words[i])) return LORA_ERR_ALIGN;
     if (T > 0 && shares_words(Mat{rows, ld_rows, P, H}, words[i], sizes[i])) return LORA_ERR_ARG;
-    for (int j = 0; j < 5 && j < i; ++j)  // an output of the plan and any other array
-      if (words[i] && words[j] && sizes[j] > 0 && shares_words(Mat{words[i], 0, sizes[i] > 0, 2 * sizes[i]}, words[j], sizes[j]))
+    for (int j = 0; j < i; ++j)  // an output of the plan, or the error word, and any other array
+      if ((j < 5 || i == 8) && words[i] && words[j] && sizes[j] > 0 && shares_words(Mat{words[i], 0, sizes[i] > 0, 2 * sizes[i]}, words[j], sizes[j]))
         return LORA_ERR_ARG;
-    if (i < 5 && T > 0 && shares_words(Mat{x, ld_x, T, H}, words[i], sizes[i])) return LORA_ERR_ARG;
+    if ((i < 5 || i == 8) && T > 0 && shares_words(Mat{x, ld_x, T, H}, words[i], sizes[i])) return LORA_ERR_ARG;
   }
   if (T > 0 && share(Mat{rows, ld_rows, P, H}, Mat{x, ld_x, T, H})) return LORA_ERR_ARG;
   const MoePlanArgs p = {{topk_ids, expert_map, n_global_experts, E}, lora_ids, P, top_k, seg_start, row_pair, pair_row,

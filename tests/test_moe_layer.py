@@ -123,6 +123,48 @@ def test_refusals_on_the_host():
     assert linear(n=2 ** 30 + 1) == unsup and linear(E=1025) == unsup and linear(E=3, seg=at[0]) == arg
 
 
+def test_refusals_of_shared_workspaces_and_error_words():
+    """The workspace and the error word are written too: no argument may lie in them."""
+    import lora_delta_gb300 as ld
+    from lora_delta_gb300.build import build
+    build()
+    L = ld.lib()
+    base, n, E = 1 << 40, 1000, 3
+    at = {name: base + i * (1 << 30) for i, name in enumerate(("out", "x", "w", "bias", "delta", "res", "seg", "err", "work"))}
+    size = int(L.lora_linear_workspace_size(n, E))
+    assert size == int(L.lora_linear_workspace_size(n, 1)) > 1 << 20
+
+    def linear(experts, **other):
+        p = {k: ctypes.c_void_p(v) for k, v in {**at, **other}.items()}
+        if experts:
+            return L.lora_moe_linear(p["out"], 48, p["x"], 64, n, 64, p["seg"], E, p["w"], 64, 48 * 64, 48, p["bias"], p["delta"], 48,
+                                     p["res"], 48, 0, 0, 0, p["work"], size, p["err"], None)
+        return L.lora_linear(p["out"], 48, p["x"], 64, n, 64, p["w"], 64, 48, p["bias"], p["delta"], 48, p["res"], 48, 0, 0, 0, p["work"],
+                             size, p["err"], None)
+
+    last = {"out": 2 * n * 48, "x": 2 * n * 64, "delta": 2 * n * 48, "res": 2 * n * 48}
+    for experts in (False, True):
+        last.update(w=2 * (E if experts else 1) * 48 * 64, bias=2 * (E if experts else 1) * 48, seg=4 * (E + 1), err=4)
+        for name in at:
+            if name == "work" or (name == "seg" and not experts):
+                continue
+            # inside the workspace, and with its last bytes in the first of it
+            assert linear(experts, **{name: at["work"] + size - 256}) == 1, name
+            end = (last[name] - 4) // 256 * 256 if name != "err" else 0
+            assert linear(experts, work=at[name] + end) == 1, name
+            if name != "err":
+                assert linear(experts, err=at[name]) == 1 and linear(experts, err=at[name] + last[name] - 4) == 1, name
+        # the residual's excuse is its own
+        assert linear(experts, res=at["out"], x=at["out"]) == 1 and linear(experts, res=at["out"], err=at["out"] + 4) == 1
+
+    def dispatch(err):
+        p = [ctypes.c_void_p(base + i * (1 << 30)) for i in range(9)]
+        return L.lora_moe_dispatch(p[0], 64, p[1], p[2], p[3], p[4], p[5], p[6], 64, p[7], p[8], None, 0, 8, 2, 4, 64, ctypes.c_void_p(err), None)
+
+    for i in range(9):
+        assert dispatch(base + i * (1 << 30)) == 1, i
+
+
 def test_plans_are_made_on_the_gpu():
     import lora_delta_gb300 as ld
     with pytest.raises(ValueError):
