@@ -867,3 +867,107 @@ def test_activations_of_every_number(ld, dtype, act, n, gated):
     tiny = 2.0 ** -25 if dtype is torch.float16 else 1.1 * 2.0 ** -134
     worst = np.abs(got[there] - want) - (STEP[dtype] * (1 + off) + off) * np.abs(want) - tiny
     assert (worst <= 0).all(), (z[there][worst.argmax()], got[there][worst.argmax()], want[worst.argmax()])
+
+
+def layer_buffers(c):
+    P, dtype = c["T"] * c["k"], c["x"].dtype
+    names = {"rows": (P, c["H"]), "d13": (P, 1, 2 * c["I"]), "act": (P, c["I"]), "y": (P, c["H"]), "out": (c["T"], c["H"])}
+    c["ptr"] = pointers(c["a13"]), pointers(c["b13"]), pointers([c["a2"]])[0].contiguous(), pointers([c["b2"]])[0].contiguous()
+    c["d_ids"], c["d_lora"] = dev(c["ids"]), dev(c["lora"])
+    return {n: torch.zeros(*shape, dtype=dtype, device="cuda") for n, shape in names.items()}
+
+
+def run_layer_with_word(ld, c, b, plan, err):
+    """The layer's calls into buffers ``b``, each with the error word."""
+    P, R, H, I, kw = c["T"] * c["k"], c["rank"], c["H"], c["I"], {"err": err}
+    a13, b13, a2, b2 = c["ptr"]
+    ld.lora_moe_dispatch(b["rows"], c["x"], c["d_ids"], plan, lora_ids=c["d_lora"], **kw)
+    ids = plan.row_expert.view(P, 1)
+    ld.lora_moe_fc1_delta(b["d13"], b["rows"], a13, R * H, b13, I * R, False, ids, plan.row_lora, c["E"], I, R, c["L"], 2.0, **kw)
+    ld.lora_moe_linear(b["act"], b["rows"], c["w13"], plan, delta=b["d13"].view(P, -1), activation="silu", gated=True, **kw)
+    ld.lora_moe_linear(b["y"], b["act"], c["w2"], plan, **kw)
+    ld.lora_moe_w2_delta(b["y"].view(P, 1, H), b["act"], a2, R * I, b2, H * R, ids, plan.row_lora, c["E"], H, R, c["L"], 2.0, **kw)
+    ld.lora_moe_combine(b["out"], b["y"], plan, weights=c["w"], residual=c["x"])
+
+
+@gpu
+@pytest.mark.parametrize("T", [90, 400])
+def test_a_layer_reports_into_one_error_word(ld, T):
+    """No call of a layer reports anything, eager, on two streams at once or replayed; one that meets a bad expert does."""
+    cases = [layer_case(ld, 90 + i, T=T) for i in range(2)]
+    want = [run_layer(ld, c)["out"].clone() for c in cases]
+    buffers, plans = [layer_buffers(c) for c in cases], [ld.MoePlan(T, c["k"], c["E"]) for c in cases]
+    words, streams = [ld.new_error_word() for _ in cases], [torch.cuda.Stream() for _ in cases]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for c, b, plan, err, s in zip(cases, buffers, plans, words, streams):
+            with torch.cuda.stream(s):
+                run_layer_with_word(ld, c, b, plan, err)
+    torch.cuda.synchronize()
+    for b, y, err in zip(buffers, want, words):
+        assert ld.lora_get_error(err) == 0 and torch.equal(b["out"], y)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=streams[0]):
+        run_layer_with_word(ld, cases[0], buffers[0], plans[0], words[0])
+    for name in ("x", "w", "d_ids", "d_lora", "w13", "w2", "a2", "b2"):
+        cases[0][name].copy_(cases[1][name])
+    for name in ("a13", "b13"):
+        for t, u in zip(cases[0][name], cases[1][name]):
+            t.copy_(u)
+    torch.cuda.synchronize()
+    for _ in range(3):
+        graph.replay()
+    torch.cuda.synchronize()
+    assert ld.lora_get_error(words[0]) == 0 and torch.equal(buffers[0]["out"], want[1])
+    cases[0]["d_ids"][T // 2, 0] = cases[0]["E"]
+    torch.cuda.synchronize()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert ld.lora_get_error(words[0]) == ref.ERR_EXPERT
+    rest = [t for t in range(T) if t != T // 2]
+    assert torch.equal(buffers[0]["out"][rest], want[1][rest])
+
+
+@gpu
+@pytest.mark.parametrize("dtype", TYPES)
+def test_a_tokens_combine_and_gradient_alone(ld, dtype):
+    """Bit for bit what they are among other tokens."""
+    rng, T, k, E, H = np.random.default_rng(91), 37, 5, 9, 1032
+    plan, _, _ = dispatched(ld, route(rng, T, k, E, none=0.2), E, normal(rng, dtype, T, 8))
+    rows, g, res, w = normal(rng, dtype, T * k, H), normal(rng, dtype, T, H), normal(rng, dtype, T, H), dev(rng.standard_normal((T, k)), np.float32)
+    out, grad_rows, grad_w = torch.empty_like(g), torch.zeros_like(rows), torch.empty(T, k, device="cuda")
+    ld.lora_moe_combine(out, rows, plan, weights=w, residual=res)
+    ld.lora_moe_combine_grad(grad_rows, grad_w, g, rows, plan, weights=w)
+    for t in range(T):
+        # the token's rows first, in a plan of its own
+        there = plan.pair_row[t] >= 0
+        mine = torch.zeros(k, H, dtype=dtype, device="cuda")
+        mine[there] = rows[plan.pair_row[t][there].long()]
+        one = ld.MoePlan(1, k, E)
+        one.pair_row.copy_(torch.where(there, torch.arange(k, device="cuda"), -1).view(1, k))
+        y, gr, gw = torch.empty(1, H, dtype=dtype, device="cuda"), torch.zeros_like(mine), torch.empty(1, k, device="cuda")
+        ld.lora_moe_combine(y, mine, one, weights=w[t:t + 1], residual=res[t:t + 1])
+        ld.lora_moe_combine_grad(gr, gw, g[t:t + 1], mine, one, weights=w[t:t + 1])
+        assert torch.equal(y, out[t:t + 1]) and torch.equal(gw, grad_w[t:t + 1])
+        assert torch.equal(gr[there], grad_rows[plan.pair_row[t][there].long()])
+
+
+@gpu
+@pytest.mark.parametrize("T,k,E,K,N,gated", [(64, 8, 64, 512, 272, True), (400, 2, 3, 4096, 128, False), (2000, 4, 16, 64, 528, True)])
+def test_products_of_experts_repeat(ld, T, k, E, K, N, gated):
+    """Bit for bit the same again, with others between that leave their parts in the same workspace: few rows, tiles shared by
+    many pairs, whole rounds of tiles."""
+    rng = np.random.default_rng(92)
+    plan, x, _ = dispatched(ld, route(rng, T, k, max(E, k), none=0.1, skew=True) % E, E, normal(rng, torch.bfloat16, T, K))
+    w, other = normal(rng, torch.bfloat16, E, N, K, std=K ** -0.5), normal(rng, torch.bfloat16, 700, 2048)
+    wo, oo = normal(rng, torch.bfloat16, 512, 2048), torch.empty(700, 512, device="cuda").bfloat16()
+    want, out = torch.zeros(2, T * k, N // 2 if gated else N, device="cuda").bfloat16()
+    err = ld.new_error_word()
+    ld.lora_moe_linear(want, x, w, plan, gated=gated, err=err)
+    for i in range(12):
+        if i % 2:
+            ld.lora_linear(oo, other, wo, err=err)
+        out.fill_(0)
+        ld.lora_moe_linear(out, x, w, plan, gated=gated, err=err)
+        assert torch.equal(out, want)
+    assert ld.lora_get_error(err) == 0
