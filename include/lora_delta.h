@@ -25,6 +25,11 @@
  *    as stated per call and a LORA_DEV_ERR_* bit is OR-ed into the caller's
  *    `err_word` (a device uint32, may be NULL to ignore).  Read it with
  *    lora_get_error.
+ *  - Adapter weights, and the tables of their addresses and scales, are read
+ *    ahead of the end of the library call before on the stream: they must not
+ *    be what that call itself writes (a lora_linear into a pool slot, say).
+ *    Other work between the two, such as lora_pool_pack, a copy or a kernel of
+ *    the caller's, puts them in order.  Rows, ids and plans need none.
  *  - Alignment: k_in, every slice width, ld_out, offset_start and the pool
  *    rank R must be multiples of 8 elements (16 bytes of bf16), and x / out /
  *    h must be 16-byte aligned; otherwise LORA_ERR_ALIGN.  A pool address in a
@@ -578,8 +583,9 @@ int lora_kv4_attention(void *out, int64_t ld_out, const void *q, int64_t ld_q, i
  * None of the pages has these calls.  Matrices hold 16-bit values, row-major
  * with row strides ld in elements, multiples of 8 (of one row it does not
  * matter), 16-byte aligned; H, k_in, n_out are multiples of 8 (LORA_ERR_ALIGN).
- * No output may share memory with another argument (LORA_ERR_ARG), but for
- * `out` with `residual` as stated.  Columns of one buffer may interleave.
+ * No output, the workspace and the error word among them, may share memory with
+ * another argument (LORA_ERR_ARG), but for `out` with `residual` as stated.
+ * Columns of one buffer may interleave.
  * Limits: E <= 1024, top_k <= 64, T * top_k < 2^30, n <= 2^30 rows of a product
  * (LORA_ERR_UNSUPPORTED).
  */
@@ -654,8 +660,8 @@ int lora_moe_combine_grad(void *grad_rows, int64_t ld_grad_rows, float *grad_wei
  * workspace: lora_linear_workspace_size(n, 1) bytes (0, or some 42 MB at any size),
  * 256-byte aligned, or NULL: with it, tiles may be shared by several SMs along k_in
  * where there are not enough for all.  Its first lora_linear_zeroed_bytes() bytes must be
- * zero before its first use and are left zero; calls that may overlap (a graph's
- * replays among them) need workspaces of their own.
+ * zero before its first use and are left zero, after LORA_DEV_ERR_TIMEOUT too; calls that
+ * may overlap (a graph's replays among them) need workspaces of their own.
  */
 size_t lora_linear_workspace_size(int n, int groups);
 size_t lora_linear_zeroed_bytes(void);

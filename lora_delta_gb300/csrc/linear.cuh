@@ -193,8 +193,8 @@ __device__ __forceinline__ V linear_finish(const LinearArgs& a, const LinearBias
 // finishing its share of the tile.  Grid: (feature tile, part of K), group, and
 // row tiles in turn.  Two CTAs fit an SM.
 // Bound: W's bytes, and launch, first copies and the parts' way where they are few.  1 row
-// of 4096 by 6144 11.5 us (4.4 TB/s), 64 rows 14.3, 128 rows 17.0; 64 tokens of 8 experts,
-// 2048 by 1536 gated, 70.3 us (5.8 TB/s).  Parts read 32 bytes a thread instead of 16, so
+// of 4096 by 6144 12 us (4.2 TB/s), 64 rows 14.5, 128 rows 17.4; 64 tokens of 8 experts,
+// 2048 by 1536 gated, 67 to 74 us (5.5 to 6.1 TB/s).  Parts read 32 bytes a thread instead of 16, so
 // that a warp's lie apart: 64 rows 16.3, 128 rows 21.0 (from the CTA's own memory 13.0).
 // Tiles of 256 rows of x in this form lost to the pairs below, as the parts' way grows
 // with the rows (192 rows of 2048 by 2048 26 us, 17 there).
@@ -392,10 +392,11 @@ __global__ void __launch_bounds__(C::THREADS, 2) linear_few_kernel(const LinearA
 // items ahead, a load warp, an MMA warp (of the even CTA) and 8 epilogue warps, the
 // sums of one tile in one half of tensor memory while the epilogue reads the other's.
 // Bound: the tensor cores while K is long (8192 x 4096 by 28672 1045 to 1075 us, 1790
-// to 1840 TFLOP/s; gated with silu and delta 1060 to 1110; products without copies or an
+// to 1840 TFLOP/s; gated with silu and delta 1060 to 1120; products without copies or an
 // epilogue 1000, copies alone 875), W's bytes for the experts of few tokens (16384 rows
-// of 64 experts, 2048 by 1536 gated with delta: 106.5 us, 5.1 TB/s; without an epilogue
-// 88), and the epilogue where K is short (768 by 2048: 64 us, without one 48).  Tried:
+// of 64 experts, 2048 by 1536 gated with delta: 106 to 122 us, by the run; without an
+// epilogue 88), and the epilogue where K is short (768 by 2048: 63 to 74 us, without one
+// 48).  Tried:
 // descriptors from one lane 1086 us where the whole warp takes 1000 (products alone); six
 // stages and 16 columns of the epilogue at once, with flags instead of forms of the
 // kernel, 154 us for the experts' 106; erf and tanh inlined for every value 376 us where
@@ -464,6 +465,7 @@ struct PairWalk {
       // Shared, row tiles that use the same weights are no longer at the same place in
       // K, and weights that L2 does not hold meanwhile are read again (600 rows of 13824
       // by 5120: 71 us whole, 97 shared; 1023 rows, just above one tile a pair, 135 and 98).
+      // Between 9/8 of a round and two, sharing is not measured (1280 rows, 1.32: whole 134).
       const int left = tiles - t_end;
       const bool again = a.groups == 1 && width > 1 && (int64_t)(left / width) * (256 * 2) * a.K > (64 << 20) &&
                          (left < pairs || left * 8 > pairs * 9);

@@ -184,7 +184,8 @@ def lora_linear(out, x, weight, bias=None, delta=None, residual=None, activation
 
     ``x`` [n, k_in], ``weight`` [n_out, k_in], ``bias`` [n_out], ``delta`` [n, n_out] (what the LoRA calls leave: it goes
     ahead of the activation), all bfloat16 or all float16, and ``residual`` as ``out``, which it may be itself.  ``activation``:
-    "none", "relu", "silu", "gelu" (by erf) or "gelu_tanh"."""
+    "none", "relu", "silu", "gelu" (by erf) or "gelu_tanh".  No argument may lie in ``workspace`` or hold ``err``.  ``out`` may be
+    an adapter's weights only where other work on the stream comes between this call and the delta that reads them."""
     here = torch._C._cuda_getDevice()
     dtype, n = _rows_dtype(x, "x"), x.shape[0]
     if weight.dim() != 2:
