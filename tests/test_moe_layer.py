@@ -971,3 +971,47 @@ def test_products_of_experts_repeat(ld, T, k, E, K, N, gated):
         ld.lora_moe_linear(out, x, w, plan, gated=gated, err=err)
         assert torch.equal(out, want)
     assert ld.lora_get_error(err) == 0
+
+
+@gpu
+def test_offsets_beyond_32_bits(ld):
+    """Rows whose elements lie past 2^31: a dispatch, its way back with weights, its gradient, and products of them."""
+    T, k, E, H = 34000, 8, 16, 8192
+    rng = np.random.default_rng(95)
+    ids = dev(rng.permuted(np.tile(np.arange(E), (T, 1)), axis=1)[:, :k])
+    g = torch.Generator(device="cuda").manual_seed(95)
+    x = torch.randn(T, H, device="cuda", generator=g).bfloat16()
+    w = torch.rand(T, k, device="cuda", generator=g)
+    plan, rows, err = ld.MoePlan(T, k, E), torch.zeros(T * k, H, device="cuda").bfloat16(), ld.new_error_word()
+    assert rows.numel() > 2 ** 31
+    ld.lora_moe_dispatch(rows, x, ids, plan, err=err)
+    token = torch.div(plan.row_pair, k, rounding_mode="floor").long()
+    for a in range(0, T * k, 16384):
+        assert torch.equal(rows[a:a + 16384], x[token[a:a + 16384]])
+    out = torch.empty_like(x)
+    ld.lora_moe_combine(out, rows, plan, weights=w)
+    want = x[-500:].double() * w[-500:].double().sum(1, keepdim=True)
+    # (k additions in float32 of terms of one sign)
+    assert ((out[-500:].double() - want).abs() <= (2.0 ** -8 + (k + 2) * 2.0 ** -23) * want.abs() + 2.0 ** -134).all()
+    grad, grad_w = torch.zeros_like(rows), torch.empty(T, k, device="cuda")
+    ld.lora_moe_combine_grad(grad, grad_w, x, rows, plan, weights=w)
+    for a in (0, T * k - 16384):
+        t, p = token[a:a + 16384], plan.row_pair[a:a + 16384].long()
+        assert torch.equal(grad[a:a + 16384], (x[t].float() * w.view(-1)[p][:, None]).bfloat16())
+    # products: the many-rows kernel over all rows, in narrow columns of a wide result and to 8192 columns of it
+    weight = torch.randn(E, 256, H, device="cuda", generator=g).bfloat16() * H ** -0.5
+    y = torch.empty(T * k, 256, device="cuda").bfloat16()
+    ld.lora_moe_linear(y, rows, weight, plan, err=err)
+    ld.lora_linear(grad[:, -256:], rows, weight[3], delta=y, residual=y, err=err)
+    wide = torch.randn(H, 64, device="cuda", generator=g).bfloat16() / 8
+    ld.lora_linear(rows, y[:, :64], wide, err=err)
+    assert ld.lora_get_error(err) == 0
+    last, seg = slice(T * k - 300, T * k), host(plan.seg_start)
+    assert seg[E - 1] < T * k - 300
+    x64 = host(x[token[last]])
+    want, bound = ref.linear(x64, host(weight[E - 1]))
+    close(host(y[last]), want, bound, torch.bfloat16)
+    want, bound = ref.linear(x64, host(weight[3]), delta=host(y[last]), residual=host(y[last]))
+    close(host(grad[last, -256:]), want, bound, torch.bfloat16)
+    want, bound = ref.linear(host(y[last, :64]), host(wide))
+    close(host(rows[last]), want, bound, torch.bfloat16)
